@@ -6,6 +6,11 @@ residual or bonus sampling; and the greedy variant) as hand-written CUDA for
 sm_103a behind the C ABI in include/spec_verify.h. This package is the thin
 Python binding: ``spec_verify`` and friends take torch tensors and call the
 library; there is no CPU or eager fallback.
+
+``sv_kv_append``, ``sv_kv_read`` and ``sv_chunk_attention`` (include/sv_attention.h,
+libsvattention.so) are the step before it in the target model: the new
+positions' keys and values go into a paged cache, 16-bit or e4m3, and their
+queries attend to it.
 """
 from .api import (  # noqa: F401
     SV_BF16,
@@ -44,4 +49,14 @@ from .api import (  # noqa: F401
     sv_workspace_bytes,
     version,
 )
-from ._lib import LIB_PATH, LibraryMissing, load  # noqa: F401
+from .attention import (  # noqa: F401
+    SV_E4M3,
+    SV_F16,
+    SV_SEQ_BAD_LENGTH,
+    SV_SEQ_BAD_PAGE,
+    sv_chunk_attention,
+    sv_chunk_attention_workspace_bytes,
+    sv_kv_append,
+    sv_kv_read,
+)
+from ._lib import LIB_PATH, LibraryMissing, load, load_attention  # noqa: F401

@@ -1,8 +1,9 @@
-"""Build libspecverify.so in-tree for sm_103a (GB300) with nvcc.
+"""Build libspecverify.so and libsvattention.so in-tree for sm_103a (GB300) with nvcc.
 
 Each .cu under csrc/ compiles to its own object in parallel, then nvcc links
-them into a shared library beside this file. Only the names the public header
-declares are exported (-fvisibility=hidden plus explicit default visibility).
+them into a shared library beside this file. Only the names the public headers
+(include/spec_verify.h, include/sv_attention.h) declare are exported
+(-fvisibility=hidden plus explicit default visibility).
 """
 from __future__ import annotations
 
@@ -24,6 +25,10 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libspecverify_debug.so")
 DEBUG_FLAGS = ["-DSV_DEVICE_CHECKS=1"]
 SOURCES = ["row_stats.cu", "scan.cu", "sample.cu", "filter.cu", "hist.cu", "lmhead.cu", "sv_api.cu",
            "sv_static.cu", "philox.cu"]
+# The paged cache and its attention (csrc/attention).
+ATTENTION_LIB_PATH = os.path.join(PKG, "libsvattention.so")
+ATTENTION_CSRC = os.path.join(CSRC, "attention")
+ATTENTION_SOURCES = ["kv_cache.cu", "attn_rows.cu", "attn_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -69,13 +74,29 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         extra_flags = (*DEBUG_FLAGS, *extra_flags)
     if not force and not stale(lib_path):
         return lib_path
+    return _compile(CSRC, SOURCES, build_dir, lib_path, verbose, extra_flags)
+
+
+def build_attention(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Compile (if needed) libsvattention.so and return its path."""
+    files = [os.path.join(ATTENTION_CSRC, f) for f in os.listdir(ATTENTION_CSRC)]
+    files += [os.path.join(CSRC, "sv_device.cuh"), os.path.join(INCLUDE, "spec_verify.h"),
+              os.path.join(INCLUDE, "sv_attention.h")]
+    if not force and os.path.exists(ATTENTION_LIB_PATH) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(ATTENTION_LIB_PATH) for f in files):
+        return ATTENTION_LIB_PATH
+    return _compile(ATTENTION_CSRC, ATTENTION_SOURCES, os.path.join(BUILD_DIR, "attention"),
+                    ATTENTION_LIB_PATH, verbose, extra_flags)
+
+
+def _compile(csrc, sources, build_dir, lib_path, verbose, extra_flags) -> str:
     os.makedirs(build_dir, exist_ok=True)
     cc = nvcc()
     objs = []
 
     def one(src):
         obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
-        cmd = [cc, *compile_flags(extra_flags), "-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [cc, *compile_flags(extra_flags), "-c", os.path.join(csrc, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         p = subprocess.run(cmd, capture_output=True, text=True)
@@ -83,8 +104,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
             raise RuntimeError(f"nvcc failed on {src}:\n{p.stdout}\n{p.stderr}")
         return obj, p.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        results = list(ex.map(one, SOURCES))
+    with ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        results = list(ex.map(one, sources))
     for obj, log in results:
         objs.append(obj)
         if verbose and log:
@@ -102,3 +123,4 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
 if __name__ == "__main__":
     import sys
     print(build(force=True, verbose="-v" in sys.argv, debug="--debug" in sys.argv))
+    print(build_attention(force=True, verbose="-v" in sys.argv))

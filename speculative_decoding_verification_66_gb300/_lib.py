@@ -1,4 +1,4 @@
-"""ctypes loader for libspecverify.so (argument types only; no logic)."""
+"""ctypes loaders for libspecverify.so and libsvattention.so (argument types only; no logic)."""
 from __future__ import annotations
 
 import ctypes
@@ -63,8 +63,24 @@ SIGNATURES = {
     "sv_device_checks": (_i32, []),
 }
 
+# The same for libsvattention.so and include/sv_attention.h. Its calls take many
+# small arguments, some of them every step of a decode loop, so pointers are
+# passed as plain integers (c_void_p takes them) and the cache description as
+# packed bytes.
+ATTENTION_PATH = os.path.join(_DIR, "libsvattention.so")
+ATTENTION_SIGNATURES = {
+    "sv_kv_append": (_i32, [ctypes.c_char_p, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp,
+                            _vp]),
+    "sv_kv_read": (_i32, [ctypes.c_char_p, _vp, _vp, _i32, _i64, _vp, _vp]),
+    "sv_chunk_attention_workspace_bytes": (_i32, [_i64, _i64, _i64, _i64, _i64, _i64,
+                                                  ctypes.POINTER(_sz)]),
+    "sv_chunk_attention": (_i32, [ctypes.c_char_p, _vp, _i32, _i64, _i64, _i64, _i64, _f32, _i64,
+                                  _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+}
+
 _lock = threading.Lock()
 _lib = None
+_attention = None
 
 
 class LibraryMissing(RuntimeError):
@@ -82,11 +98,30 @@ def load() -> ctypes.CDLL:
                 raise LibraryMissing(
                     f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                     "(nvcc, sm_103a). The verification path has no CPU fallback.")
-            import torch  # noqa: F401  -- share torch's CUDA runtime when both are loaded
-            L = ctypes.CDLL(LIB_PATH)
-            for name, (res, args) in SIGNATURES.items():
-                fn = getattr(L, name)
-                fn.restype = res
-                fn.argtypes = args
-            _lib = L
+            _lib = _open(LIB_PATH, SIGNATURES)
     return _lib
+
+
+def _open(path: str, signatures: dict) -> ctypes.CDLL:
+    import torch  # noqa: F401  -- share torch's CUDA runtime when both are loaded
+    L = ctypes.CDLL(path)
+    for name, (res, args) in signatures.items():
+        fn = getattr(L, name)
+        fn.restype = res
+        fn.argtypes = args
+    return L
+
+
+def load_attention() -> ctypes.CDLL:
+    """Load the in-tree library of the paged cache and its attention, which has
+    no fallback either."""
+    global _attention
+    if _attention is None:
+        with _lock:
+            if _attention is None:
+                if not os.path.exists(ATTENTION_PATH):
+                    raise LibraryMissing(
+                        f"{ATTENTION_PATH} is missing: build it with __graft_entry__.build() "
+                        "(nvcc, sm_103a). The attention has no CPU fallback.")
+                _attention = _open(ATTENTION_PATH, ATTENTION_SIGNATURES)
+    return _attention

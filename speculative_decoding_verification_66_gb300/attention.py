@@ -1,0 +1,232 @@
+"""Python binding of the paged cache and its attention (include/sv_attention.h):
+the same names, torch tensors in.
+
+Argument marshalling only, as in api.py. A cache is described by the tensors it
+lies in:
+
+    k_pages, v_pages  [pages, page_size, kv_heads, head_dim], bfloat16, float16
+                      or float8_e4m3fn; any strides but the last (a cache with
+                      its heads outermost in a page is a transposed view)
+    k_exps, v_exps    [pages, page_size, kv_heads] uint8, e4m3 only
+    page_table        [B, max_pages] int32
+    cached_lens       [B] int32: tokens in the cache before this call's
+    chunk_starts      [B + 1] int32: where each sequence's new tokens begin in
+                      the packed arrays
+
+Lengths and pages are read on the device only, so every call can be captured
+into a CUDA graph and replayed with new ones.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+from contextlib import ExitStack
+
+import torch
+
+from . import _lib
+from .api import SV_BF16, _check
+
+SV_F16, SV_E4M3 = 2, 3
+SV_SEQ_BAD_PAGE, SV_SEQ_BAD_LENGTH = 16, 32
+
+_CODES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3}
+# struct sv_paged_cache
+_CACHE = struct.Struct("@4P12qq4iP2q2Pq")
+_NO_EXPS = (0, 0, 0)
+
+
+def _require(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps, v_exps):
+    """(packed struct sv_paged_cache, element type code, device)."""
+    dev, dt, shape = k_pages.device, k_pages.dtype, k_pages.shape
+    _require(dev.type == "cuda" and len(shape) == 4,
+             "k_pages must be a CUDA tensor [pages, page_size, kv_heads, head_dim]")
+    code = _CODES.get(dt)
+    if code is None:
+        raise TypeError(f"pages must be bfloat16, float16 or float8_e4m3fn, got {dt}")
+    ks, vs = k_pages.stride(), v_pages.stride()
+    _require(v_pages.shape == shape and v_pages.dtype == dt and v_pages.device == dev,
+             "v_pages must have k_pages' shape, dtype and device")
+    _require(ks[3] == 1 and vs[3] == 1, "pages must be contiguous along head_dim")
+    if code == SV_E4M3:
+        for e in (k_exps, v_exps):
+            _require(e is not None and e.dtype == torch.uint8 and e.shape == shape[:3]
+                     and e.device == dev,
+                     "k_exps and v_exps must be uint8 [pages, page_size, kv_heads] beside "
+                     "e4m3 pages")
+        kep, vep, kes, ves = k_exps.data_ptr(), v_exps.data_ptr(), k_exps.stride(), v_exps.stride()
+    else:
+        _require(k_exps is None and v_exps is None, "only e4m3 pages have exponents")
+        kep, vep, kes, ves = 0, 0, _NO_EXPS, _NO_EXPS
+    B = cached_lens.numel()
+    _require(page_table.dim() == 2 and page_table.shape[0] == B and page_table.dtype == torch.int32
+             and (page_table.stride(1) == 1 or page_table.shape[1] <= 1)
+             and page_table.device == dev,
+             "page_table must be int32 [B, max_pages], rows contiguous")
+    _require(cached_lens.dim() == 1 and cached_lens.dtype == torch.int32
+             and cached_lens.is_contiguous() and cached_lens.device == dev,
+             "cached_lens must be contiguous int32 [B]")
+    _require(chunk_starts.dim() == 1 and chunk_starts.numel() == B + 1
+             and chunk_starts.dtype == torch.int32 and chunk_starts.is_contiguous()
+             and chunk_starts.device == dev, "chunk_starts must be contiguous int32 [B + 1]")
+    max_pages = page_table.shape[1]
+    packed = _CACHE.pack(
+        k_pages.data_ptr(), v_pages.data_ptr(), kep, vep, ks[0], vs[0], ks[1], vs[1], ks[2], vs[2],
+        kes[0], ves[0], kes[1], ves[1], kes[2], ves[2], shape[0], shape[1], shape[2], shape[3],
+        code, page_table.data_ptr(), max(page_table.stride(0), max_pages), max_pages,
+        cached_lens.data_ptr(), chunk_starts.data_ptr(), B)
+    return packed, code, dev
+
+
+def _rows(x, name, heads, head_dim, dev, cache_code):
+    """Type code of a packed array [tokens, heads, head_dim]."""
+    code = _CODES.get(x.dtype)
+    if code is None or code == SV_E4M3 or (cache_code != SV_E4M3 and code != cache_code):
+        raise TypeError(f"{name} must be bfloat16 or float16, and of the cache's type unless that "
+                        f"is e4m3, got {x.dtype}")
+    _require(x.dim() == 3 and x.device == dev and x.shape[2] == head_dim and
+             (heads is None or x.shape[1] == heads),
+             f"{name} must be [tokens, heads, head_dim] on the cache's device")
+    _require(x.stride(2) == 1 or x.numel() == 0, f"{name} must be contiguous along head_dim")
+    return code
+
+
+def _status(seq_status, B, dev):
+    if seq_status is None:
+        return None
+    _require(seq_status.dtype == torch.int32 and seq_status.shape == (B,)
+             and seq_status.is_contiguous() and seq_status.device == dev,
+             "seq_status must be contiguous int32 [B]")
+    return seq_status.data_ptr()
+
+
+def _enter(stack, dev, stream, *tensors):
+    """Make dev and stream current, so that what is allocated below belongs to the stream the
+    kernels run on, and tell the allocator of the tensors used on a stream not their own."""
+    if torch.cuda.current_device() != dev.index:
+        stack.enter_context(torch.cuda.device(dev))
+    if stream is not None and stream != torch.cuda.current_stream(dev):
+        stack.enter_context(torch.cuda.stream(stream))
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    # (the handle of the current stream, without building a Stream object)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def sv_kv_append(key, value, k_pages, v_pages, page_table, cached_lens, chunk_starts, *,
+                 k_exps=None, v_exps=None, seq_status=None, stream=None) -> None:
+    """Write the new tokens' key and value [tokens, kv_heads, head_dim] (any strides but the last)
+    into the cache, quantised where it is e4m3. Asynchronous on ``stream`` (default: the current
+    stream of the pages' device)."""
+    cache, code, dev = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
+                              v_exps)
+    H, D = k_pages.shape[2:]
+    dtype = _rows(key, "key", H, D, dev, code)
+    _rows(value, "value", H, D, dev, code)
+    _require(value.shape == key.shape and value.dtype == key.dtype,
+             "value must have key's shape and dtype")
+    status = _status(seq_status, cached_lens.numel(), dev)
+    ks, vs = key.stride(), value.stride()
+    with ExitStack() as stack:
+        s = _enter(stack, dev, stream, key, value, k_pages, v_pages, page_table, cached_lens,
+                   chunk_starts, k_exps, v_exps, seq_status)
+        _check(_lib.load_attention().sv_kv_append(
+            cache, key.data_ptr(), value.data_ptr(), dtype, key.shape[0], ks[0], ks[1], vs[0],
+            vs[1], status, s), "sv_kv_append")
+
+
+def sv_kv_read(k_pages, v_pages, page_table, cached_lens, chunk_starts, tokens: int, *,
+               k_exps=None, v_exps=None, dtype=None, key=None, value=None, seq_status=None,
+               stream=None):
+    """Read positions cached_lens[b] .. cached_lens[b] + (chunk_starts[b + 1] - chunk_starts[b])
+    of every sequence back. Returns (key, value) [tokens, kv_heads, head_dim] of ``dtype``
+    (default: the cache's, bfloat16 from e4m3); ``tokens`` is chunk_starts[B], which the host has
+    to know."""
+    cache, code, dev = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
+                              v_exps)
+    H, D = k_pages.shape[2:]
+    if dtype is None:
+        dtype = key.dtype if key is not None else \
+            torch.bfloat16 if code == SV_E4M3 else k_pages.dtype
+    status = _status(seq_status, cached_lens.numel(), dev)
+    with ExitStack() as stack:
+        s = _enter(stack, dev, stream, key, value, k_pages, v_pages, page_table, cached_lens,
+                   chunk_starts, k_exps, v_exps, seq_status)
+        _require(tokens >= 0, "tokens must not be negative")
+        if key is None:
+            key = torch.empty((tokens, H, D), dtype=dtype, device=dev)
+        if value is None:
+            value = torch.empty((tokens, H, D), dtype=dtype, device=dev)
+        for name, x in (("key", key), ("value", value)):
+            d = _rows(x, name, H, D, dev, code)
+            _require(x.shape[0] == tokens and x.dtype == dtype and x.is_contiguous(),
+                     f"{name} must be contiguous [tokens, kv_heads, head_dim] of dtype")
+        _check(_lib.load_attention().sv_kv_read(cache, key.data_ptr(), value.data_ptr(), d, tokens,
+                                                status, s), "sv_kv_read")
+    return key, value
+
+
+def sv_chunk_attention_workspace_bytes(B: int, tokens: int, q_heads: int, kv_heads: int,
+                                       head_dim: int, max_chunk: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.load_attention().sv_chunk_attention_workspace_bytes(
+        B, tokens, q_heads, kv_heads, head_dim, max_chunk, ctypes.byref(n)),
+        "sv_chunk_attention_workspace_bytes")
+    return n.value
+
+
+def sv_chunk_attention(query, k_pages, v_pages, page_table, cached_lens, chunk_starts, *,
+                       k_exps=None, v_exps=None, scale=None, window: int = 0, max_chunk: int = 0,
+                       out=None, lse=None, return_lse: bool = False, seq_status=None,
+                       workspace=None, stream=None):
+    """Attention of the new tokens' query [tokens, q_heads, head_dim] over their sequences' caches,
+    which hold the new tokens too (``sv_kv_append`` first): query t of sequence b sees positions up
+    to its own, cached_lens[b] + t, and with a ``window`` only the last ``window`` of them.
+
+    ``scale`` defaults to head_dim ** -0.5. ``max_chunk``: an upper bound of the sequences' new
+    tokens (0: tokens); a tight one lets the launches be planned for it. Returns out, or (out, lse)
+    with ``return_lse`` or an ``lse`` tensor (float32 [tokens, q_heads])."""
+    cache, code, dev = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
+                              v_exps)
+    H, D = k_pages.shape[2:]
+    dtype = _rows(query, "query", None, D, dev, code)
+    N, Hq = query.shape[:2]
+    B = cached_lens.numel()
+    _require(H > 0 and Hq > 0 and Hq % H == 0, "query heads must be a multiple of kv_heads")
+    status = _status(seq_status, B, dev)
+    if scale is None:
+        scale = D ** -0.5
+    with ExitStack() as stack:
+        s = _enter(stack, dev, stream, query, k_pages, v_pages, page_table, cached_lens,
+                   chunk_starts, k_exps, v_exps, out, lse, seq_status, workspace)
+        if out is None:
+            out = torch.empty((N, Hq, D), dtype=query.dtype, device=dev)
+        else:
+            _require(out.shape == query.shape and out.dtype == query.dtype and
+                     out.device == dev and out.is_contiguous(),
+                     "out must be contiguous, of query's shape, dtype and device")
+        if lse is not None:
+            _require(lse.shape == (N, Hq) and lse.dtype == torch.float32 and lse.device == dev
+                     and lse.is_contiguous(), "lse must be contiguous float32 [tokens, q_heads]")
+        elif return_lse:
+            lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            # A new one every call, from the allocator's pool of this stream (or of the graph
+            # being captured): nothing that an earlier call or a replay still uses is touched.
+            workspace = torch.empty(sv_chunk_attention_workspace_bytes(B, N, Hq, H, D, max_chunk),
+                                    dtype=torch.uint8, device=dev)
+        else:
+            _require(workspace.device == dev and workspace.dtype == torch.uint8 and
+                     workspace.is_contiguous(), "workspace must be contiguous uint8 on the device")
+        qs = query.stride()
+        _check(_lib.load_attention().sv_chunk_attention(
+            cache, query.data_ptr(), dtype, N, Hq, qs[0], qs[1], scale, window, max_chunk,
+            out.data_ptr(), None if lse is None else lse.data_ptr(), status,
+            workspace.data_ptr(), workspace.numel(), s), "sv_chunk_attention")
+    return out if lse is None else (out, lse)

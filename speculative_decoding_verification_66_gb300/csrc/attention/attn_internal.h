@@ -1,0 +1,21 @@
+// attn_internal.h -- launchers of libsvattention's translation units.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace sva {
+
+// One side (keys or values) of the packed arrays of an append or a read.
+struct Packed {
+    uint8_t* x[2];
+    int64_t token_stride[2], head_stride[2];  // bytes
+    int64_t tokens;
+    int32_t* status;
+};
+
+cudaError_t launch_append(const Cache& c, const Packed& p, bool f16, bool e4m3, cudaStream_t s);
+cudaError_t launch_read(const Cache& c, const Packed& p, bool f16, bool e4m3, cudaStream_t s);
+
+cudaError_t launch_attention_rows(const Attn& a, bool f16, bool e4m3, cudaStream_t s);
+
+}  // namespace sva
