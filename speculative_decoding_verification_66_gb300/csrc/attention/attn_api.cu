@@ -10,6 +10,7 @@
 namespace {
 
 constexpr int64_t kMax31 = int64_t(1) << 31;
+constexpr int64_t kMaxTileDim = 128;  // the tile kernel's largest head size
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -172,6 +173,8 @@ int check_attention(int64_t batch, int64_t tokens, int64_t q_heads, int64_t kv_h
         head_dim > 256 || head_dim % 16 != 0 || tokens * q_heads >= (int64_t(1) << 40))
         return SV_ERR_SIZE;
     if (*max_chunk == 0 || *max_chunk > tokens) *max_chunk = tokens;
+    // (a sequence's rows are counted in 32 bits)
+    if (*max_chunk * (q_heads / kv_heads) >= kMax31 - 512) return SV_ERR_SIZE;
     return SV_OK;
 }
 
@@ -184,7 +187,8 @@ SV_EXPORT int sv_chunk_attention_workspace_bytes(int64_t batch, int64_t tokens, 
     if (bytes == nullptr) return SV_ERR_ARG;
     const int rc = check_attention(batch, tokens, q_heads, kv_heads, head_dim, &max_chunk);
     if (rc != SV_OK) return rc;
-    *bytes = 256;
+    *bytes = head_dim <= kMaxTileDim ? sva::tiles_workspace(max_chunk, q_heads / kv_heads, head_dim)
+                                     : 256;
     return SV_OK;
 }
 
@@ -229,8 +233,11 @@ SV_EXPORT int sv_chunk_attention(const sv_paged_cache* cache, const void* query,
     a.G = static_cast<int32_t>(q_heads / cache->kv_heads);
     a.scale = scale;
     a.scale_log2 = scale * 1.44269504088896341f;
-    return sva::launch_attention_rows(a, dtype == SV_F16, cache->dtype == SV_E4M3, s) ==
-                   cudaSuccess
-               ? SV_OK
-               : SV_ERR_CUDA;
+    const bool f16 = dtype == SV_F16, e4m3 = cache->dtype == SV_E4M3;
+    bool done = false;
+    if (a.c.D <= kMaxTileDim && a.c.num_pages > 0 &&
+        sva::launch_attention_tiles(a, f16, e4m3, workspace, s, &done) != cudaSuccess)
+        return SV_ERR_CUDA;
+    if (!done && sva::launch_attention_rows(a, f16, e4m3, s) != cudaSuccess) return SV_ERR_CUDA;
+    return SV_OK;
 }

@@ -16,6 +16,13 @@ struct Packed {
 cudaError_t launch_append(const Cache& c, const Packed& p, bool f16, bool e4m3, cudaStream_t s);
 cudaError_t launch_read(const Cache& c, const Packed& p, bool f16, bool e4m3, cudaStream_t s);
 
+// Head sizes up to 128; *mapped is false, and nothing is launched, where the
+// tensor copies cannot describe the pages' strides.
+size_t tiles_workspace(int64_t max_chunk, int64_t G, int64_t D);
+cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* workspace,
+                                   cudaStream_t s, bool* mapped);
+
+// Any head size.
 cudaError_t launch_attention_rows(const Attn& a, bool f16, bool e4m3, cudaStream_t s);
 
 }  // namespace sva

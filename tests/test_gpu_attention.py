@@ -95,6 +95,14 @@ def test_long_context(dtype, e4m3, T):
 
 
 @pytest.mark.parametrize("dtype,e4m3", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 5, 40])
+def test_many_tiles_a_block(dtype, e4m3, d, T):
+    """More tiles of several items to a thread block than its shared memory holds at one time."""
+    run([6000, 4100, 5003, 777], [T] * 4, 16, 4, d, 64, dtype, e4m3, seed=4, max_chunk=T)
+
+
+@pytest.mark.parametrize("dtype,e4m3", TYPES)
 def test_long_piece(dtype, e4m3):
     run([257], [600], 2, 2, 128, 64, dtype, e4m3, seed=5)
 
