@@ -25,12 +25,13 @@
 //   0-3, 4-7  softmax of slots 0 and 1 (row = tensor-memory lane = thread), the
 //             loads of the queries and the outputs
 //   8         issues the products
-//   9         loads: page numbers, one bulk tensor copy a page and 64 elements,
-//             exponents
-//   10-..     16-bit caches: makes the values at a tile's hidden positions
-//             harmless. e4m3 caches: also expand every tile to the query's
-//             type, exactly (see e4m3_words), into the stage that the products
-//             read.
+//   9, 10     load keys and values: page numbers, a bulk tensor copy a page,
+//             exponents. Warp 9 also plans the block's segments for all.
+//   11-15     helpers. 16-bit caches: make the values at a tile's hidden
+//             positions harmless. e4m3 caches: also expand every tile, exactly,
+//             into the stage that the products read.
+// The next segment's queries are fetched while the last products of a segment
+// run, and its scores begin while the segment's results are written.
 //
 // Masks. A hidden score is replaced by -inf, whatever it was. A hidden value
 // would still be multiplied by a zero weight, and NaN and infinity would come
@@ -41,10 +42,18 @@
 // Positions outside the item's range are always cleared: what lies there may
 // never have been written.
 //
+// e4m3. Values are expanded to the query's type, code and exponent, which is
+// exact (expand_values). Of keys only the codes are, to float16, two an
+// instruction; their exponents are columns of the scores, which are multiplied
+// by them in float32. bfloat16 queries become float16 for this, each row scaled
+// by a power of two that brings its largest element to [2^14, 2^15): exact down
+// to 2^-38 of that.
+//
 // Work is shared among one block per SM as attn_plan.cuh says; items that
 // several blocks share are joined by join_kernel in block order, so results
 // depend on the lengths and the number of blocks alone.
 #include <climits>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "attn_plan.cuh"
@@ -55,8 +64,8 @@ namespace {
 
 constexpr float kSlack = 8.f;
 constexpr int kMaxBlocks = 160;  // shares in the workspace; grids are no larger
-constexpr int kNoted = 8;        // noted positions an item can hold
-constexpr int kItems = 8;        // items whose notes are kept at one time
+constexpr int kNoted = 4;        // noted positions a segment can hold
+constexpr int kItems = 16;       // segments whose plans and notes are kept at one time
 constexpr size_t kMaxSmem = 232448;
 
 template <int DP, bool E4M3, bool PAIR>
@@ -67,14 +76,28 @@ struct Shape {
     static constexpr int kQBytes = kRows * DP * 2;
     // Stages in tiles of K or V: what the SM's shared memory holds. (The loads
     // and the notes of hidden values run at most kStages + kRawStages tiles, half
-    // as many items, ahead of the products: below kItems.)
+    // as many segments, ahead of the products: well below kItems.)
     static constexpr int kStages = DP == 128 ? (E4M3 ? 3 : (PAIR ? 5 : 6)) : (E4M3 ? 4 : 8);
-    static constexpr int kRawStages = E4M3 ? (DP == 128 ? (PAIR ? 4 : 5) : 8) : 0;
-    static_assert((kStages + kRawStages) / 2 < kItems - 1, "notes");
-    static constexpr int kHelpers = E4M3 ? 8 : 4;
-    static constexpr int kThreads = (10 + kHelpers) * 32;
+    static constexpr int kRawStages = E4M3 ? (DP == 128 ? (PAIR ? 3 : 5) : 8) : 0;
+    static_assert((kStages + kRawStages) / 2 + 1 < kItems - 2, "notes");
+    static constexpr int kHelpers = 5;
+    static constexpr int kThreads = 512;
     static constexpr int kPanel = kTile * 128;  // bytes of 64 elements of every row
     static constexpr int kTiles = kQBytes + kStages * kTileBytes + kRawStages * kRawBytes;
+};
+
+// A segment as the warps need it. Positions count from the segment's first
+// tile; tiles are numbered from it.
+struct Plan {
+    int32_t n;                         // tiles; 0: no more segments
+    int32_t b, h, q0, row0, rows;
+    int32_t tile0;                     // the first tile's number in the sequence
+    int32_t cached;                    // row r stands at position cached + r / G
+    int32_t lo0, hi0, lo1, hi1;        // PAIR: tiles of either slot
+    int32_t any_lo, any_hi;            // positions that some row sees
+    int32_t all_lo, all_hi;            // positions that every row sees
+    int32_t inner_lo, inner_hi;        // tiles wholly in `all`; the others have hidden values
+    int32_t begins, whole;             // the item begins here; is all here
 };
 
 // Shared memory besides the tiles.
@@ -82,16 +105,19 @@ template <int STAGES, int RAW, bool PAIR>
 struct Control {
     uint64_t full[STAGES], empty[STAGES], fixed[STAGES];
     uint64_t raw_full[RAW > 0 ? RAW : 1], raw_empty[RAW > 0 ? RAW : 1];
-    uint64_t s_full[2], p_ready[2], q_ready, o_full, ml_ready, done;
+    uint64_t s_full[2], p_ready[2], q_ready, o_full, o_free, ml_ready, done;
+    uint64_t plan_ready[kItems];
     uint32_t tmem;
     int stop;
     Start start;
-    int64_t sums[18];
+    int64_t sums[16];
+    Plan plan[kItems];
     int noted[kItems];             // how many positions are noted
-    uint32_t note[kItems][kNoted]; // which
+    int note[kItems][kNoted];      // which, counted as in the plan
     int bad_page[kItems];
-    float2 ml[2][PAIR ? 1 : kTile]; // a row's maximum and sum in either slot
-    uint8_t exps[RAW > 0 ? RAW : 1][kTile];
+    float q_scale[RAW > 0 ? (PAIR ? 256 : 128) : 1];  // e4m3: power of two a row is divided by
+    alignas(16) float k_scale[RAW > 0 ? 4 : 1][RAW > 0 ? kTile : 4];  // .. of the last tiles' keys
+    uint8_t exps[RAW > 0 ? RAW : 1][RAW > 0 ? kTile : 4];
 };
 
 struct Tiles {
@@ -99,55 +125,91 @@ struct Tiles {
     float* part;   // [blocks][2][rows][part_cols]: unnormalised O, then m and l
     Share* shares; // [blocks]
     int32_t part_rows;
+    // A tile in shared memory: rows of 128 bytes (64 elements), eight to a
+    // group; bytes from a group to the next, and to the next 64 elements.
+    int32_t group, panel;
+    // Copies of whole 128-element rows: pages and heads are one axis, a page
+    // page_heads steps, a head head_step. 0: a copy for each 64 elements.
+    int32_t page_heads, head_step;
 };
 
 // Where the tiles of a segment lie in the ring: the order in which the products
 // use them. PAIR: K0 V0 K1 V1 ..; otherwise K0 K1 V0 K2 V1 .., since the second
 // slot's scores come before the first slot's values.
 template <bool PAIR>
-__device__ __forceinline__ int64_t ring_k(int64_t base, int k)
+__device__ __forceinline__ int ring_v(int k, int n)
 {
-    return base + (PAIR ? 2 * k : (k == 0 ? 0 : 2 * k - 1));
+    return PAIR ? 2 * k + 1 : (k == n - 1 ? 2 * k + 1 : 2 * k + 2);
+}
+// From a tile's keys, and its values, to the next tile's.
+template <bool PAIR>
+__device__ __forceinline__ int ring_k_step(int k)
+{
+    return !PAIR && k == 0 ? 1 : 2;
 }
 template <bool PAIR>
-__device__ __forceinline__ int64_t ring_v(int64_t base, int k, int n)
+__device__ __forceinline__ int ring_v_step(int k, int n)
 {
-    return base + (PAIR ? 2 * k + 1 : (k == n - 1 ? 2 * k + 1 : 2 * k + 2));
+    return !PAIR && k == n - 2 ? 1 : 2;
 }
 
-// The tiles of a segment that slot s works on: [lo, hi) in steps of `step`.
-struct SlotTiles {
-    int lo, hi, step;
+// A place in a ring of S stages, and the round it is in.
+template <int S>
+struct Place {
+    int stage = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void advance(int n)
+    {
+        stage += n;
+        while (stage >= S) {
+            stage -= S;
+            ++round;
+        }
+    }
 };
+
+__device__ __forceinline__ int clamp32(int64_t v)
+{
+    return static_cast<int>(max(min(v, int64_t(INT_MAX / 2)), int64_t(INT_MIN / 2)));
+}
+
 template <bool PAIR>
-__device__ __forceinline__ SlotTiles slot_tiles(const Attn& a, const Segment& g, int s)
+__device__ __forceinline__ Plan plan_of(const Attn& a, const Segment& g)
 {
-    if (!PAIR) return SlotTiles{g.t.lo + s, g.t.hi, 2};
-    const int r0 = g.row0 + 128 * s, r1 = min(g.row0 + g.rows, r0 + 128);
-    if (r0 >= r1) return SlotTiles{g.t.hi, g.t.hi, 1};
-    const Range t = row_tiles(a, g.cached, r0, r1);
-    return SlotTiles{max(g.t.lo, t.lo), min(g.t.hi, t.hi), 1};
-}
-__device__ __forceinline__ bool works_on(const SlotTiles& t, int j)
-{
-    return j >= t.lo && j < t.hi && (t.step == 1 || ((j - t.lo) & 1) == 0);
-}
-
-// The positions that every row of an item sees, and those that any row sees,
-// relative to tile j: [lo, hi] each. Beyond `all` a tile needs its hidden
-// values made harmless.
-struct Seen {
-    int64_t all_lo, all_hi, any_lo, any_hi;
-};
-__device__ __forceinline__ Seen item_seen(const Attn& a, const Segment& g)
-{
-    const int64_t p0 = g.cached + g.row0 / a.G, p1 = g.cached + (g.row0 + g.rows - 1) / a.G;
-    return Seen{first_key(a, p1), p0, first_key(a, p0), p1};
-}
-__device__ __forceinline__ bool at_edge(const Seen& s, int j)
-{
-    const int64_t lo = static_cast<int64_t>(j) << kTileShift;
-    return lo < s.all_lo || lo + kTile - 1 > s.all_hi;
+    Plan p;
+    const int64_t origin = static_cast<int64_t>(g.t.lo) << kTileShift;
+    const int r1 = g.row0 + g.rows - 1;
+    const int64_t p0 = g.cached + g.row0 / a.G, p1 = g.cached + r1 / a.G;
+    p.n = g.t.hi - g.t.lo;
+    p.b = g.b;
+    p.h = g.h;
+    p.q0 = g.q0;
+    p.row0 = g.row0;
+    p.rows = g.rows;
+    p.tile0 = g.t.lo;
+    p.cached = clamp32(g.cached - origin);
+    p.any_lo = clamp32(first_key(a, p0) - origin);
+    p.any_hi = clamp32(p1 - origin);
+    p.all_lo = clamp32(first_key(a, p1) - origin);
+    p.all_hi = clamp32(p0 - origin);
+    p.inner_lo = (p.all_lo + kTile - 1) >> kTileShift;
+    p.inner_hi = ((p.all_hi + 1) >> kTileShift) - 1;
+    p.begins = g.t.lo == g.item.lo;
+    p.whole = p.begins && g.t.hi == g.item.hi;
+    p.lo0 = p.lo1 = 0;
+    p.hi0 = p.hi1 = p.n;
+    if (PAIR) {
+        const Range t0 = row_tiles(a, g.cached, g.row0, g.row0 + min(g.rows, 128));
+        p.lo0 = max(t0.lo - g.t.lo, 0);
+        p.hi0 = min(t0.hi - g.t.lo, p.n);
+        p.hi1 = 0;
+        if (g.rows > 128) {
+            const Range t1 = row_tiles(a, g.cached, g.row0 + 128, g.row0 + g.rows);
+            p.lo1 = max(t1.lo - g.t.lo, 0);
+            p.hi1 = min(t1.hi - g.t.lo, p.n);
+        }
+    }
+    return p;
 }
 
 // ---------------------------------------------------------------------------
@@ -202,7 +264,7 @@ __device__ __forceinline__ uint2 spread(uint32_t w, F16)
     return make_uint2(e4m3_to_f16x2(w & 0xFFFFu), e4m3_to_f16x2(w >> 16));
 }
 template <class T>
-__device__ __forceinline__ void e4m3_words(uint4 codes, const Factor& f, uint4* lo, uint4* hi)
+__device__ __forceinline__ void expand_values(uint4 codes, const Factor& f, uint4* lo, uint4* hi)
 {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
     uint32_t o[8];
@@ -218,6 +280,14 @@ __device__ __forceinline__ void e4m3_words(uint4 codes, const Factor& f, uint4* 
     }
     *lo = make_uint4(o[0], o[1], o[2], o[3]);
     *hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+// The codes alone, as float16.
+__device__ __forceinline__ void expand_codes(uint4 c, uint4* lo, uint4* hi)
+{
+    const uint2 a = spread(c.x, F16()), b = spread(c.y, F16());
+    const uint2 d = spread(c.z, F16()), e = spread(c.w, F16());
+    *lo = make_uint4(a.x, a.y, b.x, b.y);
+    *hi = make_uint4(d.x, d.y, e.x, e.y);
 }
 
 __device__ __forceinline__ bool any_special(uint4 w, uint32_t exponent)
@@ -247,17 +317,13 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
                  : "memory");
     return v;
 }
-// Byte offset of 16-byte chunk `chunk` of a row in a tile of 64-element panels
-// with the 128-byte swizzle.
-__device__ __forceinline__ uint32_t tile_chunk(int row, int chunk, int panel_bytes)
+// Byte offset of 16-byte chunk `chunk` of a row in a tile with the 128-byte
+// swizzle (group and panel: see Tiles).
+__device__ __forceinline__ uint32_t tile_chunk(int row, int chunk, int group, int panel)
 {
-    return (chunk >> 3) * panel_bytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+    return (row >> 3) * group + (chunk >> 3) * panel + (row & 7) * 128 +
+           (((chunk & 7) ^ (row & 7)) << 4);
 }
-
-// Scores at columns [0, lo) and (hi, 127] of a tile do not count.
-struct Columns {
-    int lo, hi;
-};
 
 // Sum of int64 over the block; every thread gets it.
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sums, int warps)
@@ -307,6 +373,40 @@ __device__ __forceinline__ int64_t out_row(const Attn& a, int q0, int h, int r)
     return (static_cast<int64_t>(q0) + t) * a.Hq + h * a.G + (r - t * a.G);
 }
 
+// Row r of a segment's item again, key by key, by a warp: to the output or to the
+// block's share at `part`.
+template <class T, bool E4M3, int DP>
+__device__ __noinline__ void again_row(const Tiles& args, const Plan& g, int r, float* part)
+{
+    const Attn& a = args.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t origin = static_cast<int64_t>(g.tile0) << kTileShift;
+    const int t = (g.row0 + r) / a.G, hq = g.h * a.G + (g.row0 + r - t * a.G);
+    const int64_t pos = origin + g.cached + t, token = static_cast<int64_t>(g.q0) + t;
+    const int64_t lo = max(first_key(a, pos), origin);
+    const int64_t hi = min(pos + 1, origin + (static_cast<int64_t>(g.n) << kTileShift));
+    const int64_t orow = token * a.Hq + hq;
+    float m, l, o[8];
+    attend_row<T, E4M3>(a, g.b, g.h, a.q + token * a.q_token + hq * a.q_head, lo, hi, lane, &m, &l, o);
+    if (g.whole) {
+        const float x = 1.f / l;
+        if (lane * 8 < a.c.D)
+            *reinterpret_cast<uint4*>(a.out + (orow * a.c.D + lane * 8) * 2) =
+                make_uint4(narrow2(o[0] * x, o[1] * x, T()), narrow2(o[2] * x, o[3] * x, T()),
+                           narrow2(o[4] * x, o[5] * x, T()), narrow2(o[6] * x, o[7] * x, T()));
+        if (a.lse != nullptr && lane == 0) a.lse[orow] = fmaf(m, kLn2, logf(l));
+        return;
+    }
+    if (lane * 8 < DP) {
+        *reinterpret_cast<float4*>(part + lane * 8) = make_float4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<float4*>(part + lane * 8 + 4) = make_float4(o[4], o[5], o[6], o[7]);
+    }
+    if (lane == 0) {
+        part[DP] = m;
+        part[DP + 1] = l;
+    }
+}
+
 template <class T, int DP, bool E4M3, bool PAIR>
 __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
     tiles_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -343,7 +443,9 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         sv::mbar_init(&ctl.q_ready, 8);
         sv::mbar_init(&ctl.o_full, 1);
         sv::mbar_init(&ctl.ml_ready, 8);
+        sv::mbar_init(&ctl.o_free, 8);
         sv::mbar_init(&ctl.done, 1);
+        for (int i = 0; i < kItems; ++i) sv::mbar_init(&ctl.plan_ready[i], 1);
         // (The swizzle needs tiles on 1024-byte boundaries. There is no static
         // shared memory before them, so they are; if not, the call fails.)
         ctl.stop = (base & 1023u) != 0;
@@ -419,9 +521,13 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0;
     };
-    Walk<R> walk(a, start);
-    Segment g;
     int item = 0;  // segments taken so far
+    // The next segment's plan, or nullptr when there is none or a wait ran out.
+    auto plan_at = [&](int i) -> const Plan* {
+        if (!wait_all(&ctl.plan_ready[i % kItems], i / kItems)) return nullptr;
+        const Plan* p = &ctl.plan[i % kItems];
+        return p->n > 0 ? p : nullptr;
+    };
 
     if (warp < 8) {
         // ------------------------------------------------------------------
@@ -430,200 +536,299 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t s_addr = lane_base + s * 128, o_addr = lane_base + 256 + s * DP;
-        const float c = a.scale_log2;
         const float ninf = __uint_as_float(sv::kF32NegInfBits);
+        const int slot_row = PAIR ? 128 * s + row : row;  // row of the item
+        const int warp_row = slot_row - lane;
         uint32_t tiles_done = 0;
-        bool ok = true;
-        for (; ok && walk.next(&g); ++item) {
-            // The queries: rows of 64-element panels, swizzled; zeros past D.
-            {
-                constexpr int kChunks = DP / 8;
-                const int first = PAIR ? s * 128 : s * 64, count = PAIR ? 128 : 64;
-                const int tid = threadIdx.x & 127;
-#pragma unroll 4
-                for (int i = tid; i < count * kChunks; i += 128) {
-                    const int r = first + i / kChunks, ch = i % kChunks;
-                    if (r >= g.rows) continue;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    const int rr = g.row0 + r, t = rr / a.G;
-                    if (ch * 8 < a.c.D)
-                        v = *reinterpret_cast<const uint4*>(
-                            a.q + (static_cast<int64_t>(g.q0) + t) * a.q_token +
-                            static_cast<int64_t>(g.h * a.G + (rr - t * a.G)) * a.q_head + ch * 16);
-                    st_shared_v4(sq + (PAIR ? s * 128 * DP * 2 : 0) +
-                                     tile_chunk(PAIR ? r - first : r, ch, X::kPanel),
-                                 v);
+        int tiles_before = 0;  // of the segments before, for the keys' exponents
+
+        // Queries of a segment: PAIR: the slot's 128 rows; otherwise half of the
+        // item's rows each slot. Fetched into registers first, stored when the
+        // products of the segment before have read theirs: panels of 64
+        // elements, swizzled, zeros past D.
+        constexpr int kChunks = DP / 8, kCount = PAIR ? 128 : 64;
+        constexpr int kFetch = kCount * kChunks / 128;
+        uint4 qv[kFetch];
+        const int first = (threadIdx.x & 127) / kChunks + (PAIR ? 128 * s : 64 * s);
+        const int ch = threadIdx.x % kChunks;
+        auto fetch = [&](const Plan& x) {
+#pragma unroll
+            for (int i = 0; i < kFetch; ++i) {
+                const int r = first + i * (128 / kChunks);
+                qv[i] = make_uint4(0, 0, 0, 0);
+                if (r < x.rows && ch * 8 < a.c.D) {
+                    const int rr = x.row0 + r, t = rr / a.G;
+                    qv[i] = *reinterpret_cast<const uint4*>(
+                        a.q + (static_cast<int64_t>(x.q0) + t) * a.q_token +
+                        static_cast<int64_t>(x.h * a.G + (rr - t * a.G)) * a.q_head + ch * 16);
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) sv::mbar_arrive(&ctl.q_ready);
             }
-            const int slot_row = PAIR ? 128 * s + row : row;  // row of the item
-            const int warp_row = PAIR ? 128 * s + quad * 32 : quad * 32;
-            const bool live = warp_row < g.rows;  // some row of this warp exists
-            const int r = g.row0 + min(slot_row, g.rows - 1);
-            const int64_t pos = g.cached + r / a.G;  // last position seen
-            const int64_t low = first_key(a, pos);
-            const SlotTiles mine = slot_tiles<PAIR>(a, g, s);
+        };
+        auto store = [&](const Plan& x) {
+#pragma unroll
+            for (int i = 0; i < kFetch; ++i) {
+                const int r = first + i * (128 / kChunks);
+                const bool has = r < x.rows;
+                if constexpr (E4M3 && std::is_same<T, Bf16>::value) {
+                    // To float16, scaled. The kChunks lanes of a row are neighbours.
+                    const uint32_t u[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        top = max(top, max(u[k] << 16 & 0x7FFF0000u, u[k] & 0x7FFF0000u));
+#pragma unroll
+                    for (int d = kChunks / 2; d > 0; d >>= 1)
+                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    // 2^(14 - exponent), at most 2^126
+                    const int e = max(static_cast<int>(top >> 23), 15);
+                    const float up = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        h[k] = narrow2(sv::bf16_lo(u[k]) * up, sv::bf16_hi(u[k]) * up, F16());
+                    qv[i] = make_uint4(h[0], h[1], h[2], h[3]);
+                    if (has && ch == 0)
+                        ctl.q_scale[r] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+                }
+                if (has)
+                    st_shared_v4(sq + (r >> 7) * (128 * DP * 2) +
+                                     tile_chunk(r & 127, ch, 1024, X::kPanel),
+                                 qv[i]);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) sv::mbar_arrive(&ctl.q_ready);
+        };
+
+        const Plan* ahead = plan_at(0);
+        if (ahead != nullptr) {
+            fetch(*ahead);
+            store(*ahead);
+        }
+        bool ok = true;
+        for (; ahead != nullptr; ++item) {
+            const Plan& g = *ahead;
+            const int rows = g.rows;
+            const bool live = warp_row < rows;  // some row of this warp exists
             float m = ninf, l = 0.f;
             bool begun = false;
-            for (int j = mine.lo; j < mine.hi; j += mine.step) {
-                if (!(ok = wait_all(&ctl.s_full[s], tiles_done))) break;
-                ++tiles_done;
-                if (live) {
-                    fence_after();
-                    const int64_t p0 = static_cast<int64_t>(j) << kTileShift;
-                    const int clo = static_cast<int>(max(low - p0, int64_t(0)));
-                    const int chi = static_cast<int>(min(pos - p0, int64_t(kTile - 1)));
-                    const bool masked =
-                        __any_sync(0xFFFFFFFFu, clo > 0 || chi < kTile - 1) != 0;
-                    float top = ninf;
+            {
+                // The last position that the row sees, and the first.
+                const int pos = g.cached + (g.row0 + min(slot_row, rows - 1)) / a.G;
+                const int low = a.window > 0 ? pos - static_cast<int>(a.window) + 1 : INT_MIN / 2;
+                const int k0 = PAIR ? (s ? g.lo1 : g.lo0) : s;
+                const int k1 = PAIR ? (s ? g.hi1 : g.hi0) : g.n;
+                float c = a.scale_log2;
+                for (int k = k0; k < k1; k += PAIR ? 1 : 2) {
+                    if (!(ok = wait_all(&ctl.s_full[s], tiles_done))) break;
+                    ++tiles_done;
+                    if (live) {
+                        fence_after();
+                        if (E4M3 && std::is_same<T, Bf16>::value && !begun)
+                            c = a.scale_log2 * ctl.q_scale[min(slot_row, rows - 1)];
+                        const int clo = low - k * kTile, chi = pos - k * kTile;
+                        const bool masked =
+                            __any_sync(0xFFFFFFFFu, clo > 0 || chi < kTile - 1) != 0;
+                        // Scores of columns 64 x .., in units of the scale.
+                        auto half = [&](int x, float (&v)[64]) {
+                            tmem_ld(s_addr + 64 * x, v);
+                            if constexpr (E4M3) {
+                                const float4* ks = reinterpret_cast<const float4*>(
+                                    &ctl.k_scale[(tiles_before + k) & 3][64 * x]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float v[32];
-                        tmem_ld32(s_addr + 32 * k, v);
-                        if (masked) {
+                                for (int i = 0; i < 16; ++i) {
+                                    const float4 k4 = ks[i];
+                                    const float2 p = mul2f(make_float2(v[4 * i], v[4 * i + 1]),
+                                                           make_float2(k4.x, k4.y));
+                                    const float2 q = mul2f(make_float2(v[4 * i + 2], v[4 * i + 3]),
+                                                           make_float2(k4.z, k4.w));
+                                    v[4 * i] = p.x;
+                                    v[4 * i + 1] = p.y;
+                                    v[4 * i + 2] = q.x;
+                                    v[4 * i + 3] = q.y;
+                                }
+                            }
+                            if (masked) {
+                                const int lo = clo - 64 * x, hi = chi - 64 * x;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[i] = 32 * k + i >= clo && 32 * k + i <= chi ? v[i] : ninf;
-                        }
-                        float t0 = v[0], t1 = v[1];
+                                for (int i = 0; i < 64; ++i) v[i] = i >= lo && i <= hi ? v[i] : ninf;
+                            }
+                        };
+                        auto top_of = [&](const float (&v)[64]) {
+                            float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
 #pragma unroll
-                        for (int i = 2; i < 32; i += 2) {
-                            t0 = fmaxf(t0, v[i]);
-                            t1 = fmaxf(t1, v[i + 1]);
-                        }
-                        top = fmaxf(top, fmaxf(t0, t1));
-                    }
-                    const float mt = top * c;  // (scale > 0)
-                    const bool grow = mt > m + kSlack || (!begun && mt > m);
-                    if (begun && __any_sync(0xFFFFFFFFu, grow)) {
-                        // The slot's products so far are complete: s_full's commit
-                        // came after them.
-                        const float keep = grow ? sv::ex2(m - mt) : 1.f;
+                            for (int i = 4; i < 64; i += 4) {
+                                t0 = fmaxf(t0, v[i]);
+                                t1 = fmaxf(t1, v[i + 1]);
+                                t2 = fmaxf(t2, v[i + 2]);
+                                t3 = fmaxf(t3, v[i + 3]);
+                            }
+                            return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+                        };
+                        // The maximum over both halves, then the weights: of the
+                        // second half, which is in registers, and of the first,
+                        // read again. A row of 128 scores would not fit beside
+                        // what else the thread holds.
+                        float v[64];
+                        half(0, v);
+                        float mt = top_of(v);
+                        half(1, v);
+                        // (scale > 0; a NaN score is left out here and comes through below)
+                        mt = fmaxf(mt, top_of(v)) * c;
+                        const bool grow = mt > m + kSlack || (!begun && mt > m);
+                        if (begun && __any_sync(0xFFFFFFFFu, grow)) {
+                            // The slot's products so far are complete: s_full's
+                            // commit came after them.
+                            const float keep = grow ? sv::ex2(m - mt) : 1.f;
 #pragma unroll 1
-                        for (int k = 0; k < DP / 32; ++k) {
-                            float v[32];
-                            tmem_ld32(o_addr + 32 * k, v);
+                            for (int x = 0; x < DP / 16; ++x) {
+                                float o[16];
+                                tmem_ld(o_addr + 16 * x, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= keep;
-                            tmem_st32(o_addr + 32 * k, v);
+                                for (int i = 0; i < 16; ++i) o[i] *= keep;
+                                tmem_st(o_addr + 16 * x, o);
+                            }
+                            l *= keep;
                         }
-                        l *= keep;
+                        if (grow) m = mt;
+                        begun = true;
+                        const float shift = m == ninf ? 0.f : -m;
+                        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+                        // P takes the columns of the second half.
+                        auto weigh = [&](int x) {
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                uint32_t w[16];
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    const int z = 32 * y + 2 * i;
+                                    float2 p = fma2(make_float2(v[z], v[z + 1]), c, shift);
+                                    float2 q = fma2(make_float2(v[z + 2], v[z + 3]), c, shift);
+                                    p = make_float2(sv::ex2(p.x), sv::ex2(p.y));
+                                    q = make_float2(sv::ex2(q.x), sv::ex2(q.y));
+                                    l0 = add2(l0, p);
+                                    l1 = add2(l1, q);
+                                    w[i] = narrow2(p.x, p.y, T());
+                                    w[i + 1] = narrow2(q.x, q.y, T());
+                                }
+                                tmem_st(s_addr + 64 + 32 * x + 16 * y, w);
+                            }
+                        };
+                        weigh(1);
+                        half(0, v);
+                        weigh(0);
+                        l += (l0.x + l0.y) + (l1.x + l1.y);
+                        tmem_wait_st();
+                        fence_before();
                     }
-                    if (grow) m = mt;
-                    begun = true;
-                    const float shift = m == ninf ? 0.f : -m;
-                    float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float v[32];
-                        uint32_t w[16];
-                        tmem_ld32(s_addr + 32 * k, v);
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[i] = 32 * k + i >= clo && 32 * k + i <= chi ? v[i] : ninf;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float p0f = sv::ex2(fmaf(v[i], c, shift));
-                            const float p1f = sv::ex2(fmaf(v[i + 1], c, shift));
-                            l0 += p0f;
-                            l1 += p1f;
-                            w[i / 2] = narrow2(p0f, p1f, T());
-                        }
-                        tmem_st16(s_addr + 16 * k, w);
-                    }
-                    l += l0 + l1;
-                    tmem_wait_st();
-                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) sv::mbar_arrive(&ctl.p_ready[s]);
                 }
-                __syncwarp();
-                if (lane == 0) sv::mbar_arrive(&ctl.p_ready[s]);
             }
             if (!ok) break;
 
             // --------------------------------------------------------------
             // The rows' results.
             // --------------------------------------------------------------
-            bool has[2] = {begun, false};
-            float wt[2] = {1.f, 0.f};
+            const int n = g.n;
+            tiles_before += n;
+            ahead = plan_at(item + 1);
+            if (ahead != nullptr) fetch(*ahead);
+            if (!(ok = wait_all(&ctl.o_full, item))) break;
+            fence_after();
+            float w0 = 1.f, w1 = 0.f;
             if (!PAIR) {
-                ctl.ml[s][row] = make_float2(m, l);
+                // The slots exchange their rows' maxima and sums through the
+                // scores' columns, which the products have done with.
+                if (live) {
+                    tmem_st2(s_addr, m, l);
+                    tmem_wait_st();
+                    fence_before();
+                }
                 __syncwarp();
                 if (lane == 0) sv::mbar_arrive(&ctl.ml_ready);
                 if (!(ok = wait_all(&ctl.ml_ready, item))) break;
-                const float2 x0 = ctl.ml[0][row], x1 = ctl.ml[1][row];
-                has[0] = g.t.lo < g.t.hi;
-                has[1] = g.t.lo + 1 < g.t.hi;
-                m = fmaxf(x0.x, x1.x);
-                wt[0] = x0.x == m ? 1.f : sv::ex2(x0.x - m);
-                wt[1] = x1.x == m ? 1.f : sv::ex2(x1.x - m);
-                l = x0.y * wt[0] + x1.y * wt[1];
+                if (live) {
+                    fence_after();
+                    float om, ol;
+                    tmem_ld2(lane_base + (1 - s) * 128, om, ol);
+                    fence_before();
+                    const float top = fmaxf(m, om);
+                    const float wm = m == top ? 1.f : sv::ex2(m - top);
+                    const float wo = om == top ? 1.f : sv::ex2(om - top);
+                    w0 = s ? wo : wm;
+                    w1 = s ? wm : wo;
+                    // (the same order in both slots)
+                    l = (s ? ol : l) * w0 + (s ? l : ol) * w1;
+                    m = top;
+                }
+                __syncwarp();
             }
-            if (!(ok = wait_all(&ctl.o_full, item))) break;
-            fence_after();
-            const bool whole = g.t.lo == g.item.lo && g.t.hi == g.item.hi;
-            const bool valid = slot_row < g.rows;
+            if (ahead != nullptr) store(*ahead);
+            const bool whole = g.whole != 0, valid = slot_row < rows;
             // A row that sees a noted position is computed again below.
             const int noted = *reinterpret_cast<volatile int*>(&ctl.noted[item % kItems]);
             const bool bad = *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0;
+            const int r = g.row0 + min(slot_row, rows - 1), token = r / a.G;
             bool again = noted > kNoted;
-            for (int i = 0; i < min(noted, kNoted); ++i) {
-                const int64_t p = *reinterpret_cast<volatile uint32_t*>(&ctl.note[item % kItems][i]);
-                again |= p >= low && p <= pos;
+            if (noted > 0) {
+                const int pos = g.cached + token;
+                const int low = a.window > 0 ? pos - static_cast<int>(a.window) + 1 : INT_MIN / 2;
+                for (int i = 0; i < min(noted, kNoted); ++i) {
+                    const int p = *reinterpret_cast<volatile int*>(&ctl.note[item % kItems][i]);
+                    again |= p >= low && p <= pos;
+                }
             }
             again = again && valid && !bad;
             const float nan = __uint_as_float(0x7FFFFFFFu);
-            const float inv = bad ? nan : (whole ? 1.f / l : 1.f);
-            const int64_t orow = valid ? out_row(a, g.q0, g.h, r) : 0;
-            float* part = args.part +
-                          ((static_cast<int64_t>(blockIdx.x) * 2 + (g.t.lo == g.item.lo ? 1 : 0)) *
-                               args.part_rows + slot_row) * (DP + 4);
+            float* share = args.part + (static_cast<int64_t>(blockIdx.x) * 2 + (g.begins ? 1 : 0)) *
+                                           args.part_rows * (DP + 4);
             if (live) {
-                // !PAIR: slot s writes its half of the columns.
-                constexpr int kParts = DP / 32;
-                const int k0 = PAIR ? 0 : s * kParts / 2, k1 = PAIR ? kParts : (s + 1) * kParts / 2;
+                // Columns of the row, kCols at a time: all, or the slot's half
+                // where both slots hold the row.
+                constexpr int kCols = PAIR ? 64 : DP / 2;
+                const int64_t orow = (static_cast<int64_t>(g.q0) + token) * a.Hq + g.h * a.G +
+                                     (r - token * a.G);
+                const float inv = bad ? nan : (whole ? 1.f / l : 1.f);
+                float* part = share + static_cast<int64_t>(slot_row) * (DP + 4);
 #pragma unroll 1
-                for (int k = k0; k < k1; ++k) {
-                    float o[32];
+                for (int x = 0; x < (PAIR ? DP / 64 : 1); ++x) {
+                    const int k0 = PAIR ? 64 * x : s * kCols;
+                    float o[kCols];
                     __syncwarp();
-                    if (PAIR) {
-                        if (has[0]) {
-                            tmem_ld32(o_addr + 32 * k, o);
-                        } else {
+                    if constexpr (PAIR) {
+                        tmem_ld(o_addr + k0, o);
+                        if (!begun) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                            for (int i = 0; i < kCols; ++i) o[i] = 0.f;
                         }
                     } else {
-                        tmem_ld32(lane_base + 256 + 32 * k, o);
-                        if (has[1]) {
-                            float p[32];
-                            tmem_ld32(lane_base + 256 + DP + 32 * k, p);
+                        float p[kCols];
+                        // (slot 1 without a tile: its columns are read and not used)
+                        tmem_ld(lane_base + 256 + k0, o, lane_base + 256 + DP + k0, p);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = o[i] * wt[0] + p[i] * wt[1];
-                        }
+                        for (int i = 0; i < kCols; ++i) o[i] = n > 1 ? o[i] * w0 + p[i] * w1 : o[i];
                     }
                     if (!valid || again) continue;
-                    if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            if (32 * k + i < a.c.D)
-                                *reinterpret_cast<uint4*>(a.out +
-                                                          (orow * a.c.D + 32 * k + i) * 2) =
-                                    make_uint4(narrow2(o[i] * inv, o[i + 1] * inv, T()),
-                                               narrow2(o[i + 2] * inv, o[i + 3] * inv, T()),
-                                               narrow2(o[i + 4] * inv, o[i + 5] * inv, T()),
-                                               narrow2(o[i + 6] * inv, o[i + 7] * inv, T()));
+                    for (int i = 0; i < kCols; ++i) o[i] *= inv;
+                    if (whole) {
+                        uint8_t* to = a.out + (orow * a.c.D + k0) * 2;
+#pragma unroll
+                        for (int i = 0; i < kCols; i += 8)
+                            if (k0 + i < a.c.D)
+                                *reinterpret_cast<uint4*>(to + i * 2) =
+                                    make_uint4(narrow2(o[i], o[i + 1], T()),
+                                               narrow2(o[i + 2], o[i + 3], T()),
+                                               narrow2(o[i + 4], o[i + 5], T()),
+                                               narrow2(o[i + 6], o[i + 7], T()));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4*>(part + 32 * k + i) =
-                                make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+                        for (int i = 0; i < kCols; i += 4)
+                            *reinterpret_cast<float4*>(part + k0 + i) =
+                                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
                 }
-                __syncwarp();
                 if (valid && !again && (PAIR || s == 0)) {
                     if (!whole) {
                         part[DP] = m;
@@ -632,262 +837,308 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         a.lse[orow] = bad ? nan : fmaf(m, kLn2, logf(l));
                     }
                 }
+                __syncwarp();
                 unsigned todo = PAIR || s == 0 ? __ballot_sync(0xFFFFFFFFu, again) : 0u;
                 while (todo != 0) {
                     const int i = __ffs(static_cast<int>(todo)) - 1;
                     todo &= todo - 1;
-                    const int ri = g.row0 + warp_row + i;
-                    const int64_t pi = g.cached + ri / a.G, row_i = out_row(a, g.q0, g.h, ri);
-                    const int64_t lo = max(first_key(a, pi), static_cast<int64_t>(g.t.lo) << kTileShift);
-                    const int64_t hi = min(pi + 1, static_cast<int64_t>(g.t.hi) << kTileShift);
-                    const int64_t t = row_i / a.Hq;
-                    float om, ol, o[8];
-                    attend_row<T, E4M3>(a, g.b, g.h, a.q + t * a.q_token + (row_i - t * a.Hq) * a.q_head,
-                                        lo, hi, lane, &om, &ol, o);
-                    if (whole) {
-                        const float x = 1.f / ol;
-                        if (lane * 8 < a.c.D)
-                            *reinterpret_cast<uint4*>(a.out + (row_i * a.c.D + lane * 8) * 2) =
-                                make_uint4(narrow2(o[0] * x, o[1] * x, T()),
-                                           narrow2(o[2] * x, o[3] * x, T()),
-                                           narrow2(o[4] * x, o[5] * x, T()),
-                                           narrow2(o[6] * x, o[7] * x, T()));
-                        if (a.lse != nullptr && lane == 0) a.lse[row_i] = fmaf(om, kLn2, logf(ol));
-                    } else {
-                        float* p = args.part +
-                                   ((static_cast<int64_t>(blockIdx.x) * 2 +
-                                     (g.t.lo == g.item.lo ? 1 : 0)) * args.part_rows +
-                                    warp_row + i) * (DP + 4);
-                        if (lane * 8 < DP) {
-                            *reinterpret_cast<float4*>(p + lane * 8) =
-                                make_float4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<float4*>(p + lane * 8 + 4) =
-                                make_float4(o[4], o[5], o[6], o[7]);
-                        }
-                        if (lane == 0) {
-                            p[DP] = om;
-                            p[DP + 1] = ol;
-                        }
-                    }
+                    again_row<T, E4M3, DP>(args, g, warp_row + i,
+                                           share + static_cast<int64_t>(warp_row + i) * (DP + 4));
                 }
                 fence_before();
             }
-            // The notes of the item before: every warp has read them (this item's
-            // products began after all had), and the item that gets their place
-            // waits for products that come after this thread's next arrival.
+            // The notes of two segments before: their readers have all come to
+            // this one since, and the segment that gets their place is still out
+            // of the loads' reach.
             __syncwarp();
             if (threadIdx.x == 0) {
-                ctl.noted[(item + kItems - 1) % kItems] = 0;
-                ctl.bad_page[(item + kItems - 1) % kItems] = 0;
+                ctl.noted[(item + kItems - 2) % kItems] = 0;
+                ctl.bad_page[(item + kItems - 2) % kItems] = 0;
             }
+            if (lane == 0) sv::mbar_arrive(&ctl.o_free);
         }
     } else if (warp == 8) {
         // ------------------------------------------------------------------
-        // Products, from one lane.
+        // Products: the warp stays together, one lane issues.
         // ------------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc<T, kTile, false>(), id_o = idesc<T, DP, true>();
-            int64_t ring = 0;
-            uint32_t fixes = 0;      // parity of each stage's next fix
-            uint32_t p_count[2] = {0, 0};
-            bool ok = true;
-            for (; ok && walk.next(&g); ++item) {
-                if (!(ok = wait(&ctl.q_ready, item))) break;
-                fence_after();
-                const int n = g.t.hi - g.t.lo;
-                const SlotTiles mine[2] = {slot_tiles<PAIR>(a, g, 0), slot_tiles<PAIR>(a, g, 1)};
-                const Seen seen = item_seen(a, g);
-                bool out[2] = {false, false}, begun[2] = {false, false};
-                int qj = g.t.lo, qs = 0, vj = g.t.lo, vs = 0;
-                auto settle = [&](int& j, int& s) {
-                    while (j < g.t.hi && !works_on(mine[s], j)) {
-                        s ^= 1;
-                        if (s == 0) ++j;
-                    }
-                };
-                auto last_user = [&](int j, int s) { return s == 1 || !works_on(mine[1], j); };
-                settle(qj, qs);
-                settle(vj, vs);
-                while (vj < g.t.hi) {
-                    while (qj < g.t.hi && !out[qs]) {
-                        const int64_t at = ring_k<PAIR>(ring, qj - g.t.lo);
-                        const int stage = static_cast<int>(at % S);
-                        if (!(ok = wait(&ctl.full[stage], static_cast<uint32_t>(at / S)))) break;
-                        fence_after();
-                        const uint32_t q = sq + (PAIR ? qs * 128 * DP * 2 : 0);
-                        const uint32_t k = st + stage * X::kTileBytes;
+        using TS = typename std::conditional<E4M3, F16, T>::type;
+        constexpr uint32_t id_s = idesc<TS, kTile, false>(), id_o = idesc<T, DP, true>();
+        const uint64_t dq = smem_desc(sq, 16, 1024), dk = smem_desc(st, 16, args.group),
+                       dv = smem_desc(st, args.panel, args.group);
+        const uint32_t panel = args.panel >> 4, v_step = args.group >> 3;  // 16 keys: two groups
+        Place<S> base_at;
+        uint32_t fixes = 0, p_count0 = 0, p_count1 = 0;
+        bool ok = true;
+        for (; ok; ++item) {
+            const Plan* g = plan_at(item);
+            if (g == nullptr || !(ok = wait_all(&ctl.q_ready, item))) break;
+            const int n = g->n, inner_lo = g->inner_lo, inner_hi = g->inner_hi;
+            // PAIR: the slots' tiles; every tile has at least one of them.
+            const int lo0 = g->lo0, hi0 = g->hi0, lo1 = g->lo1, hi1 = g->hi1;
+            auto in0 = [&](int k) { return k >= lo0 && k < hi0; };
+            auto in1 = [&](int k) { return k >= lo1 && k < hi1; };
+            auto step = [&](int& k, int& sl) {
+                if (!PAIR) {
+                    ++k;
+                    sl ^= 1;
+                } else if (sl == 0 && in1(k)) {
+                    sl = 1;
+                } else {
+                    ++k;
+                    sl = in0(k) ? 0 : 1;
+                }
+            };
+            auto last_user = [&](int k, int sl) { return !PAIR || sl == 1 || !in1(k); };
+            const int s0 = !PAIR || in0(0) ? 0 : 1;
+            int qk = 0, qs = s0, vk = 0, vs = s0;
+            uint32_t out = 0, begun = 0;  // bit s: slot s's scores are under way; has a product
+            Place<S> kat = base_at, vat = base_at;
+            vat.advance(ring_v<PAIR>(0, n));
+            bool freed = item == 0;  // the results before have been read
+            while (vk < n) {
+                while (qk < n && !(out >> qs & 1u)) {
+                    if (!(ok = wait_all(&ctl.full[kat.stage], kat.round))) break;
+                    fence_after();
+                    const bool last = last_user(qk, qs);
+                    if (elect_one()) {
+                        const uint64_t q = dq + (PAIR ? qs * (128 * DP * 2 >> 4) : 0);
+                        const uint64_t k = dk + kat.stage * (X::kTileBytes >> 4);
 #pragma unroll
                         for (int i = 0; i < DP / 16; ++i) {
-                            const uint32_t o = (i >> 2) * X::kPanel + (i & 3) * 32;
-                            mma_ss(tmem + qs * 128, smem_desc(q + o, 16), smem_desc(k + o, 16), id_s,
-                                   i > 0);
+                            const uint32_t o = (i & 3) * 2;
+                            mma_ss(tmem + qs * 128, q + o + (i >> 2) * (X::kPanel >> 4),
+                                   k + o + (i >> 2) * panel, id_s, i > 0);
                         }
                         mma_commit(&ctl.s_full[qs]);
-                        if (last_user(qj, qs)) mma_commit(&ctl.empty[stage]);
-                        out[qs] = true;
-                        qs ^= 1;
-                        if (qs == 0) ++qj;
-                        settle(qj, qs);
+                        if (last) mma_commit(&ctl.empty[kat.stage]);
                     }
-                    if (!ok) break;
-                    const int64_t at = ring_v<PAIR>(ring, vj - g.t.lo, n);
-                    const int stage = static_cast<int>(at % S);
-                    if (!(ok = wait(&ctl.full[stage], static_cast<uint32_t>(at / S)))) break;
-                    if (!E4M3 && at_edge(seen, vj) && (PAIR ? (vs == 0 || !works_on(mine[0], vj)) : true)) {
-                        if (!(ok = wait(&ctl.fixed[stage], fixes >> stage))) break;
-                        fixes ^= 1u << stage;
-                    }
-                    if (!(ok = wait(&ctl.p_ready[vs], p_count[vs]))) break;
-                    ++p_count[vs];
-                    fence_after();
-                    const uint32_t v = st + stage * X::kTileBytes;
-#pragma unroll
-                    for (int i = 0; i < kTile / 16; ++i)
-                        mma_ts(tmem + 256 + vs * DP, tmem + vs * 128 + i * 8,
-                               smem_desc(v + i * 2048, X::kPanel), id_o, begun[vs] || i > 0);
-                    begun[vs] = true;
-                    out[vs] = false;
-                    if (last_user(vj, vs)) mma_commit(&ctl.empty[stage]);
-                    vs ^= 1;
-                    if (vs == 0) ++vj;
-                    settle(vj, vs);
+                    __syncwarp();
+                    out |= 1u << qs;
+                    const int was = qk;
+                    step(qk, qs);
+                    if (qk != was) kat.advance(ring_k_step<PAIR>(was));
                 }
                 if (!ok) break;
-                mma_commit(&ctl.o_full);
-                ring += 2 * n;
+                if (!(ok = wait_all(&ctl.full[vat.stage], vat.round))) break;
+                if (!E4M3 && (vk < inner_lo || vk > inner_hi) && (!PAIR || vs == 0 || !in0(vk))) {
+                    if (!(ok = wait_all(&ctl.fixed[vat.stage], fixes >> vat.stage))) break;
+                    fixes ^= 1u << vat.stage;
+                }
+                if (!freed) {
+                    if (!(ok = wait_all(&ctl.o_free, item - 1))) break;
+                    freed = true;
+                }
+                if (!(ok = wait_all(&ctl.p_ready[vs], vs ? p_count1 : p_count0))) break;
+                if (vs)
+                    ++p_count1;
+                else
+                    ++p_count0;
+                fence_after();
+                const bool last = last_user(vk, vs);
+                if (elect_one()) {
+                    const uint64_t v = dv + vat.stage * (X::kTileBytes >> 4);
+                    const bool more = (begun >> vs & 1u) != 0;
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i)
+                        mma_ts(tmem + 256 + vs * DP, tmem + vs * 128 + 64 + i * 8, v + i * v_step, id_o,
+                               more || i > 0);
+                    if (last) mma_commit(&ctl.empty[vat.stage]);
+                }
+                __syncwarp();
+                begun |= 1u << vs;
+                out &= ~(1u << vs);
+                const int was = vk;
+                step(vk, vs);
+                if (vk != was) vat.advance(ring_v_step<PAIR>(was, n));
             }
-            // Everything issued has completed once this arrives.
-            mma_commit(&ctl.done);
-            sv::mbar_wait_bounded(&ctl.done, 0, nullptr);
+            if (!ok) break;
+            if (elect_one()) mma_commit(&ctl.o_full);
+            __syncwarp();
+            base_at.advance(2 * n);
         }
-    } else if (warp == 9) {
+        // Everything issued has completed once this arrives.
+        if (elect_one()) mma_commit(&ctl.done);
+        __syncwarp();
+        sv::mbar_wait_bounded(&ctl.done, 0, nullptr);
+    } else if (warp < 11) {
         // ------------------------------------------------------------------
-        // Copies.
+        // Copies of keys (warp 9, which also plans the segments) and values
+        // (warp 10). The page of tile k + 2 and the exponents of tile k + 1 are
+        // on their way while tile k is issued.
         // ------------------------------------------------------------------
+        const int kv = warp - 9;
+        const CUtensorMap* map = kv ? &vmap : &kmap;
         uint64_t* fullbar = E4M3 ? ctl.raw_full : ctl.full;
         uint64_t* emptybar = E4M3 ? ctl.raw_empty : ctl.empty;
         const int P = 1 << a.c.page_shift, box = min(P, kTile);
-        const int row_bytes = a.c.D;  // of a raw e4m3 row
-        int64_t ring = 0, issued = 0;
+        const uint32_t box_bytes = E4M3 ? box * a.c.D : box * DP * 2;
+        const uint32_t lane_bytes = E4M3 ? lane * 4 * a.c.D : lane * 4 / 8 * args.group;
+        const bool first_of_box = P >= kTile ? lane == 0 : ((lane * 4) & (P - 1)) == 0;
+        const uint8_t* exps = kv ? a.c.exps[1] : a.c.exps[0];
+        const int64_t exp_step = kv ? a.c.exp_slot_stride[1] : a.c.exp_slot_stride[0];
+        Place<kFill> base_at;
+        uint32_t used = 0, rounds = 0;  // a stage's bit: filled by this warp; parity of the last fill
+        Walk<R> walk(a, start);
+        Share sh{};
+        int64_t units = start.u0;
         bool ok = true;
-        for (; ok && walk.next(&g); ++item) {
-            const int n = g.t.hi - g.t.lo;
-            const Seen seen = item_seen(a, g);
-            // Page and exponents of this lane's four positions in tile k; loaded
-            // one tile ahead.
-            auto page_at = [&](int k) {
-                const int64_t p = (static_cast<int64_t>(g.t.lo + k) << kTileShift) + lane * 4;
-                // (a page is needed if any of its positions is seen)
-                const int64_t page0 = p & ~static_cast<int64_t>(P - 1);
-                if (k >= n || page0 > seen.any_hi || page0 + P - 1 < seen.any_lo) return INT_MIN;
-                return page_of(a.c, g.b, p);
-            };
-            auto load_tile = [&](int kv, int k, int32_t page) {
-                const int64_t at = kv == 0 ? ring_k<PAIR>(ring, k) : ring_v<PAIR>(ring, k, n);
-                const int stage = static_cast<int>(at % kFill);
-                const int64_t round = at / kFill;
-                const bool needed = page != INT_MIN;
-                // A page out of range: page 0 in its place, and NaN for the item.
-                const bool bad = needed && page < 0;
-                if (bad) page = 0;
-                const int slot = (lane * 4) & (P - 1);
-                const int64_t p = (static_cast<int64_t>(g.t.lo + k) << kTileShift) + lane * 4;
-                uint32_t e4 = 0;
-                if (E4M3 && needed) {
-                    const uint8_t* e = (kv ? a.c.exps[1] : a.c.exps[0]) +
-                                       exp_at(a.c, kv, page, static_cast<int32_t>(p) & (P - 1), g.h);
-                    const int64_t es = kv ? a.c.exp_slot_stride[1] : a.c.exp_slot_stride[0];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) e4 |= static_cast<uint32_t>(e[i * es]) << (8 * i);
+        for (; ok; ++item) {
+            const Plan* g;
+            if (kv == 0) {
+                Segment seg;
+                const bool any = walk.next(&seg);
+                Plan p{};
+                if (any) {
+                    p = plan_of<PAIR>(a, seg);
+                    units += p.n;
+                    if (p.begins && !p.whole) {
+                        // For join_kernel: the item that this block began and did
+                        // not finish, and the block that did.
+                        const int64_t end = units + (seg.item.hi - seg.t.hi) - 1;  // its last unit
+                        int c = blockIdx.x + 1;
+                        while (share_begin(start.U, c + 1, gridDim.x) <= end) ++c;
+                        sh.leads = 1;
+                        sh.b = p.b;
+                        sh.h = p.h;
+                        sh.row0 = p.row0;
+                        sh.rows = p.rows;
+                        sh.q0 = p.q0;
+                        sh.last = c;
+                    }
                 }
-                if (round > 0 && !wait_all(&emptybar[stage], static_cast<uint32_t>(round - 1)))
-                    return false;
-                if (bad) {
-                    *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) = 1;
-                    if (a.status != nullptr) atomicOr(a.status + g.b, kBadPage);
+                // (Its place was the plan of kItems segments ago, which the ring
+                // of tiles keeps out of everybody's reach.)
+                if (lane == 0) {
+                    ctl.plan[item % kItems] = p;
+                    sv::mbar_arrive(&ctl.plan_ready[item % kItems]);
                 }
-                if (E4M3) *reinterpret_cast<uint32_t*>(&ctl.exps[stage][lane * 4]) = e4;
-                // One lane a box: the lane whose first position is the box's first.
-                const bool leader = needed && (P >= kTile ? lane == 0 : slot == 0);
-                const unsigned boxes = __ballot_sync(0xFFFFFFFFu, leader);
-                const uint32_t bytes = E4M3 ? box * row_bytes : box * DP * 2;
                 __syncwarp();
+                if (!any) break;
+                g = &ctl.plan[item % kItems];
+            } else if ((g = plan_at(item)) == nullptr) {
+                break;
+            }
+            const int n = g->n, any_lo = g->any_lo, any_hi = g->any_hi, h = g->h;
+            const int64_t page_row = g->b * a.c.table_stride +
+                                     ((static_cast<int64_t>(g->tile0) << kTileShift) >> a.c.page_shift);
+            const int in_page0 =
+                static_cast<int>((static_cast<int64_t>(g->tile0) << kTileShift) & (P - 1));
+            // The table's entry for this lane's four positions in tile k; INT_MIN
+            // if no row sees a position of that page.
+            auto entry = [&](int k) {
+                const int p = k * kTile + lane * 4 + in_page0;  // from the first tile's page
+                const int page0 = (p & ~(P - 1)) - in_page0;
+                return k < n && page0 <= any_hi && page0 + P - 1 >= any_lo
+                           ? a.c.table[page_row + (p >> a.c.page_shift)]
+                           : INT_MIN;
+            };
+            auto good = [&](int32_t page) { return page >= 0 && page < a.c.num_pages; };
+            auto slot_of = [&](int k) { return (k * kTile + lane * 4 + in_page0) & (P - 1); };
+            struct Exps {
+                uint32_t e[4];
+            };
+            auto exps_of = [&](int k, int32_t page) {
+                Exps x{};
+                if (E4M3 && page != INT_MIN) {
+                    const uint8_t* e = exps + exp_at(a.c, kv, good(page) ? page : 0, slot_of(k), h);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x.e[i] = e[i * exp_step];
+                }
+                return x;
+            };
+            int32_t cur = entry(0), next = entry(1);
+            Exps xc = exps_of(0, cur), xn = exps_of(1, next);
+            Place<kFill> at = base_at;
+            if (kv) at.advance(ring_v<PAIR>(0, n));
+            for (int k = 0; k < n; ++k) {
+                const int32_t after = entry(k + 2);
+                const bool needed = cur != INT_MIN;
+                // A page out of range: page 0 in its place, and NaN for the item.
+                const bool bad = needed && !good(cur);
+                if (at.round > 0 && !(ok = wait_all(&emptybar[at.stage], at.round - 1))) break;
+                if (bad) {
+                    cur = 0;
+                    *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) = 1;
+                    if (a.status != nullptr) atomicOr(a.status + g->b, kBadPage);
+                }
+                if (E4M3)
+                    *reinterpret_cast<uint32_t*>(&ctl.exps[at.stage][lane * 4]) =
+                        xc.e[0] | xc.e[1] << 8 | xc.e[2] << 16 | xc.e[3] << 24;
+                const bool leader = needed && first_of_box;
+                const unsigned boxes = __ballot_sync(0xFFFFFFFFu, leader);
                 if (lane == 0)
-                    sv::mbar_arrive_expect_tx(&fullbar[stage], __popc(boxes) * bytes);
+                    sv::mbar_arrive_expect_tx(&fullbar[at.stage], __popc(boxes) * box_bytes);
                 __syncwarp();
                 if (leader) {
-                    const CUtensorMap* map = kv ? &vmap : &kmap;
-                    const int c1 = static_cast<int>(p) & (P - 1);
+                    const int c1 = slot_of(k);
                     if (E4M3) {
-                        tma_load_4d(sr + stage * X::kRawBytes + lane * 4 * row_bytes, map, 0, c1,
-                                    g.h, page, &fullbar[stage]);
+                        tma_load_4d(sr + at.stage * X::kRawBytes + lane_bytes, map, 0, c1, h, cur,
+                                    &fullbar[at.stage]);
+                    } else if (args.page_heads > 0) {
+                        tma_load_5d(st + at.stage * X::kTileBytes + lane_bytes, map, 0, 0, 0, c1 >> 3,
+                                    cur * args.page_heads + h * args.head_step, &fullbar[at.stage]);
                     } else {
 #pragma unroll
                         for (int q = 0; q < DP / 64; ++q)
-                            tma_load_4d(st + stage * X::kTileBytes + q * X::kPanel + lane * 512,
-                                        map, q * 64, c1, g.h, page, &fullbar[stage]);
+                            tma_load_4d(st + at.stage * X::kTileBytes + q * X::kPanel + lane_bytes,
+                                        map, q * 64, c1, h, cur, &fullbar[at.stage]);
                     }
                 }
-                issued = at + 1;
-                return true;
-            };
-            int32_t cur = page_at(0), next = page_at(1);
-            ok = load_tile(0, 0, cur);
-            for (int k = 0; ok && k < n; ++k) {
-                const int32_t after = page_at(k + 2);
-                if (PAIR) {
-                    ok = load_tile(1, k, cur) && (k + 1 >= n || load_tile(0, k + 1, next));
-                } else {
-                    ok = (k + 1 >= n || load_tile(0, k + 1, next)) && load_tile(1, k, cur);
-                }
+                __syncwarp();
+                used |= 1u << at.stage;
+                rounds = (rounds & ~(1u << at.stage)) | (at.round & 1u) << at.stage;
+                at.advance(kv ? ring_v_step<PAIR>(k, n) : ring_k_step<PAIR>(k));
                 cur = next;
                 next = after;
+                xc = xn;
+                xn = exps_of(k + 2, next);
             }
-            ring += 2 * n;
+            base_at.advance(2 * n);
+        }
+        if (kv == 0 && lane == 0) {
+            sh.units = start.U;
+            args.shares[blockIdx.x] = sh;
         }
         if (!ok) {
             // No copy may be under way when the block ends.
-            const int64_t first = issued > kFill ? issued - kFill : 0;
-            for (int64_t i = first; i < issued; ++i)
-                sv::mbar_wait_bounded(&fullbar[i % kFill], static_cast<uint32_t>((i / kFill) & 1),
-                                      nullptr);
+            for (int i = 0; i < kFill; ++i)
+                if (used >> i & 1u) sv::mbar_wait_bounded(&fullbar[i], rounds >> i & 1u, nullptr);
         }
     } else {
         // ------------------------------------------------------------------
-        // Helpers: hidden values, and e4m3.
+        // Helpers: hidden values, and e4m3. They pass every tile in order (else
+        // a parity could stand for another round of the stage than they mean).
         // ------------------------------------------------------------------
-        const int helper = warp - 10, tid = helper * 32 + lane;
+        const int tid = (warp - (16 - X::kHelpers)) * 32 + lane;
         constexpr int kThreadsH = X::kHelpers * 32;
-        int64_t ring = 0;
+        Place<S> at;
+        Place<kFill> raw_at;
+        int k_tiles = 0;  // key tiles so far
         bool ok = true;
-        for (; ok && walk.next(&g); ++item) {
-            const int n = g.t.hi - g.t.lo;
-            const Seen seen = item_seen(a, g);
-            auto note = [&](int64_t p) {
+        for (; ok; ++item) {
+            const Plan* g = plan_at(item);
+            if (g == nullptr) break;
+            const int n = g->n, inner_lo = g->inner_lo, inner_hi = g->inner_hi;
+            auto note = [&](int p) {
                 const int i = atomicAdd(&ctl.noted[item % kItems], 1);
-                if (i < kNoted) ctl.note[item % kItems][i] = static_cast<uint32_t>(p);
+                if (i < kNoted) ctl.note[item % kItems][i] = p;
             };
-            // Every tile in ring order.
             int kk = 0, vv = 0;
             for (int i = 0; ok && i < 2 * n; ++i) {
-                const int64_t at = ring + i;
-                const bool is_v = vv < n && ring_v<PAIR>(ring, vv, n) == at;
-                const int j = g.t.lo + (is_v ? vv++ : kk++);
-                const bool edge = is_v && at_edge(seen, j);
-                const int64_t p0 = static_cast<int64_t>(j) << kTileShift;
-                const int cs = static_cast<int>(at % S);
+                const bool is_v = vv < n && ring_v<PAIR>(vv, n) == i;
+                const int k = is_v ? vv++ : kk++;
+                const bool edge = is_v && (k < inner_lo || k > inner_hi);
                 if constexpr (!E4M3) {
-                    if (!(ok = wait_all(&ctl.full[cs], static_cast<uint32_t>(at / S)))) break;
+                    if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
                     if (edge) {
-                        const uint32_t v = st + cs * X::kTileBytes;
+                        const uint32_t v = st + at.stage * X::kTileBytes;
                         constexpr int kLanes = DP / 8;  // lanes to a row
 #pragma unroll 4
                         for (int x = tid; x < kTile * kLanes; x += kThreadsH) {
-                            const int row = x / kLanes, ch = x % kLanes;
-                            const int64_t p = p0 + row;
-                            const uint32_t addr = v + tile_chunk(row, ch, X::kPanel);
-                            const bool outside = p < seen.any_lo || p > seen.any_hi;
-                            const bool common = p >= seen.all_lo && p <= seen.all_hi;
+                            const int row = x / kLanes, ch = x % kLanes, p = k * kTile + row;
+                            const uint32_t addr = v + tile_chunk(row, ch, args.group, args.panel);
+                            const bool outside = p < g->any_lo || p > g->any_hi;
+                            const bool common = p >= g->all_lo && p <= g->all_hi;
                             bool special = false;
                             if (!outside && !common)
                                 special = any_special(ld_shared_v4(addr), exponent_mask(T()));
@@ -901,81 +1152,77 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     }
                     __syncwarp();
                     if (lane == 0) {
-                        if (edge) sv::mbar_arrive(&ctl.fixed[cs]);
-                        sv::mbar_arrive(&ctl.empty[cs]);
+                        if (edge) sv::mbar_arrive(&ctl.fixed[at.stage]);
+                        sv::mbar_arrive(&ctl.empty[at.stage]);
                     }
                 } else {
-                    const int rs = static_cast<int>(at % RS);
-                    if (!(ok = wait_all(&ctl.raw_full[rs], static_cast<uint32_t>(at / RS)))) break;
-                    if (at >= S &&
-                        !(ok = wait_all(&ctl.empty[cs], static_cast<uint32_t>(at / S - 1))))
-                        break;
-                    const uint32_t raw = sr + rs * X::kRawBytes, dst = st + cs * X::kTileBytes;
-                    // A thread expands 16 codes of a row. Eight lanes of a phase
-                    // of the stores take four pieces of two rows, whose swizzled
-                    // 16-byte columns differ.
-                    constexpr int kPieces = DP / 16;
+                    if (!(ok = wait_all(&ctl.raw_full[raw_at.stage], raw_at.round))) break;
+                    if (at.round > 0 && !(ok = wait_all(&ctl.empty[at.stage], at.round - 1))) break;
+                    const uint32_t raw = sr + raw_at.stage * X::kRawBytes;
+                    const uint32_t dst = st + at.stage * X::kTileBytes;
+                    // A thread expands 16 codes of a row, four times side by side.
+                    // Eight lanes of a phase of the stores take four pieces of
+                    // two rows, whose swizzled 16-byte columns differ.
+                    constexpr int kPieces = DP / 16, kAll = kTile * kPieces, kBatch = 4;
+                    for (int x0 = tid; x0 < kAll; x0 += kBatch * kThreadsH) {
+                        uint4 codes[kBatch];
+                        uint32_t e[kBatch];
+                        uint32_t to[kBatch];
 #pragma unroll
-                    for (int t = 0; t < kTile * kPieces / kThreadsH; ++t) {
-                        const int x = t * kThreadsH + tid;
-                        const int row = (x / (8 * kPieces / 4)) * 2 + ((x >> 2) & 1);
-                        const int piece = (x & 3) + (((x >> 3) % (kPieces / 4)) << 2);
-                        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                        const uint32_t e = ctl.exps[rs][row];
-                        bool use = piece * 16 < a.c.D;
-                        if (edge) {
-                            const int64_t p = p0 + row;
-                            const bool outside = p < seen.any_lo || p > seen.any_hi;
-                            const bool common = p >= seen.all_lo && p <= seen.all_hi;
-                            if (outside) use = false;
-                            if (!outside && !common && e == 255u) {
-                                use = false;
-                                if (piece == 0) note(p);
+                        for (int u = 0; u < kBatch; ++u) {
+                            const int x = x0 + u * kThreadsH;
+                            const int row = (x / (8 * kPieces / 4)) * 2 + ((x >> 2) & 1);
+                            const int piece = (x & 3) + (((x >> 3) % (kPieces / 4)) << 2);
+                            to[u] = dst + tile_chunk(row, piece * 2, 1024, X::kPanel);
+                            codes[u] = make_uint4(0, 0, 0, 0);
+                            e[u] = 0;
+                            if (x < kAll) {
+                                e[u] = ctl.exps[raw_at.stage][row];
+                                bool use = piece * 16 < a.c.D;
+                                if (edge) {
+                                    const int p = k * kTile + row;
+                                    const bool outside = p < g->any_lo || p > g->any_hi;
+                                    const bool common = p >= g->all_lo && p <= g->all_hi;
+                                    const bool clear = !outside && !common && e[u] == 255u;
+                                    if (clear && piece == 0) note(p);
+                                    if (outside || clear) {
+                                        use = false;
+                                        e[u] = 127;
+                                    }
+                                }
+                                if (use) codes[u] = ld_shared_v4(raw + row * a.c.D + piece * 16);
+                                if (!is_v && piece == 0)
+                                    ctl.k_scale[k_tiles & 3][row] = exp_value(e[u]);
                             }
                         }
-                        if (use)
-                            e4m3_words<T>(ld_shared_v4(raw + row * a.c.D + piece * 16),
-                                          factor_of(e, T()), &lo, &hi);
-                        st_shared_v4(dst + tile_chunk(row, piece * 2, X::kPanel), lo);
-                        st_shared_v4(dst + tile_chunk(row, piece * 2 + 1, X::kPanel), hi);
+#pragma unroll
+                        for (int u = 0; u < kBatch; ++u) {
+                            if (x0 + u * kThreadsH >= kAll) continue;
+                            uint4 lo, hi;
+                            if (is_v)
+                                expand_values<T>(codes[u], factor_of(e[u], T()), &lo, &hi);
+                            else
+                                expand_codes(codes[u], &lo, &hi);
+                            // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
+                            st_shared_v4(to[u], lo);
+                            st_shared_v4(to[u] ^ 16u, hi);
+                        }
                     }
+                    if (!is_v) ++k_tiles;
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        sv::mbar_arrive(&ctl.full[cs]);
-                        sv::mbar_arrive(&ctl.raw_empty[rs]);
+                        sv::mbar_arrive(&ctl.full[at.stage]);
+                        sv::mbar_arrive(&ctl.raw_empty[raw_at.stage]);
                     }
+                    raw_at.advance(1);
                 }
+                at.advance(1);
             }
-            ring += 2 * n;
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        // What join_kernel has to know: the item that this block began and did
-        // not finish, and the block that did.
-        Share sh{};
-        sh.failed = *stop;
-        sh.units = start.U;
-        Walk<R> again(a, start);
-        int64_t u = start.u0;
-        while (again.next(&g)) {
-            u += g.t.hi - g.t.lo;
-            if (g.t.lo == g.item.lo && g.t.hi < g.item.hi) {
-                const int64_t end = u + (g.item.hi - g.t.hi) - 1;  // the item's last unit
-                int c = blockIdx.x + 1;
-                while (share_begin(start.U, c + 1, gridDim.x) <= end) ++c;
-                sh.leads = 1;
-                sh.b = g.b;
-                sh.h = g.h;
-                sh.row0 = g.row0;
-                sh.rows = g.rows;
-                sh.q0 = g.q0;
-                sh.last = c;
-            }
-        }
-        args.shares[blockIdx.x] = sh;
-    }
+    if (threadIdx.x == 0) args.shares[blockIdx.x].failed = *stop;
     if (warp == 8) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
@@ -1055,12 +1302,19 @@ EncodeTiled lookup_encode()
     return nullptr;
 }
 
+// The driver's tensor-map encoder, looked up once.
+EncodeTiled encode_fn()
+{
+    static const EncodeTiled fn = lookup_encode();
+    return fn;
+}
+
 // Keys (kv = 0) or values (1) as [page][head][slot][element]; a box is the slots
 // of one page in one tile, times 64 16-bit elements with the 128-byte swizzle or
 // a whole row of codes.
 bool make_map(CUtensorMap* map, const Cache& c, int kv, bool f16, bool e4m3)
 {
-    static const EncodeTiled fn = lookup_encode();
+    const EncodeTiled fn = encode_fn();
     if (fn == nullptr) return false;
     const int P = 1 << c.page_shift;
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(P),
@@ -1081,13 +1335,54 @@ bool make_map(CUtensorMap* map, const Cache& c, int kv, bool f16, bool e4m3)
            CUDA_SUCCESS;
 }
 
+// 16-bit rows of 128 elements, one copy a page for both halves of the rows:
+// [page and head][slot / 8][half][slot % 8][64 elements]. Pages and heads are one
+// axis, in steps of a head (one head: of a page); see heads_to_a_page.
+bool make_map5(CUtensorMap* map, const Cache& c, int kv, bool f16, int64_t page_heads)
+{
+    const EncodeTiled fn = encode_fn();
+    if (fn == nullptr) return false;
+    const int P = 1 << c.page_shift;
+    const int64_t step = c.Hkv > 1 ? c.head_stride[kv] : c.page_stride[kv];
+    const cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(P / 8),
+                                static_cast<cuuint64_t>((c.num_pages - 1) * page_heads + c.Hkv)};
+    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(c.slot_stride[kv]), 128,
+                                   static_cast<cuuint64_t>(c.slot_stride[kv]) * 8,
+                                   static_cast<cuuint64_t>(step)};
+    const cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>((P < kTile ? P : kTile) / 8), 1};
+    const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+    return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+              c.pages[kv], dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How far apart pages are on make_map5's axis of pages and heads; 0 where it
+// cannot be used: the page stride has to be a multiple of the head stride, the
+// same in keys and values.
+int64_t heads_to_a_page(const Cache& c, bool e4m3)
+{
+    if (e4m3 || c.D != 128) return 0;
+    int64_t n = 1;
+    if (c.Hkv > 1) {
+        if (c.head_stride[0] <= 0 || c.page_stride[0] % c.head_stride[0] != 0) return 0;
+        n = c.page_stride[0] / c.head_stride[0];
+        if (n <= 0 || c.head_stride[1] <= 0 || c.page_stride[1] != n * c.head_stride[1]) return 0;
+    }
+    // (coordinates are 32 bits)
+    return n < (int64_t(1) << 31) / c.num_pages - c.Hkv ? n : 0;
+}
+
 template <class T, int DP, bool E4M3, bool PAIR>
 cudaError_t launch_shape(const CUtensorMap& k, const CUtensorMap& v, const Tiles& t, int blocks,
                          int64_t rows, cudaStream_t s)
 {
     using X = Shape<DP, E4M3, PAIR>;
-    constexpr size_t smem = X::kTiles + sizeof(Control<X::kStages, X::kRawStages, PAIR>);
+    using Ctl = Control<X::kStages, X::kRawStages, PAIR>;
+    constexpr size_t smem = X::kTiles + sizeof(Ctl);
     static_assert(smem <= kMaxSmem, "shared memory");
+    // (k_scale is read 16 bytes at a time)
+    static_assert(alignof(Ctl) == 16 && X::kTiles % 1024 == 0, "alignment");
     auto* f = tiles_kernel<T, DP, E4M3, PAIR>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
@@ -1135,7 +1430,10 @@ cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* wor
                                    cudaStream_t s, bool* mapped)
 {
     CUtensorMap k, v;
-    *mapped = make_map(&k, a.c, 0, f16, e4m3) && make_map(&v, a.c, 1, f16, e4m3);
+    const int64_t page_heads = heads_to_a_page(a.c, e4m3);
+    const bool five = page_heads > 0 && make_map5(&k, a.c, 0, f16, page_heads) &&
+                      make_map5(&v, a.c, 1, f16, page_heads);
+    *mapped = five || (make_map(&k, a.c, 0, f16, e4m3) && make_map(&v, a.c, 1, f16, e4m3));
     if (!*mapped) return cudaSuccess;
     int dev = 0, sms = 0;
     cudaError_t e;
@@ -1145,7 +1443,9 @@ cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* wor
     const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
     const int64_t rows = item_rows(a.max_chunk, a.G);
     Tiles t{a, reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kShareBytes),
-            static_cast<Share*>(workspace), static_cast<int32_t>(rows)};
+            static_cast<Share*>(workspace), static_cast<int32_t>(rows),
+            five ? 2048 : 1024, five ? 1024 : kTile * 128,
+            five ? static_cast<int32_t>(page_heads) : 0, a.c.Hkv > 1 ? 1 : 0};
     const bool pair = rows > 128;
     if (a.c.D <= 64)
         return f16 ? launch_type<F16, 64>(k, v, t, blocks, rows, e4m3, pair, s)

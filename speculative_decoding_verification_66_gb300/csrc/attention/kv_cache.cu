@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const Cache c, const Pac
         row_off[u] = (kv[u] ? t * p.token_stride[1] + h * p.head_stride[1]
                             : t * p.token_stride[0] + h * p.head_stride[0]) + sub * 16;
     }
-    if (READ) {
+    if constexpr (READ) {
         uint4 r[kUnroll];
         uint2 codes[kUnroll];
         uint32_t eb[kUnroll];
@@ -165,8 +165,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const Cache c, const Pac
             }
             *reinterpret_cast<uint4*>((kv[u] ? p.x[1] : p.x[0]) + row_off[u]) = r[u];
         }
-        return;
-    }
+    } else {
     uint4 x[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
@@ -195,6 +194,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const Cache c, const Pac
         *reinterpret_cast<uint2*>((kv[u] ? c.pages[1] : c.pages[0]) + cache_off[u]) =
             make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
         if (sub == 0) (kv[u] ? c.exps[1] : c.exps[0])[exp_off[u]] = static_cast<uint8_t>(e);
+    }
     }
 }
 
