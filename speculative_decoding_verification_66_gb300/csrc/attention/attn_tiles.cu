@@ -27,7 +27,7 @@
 //   8         issues the products
 //   9, 10     load keys and values: page numbers, a bulk tensor copy a page,
 //             exponents. Warp 9 also plans the block's segments for all.
-//   11-15     helpers. 16-bit caches: make the values at a tile's hidden
+//   12-15     helpers. 16-bit caches: make the values at a tile's hidden
 //             positions harmless. e4m3 caches: also expand every tile, exactly,
 //             into the stage that the products read.
 // The next segment's queries are fetched while the last products of a segment
@@ -80,7 +80,7 @@ struct Shape {
     static constexpr int kStages = DP == 128 ? (E4M3 ? 3 : (PAIR ? 5 : 6)) : (E4M3 ? 4 : 8);
     static constexpr int kRawStages = E4M3 ? (DP == 128 ? (PAIR ? 3 : 5) : 8) : 0;
     static_assert((kStages + kRawStages) / 2 + 1 < kItems - 2, "notes");
-    static constexpr int kHelpers = 5;
+    static constexpr int kHelpers = 4;
     static constexpr int kThreads = 512;
     static constexpr int kPanel = kTile * 128;  // bytes of 64 elements of every row
     static constexpr int kTiles = kQBytes + kStages * kTileBytes + kRawStages * kRawBytes;
@@ -228,9 +228,9 @@ struct Factor {
 __device__ __forceinline__ uint32_t both(uint32_t h) { return h | (h << 16); }
 __device__ __forceinline__ Factor factor_of(uint32_t e, Bf16)
 {
-    if (e == 255u) return Factor{both(0x7FFFu), both(0x3F80u), false};
-    const uint32_t x = min(e, 134u), y = e - x;
-    return Factor{both((x + 120u) << 7), both((y + 127u) << 7), y != 0};
+    const uint32_t x = min(e, 134u), y = e == 255u ? 0u : e - x;
+    return Factor{e == 255u ? both(0x7FFFu) : (x + 120u) * 0x00800080u, (y + 127u) * 0x00800080u,
+                  y != 0};
 }
 __device__ __forceinline__ Factor factor_of(uint32_t e, F16)
 {
@@ -1104,7 +1104,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             for (int i = 0; i < kFill; ++i)
                 if (used >> i & 1u) sv::mbar_wait_bounded(&fullbar[i], rounds >> i & 1u, nullptr);
         }
-    } else {
+    } else if (warp >= 16 - X::kHelpers) {
         // ------------------------------------------------------------------
         // Helpers: hidden values, and e4m3. They pass every tile in order (else
         // a parity could stand for another round of the stage than they mean).
@@ -1160,52 +1160,60 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     if (at.round > 0 && !(ok = wait_all(&ctl.empty[at.stage], at.round - 1))) break;
                     const uint32_t raw = sr + raw_at.stage * X::kRawBytes;
                     const uint32_t dst = st + at.stage * X::kTileBytes;
-                    // A thread expands 16 codes of a row, four times side by side.
-                    // Eight lanes of a phase of the stores take four pieces of
-                    // two rows, whose swizzled 16-byte columns differ.
-                    constexpr int kPieces = DP / 16, kAll = kTile * kPieces, kBatch = 4;
-                    for (int x0 = tid; x0 < kAll; x0 += kBatch * kThreadsH) {
+                    // A thread expands 16 codes of a row, the same piece of every
+                    // kStep-th row. Eight neighbouring lanes take half of the
+                    // pieces of two rows, the other half of the second: their
+                    // 16-byte columns differ in the loads and, swizzled, in the
+                    // stores.
+                    constexpr int kPieces = DP / 16, kStep = kThreadsH / kPieces;
+                    const int pair = tid / (2 * kPieces), odd = (tid >> 2) & 1;
+                    const int row0 = pair * 2 + odd;
+                    const int piece = (tid & 3) + (kPieces > 4 ? (((tid >> 3) & 1) ^ odd) << 2 : 0);
+                    const bool in_row = piece * 16 < a.c.D;
+                    const uint32_t from = raw + row0 * a.c.D + piece * 16;
+                    const uint32_t to = dst + tile_chunk(row0, piece * 2, 1024, X::kPanel);
+                    const uint8_t* exps = &ctl.exps[raw_at.stage][0];
+                    if (!is_v) {
+                        for (int row = tid; row < kTile; row += kThreadsH)
+                            ctl.k_scale[k_tiles & 3][row] = exp_value(exps[row]);
+                    }
+                    constexpr int kBatch = 4;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < kTile / kStep; i0 += kBatch) {
                         uint4 codes[kBatch];
                         uint32_t e[kBatch];
-                        uint32_t to[kBatch];
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
-                            const int x = x0 + u * kThreadsH;
-                            const int row = (x / (8 * kPieces / 4)) * 2 + ((x >> 2) & 1);
-                            const int piece = (x & 3) + (((x >> 3) % (kPieces / 4)) << 2);
-                            to[u] = dst + tile_chunk(row, piece * 2, 1024, X::kPanel);
-                            codes[u] = make_uint4(0, 0, 0, 0);
-                            e[u] = 0;
-                            if (x < kAll) {
-                                e[u] = ctl.exps[raw_at.stage][row];
-                                bool use = piece * 16 < a.c.D;
-                                if (edge) {
-                                    const int p = k * kTile + row;
-                                    const bool outside = p < g->any_lo || p > g->any_hi;
-                                    const bool common = p >= g->all_lo && p <= g->all_hi;
-                                    const bool clear = !outside && !common && e[u] == 255u;
-                                    if (clear && piece == 0) note(p);
-                                    if (outside || clear) {
-                                        use = false;
-                                        e[u] = 127;
-                                    }
+                            const int at_row = (i0 + u) * kStep;
+                            codes[u] = in_row ? ld_shared_v4(from + at_row * a.c.D)
+                                              : make_uint4(0, 0, 0, 0);
+                            e[u] = is_v ? exps[row0 + at_row] : 127u;
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int u = 0; u < kBatch; ++u) {
+                                const int p = k * kTile + row0 + (i0 + u) * kStep;
+                                const bool outside = p < g->any_lo || p > g->any_hi;
+                                const bool common = p >= g->all_lo && p <= g->all_hi;
+                                const bool clear = !outside && !common && e[u] == 255u;
+                                if (clear && piece == 0) note(p);
+                                if (outside || clear) {
+                                    codes[u] = make_uint4(0, 0, 0, 0);
+                                    e[u] = 127u;
                                 }
-                                if (use) codes[u] = ld_shared_v4(raw + row * a.c.D + piece * 16);
-                                if (!is_v && piece == 0)
-                                    ctl.k_scale[k_tiles & 3][row] = exp_value(e[u]);
                             }
                         }
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
-                            if (x0 + u * kThreadsH >= kAll) continue;
+                            const uint32_t t = to + (i0 + u) * (kStep * 128);
                             uint4 lo, hi;
                             if (is_v)
                                 expand_values<T>(codes[u], factor_of(e[u], T()), &lo, &hi);
                             else
                                 expand_codes(codes[u], &lo, &hi);
                             // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
-                            st_shared_v4(to[u], lo);
-                            st_shared_v4(to[u] ^ 16u, hi);
+                            st_shared_v4(t, lo);
+                            st_shared_v4(t ^ 16u, hi);
                         }
                     }
                     if (!is_v) ++k_tiles;
