@@ -7,9 +7,9 @@
 // with c = scale log2(e): one pass over the cache, the softmax never leaves the
 // chip. S, P and O live in tensor memory, a row to a lane: a thread owns a row,
 // so the maximum and the sum need no exchange between threads. O is rescaled
-// only when the maximum has grown by more than 2^kSlack since the last time
-// (the weights stay below 2^kSlack; the sum is exact either way), which is
-// rare after the first tiles.
+// only when the maximum has grown by more than slack() powers of two since the
+// last time: the weights stay below 2^slack(), which is what their type holds
+// without loss, and hardly any tile after the first needs it.
 //
 // Two slots, each with its own S, O and softmax warpgroup, take turns on the
 // tensor core: while one slot's rows go through the softmax, the other's
@@ -24,7 +24,9 @@
 // Warps:
 //   0-3, 4-7  softmax of slots 0 and 1 (row = tensor-memory lane = thread), the
 //             loads of the queries and the outputs
-//   8         issues the products
+//   8, 11     issue the products of slots 0 and 1. A warp's later instructions
+//             queue behind the products it has issued, so one warp could not
+//             look after one slot's barriers while the other's products run.
 //   9, 10     load keys and values: page numbers, a bulk tensor copy a page,
 //             exponents. Warp 9 also plans the block's segments for all.
 //   12-15     helpers. 16-bit caches: make the values at a tile's hidden
@@ -62,7 +64,8 @@
 namespace sva {
 namespace {
 
-constexpr float kSlack = 8.f;
+__device__ __forceinline__ float slack(Bf16) { return 60.f; }
+__device__ __forceinline__ float slack(F16) { return 14.f; }  // (below 65504, with 1 to spare)
 constexpr int kMaxBlocks = 160;  // shares in the workspace; grids are no larger
 constexpr int kNoted = 4;        // noted positions a segment can hold
 constexpr int kItems = 16;       // segments whose plans and notes are kept at one time
@@ -105,7 +108,7 @@ template <int STAGES, int RAW, bool PAIR>
 struct Control {
     uint64_t full[STAGES], empty[STAGES], fixed[STAGES];
     uint64_t raw_full[RAW > 0 ? RAW : 1], raw_empty[RAW > 0 ? RAW : 1];
-    uint64_t s_full[2], p_ready[2], q_ready, o_full, o_free, ml_ready, done;
+    uint64_t s_full[2], p_ready[2], q_ready, q_free, o_full, o_free, s_free, ml_ready, done;
     uint64_t plan_ready[kItems];
     uint32_t tmem;
     int stop;
@@ -115,8 +118,9 @@ struct Control {
     int noted[kItems];             // how many positions are noted
     int note[kItems][kNoted];      // which, counted as in the plan
     int bad_page[kItems];
-    float q_scale[RAW > 0 ? (PAIR ? 256 : 128) : 1];  // e4m3: power of two a row is divided by
-    alignas(16) float k_scale[RAW > 0 ? 4 : 1][RAW > 0 ? kTile : 4];  // .. of the last tiles' keys
+    // e4m3: powers of two that the rows of this segment and the next are divided by
+    float q_scale[2][RAW > 0 ? (PAIR ? 256 : 128) : 1];
+    alignas(16) float k_scale[RAW > 0 ? 5 : 1][RAW > 0 ? kTile : 4];  // .. of the last tiles' keys; 1
     uint8_t exps[RAW > 0 ? RAW : 1][RAW > 0 ? kTile : 4];
 };
 
@@ -427,9 +431,10 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             sv::mbar_init(&ctl.full[i], E4M3 ? X::kHelpers : 1);
-            // (16-bit: the helpers, too, pass every tile in order, or a parity
-            // would stand for another round of the stage than they mean)
-            sv::mbar_init(&ctl.empty[i], E4M3 ? 1 : 1 + X::kHelpers);
+            // Both slots' products and, for 16 bits, the helpers pass every tile
+            // in order, used or not: else a parity could stand for another round
+            // of the stage than they mean.
+            sv::mbar_init(&ctl.empty[i], E4M3 ? 2 : 2 + X::kHelpers);
             sv::mbar_init(&ctl.fixed[i], X::kHelpers);
         }
         for (int i = 0; i < RS; ++i) {
@@ -441,10 +446,12 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             sv::mbar_init(&ctl.p_ready[i], 4);
         }
         sv::mbar_init(&ctl.q_ready, 8);
-        sv::mbar_init(&ctl.o_full, 1);
+        sv::mbar_init(&ctl.o_full, 2);
         sv::mbar_init(&ctl.ml_ready, 8);
+        sv::mbar_init(&ctl.q_free, 2);
         sv::mbar_init(&ctl.o_free, 8);
-        sv::mbar_init(&ctl.done, 1);
+        sv::mbar_init(&ctl.s_free, 8);
+        sv::mbar_init(&ctl.done, 2);
         for (int i = 0; i < kItems; ++i) sv::mbar_init(&ctl.plan_ready[i], 1);
         // (The swizzle needs tiles on 1024-byte boundaries. There is no static
         // shared memory before them, so they are; if not, the call fails.)
@@ -452,6 +459,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         for (int i = 0; i < kItems; ++i) ctl.noted[i] = ctl.bad_page[i] = 0;
         sv::fence_barrier_init();
     }
+    if (E4M3 && threadIdx.x < kTile) ctl.k_scale[4][threadIdx.x] = 1.f;
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          sv::smem_addr(&ctl.tmem)),
@@ -564,7 +572,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                 }
             }
         };
-        auto store = [&](const Plan& x) {
+        auto store = [&](const Plan& x, int at) {
 #pragma unroll
             for (int i = 0; i < kFetch; ++i) {
                 const int r = first + i * (128 / kChunks);
@@ -588,7 +596,8 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         h[k] = narrow2(sv::bf16_lo(u[k]) * up, sv::bf16_hi(u[k]) * up, F16());
                     qv[i] = make_uint4(h[0], h[1], h[2], h[3]);
                     if (has && ch == 0)
-                        ctl.q_scale[r] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+                        ctl.q_scale[at & 1][r] =
+                            __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
                 }
                 if (has)
                     st_shared_v4(sq + (r >> 7) * (128 * DP * 2) +
@@ -603,7 +612,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         const Plan* ahead = plan_at(0);
         if (ahead != nullptr) {
             fetch(*ahead);
-            store(*ahead);
+            store(*ahead, 0);
         }
         bool ok = true;
         for (; ahead != nullptr; ++item) {
@@ -625,57 +634,66 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     if (live) {
                         fence_after();
                         if (E4M3 && std::is_same<T, Bf16>::value && !begun)
-                            c = a.scale_log2 * ctl.q_scale[min(slot_row, rows - 1)];
+                            c = a.scale_log2 * ctl.q_scale[item & 1][min(slot_row, rows - 1)];
                         const int clo = low - k * kTile, chi = pos - k * kTile;
                         const bool masked =
                             __any_sync(0xFFFFFFFFu, clo > 0 || chi < kTile - 1) != 0;
-                        // Scores of columns 64 x .., in units of the scale.
-                        auto half = [&](int x, float (&v)[64]) {
-                            tmem_ld(s_addr + 64 * x, v);
-                            if constexpr (E4M3) {
-                                const float4* ks = reinterpret_cast<const float4*>(
-                                    &ctl.k_scale[(tiles_before + k) & 3][64 * x]);
+                        // The loops below are kept rolled: all roles' code has to
+                        // stay in the instruction caches.
+                        const float* ks = &ctl.k_scale[E4M3 ? (tiles_before + k) & 3 : 0][0];
+                        if (masked) {
+#pragma unroll 1
+                            for (int x = 0; x < kTile; x += 16) {
+                                float v[16];
+                                tmem_ld(s_addr + x, v);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float4 k4 = ks[i];
-                                    const float2 p = mul2f(make_float2(v[4 * i], v[4 * i + 1]),
-                                                           make_float2(k4.x, k4.y));
-                                    const float2 q = mul2f(make_float2(v[4 * i + 2], v[4 * i + 3]),
-                                                           make_float2(k4.z, k4.w));
-                                    v[4 * i] = p.x;
-                                    v[4 * i + 1] = p.y;
-                                    v[4 * i + 2] = q.x;
-                                    v[4 * i + 3] = q.y;
+                                for (int i = 0; i < 16; ++i)
+                                    v[i] = x + i >= clo && x + i <= chi
+                                               ? (E4M3 ? v[i] * ks[x + i] : v[i])
+                                               : ninf;
+                                tmem_st(s_addr + x, v);
+                            }
+                            tmem_wait_st();
+                            if (E4M3) ks = &ctl.k_scale[4][0];
+                        }
+                        // 64 columns; e4m3: times their keys' powers of two.
+                        float va[32], vb[32];
+                        auto load = [&](int x) {
+                            tmem_ld(s_addr + x, va, s_addr + x + 32, vb);
+                            if constexpr (E4M3) {
+#pragma unroll
+                                for (int i = 0; i < 32; i += 4) {
+                                    const float4 ka = *reinterpret_cast<const float4*>(ks + x + i);
+                                    const float4 kb =
+                                        *reinterpret_cast<const float4*>(ks + x + 32 + i);
+                                    float2 p = mul2f(make_float2(va[i], va[i + 1]),
+                                                     make_float2(ka.x, ka.y));
+                                    float2 q = mul2f(make_float2(va[i + 2], va[i + 3]),
+                                                     make_float2(ka.z, ka.w));
+                                    va[i] = p.x, va[i + 1] = p.y, va[i + 2] = q.x, va[i + 3] = q.y;
+                                    p = mul2f(make_float2(vb[i], vb[i + 1]), make_float2(kb.x, kb.y));
+                                    q = mul2f(make_float2(vb[i + 2], vb[i + 3]),
+                                              make_float2(kb.z, kb.w));
+                                    vb[i] = p.x, vb[i + 1] = p.y, vb[i + 2] = q.x, vb[i + 3] = q.y;
                                 }
                             }
-                            if (masked) {
-                                const int lo = clo - 64 * x, hi = chi - 64 * x;
-#pragma unroll
-                                for (int i = 0; i < 64; ++i) v[i] = i >= lo && i <= hi ? v[i] : ninf;
-                            }
                         };
-                        auto top_of = [&](const float (&v)[64]) {
-                            float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+                        float mt = ninf;
+#pragma unroll 1
+                        for (int x = 0; x < kTile; x += 64) {
+                            load(x);
+                            float t[4] = {va[0], va[1], va[2], va[3]};
 #pragma unroll
-                            for (int i = 4; i < 64; i += 4) {
-                                t0 = fmaxf(t0, v[i]);
-                                t1 = fmaxf(t1, v[i + 1]);
-                                t2 = fmaxf(t2, v[i + 2]);
-                                t3 = fmaxf(t3, v[i + 3]);
+                            for (int i = 0; i < 32; i += 4) {
+#pragma unroll
+                                for (int z = 0; z < 4; ++z)
+                                    t[z] = fmaxf(t[z], fmaxf(va[i + z], vb[i + z]));
                             }
-                            return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-                        };
-                        // The maximum over both halves, then the weights: of the
-                        // second half, which is in registers, and of the first,
-                        // read again. A row of 128 scores would not fit beside
-                        // what else the thread holds.
-                        float v[64];
-                        half(0, v);
-                        float mt = top_of(v);
-                        half(1, v);
+                            mt = fmaxf(mt, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
+                        }
                         // (scale > 0; a NaN score is left out here and comes through below)
-                        mt = fmaxf(mt, top_of(v)) * c;
-                        const bool grow = mt > m + kSlack || (!begun && mt > m);
+                        mt *= c;
+                        const bool grow = mt > m + slack(T()) || (!begun && mt > m);
                         if (begun && __any_sync(0xFFFFFFFFu, grow)) {
                             // The slot's products so far are complete: s_full's
                             // commit came after them.
@@ -694,29 +712,31 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         begun = true;
                         const float shift = m == ninf ? 0.f : -m;
                         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-                        // P takes the columns of the second half.
-                        auto weigh = [&](int x) {
+                        auto weigh = [&](const float (&v)[32], uint32_t to) {
+                            uint32_t w[16];
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                uint32_t w[16];
-#pragma unroll
-                                for (int i = 0; i < 16; i += 2) {
-                                    const int z = 32 * y + 2 * i;
-                                    float2 p = fma2(make_float2(v[z], v[z + 1]), c, shift);
-                                    float2 q = fma2(make_float2(v[z + 2], v[z + 3]), c, shift);
-                                    p = make_float2(sv::ex2(p.x), sv::ex2(p.y));
-                                    q = make_float2(sv::ex2(q.x), sv::ex2(q.y));
-                                    l0 = add2(l0, p);
-                                    l1 = add2(l1, q);
-                                    w[i] = narrow2(p.x, p.y, T());
-                                    w[i + 1] = narrow2(q.x, q.y, T());
-                                }
-                                tmem_st(s_addr + 64 + 32 * x + 16 * y, w);
+                            for (int i = 0; i < 16; i += 2) {
+                                float2 p = fma2(make_float2(v[2 * i], v[2 * i + 1]), c, shift);
+                                float2 q = fma2(make_float2(v[2 * i + 2], v[2 * i + 3]), c, shift);
+                                p = make_float2(sv::ex2(p.x), sv::ex2(p.y));
+                                q = make_float2(sv::ex2(q.x), sv::ex2(q.y));
+                                l0 = add2(l0, p);
+                                l1 = add2(l1, q);
+                                w[i] = narrow2(p.x, p.y, T());
+                                w[i + 1] = narrow2(q.x, q.y, T());
                             }
+                            tmem_st(to, w);
                         };
-                        weigh(1);
-                        half(0, v);
-                        weigh(0);
+                        // The weights: of the second half, which is in registers,
+                        // then of the first, read again. They take the columns of
+                        // the second half.
+#pragma unroll 1
+                        for (int x = 64;; x = 0) {
+                            weigh(va, s_addr + 64 + x / 2);
+                            weigh(vb, s_addr + 64 + x / 2 + 16);
+                            if (x == 0) break;
+                            load(0);
+                        }
                         l += (l0.x + l0.y) + (l1.x + l1.y);
                         tmem_wait_st();
                         fence_before();
@@ -733,7 +753,11 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             const int n = g.n;
             tiles_before += n;
             ahead = plan_at(item + 1);
-            if (ahead != nullptr) fetch(*ahead);
+            if (ahead != nullptr) {
+                fetch(*ahead);
+                if (!(ok = wait_all(&ctl.q_free, item))) break;
+                store(*ahead, item + 1);
+            }
             if (!(ok = wait_all(&ctl.o_full, item))) break;
             fence_after();
             float w0 = 1.f, w1 = 0.f;
@@ -763,8 +787,8 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     m = top;
                 }
                 __syncwarp();
+                if (lane == 0) sv::mbar_arrive(&ctl.s_free);
             }
-            if (ahead != nullptr) store(*ahead);
             const bool whole = g.whole != 0, valid = slot_row < rows;
             // A row that sees a noted position is computed again below.
             const int noted = *reinterpret_cast<volatile int*>(&ctl.noted[item % kItems]);
@@ -857,110 +881,85 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             }
             if (lane == 0) sv::mbar_arrive(&ctl.o_free);
         }
-    } else if (warp == 8) {
+    } else if (warp == 8 || warp == 11) {
         // ------------------------------------------------------------------
-        // Products: the warp stays together, one lane issues.
+        // Products of slot s: the warp stays together, one lane issues. It
+        // passes every tile in ring order, its own and the other slot's.
         // ------------------------------------------------------------------
         using TS = typename std::conditional<E4M3, F16, T>::type;
         constexpr uint32_t id_s = idesc<TS, kTile, false>(), id_o = idesc<T, DP, true>();
-        const uint64_t dq = smem_desc(sq, 16, 1024), dk = smem_desc(st, 16, args.group),
-                       dv = smem_desc(st, args.panel, args.group);
+        const int s = warp == 8 ? 0 : 1;
+        const uint64_t dq = smem_desc(sq + (PAIR ? s * (128 * DP * 2) : 0), 16, 1024);
+        const uint64_t dk = smem_desc(st, 16, args.group), dv = smem_desc(st, args.panel, args.group);
         const uint32_t panel = args.panel >> 4, v_step = args.group >> 3;  // 16 keys: two groups
-        Place<S> base_at;
-        uint32_t fixes = 0, p_count0 = 0, p_count1 = 0;
+        const uint32_t s_addr = tmem + s * 128, o_addr = tmem + 256 + s * DP;
+        Place<S> at;
+        uint32_t fixes = 0, tiles = 0;
         bool ok = true;
         for (; ok; ++item) {
             const Plan* g = plan_at(item);
             if (g == nullptr || !(ok = wait_all(&ctl.q_ready, item))) break;
             const int n = g->n, inner_lo = g->inner_lo, inner_hi = g->inner_hi;
-            // PAIR: the slots' tiles; every tile has at least one of them.
-            const int lo0 = g->lo0, hi0 = g->hi0, lo1 = g->lo1, hi1 = g->hi1;
-            auto in0 = [&](int k) { return k >= lo0 && k < hi0; };
-            auto in1 = [&](int k) { return k >= lo1 && k < hi1; };
-            auto step = [&](int& k, int& sl) {
-                if (!PAIR) {
-                    ++k;
-                    sl ^= 1;
-                } else if (sl == 0 && in1(k)) {
-                    sl = 1;
-                } else {
-                    ++k;
-                    sl = in0(k) ? 0 : 1;
-                }
-            };
-            auto last_user = [&](int k, int sl) { return !PAIR || sl == 1 || !in1(k); };
-            const int s0 = !PAIR || in0(0) ? 0 : 1;
-            int qk = 0, qs = s0, vk = 0, vs = s0;
-            uint32_t out = 0, begun = 0;  // bit s: slot s's scores are under way; has a product
-            Place<S> kat = base_at, vat = base_at;
-            vat.advance(ring_v<PAIR>(0, n));
-            bool freed = item == 0;  // the results before have been read
-            while (vk < n) {
-                while (qk < n && !(out >> qs & 1u)) {
-                    if (!(ok = wait_all(&ctl.full[kat.stage], kat.round))) break;
+            const int k0 = PAIR ? (s ? g->lo1 : g->lo0) : s, k1 = PAIR ? (s ? g->hi1 : g->hi0) : n;
+            // !PAIR: the slots have exchanged their rows' sums of the segment
+            // before, through the scores' columns.
+            if (!PAIR && item > 0 && !(ok = wait_all(&ctl.s_free, item - 1))) break;
+            bool begun = false;
+            int kk = 0, vv = 0, left = k1 <= k0 ? 0 : PAIR ? k1 - k0 : (k1 - k0 + 1) / 2;
+            if (left == 0 && lane == 0) sv::mbar_arrive(&ctl.q_free);
+            for (int i = 0; i < 2 * n; ++i) {
+                const bool is_v = vv < n && ring_v<PAIR>(vv, n) == i;
+                const int k = is_v ? vv++ : kk++;
+                const bool mine = k >= k0 && k < k1 && (PAIR || ((k - k0) & 1) == 0);
+                const bool edge = !E4M3 && is_v && (k < inner_lo || k > inner_hi);
+                if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
+                if (!mine) {
+                    if (lane == 0) sv::mbar_arrive(&ctl.empty[at.stage]);
+                } else if (!is_v) {
                     fence_after();
-                    const bool last = last_user(qk, qs);
                     if (elect_one()) {
-                        const uint64_t q = dq + (PAIR ? qs * (128 * DP * 2 >> 4) : 0);
-                        const uint64_t k = dk + kat.stage * (X::kTileBytes >> 4);
+                        const uint64_t b = dk + at.stage * (X::kTileBytes >> 4);
 #pragma unroll
-                        for (int i = 0; i < DP / 16; ++i) {
-                            const uint32_t o = (i & 3) * 2;
-                            mma_ss(tmem + qs * 128, q + o + (i >> 2) * (X::kPanel >> 4),
-                                   k + o + (i >> 2) * panel, id_s, i > 0);
+                        for (int x = 0; x < DP / 16; ++x) {
+                            const uint32_t o = (x & 3) * 2;
+                            mma_ss(s_addr, dq + o + (x >> 2) * (X::kPanel >> 4),
+                                   b + o + (x >> 2) * panel, id_s, x > 0);
                         }
-                        mma_commit(&ctl.s_full[qs]);
-                        if (last) mma_commit(&ctl.empty[kat.stage]);
+                        mma_commit(&ctl.s_full[s]);
+                        mma_commit(&ctl.empty[at.stage]);
+                        if (left == 1) mma_commit(&ctl.q_free);
                     }
                     __syncwarp();
-                    out |= 1u << qs;
-                    const int was = qk;
-                    step(qk, qs);
-                    if (qk != was) kat.advance(ring_k_step<PAIR>(was));
-                }
-                if (!ok) break;
-                if (!(ok = wait_all(&ctl.full[vat.stage], vat.round))) break;
-                if (!E4M3 && (vk < inner_lo || vk > inner_hi) && (!PAIR || vs == 0 || !in0(vk))) {
-                    if (!(ok = wait_all(&ctl.fixed[vat.stage], fixes >> vat.stage))) break;
-                    fixes ^= 1u << vat.stage;
-                }
-                if (!freed) {
-                    if (!(ok = wait_all(&ctl.o_free, item - 1))) break;
-                    freed = true;
-                }
-                if (!(ok = wait_all(&ctl.p_ready[vs], vs ? p_count1 : p_count0))) break;
-                if (vs)
-                    ++p_count1;
-                else
-                    ++p_count0;
-                fence_after();
-                const bool last = last_user(vk, vs);
-                if (elect_one()) {
-                    const uint64_t v = dv + vat.stage * (X::kTileBytes >> 4);
-                    const bool more = (begun >> vs & 1u) != 0;
+                    --left;
+                } else {
+                    if (edge && !(ok = wait_all(&ctl.fixed[at.stage], fixes >> at.stage))) break;
+                    // (the results before have been read)
+                    if (!begun && item > 0 && !(ok = wait_all(&ctl.o_free, item - 1))) break;
+                    if (!(ok = wait_all(&ctl.p_ready[s], tiles))) break;
+                    ++tiles;
+                    fence_after();
+                    if (elect_one()) {
+                        const uint64_t b = dv + at.stage * (X::kTileBytes >> 4);
 #pragma unroll
-                    for (int i = 0; i < kTile / 16; ++i)
-                        mma_ts(tmem + 256 + vs * DP, tmem + vs * 128 + 64 + i * 8, v + i * v_step, id_o,
-                               more || i > 0);
-                    if (last) mma_commit(&ctl.empty[vat.stage]);
+                        for (int x = 0; x < kTile / 16; ++x)
+                            mma_ts(o_addr, s_addr + 64 + x * 8, b + x * v_step, id_o, begun || x > 0);
+                        mma_commit(&ctl.empty[at.stage]);
+                    }
+                    __syncwarp();
+                    begun = true;
                 }
-                __syncwarp();
-                begun |= 1u << vs;
-                out &= ~(1u << vs);
-                const int was = vk;
-                step(vk, vs);
-                if (vk != was) vat.advance(ring_v_step<PAIR>(was, n));
+                if (edge) fixes ^= 1u << at.stage;
+                at.advance(1);
             }
             if (!ok) break;
             if (elect_one()) mma_commit(&ctl.o_full);
             __syncwarp();
-            base_at.advance(2 * n);
         }
-        // Everything issued has completed once this arrives.
+        // Everything issued has completed once both have arrived.
         if (elect_one()) mma_commit(&ctl.done);
         __syncwarp();
         sv::mbar_wait_bounded(&ctl.done, 0, nullptr);
-    } else if (warp < 11) {
+    } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------------------------
         // Copies of keys (warp 9, which also plans the segments) and values
         // (warp 10). The page of tile k + 2 and the exponents of tile k + 1 are
@@ -1106,8 +1105,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         }
     } else if (warp >= 16 - X::kHelpers) {
         // ------------------------------------------------------------------
-        // Helpers: hidden values, and e4m3. They pass every tile in order (else
-        // a parity could stand for another round of the stage than they mean).
+        // Helpers: hidden values, and e4m3.
         // ------------------------------------------------------------------
         const int tid = (warp - (16 - X::kHelpers)) * 32 + lane;
         constexpr int kThreadsH = X::kHelpers * 32;
