@@ -112,6 +112,7 @@ struct Control {
     uint64_t plan_ready[kItems];
     uint32_t tmem;
     int stop;
+    int burst;  // PAIR: a slot's products are under way
     Start start;
     int64_t sums[16];
     Plan plan[kItems];
@@ -455,6 +456,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         for (int i = 0; i < kItems; ++i) sv::mbar_init(&ctl.plan_ready[i], 1);
         // (The swizzle needs tiles on 1024-byte boundaries. There is no static
         // shared memory before them, so they are; if not, the call fails.)
+        ctl.burst = 0;
         ctl.stop = (base & 1023u) != 0;
         for (int i = 0; i < kItems; ++i) ctl.noted[i] = ctl.bad_page[i] = 0;
         sv::fence_barrier_init();
@@ -681,15 +683,19 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         float mt = ninf;
 #pragma unroll 1
                         for (int x = 0; x < kTile; x += 64) {
-                            load(x);
-                            float t[4] = {va[0], va[1], va[2], va[3]};
+                            if constexpr (E4M3) {
+                                load(x);
+                                float t[4] = {va[0], va[1], va[2], va[3]};
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
+                                for (int i = 0; i < 32; i += 4) {
 #pragma unroll
-                                for (int z = 0; z < 4; ++z)
-                                    t[z] = fmaxf(t[z], fmaxf(va[i + z], vb[i + z]));
+                                    for (int z = 0; z < 4; ++z)
+                                        t[z] = fmaxf(t[z], fmaxf(va[i + z], vb[i + z]));
+                                }
+                                mt = fmaxf(mt, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
+                            } else {
+                                mt = fmaxf(mt, tmem_ld_max(s_addr + x, va, s_addr + x + 32, vb));
                             }
-                            mt = fmaxf(mt, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
                         }
                         // (scale > 0; a NaN score is left out here and comes through below)
                         mt *= c;
@@ -907,6 +913,18 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             bool begun = false;
             int kk = 0, vv = 0, left = k1 <= k0 ? 0 : PAIR ? k1 - k0 : (k1 - k0 + 1) / 2;
             if (left == 0 && lane == 0) sv::mbar_arrive(&ctl.q_free);
+            auto scores = [&](const Place<S>& p, bool last) {
+                const uint64_t b = dk + p.stage * (X::kTileBytes >> 4);
+#pragma unroll
+                for (int x = 0; x < DP / 16; ++x) {
+                    const uint32_t o = (x & 3) * 2;
+                    mma_ss(s_addr, dq + o + (x >> 2) * (X::kPanel >> 4), b + o + (x >> 2) * panel, id_s,
+                           x > 0);
+                }
+                mma_commit(&ctl.s_full[s]);
+                mma_commit(&ctl.empty[p.stage]);
+                if (last) mma_commit(&ctl.q_free);
+            };
             for (int i = 0; i < 2 * n; ++i) {
                 const bool is_v = vv < n && ring_v<PAIR>(vv, n) == i;
                 const int k = is_v ? vv++ : kk++;
@@ -917,18 +935,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     if (lane == 0) sv::mbar_arrive(&ctl.empty[at.stage]);
                 } else if (!is_v) {
                     fence_after();
-                    if (elect_one()) {
-                        const uint64_t b = dk + at.stage * (X::kTileBytes >> 4);
-#pragma unroll
-                        for (int x = 0; x < DP / 16; ++x) {
-                            const uint32_t o = (x & 3) * 2;
-                            mma_ss(s_addr, dq + o + (x >> 2) * (X::kPanel >> 4),
-                                   b + o + (x >> 2) * panel, id_s, x > 0);
-                        }
-                        mma_commit(&ctl.s_full[s]);
-                        mma_commit(&ctl.empty[at.stage]);
-                        if (left == 1) mma_commit(&ctl.q_free);
-                    }
+                    if (elect_one()) scores(at, left == 1);
                     __syncwarp();
                     --left;
                 } else {
@@ -937,6 +944,30 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     if (!begun && item > 0 && !(ok = wait_all(&ctl.o_free, item - 1))) break;
                     if (!(ok = wait_all(&ctl.p_ready[s], tiles))) break;
                     ++tiles;
+                    // The slot's next keys are next in the ring. Where they are there
+                    // already their scores follow at once: looking at a barrier
+                    // between the two would let the tensor core run dry.
+                    Place<S> next = at;
+                    next.advance(1);
+                    const bool both =
+                        left > 0 && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.full[next.stage],
+                                                                      next.round & 1u));
+                    if (PAIR) {
+                        // One slot's products after the other's: side by side both
+                        // would end late, and both softmaxes would then run while
+                        // the tensor core idles.
+                        const long long t0 = clock64();
+                        bool got;
+                        do {
+                            got = __any_sync(0xFFFFFFFFu,
+                                             lane == 0 && atomicCAS(&ctl.burst, 0, 1) == 0) != 0;
+                        } while (!got && __all_sync(0xFFFFFFFFu, *stop == 0 && clock64() - t0 <
+                                                                                  sv::kWaitLimitCycles));
+                        if (!(ok = got)) {
+                            *stop = 1;
+                            break;
+                        }
+                    }
                     fence_after();
                     if (elect_one()) {
                         const uint64_t b = dv + at.stage * (X::kTileBytes >> 4);
@@ -944,9 +975,19 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         for (int x = 0; x < kTile / 16; ++x)
                             mma_ts(o_addr, s_addr + 64 + x * 8, b + x * v_step, id_o, begun || x > 0);
                         mma_commit(&ctl.empty[at.stage]);
+                        if (both) scores(next, left == 1);
+                        if (PAIR) atomicExch(&ctl.burst, 0);
                     }
                     __syncwarp();
                     begun = true;
+                    if (both) {
+                        if (edge) fixes ^= 1u << at.stage;
+                        --left;
+                        ++kk;
+                        ++i;
+                        at.advance(2);
+                        continue;
+                    }
                 }
                 if (edge) fixes ^= 1u << at.stage;
                 at.advance(1);

@@ -45,6 +45,20 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
     return d;
 }
 
+// Whether phase `parity` of `bar` is complete.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(sv::smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -219,6 +233,34 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[64], uint32_t 
           "=f"(w[58]), "=f"(w[59]), "=f"(w[60]), "=f"(w[61]), "=f"(w[62]), "=f"(w[63])
         : "r"(addr), "r"(addr_w)
         : "memory");
+}
+// The same, and the largest of all columns (NaN left out).
+__device__ __forceinline__ float tmem_ld_max(uint32_t addr, float (&v)[32], uint32_t addr_w,
+                                             float (&w)[32])
+{
+    float a, b;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, "
+        "%7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+        "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %64, [%66]; "
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%32, %33, %34, %35, %36, "
+        "%37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, "
+        "%52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, %65, [%67]; "
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]),
+          "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+          "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]),
+          "=f"(v[31]), "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]),
+          "=f"(w[6]), "=f"(w[7]), "=f"(w[8]), "=f"(w[9]), "=f"(w[10]), "=f"(w[11]),
+          "=f"(w[12]), "=f"(w[13]), "=f"(w[14]), "=f"(w[15]), "=f"(w[16]), "=f"(w[17]),
+          "=f"(w[18]), "=f"(w[19]), "=f"(w[20]), "=f"(w[21]), "=f"(w[22]), "=f"(w[23]),
+          "=f"(w[24]), "=f"(w[25]), "=f"(w[26]), "=f"(w[27]), "=f"(w[28]), "=f"(w[29]),
+          "=f"(w[30]), "=f"(w[31]), "=f"(a), "=f"(b)
+        : "r"(addr), "r"(addr_w)
+        : "memory");
+    return fmaxf(a, b);
 }
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[16])
 {
