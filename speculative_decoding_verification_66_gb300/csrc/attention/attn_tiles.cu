@@ -29,7 +29,7 @@
 //             look after one slot's barriers while the other's products run.
 //   9, 10     load keys and values: page numbers, a bulk tensor copy a page,
 //             exponents. Warp 9 also plans the block's segments for all.
-//   12-15     helpers. 16-bit caches: make the values at a tile's hidden
+//   12-..     helpers (4; e4m3: 8). 16-bit caches: make the values at a tile's hidden
 //             positions harmless. e4m3 caches: also expand every tile, exactly,
 //             into the stage that the products read.
 // The next segment's queries are fetched while the last products of a segment
@@ -45,11 +45,13 @@
 // never have been written.
 //
 // e4m3. Values are expanded to the query's type, code and exponent, which is
-// exact (expand_values). Of keys only the codes are, to float16, two an
-// instruction; their exponents are columns of the scores, which are multiplied
-// by them in float32. bfloat16 queries become float16 for this, each row scaled
-// by a power of two that brings its largest element to [2^14, 2^15): exact down
-// to 2^-38 of that.
+// exact. Keys are expanded to float16 relative to the largest exponent of their
+// tile, which multiplies the tile's scores: exact for keys down to 2^-15 of the
+// tile's largest, and to 2^-33 of the largest key's magnitude below that, far
+// under what float32 keeps of that key's scores. bfloat16 queries become float16
+// for this, each row scaled by a power of two that brings its largest element to
+// [2^14, 2^15): exact down to 2^-38 of that. float16 takes 25 instructions for 16
+// codes, bfloat16 45: the helpers' time is what bounds e4m3 caches.
 //
 // Work is shared among one block per SM as attn_plan.cuh says; items that
 // several blocks share are joined by join_kernel in block order, so results
@@ -83,8 +85,12 @@ struct Shape {
     static constexpr int kStages = DP == 128 ? (E4M3 ? 3 : (PAIR ? 5 : 6)) : (E4M3 ? 4 : 8);
     static constexpr int kRawStages = E4M3 ? (DP == 128 ? (PAIR ? 3 : 5) : 8) : 0;
     static_assert((kStages + kRawStages) / 2 + 1 < kItems - 2, "notes");
-    static constexpr int kHelpers = 4;
-    static constexpr int kThreads = 512;
+    static constexpr int kHelpers = E4M3 ? 8 : 4;
+    static constexpr int kThreads = (12 + kHelpers) * 32;
+    // e4m3: registers a thread of the softmax warps and of the others; together
+    // no more than the 640 threads are launched with, 96 each.
+    static constexpr int kRegsRow = 128, kRegsOther = 72, kRegsLaunch = 96;
+    static_assert(8 * kRegsRow + 12 * kRegsOther <= 20 * kRegsLaunch, "registers");
     static constexpr int kPanel = kTile * 128;  // bytes of 64 elements of every row
     static constexpr int kTiles = kQBytes + kStages * kTileBytes + kRawStages * kRawBytes;
 };
@@ -114,14 +120,18 @@ struct Control {
     int stop;
     int burst;  // PAIR: a slot's products are under way
     Start start;
-    int64_t sums[16];
+    int64_t sums[20];
     Plan plan[kItems];
     int noted[kItems];             // how many positions are noted
     int note[kItems][kNoted];      // which, counted as in the plan
     int bad_page[kItems];
     // e4m3: powers of two that the rows of this segment and the next are divided by
     float q_scale[2][RAW > 0 ? (PAIR ? 256 : 128) : 1];
-    alignas(16) float k_scale[RAW > 0 ? 5 : 1][RAW > 0 ? kTile : 4];  // .. of the last tiles' keys; 1
+    float k_scale[4];  // .. and of the keys of the last four tiles
+    // e4m3, for every raw stage: a row's factor (two 16-bit halves), the largest
+    // exponent (keys), whether some row needs two factors (values), exponents.
+    alignas(16) uint32_t factor[RAW > 0 ? RAW : 1][RAW > 0 ? kTile : 4];
+    uint32_t top[RAW > 0 ? RAW : 1], two[RAW > 0 ? RAW : 1];
     uint8_t exps[RAW > 0 ? RAW : 1][RAW > 0 ? kTile : 4];
 };
 
@@ -268,31 +278,24 @@ __device__ __forceinline__ uint2 spread(uint32_t w, F16)
 {
     return make_uint2(e4m3_to_f16x2(w & 0xFFFFu), e4m3_to_f16x2(w >> 16));
 }
+// Factor of a key's codes relative to the tile's largest exponent.
+__device__ __forceinline__ uint32_t key_factor(uint32_t e, uint32_t top)
+{
+    if (e == 255u) return both(0x7FFFu);
+    const int d = static_cast<int>(top) - static_cast<int>(e);
+    return both(d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u);
+}
+// 16 codes times a factor, as sixteen 16-bit values.
 template <class T>
-__device__ __forceinline__ void expand_values(uint4 codes, const Factor& f, uint4* lo, uint4* hi)
+__device__ __forceinline__ void expand(uint4 codes, uint32_t f, uint32_t (&o)[8])
 {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint2 s = spread(w[i], T());
-        o[2 * i] = mul2(s.x, f.f1, T());
-        o[2 * i + 1] = mul2(s.y, f.f1, T());
+        o[2 * i] = mul2(s.x, f, T());
+        o[2 * i + 1] = mul2(s.y, f, T());
     }
-    if (f.two) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = mul2(o[i], f.f2, T());
-    }
-    *lo = make_uint4(o[0], o[1], o[2], o[3]);
-    *hi = make_uint4(o[4], o[5], o[6], o[7]);
-}
-// The codes alone, as float16.
-__device__ __forceinline__ void expand_codes(uint4 c, uint4* lo, uint4* hi)
-{
-    const uint2 a = spread(c.x, F16()), b = spread(c.y, F16());
-    const uint2 d = spread(c.z, F16()), e = spread(c.w, F16());
-    *lo = make_uint4(a.x, a.y, b.x, b.y);
-    *hi = make_uint4(d.x, d.y, e.x, e.y);
 }
 
 __device__ __forceinline__ bool any_special(uint4 w, uint32_t exponent)
@@ -461,7 +464,6 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         for (int i = 0; i < kItems; ++i) ctl.noted[i] = ctl.bad_page[i] = 0;
         sv::fence_barrier_init();
     }
-    if (E4M3 && threadIdx.x < kTile) ctl.k_scale[4][threadIdx.x] = 1.f;
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          sv::smem_addr(&ctl.tmem)),
@@ -543,6 +545,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         // ------------------------------------------------------------------
         // Softmax of slot s; thread = row.
         // ------------------------------------------------------------------
+        if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kRegsRow));
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t s_addr = lane_base + s * 128, o_addr = lane_base + 256 + s * DP;
@@ -629,20 +632,20 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                 const int low = a.window > 0 ? pos - static_cast<int>(a.window) + 1 : INT_MIN / 2;
                 const int k0 = PAIR ? (s ? g.lo1 : g.lo0) : s;
                 const int k1 = PAIR ? (s ? g.hi1 : g.hi0) : g.n;
-                float c = a.scale_log2;
+                float row_c = a.scale_log2, c = row_c;
                 for (int k = k0; k < k1; k += PAIR ? 1 : 2) {
                     if (!(ok = wait_all(&ctl.s_full[s], tiles_done))) break;
                     ++tiles_done;
                     if (live) {
                         fence_after();
                         if (E4M3 && std::is_same<T, Bf16>::value && !begun)
-                            c = a.scale_log2 * ctl.q_scale[item & 1][min(slot_row, rows - 1)];
+                            row_c = a.scale_log2 * ctl.q_scale[item & 1][min(slot_row, rows - 1)];
                         const int clo = low - k * kTile, chi = pos - k * kTile;
                         const bool masked =
                             __any_sync(0xFFFFFFFFu, clo > 0 || chi < kTile - 1) != 0;
                         // The loops below are kept rolled: all roles' code has to
                         // stay in the instruction caches.
-                        const float* ks = &ctl.k_scale[E4M3 ? (tiles_before + k) & 3 : 0][0];
+                        if (E4M3) c = row_c * ctl.k_scale[(tiles_before + k) & 3];
                         if (masked) {
 #pragma unroll 1
                             for (int x = 0; x < kTile; x += 16) {
@@ -650,53 +653,16 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                                 tmem_ld(s_addr + x, v);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
-                                    v[i] = x + i >= clo && x + i <= chi
-                                               ? (E4M3 ? v[i] * ks[x + i] : v[i])
-                                               : ninf;
+                                    v[i] = x + i >= clo && x + i <= chi ? v[i] : ninf;
                                 tmem_st(s_addr + x, v);
                             }
                             tmem_wait_st();
-                            if (E4M3) ks = &ctl.k_scale[4][0];
                         }
-                        // 64 columns; e4m3: times their keys' powers of two.
                         float va[32], vb[32];
-                        auto load = [&](int x) {
-                            tmem_ld(s_addr + x, va, s_addr + x + 32, vb);
-                            if constexpr (E4M3) {
-#pragma unroll
-                                for (int i = 0; i < 32; i += 4) {
-                                    const float4 ka = *reinterpret_cast<const float4*>(ks + x + i);
-                                    const float4 kb =
-                                        *reinterpret_cast<const float4*>(ks + x + 32 + i);
-                                    float2 p = mul2f(make_float2(va[i], va[i + 1]),
-                                                     make_float2(ka.x, ka.y));
-                                    float2 q = mul2f(make_float2(va[i + 2], va[i + 3]),
-                                                     make_float2(ka.z, ka.w));
-                                    va[i] = p.x, va[i + 1] = p.y, va[i + 2] = q.x, va[i + 3] = q.y;
-                                    p = mul2f(make_float2(vb[i], vb[i + 1]), make_float2(kb.x, kb.y));
-                                    q = mul2f(make_float2(vb[i + 2], vb[i + 3]),
-                                              make_float2(kb.z, kb.w));
-                                    vb[i] = p.x, vb[i + 1] = p.y, vb[i + 2] = q.x, vb[i + 3] = q.y;
-                                }
-                            }
-                        };
                         float mt = ninf;
 #pragma unroll 1
-                        for (int x = 0; x < kTile; x += 64) {
-                            if constexpr (E4M3) {
-                                load(x);
-                                float t[4] = {va[0], va[1], va[2], va[3]};
-#pragma unroll
-                                for (int i = 0; i < 32; i += 4) {
-#pragma unroll
-                                    for (int z = 0; z < 4; ++z)
-                                        t[z] = fmaxf(t[z], fmaxf(va[i + z], vb[i + z]));
-                                }
-                                mt = fmaxf(mt, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
-                            } else {
-                                mt = fmaxf(mt, tmem_ld_max(s_addr + x, va, s_addr + x + 32, vb));
-                            }
-                        }
+                        for (int x = 0; x < kTile; x += 64)
+                            mt = fmaxf(mt, tmem_ld_max(s_addr + x, va, s_addr + x + 32, vb));
                         // (scale > 0; a NaN score is left out here and comes through below)
                         mt *= c;
                         const bool grow = mt > m + slack(T()) || (!begun && mt > m);
@@ -741,7 +707,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             weigh(va, s_addr + 64 + x / 2);
                             weigh(vb, s_addr + 64 + x / 2 + 16);
                             if (x == 0) break;
-                            load(0);
+                            tmem_ld(s_addr, va, s_addr + 32, vb);
                         }
                         l += (l0.x + l0.y) + (l1.x + l1.y);
                         tmem_wait_st();
@@ -887,7 +853,9 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             }
             if (lane == 0) sv::mbar_arrive(&ctl.o_free);
         }
-    } else if (warp == 8 || warp == 11) {
+    } else {
+    if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kRegsOther));
+    if (warp == 8 || warp == 11) {
         // ------------------------------------------------------------------
         // Products of slot s: the warp stays together, one lane issues. It
         // passes every tile in ring order, its own and the other slot's.
@@ -942,16 +910,18 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     if (edge && !(ok = wait_all(&ctl.fixed[at.stage], fixes >> at.stage))) break;
                     // (the results before have been read)
                     if (!begun && item > 0 && !(ok = wait_all(&ctl.o_free, item - 1))) break;
-                    if (!(ok = wait_all(&ctl.p_ready[s], tiles))) break;
-                    ++tiles;
                     // The slot's next keys are next in the ring. Where they are there
                     // already their scores follow at once: looking at a barrier
                     // between the two would let the tensor core run dry.
                     Place<S> next = at;
                     next.advance(1);
-                    const bool both =
+                    bool both =
                         left > 0 && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.full[next.stage],
                                                                       next.round & 1u));
+                    if (!(ok = wait_all(&ctl.p_ready[s], tiles))) break;
+                    ++tiles;
+                    if (left > 0 && !both)
+                        both = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.full[next.stage], next.round & 1u));
                     if (PAIR) {
                         // One slot's products after the other's: side by side both
                         // would end late, and both softmaxes would then run while
@@ -1101,9 +1071,37 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) = 1;
                     if (a.status != nullptr) atomicOr(a.status + g->b, kBadPage);
                 }
-                if (E4M3)
+                if constexpr (E4M3) {
+                    // Positions that no row sees may hold anything: exponent 0.
+                    uint32_t top = 0, f[4], two = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int p = k * kTile + lane * 4 + i;
+                        if (p < any_lo || p > any_hi) xc.e[i] = 0;
+                        if (xc.e[i] != 255u) top = max(top, xc.e[i]);
+                    }
+                    top = __reduce_max_sync(0xFFFFFFFFu, top);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (kv == 0) {
+                            f[i] = key_factor(xc.e[i], top);
+                        } else {
+                            const Factor x = factor_of(xc.e[i], T());
+                            f[i] = x.f1;
+                            two |= x.two && xc.e[i] != 0;
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(&ctl.factor[at.stage][lane * 4]) =
+                        make_uint4(f[0], f[1], f[2], f[3]);
                     *reinterpret_cast<uint32_t*>(&ctl.exps[at.stage][lane * 4]) =
                         xc.e[0] | xc.e[1] << 8 | xc.e[2] << 16 | xc.e[3] << 24;
+                    const bool any_two = __any_sync(0xFFFFFFFFu, two != 0) != 0;
+                    if (lane == 0) {
+                        ctl.top[at.stage] = top;
+                        ctl.two[at.stage] = any_two;
+                    }
+                    __syncwarp();
+                }
                 const bool leader = needed && first_of_box;
                 const unsigned boxes = __ballot_sync(0xFFFFFFFFu, leader);
                 if (lane == 0)
@@ -1144,11 +1142,11 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             for (int i = 0; i < kFill; ++i)
                 if (used >> i & 1u) sv::mbar_wait_bounded(&fullbar[i], rounds >> i & 1u, nullptr);
         }
-    } else if (warp >= 16 - X::kHelpers) {
+    } else {
         // ------------------------------------------------------------------
         // Helpers: hidden values, and e4m3.
         // ------------------------------------------------------------------
-        const int tid = (warp - (16 - X::kHelpers)) * 32 + lane;
+        const int tid = (warp - 12) * 32 + lane;
         constexpr int kThreadsH = X::kHelpers * 32;
         Place<S> at;
         Place<kFill> raw_at;
@@ -1200,7 +1198,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const uint32_t raw = sr + raw_at.stage * X::kRawBytes;
                     const uint32_t dst = st + at.stage * X::kTileBytes;
                     // A thread expands 16 codes of a row, the same piece of every
-                    // kStep-th row. Eight neighbouring lanes take half of the
+                    // kStep-th row, four at a time. Eight neighbouring lanes take half of the
                     // pieces of two rows, the other half of the second: their
                     // 16-byte columns differ in the loads and, swizzled, in the
                     // stores.
@@ -1211,22 +1209,20 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const bool in_row = piece * 16 < a.c.D;
                     const uint32_t from = raw + row0 * a.c.D + piece * 16;
                     const uint32_t to = dst + tile_chunk(row0, piece * 2, 1024, X::kPanel);
-                    const uint8_t* exps = &ctl.exps[raw_at.stage][0];
-                    if (!is_v) {
-                        for (int row = tid; row < kTile; row += kThreadsH)
-                            ctl.k_scale[k_tiles & 3][row] = exp_value(exps[row]);
-                    }
-                    constexpr int kBatch = 4;
+                    const uint32_t* factor = &ctl.factor[raw_at.stage][row0];
+                    const bool two = is_v && ctl.two[raw_at.stage] != 0;
+                    if (!is_v && tid == 0) ctl.k_scale[k_tiles & 3] = exp_value(ctl.top[raw_at.stage]);
+                    constexpr int kBatch = kTile / kStep < 4 ? kTile / kStep : 4;
 #pragma unroll 1
                     for (int i0 = 0; i0 < kTile / kStep; i0 += kBatch) {
                         uint4 codes[kBatch];
-                        uint32_t e[kBatch];
+                        uint32_t f[kBatch];
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
                             const int at_row = (i0 + u) * kStep;
                             codes[u] = in_row ? ld_shared_v4(from + at_row * a.c.D)
                                               : make_uint4(0, 0, 0, 0);
-                            e[u] = is_v ? exps[row0 + at_row] : 127u;
+                            f[u] = factor[at_row];
                         }
                         if (edge) {
 #pragma unroll
@@ -1234,25 +1230,31 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                                 const int p = k * kTile + row0 + (i0 + u) * kStep;
                                 const bool outside = p < g->any_lo || p > g->any_hi;
                                 const bool common = p >= g->all_lo && p <= g->all_hi;
-                                const bool clear = !outside && !common && e[u] == 255u;
+                                const bool clear = !outside && !common && f[u] == both(0x7FFFu);
                                 if (clear && piece == 0) note(p);
                                 if (outside || clear) {
                                     codes[u] = make_uint4(0, 0, 0, 0);
-                                    e[u] = 127u;
+                                    f[u] = 0;
                                 }
                             }
                         }
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
                             const uint32_t t = to + (i0 + u) * (kStep * 128);
-                            uint4 lo, hi;
+                            uint32_t o[8];
                             if (is_v)
-                                expand_values<T>(codes[u], factor_of(e[u], T()), &lo, &hi);
+                                expand<T>(codes[u], f[u], o);
                             else
-                                expand_codes(codes[u], &lo, &hi);
+                                expand<F16>(codes[u], f[u], o);
+                            if (two) {
+                                const uint32_t f2 =
+                                    factor_of(ctl.exps[raw_at.stage][row0 + (i0 + u) * kStep], T()).f2;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[i] = mul2(o[i], f2, T());
+                            }
                             // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
-                            st_shared_v4(t, lo);
-                            st_shared_v4(t ^ 16u, hi);
+                            st_shared_v4(t, make_uint4(o[0], o[1], o[2], o[3]));
+                            st_shared_v4(t ^ 16u, make_uint4(o[4], o[5], o[6], o[7]));
                         }
                     }
                     if (!is_v) ++k_tiles;
@@ -1267,6 +1269,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                 at.advance(1);
             }
         }
+    }
     }
     __syncthreads();
     if (threadIdx.x == 0) args.shares[blockIdx.x].failed = *stop;
@@ -1428,12 +1431,20 @@ cudaError_t launch_shape(const CUtensorMap& k, const CUtensorMap& v, const Tiles
     using Ctl = Control<X::kStages, X::kRawStages, PAIR>;
     constexpr size_t smem = X::kTiles + sizeof(Ctl);
     static_assert(smem <= kMaxSmem, "shared memory");
-    // (k_scale is read 16 bytes at a time)
+    // (factor is written 16 bytes at a time)
     static_assert(alignof(Ctl) == 16 && X::kTiles % 1024 == 0, "alignment");
     auto* f = tiles_kernel<T, DP, E4M3, PAIR>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
+    if (E4M3) {
+        // (the split of registers waits for what the block was not launched with)
+        static const int regs = [f] {
+            cudaFuncAttributes at{};
+            return cudaFuncGetAttributes(&at, f) == cudaSuccess ? at.numRegs : 0;
+        }();
+        if (regs < X::kRegsLaunch) return cudaErrorInvalidConfiguration;
+    }
     f<<<blocks, X::kThreads, smem, s>>>(k, v, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
