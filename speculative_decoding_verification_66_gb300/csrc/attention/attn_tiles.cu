@@ -658,11 +658,9 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             }
                             tmem_wait_st();
                         }
-                        float va[32], vb[32];
-                        float mt = ninf;
+                        float v[32], mt = ninf;
 #pragma unroll 1
-                        for (int x = 0; x < kTile; x += 64)
-                            mt = fmaxf(mt, tmem_ld_max(s_addr + x, va, s_addr + x + 32, vb));
+                        for (int x = 0; x < kTile; x += 32) mt = fmaxf(mt, tmem_ld_max(s_addr + x, v));
                         // (scale > 0; a NaN score is left out here and comes through below)
                         mt *= c;
                         const bool grow = mt > m + slack(T()) || (!begun && mt > m);
@@ -684,7 +682,10 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         begun = true;
                         const float shift = m == ninf ? 0.f : -m;
                         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-                        auto weigh = [&](const float (&v)[32], uint32_t to) {
+                        // The weights, the last 32 columns first: they take the
+                        // columns of the upper half from the top.
+#pragma unroll 1
+                        for (int x = kTile - 32;;) {
                             uint32_t w[16];
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
@@ -697,17 +698,10 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                                 w[i] = narrow2(p.x, p.y, T());
                                 w[i + 1] = narrow2(q.x, q.y, T());
                             }
-                            tmem_st(to, w);
-                        };
-                        // The weights: of the second half, which is in registers,
-                        // then of the first, read again. They take the columns of
-                        // the second half.
-#pragma unroll 1
-                        for (int x = 64;; x = 0) {
-                            weigh(va, s_addr + 64 + x / 2);
-                            weigh(vb, s_addr + 64 + x / 2 + 16);
+                            tmem_st(s_addr + 64 + x / 2, w);
                             if (x == 0) break;
-                            tmem_ld(s_addr, va, s_addr + 32, vb);
+                            x -= 32;
+                            tmem_ld(s_addr + x, v);
                         }
                         l += (l0.x + l0.y) + (l1.x + l1.y);
                         tmem_wait_st();
@@ -881,47 +875,30 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             bool begun = false;
             int kk = 0, vv = 0, left = k1 <= k0 ? 0 : PAIR ? k1 - k0 : (k1 - k0 + 1) / 2;
             if (left == 0 && lane == 0) sv::mbar_arrive(&ctl.q_free);
-            auto scores = [&](const Place<S>& p, bool last) {
-                const uint64_t b = dk + p.stage * (X::kTileBytes >> 4);
-#pragma unroll
-                for (int x = 0; x < DP / 16; ++x) {
-                    const uint32_t o = (x & 3) * 2;
-                    mma_ss(s_addr, dq + o + (x >> 2) * (X::kPanel >> 4), b + o + (x >> 2) * panel, id_s,
-                           x > 0);
-                }
-                mma_commit(&ctl.s_full[s]);
-                mma_commit(&ctl.empty[p.stage]);
-                if (last) mma_commit(&ctl.q_free);
-            };
             for (int i = 0; i < 2 * n; ++i) {
                 const bool is_v = vv < n && ring_v<PAIR>(vv, n) == i;
                 const int k = is_v ? vv++ : kk++;
                 const bool mine = k >= k0 && k < k1 && (PAIR || ((k - k0) & 1) == 0);
                 const bool edge = !E4M3 && is_v && (k < inner_lo || k > inner_hi);
                 if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
-                if (!mine) {
-                    if (lane == 0) sv::mbar_arrive(&ctl.empty[at.stage]);
-                } else if (!is_v) {
-                    fence_after();
-                    if (elect_one()) scores(at, left == 1);
-                    __syncwarp();
-                    --left;
-                } else {
+                Place<S> keys = at;
+                bool scores = mine && !is_v;
+                if (mine && is_v) {
                     if (edge && !(ok = wait_all(&ctl.fixed[at.stage], fixes >> at.stage))) break;
                     // (the results before have been read)
                     if (!begun && item > 0 && !(ok = wait_all(&ctl.o_free, item - 1))) break;
                     // The slot's next keys are next in the ring. Where they are there
                     // already their scores follow at once: looking at a barrier
                     // between the two would let the tensor core run dry.
-                    Place<S> next = at;
-                    next.advance(1);
-                    bool both =
-                        left > 0 && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.full[next.stage],
-                                                                      next.round & 1u));
-                    if (!(ok = wait_all(&ctl.p_ready[s], tiles))) break;
+                    keys.advance(1);
+                    for (int x = 0; x < 2; ++x) {
+                        if (left > 0 && !scores)
+                            scores = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.full[keys.stage],
+                                                                       keys.round & 1u));
+                        if (x == 0 && !(ok = wait_all(&ctl.p_ready[s], tiles))) break;
+                    }
+                    if (!ok) break;
                     ++tiles;
-                    if (left > 0 && !both)
-                        both = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.full[next.stage], next.round & 1u));
                     if (PAIR) {
                         // One slot's products after the other's: side by side both
                         // would end late, and both softmaxes would then run while
@@ -938,28 +915,44 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             break;
                         }
                     }
-                    fence_after();
+                }
+                fence_after();
+                if (mine) {
                     if (elect_one()) {
-                        const uint64_t b = dv + at.stage * (X::kTileBytes >> 4);
+                        if (is_v) {
+                            const uint64_t b = dv + at.stage * (X::kTileBytes >> 4);
 #pragma unroll
-                        for (int x = 0; x < kTile / 16; ++x)
-                            mma_ts(o_addr, s_addr + 64 + x * 8, b + x * v_step, id_o, begun || x > 0);
-                        mma_commit(&ctl.empty[at.stage]);
-                        if (both) scores(next, left == 1);
-                        if (PAIR) atomicExch(&ctl.burst, 0);
+                            for (int x = 0; x < kTile / 16; ++x)
+                                mma_ts(o_addr, s_addr + 64 + x * 8, b + x * v_step, id_o,
+                                       begun || x > 0);
+                            mma_commit(&ctl.empty[at.stage]);
+                        }
+                        if (scores) {
+                            const uint64_t b = dk + keys.stage * (X::kTileBytes >> 4);
+#pragma unroll
+                            for (int x = 0; x < DP / 16; ++x) {
+                                const uint32_t o = (x & 3) * 2;
+                                mma_ss(s_addr, dq + o + (x >> 2) * (X::kPanel >> 4),
+                                       b + o + (x >> 2) * panel, id_s, x > 0);
+                            }
+                            mma_commit(&ctl.s_full[s]);
+                            mma_commit(&ctl.empty[keys.stage]);
+                            if (left == 1) mma_commit(&ctl.q_free);
+                        }
+                        if (PAIR && is_v) atomicExch(&ctl.burst, 0);
                     }
                     __syncwarp();
-                    begun = true;
-                    if (both) {
-                        if (edge) fixes ^= 1u << at.stage;
-                        --left;
-                        ++kk;
-                        ++i;
-                        at.advance(2);
-                        continue;
-                    }
+                    begun |= is_v;
+                    left -= scores;
+                } else if (lane == 0) {
+                    sv::mbar_arrive(&ctl.empty[at.stage]);
                 }
                 if (edge) fixes ^= 1u << at.stage;
+                if (is_v && scores) {
+                    ++kk;
+                    ++i;
+                    at.advance(1);
+                }
                 at.advance(1);
             }
             if (!ok) break;
@@ -1072,13 +1065,22 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     if (a.status != nullptr) atomicOr(a.status + g->b, kBadPage);
                 }
                 if constexpr (E4M3) {
-                    // Positions that no row sees may hold anything: exponent 0.
-                    uint32_t top = 0, f[4], two = 0;
+                    // Positions that no row sees may hold anything: factor 0, which
+                    // the helpers turn into zeros. So do values that are NaN at
+                    // positions that not every row sees; these are noted.
+                    uint32_t top = 0, f[4], two = 0, hidden = 0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int p = k * kTile + lane * 4 + i;
-                        if (p < any_lo || p > any_hi) xc.e[i] = 0;
-                        if (xc.e[i] != 255u) top = max(top, xc.e[i]);
+                        if (p < any_lo || p > any_hi) {
+                            hidden |= 1u << i;
+                        } else if (xc.e[i] != 255u) {
+                            top = max(top, xc.e[i]);
+                        } else if (kv == 1 && (p < g->all_lo || p > g->all_hi)) {
+                            hidden |= 1u << i;
+                            const int x = atomicAdd(&ctl.noted[item % kItems], 1);
+                            if (x < kNoted) ctl.note[item % kItems][x] = p;
+                        }
                     }
                     top = __reduce_max_sync(0xFFFFFFFFu, top);
 #pragma unroll
@@ -1088,8 +1090,9 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         } else {
                             const Factor x = factor_of(xc.e[i], T());
                             f[i] = x.f1;
-                            two |= x.two && xc.e[i] != 0;
+                            two |= x.two && !(hidden >> i & 1u);
                         }
+                        if (hidden >> i & 1u) f[i] = 0;
                     }
                     *reinterpret_cast<uint4*>(&ctl.factor[at.stage][lane * 4]) =
                         make_uint4(f[0], f[1], f[2], f[3]);
@@ -1164,7 +1167,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             for (int i = 0; ok && i < 2 * n; ++i) {
                 const bool is_v = vv < n && ring_v<PAIR>(vv, n) == i;
                 const int k = is_v ? vv++ : kk++;
-                const bool edge = is_v && (k < inner_lo || k > inner_hi);
+                const bool edge = !E4M3 && is_v && (k < inner_lo || k > inner_hi);
                 if constexpr (!E4M3) {
                     if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
                     if (edge) {
@@ -1198,7 +1201,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const uint32_t raw = sr + raw_at.stage * X::kRawBytes;
                     const uint32_t dst = st + at.stage * X::kTileBytes;
                     // A thread expands 16 codes of a row, the same piece of every
-                    // kStep-th row, four at a time. Eight neighbouring lanes take half of the
+                    // kStep-th row, two at a time. Eight neighbouring lanes take half of the
                     // pieces of two rows, the other half of the second: their
                     // 16-byte columns differ in the loads and, swizzled, in the
                     // stores.
@@ -1207,55 +1210,53 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const int row0 = pair * 2 + odd;
                     const int piece = (tid & 3) + (kPieces > 4 ? (((tid >> 3) & 1) ^ odd) << 2 : 0);
                     const bool in_row = piece * 16 < a.c.D;
-                    const uint32_t from = raw + row0 * a.c.D + piece * 16;
+                    const uint32_t from = raw + row0 * a.c.D + (in_row ? piece * 16 : 0);
                     const uint32_t to = dst + tile_chunk(row0, piece * 2, 1024, X::kPanel);
                     const uint32_t* factor = &ctl.factor[raw_at.stage][row0];
-                    const bool two = is_v && ctl.two[raw_at.stage] != 0;
                     if (!is_v && tid == 0) ctl.k_scale[k_tiles & 3] = exp_value(ctl.top[raw_at.stage]);
-                    constexpr int kBatch = kTile / kStep < 4 ? kTile / kStep : 4;
+                    constexpr int kBatch = 2;
+                    auto expand_rows = [&](auto type) {
+                        using U = decltype(type);
 #pragma unroll 1
-                    for (int i0 = 0; i0 < kTile / kStep; i0 += kBatch) {
-                        uint4 codes[kBatch];
-                        uint32_t f[kBatch];
-#pragma unroll
-                        for (int u = 0; u < kBatch; ++u) {
-                            const int at_row = (i0 + u) * kStep;
-                            codes[u] = in_row ? ld_shared_v4(from + at_row * a.c.D)
-                                              : make_uint4(0, 0, 0, 0);
-                            f[u] = factor[at_row];
-                        }
-                        if (edge) {
+                        for (int r = 0; r < kTile; r += kBatch * kStep) {
+                            uint4 codes[kBatch];
+                            uint32_t f[kBatch];
 #pragma unroll
                             for (int u = 0; u < kBatch; ++u) {
-                                const int p = k * kTile + row0 + (i0 + u) * kStep;
-                                const bool outside = p < g->any_lo || p > g->any_hi;
-                                const bool common = p >= g->all_lo && p <= g->all_hi;
-                                const bool clear = !outside && !common && f[u] == both(0x7FFFu);
-                                if (clear && piece == 0) note(p);
-                                if (outside || clear) {
-                                    codes[u] = make_uint4(0, 0, 0, 0);
-                                    f[u] = 0;
-                                }
+                                const int row = r + u * kStep;
+                                codes[u] = ld_shared_v4(from + row * a.c.D);
+                                f[u] = in_row ? factor[row] : 0u;
+                            }
+#pragma unroll
+                            for (int u = 0; u < kBatch; ++u) {
+                                // (a factor of zero: whatever the codes are)
+                                if (f[u] == 0u) codes[u] = make_uint4(0, 0, 0, 0);
+                                uint32_t o[8];
+                                expand<U>(codes[u], f[u], o);
+                                // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
+                                const uint32_t t = to + (r + u * kStep) * 128;
+                                st_shared_v4(t, make_uint4(o[0], o[1], o[2], o[3]));
+                                st_shared_v4(t ^ 16u, make_uint4(o[4], o[5], o[6], o[7]));
                             }
                         }
-#pragma unroll
-                        for (int u = 0; u < kBatch; ++u) {
-                            const uint32_t t = to + (i0 + u) * (kStep * 128);
-                            uint32_t o[8];
-                            if (is_v)
-                                expand<T>(codes[u], f[u], o);
-                            else
-                                expand<F16>(codes[u], f[u], o);
-                            if (two) {
+                    };
+                    if (is_v) {
+                        expand_rows(T());
+                        if (ctl.two[raw_at.stage] != 0) {
+                            // Rare: some rows' second factor.
+#pragma unroll 1
+                            for (int r = 0; r < 2 * kTile; r += kStep) {
+                                const uint32_t t = (to + (r >> 1) / kStep * kStep * 128) ^ ((r / kStep & 1) << 4);
                                 const uint32_t f2 =
-                                    factor_of(ctl.exps[raw_at.stage][row0 + (i0 + u) * kStep], T()).f2;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) o[i] = mul2(o[i], f2, T());
+                                    factor_of(ctl.exps[raw_at.stage][row0 + (r >> 1) / kStep * kStep], T()).f2;
+                                uint4 x = ld_shared_v4(t);
+                                x = make_uint4(mul2(x.x, f2, T()), mul2(x.y, f2, T()),
+                                               mul2(x.z, f2, T()), mul2(x.w, f2, T()));
+                                st_shared_v4(t, x);
                             }
-                            // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
-                            st_shared_v4(t, make_uint4(o[0], o[1], o[2], o[3]));
-                            st_shared_v4(t ^ 16u, make_uint4(o[4], o[5], o[6], o[7]));
                         }
+                    } else {
+                        expand_rows(F16());
                     }
                     if (!is_v) ++k_tiles;
                     fence_async_smem();
