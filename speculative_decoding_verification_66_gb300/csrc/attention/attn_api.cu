@@ -235,9 +235,11 @@ SV_EXPORT int sv_chunk_attention(const sv_paged_cache* cache, const void* query,
     a.scale_log2 = scale * 1.44269504088896341f;
     const bool f16 = dtype == SV_F16, e4m3 = cache->dtype == SV_E4M3;
     bool done = false;
-    if (a.c.D <= kMaxTileDim && a.c.num_pages > 0 &&
-        sva::launch_attention_tiles(a, f16, e4m3, workspace, s, &done) != cudaSuccess)
-        return SV_ERR_CUDA;
+    if (a.c.D <= kMaxTileDim && a.c.num_pages > 0) {
+        const auto launch = max_chunk * a.G <= sva::kFewRows ? sva::launch_attention_few
+                                                             : sva::launch_attention_tiles;
+        if (launch(a, f16, e4m3, workspace, s, &done) != cudaSuccess) return SV_ERR_CUDA;
+    }
     if (!done && sva::launch_attention_rows(a, f16, e4m3, s) != cudaSuccess) return SV_ERR_CUDA;
     return SV_OK;
 }

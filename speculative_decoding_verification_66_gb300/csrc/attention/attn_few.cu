@@ -1,0 +1,641 @@
+// attn_few.cu -- attention over the paged cache for items of up to 32 rows (a
+// single token, a short draft), head sizes up to 128.
+//
+// Such items are bound by the reads of the cache: 2 D (1 + rows) operations meet
+// 2 bytes of a key (or 1), far from the tensor cores' balance. The 128-row
+// products of attn_tiles.cu would spend most of their time, and of the softmax
+// warps' time, on rows that do not exist; here eight warps take 16 keys each of
+// every 128-key tile, all rows, through m16n8k16 products in registers: the
+// scores' accumulators are the weights' operands as they lie, no tile goes
+// through tensor memory and no warp waits for another until the segment ends.
+// A warp keeps a maximum, a sum and an output of its own for every row; they
+// are joined through shared memory at the end of a segment.
+//
+// Warps 0-7 work, 8 and 9 load keys and values (attn_feed.cuh). Masks, hidden
+// values and the sharing among blocks are those of attn_tiles.cu.
+//
+// e4m3. A lane reads 16 codes of a row at a time and expands them in registers.
+// Keys: as float16 codes alone (the exponents multiply the scores' columns);
+// which d an operand's k slots stand for is free as long as the queries agree,
+// so slots 2c, 2c+1, 2c+8, 2c+9 of step (h, s) are d = 16 (2c + h) + 4 s + 0..3,
+// four neighbouring codes. Values: lane (g, c) reads d = DP/8 g .. of its four
+// keys; codes of two keys are interleaved, moved under the query type's exponent
+// and multiplied by the two keys' factors; the products' column n of step j is
+// then d = DP/8 n + j.
+#include "attn_feed.cuh"
+
+namespace sva {
+namespace {
+
+constexpr int kWorkers = 8;
+constexpr int kFewThreads = (kWorkers + 2) * 32;
+
+template <int DP, bool E4M3, int MT>
+struct FewShape {
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kTileBytes = kTile * DP * (E4M3 ? 1 : 2);
+    // Up to 192 KB of tiles.
+    static constexpr int kMost = E4M3 ? 10 : 12;
+    static constexpr int kStages = 196608 / kTileBytes < kMost ? 196608 / kTileBytes : kMost;
+    static constexpr int kSteps = DP / 16;                  // products along d
+    static constexpr int kQBytes = MT * kSteps * 32 * 16;   // operands as the lanes hold them
+    static constexpr int kJoin = MT == 1 ? 32 : 16;         // columns joined at a time
+    static constexpr int kJoinBytes = kWorkers * kRows * kJoin * 4;
+    static constexpr int kBytes = kStages * kTileBytes + kQBytes + kJoinBytes;
+};
+
+template <int STAGES, bool E4M3, int MT>
+struct FewControl {
+    uint64_t full[STAGES], empty[STAGES], sync;
+    uint64_t plan_ready[kItems];
+    int stop;
+    Start start;
+    int64_t sums[kFewThreads / 32];
+    Plan plan[kItems];
+    int noted[kItems];
+    int note[kItems][kNoted];
+    int bad_page[kItems];
+    float2 ml[kWorkers][16 * MT];
+    float q_scale[16 * MT];
+    alignas(16) uint32_t factor[E4M3 ? STAGES : 1][E4M3 ? kTile : 4];
+    uint32_t top[E4M3 ? STAGES : 1], two[E4M3 ? STAGES : 1];
+    uint8_t exps[E4M3 ? STAGES : 1][E4M3 ? kTile : 4];
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, Bf16)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, F16)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <class T, int DP, bool E4M3, int MT>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+               const __grid_constant__ Tiles args)
+{
+    using X = FewShape<DP, E4M3, MT>;
+    constexpr int S = X::kStages, R = X::kRows;
+    // Type of the first product's operands.
+    using TS = typename std::conditional<E4M3, F16, T>::type;
+    const Attn& a = args.a;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    FewControl<S, E4M3, MT>& ctl = *reinterpret_cast<FewControl<S, E4M3, MT>*>(smem + X::kBytes);
+    const uint32_t st = sv::smem_addr(smem), sq = st + S * X::kTileBytes;
+    float* join = reinterpret_cast<float*>(smem + S * X::kTileBytes + X::kQBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    sv::pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            sv::mbar_init(&ctl.full[i], 1);
+            sv::mbar_init(&ctl.empty[i], kWorkers);
+        }
+        sv::mbar_init(&ctl.sync, kWorkers);
+        for (int i = 0; i < kItems; ++i) sv::mbar_init(&ctl.plan_ready[i], 1);
+        ctl.stop = (st & 1023u) != 0;  // (see attn_tiles.cu)
+        for (int i = 0; i < kItems; ++i) ctl.noted[i] = ctl.bad_page[i] = 0;
+        sv::fence_barrier_init();
+    }
+    find_start<R, kFewThreads>(a, ctl);
+    refuse_sequences<T>(a);
+    __syncthreads();
+    const Start start = ctl.start;
+    volatile int* stop = &ctl.stop;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (sv::mbar_wait_bounded(bar, parity & 1u, stop)) return true;
+        *stop = 1;
+        return false;
+    };
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0;
+    };
+    if (warp >= kWorkers) {
+        feed<T, DP, E4M3, R, false, false, S>(args, ctl, warp == kWorkers ? &kmap : &vmap,
+                                              warp - kWorkers, st, X::kTileBytes, ctl.full, ctl.empty,
+                                              start, wait_all);
+    } else {
+        const int g = lane >> 2, c4 = lane & 3;
+        const float ninf = __uint_as_float(sv::kF32NegInfBits);
+        uint32_t syncs = 0;
+        // All eight warps come here; what they wrote before is seen after.
+        auto meet = [&] {
+            __syncwarp();
+            if (lane == 0) sv::mbar_arrive(&ctl.sync);
+            return wait_all(&ctl.sync, syncs++);
+        };
+        Place<S> at;
+        bool ok = true;
+        for (int item = 0; ok; ++item) {
+            const Plan* plan = plan_at(ctl, item, wait_all);
+            if (plan == nullptr) break;
+            const Plan& p = *plan;
+            const int n = p.n, rows = p.rows;
+            auto row_ptr = [&](int r) {
+                const int rr = p.row0 + r, t = rr / a.G;
+                return a.q + (static_cast<int64_t>(p.q0) + t) * a.q_token +
+                       static_cast<int64_t>(p.h * a.G + (rr - t * a.G)) * a.q_head;
+            };
+            // The queries' operands, as the lanes will hold them: step w by warp w.
+            // (Every warp has done with those of the segment before: it came to
+            // that segment's last meeting.)
+            if constexpr (E4M3 && std::is_same<T, Bf16>::value) {
+                // To float16: powers of two that bring a row's largest element to
+                // [2^14, 2^15).
+                for (int r = warp; r < R; r += kWorkers) {
+                    uint32_t top = 0;
+                    if (r < rows && lane * 4 < a.c.D) {
+                        const uint2 u = *reinterpret_cast<const uint2*>(row_ptr(r) + lane * 8);
+                        top = max(max(u.x << 16 & 0x7FFF0000u, u.x & 0x7FFF0000u),
+                                  max(u.y << 16 & 0x7FFF0000u, u.y & 0x7FFF0000u));
+                    }
+                    top = __reduce_max_sync(0xFFFFFFFFu, top);
+                    if (lane == 0)
+                        ctl.q_scale[r] =
+                            __uint_as_float(static_cast<uint32_t>(max(static_cast<int>(top >> 23), 15) - 14)
+                                            << 23);
+                }
+                if (!(ok = meet())) break;
+            }
+            for (int step = warp; step < X::kSteps; step += kWorkers) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t f[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int r = mt * 16 + half * 8 + g;
+                        if (r >= rows) continue;
+                        const uint8_t* q = row_ptr(r);
+                        uint2 u = make_uint2(0, 0);
+                        if constexpr (E4M3) {
+                            // d = 16 (2 c + h) + 4 s (DP = 64: 16 c + 4 s)
+                            const int d = (DP == 128 ? 16 * (2 * c4 + (step >> 2)) : 16 * c4) +
+                                          4 * (step & 3);
+                            if (d < a.c.D) u = *reinterpret_cast<const uint2*>(q + d * 2);
+                            if constexpr (std::is_same<T, Bf16>::value) {
+                                const uint32_t e = __float_as_uint(ctl.q_scale[r]) >> 23;
+                                const float up = __uint_as_float((254u - e) << 23);
+                                u.x = narrow2(sv::bf16_lo(u.x) * up, sv::bf16_hi(u.x) * up, F16());
+                                u.y = narrow2(sv::bf16_lo(u.y) * up, sv::bf16_hi(u.y) * up, F16());
+                            }
+                        } else {
+                            const int d = 16 * step + 2 * c4;
+                            if (16 * step < a.c.D) {
+                                u.x = *reinterpret_cast<const uint32_t*>(q + d * 2);
+                                u.y = *reinterpret_cast<const uint32_t*>(q + d * 2 + 16);
+                            }
+                        }
+                        f[half] = u.x;
+                        f[2 + half] = u.y;
+                    }
+                    st_shared_v4(sq + ((mt * X::kSteps + step) * 32 + lane) * 16,
+                                 make_uint4(f[0], f[1], f[2], f[3]));
+                }
+            }
+            if (!(ok = meet())) break;
+
+            // This thread's rows: g + 8 i.
+            int pos[2 * MT], low[2 * MT];
+            float cs[2 * MT], m[2 * MT], l[2 * MT];
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                const int r = min(g + 8 * i, rows - 1);
+                pos[i] = p.cached + (p.row0 + r) / a.G;
+                low[i] = a.window > 0 ? pos[i] - static_cast<int>(a.window) + 1 : INT_MIN / 2;
+                cs[i] = a.scale_log2;
+                if constexpr (E4M3 && std::is_same<T, Bf16>::value) cs[i] *= ctl.q_scale[r];
+                m[i] = ninf;
+                l[i] = 0.f;
+            }
+            float o[MT][DP / 8][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int j = 0; j < DP / 8; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.f;
+
+            for (int k = 0; k < n; ++k) {
+                const bool edge = k < p.inner_lo || k > p.inner_hi;
+                const int key0 = 16 * warp;  // this warp's keys of the tile
+                // ---- scores: two products of eight keys side by side
+                if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
+                const uint32_t kt = st + at.stage * X::kTileBytes;
+                float s[MT][2][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[mt][t][i] = 0.f;
+                auto scores = [&](int step, const uint32_t (&b)[4]) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint4 q = ld_shared_v4(sq + ((mt * X::kSteps + step) * 32 + lane) * 16);
+                        const uint32_t f[4] = {q.x, q.y, q.z, q.w};
+                        mma16816(s[mt][0], f, b[0], b[1], TS());
+                        mma16816(s[mt][1], f, b[2], b[3], TS());
+                    }
+                };
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int h = 0; h < DP / 64; ++h) {
+                        uint4 w[2];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int row = key0 + 8 * t + g, ch = DP == 128 ? 2 * c4 + h : c4;
+                            w[t] = make_uint4(0, 0, 0, 0);
+                            if (ch * 16 < a.c.D) w[t] = ld_shared_v4(kt + row * a.c.D + few_swizzle<DP>(row, ch, args.swizzled) * 16);
+                        }
+                        const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+                        const uint32_t w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint2 x = spread(w0[i], F16()), y = spread(w1[i], F16());
+                            const uint32_t b[4] = {x.x, x.y, y.x, y.y};
+                            scores(4 * h + i, b);
+                        }
+                    }
+                    // The keys' powers of two.
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t e =
+                            *reinterpret_cast<const uint16_t*>(&ctl.exps[at.stage][key0 + 8 * t + 2 * c4]);
+                        const float e0 = exp_value(e & 255u), e1 = exp_value(e >> 8);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            s[mt][t][0] *= e0;
+                            s[mt][t][1] *= e1;
+                            s[mt][t][2] *= e0;
+                            s[mt][t][3] *= e1;
+                        }
+                    }
+                } else {
+                    const int row = key0 + (lane & 7) + ((lane >> 4) << 3);
+                    const uint32_t from = kt + (row >> 3) * args.group + (row & 7) * 128;
+                    const int y = ((lane >> 3) & 1) ^ (row & 7);
+#pragma unroll
+                    for (int step = 0; step < X::kSteps; ++step) {
+                        uint32_t b[4];
+                        ldmatrix4(from + (step >> 2) * args.panel + (((2 * (step & 3)) ^ y) << 4), b);
+                        scores(step, b);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) sv::mbar_arrive(&ctl.empty[at.stage]);
+                at.advance(1);
+                // ---- weights
+                if (edge) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int x = k * kTile + key0 + 8 * t + 2 * c4 + i;
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                if (x < low[2 * mt] || x > pos[2 * mt]) s[mt][t][i] = ninf;
+                                if (x < low[2 * mt + 1] || x > pos[2 * mt + 1]) s[mt][t][2 + i] = ninf;
+                            }
+                        }
+                }
+                bool grow = false;
+                float top[2 * MT];
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                    const float(&x)[2][4] = s[i >> 1];
+                    const int z = 2 * (i & 1);
+                    top[i] = fmaxf(fmaxf(x[0][z], x[0][z + 1]), fmaxf(x[1][z], x[1][z + 1])) * cs[i];
+                    grow |= top[i] > m[i] + slack(T());
+                }
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+                    for (int i = 0; i < 2 * MT; ++i) {
+                        float x = top[i];
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+                        if (x > m[i] + slack(T())) {
+                            const float keep = sv::ex2(m[i] - x);
+                            l[i] *= keep;
+#pragma unroll
+                            for (int j = 0; j < DP / 8; ++j) {
+                                o[i >> 1][j][2 * (i & 1)] *= keep;
+                                o[i >> 1][j][2 * (i & 1) + 1] *= keep;
+                            }
+                            m[i] = x;
+                        }
+                    }
+                }
+                uint32_t w[MT][4];
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                    const float shift = m[i] == ninf ? 0.f : -m[i];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const float p0 = sv::ex2(fmaf(s[i >> 1][t][2 * (i & 1)], cs[i], shift));
+                        const float p1 = sv::ex2(fmaf(s[i >> 1][t][2 * (i & 1) + 1], cs[i], shift));
+                        l[i] += p0 + p1;
+                        w[i >> 1][2 * t + (i & 1)] = narrow2(p0, p1, T());
+                    }
+                }
+                // ---- values
+                if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
+                const uint32_t vt = st + at.stage * X::kTileBytes;
+                if constexpr (E4M3) {
+                    // Keys 2 c, 2 c + 1 and those eight further, as two pairs.
+                    constexpr int kWords = DP / 32;  // of four codes of a key to a lane
+                    uint32_t f[4], codes[4][kWords];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const int row = key0 + 2 * c4 + (z & 1) + 8 * (z >> 1);
+                        f[z] = ctl.factor[at.stage][row] & 0xFFFFu;
+                        const uint32_t from = vt + row * a.c.D;
+                        if constexpr (DP == 128) {
+                            uint4 x = make_uint4(0, 0, 0, 0);
+                            if (g * 16 < a.c.D) x = ld_shared_v4(from + few_swizzle<DP>(row, g, args.swizzled) * 16);
+                            codes[z][0] = x.x, codes[z][1] = x.y, codes[z][2] = x.z, codes[z][3] = x.w;
+                        } else {
+                            uint2 x = make_uint2(0, 0);
+                            if (g * 8 < a.c.D)
+                                x = ld_shared_v2(from + few_swizzle<DP>(row, g >> 1, args.swizzled) * 16 + (g & 1) * 8);
+                            codes[z][0] = x.x, codes[z][1] = x.y;
+                        }
+                        if (edge && f[z] == 0u) {  // hidden: whatever the codes are
+#pragma unroll
+                            for (int i = 0; i < kWords; ++i) codes[z][i] = 0;
+                        }
+                    }
+                    const uint32_t f01 = f[0] | f[1] << 16, f23 = f[2] | f[3] << 16;
+                    uint32_t f01b = 0, f23b = 0;
+                    const bool two = ctl.two[at.stage] != 0;
+                    if (two) {
+                        const uint8_t* e = &ctl.exps[at.stage][key0 + 2 * c4];
+                        f01b = (factor_of(e[0], T()).f2 & 0xFFFFu) | factor_of(e[1], T()).f2 << 16;
+                        f23b = (factor_of(e[8], T()).f2 & 0xFFFFu) | factor_of(e[9], T()).f2 << 16;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kWords; ++i) {
+#pragma unroll
+                        for (int hi = 0; hi < 2; ++hi) {
+                            const int sel = hi ? 0x7362 : 0x5140;  // codes 2 hi, 2 hi + 1 of either key
+                            const uint2 x = spread(__byte_perm(codes[0][i], codes[1][i], sel), T());
+                            const uint2 y = spread(__byte_perm(codes[2][i], codes[3][i], sel), T());
+                            uint32_t x0 = mul2(x.x, f01, T()), x1 = mul2(x.y, f01, T());
+                            uint32_t y0 = mul2(y.x, f23, T()), y1 = mul2(y.y, f23, T());
+                            if (two) {
+                                x0 = mul2(x0, f01b, T()), x1 = mul2(x1, f01b, T());
+                                y0 = mul2(y0, f23b, T()), y1 = mul2(y1, f23b, T());
+                            }
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                mma16816(o[mt][4 * i + 2 * hi], w[mt], x0, y0, T());
+                                mma16816(o[mt][4 * i + 2 * hi + 1], w[mt], x1, y1, T());
+                            }
+                        }
+                    }
+                } else {
+                    if (edge) {
+                        // Hidden values: see attn_tiles.cu.
+                        constexpr int kLanes = DP / 8;  // lanes to a row
+#pragma unroll 1
+                        for (int x = lane; x < 16 * kLanes; x += 32) {
+                            const int row = key0 + x / kLanes, ch = x % kLanes, q = k * kTile + row;
+                            const uint32_t addr = vt + tile_chunk(row, ch, args.group, args.panel);
+                            const bool outside = q < p.any_lo || q > p.any_hi;
+                            const bool common = q >= p.all_lo && q <= p.all_hi;
+                            bool special = false;
+                            if (!outside && !common)
+                                special = any_special(ld_shared_v4(addr), exponent_mask(T()));
+                            const unsigned mask = __ballot_sync(0xFFFFFFFFu, special) >>
+                                                  (lane & ~(kLanes - 1));
+                            const bool clear = (mask & ((1ull << kLanes) - 1)) != 0;
+                            if (outside || clear) st_shared_v4(addr, make_uint4(0, 0, 0, 0));
+                            if (clear && ch == 0) {
+                                const int z = atomicAdd(&ctl.noted[item % kItems], 1);
+                                if (z < kNoted) ctl.note[item % kItems][z] = q;
+                            }
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+                    const int row = key0 + (lane & 7) + (((lane >> 3) & 1) << 3);
+                    const uint32_t from = vt + (row >> 3) * args.group + (row & 7) * 128;
+                    const int y = (lane >> 4) ^ (row & 7);
+#pragma unroll
+                    for (int j = 0; j < DP / 16; ++j) {
+                        uint32_t b[4];
+                        ldmatrix4_trans(from + (j >> 2) * args.panel + (((2 * (j & 3)) ^ y) << 4), b);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            mma16816(o[mt][2 * j], w[mt], b[0], b[1], T());
+                            mma16816(o[mt][2 * j + 1], w[mt], b[2], b[3], T());
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) sv::mbar_arrive(&ctl.empty[at.stage]);
+                at.advance(1);
+            }
+            if (!ok) break;
+
+            // ---- the warps' results joined
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+                if (c4 == 0) ctl.ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
+            }
+            if (!(ok = meet())) break;
+            const int noted = *reinterpret_cast<volatile int*>(&ctl.noted[item % kItems]);
+            const bool bad = *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0;
+            const bool whole = p.whole != 0;
+            const float nan = __uint_as_float(0x7FFFFFFFu);
+            float* share = args.part + (static_cast<int64_t>(blockIdx.x) * 2 + (p.begins ? 1 : 0)) *
+                                           args.part_rows * (DP + 4);
+            // A row that sees a noted position is computed again below.
+            auto again = [&](int r) {
+                if (noted == 0 || bad) return false;
+                const int at_row = p.cached + (p.row0 + r) / a.G;
+                const int from = a.window > 0 ? at_row - static_cast<int>(a.window) + 1 : INT_MIN / 2;
+                bool x = noted > kNoted;
+                for (int i = 0; i < min(noted, kNoted); ++i) {
+                    const int q = *reinterpret_cast<volatile int*>(&ctl.note[item % kItems][i]);
+                    x |= q >= from && q <= at_row;
+                }
+                return x;
+            };
+            auto row_max = [&](int r) {
+                float x = ninf;
+#pragma unroll
+                for (int w = 0; w < kWorkers; ++w) x = fmaxf(x, ctl.ml[w][r].x);
+                return x;
+            };
+            float weight[2 * MT];
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                const float top = row_max(g + 8 * i);
+                weight[i] = m[i] == top ? 1.f : sv::ex2(m[i] - top);
+            }
+            // kJoin columns at a time: every warp's, weighted, into shared memory;
+            // then all threads add up eight and write.
+            constexpr int kStepsJ = X::kJoin / 8;
+#pragma unroll
+            for (int j0 = 0; j0 < DP / 8; j0 += kStepsJ) {
+                if (j0 > 0 && !(ok = meet())) break;
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < kStepsJ; ++j)
+                        *reinterpret_cast<float2*>(
+                            join + (warp * R + g + 8 * i) * X::kJoin + j * 8 + 2 * c4) =
+                            make_float2(o[i >> 1][j0 + j][2 * (i & 1)] * weight[i],
+                                        o[i >> 1][j0 + j][2 * (i & 1) + 1] * weight[i]);
+                if (!(ok = meet())) break;
+                for (int x = threadIdx.x; x < R * X::kJoin; x += kWorkers * 32) {
+                    const int r = x / X::kJoin, y = x % X::kJoin;
+                    if (r >= rows || again(r)) continue;
+                    // e4m3: column n of step j is d = DP / 8 n + j
+                    const int j = E4M3 ? y % kStepsJ : y >> 3, col = E4M3 ? y / kStepsJ : y & 7;
+                    const int d = E4M3 ? DP / 8 * col + j0 + j : 8 * (j0 + j) + col;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWorkers; ++w)
+                        sum += join[(w * R + r) * X::kJoin + j * 8 + col];
+                    if (!whole) {
+                        share[static_cast<int64_t>(r) * (DP + 4) + d] = sum;
+                        continue;
+                    }
+                    if (d >= a.c.D) continue;
+                    const float top = row_max(r);
+                    float total = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWorkers; ++w) {
+                        const float2 z = ctl.ml[w][r];
+                        total += z.y * (z.x == top ? 1.f : sv::ex2(z.x - top));
+                    }
+                    const int rr = p.row0 + r, t = rr / a.G;
+                    const int64_t orow = (static_cast<int64_t>(p.q0) + t) * a.Hq + p.h * a.G +
+                                         (rr - t * a.G);
+                    *reinterpret_cast<uint16_t*>(a.out + (orow * a.c.D + d) * 2) =
+                        static_cast<uint16_t>(narrow2(bad ? nan : sum / total, 0.f, T()));
+                }
+            }
+            if (!ok) break;
+            if (threadIdx.x < rows && !again(threadIdx.x)) {
+                const int r = threadIdx.x;
+                const float top = row_max(r);
+                float total = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWorkers; ++w) {
+                    const float2 z = ctl.ml[w][r];
+                    total += z.y * (z.x == top ? 1.f : sv::ex2(z.x - top));
+                }
+                if (!whole) {
+                    share[static_cast<int64_t>(r) * (DP + 4) + DP] = top;
+                    share[static_cast<int64_t>(r) * (DP + 4) + DP + 1] = bad ? nan : total;
+                } else if (a.lse != nullptr) {
+                    const int rr = p.row0 + r, t = rr / a.G;
+                    a.lse[(static_cast<int64_t>(p.q0) + t) * a.Hq + p.h * a.G + (rr - t * a.G)] =
+                        bad ? nan : fmaf(top, kLn2, logf(total));
+                }
+            }
+            if (noted != 0 && !bad) {
+                for (int r = warp; r < rows; r += kWorkers) {
+                    __syncwarp();
+                    if (again(r))
+                        again_row<T, E4M3, DP>(args, p, r, share + static_cast<int64_t>(r) * (DP + 4));
+                }
+            }
+            __syncwarp();
+            // (see attn_tiles.cu; every warp has read the notes of two segments ago)
+            if (threadIdx.x == 0) {
+                ctl.noted[(item + kItems - 2) % kItems] = 0;
+                ctl.bad_page[(item + kItems - 2) % kItems] = 0;
+            }
+            if (!(ok = meet())) break;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) args.shares[blockIdx.x].failed = *stop;
+}
+
+template <class T, int DP, bool E4M3, int MT>
+cudaError_t launch_few_shape(const CUtensorMap& k, const CUtensorMap& v, const Tiles& t, int blocks,
+                             int64_t rows, cudaStream_t s)
+{
+    using X = FewShape<DP, E4M3, MT>;
+    using Ctl = FewControl<X::kStages, E4M3, MT>;
+    constexpr size_t smem = X::kBytes + sizeof(Ctl);
+    static_assert(smem <= kMaxSmem, "shared memory");
+    static_assert(alignof(Ctl) == 16 && X::kBytes % 1024 == 0, "alignment");
+    static_assert(X::kStages / 2 + 1 < kItems - 2, "notes");
+    auto* f = few_kernel<T, DP, E4M3, MT>;
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    f<<<blocks, kFewThreads, smem, s>>>(k, v, t);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_join<T, DP>(t, blocks, rows, s);
+}
+
+template <class T, int DP>
+cudaError_t launch_few_type(const CUtensorMap& k, const CUtensorMap& v, const Tiles& t, int blocks,
+                            int64_t rows, bool e4m3, cudaStream_t s)
+{
+    if (e4m3)
+        return rows <= 16 ? launch_few_shape<T, DP, true, 1>(k, v, t, blocks, rows, s)
+                          : launch_few_shape<T, DP, true, 2>(k, v, t, blocks, rows, s);
+    return rows <= 16 ? launch_few_shape<T, DP, false, 1>(k, v, t, blocks, rows, s)
+                      : launch_few_shape<T, DP, false, 2>(k, v, t, blocks, rows, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_few(const Attn& a, bool f16, bool e4m3, void* workspace,
+                                 cudaStream_t s, bool* mapped)
+{
+    CUtensorMap k, v;
+    Tiles t;
+    int blocks = 0;
+    const int64_t rows = a.max_chunk * a.G;
+    cudaError_t e = set_up(a, f16, e4m3, rows, workspace, true, &k, &v, &t, &blocks, mapped);
+    if (e != cudaSuccess || !*mapped) return e;
+    if (a.c.D <= 64)
+        return f16 ? launch_few_type<F16, 64>(k, v, t, blocks, rows, e4m3, s)
+                   : launch_few_type<Bf16, 64>(k, v, t, blocks, rows, e4m3, s);
+    return f16 ? launch_few_type<F16, 128>(k, v, t, blocks, rows, e4m3, s)
+               : launch_few_type<Bf16, 128>(k, v, t, blocks, rows, e4m3, s);
+}
+
+}  // namespace sva

@@ -22,6 +22,11 @@ size_t tiles_workspace(int64_t max_chunk, int64_t G, int64_t D);
 cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* workspace,
                                    cudaStream_t s, bool* mapped);
 
+// The same for at most kFewRows rows a sequence and key/value head.
+constexpr int64_t kFewRows = 32;
+cudaError_t launch_attention_few(const Attn& a, bool f16, bool e4m3, void* workspace,
+                                 cudaStream_t s, bool* mapped);
+
 // Any head size.
 cudaError_t launch_attention_rows(const Attn& a, bool f16, bool e4m3, cudaStream_t s);
 

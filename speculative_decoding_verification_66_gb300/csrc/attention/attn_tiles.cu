@@ -56,22 +56,11 @@
 // Work is shared among one block per SM as attn_plan.cuh says; items that
 // several blocks share are joined by join_kernel in block order, so results
 // depend on the lengths and the number of blocks alone.
-#include <climits>
-#include <type_traits>
-
-#include "attn_internal.h"
-#include "attn_plan.cuh"
-#include "tensor_core.cuh"
+#include "attn_feed.cuh"
 
 namespace sva {
 namespace {
 
-__device__ __forceinline__ float slack(Bf16) { return 60.f; }
-__device__ __forceinline__ float slack(F16) { return 14.f; }  // (below 65504, with 1 to spare)
-constexpr int kMaxBlocks = 160;  // shares in the workspace; grids are no larger
-constexpr int kNoted = 4;        // noted positions a segment can hold
-constexpr int kItems = 16;       // segments whose plans and notes are kept at one time
-constexpr size_t kMaxSmem = 232448;
 
 template <int DP, bool E4M3, bool PAIR>
 struct Shape {
@@ -93,20 +82,6 @@ struct Shape {
     static_assert(8 * kRegsRow + 12 * kRegsOther <= 20 * kRegsLaunch, "registers");
     static constexpr int kPanel = kTile * 128;  // bytes of 64 elements of every row
     static constexpr int kTiles = kQBytes + kStages * kTileBytes + kRawStages * kRawBytes;
-};
-
-// A segment as the warps need it. Positions count from the segment's first
-// tile; tiles are numbered from it.
-struct Plan {
-    int32_t n;                         // tiles; 0: no more segments
-    int32_t b, h, q0, row0, rows;
-    int32_t tile0;                     // the first tile's number in the sequence
-    int32_t cached;                    // row r stands at position cached + r / G
-    int32_t lo0, hi0, lo1, hi1;        // PAIR: tiles of either slot
-    int32_t any_lo, any_hi;            // positions that some row sees
-    int32_t all_lo, all_hi;            // positions that every row sees
-    int32_t inner_lo, inner_hi;        // tiles wholly in `all`; the others have hidden values
-    int32_t begins, whole;             // the item begins here; is all here
 };
 
 // Shared memory besides the tiles.
@@ -134,286 +109,6 @@ struct Control {
     uint32_t top[RAW > 0 ? RAW : 1], two[RAW > 0 ? RAW : 1];
     uint8_t exps[RAW > 0 ? RAW : 1][RAW > 0 ? kTile : 4];
 };
-
-struct Tiles {
-    Attn a;
-    float* part;   // [blocks][2][rows][part_cols]: unnormalised O, then m and l
-    Share* shares; // [blocks]
-    int32_t part_rows;
-    // A tile in shared memory: rows of 128 bytes (64 elements), eight to a
-    // group; bytes from a group to the next, and to the next 64 elements.
-    int32_t group, panel;
-    // Copies of whole 128-element rows: pages and heads are one axis, a page
-    // page_heads steps, a head head_step. 0: a copy for each 64 elements.
-    int32_t page_heads, head_step;
-};
-
-// Where the tiles of a segment lie in the ring: the order in which the products
-// use them. PAIR: K0 V0 K1 V1 ..; otherwise K0 K1 V0 K2 V1 .., since the second
-// slot's scores come before the first slot's values.
-template <bool PAIR>
-__device__ __forceinline__ int ring_v(int k, int n)
-{
-    return PAIR ? 2 * k + 1 : (k == n - 1 ? 2 * k + 1 : 2 * k + 2);
-}
-// From a tile's keys, and its values, to the next tile's.
-template <bool PAIR>
-__device__ __forceinline__ int ring_k_step(int k)
-{
-    return !PAIR && k == 0 ? 1 : 2;
-}
-template <bool PAIR>
-__device__ __forceinline__ int ring_v_step(int k, int n)
-{
-    return !PAIR && k == n - 2 ? 1 : 2;
-}
-
-// A place in a ring of S stages, and the round it is in.
-template <int S>
-struct Place {
-    int stage = 0;
-    uint32_t round = 0;
-    __device__ __forceinline__ void advance(int n)
-    {
-        stage += n;
-        while (stage >= S) {
-            stage -= S;
-            ++round;
-        }
-    }
-};
-
-__device__ __forceinline__ int clamp32(int64_t v)
-{
-    return static_cast<int>(max(min(v, int64_t(INT_MAX / 2)), int64_t(INT_MIN / 2)));
-}
-
-template <bool PAIR>
-__device__ __forceinline__ Plan plan_of(const Attn& a, const Segment& g)
-{
-    Plan p;
-    const int64_t origin = static_cast<int64_t>(g.t.lo) << kTileShift;
-    const int r1 = g.row0 + g.rows - 1;
-    const int64_t p0 = g.cached + g.row0 / a.G, p1 = g.cached + r1 / a.G;
-    p.n = g.t.hi - g.t.lo;
-    p.b = g.b;
-    p.h = g.h;
-    p.q0 = g.q0;
-    p.row0 = g.row0;
-    p.rows = g.rows;
-    p.tile0 = g.t.lo;
-    p.cached = clamp32(g.cached - origin);
-    p.any_lo = clamp32(first_key(a, p0) - origin);
-    p.any_hi = clamp32(p1 - origin);
-    p.all_lo = clamp32(first_key(a, p1) - origin);
-    p.all_hi = clamp32(p0 - origin);
-    p.inner_lo = (p.all_lo + kTile - 1) >> kTileShift;
-    p.inner_hi = ((p.all_hi + 1) >> kTileShift) - 1;
-    p.begins = g.t.lo == g.item.lo;
-    p.whole = p.begins && g.t.hi == g.item.hi;
-    p.lo0 = p.lo1 = 0;
-    p.hi0 = p.hi1 = p.n;
-    if (PAIR) {
-        const Range t0 = row_tiles(a, g.cached, g.row0, g.row0 + min(g.rows, 128));
-        p.lo0 = max(t0.lo - g.t.lo, 0);
-        p.hi0 = min(t0.hi - g.t.lo, p.n);
-        p.hi1 = 0;
-        if (g.rows > 128) {
-            const Range t1 = row_tiles(a, g.cached, g.row0 + 128, g.row0 + g.rows);
-            p.lo1 = max(t1.lo - g.t.lo, 0);
-            p.hi1 = min(t1.hi - g.t.lo, p.n);
-        }
-    }
-    return p;
-}
-
-// ---------------------------------------------------------------------------
-// Expanding e4m3. A value is code 2^(e - 127). bfloat16: the code's exponent
-// and mantissa bits, moved under bfloat16's wider exponent, read as the value
-// times 2^-120 (the biases differ by 127 - 7; subnormal codes land on subnormal
-// bfloat16s), so one multiplication by 2^(e - 7) gives the value exactly; it
-// takes two where that exceeds bfloat16. float16: the conversion instruction,
-// then one multiplication by 2^(e - 127), two where that is not a normal
-// float16. Either way two values an instruction.
-// ---------------------------------------------------------------------------
-struct Factor {
-    uint32_t f1, f2;  // both halves alike
-    bool two;
-};
-__device__ __forceinline__ uint32_t both(uint32_t h) { return h | (h << 16); }
-__device__ __forceinline__ Factor factor_of(uint32_t e, Bf16)
-{
-    const uint32_t x = min(e, 134u), y = e == 255u ? 0u : e - x;
-    return Factor{e == 255u ? both(0x7FFFu) : (x + 120u) * 0x00800080u, (y + 127u) * 0x00800080u,
-                  y != 0};
-}
-__device__ __forceinline__ Factor factor_of(uint32_t e, F16)
-{
-    if (e == 255u) return Factor{both(0x7FFFu), both(0x3C00u), false};
-    const int x = static_cast<int>(e) - 127;
-    const int g = min(max(x, -14), 15), h = x - g;
-    const uint32_t second = h < -24 ? 0u : h < -14 ? 1u << (h + 24) : (h > 15 ? 30u : h + 15u) << 10;
-    return Factor{both(static_cast<uint32_t>(g + 15) << 10), both(second), h != 0};
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b, Bf16)
-{
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b, F16)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// Four codes to two words of 16-bit values, before the factor.
-__device__ __forceinline__ uint2 spread(uint32_t w, Bf16)
-{
-    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-    return make_uint2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u),
-                      (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u));
-}
-__device__ __forceinline__ uint2 spread(uint32_t w, F16)
-{
-    return make_uint2(e4m3_to_f16x2(w & 0xFFFFu), e4m3_to_f16x2(w >> 16));
-}
-// Factor of a key's codes relative to the tile's largest exponent.
-__device__ __forceinline__ uint32_t key_factor(uint32_t e, uint32_t top)
-{
-    if (e == 255u) return both(0x7FFFu);
-    const int d = static_cast<int>(top) - static_cast<int>(e);
-    return both(d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u);
-}
-// 16 codes times a factor, as sixteen 16-bit values.
-template <class T>
-__device__ __forceinline__ void expand(uint4 codes, uint32_t f, uint32_t (&o)[8])
-{
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint2 s = spread(w[i], T());
-        o[2 * i] = mul2(s.x, f, T());
-        o[2 * i + 1] = mul2(s.y, f, T());
-    }
-}
-
-__device__ __forceinline__ bool any_special(uint4 w, uint32_t exponent)
-{
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    bool s = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        s |= (u[i] & exponent) == exponent || ((u[i] >> 16) & exponent) == exponent;
-    return s;
-}
-__device__ __forceinline__ uint32_t exponent_mask(Bf16) { return 0x7F80u; }
-__device__ __forceinline__ uint32_t exponent_mask(F16) { return 0x7C00u; }
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v)
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
-                 "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-// Byte offset of 16-byte chunk `chunk` of a row in a tile with the 128-byte
-// swizzle (group and panel: see Tiles).
-__device__ __forceinline__ uint32_t tile_chunk(int row, int chunk, int group, int panel)
-{
-    return (row >> 3) * group + (chunk >> 3) * panel + (row & 7) * 128 +
-           (((chunk & 7) ^ (row & 7)) << 4);
-}
-
-// Sum of int64 over the block; every thread gets it.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sums, int warps)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int64_t t = 0;
-    for (int w = 0; w < warps; ++w) t += sums[w];
-    return t;
-}
-
-// Rows of sequences whose lengths are bad become NaN; block c of n takes
-// sequences c, c + n, ..
-template <class T>
-__device__ void refuse_sequences(const Attn& a)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const uint32_t nan2 = narrow2(__uint_as_float(0x7FFFFFFFu), __uint_as_float(0x7FFFFFFFu), T());
-    for (int64_t base = blockIdx.x; base < a.c.B; base += static_cast<int64_t>(gridDim.x) * 32) {
-        const int64_t b = base + static_cast<int64_t>(gridDim.x) * lane;
-        Seq q{0, 0, 0, 0};
-        if (b < a.c.B) q = seq_of(a.c, static_cast<int>(b), a.tokens, a.max_chunk);
-        if (q.bad && a.status != nullptr && warp == 0) atomicOr(a.status + b, q.bad);
-        unsigned m = __ballot_sync(0xFFFFFFFFu, q.bad && q.count > 0);
-        while (m != 0) {
-            const int i = __ffs(static_cast<int>(m)) - 1;
-            m &= m - 1;
-            const int64_t t0 = __shfl_sync(0xFFFFFFFFu, q.start, i);
-            const int64_t n = __shfl_sync(0xFFFFFFFFu, q.count, i);
-            const int64_t words = n * a.Hq * a.c.D / 2, w0 = t0 * a.Hq * a.c.D / 2;
-            uint32_t* o = reinterpret_cast<uint32_t*>(a.out);
-            for (int64_t w = warp * 32 + lane; w < words; w += warps * 32) o[w0 + w] = nan2;
-            if (a.lse != nullptr)
-                for (int64_t w = warp * 32 + lane; w < n * a.Hq; w += warps * 32)
-                    a.lse[t0 * a.Hq + w] = __uint_as_float(0x7FFFFFFFu);
-        }
-    }
-}
-
-// Output row r of a segment: index of its (token, head) in [tokens, Hq].
-__device__ __forceinline__ int64_t out_row(const Attn& a, int q0, int h, int r)
-{
-    const int t = r / a.G;
-    return (static_cast<int64_t>(q0) + t) * a.Hq + h * a.G + (r - t * a.G);
-}
-
-// Row r of a segment's item again, key by key, by a warp: to the output or to the
-// block's share at `part`.
-template <class T, bool E4M3, int DP>
-__device__ __noinline__ void again_row(const Tiles& args, const Plan& g, int r, float* part)
-{
-    const Attn& a = args.a;
-    const int lane = threadIdx.x & 31;
-    const int64_t origin = static_cast<int64_t>(g.tile0) << kTileShift;
-    const int t = (g.row0 + r) / a.G, hq = g.h * a.G + (g.row0 + r - t * a.G);
-    const int64_t pos = origin + g.cached + t, token = static_cast<int64_t>(g.q0) + t;
-    const int64_t lo = max(first_key(a, pos), origin);
-    const int64_t hi = min(pos + 1, origin + (static_cast<int64_t>(g.n) << kTileShift));
-    const int64_t orow = token * a.Hq + hq;
-    float m, l, o[8];
-    attend_row<T, E4M3>(a, g.b, g.h, a.q + token * a.q_token + hq * a.q_head, lo, hi, lane, &m, &l, o);
-    if (g.whole) {
-        const float x = 1.f / l;
-        if (lane * 8 < a.c.D)
-            *reinterpret_cast<uint4*>(a.out + (orow * a.c.D + lane * 8) * 2) =
-                make_uint4(narrow2(o[0] * x, o[1] * x, T()), narrow2(o[2] * x, o[3] * x, T()),
-                           narrow2(o[4] * x, o[5] * x, T()), narrow2(o[6] * x, o[7] * x, T()));
-        if (a.lse != nullptr && lane == 0) a.lse[orow] = fmaf(m, kLn2, logf(l));
-        return;
-    }
-    if (lane * 8 < DP) {
-        *reinterpret_cast<float4*>(part + lane * 8) = make_float4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<float4*>(part + lane * 8 + 4) = make_float4(o[4], o[5], o[6], o[7]);
-    }
-    if (lane == 0) {
-        part[DP] = m;
-        part[DP + 1] = l;
-    }
-}
 
 template <class T, int DP, bool E4M3, bool PAIR>
 __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
@@ -472,54 +167,8 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
 
-    // Where this block starts.
-    {
-        const int tid = threadIdx.x;
-        int64_t mine = 0, first = 0;
-        for (int64_t b = tid; b < a.c.B; b += X::kThreads) {
-            const Seq q = seq_of(a.c, static_cast<int>(b), a.tokens, a.max_chunk);
-            const int64_t u = head_units<R>(a, q) * a.c.Hkv;
-            if (b == tid) first = u;
-            mine += u;
-        }
-        const int64_t U = block_sum(mine, ctl.sums, kWarps);
-        const int64_t u0 = share_begin(U, blockIdx.x, gridDim.x);
-        const int64_t u1 = share_begin(U, blockIdx.x + 1, gridDim.x);
-        if (tid == 0) ctl.start = Start{u0, u1, U, 0, 0};
-        __syncthreads();
-        if (u0 < u1) {
-            int64_t before = 0;
-            for (int64_t base_b = 0; base_b < a.c.B && before <= u0; base_b += X::kThreads) {
-                const int64_t b = base_b + tid;
-                int64_t u = first;
-                if (base_b > 0)
-                    u = b < a.c.B ? head_units<R>(a, seq_of(a.c, static_cast<int>(b), a.tokens,
-                                                            a.max_chunk)) * a.c.Hkv
-                                  : 0;
-                int64_t scan = u;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, scan, d);
-                    if (lane >= d) scan += o;
-                }
-                __syncthreads();
-                if (lane == 31) ctl.sums[warp] = scan;
-                __syncthreads();
-                int64_t chunk = 0;
-                for (int w = 0; w < kWarps; ++w) {
-                    if (w < warp) scan += ctl.sums[w];
-                    chunk += ctl.sums[w];
-                }
-                const int64_t begin = before + scan - u;
-                if (u0 >= begin && u0 < begin + u) {
-                    ctl.start.off = u0 - begin;
-                    ctl.start.b = static_cast<int32_t>(b);
-                }
-                before += chunk;
-            }
-        }
-        refuse_sequences<T>(a);
-    }
+    find_start<R, X::kThreads>(a, ctl);
+    refuse_sequences<T>(a);
     __syncthreads();
     fence_after();
     const uint32_t tmem = ctl.tmem;
@@ -534,12 +183,6 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0;
     };
     int item = 0;  // segments taken so far
-    // The next segment's plan, or nullptr when there is none or a wait ran out.
-    auto plan_at = [&](int i) -> const Plan* {
-        if (!wait_all(&ctl.plan_ready[i % kItems], i / kItems)) return nullptr;
-        const Plan* p = &ctl.plan[i % kItems];
-        return p->n > 0 ? p : nullptr;
-    };
 
     if (warp < 8) {
         // ------------------------------------------------------------------
@@ -614,7 +257,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             if (lane == 0) sv::mbar_arrive(&ctl.q_ready);
         };
 
-        const Plan* ahead = plan_at(0);
+        const Plan* ahead = plan_at(ctl, 0, wait_all);
         if (ahead != nullptr) {
             fetch(*ahead);
             store(*ahead, 0);
@@ -718,7 +361,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             // --------------------------------------------------------------
             const int n = g.n;
             tiles_before += n;
-            ahead = plan_at(item + 1);
+            ahead = plan_at(ctl, item + 1, wait_all);
             if (ahead != nullptr) {
                 fetch(*ahead);
                 if (!(ok = wait_all(&ctl.q_free, item))) break;
@@ -865,7 +508,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         uint32_t fixes = 0, tiles = 0;
         bool ok = true;
         for (; ok; ++item) {
-            const Plan* g = plan_at(item);
+            const Plan* g = plan_at(ctl, item, wait_all);
             if (g == nullptr || !(ok = wait_all(&ctl.q_ready, item))) break;
             const int n = g->n, inner_lo = g->inner_lo, inner_hi = g->inner_hi;
             const int k0 = PAIR ? (s ? g->lo1 : g->lo0) : s, k1 = PAIR ? (s ? g->hi1 : g->hi0) : n;
@@ -876,7 +519,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             int kk = 0, vv = 0, left = k1 <= k0 ? 0 : PAIR ? k1 - k0 : (k1 - k0 + 1) / 2;
             if (left == 0 && lane == 0) sv::mbar_arrive(&ctl.q_free);
             for (int i = 0; i < 2 * n; ++i) {
-                const bool is_v = vv < n && ring_v<PAIR>(vv, n) == i;
+                const bool is_v = vv < n && ring_v<!PAIR>(vv, n) == i;
                 const int k = is_v ? vv++ : kk++;
                 const bool mine = k >= k0 && k < k1 && (PAIR || ((k - k0) & 1) == 0);
                 const bool edge = !E4M3 && is_v && (k < inner_lo || k > inner_hi);
@@ -964,187 +607,11 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         __syncwarp();
         sv::mbar_wait_bounded(&ctl.done, 0, nullptr);
     } else if (warp == 9 || warp == 10) {
-        // ------------------------------------------------------------------
-        // Copies of keys (warp 9, which also plans the segments) and values
-        // (warp 10). The page of tile k + 2 and the exponents of tile k + 1 are
-        // on their way while tile k is issued.
-        // ------------------------------------------------------------------
-        const int kv = warp - 9;
-        const CUtensorMap* map = kv ? &vmap : &kmap;
-        uint64_t* fullbar = E4M3 ? ctl.raw_full : ctl.full;
-        uint64_t* emptybar = E4M3 ? ctl.raw_empty : ctl.empty;
-        const int P = 1 << a.c.page_shift, box = min(P, kTile);
-        const uint32_t box_bytes = E4M3 ? box * a.c.D : box * DP * 2;
-        const uint32_t lane_bytes = E4M3 ? lane * 4 * a.c.D : lane * 4 / 8 * args.group;
-        const bool first_of_box = P >= kTile ? lane == 0 : ((lane * 4) & (P - 1)) == 0;
-        const uint8_t* exps = kv ? a.c.exps[1] : a.c.exps[0];
-        const int64_t exp_step = kv ? a.c.exp_slot_stride[1] : a.c.exp_slot_stride[0];
-        Place<kFill> base_at;
-        uint32_t used = 0, rounds = 0;  // a stage's bit: filled by this warp; parity of the last fill
-        Walk<R> walk(a, start);
-        Share sh{};
-        int64_t units = start.u0;
-        bool ok = true;
-        for (; ok; ++item) {
-            const Plan* g;
-            if (kv == 0) {
-                Segment seg;
-                const bool any = walk.next(&seg);
-                Plan p{};
-                if (any) {
-                    p = plan_of<PAIR>(a, seg);
-                    units += p.n;
-                    if (p.begins && !p.whole) {
-                        // For join_kernel: the item that this block began and did
-                        // not finish, and the block that did.
-                        const int64_t end = units + (seg.item.hi - seg.t.hi) - 1;  // its last unit
-                        int c = blockIdx.x + 1;
-                        while (share_begin(start.U, c + 1, gridDim.x) <= end) ++c;
-                        sh.leads = 1;
-                        sh.b = p.b;
-                        sh.h = p.h;
-                        sh.row0 = p.row0;
-                        sh.rows = p.rows;
-                        sh.q0 = p.q0;
-                        sh.last = c;
-                    }
-                }
-                // (Its place was the plan of kItems segments ago, which the ring
-                // of tiles keeps out of everybody's reach.)
-                if (lane == 0) {
-                    ctl.plan[item % kItems] = p;
-                    sv::mbar_arrive(&ctl.plan_ready[item % kItems]);
-                }
-                __syncwarp();
-                if (!any) break;
-                g = &ctl.plan[item % kItems];
-            } else if ((g = plan_at(item)) == nullptr) {
-                break;
-            }
-            const int n = g->n, any_lo = g->any_lo, any_hi = g->any_hi, h = g->h;
-            const int64_t page_row = g->b * a.c.table_stride +
-                                     ((static_cast<int64_t>(g->tile0) << kTileShift) >> a.c.page_shift);
-            const int in_page0 =
-                static_cast<int>((static_cast<int64_t>(g->tile0) << kTileShift) & (P - 1));
-            // The table's entry for this lane's four positions in tile k; INT_MIN
-            // if no row sees a position of that page.
-            auto entry = [&](int k) {
-                const int p = k * kTile + lane * 4 + in_page0;  // from the first tile's page
-                const int page0 = (p & ~(P - 1)) - in_page0;
-                return k < n && page0 <= any_hi && page0 + P - 1 >= any_lo
-                           ? a.c.table[page_row + (p >> a.c.page_shift)]
-                           : INT_MIN;
-            };
-            auto good = [&](int32_t page) { return page >= 0 && page < a.c.num_pages; };
-            auto slot_of = [&](int k) { return (k * kTile + lane * 4 + in_page0) & (P - 1); };
-            struct Exps {
-                uint32_t e[4];
-            };
-            auto exps_of = [&](int k, int32_t page) {
-                Exps x{};
-                if (E4M3 && page != INT_MIN) {
-                    const uint8_t* e = exps + exp_at(a.c, kv, good(page) ? page : 0, slot_of(k), h);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x.e[i] = e[i * exp_step];
-                }
-                return x;
-            };
-            int32_t cur = entry(0), next = entry(1);
-            Exps xc = exps_of(0, cur), xn = exps_of(1, next);
-            Place<kFill> at = base_at;
-            if (kv) at.advance(ring_v<PAIR>(0, n));
-            for (int k = 0; k < n; ++k) {
-                const int32_t after = entry(k + 2);
-                const bool needed = cur != INT_MIN;
-                // A page out of range: page 0 in its place, and NaN for the item.
-                const bool bad = needed && !good(cur);
-                if (at.round > 0 && !(ok = wait_all(&emptybar[at.stage], at.round - 1))) break;
-                if (bad) {
-                    cur = 0;
-                    *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) = 1;
-                    if (a.status != nullptr) atomicOr(a.status + g->b, kBadPage);
-                }
-                if constexpr (E4M3) {
-                    // Positions that no row sees may hold anything: factor 0, which
-                    // the helpers turn into zeros. So do values that are NaN at
-                    // positions that not every row sees; these are noted.
-                    uint32_t top = 0, f[4], two = 0, hidden = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int p = k * kTile + lane * 4 + i;
-                        if (p < any_lo || p > any_hi) {
-                            hidden |= 1u << i;
-                        } else if (xc.e[i] != 255u) {
-                            top = max(top, xc.e[i]);
-                        } else if (kv == 1 && (p < g->all_lo || p > g->all_hi)) {
-                            hidden |= 1u << i;
-                            const int x = atomicAdd(&ctl.noted[item % kItems], 1);
-                            if (x < kNoted) ctl.note[item % kItems][x] = p;
-                        }
-                    }
-                    top = __reduce_max_sync(0xFFFFFFFFu, top);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (kv == 0) {
-                            f[i] = key_factor(xc.e[i], top);
-                        } else {
-                            const Factor x = factor_of(xc.e[i], T());
-                            f[i] = x.f1;
-                            two |= x.two && !(hidden >> i & 1u);
-                        }
-                        if (hidden >> i & 1u) f[i] = 0;
-                    }
-                    *reinterpret_cast<uint4*>(&ctl.factor[at.stage][lane * 4]) =
-                        make_uint4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<uint32_t*>(&ctl.exps[at.stage][lane * 4]) =
-                        xc.e[0] | xc.e[1] << 8 | xc.e[2] << 16 | xc.e[3] << 24;
-                    const bool any_two = __any_sync(0xFFFFFFFFu, two != 0) != 0;
-                    if (lane == 0) {
-                        ctl.top[at.stage] = top;
-                        ctl.two[at.stage] = any_two;
-                    }
-                    __syncwarp();
-                }
-                const bool leader = needed && first_of_box;
-                const unsigned boxes = __ballot_sync(0xFFFFFFFFu, leader);
-                if (lane == 0)
-                    sv::mbar_arrive_expect_tx(&fullbar[at.stage], __popc(boxes) * box_bytes);
-                __syncwarp();
-                if (leader) {
-                    const int c1 = slot_of(k);
-                    if (E4M3) {
-                        tma_load_4d(sr + at.stage * X::kRawBytes + lane_bytes, map, 0, c1, h, cur,
-                                    &fullbar[at.stage]);
-                    } else if (args.page_heads > 0) {
-                        tma_load_5d(st + at.stage * X::kTileBytes + lane_bytes, map, 0, 0, 0, c1 >> 3,
-                                    cur * args.page_heads + h * args.head_step, &fullbar[at.stage]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < DP / 64; ++q)
-                            tma_load_4d(st + at.stage * X::kTileBytes + q * X::kPanel + lane_bytes,
-                                        map, q * 64, c1, h, cur, &fullbar[at.stage]);
-                    }
-                }
-                __syncwarp();
-                used |= 1u << at.stage;
-                rounds = (rounds & ~(1u << at.stage)) | (at.round & 1u) << at.stage;
-                at.advance(kv ? ring_v_step<PAIR>(k, n) : ring_k_step<PAIR>(k));
-                cur = next;
-                next = after;
-                xc = xn;
-                xn = exps_of(k + 2, next);
-            }
-            base_at.advance(2 * n);
-        }
-        if (kv == 0 && lane == 0) {
-            sh.units = start.U;
-            args.shares[blockIdx.x] = sh;
-        }
-        if (!ok) {
-            // No copy may be under way when the block ends.
-            for (int i = 0; i < kFill; ++i)
-                if (used >> i & 1u) sv::mbar_wait_bounded(&fullbar[i], rounds >> i & 1u, nullptr);
-        }
+        // Copies of keys (warp 9, which also plans the segments) and values (10).
+        feed<T, DP, E4M3, R, PAIR, !PAIR, kFill>(
+            args, ctl, warp == 9 ? &kmap : &vmap, warp - 9, E4M3 ? sr : st,
+            E4M3 ? X::kRawBytes : X::kTileBytes, E4M3 ? ctl.raw_full : ctl.full,
+            E4M3 ? ctl.raw_empty : ctl.empty, start, wait_all);
     } else {
         // ------------------------------------------------------------------
         // Helpers: hidden values, and e4m3.
@@ -1156,7 +623,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         int k_tiles = 0;  // key tiles so far
         bool ok = true;
         for (; ok; ++item) {
-            const Plan* g = plan_at(item);
+            const Plan* g = plan_at(ctl, item, wait_all);
             if (g == nullptr) break;
             const int n = g->n, inner_lo = g->inner_lo, inner_hi = g->inner_hi;
             auto note = [&](int p) {
@@ -1165,7 +632,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             };
             int kk = 0, vv = 0;
             for (int i = 0; ok && i < 2 * n; ++i) {
-                const bool is_v = vv < n && ring_v<PAIR>(vv, n) == i;
+                const bool is_v = vv < n && ring_v<!PAIR>(vv, n) == i;
                 const int k = is_v ? vv++ : kk++;
                 const bool edge = !E4M3 && is_v && (k < inner_lo || k > inner_hi);
                 if constexpr (!E4M3) {
@@ -1281,149 +748,6 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
     }
 }
 
-// Joins the items that several blocks worked on, in block order: block x takes
-// the item that block x of the tile kernel began and did not finish, a warp a
-// row.
-template <class T, int DP>
-__global__ void __launch_bounds__(128) join_kernel(const Tiles args, int blocks)
-{
-    const Attn& a = args.a;
-    const int lane = threadIdx.x & 31;
-    sv::pdl_wait();
-    const Share sh = args.shares[blockIdx.x];
-    const float nan = __uint_as_float(0x7FFFFFFFu);
-    if (sh.failed) {
-        // A wait ran out: no output of this call can be trusted.
-        const int64_t n = static_cast<int64_t>(gridDim.y) * blockDim.x;
-        const int64_t i0 = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-        uint32_t* o = reinterpret_cast<uint32_t*>(a.out);
-        for (int64_t i = i0; i < a.tokens * a.Hq * a.c.D / 2; i += n) o[i] = narrow2(nan, nan, T());
-        if (a.lse != nullptr)
-            for (int64_t i = i0; i < a.tokens * a.Hq; i += n) a.lse[i] = nan;
-        if (a.status != nullptr)
-            for (int64_t i = i0; i < a.c.B; i += n) atomicOr(a.status + i, kTimeout);
-        return;
-    }
-    if (!sh.leads) return;
-    const int r = blockIdx.y * (blockDim.x / 32) + (threadIdx.x >> 5);
-    if (r >= sh.rows) return;
-    constexpr int kPer = DP / 32;
-    float m = __uint_as_float(sv::kF32NegInfBits), l = 0.f, o[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-    for (int c = blockIdx.x; c <= sh.last; ++c) {
-        if (share_begin(sh.units, c, blocks) == share_begin(sh.units, c + 1, blocks)) continue;
-        const float* p = args.part +
-                         ((static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x) ? 1 : 0)) *
-                              args.part_rows + r) * (DP + 4);
-        const float pm = p[DP], pl = p[DP + 1];
-        const float mn = fmaxf(m, pm);
-        const float keep = m == mn ? 1.f : sv::ex2(m - mn);
-        const float w = pm == mn ? 1.f : sv::ex2(pm - mn);
-        l = l * keep + pl * w;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = o[i] * keep + p[lane + 32 * i] * w;
-        m = mn;
-    }
-    const int64_t orow = out_row(a, sh.q0, sh.h, sh.row0 + r);
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int d = lane + 32 * i;
-        if (d < a.c.D)
-            *reinterpret_cast<uint16_t*>(a.out + (orow * a.c.D + d) * 2) =
-                static_cast<uint16_t>(narrow2(o[i] * inv, 0.f, T()));
-    }
-    if (a.lse != nullptr && lane == 0) a.lse[orow] = fmaf(m, kLn2, logf(l));
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled lookup_encode()
-{
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-        return reinterpret_cast<EncodeTiled>(p);
-    return nullptr;
-}
-
-// The driver's tensor-map encoder, looked up once.
-EncodeTiled encode_fn()
-{
-    static const EncodeTiled fn = lookup_encode();
-    return fn;
-}
-
-// Keys (kv = 0) or values (1) as [page][head][slot][element]; a box is the slots
-// of one page in one tile, times 64 16-bit elements with the 128-byte swizzle or
-// a whole row of codes.
-bool make_map(CUtensorMap* map, const Cache& c, int kv, bool f16, bool e4m3)
-{
-    const EncodeTiled fn = encode_fn();
-    if (fn == nullptr) return false;
-    const int P = 1 << c.page_shift;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(P),
-                                static_cast<cuuint64_t>(c.Hkv),
-                                static_cast<cuuint64_t>(c.num_pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.slot_stride[kv]),
-                                   static_cast<cuuint64_t>(c.head_stride[kv]),
-                                   static_cast<cuuint64_t>(c.page_stride[kv])};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(e4m3 ? c.D : 64),
-                               static_cast<cuuint32_t>(P < kTile ? P : kTile), 1, 1};
-    const cuuint32_t unit[4] = {1, 1, 1, 1};
-    return fn(map,
-              e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                   : f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-              4, c.pages[kv], dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
-}
-
-// 16-bit rows of 128 elements, one copy a page for both halves of the rows:
-// [page and head][slot / 8][half][slot % 8][64 elements]. Pages and heads are one
-// axis, in steps of a head (one head: of a page); see heads_to_a_page.
-bool make_map5(CUtensorMap* map, const Cache& c, int kv, bool f16, int64_t page_heads)
-{
-    const EncodeTiled fn = encode_fn();
-    if (fn == nullptr) return false;
-    const int P = 1 << c.page_shift;
-    const int64_t step = c.Hkv > 1 ? c.head_stride[kv] : c.page_stride[kv];
-    const cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(P / 8),
-                                static_cast<cuuint64_t>((c.num_pages - 1) * page_heads + c.Hkv)};
-    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(c.slot_stride[kv]), 128,
-                                   static_cast<cuuint64_t>(c.slot_stride[kv]) * 8,
-                                   static_cast<cuuint64_t>(step)};
-    const cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>((P < kTile ? P : kTile) / 8), 1};
-    const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
-    return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
-              c.pages[kv], dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// How far apart pages are on make_map5's axis of pages and heads; 0 where it
-// cannot be used: the page stride has to be a multiple of the head stride, the
-// same in keys and values.
-int64_t heads_to_a_page(const Cache& c, bool e4m3)
-{
-    if (e4m3 || c.D != 128) return 0;
-    int64_t n = 1;
-    if (c.Hkv > 1) {
-        if (c.head_stride[0] <= 0 || c.page_stride[0] % c.head_stride[0] != 0) return 0;
-        n = c.page_stride[0] / c.head_stride[0];
-        if (n <= 0 || c.head_stride[1] <= 0 || c.page_stride[1] != n * c.head_stride[1]) return 0;
-    }
-    // (coordinates are 32 bits)
-    return n < (int64_t(1) << 31) / c.num_pages - c.Hkv ? n : 0;
-}
-
 template <class T, int DP, bool E4M3, bool PAIR>
 cudaError_t launch_shape(const CUtensorMap& k, const CUtensorMap& v, const Tiles& t, int blocks,
                          int64_t rows, cudaStream_t s)
@@ -1448,16 +772,7 @@ cudaError_t launch_shape(const CUtensorMap& k, const CUtensorMap& v, const Tiles
     }
     f<<<blocks, X::kThreads, smem, s>>>(k, v, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks, static_cast<unsigned>((rows + 3) / 4));
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<T, DP>, t, blocks);
+    return launch_join<T, DP>(t, blocks, rows, s);
 }
 
 template <class T, int DP>
@@ -1474,8 +789,6 @@ cudaError_t launch_type(const CUtensorMap& k, const CUtensorMap& v, const Tiles&
 // Rows of the largest item.
 int64_t item_rows(int64_t max_chunk, int64_t G) { return max_chunk * G < 256 ? max_chunk * G : 256; }
 
-constexpr size_t kShareBytes = (sizeof(Share) * kMaxBlocks + 255) / 256 * 256;
-
 }  // namespace
 
 size_t tiles_workspace(int64_t max_chunk, int64_t G, int64_t D)
@@ -1489,22 +802,11 @@ cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* wor
                                    cudaStream_t s, bool* mapped)
 {
     CUtensorMap k, v;
-    const int64_t page_heads = heads_to_a_page(a.c, e4m3);
-    const bool five = page_heads > 0 && make_map5(&k, a.c, 0, f16, page_heads) &&
-                      make_map5(&v, a.c, 1, f16, page_heads);
-    *mapped = five || (make_map(&k, a.c, 0, f16, e4m3) && make_map(&v, a.c, 1, f16, e4m3));
-    if (!*mapped) return cudaSuccess;
-    int dev = 0, sms = 0;
-    cudaError_t e;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-        return e;
-    const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
+    Tiles t;
+    int blocks = 0;
     const int64_t rows = item_rows(a.max_chunk, a.G);
-    Tiles t{a, reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kShareBytes),
-            static_cast<Share*>(workspace), static_cast<int32_t>(rows),
-            five ? 2048 : 1024, five ? 1024 : kTile * 128,
-            five ? static_cast<int32_t>(page_heads) : 0, a.c.Hkv > 1 ? 1 : 0};
+    cudaError_t e = set_up(a, f16, e4m3, rows, workspace, false, &k, &v, &t, &blocks, mapped);
+    if (e != cudaSuccess || !*mapped) return e;
     const bool pair = rows > 128;
     if (a.c.D <= 64)
         return f16 ? launch_type<F16, 64>(k, v, t, blocks, rows, e4m3, pair, s)
