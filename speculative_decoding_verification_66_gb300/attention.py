@@ -21,6 +21,7 @@ from __future__ import annotations
 import ctypes
 import struct
 from contextlib import ExitStack
+from functools import lru_cache
 
 import torch
 
@@ -105,18 +106,21 @@ def _status(seq_status, B, dev):
     return seq_status.data_ptr()
 
 
-def _enter(stack, dev, stream, *tensors):
-    """Make dev and stream current, so that what is allocated below belongs to the stream the
-    kernels run on, and tell the allocator of the tensors used on a stream not their own."""
-    if torch.cuda.current_device() != dev.index:
-        stack.enter_context(torch.cuda.device(dev))
-    if stream is not None and stream != torch.cuda.current_stream(dev):
-        stack.enter_context(torch.cuda.stream(stream))
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-    # (the handle of the current stream, without building a Stream object)
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+def _on(dev, stream, call, tensors):
+    """call(raw stream) with dev and stream current, so that what it allocates belongs to the
+    stream the kernels run on. The allocator is told of tensors used on a stream not their own."""
+    if torch.cuda.current_device() == dev.index and stream is None:
+        # (the handle of the current stream, without building a Stream object)
+        return call(torch._C._cuda_getCurrentRawStream(dev.index))
+    with ExitStack() as stack:
+        if torch.cuda.current_device() != dev.index:
+            stack.enter_context(torch.cuda.device(dev))
+        if stream is not None and stream != torch.cuda.current_stream(dev):
+            stack.enter_context(torch.cuda.stream(stream))
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        return call(torch._C._cuda_getCurrentRawStream(dev.index))
 
 
 def sv_kv_append(key, value, k_pages, v_pages, page_table, cached_lens, chunk_starts, *,
@@ -133,12 +137,14 @@ def sv_kv_append(key, value, k_pages, v_pages, page_table, cached_lens, chunk_st
              "value must have key's shape and dtype")
     status = _status(seq_status, cached_lens.numel(), dev)
     ks, vs = key.stride(), value.stride()
-    with ExitStack() as stack:
-        s = _enter(stack, dev, stream, key, value, k_pages, v_pages, page_table, cached_lens,
-                   chunk_starts, k_exps, v_exps, seq_status)
+
+    def call(s):
         _check(_lib.load_attention().sv_kv_append(
             cache, key.data_ptr(), value.data_ptr(), dtype, key.shape[0], ks[0], ks[1], vs[0],
             vs[1], status, s), "sv_kv_append")
+
+    _on(dev, stream, call, (key, value, k_pages, v_pages, page_table, cached_lens, chunk_starts,
+                            k_exps, v_exps, seq_status))
 
 
 def sv_kv_read(k_pages, v_pages, page_table, cached_lens, chunk_starts, tokens: int, *,
@@ -155,23 +161,26 @@ def sv_kv_read(k_pages, v_pages, page_table, cached_lens, chunk_starts, tokens: 
         dtype = key.dtype if key is not None else \
             torch.bfloat16 if code == SV_E4M3 else k_pages.dtype
     status = _status(seq_status, cached_lens.numel(), dev)
-    with ExitStack() as stack:
-        s = _enter(stack, dev, stream, key, value, k_pages, v_pages, page_table, cached_lens,
-                   chunk_starts, k_exps, v_exps, seq_status)
-        _require(tokens >= 0, "tokens must not be negative")
-        if key is None:
-            key = torch.empty((tokens, H, D), dtype=dtype, device=dev)
-        if value is None:
-            value = torch.empty((tokens, H, D), dtype=dtype, device=dev)
+    _require(tokens >= 0, "tokens must not be negative")
+
+    def call(s):
+        out = []
         for name, x in (("key", key), ("value", value)):
+            if x is None:
+                x = torch.empty((tokens, H, D), dtype=dtype, device=dev)
             d = _rows(x, name, H, D, dev, code)
             _require(x.shape[0] == tokens and x.dtype == dtype and x.is_contiguous(),
                      f"{name} must be contiguous [tokens, kv_heads, head_dim] of dtype")
-        _check(_lib.load_attention().sv_kv_read(cache, key.data_ptr(), value.data_ptr(), d, tokens,
-                                                status, s), "sv_kv_read")
-    return key, value
+            out.append(x)
+        _check(_lib.load_attention().sv_kv_read(cache, out[0].data_ptr(), out[1].data_ptr(), d,
+                                                tokens, status, s), "sv_kv_read")
+        return tuple(out)
+
+    return _on(dev, stream, call, (key, value, k_pages, v_pages, page_table, cached_lens,
+                                   chunk_starts, k_exps, v_exps, seq_status))
 
 
+@lru_cache(maxsize=256)
 def sv_chunk_attention_workspace_bytes(B: int, tokens: int, q_heads: int, kv_heads: int,
                                        head_dim: int, max_chunk: int = 0) -> int:
     n = ctypes.c_size_t(0)
@@ -202,31 +211,30 @@ def sv_chunk_attention(query, k_pages, v_pages, page_table, cached_lens, chunk_s
     status = _status(seq_status, B, dev)
     if scale is None:
         scale = D ** -0.5
-    with ExitStack() as stack:
-        s = _enter(stack, dev, stream, query, k_pages, v_pages, page_table, cached_lens,
-                   chunk_starts, k_exps, v_exps, out, lse, seq_status, workspace)
-        if out is None:
-            out = torch.empty((N, Hq, D), dtype=query.dtype, device=dev)
-        else:
-            _require(out.shape == query.shape and out.dtype == query.dtype and
-                     out.device == dev and out.is_contiguous(),
-                     "out must be contiguous, of query's shape, dtype and device")
-        if lse is not None:
-            _require(lse.shape == (N, Hq) and lse.dtype == torch.float32 and lse.device == dev
-                     and lse.is_contiguous(), "lse must be contiguous float32 [tokens, q_heads]")
-        elif return_lse:
-            lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
-        if workspace is None:
-            # A new one every call, from the allocator's pool of this stream (or of the graph
-            # being captured): nothing that an earlier call or a replay still uses is touched.
-            workspace = torch.empty(sv_chunk_attention_workspace_bytes(B, N, Hq, H, D, max_chunk),
-                                    dtype=torch.uint8, device=dev)
-        else:
-            _require(workspace.device == dev and workspace.dtype == torch.uint8 and
-                     workspace.is_contiguous(), "workspace must be contiguous uint8 on the device")
-        qs = query.stride()
+    if out is not None:
+        _require(out.shape == query.shape and out.dtype == query.dtype and out.device == dev and
+                 out.is_contiguous(), "out must be contiguous, of query's shape, dtype and device")
+    if lse is not None:
+        _require(lse.shape == (N, Hq) and lse.dtype == torch.float32 and lse.device == dev
+                 and lse.is_contiguous(), "lse must be contiguous float32 [tokens, q_heads]")
+    if workspace is not None:
+        _require(workspace.device == dev and workspace.dtype == torch.uint8 and
+                 workspace.is_contiguous(), "workspace must be contiguous uint8 on the device")
+    qs = query.stride()
+
+    def call(s):
+        o = torch.empty((N, Hq, D), dtype=query.dtype, device=dev) if out is None else out
+        z = torch.empty((N, Hq), dtype=torch.float32, device=dev) if lse is None and return_lse \
+            else lse
+        # A new workspace every call, from the allocator's pool of this stream (or of the graph
+        # being captured): nothing that an earlier call or a replay still uses is touched.
+        w = torch.empty(sv_chunk_attention_workspace_bytes(B, N, Hq, H, D, max_chunk),
+                        dtype=torch.uint8, device=dev) if workspace is None else workspace
         _check(_lib.load_attention().sv_chunk_attention(
             cache, query.data_ptr(), dtype, N, Hq, qs[0], qs[1], scale, window, max_chunk,
-            out.data_ptr(), None if lse is None else lse.data_ptr(), status,
-            workspace.data_ptr(), workspace.numel(), s), "sv_chunk_attention")
-    return out if lse is None else (out, lse)
+            o.data_ptr(), None if z is None else z.data_ptr(), status, w.data_ptr(), w.numel(), s),
+            "sv_chunk_attention")
+        return o if z is None else (o, z)
+
+    return _on(dev, stream, call, (query, k_pages, v_pages, page_table, cached_lens, chunk_starts,
+                                   k_exps, v_exps, out, lse, seq_status, workspace))

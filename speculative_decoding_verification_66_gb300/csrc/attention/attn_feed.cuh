@@ -387,9 +387,11 @@ __device__ __forceinline__ const Plan* plan_at(Ctl& ctl, int i, Wait& wait_all)
 }
 
 // Copies of keys (kv = 0) or values (1), by a warp; the keys' warp also plans the
-// segments. The page of tile k + 3 and the exponents of tile k + 2 are on their
+// segments. e4m3: the factors that the codes are multiplied by (FEW: of keys, the
+// powers of two themselves; of values, as halves). The page of tile k + 3 and the exponents of tile k + 2 are on their
 // way while tile k is issued.
-template <class T, int DP, bool E4M3, int R, bool SPLIT, bool ALT, int FILL, class Ctl, class Wait>
+template <class T, int DP, bool E4M3, int R, bool SPLIT, bool ALT, int FILL, bool FEW, class Ctl,
+          class Wait>
 __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensorMap* map, int kv,
                                      uint32_t stages, uint32_t stage_bytes, uint64_t* fullbar,
                                      uint64_t* emptybar, const Start& start, Wait& wait_all)
@@ -506,29 +508,36 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                         if (x < kNoted) ctl.note[item % kItems][x] = p;
                     }
                 }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                if (!FEW && kv == 0) top = __reduce_max_sync(0xFFFFFFFFu, top);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (kv == 0) {
-                        f[i] = key_factor(xc.e[i], top);
-                    } else {
-                        const Factor x = factor_of(xc.e[i], T());
-                        f[i] = x.f1;
-                        two |= x.two && !(hidden >> i & 1u);
-                    }
-                    if (hidden >> i & 1u) f[i] = 0;
+            for (int i = 0; i < 4; ++i) {
+                if (kv == 0) {
+                    f[i] = FEW ? __float_as_uint(exp_value(xc.e[i])) : key_factor(xc.e[i], top);
+                } else {
+                    const Factor x = factor_of(xc.e[i], T());
+                    f[i] = x.f1;
+                    two |= x.two && !(hidden >> i & 1u);
                 }
+                if (hidden >> i & 1u) f[i] = 0;
+            }
+            const bool any_two = __any_sync(0xFFFFFFFFu, two != 0) != 0;
+            *reinterpret_cast<uint32_t*>(&ctl.exps[at.stage][lane * 4]) =
+                xc.e[0] | xc.e[1] << 8 | xc.e[2] << 16 | xc.e[3] << 24;
+            if constexpr (FEW) {
+                if (kv == 0)
+                    *reinterpret_cast<uint4*>(&ctl.scale[at.stage][lane * 4]) =
+                        make_uint4(f[0], f[1], f[2], f[3]);
+                else
+                    *reinterpret_cast<uint2*>(&ctl.scale[at.stage][lane * 2]) = make_uint2(
+                        (f[0] & 0xFFFFu) | f[1] << 16, (f[2] & 0xFFFFu) | f[3] << 16);
+            } else {
                 *reinterpret_cast<uint4*>(&ctl.factor[at.stage][lane * 4]) =
                     make_uint4(f[0], f[1], f[2], f[3]);
-                *reinterpret_cast<uint32_t*>(&ctl.exps[at.stage][lane * 4]) =
-                    xc.e[0] | xc.e[1] << 8 | xc.e[2] << 16 | xc.e[3] << 24;
-                const bool any_two = __any_sync(0xFFFFFFFFu, two != 0) != 0;
-                if (lane == 0) {
-                    ctl.top[at.stage] = top;
-                    ctl.two[at.stage] = any_two;
-                }
-                __syncwarp();
+                if (lane == 0) ctl.top[at.stage] = top;
             }
+            if (lane == 0) ctl.two[at.stage] = any_two;
+            __syncwarp();
+        }
             const bool leader = needed && first_of_box;
             const unsigned boxes = __ballot_sync(0xFFFFFFFFu, leader);
             if (lane == 0)
@@ -598,22 +607,40 @@ __global__ void __launch_bounds__(128) join_kernel(const Tiles args, int blocks)
     const int r = blockIdx.y * (blockDim.x / 32) + (threadIdx.x >> 5);
     if (r >= sh.rows) return;
     constexpr int kPer = DP / 32;
-    float m = __uint_as_float(sv::kF32NegInfBits), l = 0.f, o[kPer];
+    const float ninf = __uint_as_float(sv::kF32NegInfBits);
+    // Shares first .. sh.last, of which some may be empty (fewer units than
+    // blocks): 32 at a time, the maxima and sums by a lane each, then the columns.
+    float m = ninf, l = 0.f, o[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-    for (int c = blockIdx.x; c <= sh.last; ++c) {
-        if (share_begin(sh.units, c, blocks) == share_begin(sh.units, c + 1, blocks)) continue;
-        const float* p = args.part +
-                         ((static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x) ? 1 : 0)) *
-                              args.part_rows + r) * (DP + 4);
-        const float pm = p[DP], pl = p[DP + 1];
-        const float mn = fmaxf(m, pm);
-        const float keep = m == mn ? 1.f : sv::ex2(m - mn);
-        const float w = pm == mn ? 1.f : sv::ex2(pm - mn);
-        l = l * keep + pl * w;
+    const int first = blockIdx.x;
+    for (int c0 = first; c0 <= sh.last; c0 += 32) {
+        const int c = c0 + lane;
+        const int64_t at = ((static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * args.part_rows + r) *
+                           (DP + 4);
+        const bool has = c <= sh.last &&
+                         share_begin(sh.units, c, blocks) < share_begin(sh.units, c + 1, blocks);
+        const float pm = has ? args.part[at + DP] : ninf, pl = has ? args.part[at + DP + 1] : 0.f;
+        float top = fmaxf(m, pm);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = o[i] * keep + p[lane + 32 * i] * w;
-        m = mn;
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const float keep = m == top ? 1.f : sv::ex2(m - top);
+        const float w = !has ? 0.f : pm == top ? 1.f : sv::ex2(pm - top);
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] *= keep;
+        unsigned left = __ballot_sync(0xFFFFFFFFu, has);
+#pragma unroll 4
+        while (left != 0) {
+            const int x = __ffs(static_cast<int>(left)) - 1;
+            left &= left - 1;
+            const float wx = __shfl_sync(0xFFFFFFFFu, w, x);
+            const float* from = args.part + __shfl_sync(0xFFFFFFFFu, at, x);
+            l = fmaf(__shfl_sync(0xFFFFFFFFu, pl, x), wx, l);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) o[i] = fmaf(from[lane + 32 * i], wx, o[i]);
+        }
+        m = top;
     }
     const int64_t orow = out_row(a, sh.q0, sh.h, sh.row0 + r);
     const float inv = 1.f / l;

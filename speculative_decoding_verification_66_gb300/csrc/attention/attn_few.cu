@@ -1,4 +1,4 @@
-// attn_few.cu -- attention over the paged cache for items of up to 32 rows (a
+// attn_few.cu -- attention over the paged cache for items of up to 16 rows (a
 // single token, a short draft), head sizes up to 128.
 //
 // Such items are bound by the reads of the cache: 2 D (1 + rows) operations meet
@@ -29,8 +29,9 @@ namespace {
 
 constexpr int kWorkers = 8;
 constexpr int kFewThreads = (kWorkers + 2) * 32;
+constexpr int MT = 1;  // blocks of 16 rows
 
-template <int DP, bool E4M3, int MT>
+template <int DP, bool E4M3>
 struct FewShape {
     static constexpr int kRows = 16 * MT;
     static constexpr int kTileBytes = kTile * DP * (E4M3 ? 1 : 2);
@@ -39,12 +40,12 @@ struct FewShape {
     static constexpr int kStages = 196608 / kTileBytes < kMost ? 196608 / kTileBytes : kMost;
     static constexpr int kSteps = DP / 16;                  // products along d
     static constexpr int kQBytes = MT * kSteps * 32 * 16;   // operands as the lanes hold them
-    static constexpr int kJoin = MT == 1 ? 32 : 16;         // columns joined at a time
+    static constexpr int kJoin = 32;                        // columns joined at a time
     static constexpr int kJoinBytes = kWorkers * kRows * kJoin * 4;
     static constexpr int kBytes = kStages * kTileBytes + kQBytes + kJoinBytes;
 };
 
-template <int STAGES, bool E4M3, int MT>
+template <int STAGES, bool E4M3>
 struct FewControl {
     uint64_t full[STAGES], empty[STAGES], sync;
     uint64_t plan_ready[kItems];
@@ -57,8 +58,10 @@ struct FewControl {
     int bad_page[kItems];
     float2 ml[kWorkers][16 * MT];
     float q_scale[16 * MT];
-    alignas(16) uint32_t factor[E4M3 ? STAGES : 1][E4M3 ? kTile : 4];
-    uint32_t top[E4M3 ? STAGES : 1], two[E4M3 ? STAGES : 1];
+    // e4m3, for every stage: the keys' powers of two, or (values) the rows' factors
+    // as halves, whether some row needs two, and the exponents.
+    alignas(16) float scale[E4M3 ? STAGES : 1][E4M3 ? kTile : 4];
+    uint32_t two[E4M3 ? STAGES : 1];
     uint8_t exps[E4M3 ? STAGES : 1][E4M3 ? kTile : 4];
 };
 
@@ -101,18 +104,18 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr)
     return v;
 }
 
-template <class T, int DP, bool E4M3, int MT>
+template <class T, int DP, bool E4M3>
 __global__ void __launch_bounds__(kFewThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                const __grid_constant__ Tiles args)
 {
-    using X = FewShape<DP, E4M3, MT>;
+    using X = FewShape<DP, E4M3>;
     constexpr int S = X::kStages, R = X::kRows;
     // Type of the first product's operands.
     using TS = typename std::conditional<E4M3, F16, T>::type;
     const Attn& a = args.a;
     extern __shared__ __align__(1024) uint8_t smem[];
-    FewControl<S, E4M3, MT>& ctl = *reinterpret_cast<FewControl<S, E4M3, MT>*>(smem + X::kBytes);
+    FewControl<S, E4M3>& ctl = *reinterpret_cast<FewControl<S, E4M3>*>(smem + X::kBytes);
     const uint32_t st = sv::smem_addr(smem), sq = st + S * X::kTileBytes;
     float* join = reinterpret_cast<float*>(smem + S * X::kTileBytes + X::kQBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0;
     };
     if (warp >= kWorkers) {
-        feed<T, DP, E4M3, R, false, false, S>(args, ctl, warp == kWorkers ? &kmap : &vmap,
+        feed<T, DP, E4M3, R, false, false, S, true>(args, ctl, warp == kWorkers ? &kmap : &vmap,
                                               warp - kWorkers, st, X::kTileBytes, ctl.full, ctl.empty,
                                               start, wait_all);
     } else {
@@ -156,75 +159,80 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (lane == 0) sv::mbar_arrive(&ctl.sync);
             return wait_all(&ctl.sync, syncs++);
         };
-        Place<S> at;
-        bool ok = true;
-        for (int item = 0; ok; ++item) {
-            const Plan* plan = plan_at(ctl, item, wait_all);
-            if (plan == nullptr) break;
-            const Plan& p = *plan;
-            const int n = p.n, rows = p.rows;
-            auto row_ptr = [&](int r) {
-                const int rr = p.row0 + r, t = rr / a.G;
-                return a.q + (static_cast<int64_t>(p.q0) + t) * a.q_token +
-                       static_cast<int64_t>(p.h * a.G + (rr - t * a.G)) * a.q_head;
-            };
-            // The queries' operands, as the lanes will hold them: step w by warp w.
-            // (Every warp has done with those of the segment before: it came to
-            // that segment's last meeting.)
-            if constexpr (E4M3 && std::is_same<T, Bf16>::value) {
+        auto row_ptr = [&](const Plan& p, int r) {
+            const int rr = p.row0 + r, t = rr / a.G;
+            return a.q + (static_cast<int64_t>(p.q0) + t) * a.q_token +
+                   static_cast<int64_t>(p.h * a.G + (rr - t * a.G)) * a.q_head;
+        };
+        // The queries' operands, as the lanes will hold them: step w by warp w.
+        // Fetched into registers while a segment's results are joined, stored after.
+        constexpr bool kScaled = E4M3 && std::is_same<T, Bf16>::value;
+        static_assert(X::kSteps <= kWorkers && MT == 1, "a step a warp");
+        uint2 qv[2];       // rows g, g + 8
+        uint2 qrow[2];     // kScaled: elements 4 lane .. of rows warp, warp + 8
+        auto fetch = [&](const Plan& p) {
+            if (kScaled) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = warp + 8 * i;
+                    qrow[i] = make_uint2(0, 0);
+                    if (r < p.rows && lane * 4 < a.c.D)
+                        qrow[i] = *reinterpret_cast<const uint2*>(row_ptr(p, r) + lane * 8);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = g + 8 * i;
+                qv[i] = make_uint2(0, 0);
+                if (warp >= X::kSteps || r >= p.rows) continue;
+                const uint8_t* q = row_ptr(p, r);
+                if constexpr (E4M3) {
+                    // d = 16 (2 c + h) + 4 s (DP = 64: 16 c + 4 s)
+                    const int d = (DP == 128 ? 16 * (2 * c4 + (warp >> 2)) : 16 * c4) + 4 * (warp & 3);
+                    if (d < a.c.D) qv[i] = *reinterpret_cast<const uint2*>(q + d * 2);
+                } else if (16 * warp < a.c.D) {
+                    const int d = 16 * warp + 2 * c4;
+                    qv[i].x = *reinterpret_cast<const uint32_t*>(q + d * 2);
+                    qv[i].y = *reinterpret_cast<const uint32_t*>(q + d * 2 + 16);
+                }
+            }
+        };
+        auto store = [&]() {
+            if (kScaled) {
                 // To float16: powers of two that bring a row's largest element to
                 // [2^14, 2^15).
-                for (int r = warp; r < R; r += kWorkers) {
-                    uint32_t top = 0;
-                    if (r < rows && lane * 4 < a.c.D) {
-                        const uint2 u = *reinterpret_cast<const uint2*>(row_ptr(r) + lane * 8);
-                        top = max(max(u.x << 16 & 0x7FFF0000u, u.x & 0x7FFF0000u),
-                                  max(u.y << 16 & 0x7FFF0000u, u.y & 0x7FFF0000u));
-                    }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint2 u = qrow[i];
+                    uint32_t top = max(max(u.x << 16 & 0x7FFF0000u, u.x & 0x7FFF0000u),
+                                       max(u.y << 16 & 0x7FFF0000u, u.y & 0x7FFF0000u));
                     top = __reduce_max_sync(0xFFFFFFFFu, top);
                     if (lane == 0)
-                        ctl.q_scale[r] =
-                            __uint_as_float(static_cast<uint32_t>(max(static_cast<int>(top >> 23), 15) - 14)
-                                            << 23);
+                        ctl.q_scale[warp + 8 * i] = __uint_as_float(
+                            static_cast<uint32_t>(max(static_cast<int>(top >> 23), 15) - 14) << 23);
                 }
-                if (!(ok = meet())) break;
-            }
-            for (int step = warp; step < X::kSteps; step += kWorkers) {
+                if (!meet()) return false;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    uint32_t f[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int r = mt * 16 + half * 8 + g;
-                        if (r >= rows) continue;
-                        const uint8_t* q = row_ptr(r);
-                        uint2 u = make_uint2(0, 0);
-                        if constexpr (E4M3) {
-                            // d = 16 (2 c + h) + 4 s (DP = 64: 16 c + 4 s)
-                            const int d = (DP == 128 ? 16 * (2 * c4 + (step >> 2)) : 16 * c4) +
-                                          4 * (step & 3);
-                            if (d < a.c.D) u = *reinterpret_cast<const uint2*>(q + d * 2);
-                            if constexpr (std::is_same<T, Bf16>::value) {
-                                const uint32_t e = __float_as_uint(ctl.q_scale[r]) >> 23;
-                                const float up = __uint_as_float((254u - e) << 23);
-                                u.x = narrow2(sv::bf16_lo(u.x) * up, sv::bf16_hi(u.x) * up, F16());
-                                u.y = narrow2(sv::bf16_lo(u.y) * up, sv::bf16_hi(u.y) * up, F16());
-                            }
-                        } else {
-                            const int d = 16 * step + 2 * c4;
-                            if (16 * step < a.c.D) {
-                                u.x = *reinterpret_cast<const uint32_t*>(q + d * 2);
-                                u.y = *reinterpret_cast<const uint32_t*>(q + d * 2 + 16);
-                            }
-                        }
-                        f[half] = u.x;
-                        f[2 + half] = u.y;
-                    }
-                    st_shared_v4(sq + ((mt * X::kSteps + step) * 32 + lane) * 16,
-                                 make_uint4(f[0], f[1], f[2], f[3]));
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t e = __float_as_uint(ctl.q_scale[g + 8 * i]) >> 23;
+                    const float up = __uint_as_float((254u - e) << 23);
+                    qv[i].x = narrow2(sv::bf16_lo(qv[i].x) * up, sv::bf16_hi(qv[i].x) * up, F16());
+                    qv[i].y = narrow2(sv::bf16_lo(qv[i].y) * up, sv::bf16_hi(qv[i].y) * up, F16());
                 }
             }
-            if (!(ok = meet())) break;
+            if (warp < X::kSteps)
+                st_shared_v4(sq + (warp * 32 + lane) * 16,
+                             make_uint4(qv[0].x, qv[1].x, qv[0].y, qv[1].y));
+            return meet();
+        };
+        Place<S> at;
+        const Plan* plan = plan_at(ctl, 0, wait_all);
+        if (plan != nullptr) fetch(*plan);
+        bool ok = true;
+        for (int item = 0; plan != nullptr; ++item) {
+            const Plan& p = *plan;
+            const int n = p.n, rows = p.rows;
+            if (!(ok = store())) break;
 
             // This thread's rows: g + 8 i.
             int pos[2 * MT], low[2 * MT];
@@ -291,15 +299,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     // The keys' powers of two.
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const uint32_t e =
-                            *reinterpret_cast<const uint16_t*>(&ctl.exps[at.stage][key0 + 8 * t + 2 * c4]);
-                        const float e0 = exp_value(e & 255u), e1 = exp_value(e >> 8);
+                        const float2 e = *reinterpret_cast<const float2*>(
+                            &ctl.scale[at.stage][key0 + 8 * t + 2 * c4]);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
-                            s[mt][t][0] *= e0;
-                            s[mt][t][1] *= e1;
-                            s[mt][t][2] *= e0;
-                            s[mt][t][3] *= e1;
+                            s[mt][t][0] *= e.x;
+                            s[mt][t][1] *= e.y;
+                            s[mt][t][2] *= e.x;
+                            s[mt][t][3] *= e.y;
                         }
                     }
                 } else {
@@ -375,11 +382,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 if constexpr (E4M3) {
                     // Keys 2 c, 2 c + 1 and those eight further, as two pairs.
                     constexpr int kWords = DP / 32;  // of four codes of a key to a lane
-                    uint32_t f[4], codes[4][kWords];
+                    uint32_t codes[4][kWords];
+                    const uint16_t* factor =
+                        reinterpret_cast<const uint16_t*>(&ctl.scale[at.stage][0]) + key0 + 2 * c4;
+                    const uint32_t f01 = *reinterpret_cast<const uint32_t*>(factor);
+                    const uint32_t f23 = *reinterpret_cast<const uint32_t*>(factor + 8);
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
                         const int row = key0 + 2 * c4 + (z & 1) + 8 * (z >> 1);
-                        f[z] = ctl.factor[at.stage][row] & 0xFFFFu;
                         const uint32_t from = vt + row * a.c.D;
                         if constexpr (DP == 128) {
                             uint4 x = make_uint4(0, 0, 0, 0);
@@ -391,12 +401,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                                 x = ld_shared_v2(from + few_swizzle<DP>(row, g >> 1, args.swizzled) * 16 + (g & 1) * 8);
                             codes[z][0] = x.x, codes[z][1] = x.y;
                         }
-                        if (edge && f[z] == 0u) {  // hidden: whatever the codes are
+                        // (a factor of zero: hidden, whatever the codes are)
+                        if (edge && (((z >> 1 ? f23 : f01) >> (16 * (z & 1))) & 0xFFFFu) == 0u) {
 #pragma unroll
                             for (int i = 0; i < kWords; ++i) codes[z][i] = 0;
                         }
                     }
-                    const uint32_t f01 = f[0] | f[1] << 16, f23 = f[2] | f[3] << 16;
                     uint32_t f01b = 0, f23b = 0;
                     const bool two = ctl.two[at.stage] != 0;
                     if (two) {
@@ -470,19 +480,22 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (!ok) break;
 
             // ---- the warps' results joined
+            plan = plan_at(ctl, item + 1, wait_all);
+            if (plan != nullptr) fetch(*plan);
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
                 if (c4 == 0) ctl.ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
             }
-            if (!(ok = meet())) break;
-            const int noted = *reinterpret_cast<volatile int*>(&ctl.noted[item % kItems]);
-            const bool bad = *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0;
             const bool whole = p.whole != 0;
             const float nan = __uint_as_float(0x7FFFFFFFu);
             float* share = args.part + (static_cast<int64_t>(blockIdx.x) * 2 + (p.begins ? 1 : 0)) *
                                            args.part_rows * (DP + 4);
+            // Every warp's rows, `width` columns of them from step j0 on, lie in
+            // shared memory: added up, weighted, and written.
+            int noted = 0;
+            bool bad = false;
             // A row that sees a noted position is computed again below.
             auto again = [&](int r) {
                 if (noted == 0 || bad) return false;
@@ -495,81 +508,71 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
                 return x;
             };
-            auto row_max = [&](int r) {
-                float x = ninf;
-#pragma unroll
-                for (int w = 0; w < kWorkers; ++w) x = fmaxf(x, ctl.ml[w][r].x);
-                return x;
-            };
-            float weight[2 * MT];
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
-                const float top = row_max(g + 8 * i);
-                weight[i] = m[i] == top ? 1.f : sv::ex2(m[i] - top);
-            }
-            // kJoin columns at a time: every warp's, weighted, into shared memory;
-            // then all threads add up eight and write.
-            constexpr int kStepsJ = X::kJoin / 8;
-#pragma unroll
-            for (int j0 = 0; j0 < DP / 8; j0 += kStepsJ) {
-                if (j0 > 0 && !(ok = meet())) break;
-#pragma unroll
-                for (int i = 0; i < 2 * MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < kStepsJ; ++j)
-                        *reinterpret_cast<float2*>(
-                            join + (warp * R + g + 8 * i) * X::kJoin + j * 8 + 2 * c4) =
-                            make_float2(o[i >> 1][j0 + j][2 * (i & 1)] * weight[i],
-                                        o[i >> 1][j0 + j][2 * (i & 1) + 1] * weight[i]);
-                if (!(ok = meet())) break;
-                for (int x = threadIdx.x; x < R * X::kJoin; x += kWorkers * 32) {
-                    const int r = x / X::kJoin, y = x % X::kJoin;
-                    if (r >= rows || again(r)) continue;
+            auto add_up = [&](int j0, int width) {
+                noted = *reinterpret_cast<volatile int*>(&ctl.noted[item % kItems]);
+                bad = *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0;
+                const int steps = width >> 3;
+                for (int x = threadIdx.x; x < rows * width; x += kWorkers * 32) {
+                    const int r = x / width, y = x - r * width;
+                    if (again(r)) continue;
                     // e4m3: column n of step j is d = DP / 8 n + j
-                    const int j = E4M3 ? y % kStepsJ : y >> 3, col = E4M3 ? y / kStepsJ : y & 7;
-                    const int d = E4M3 ? DP / 8 * col + j0 + j : 8 * (j0 + j) + col;
-                    float sum = 0.f;
+                    const int col = E4M3 ? y / steps : y & 7;
+                    const int j = E4M3 ? y - col * steps : y >> 3;
+                    const int d = E4M3 ? DP / 8 * col + j0 + j : 8 * j0 + y;
+                    float top = ninf;
 #pragma unroll
-                    for (int w = 0; w < kWorkers; ++w)
-                        sum += join[(w * R + r) * X::kJoin + j * 8 + col];
-                    if (!whole) {
-                        share[static_cast<int64_t>(r) * (DP + 4) + d] = sum;
-                        continue;
-                    }
-                    if (d >= a.c.D) continue;
-                    const float top = row_max(r);
-                    float total = 0.f;
+                    for (int w = 0; w < kWorkers; ++w) top = fmaxf(top, ctl.ml[w][r].x);
+                    float sum = 0.f, total = 0.f;
 #pragma unroll
                     for (int w = 0; w < kWorkers; ++w) {
                         const float2 z = ctl.ml[w][r];
-                        total += z.y * (z.x == top ? 1.f : sv::ex2(z.x - top));
+                        const float weight = z.x == top ? 1.f : sv::ex2(z.x - top);
+                        total = fmaf(z.y, weight, total);
+                        sum = fmaf(join[(w * rows + r) * width + j * 8 + col], weight, sum);
                     }
                     const int rr = p.row0 + r, t = rr / a.G;
                     const int64_t orow = (static_cast<int64_t>(p.q0) + t) * a.Hq + p.h * a.G +
                                          (rr - t * a.G);
-                    *reinterpret_cast<uint16_t*>(a.out + (orow * a.c.D + d) * 2) =
-                        static_cast<uint16_t>(narrow2(bad ? nan : sum / total, 0.f, T()));
+                    float* part = share + static_cast<int64_t>(r) * (DP + 4);
+                    if (whole) {
+                        if (d < a.c.D)
+                            *reinterpret_cast<uint16_t*>(a.out + (orow * a.c.D + d) * 2) =
+                                static_cast<uint16_t>(narrow2(bad ? nan : sum / total, 0.f, T()));
+                        if (d == 0 && a.lse != nullptr)
+                            a.lse[orow] = bad ? nan : fmaf(top, kLn2, logf(total));
+                    } else {
+                        part[d] = sum;
+                        if (d == 0) {
+                            part[DP] = top;
+                            part[DP + 1] = bad ? nan : total;
+                        }
+                    }
                 }
-            }
-            if (!ok) break;
-            if (threadIdx.x < rows && !again(threadIdx.x)) {
-                const int r = threadIdx.x;
-                const float top = row_max(r);
-                float total = 0.f;
+            };
+            // All columns at one time where they fit, else kJoin at a time.
+            const bool once = rows * DP <= X::kRows * X::kJoin;
+            const int width = once ? DP : X::kJoin;
+            constexpr int kStepsJ = X::kJoin / 8;
 #pragma unroll
-                for (int w = 0; w < kWorkers; ++w) {
-                    const float2 z = ctl.ml[w][r];
-                    total += z.y * (z.x == top ? 1.f : sv::ex2(z.x - top));
+            for (int j0 = 0; j0 < DP / 8; j0 += kStepsJ) {
+                if (!once && j0 > 0 && !(ok = meet())) break;
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                    if (g + 8 * i >= rows) continue;
+                    float* to = join + (warp * rows + g + 8 * i) * width + 2 * c4 + (once ? 8 * j0 : 0);
+#pragma unroll
+                    for (int j = 0; j < kStepsJ; ++j)
+                        *reinterpret_cast<float2*>(to + j * 8) =
+                            make_float2(o[i >> 1][j0 + j][2 * (i & 1)],
+                                        o[i >> 1][j0 + j][2 * (i & 1) + 1]);
                 }
-                if (!whole) {
-                    share[static_cast<int64_t>(r) * (DP + 4) + DP] = top;
-                    share[static_cast<int64_t>(r) * (DP + 4) + DP + 1] = bad ? nan : total;
-                } else if (a.lse != nullptr) {
-                    const int rr = p.row0 + r, t = rr / a.G;
-                    a.lse[(static_cast<int64_t>(p.q0) + t) * a.Hq + p.h * a.G + (rr - t * a.G)] =
-                        bad ? nan : fmaf(top, kLn2, logf(total));
+                if (!once) {
+                    if (!(ok = meet())) break;
+                    add_up(j0, width);
                 }
             }
+            if (ok && once && (ok = meet())) add_up(0, width);
+            if (!ok) break;
             if (noted != 0 && !bad) {
                 for (int r = warp; r < rows; r += kWorkers) {
                     __syncwarp();
@@ -583,24 +586,24 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 ctl.noted[(item + kItems - 2) % kItems] = 0;
                 ctl.bad_page[(item + kItems - 2) % kItems] = 0;
             }
-            if (!(ok = meet())) break;
+            // (what is read here is written again behind the next segment's store())
         }
     }
     __syncthreads();
     if (threadIdx.x == 0) args.shares[blockIdx.x].failed = *stop;
 }
 
-template <class T, int DP, bool E4M3, int MT>
+template <class T, int DP, bool E4M3>
 cudaError_t launch_few_shape(const CUtensorMap& k, const CUtensorMap& v, const Tiles& t, int blocks,
                              int64_t rows, cudaStream_t s)
 {
-    using X = FewShape<DP, E4M3, MT>;
-    using Ctl = FewControl<X::kStages, E4M3, MT>;
+    using X = FewShape<DP, E4M3>;
+    using Ctl = FewControl<X::kStages, E4M3>;
     constexpr size_t smem = X::kBytes + sizeof(Ctl);
     static_assert(smem <= kMaxSmem, "shared memory");
     static_assert(alignof(Ctl) == 16 && X::kBytes % 1024 == 0, "alignment");
     static_assert(X::kStages / 2 + 1 < kItems - 2, "notes");
-    auto* f = few_kernel<T, DP, E4M3, MT>;
+    auto* f = few_kernel<T, DP, E4M3>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -613,11 +616,8 @@ template <class T, int DP>
 cudaError_t launch_few_type(const CUtensorMap& k, const CUtensorMap& v, const Tiles& t, int blocks,
                             int64_t rows, bool e4m3, cudaStream_t s)
 {
-    if (e4m3)
-        return rows <= 16 ? launch_few_shape<T, DP, true, 1>(k, v, t, blocks, rows, s)
-                          : launch_few_shape<T, DP, true, 2>(k, v, t, blocks, rows, s);
-    return rows <= 16 ? launch_few_shape<T, DP, false, 1>(k, v, t, blocks, rows, s)
-                      : launch_few_shape<T, DP, false, 2>(k, v, t, blocks, rows, s);
+    return e4m3 ? launch_few_shape<T, DP, true>(k, v, t, blocks, rows, s)
+                : launch_few_shape<T, DP, false>(k, v, t, blocks, rows, s);
 }
 
 }  // namespace

@@ -23,7 +23,7 @@ cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* wor
                                    cudaStream_t s, bool* mapped);
 
 // The same for at most kFewRows rows a sequence and key/value head.
-constexpr int64_t kFewRows = 32;
+constexpr int64_t kFewRows = 16;
 cudaError_t launch_attention_few(const Attn& a, bool f16, bool e4m3, void* workspace,
                                  cudaStream_t s, bool* mapped);
 

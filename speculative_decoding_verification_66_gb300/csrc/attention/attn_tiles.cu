@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         sv::mbar_wait_bounded(&ctl.done, 0, nullptr);
     } else if (warp == 9 || warp == 10) {
         // Copies of keys (warp 9, which also plans the segments) and values (10).
-        feed<T, DP, E4M3, R, PAIR, !PAIR, kFill>(
+        feed<T, DP, E4M3, R, PAIR, !PAIR, kFill, false>(
             args, ctl, warp == 9 ? &kmap : &vmap, warp - 9, E4M3 ? sr : st,
             E4M3 ? X::kRawBytes : X::kTileBytes, E4M3 ? ctl.raw_full : ctl.full,
             E4M3 ? ctl.raw_empty : ctl.empty, start, wait_all);
