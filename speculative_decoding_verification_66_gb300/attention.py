@@ -37,51 +37,57 @@ _CACHE = struct.Struct("@4P12qq4iP2q2Pq")
 _NO_EXPS = (0, 0, 0)
 
 
+# (The checks below run at every step of a decode loop: plain ifs, messages built only when raised.)
+
+
 def _require(ok, what):
     if not ok:
         raise ValueError(what)
 
 
 def _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps, v_exps):
-    """(packed struct sv_paged_cache, element type code, device)."""
+    """(packed struct sv_paged_cache, element type code, device, B)."""
     dev, dt, shape = k_pages.device, k_pages.dtype, k_pages.shape
-    _require(dev.type == "cuda" and len(shape) == 4,
-             "k_pages must be a CUDA tensor [pages, page_size, kv_heads, head_dim]")
+    if len(shape) != 4 or not k_pages.is_cuda:
+        raise ValueError("k_pages must be a CUDA tensor [pages, page_size, kv_heads, head_dim]")
     code = _CODES.get(dt)
     if code is None:
         raise TypeError(f"pages must be bfloat16, float16 or float8_e4m3fn, got {dt}")
+    if v_pages.shape != shape or v_pages.dtype != dt or v_pages.device != dev:
+        raise ValueError("v_pages must have k_pages' shape, dtype and device")
     ks, vs = k_pages.stride(), v_pages.stride()
-    _require(v_pages.shape == shape and v_pages.dtype == dt and v_pages.device == dev,
-             "v_pages must have k_pages' shape, dtype and device")
-    _require(ks[3] == 1 and vs[3] == 1, "pages must be contiguous along head_dim")
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("pages must be contiguous along head_dim")
     if code == SV_E4M3:
         for e in (k_exps, v_exps):
-            _require(e is not None and e.dtype == torch.uint8 and e.shape == shape[:3]
-                     and e.device == dev,
-                     "k_exps and v_exps must be uint8 [pages, page_size, kv_heads] beside "
-                     "e4m3 pages")
+            if e is None or e.dtype != torch.uint8 or e.shape != shape[:3] or e.device != dev:
+                raise ValueError("k_exps and v_exps must be uint8 [pages, page_size, kv_heads] "
+                                 "beside e4m3 pages")
         kep, vep, kes, ves = k_exps.data_ptr(), v_exps.data_ptr(), k_exps.stride(), v_exps.stride()
+    elif k_exps is not None or v_exps is not None:
+        raise ValueError("only e4m3 pages have exponents")
     else:
-        _require(k_exps is None and v_exps is None, "only e4m3 pages have exponents")
         kep, vep, kes, ves = 0, 0, _NO_EXPS, _NO_EXPS
-    B = cached_lens.numel()
-    _require(page_table.dim() == 2 and page_table.shape[0] == B and page_table.dtype == torch.int32
-             and (page_table.stride(1) == 1 or page_table.shape[1] <= 1)
-             and page_table.device == dev,
-             "page_table must be int32 [B, max_pages], rows contiguous")
-    _require(cached_lens.dim() == 1 and cached_lens.dtype == torch.int32
-             and cached_lens.is_contiguous() and cached_lens.device == dev,
-             "cached_lens must be contiguous int32 [B]")
-    _require(chunk_starts.dim() == 1 and chunk_starts.numel() == B + 1
-             and chunk_starts.dtype == torch.int32 and chunk_starts.is_contiguous()
-             and chunk_starts.device == dev, "chunk_starts must be contiguous int32 [B + 1]")
-    max_pages = page_table.shape[1]
+    i32 = torch.int32
+    if cached_lens.dim() != 1 or cached_lens.dtype != i32 or not cached_lens.is_contiguous() \
+            or cached_lens.device != dev:
+        raise ValueError("cached_lens must be contiguous int32 [B]")
+    B = cached_lens.shape[0]
+    table = page_table.shape
+    if len(table) != 2 or table[0] != B or page_table.dtype != i32 or page_table.device != dev:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    row, step = page_table.stride()
+    if step != 1 and table[1] > 1:
+        raise ValueError("page_table's rows must be contiguous")
+    if chunk_starts.shape != (B + 1,) or chunk_starts.dtype != i32 \
+            or not chunk_starts.is_contiguous() or chunk_starts.device != dev:
+        raise ValueError("chunk_starts must be contiguous int32 [B + 1]")
     packed = _CACHE.pack(
         k_pages.data_ptr(), v_pages.data_ptr(), kep, vep, ks[0], vs[0], ks[1], vs[1], ks[2], vs[2],
         kes[0], ves[0], kes[1], ves[1], kes[2], ves[2], shape[0], shape[1], shape[2], shape[3],
-        code, page_table.data_ptr(), max(page_table.stride(0), max_pages), max_pages,
-        cached_lens.data_ptr(), chunk_starts.data_ptr(), B)
-    return packed, code, dev
+        code, page_table.data_ptr(), max(row, table[1]), table[1], cached_lens.data_ptr(),
+        chunk_starts.data_ptr(), B)
+    return packed, code, dev, B
 
 
 def _rows(x, name, heads, head_dim, dev, cache_code):
@@ -90,10 +96,12 @@ def _rows(x, name, heads, head_dim, dev, cache_code):
     if code is None or code == SV_E4M3 or (cache_code != SV_E4M3 and code != cache_code):
         raise TypeError(f"{name} must be bfloat16 or float16, and of the cache's type unless that "
                         f"is e4m3, got {x.dtype}")
-    _require(x.dim() == 3 and x.device == dev and x.shape[2] == head_dim and
-             (heads is None or x.shape[1] == heads),
-             f"{name} must be [tokens, heads, head_dim] on the cache's device")
-    _require(x.stride(2) == 1 or x.numel() == 0, f"{name} must be contiguous along head_dim")
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != head_dim or (heads is not None and shape[1] != heads) \
+            or x.device != dev:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] on the cache's device")
+    if x.stride(2) != 1 and x.numel() > 0:
+        raise ValueError(f"{name} must be contiguous along head_dim")
     return code
 
 
@@ -128,14 +136,14 @@ def sv_kv_append(key, value, k_pages, v_pages, page_table, cached_lens, chunk_st
     """Write the new tokens' key and value [tokens, kv_heads, head_dim] (any strides but the last)
     into the cache, quantised where it is e4m3. Asynchronous on ``stream`` (default: the current
     stream of the pages' device)."""
-    cache, code, dev = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
-                              v_exps)
-    H, D = k_pages.shape[2:]
+    cache, code, dev, B = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
+                                 v_exps)
+    _, _, H, D = k_pages.shape
     dtype = _rows(key, "key", H, D, dev, code)
     _rows(value, "value", H, D, dev, code)
-    _require(value.shape == key.shape and value.dtype == key.dtype,
-             "value must have key's shape and dtype")
-    status = _status(seq_status, cached_lens.numel(), dev)
+    if value.shape != key.shape or value.dtype != key.dtype:
+        raise ValueError("value must have key's shape and dtype")
+    status = _status(seq_status, B, dev)
     ks, vs = key.stride(), value.stride()
 
     def call(s):
@@ -154,13 +162,13 @@ def sv_kv_read(k_pages, v_pages, page_table, cached_lens, chunk_starts, tokens: 
     of every sequence back. Returns (key, value) [tokens, kv_heads, head_dim] of ``dtype``
     (default: the cache's, bfloat16 from e4m3); ``tokens`` is chunk_starts[B], which the host has
     to know."""
-    cache, code, dev = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
-                              v_exps)
-    H, D = k_pages.shape[2:]
+    cache, code, dev, B = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
+                                 v_exps)
+    _, _, H, D = k_pages.shape
     if dtype is None:
         dtype = key.dtype if key is not None else \
             torch.bfloat16 if code == SV_E4M3 else k_pages.dtype
-    status = _status(seq_status, cached_lens.numel(), dev)
+    status = _status(seq_status, B, dev)
     _require(tokens >= 0, "tokens must not be negative")
 
     def call(s):
@@ -168,10 +176,10 @@ def sv_kv_read(k_pages, v_pages, page_table, cached_lens, chunk_starts, tokens: 
         for name, x in (("key", key), ("value", value)):
             if x is None:
                 x = torch.empty((tokens, H, D), dtype=dtype, device=dev)
-            d = _rows(x, name, H, D, dev, code)
-            _require(x.shape[0] == tokens and x.dtype == dtype and x.is_contiguous(),
-                     f"{name} must be contiguous [tokens, kv_heads, head_dim] of dtype")
+            elif x.shape[0] != tokens or x.dtype != dtype or not x.is_contiguous():
+                raise ValueError(f"{name} must be contiguous [tokens, kv_heads, head_dim] of dtype")
             out.append(x)
+            d = _rows(x, name, H, D, dev, code)
         _check(_lib.load_attention().sv_kv_read(cache, out[0].data_ptr(), out[1].data_ptr(), d,
                                                 tokens, status, s), "sv_kv_read")
         return tuple(out)
@@ -201,13 +209,13 @@ def sv_chunk_attention(query, k_pages, v_pages, page_table, cached_lens, chunk_s
     ``scale`` defaults to head_dim ** -0.5. ``max_chunk``: an upper bound of the sequences' new
     tokens (0: tokens); a tight one lets the launches be planned for it. Returns out, or (out, lse)
     with ``return_lse`` or an ``lse`` tensor (float32 [tokens, q_heads])."""
-    cache, code, dev = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
-                              v_exps)
-    H, D = k_pages.shape[2:]
+    cache, code, dev, B = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
+                                 v_exps)
+    _, _, H, D = k_pages.shape
     dtype = _rows(query, "query", None, D, dev, code)
-    N, Hq = query.shape[:2]
-    B = cached_lens.numel()
-    _require(H > 0 and Hq > 0 and Hq % H == 0, "query heads must be a multiple of kv_heads")
+    N, Hq, _ = query.shape
+    if H < 1 or Hq < 1 or Hq % H != 0:
+        raise ValueError("query heads must be a multiple of kv_heads")
     status = _status(seq_status, B, dev)
     if scale is None:
         scale = D ** -0.5

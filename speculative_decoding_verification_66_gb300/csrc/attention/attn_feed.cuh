@@ -4,6 +4,7 @@
 // several blocks worked on.
 #pragma once
 
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -244,68 +245,62 @@ __device__ __forceinline__ uint32_t tile_chunk(int row, int chunk, int group, in
            (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-// Sum of int64 over the block; every thread gets it.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sums, int warps)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int64_t t = 0;
-    for (int w = 0; w < warps; ++w) t += sums[w];
-    return t;
-}
-
-// Where this block starts, into ctl.start.
+// Where this block starts, into ctl.start. True if some sequence's lengths are
+// bad. The sequences' units are added up THREADS at a time; with no more
+// sequences than threads the one pass finds the start too.
 template <int R, int THREADS, class Ctl>
-__device__ void find_start(const Attn& a, Ctl& ctl)
+__device__ bool find_start(const Attn& a, Ctl& ctl)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tid = threadIdx.x;
-    int64_t mine = 0, first = 0;
-    for (int64_t b = tid; b < a.c.B; b += THREADS) {
-        const Seq q = seq_of(a.c, static_cast<int>(b), a.tokens, a.max_chunk);
-        const int64_t u = head_units<R>(a, q) * a.c.Hkv;
-        if (b == tid) first = u;
-        mine += u;
+    constexpr int kWarps = THREADS / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int64_t U = 0, u = 0, scan = 0, chunk = 0;
+    bool bad = false;
+    // Units of sequence base + tid, their sum up to it, and the sum of all of the
+    // pass.
+    auto pass = [&](int64_t base) {
+        const int64_t b = base + tid;
+        u = 0;
+        if (b < a.c.B) {
+            const Seq q = seq_of(a.c, static_cast<int>(b), a.tokens, a.max_chunk);
+            bad |= q.bad != 0;
+            u = head_units<R>(a, q) * a.c.Hkv;
+        }
+        scan = u;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, scan, d);
+            if (lane >= d) scan += o;
+        }
+        __syncthreads();
+        if (lane == 31) ctl.sums[warp] = scan;
+        __syncthreads();
+        chunk = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) scan += ctl.sums[w];
+            chunk += ctl.sums[w];
+        }
+    };
+    for (int64_t base = 0; base < a.c.B; base += THREADS) {
+        pass(base);
+        U += chunk;
     }
-    const int64_t U = block_sum(mine, ctl.sums, THREADS / 32);
     const int64_t u0 = share_begin(U, blockIdx.x, gridDim.x);
     const int64_t u1 = share_begin(U, blockIdx.x + 1, gridDim.x);
     if (tid == 0) ctl.start = Start{u0, u1, U, 0, 0};
     __syncthreads();
     if (u0 < u1) {
         int64_t before = 0;
-        for (int64_t base_b = 0; base_b < a.c.B && before <= u0; base_b += THREADS) {
-            const int64_t b = base_b + tid;
-            int64_t u = first;
-            if (base_b > 0)
-                u = b < a.c.B ? head_units<R>(a, seq_of(a.c, static_cast<int>(b), a.tokens,
-                                                        a.max_chunk)) * a.c.Hkv
-                              : 0;
-            int64_t scan = u;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, scan, d);
-                if (lane >= d) scan += o;
-            }
-            __syncthreads();
-            if (lane == 31) ctl.sums[warp] = scan;
-            __syncthreads();
-            int64_t chunk = 0;
-            for (int w = 0; w < THREADS / 32; ++w) {
-                if (w < warp) scan += ctl.sums[w];
-                chunk += ctl.sums[w];
-            }
+        for (int64_t base = 0; base < a.c.B && before <= u0; base += THREADS) {
+            if (a.c.B > THREADS) pass(base);
             const int64_t begin = before + scan - u;
             if (u0 >= begin && u0 < begin + u) {
                 ctl.start.off = u0 - begin;
-                ctl.start.b = static_cast<int32_t>(b);
+                ctl.start.b = static_cast<int32_t>(base + tid);
             }
             before += chunk;
         }
     }
+    return __syncthreads_or(bad) != 0;
 }
 
 // Rows of sequences whose lengths are bad become NaN; block c of n takes
@@ -652,6 +647,20 @@ __global__ void __launch_bounds__(128) join_kernel(const Tiles args, int blocks)
                 static_cast<uint16_t>(narrow2(o[i] * inv, 0.f, T()));
     }
     if (a.lse != nullptr && lane == 0) a.lse[orow] = fmaf(m, kLn2, logf(l));
+}
+
+// Allows `f` its shared memory, once a device.
+template <class F>
+cudaError_t allow_smem(F* f, size_t smem, std::atomic<uint64_t>* done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit != 0 && (done->load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 // Launch of join_kernel behind a tile kernel: it may start while that runs and

@@ -132,8 +132,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int i = 0; i < kItems; ++i) ctl.noted[i] = ctl.bad_page[i] = 0;
         sv::fence_barrier_init();
     }
-    find_start<R, kFewThreads>(a, ctl);
-    refuse_sequences<T>(a);
+    if (find_start<R, kFewThreads>(a, ctl)) refuse_sequences<T>(a);
     __syncthreads();
     const Start start = ctl.start;
     volatile int* stop = &ctl.stop;
@@ -604,8 +603,8 @@ cudaError_t launch_few_shape(const CUtensorMap& k, const CUtensorMap& v, const T
     static_assert(alignof(Ctl) == 16 && X::kBytes % 1024 == 0, "alignment");
     static_assert(X::kStages / 2 + 1 < kItems - 2, "notes");
     auto* f = few_kernel<T, DP, E4M3>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(f, smem, &allowed);
     if (e != cudaSuccess) return e;
     f<<<blocks, kFewThreads, smem, s>>>(k, v, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -56,7 +56,15 @@ __device__ __forceinline__ int64_t head_units(const Attn& a, const Seq& q)
     return n;
 }
 
-__device__ __forceinline__ int64_t share_begin(int64_t U, int c, int n) { return U * c / n; }
+// a / b, b > 0, a >= 0: a 64-bit division is a long routine, and most of these
+// numbers are small.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (static_cast<uint64_t>(a | b) >> 32 == 0)
+        return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+__device__ __forceinline__ int64_t share_begin(int64_t U, int c, int n) { return quotient(U * c, n); }
 
 // Where a block starts.
 struct Start {
@@ -90,7 +98,7 @@ struct Walk {
         if (left <= 0) return;
         q = seq_of(a.c, b, a.tokens, a.max_chunk);
         const int64_t n = head_units<R>(a, q);
-        h = static_cast<int32_t>(skip / n);
+        h = static_cast<int32_t>(quotient(skip, n));
         skip -= h * n;
     }
 

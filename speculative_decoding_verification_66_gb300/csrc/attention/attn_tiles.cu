@@ -167,8 +167,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
 
-    find_start<R, X::kThreads>(a, ctl);
-    refuse_sequences<T>(a);
+    if (find_start<R, X::kThreads>(a, ctl)) refuse_sequences<T>(a);
     __syncthreads();
     fence_after();
     const uint32_t tmem = ctl.tmem;
@@ -759,8 +758,8 @@ cudaError_t launch_shape(const CUtensorMap& k, const CUtensorMap& v, const Tiles
     // (factor is written 16 bytes at a time)
     static_assert(alignof(Ctl) == 16 && X::kTiles % 1024 == 0, "alignment");
     auto* f = tiles_kernel<T, DP, E4M3, PAIR>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(f, smem, &allowed);
     if (e != cudaSuccess) return e;
     if (E4M3) {
         // (the split of registers waits for what the block was not launched with)
