@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import threading
 from contextlib import ExitStack
 from functools import lru_cache
 
@@ -131,6 +132,22 @@ def _on(dev, stream, call, tensors):
         return call(torch._C._cuda_getCurrentRawStream(dev.index))
 
 
+_kept = threading.local()
+
+
+def _workspace(dev, stream, nbytes):
+    """At least nbytes, kept for this thread's calls on this stream, which the stream puts in
+    order. A call that is being captured gets a buffer of its own, from the graph's pool: its
+    replays may run beside anything."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    kept = _kept.__dict__
+    w = kept.get((dev.index, stream))
+    if w is None or w.numel() < nbytes:
+        w = kept[(dev.index, stream)] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return w
+
+
 def sv_kv_append(key, value, k_pages, v_pages, page_table, cached_lens, chunk_starts, *,
                  k_exps=None, v_exps=None, seq_status=None, stream=None) -> None:
     """Write the new tokens' key and value [tokens, kv_heads, head_dim] (any strides but the last)
@@ -231,13 +248,15 @@ def sv_chunk_attention(query, k_pages, v_pages, page_table, cached_lens, chunk_s
     qs = query.stride()
 
     def call(s):
-        o = torch.empty((N, Hq, D), dtype=query.dtype, device=dev) if out is None else out
+        o = out
+        if o is None:
+            o = torch.empty_like(query) if query.is_contiguous() else \
+                torch.empty((N, Hq, D), dtype=query.dtype, device=dev)
         z = torch.empty((N, Hq), dtype=torch.float32, device=dev) if lse is None and return_lse \
             else lse
-        # A new workspace every call, from the allocator's pool of this stream (or of the graph
-        # being captured): nothing that an earlier call or a replay still uses is touched.
-        w = torch.empty(sv_chunk_attention_workspace_bytes(B, N, Hq, H, D, max_chunk),
-                        dtype=torch.uint8, device=dev) if workspace is None else workspace
+        w = workspace
+        if w is None:
+            w = _workspace(dev, s, sv_chunk_attention_workspace_bytes(B, N, Hq, H, D, max_chunk))
         _check(_lib.load_attention().sv_chunk_attention(
             cache, query.data_ptr(), dtype, N, Hq, qs[0], qs[1], scale, window, max_chunk,
             o.data_ptr(), None if z is None else z.data_ptr(), status, w.data_ptr(), w.numel(), s),

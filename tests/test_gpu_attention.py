@@ -351,6 +351,35 @@ def test_given_outputs_and_workspace():
     assert torch.equal(alone, out)
 
 
+def test_kept_workspaces_grow_and_keep_apart():
+    """Calls of growing sizes, on two streams and from two threads at a time."""
+    import threading
+    cases = []
+    for i, (lens, T) in enumerate([([30], 1), ([3000, 70], 4), ([900, 5000], 40), ([200], 2)]):
+        c = Cache(lens, [T] * len(lens), 2, 128, 16, "bf16", i % 2 == 1, seed=i)
+        q = make_query(c, 4, i)
+        cases.append((c, q, T, attend(c, q, max_chunk=T)))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(stream):
+        with torch.cuda.stream(stream):
+            got = [attend(c, q, max_chunk=T) for _ in range(8) for c, q, T, _ in cases]
+            stream.synchronize()
+            for i, (o, z) in enumerate(got):
+                want = cases[i % len(cases)][3]
+                if not (torch.equal(o, want[0]) and torch.equal(z, want[1])):
+                    bad.append(i)
+
+    same, other = torch.cuda.Stream(), torch.cuda.Stream()
+    threads = [threading.Thread(target=work, args=(s,)) for s in (same, same, other)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_rows_of_no_sequence_are_left_alone():
     """Packed arrays longer than the chunks (a graph's padded batch)."""
     c = Cache([100, 3], [4, 2], 2, 128, 16, "bf16", False, seed=11)
