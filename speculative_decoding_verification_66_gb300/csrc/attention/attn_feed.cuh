@@ -15,8 +15,21 @@
 namespace sva {
 namespace {
 
-__device__ __forceinline__ float slack(Bf16) { return 60.f; }
-__device__ __forceinline__ float slack(F16) { return 14.f; }  // (below 65504, with 1 to spare)
+// Powers of two by which a weight may pass 1 before the outputs are rescaled:
+// float16 weights stay below 65504 (e4m3 caches: also after a tile's exponent,
+// see kLift), float32 sums of products with bfloat16's largest values finite.
+template <bool E4M3>
+__device__ __forceinline__ float slack()
+{
+    return E4M3 ? 8.f : 14.f;
+}
+// e4m3: the weights carry the power of two between their tile's values and the
+// outputs' reference, which follows the tiles when it is more than kLift above
+// or kSink below.
+constexpr int kLift = 7, kSink = 6;
+// Values of one tile may be this many powers of two apart (see key_factor).
+constexpr int kSpread = 13;
+
 constexpr int kMaxBlocks = 160;  // shares in the workspace; grids are no larger
 constexpr size_t kMaxSmem = 232448;
 constexpr int kNoted = 4;        // noted positions a segment can hold
@@ -140,74 +153,52 @@ __device__ __forceinline__ Plan plan_of(const Attn& a, const Segment& g)
 }
 
 // ---------------------------------------------------------------------------
-// Expanding e4m3. A value is code 2^(e - 127). bfloat16: the code's exponent
-// and mantissa bits, moved under bfloat16's wider exponent, read as the value
-// times 2^-120 (the biases differ by 127 - 7; subnormal codes land on subnormal
-// bfloat16s), so one multiplication by 2^(e - 7) gives the value exactly; it
-// takes two where that exceeds bfloat16. float16: the conversion instruction,
-// then one multiplication by 2^(e - 127), two where that is not a normal
-// float16. Either way two values an instruction.
+// Expanding e4m3 to float16, relative to the largest exponent `top` of a tile:
+// code 2^(e - top), the conversion and one multiplication for two values. Codes
+// have three mantissa bits and a least step of 2^-9, so this is exact for
+// top - e <= kSpread = 13 (2^-22, where float16 has 2^-24) and off by at most
+// 2^-25 below that.
 // ---------------------------------------------------------------------------
-struct Factor {
-    uint32_t f1, f2;  // both halves alike
-    bool two;
-};
 __device__ __forceinline__ uint32_t both(uint32_t h) { return h | (h << 16); }
-__device__ __forceinline__ Factor factor_of(uint32_t e, Bf16)
-{
-    const uint32_t x = min(e, 134u), y = e == 255u ? 0u : e - x;
-    return Factor{e == 255u ? both(0x7FFFu) : (x + 120u) * 0x00800080u, (y + 127u) * 0x00800080u,
-                  y != 0};
-}
-__device__ __forceinline__ Factor factor_of(uint32_t e, F16)
-{
-    if (e == 255u) return Factor{both(0x7FFFu), both(0x3C00u), false};
-    const int x = static_cast<int>(e) - 127;
-    const int g = min(max(x, -14), 15), h = x - g;
-    const uint32_t second = h < -24 ? 0u : h < -14 ? 1u << (h + 24) : (h > 15 ? 30u : h + 15u) << 10;
-    return Factor{both(static_cast<uint32_t>(g + 15) << 10), both(second), h != 0};
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b, Bf16)
-{
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b, F16)
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
 {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Four codes to two words of 16-bit values, before the factor.
-__device__ __forceinline__ uint2 spread(uint32_t w, Bf16)
-{
-    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-    return make_uint2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u),
-                      (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u));
-}
-__device__ __forceinline__ uint2 spread(uint32_t w, F16)
+// Four codes to two words of float16.
+__device__ __forceinline__ uint2 spread(uint32_t w)
 {
     return make_uint2(e4m3_to_f16x2(w & 0xFFFFu), e4m3_to_f16x2(w >> 16));
 }
-// Factor of a key's codes relative to the tile's largest exponent.
-__device__ __forceinline__ uint32_t key_factor(uint32_t e, uint32_t top)
+// The factor of a vector's codes, in both halves.
+__device__ __forceinline__ uint32_t code_factor(uint32_t e, uint32_t top)
 {
     if (e == 255u) return both(0x7FFFu);
     const int d = static_cast<int>(top) - static_cast<int>(e);
     return both(d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u);
 }
-// 16 codes times a factor, as sixteen 16-bit values.
-template <class T>
+// 16 codes times a factor, as sixteen float16 values.
 __device__ __forceinline__ void expand(uint4 codes, uint32_t f, uint32_t (&o)[8])
 {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint2 s = spread(w[i], T());
-        o[2 * i] = mul2(s.x, f, T());
-        o[2 * i + 1] = mul2(s.y, f, T());
+        const uint2 s = spread(w[i]);
+        o[2 * i] = mul2(s.x, f);
+        o[2 * i + 1] = mul2(s.y, f);
     }
+}
+// Whether the outputs' reference exponent (0: none yet) has to move to a tile's,
+// and the power of two that the outputs are then multiplied by. Tiles whose
+// values are all zero (exponent 10, or 0: none visible) do not count.
+__device__ __forceinline__ bool moves(int ref, int top)
+{
+    return top > 10 && (ref == 0 || top - ref > kLift || ref - top > kSink);
+}
+__device__ __forceinline__ float moved(int ref, int top)
+{
+    return ref == 0 ? 1.f : exp_value(static_cast<uint32_t>(max(min(127 + ref - top, 227), 27)));
 }
 
 __device__ __forceinline__ bool any_special(uint4 w, uint32_t exponent)
@@ -383,8 +374,9 @@ __device__ __forceinline__ const Plan* plan_at(Ctl& ctl, int i, Wait& wait_all)
 
 // Copies of keys (kv = 0) or values (1), by a warp; the keys' warp also plans the
 // segments. e4m3: the factors that the codes are multiplied by (FEW: of keys, the
-// powers of two themselves; of values, as halves). The page of tile k + 3 and the exponents of tile k + 2 are on their
-// way while tile k is issued.
+// powers of two themselves; of values, as halves), and with the keys the largest
+// exponents of the tile's keys and values. The page of tile k + 2 and the
+// exponents of tile k + 1 are on their way while tile k is issued.
 template <class T, int DP, bool E4M3, int R, bool SPLIT, bool ALT, int FILL, bool FEW, class Ctl,
           class Wait>
 __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensorMap* map, int kv,
@@ -458,7 +450,7 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
         auto good = [&](int32_t page) { return page >= 0 && page < a.c.num_pages; };
         auto slot_of = [&](int k) { return (k * kTile + lane * 4 + in_page0) & (P - 1); };
         struct Exps {
-            uint32_t e[4];
+            uint32_t e[4], v[4];  // (v: the values', loaded with the keys)
         };
         auto exps_of = [&](int k, int32_t page) {
             Exps x{};
@@ -466,16 +458,22 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                 const uint8_t* e = exps + exp_at(a.c, kv, good(page) ? page : 0, slot_of(k), h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x.e[i] = e[i * exp_step];
+                if (kv == 0) {
+                    const uint8_t* v =
+                        a.c.exps[1] + exp_at(a.c, 1, good(page) ? page : 0, slot_of(k), h);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x.v[i] = v[i * a.c.exp_slot_stride[1]];
+                }
             }
             return x;
         };
-        int32_t cur = entry(0), next = entry(1), then = entry(2);
-        Exps xc = exps_of(0, cur), xn = exps_of(1, next);
+        int32_t cur = entry(0), next = entry(1);
+        Exps xc = exps_of(0, cur);
         Place<FILL> at = base_at;
         if (kv) at.advance(ring_v<ALT>(0, n));
         for (int k = 0; k < n; ++k) {
-            const int32_t after = entry(k + 3);
-            const Exps xt = exps_of(k + 2, then);
+            const int32_t then = entry(k + 2);
+            const Exps xn = exps_of(k + 1, next);
             const bool needed = cur != INT_MIN;
             // A page out of range: page 0 in its place, and NaN for the item.
             const bool bad = needed && !good(cur);
@@ -487,52 +485,63 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
             }
             if constexpr (E4M3) {
                 // Positions that no row sees may hold anything: factor 0, which
-                // the helpers turn into zeros. So do values that are NaN at
-                // positions that not every row sees; these are noted.
-                uint32_t top = 0, f[4], two = 0, hidden = 0;
+                // turns into zeros. So do values that are NaN at positions that
+                // not every row sees; these are noted.
+                uint32_t top = 0, v_top = 0, f[4], hidden = 0;
+                auto note = [&](int p, int times) {
+                    const int x = atomicAdd(&ctl.noted[item % kItems], times);
+                    if (x < kNoted) ctl.note[item % kItems][x] = p;
+                };
+                if (k < g->inner_lo || k > g->inner_hi) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int p = k * kTile + lane * 4 + i;
-                    if (p < any_lo || p > any_hi) {
-                        hidden |= 1u << i;
-                    } else if (xc.e[i] != 255u) {
-                        top = max(top, xc.e[i]);
-                    } else if (kv == 1 && (p < g->all_lo || p > g->all_hi)) {
-                        hidden |= 1u << i;
-                        const int x = atomicAdd(&ctl.noted[item % kItems], 1);
-                        if (x < kNoted) ctl.note[item % kItems][x] = p;
+                    for (int i = 0; i < 4; ++i) {
+                        const int p = k * kTile + lane * 4 + i;
+                        const bool outside = p < any_lo || p > any_hi;
+                        const bool common = p >= g->all_lo && p <= g->all_hi;
+                        if (outside) xc.v[i] = 0;
+                        if (outside || (kv == 1 && !common && xc.e[i] == 255u)) {
+                            hidden |= 1u << i;
+                            if (!outside) note(p, 1);
+                            xc.e[i] = 0;
+                        }
                     }
                 }
-                if (!FEW && kv == 0) top = __reduce_max_sync(0xFFFFFFFFu, top);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (kv == 0) {
-                    f[i] = FEW ? __float_as_uint(exp_value(xc.e[i])) : key_factor(xc.e[i], top);
-                } else {
-                    const Factor x = factor_of(xc.e[i], T());
-                    f[i] = x.f1;
-                    two |= x.two && !(hidden >> i & 1u);
+                for (int i = 0; i < 4; ++i) {
+                    top = max(top, xc.e[i] == 255u ? 0u : xc.e[i]);
+                    if (kv == 0) v_top = max(v_top, xc.v[i] == 255u ? 0u : xc.v[i]);
                 }
-                if (hidden >> i & 1u) f[i] = 0;
-            }
-            const bool any_two = __any_sync(0xFFFFFFFFu, two != 0) != 0;
-            *reinterpret_cast<uint32_t*>(&ctl.exps[at.stage][lane * 4]) =
-                xc.e[0] | xc.e[1] << 8 | xc.e[2] << 16 | xc.e[3] << 24;
-            if constexpr (FEW) {
-                if (kv == 0)
-                    *reinterpret_cast<uint4*>(&ctl.scale[at.stage][lane * 4]) =
+                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                bool apart = false;  // further than float16 holds
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t e = xc.e[i];
+                    f[i] = FEW && kv == 0 ? __float_as_uint(exp_value(e)) : code_factor(e, top);
+                    apart |= e > 10 && e + kSpread < top;
+                }
+                if (hidden != 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (hidden >> i & 1u) f[i] = 0;
+                }
+                if (kv == 1 && apart) note(0, kNoted + 1);  // all rows again
+                if constexpr (FEW) {
+                    if (kv == 0)
+                        *reinterpret_cast<uint4*>(&ctl.scale[at.stage][lane * 4]) =
+                            make_uint4(f[0], f[1], f[2], f[3]);
+                    else
+                        *reinterpret_cast<uint2*>(&ctl.scale[at.stage][lane * 2]) = make_uint2(
+                            (f[0] & 0xFFFFu) | f[1] << 16, (f[2] & 0xFFFFu) | f[3] << 16);
+                } else {
+                    *reinterpret_cast<uint4*>(&ctl.factor[at.stage][lane * 4]) =
                         make_uint4(f[0], f[1], f[2], f[3]);
-                else
-                    *reinterpret_cast<uint2*>(&ctl.scale[at.stage][lane * 2]) = make_uint2(
-                        (f[0] & 0xFFFFu) | f[1] << 16, (f[2] & 0xFFFFu) | f[3] << 16);
-            } else {
-                *reinterpret_cast<uint4*>(&ctl.factor[at.stage][lane * 4]) =
-                    make_uint4(f[0], f[1], f[2], f[3]);
-                if (lane == 0) ctl.top[at.stage] = top;
+                }
+                if (kv == 0) {
+                    v_top = __reduce_max_sync(0xFFFFFFFFu, v_top);
+                    if (lane == 0) ctl.top[at.stage] = make_uint2(top, v_top);
+                }
+                __syncwarp();
             }
-            if (lane == 0) ctl.two[at.stage] = any_two;
-            __syncwarp();
-        }
             const bool leader = needed && first_of_box;
             const unsigned boxes = __ballot_sync(0xFFFFFFFFu, leader);
             if (lane == 0)
@@ -558,9 +567,7 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
             at.advance(kv ? ring_v_step<ALT>(k, n) : ring_k_step<ALT>(k));
             cur = next;
             next = then;
-            then = after;
             xc = xn;
-            xn = xt;
         }
         base_at.advance(2 * n);
     }

@@ -14,14 +14,13 @@
 // Warps 0-7 work, 8 and 9 load keys and values (attn_feed.cuh). Masks, hidden
 // values and the sharing among blocks are those of attn_tiles.cu.
 //
-// e4m3. A lane reads 16 codes of a row at a time and expands them in registers.
-// Keys: as float16 codes alone (the exponents multiply the scores' columns);
-// which d an operand's k slots stand for is free as long as the queries agree,
-// so slots 2c, 2c+1, 2c+8, 2c+9 of step (h, s) are d = 16 (2c + h) + 4 s + 0..3,
-// four neighbouring codes. Values: lane (g, c) reads d = DP/8 g .. of its four
-// keys; codes of two keys are interleaved, moved under the query type's exponent
-// and multiplied by the two keys' factors; the products' column n of step j is
-// then d = DP/8 n + j.
+// e4m3. A lane reads 16 codes of a row at a time and expands them to float16 in
+// registers. Keys: the codes alone (the exponents multiply the scores' columns);
+// which d an operand's k slots stand for is free as long as the queries agree, so
+// slots 2c, 2c+1, 2c+8, 2c+9 of step (h, s) are d = 16 (2c + h) + 4 s + 0..3, four
+// neighbouring codes. Values, relative to their tile's largest exponent as in
+// attn_tiles.cu: lane (g, c) reads d = DP/8 g .. of its four keys and interleaves
+// the codes of two keys; the products' column n of step j is then d = DP/8 n + j.
 #include "attn_feed.cuh"
 
 namespace sva {
@@ -58,11 +57,11 @@ struct FewControl {
     int bad_page[kItems];
     float2 ml[kWorkers][16 * MT];
     float q_scale[16 * MT];
-    // e4m3, for every stage: the keys' powers of two, or (values) the rows' factors
-    // as halves, whether some row needs two, and the exponents.
+    // e4m3, for every stage: the keys' powers of two, or the values' factors as
+    // halves; the largest exponents of its keys and of the values that belong to
+    // them.
     alignas(16) float scale[E4M3 ? STAGES : 1][E4M3 ? kTile : 4];
-    uint32_t two[E4M3 ? STAGES : 1];
-    uint8_t exps[E4M3 ? STAGES : 1][E4M3 ? kTile : 4];
+    uint2 top[E4M3 ? STAGES : 1];
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -111,8 +110,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 {
     using X = FewShape<DP, E4M3>;
     constexpr int S = X::kStages, R = X::kRows;
-    // Type of the first product's operands.
-    using TS = typename std::conditional<E4M3, F16, T>::type;
+    using TP = typename std::conditional<E4M3, F16, T>::type;  // the products' operands
     const Attn& a = args.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     FewControl<S, E4M3>& ctl = *reinterpret_cast<FewControl<S, E4M3>*>(smem + X::kBytes);
@@ -254,6 +252,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.f;
 
+            int ref = 0;  // e4m3: the outputs' exponent
             for (int k = 0; k < n; ++k) {
                 const bool edge = k < p.inner_lo || k > p.inner_hi;
                 const int key0 = 16 * warp;  // this warp's keys of the tile
@@ -272,8 +271,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     for (int mt = 0; mt < MT; ++mt) {
                         const uint4 q = ld_shared_v4(sq + ((mt * X::kSteps + step) * 32 + lane) * 16);
                         const uint32_t f[4] = {q.x, q.y, q.z, q.w};
-                        mma16816(s[mt][0], f, b[0], b[1], TS());
-                        mma16816(s[mt][1], f, b[2], b[3], TS());
+                        mma16816(s[mt][0], f, b[0], b[1], TP());
+                        mma16816(s[mt][1], f, b[2], b[3], TP());
                     }
                 };
                 if constexpr (E4M3) {
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         const uint32_t w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint2 x = spread(w0[i], F16()), y = spread(w1[i], F16());
+                            const uint2 x = spread(w0[i]), y = spread(w1[i]);
                             const uint32_t b[4] = {x.x, x.y, y.x, y.y};
                             scores(4 * h + i, b);
                         }
@@ -319,10 +318,26 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         scores(step, b);
                     }
                 }
+                const int v_top = E4M3 ? static_cast<int>(ctl.top[at.stage].y) : 0;
                 __syncwarp();
                 if (lane == 0) sv::mbar_arrive(&ctl.empty[at.stage]);
                 at.advance(1);
                 // ---- weights
+                int lift = 0;  // e4m3: the tile's values above the outputs' exponent
+                if (E4M3) {
+                    if (moves(ref, v_top)) {
+                        const float keep = moved(ref, v_top);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int j = 0; j < DP / 8; ++j)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[mt][j][i] *= keep;
+                        ref = v_top;
+                    }
+                    lift = v_top > 10 ? v_top - ref : 0;
+                }
+                const float drop = E4M3 ? exp_value(static_cast<uint32_t>(127 - lift)) : 1.f;
                 if (edge) {
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
@@ -343,7 +358,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     const float(&x)[2][4] = s[i >> 1];
                     const int z = 2 * (i & 1);
                     top[i] = fmaxf(fmaxf(x[0][z], x[0][z + 1]), fmaxf(x[1][z], x[1][z + 1])) * cs[i];
-                    grow |= top[i] > m[i] + slack(T());
+                    grow |= top[i] > m[i] + slack<E4M3>();
                 }
                 if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
@@ -351,7 +366,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         float x = top[i];
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                        if (x > m[i] + slack(T())) {
+                        if (x > m[i] + slack<E4M3>()) {
                             const float keep = sv::ex2(m[i] - x);
                             l[i] *= keep;
 #pragma unroll
@@ -366,13 +381,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 uint32_t w[MT][4];
 #pragma unroll
                 for (int i = 0; i < 2 * MT; ++i) {
-                    const float shift = m[i] == ninf ? 0.f : -m[i];
+                    const float shift = (m[i] == ninf ? 0.f : -m[i]) + static_cast<float>(lift);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const float p0 = sv::ex2(fmaf(s[i >> 1][t][2 * (i & 1)], cs[i], shift));
                         const float p1 = sv::ex2(fmaf(s[i >> 1][t][2 * (i & 1) + 1], cs[i], shift));
-                        l[i] += p0 + p1;
-                        w[i >> 1][2 * t + (i & 1)] = narrow2(p0, p1, T());
+                        l[i] = E4M3 ? fmaf(p0 + p1, drop, l[i]) : l[i] + (p0 + p1);
+                        w[i >> 1][2 * t + (i & 1)] = narrow2(p0, p1, TP());
                     }
                 }
                 // ---- values
@@ -406,30 +421,19 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                             for (int i = 0; i < kWords; ++i) codes[z][i] = 0;
                         }
                     }
-                    uint32_t f01b = 0, f23b = 0;
-                    const bool two = ctl.two[at.stage] != 0;
-                    if (two) {
-                        const uint8_t* e = &ctl.exps[at.stage][key0 + 2 * c4];
-                        f01b = (factor_of(e[0], T()).f2 & 0xFFFFu) | factor_of(e[1], T()).f2 << 16;
-                        f23b = (factor_of(e[8], T()).f2 & 0xFFFFu) | factor_of(e[9], T()).f2 << 16;
-                    }
 #pragma unroll
                     for (int i = 0; i < kWords; ++i) {
 #pragma unroll
                         for (int hi = 0; hi < 2; ++hi) {
                             const int sel = hi ? 0x7362 : 0x5140;  // codes 2 hi, 2 hi + 1 of either key
-                            const uint2 x = spread(__byte_perm(codes[0][i], codes[1][i], sel), T());
-                            const uint2 y = spread(__byte_perm(codes[2][i], codes[3][i], sel), T());
-                            uint32_t x0 = mul2(x.x, f01, T()), x1 = mul2(x.y, f01, T());
-                            uint32_t y0 = mul2(y.x, f23, T()), y1 = mul2(y.y, f23, T());
-                            if (two) {
-                                x0 = mul2(x0, f01b, T()), x1 = mul2(x1, f01b, T());
-                                y0 = mul2(y0, f23b, T()), y1 = mul2(y1, f23b, T());
-                            }
+                            const uint2 x = spread(__byte_perm(codes[0][i], codes[1][i], sel));
+                            const uint2 y = spread(__byte_perm(codes[2][i], codes[3][i], sel));
+                            const uint32_t x0 = mul2(x.x, f01), x1 = mul2(x.y, f01);
+                            const uint32_t y0 = mul2(y.x, f23), y1 = mul2(y.y, f23);
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) {
-                                mma16816(o[mt][4 * i + 2 * hi], w[mt], x0, y0, T());
-                                mma16816(o[mt][4 * i + 2 * hi + 1], w[mt], x1, y1, T());
+                                mma16816(o[mt][4 * i + 2 * hi], w[mt], x0, y0, TP());
+                                mma16816(o[mt][4 * i + 2 * hi + 1], w[mt], x1, y1, TP());
                             }
                         }
                     }
@@ -467,8 +471,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         ldmatrix4_trans(from + (j >> 2) * args.panel + (((2 * (j & 3)) ^ y) << 4), b);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
-                            mma16816(o[mt][2 * j], w[mt], b[0], b[1], T());
-                            mma16816(o[mt][2 * j + 1], w[mt], b[2], b[3], T());
+                            mma16816(o[mt][2 * j], w[mt], b[0], b[1], TP());
+                            mma16816(o[mt][2 * j + 1], w[mt], b[2], b[3], TP());
                         }
                     }
                 }
@@ -548,6 +552,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     }
                 }
             };
+            const float size = E4M3 && ref != 0 ? exp_value(static_cast<uint32_t>(ref)) : 1.f;
             // All columns at one time where they fit, else kJoin at a time.
             const bool once = rows * DP <= X::kRows * X::kJoin;
             const int width = once ? DP : X::kJoin;
@@ -562,8 +567,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kStepsJ; ++j)
                         *reinterpret_cast<float2*>(to + j * 8) =
-                            make_float2(o[i >> 1][j0 + j][2 * (i & 1)],
-                                        o[i >> 1][j0 + j][2 * (i & 1) + 1]);
+                            make_float2(o[i >> 1][j0 + j][2 * (i & 1)] * size,
+                                        o[i >> 1][j0 + j][2 * (i & 1) + 1] * size);
                 }
                 if (!once) {
                     if (!(ok = meet())) break;

@@ -44,14 +44,16 @@
 // Positions outside the item's range are always cleared: what lies there may
 // never have been written.
 //
-// e4m3. Values are expanded to the query's type, code and exponent, which is
-// exact. Keys are expanded to float16 relative to the largest exponent of their
-// tile, which multiplies the tile's scores: exact for keys down to 2^-15 of the
-// tile's largest, and to 2^-33 of the largest key's magnitude below that, far
-// under what float32 keeps of that key's scores. bfloat16 queries become float16
-// for this, each row scaled by a power of two that brings its largest element to
-// [2^14, 2^15): exact down to 2^-38 of that. float16 takes 25 instructions for 16
-// codes, bfloat16 45: the helpers' time is what bounds e4m3 caches.
+// e4m3. Keys and values are expanded to float16, relative to the largest exponent
+// of their tile (code_factor): 256 conversions and as many multiplications a tile
+// and warp-width, where bfloat16 would take four times the instructions. The
+// tile's exponents come back in where they cost nothing: the keys' in the scale of
+// the tile's scores, the values' in the exponent of its weights, which are
+// float16 too; O is kept relative to a reference exponent that follows the
+// tiles'. Values of a tile that are more than 2^13 apart would lose bits; a
+// segment that has such a tile computes its rows again, key by key. bfloat16
+// queries become float16, each row scaled by a power of two that brings its
+// largest element to [2^14, 2^15): exact down to 2^-38 of that.
 //
 // Work is shared among one block per SM as attn_plan.cuh says; items that
 // several blocks share are joined by join_kernel in block order, so results
@@ -78,7 +80,7 @@ struct Shape {
     static constexpr int kThreads = (12 + kHelpers) * 32;
     // e4m3: registers a thread of the softmax warps and of the others; together
     // no more than the 640 threads are launched with, 96 each.
-    static constexpr int kRegsRow = 128, kRegsOther = 72, kRegsLaunch = 96;
+    static constexpr int kRegsRow = 104, kRegsOther = 88, kRegsLaunch = 96;
     static_assert(8 * kRegsRow + 12 * kRegsOther <= 20 * kRegsLaunch, "registers");
     static constexpr int kPanel = kTile * 128;  // bytes of 64 elements of every row
     static constexpr int kTiles = kQBytes + kStages * kTileBytes + kRawStages * kRawBytes;
@@ -102,12 +104,13 @@ struct Control {
     int bad_page[kItems];
     // e4m3: powers of two that the rows of this segment and the next are divided by
     float q_scale[2][RAW > 0 ? (PAIR ? 256 : 128) : 1];
-    float k_scale[4];  // .. and of the keys of the last four tiles
-    // e4m3, for every raw stage: a row's factor (two 16-bit halves), the largest
-    // exponent (keys), whether some row needs two factors (values), exponents.
+    // .. of the last four tiles: the keys' power of two, the values' exponent
+    float k_scale[4];
+    int v_top[4];
+    // e4m3, for every raw stage: the rows' factors; the exponents of its keys and
+    // of the values that belong to them.
     alignas(16) uint32_t factor[RAW > 0 ? RAW : 1][RAW > 0 ? kTile : 4];
-    uint32_t top[RAW > 0 ? RAW : 1], two[RAW > 0 ? RAW : 1];
-    uint8_t exps[RAW > 0 ? RAW : 1][RAW > 0 ? kTile : 4];
+    uint2 top[RAW > 0 ? RAW : 1];
 };
 
 template <class T, int DP, bool E4M3, bool PAIR>
@@ -118,6 +121,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
     using X = Shape<DP, E4M3, PAIR>;
     constexpr int S = X::kStages, RS = X::kRawStages, R = X::kRows;
     constexpr int kFill = E4M3 ? RS : S;  // stages that the copies fill
+    using TP = typename std::conditional<E4M3, F16, T>::type;  // the products' operands
     const Attn& a = args.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     Control<S, RS, PAIR>& ctl = *reinterpret_cast<Control<S, RS, PAIR>*>(smem + X::kTiles);
@@ -267,6 +271,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             const int rows = g.rows;
             const bool live = warp_row < rows;  // some row of this warp exists
             float m = ninf, l = 0.f;
+            int ref = 0;  // e4m3: O's exponent
             bool begun = false;
             {
                 // The last position that the row sees, and the first.
@@ -287,7 +292,18 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             __any_sync(0xFFFFFFFFu, clo > 0 || chi < kTile - 1) != 0;
                         // The loops below are kept rolled: all roles' code has to
                         // stay in the instruction caches.
-                        if (E4M3) c = row_c * ctl.k_scale[(tiles_before + k) & 3];
+                        int lift = 0;  // e4m3: the tile's values above O's exponent
+                        bool move = false;
+                        float keep_v = 1.f;
+                        if (E4M3) {
+                            c = row_c * ctl.k_scale[(tiles_before + k) & 3];
+                            const int top = ctl.v_top[(tiles_before + k) & 3];
+                            if ((move = moves(ref, top))) {
+                                keep_v = moved(ref, top);
+                                ref = top;
+                            }
+                            lift = top > 10 ? top - ref : 0;
+                        }
                         if (masked) {
 #pragma unroll 1
                             for (int x = 0; x < kTile; x += 16) {
@@ -305,8 +321,8 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         for (int x = 0; x < kTile; x += 32) mt = fmaxf(mt, tmem_ld_max(s_addr + x, v));
                         // (scale > 0; a NaN score is left out here and comes through below)
                         mt *= c;
-                        const bool grow = mt > m + slack(T()) || (!begun && mt > m);
-                        if (begun && __any_sync(0xFFFFFFFFu, grow)) {
+                        const bool grow = mt > m + slack<E4M3>() || (!begun && mt > m);
+                        if (begun && __any_sync(0xFFFFFFFFu, grow || move)) {
                             // The slot's products so far are complete: s_full's
                             // commit came after them.
                             const float keep = grow ? sv::ex2(m - mt) : 1.f;
@@ -315,14 +331,14 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                                 float o[16];
                                 tmem_ld(o_addr + 16 * x, o);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] *= keep;
+                                for (int i = 0; i < 16; ++i) o[i] *= keep * keep_v;
                                 tmem_st(o_addr + 16 * x, o);
                             }
                             l *= keep;
                         }
                         if (grow) m = mt;
                         begun = true;
-                        const float shift = m == ninf ? 0.f : -m;
+                        const float shift = (m == ninf ? 0.f : -m) + static_cast<float>(lift);
                         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
                         // The weights, the last 32 columns first: they take the
                         // columns of the upper half from the top.
@@ -337,15 +353,16 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                                 q = make_float2(sv::ex2(q.x), sv::ex2(q.y));
                                 l0 = add2(l0, p);
                                 l1 = add2(l1, q);
-                                w[i] = narrow2(p.x, p.y, T());
-                                w[i + 1] = narrow2(q.x, q.y, T());
+                                w[i] = narrow2(p.x, p.y, TP());
+                                w[i + 1] = narrow2(q.x, q.y, TP());
                             }
                             tmem_st(s_addr + 64 + x / 2, w);
                             if (x == 0) break;
                             x -= 32;
                             tmem_ld(s_addr + x, v);
                         }
-                        l += (l0.x + l0.y) + (l1.x + l1.y);
+                        const float sum = (l0.x + l0.y) + (l1.x + l1.y);
+                        l += E4M3 ? sum * exp_value(static_cast<uint32_t>(127 - lift)) : sum;
                         tmem_wait_st();
                         fence_before();
                     }
@@ -368,12 +385,14 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             }
             if (!(ok = wait_all(&ctl.o_full, item))) break;
             fence_after();
-            float w0 = 1.f, w1 = 0.f;
+            // O's true size: e4m3, its reference exponent.
+            const float size = E4M3 && ref != 0 ? exp_value(static_cast<uint32_t>(ref)) : 1.f;
+            float w0 = size, w1 = 0.f;
             if (!PAIR) {
                 // The slots exchange their rows' maxima and sums through the
                 // scores' columns, which the products have done with.
                 if (live) {
-                    tmem_st2(s_addr, m, l);
+                    tmem_st4(s_addr, m, l, size, 0.f);
                     tmem_wait_st();
                     fence_before();
                 }
@@ -382,16 +401,16 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                 if (!(ok = wait_all(&ctl.ml_ready, item))) break;
                 if (live) {
                     fence_after();
-                    float om, ol;
-                    tmem_ld2(lane_base + (1 - s) * 128, om, ol);
+                    float om, ol, osize, none;
+                    tmem_ld4(lane_base + (1 - s) * 128, om, ol, osize, none);
                     fence_before();
                     const float top = fmaxf(m, om);
                     const float wm = m == top ? 1.f : sv::ex2(m - top);
                     const float wo = om == top ? 1.f : sv::ex2(om - top);
-                    w0 = s ? wo : wm;
-                    w1 = s ? wm : wo;
                     // (the same order in both slots)
-                    l = (s ? ol : l) * w0 + (s ? l : ol) * w1;
+                    l = (s ? ol * wo : l * wm) + (s ? l * wm : ol * wo);
+                    w0 = s ? wo * osize : wm * size;
+                    w1 = s ? wm * size : wo * osize;
                     m = top;
                 }
                 __syncwarp();
@@ -421,7 +440,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                 constexpr int kCols = PAIR ? 64 : DP / 2;
                 const int64_t orow = (static_cast<int64_t>(g.q0) + token) * a.Hq + g.h * a.G +
                                      (r - token * a.G);
-                const float inv = bad ? nan : (whole ? 1.f / l : 1.f);
+                const float inv = bad ? nan : (whole ? 1.f / l : 1.f) * (PAIR ? size : 1.f);
                 float* part = share + static_cast<int64_t>(slot_row) * (DP + 4);
 #pragma unroll 1
                 for (int x = 0; x < (PAIR ? DP / 64 : 1); ++x) {
@@ -439,7 +458,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         // (slot 1 without a tile: its columns are read and not used)
                         tmem_ld(lane_base + 256 + k0, o, lane_base + 256 + DP + k0, p);
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i) o[i] = n > 1 ? o[i] * w0 + p[i] * w1 : o[i];
+                        for (int i = 0; i < kCols; ++i) o[i] = n > 1 ? o[i] * w0 + p[i] * w1 : o[i] * w0;
                     }
                     if (!valid || again) continue;
 #pragma unroll
@@ -496,8 +515,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         // Products of slot s: the warp stays together, one lane issues. It
         // passes every tile in ring order, its own and the other slot's.
         // ------------------------------------------------------------------
-        using TS = typename std::conditional<E4M3, F16, T>::type;
-        constexpr uint32_t id_s = idesc<TS, kTile, false>(), id_o = idesc<T, DP, true>();
+        constexpr uint32_t id_s = idesc<TP, kTile, false>(), id_o = idesc<TP, DP, true>();
         const int s = warp == 8 ? 0 : 1;
         const uint64_t dq = smem_desc(sq + (PAIR ? s * (128 * DP * 2) : 0), 16, 1024);
         const uint64_t dk = smem_desc(st, 16, args.group), dv = smem_desc(st, args.panel, args.group);
@@ -667,7 +685,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const uint32_t raw = sr + raw_at.stage * X::kRawBytes;
                     const uint32_t dst = st + at.stage * X::kTileBytes;
                     // A thread expands 16 codes of a row, the same piece of every
-                    // kStep-th row, two at a time. Eight neighbouring lanes take half of the
+                    // kStep-th row, four at a time. Eight neighbouring lanes take half of the
                     // pieces of two rows, the other half of the second: their
                     // 16-byte columns differ in the loads and, swizzled, in the
                     // stores.
@@ -679,50 +697,33 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const uint32_t from = raw + row0 * a.c.D + (in_row ? piece * 16 : 0);
                     const uint32_t to = dst + tile_chunk(row0, piece * 2, 1024, X::kPanel);
                     const uint32_t* factor = &ctl.factor[raw_at.stage][row0];
-                    if (!is_v && tid == 0) ctl.k_scale[k_tiles & 3] = exp_value(ctl.top[raw_at.stage]);
-                    constexpr int kBatch = 2;
-                    auto expand_rows = [&](auto type) {
-                        using U = decltype(type);
+                    if (!is_v && tid == 0) {
+                        const uint2 top = ctl.top[raw_at.stage];
+                        ctl.k_scale[k_tiles & 3] = exp_value(top.x);
+                        ctl.v_top[k_tiles & 3] = static_cast<int>(top.y);
+                    }
+                    constexpr int kBatch = kTile / kStep < 4 ? kTile / kStep : 4;
 #pragma unroll 1
-                        for (int r = 0; r < kTile; r += kBatch * kStep) {
-                            uint4 codes[kBatch];
-                            uint32_t f[kBatch];
+                    for (int r = 0; r < kTile; r += kBatch * kStep) {
+                        uint4 codes[kBatch];
+                        uint32_t f[kBatch];
 #pragma unroll
-                            for (int u = 0; u < kBatch; ++u) {
-                                const int row = r + u * kStep;
-                                codes[u] = ld_shared_v4(from + row * a.c.D);
-                                f[u] = in_row ? factor[row] : 0u;
-                            }
+                        for (int u = 0; u < kBatch; ++u) {
+                            const int row = r + u * kStep;
+                            codes[u] = ld_shared_v4(from + row * a.c.D);
+                            f[u] = in_row ? factor[row] : 0u;
+                        }
 #pragma unroll
-                            for (int u = 0; u < kBatch; ++u) {
-                                // (a factor of zero: whatever the codes are)
-                                if (f[u] == 0u) codes[u] = make_uint4(0, 0, 0, 0);
-                                uint32_t o[8];
-                                expand<U>(codes[u], f[u], o);
-                                // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
-                                const uint32_t t = to + (r + u * kStep) * 128;
-                                st_shared_v4(t, make_uint4(o[0], o[1], o[2], o[3]));
-                                st_shared_v4(t ^ 16u, make_uint4(o[4], o[5], o[6], o[7]));
-                            }
+                        for (int u = 0; u < kBatch; ++u) {
+                            // (a factor of zero: whatever the codes are)
+                            if (f[u] == 0u) codes[u] = make_uint4(0, 0, 0, 0);
+                            uint32_t o[8];
+                            expand(codes[u], f[u], o);
+                            // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
+                            const uint32_t t = to + (r + u * kStep) * 128;
+                            st_shared_v4(t, make_uint4(o[0], o[1], o[2], o[3]));
+                            st_shared_v4(t ^ 16u, make_uint4(o[4], o[5], o[6], o[7]));
                         }
-                    };
-                    if (is_v) {
-                        expand_rows(T());
-                        if (ctl.two[raw_at.stage] != 0) {
-                            // Rare: some rows' second factor.
-#pragma unroll 1
-                            for (int r = 0; r < 2 * kTile; r += kStep) {
-                                const uint32_t t = (to + (r >> 1) / kStep * kStep * 128) ^ ((r / kStep & 1) << 4);
-                                const uint32_t f2 =
-                                    factor_of(ctl.exps[raw_at.stage][row0 + (r >> 1) / kStep * kStep], T()).f2;
-                                uint4 x = ld_shared_v4(t);
-                                x = make_uint4(mul2(x.x, f2, T()), mul2(x.y, f2, T()),
-                                               mul2(x.z, f2, T()), mul2(x.w, f2, T()));
-                                st_shared_v4(t, x);
-                            }
-                        }
-                    } else {
-                        expand_rows(F16());
                     }
                     if (!is_v) ++k_tiles;
                     fence_async_smem();

@@ -289,17 +289,18 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&r)[16])
           "f"(r[14]), "f"(r[15]), "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld2(uint32_t addr, float& x, float& y)
+__device__ __forceinline__ void tmem_ld4(uint32_t addr, float& a, float& b, float& c, float& d)
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2]; tcgen05.wait::ld.sync.aligned;"
-        : "=f"(x), "=f"(y)
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4]; tcgen05.wait::ld.sync.aligned;"
+        : "=f"(a), "=f"(b), "=f"(c), "=f"(d)
         : "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st2(uint32_t addr, float x, float y)
+__device__ __forceinline__ void tmem_st4(uint32_t addr, float a, float b, float c, float d)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%2], {%0, %1};" ::"f"(x), "f"(y), "r"(addr)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"f"(a), "f"(b),
+                 "f"(c), "f"(d), "r"(addr)
                  : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st()

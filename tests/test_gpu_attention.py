@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import speculative_decoding_verification_66_gb300 as sv
-from attention_util import Cache, check, reference
+from attention_util import Cache, check, quantise, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -134,7 +134,6 @@ def test_masked_values_have_no_influence(dtype, e4m3, bad, lens, T, at, window):
     c.parts[0][c.pages_of[0][at // 16], at % 16, :, 3] = bad
     c.parts[1][c.pages_of[0][at // 16], at % 16, 1, 7] = bad
     if e4m3:
-        from attention_util import quantise
         c.e4m3 = True
         for i in range(2):
             code, c.exps[i] = quantise(c.parts[i])
@@ -186,6 +185,31 @@ def test_extreme_scores(dtype, e4m3, T):
         q = torch.full((T, 4, 64), 1.5, dtype=c.dtype, device="cuda")
         out, lse = attend(c, q, max_chunk=T)
         check(out, lse, c, q, 0.125)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [1, 5, 60])
+@pytest.mark.parametrize("kind", ["drift", "steps", "apart", "zeros"])
+def test_e4m3_exponents(dtype, T, kind):
+    """Keys and values whose sizes drift along the sequence, change between tiles, lie far apart
+    within a tile, or are all zero for long stretches."""
+    n = 900 + T
+    c = Cache([900, 40], [T, T], 2, 128, 16, dtype, False, seed=4)
+    p = torch.arange(n, device="cuda")
+    size = {"drift": torch.exp2(p / 60.0 - 8.0),
+            "steps": torch.exp2(((p // 150) % 3 - 1) * 5.0),
+            "apart": torch.exp2(-(p % 3) * 8.0),
+            "zeros": ((p // 200) % 2).double()}[kind]
+    page, slot = c.table[0].long()[p // 16], p % 16
+    for i in range(2):
+        x = c.parts[i][page, slot].double() * size[:, None, None]
+        c.parts[i][page, slot] = x.to(c.dtype)
+        c.parts[i], c.exps[i] = (lambda q: (q[0].view(torch.float8_e4m3fn), q[1]))(
+            quantise(c.parts[i]))
+    c.e4m3 = True
+    q = make_query(c, 4, 9, spread=0.02 if kind == "drift" else 1.0)
+    out, lse = attend(c, q, max_chunk=T)
+    check(out, lse, c, q, 128 ** -0.5)
 
 
 @pytest.mark.parametrize("T", [1, 5, 80])
