@@ -169,7 +169,12 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
 // Four codes to two words of float16.
 __device__ __forceinline__ uint2 spread(uint32_t w)
 {
-    return make_uint2(e4m3_to_f16x2(w & 0xFFFFu), e4m3_to_f16x2(w >> 16));
+    uint2 r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(r.x), "=r"(r.y)
+        : "r"(w));
+    return r;
 }
 // The factor of a vector's codes, in both halves.
 __device__ __forceinline__ uint32_t code_factor(uint32_t e, uint32_t top)
@@ -391,6 +396,7 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
     const bool first_of_box = P >= kTile ? lane == 0 : ((lane * 4) & (P - 1)) == 0;
     const uint8_t* exps = kv ? a.c.exps[1] : a.c.exps[0];
     const int64_t exp_step = kv ? a.c.exp_slot_stride[1] : a.c.exp_slot_stride[0];
+    const int64_t exp_page = kv ? a.c.exp_page_stride[1] : a.c.exp_page_stride[0];
     Place<FILL> base_at;
     uint32_t used = 0, rounds = 0;  // a stage's bit: filled by this warp; parity of the last fill
     Walk<R> walk(a, start);
@@ -452,15 +458,18 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
         struct Exps {
             uint32_t e[4], v[4];  // (v: the values', loaded with the keys)
         };
+        const uint8_t* exps_h = exps + (kv ? h * a.c.exp_head_stride[1] : h * a.c.exp_head_stride[0]);
+        const uint8_t* v_exps_h = a.c.exps[1] + h * a.c.exp_head_stride[1];
         auto exps_of = [&](int k, int32_t page) {
             Exps x{};
             if (E4M3 && page != INT_MIN) {
-                const uint8_t* e = exps + exp_at(a.c, kv, good(page) ? page : 0, slot_of(k), h);
+                const int64_t pg = good(page) ? page : 0, slot = slot_of(k);
+                const uint8_t* e = exps_h + pg * exp_page + slot * exp_step;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x.e[i] = e[i * exp_step];
                 if (kv == 0) {
-                    const uint8_t* v =
-                        a.c.exps[1] + exp_at(a.c, 1, good(page) ? page : 0, slot_of(k), h);
+                    const uint8_t* v = v_exps_h + pg * a.c.exp_page_stride[1] +
+                                       slot * a.c.exp_slot_stride[1];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x.v[i] = v[i * a.c.exp_slot_stride[1]];
                 }

@@ -702,6 +702,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         ctl.k_scale[k_tiles & 3] = exp_value(top.x);
                         ctl.v_top[k_tiles & 3] = static_cast<int>(top.y);
                     }
+                    const bool ragged = k < inner_lo || k > inner_hi;
                     constexpr int kBatch = kTile / kStep < 4 ? kTile / kStep : 4;
 #pragma unroll 1
                     for (int r = 0; r < kTile; r += kBatch * kStep) {
@@ -715,8 +716,8 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         }
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
-                            // (a factor of zero: whatever the codes are)
-                            if (f[u] == 0u) codes[u] = make_uint4(0, 0, 0, 0);
+                            // (a factor of zero: hidden, whatever the codes are)
+                            if (ragged && f[u] == 0u) codes[u] = make_uint4(0, 0, 0, 0);
                             uint32_t o[8];
                             expand(codes[u], f[u], o);
                             // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
