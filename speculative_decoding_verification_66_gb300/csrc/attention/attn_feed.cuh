@@ -17,11 +17,11 @@ namespace {
 
 // Powers of two by which a weight may pass 1 before the outputs are rescaled:
 // float16 weights stay below 65504 (e4m3 caches: also after a tile's exponent,
-// see kLift), float32 sums of products with bfloat16's largest values finite.
-template <bool E4M3>
+// see kLift); bfloat16 weights leave float32 sums room for values up to 2^90.
+template <class T, bool E4M3>
 __device__ __forceinline__ float slack()
 {
-    return E4M3 ? 8.f : 14.f;
+    return E4M3 ? 8.f : std::is_same<T, F16>::value ? 14.f : 30.f;
 }
 // e4m3: the weights carry the power of two between their tile's values and the
 // outputs' reference, which follows the tiles when it is more than kLift above

@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     const float(&x)[2][4] = s[i >> 1];
                     const int z = 2 * (i & 1);
                     top[i] = fmaxf(fmaxf(x[0][z], x[0][z + 1]), fmaxf(x[1][z], x[1][z + 1])) * cs[i];
-                    grow |= top[i] > m[i] + slack<E4M3>();
+                    grow |= top[i] > m[i] + slack<T, E4M3>();
                 }
                 if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         float x = top[i];
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                        if (x > m[i] + slack<E4M3>()) {
+                        if (x > m[i] + slack<T, E4M3>()) {
                             const float keep = sv::ex2(m[i] - x);
                             l[i] *= keep;
 #pragma unroll

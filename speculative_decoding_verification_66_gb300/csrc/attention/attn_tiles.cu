@@ -193,6 +193,11 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         // ------------------------------------------------------------------
         if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kRegsRow));
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        // Columns of scores in registers at a time: 64 wait for fewer loads, and
+        // where every row exists that counts (a 2048-token piece: 210 us against
+        // 229); e4m3 has more code to keep in the instruction caches and fewer
+        // registers (256 x 9: 738 us against 1075 with 64).
+        constexpr bool kWide = !E4M3;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t s_addr = lane_base + s * 128, o_addr = lane_base + 256 + s * DP;
         const float ninf = __uint_as_float(sv::kF32NegInfBits);
@@ -316,12 +321,15 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             }
                             tmem_wait_st();
                         }
-                        float v[32], mt = ninf;
+                        // 32 or (kWide) 64 columns at a time.
+                        float v[32], v2[32], mt = ninf;
 #pragma unroll 1
-                        for (int x = 0; x < kTile; x += 32) mt = fmaxf(mt, tmem_ld_max(s_addr + x, v));
+                        for (int x = 0; x < kTile; x += kWide ? 64 : 32)
+                            mt = fmaxf(mt, kWide ? tmem_ld_max(s_addr + x, v, s_addr + x + 32, v2)
+                                                 : tmem_ld_max(s_addr + x, v));
                         // (scale > 0; a NaN score is left out here and comes through below)
                         mt *= c;
-                        const bool grow = mt > m + slack<E4M3>() || (!begun && mt > m);
+                        const bool grow = mt > m + slack<T, E4M3>() || (!begun && mt > m);
                         if (begun && __any_sync(0xFFFFFFFFu, grow || move)) {
                             // The slot's products so far are complete: s_full's
                             // commit came after them.
@@ -340,15 +348,12 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         begun = true;
                         const float shift = (m == ninf ? 0.f : -m) + static_cast<float>(lift);
                         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-                        // The weights, the last 32 columns first: they take the
-                        // columns of the upper half from the top.
-#pragma unroll 1
-                        for (int x = kTile - 32;;) {
+                        auto weigh = [&](const float (&y)[32], int x) {
                             uint32_t w[16];
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                float2 p = fma2(make_float2(v[2 * i], v[2 * i + 1]), c, shift);
-                                float2 q = fma2(make_float2(v[2 * i + 2], v[2 * i + 3]), c, shift);
+                                float2 p = fma2(make_float2(y[2 * i], y[2 * i + 1]), c, shift);
+                                float2 q = fma2(make_float2(y[2 * i + 2], y[2 * i + 3]), c, shift);
                                 p = make_float2(sv::ex2(p.x), sv::ex2(p.y));
                                 q = make_float2(sv::ex2(q.x), sv::ex2(q.y));
                                 l0 = add2(l0, p);
@@ -357,9 +362,19 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                                 w[i + 1] = narrow2(q.x, q.y, TP());
                             }
                             tmem_st(s_addr + 64 + x / 2, w);
+                        };
+                        // The weights, the last columns first: they take the columns
+                        // of the upper half from the top.
+#pragma unroll 1
+                        for (int x = kTile - (kWide ? 64 : 32);;) {
+                            weigh(v, x);
+                            if (kWide) weigh(v2, x + 32);
                             if (x == 0) break;
-                            x -= 32;
-                            tmem_ld(s_addr + x, v);
+                            x -= kWide ? 64 : 32;
+                            if (kWide)
+                                tmem_ld(s_addr + x, v, s_addr + x + 32, v2);
+                            else
+                                tmem_ld(s_addr + x, v);
                         }
                         const float sum = (l0.x + l0.y) + (l1.x + l1.y);
                         l += E4M3 ? sum * exp_value(static_cast<uint32_t>(127 - lift)) : sum;
@@ -551,13 +566,13 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     // already their scores follow at once: looking at a barrier
                     // between the two would let the tensor core run dry.
                     keys.advance(1);
-                    for (int x = 0; x < 2; ++x) {
-                        if (left > 0 && !scores)
-                            scores = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.full[keys.stage],
-                                                                       keys.round & 1u));
-                        if (x == 0 && !(ok = wait_all(&ctl.p_ready[s], tiles))) break;
-                    }
-                    if (!ok) break;
+                    auto keys_here = [&] {
+                        return __all_sync(0xFFFFFFFFu,
+                                          mbar_test(&ctl.full[keys.stage], keys.round & 1u)) != 0;
+                    };
+                    if (left > 0) scores = keys_here();
+                    if (!(ok = wait_all(&ctl.p_ready[s], tiles))) break;
+                    if (left > 0 && !scores) scores = keys_here();
                     ++tiles;
                     if (PAIR) {
                         // One slot's products after the other's: side by side both
