@@ -15,19 +15,28 @@
 namespace sva {
 namespace {
 
-// Powers of two by which a weight may pass 1 before the outputs are rescaled:
-// float16 weights stay below 65504 (e4m3 caches: also after a tile's exponent,
-// see kLift); bfloat16 weights leave float32 sums room for values up to 2^90.
+// The outputs are rescaled when a weight would pass 2^slack(); the largest weight
+// is then 2^rise(). float16 weights stay below 65504 (e4m3 caches: also after a
+// tile's exponent, see kLift) and start well above 1: what is lost below their
+// least step 2^-24, for each of many keys in the same direction, is 2^-32 of the
+// largest weight (e4m3: 2^-27; with a start at 1 and tiles 2^6 below the
+// reference 131072 keys of 2^-19.5 would vanish, a seventh of the sum). bfloat16
+// has float32's range; slack 30 leaves sums room for values up to 2^90.
 template <class T, bool E4M3>
 __device__ __forceinline__ float slack()
 {
     return E4M3 ? 8.f : std::is_same<T, F16>::value ? 14.f : 30.f;
 }
+template <class T, bool E4M3>
+__device__ __forceinline__ float rise()
+{
+    return E4M3 ? 4.f : std::is_same<T, F16>::value ? 7.f : 0.f;
+}
 // e4m3: the weights carry the power of two between their tile's values and the
-// outputs' reference, which follows the tiles when it is more than kLift above
+// outputs' reference, which follows the tiles when they are more than kLift above
 // or kSink below.
-constexpr int kLift = 7, kSink = 6;
-// Values of one tile may be this many powers of two apart (see key_factor).
+constexpr int kLift = 7, kSink = 2;
+// Values of one tile may be this many powers of two apart (see code_factor).
 constexpr int kSpread = 13;
 
 constexpr int kMaxBlocks = 160;  // shares in the workspace; grids are no larger

@@ -28,17 +28,16 @@ namespace {
 
 constexpr int kWorkers = 8;
 constexpr int kFewThreads = (kWorkers + 2) * 32;
-constexpr int MT = 1;  // blocks of 16 rows
 
 template <int DP, bool E4M3>
 struct FewShape {
-    static constexpr int kRows = 16 * MT;
+    static constexpr int kRows = 16;
     static constexpr int kTileBytes = kTile * DP * (E4M3 ? 1 : 2);
     // Up to 192 KB of tiles.
     static constexpr int kMost = E4M3 ? 10 : 12;
     static constexpr int kStages = 196608 / kTileBytes < kMost ? 196608 / kTileBytes : kMost;
     static constexpr int kSteps = DP / 16;                  // products along d
-    static constexpr int kQBytes = MT * kSteps * 32 * 16;   // operands as the lanes hold them
+    static constexpr int kQBytes = kSteps * 32 * 16;        // operands as the lanes hold them
     static constexpr int kJoin = 32;                        // columns joined at a time
     static constexpr int kJoinBytes = kWorkers * kRows * kJoin * 4;
     static constexpr int kBytes = kStages * kTileBytes + kQBytes + kJoinBytes;
@@ -55,8 +54,8 @@ struct FewControl {
     int noted[kItems];
     int note[kItems][kNoted];
     int bad_page[kItems];
-    float2 ml[kWorkers][16 * MT];
-    float q_scale[16 * MT];
+    float2 ml[kWorkers][16];
+    float q_scale[16];
     // e4m3, for every stage: the keys' powers of two, or the values' factors as
     // halves; the largest exponents of its keys and of the values that belong to
     // them.
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         // The queries' operands, as the lanes will hold them: step w by warp w.
         // Fetched into registers while a segment's results are joined, stored after.
         constexpr bool kScaled = E4M3 && std::is_same<T, Bf16>::value;
-        static_assert(X::kSteps <= kWorkers && MT == 1, "a step a warp");
+        static_assert(X::kSteps <= kWorkers, "a step a warp");
         uint2 qv[2];       // rows g, g + 8
         uint2 qrow[2];     // kScaled: elements 4 lane .. of rows warp, warp + 8
         auto fetch = [&](const Plan& p) {
@@ -232,10 +231,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (!(ok = store())) break;
 
             // This thread's rows: g + 8 i.
-            int pos[2 * MT], low[2 * MT];
-            float cs[2 * MT], m[2 * MT], l[2 * MT];
+            int pos[2], low[2];
+            float cs[2], m[2], l[2];
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 const int r = min(g + 8 * i, rows - 1);
                 pos[i] = p.cached + (p.row0 + r) / a.G;
                 low[i] = a.window > 0 ? pos[i] - static_cast<int>(a.window) + 1 : INT_MIN / 2;
@@ -244,13 +243,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 m[i] = ninf;
                 l[i] = 0.f;
             }
-            float o[MT][DP / 8][4];
+            float o[DP / 8][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int j = 0; j < DP / 8; ++j)
 #pragma unroll
-                for (int j = 0; j < DP / 8; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.f;
+                for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
 
             int ref = 0;  // e4m3: the outputs' exponent
             for (int k = 0; k < n; ++k) {
@@ -259,21 +256,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 // ---- scores: two products of eight keys side by side
                 if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
                 const uint32_t kt = st + at.stage * X::kTileBytes;
-                float s[MT][2][4];
+                float s[2][4];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[mt][t][i] = 0.f;
+                    for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
                 auto scores = [&](int step, const uint32_t (&b)[4]) {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const uint4 q = ld_shared_v4(sq + ((mt * X::kSteps + step) * 32 + lane) * 16);
-                        const uint32_t f[4] = {q.x, q.y, q.z, q.w};
-                        mma16816(s[mt][0], f, b[0], b[1], TP());
-                        mma16816(s[mt][1], f, b[2], b[3], TP());
-                    }
+                    const uint4 q = ld_shared_v4(sq + (step * 32 + lane) * 16);
+                    const uint32_t f[4] = {q.x, q.y, q.z, q.w};
+                    mma16816(s[0], f, b[0], b[1], TP());
+                    mma16816(s[1], f, b[2], b[3], TP());
                 };
                 if constexpr (E4M3) {
 #pragma unroll
@@ -299,13 +291,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     for (int t = 0; t < 2; ++t) {
                         const float2 e = *reinterpret_cast<const float2*>(
                             &ctl.scale[at.stage][key0 + 8 * t + 2 * c4]);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            s[mt][t][0] *= e.x;
-                            s[mt][t][1] *= e.y;
-                            s[mt][t][2] *= e.x;
-                            s[mt][t][3] *= e.y;
-                        }
+                        s[t][0] *= e.x;
+                        s[t][1] *= e.y;
+                        s[t][2] *= e.x;
+                        s[t][3] *= e.y;
                     }
                 } else {
                     const int row = key0 + (lane & 7) + ((lane >> 4) << 3);
@@ -328,11 +317,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     if (moves(ref, v_top)) {
                         const float keep = moved(ref, v_top);
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
+                        for (int j = 0; j < DP / 8; ++j)
 #pragma unroll
-                            for (int j = 0; j < DP / 8; ++j)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) o[mt][j][i] *= keep;
+                            for (int i = 0; i < 4; ++i) o[j][i] *= keep;
                         ref = v_top;
                     }
                     lift = v_top > 10 ? v_top - ref : 0;
@@ -344,50 +331,47 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int x = k * kTile + key0 + 8 * t + 2 * c4 + i;
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                if (x < low[2 * mt] || x > pos[2 * mt]) s[mt][t][i] = ninf;
-                                if (x < low[2 * mt + 1] || x > pos[2 * mt + 1]) s[mt][t][2 + i] = ninf;
-                            }
+                            if (x < low[0] || x > pos[0]) s[t][i] = ninf;
+                            if (x < low[1] || x > pos[1]) s[t][2 + i] = ninf;
                         }
                 }
                 bool grow = false;
-                float top[2 * MT];
+                float top[2];
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
-                    const float(&x)[2][4] = s[i >> 1];
-                    const int z = 2 * (i & 1);
-                    top[i] = fmaxf(fmaxf(x[0][z], x[0][z + 1]), fmaxf(x[1][z], x[1][z + 1])) * cs[i];
+                for (int i = 0; i < 2; ++i) {
+                    const int z = 2 * i;
+                    top[i] = fmaxf(fmaxf(s[0][z], s[0][z + 1]), fmaxf(s[1][z], s[1][z + 1])) * cs[i];
                     grow |= top[i] > m[i] + slack<T, E4M3>();
                 }
                 if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
-                    for (int i = 0; i < 2 * MT; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         float x = top[i];
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
                         if (x > m[i] + slack<T, E4M3>()) {
+                            x -= rise<T, E4M3>();
                             const float keep = sv::ex2(m[i] - x);
                             l[i] *= keep;
 #pragma unroll
                             for (int j = 0; j < DP / 8; ++j) {
-                                o[i >> 1][j][2 * (i & 1)] *= keep;
-                                o[i >> 1][j][2 * (i & 1) + 1] *= keep;
+                                o[j][2 * i] *= keep;
+                                o[j][2 * i + 1] *= keep;
                             }
                             m[i] = x;
                         }
                     }
                 }
-                uint32_t w[MT][4];
+                uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     const float shift = (m[i] == ninf ? 0.f : -m[i]) + static_cast<float>(lift);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const float p0 = sv::ex2(fmaf(s[i >> 1][t][2 * (i & 1)], cs[i], shift));
-                        const float p1 = sv::ex2(fmaf(s[i >> 1][t][2 * (i & 1) + 1], cs[i], shift));
+                        const float p0 = sv::ex2(fmaf(s[t][2 * i], cs[i], shift));
+                        const float p1 = sv::ex2(fmaf(s[t][2 * i + 1], cs[i], shift));
                         l[i] = E4M3 ? fmaf(p0 + p1, drop, l[i]) : l[i] + (p0 + p1);
-                        w[i >> 1][2 * t + (i & 1)] = narrow2(p0, p1, TP());
+                        w[2 * t + i] = narrow2(p0, p1, TP());
                     }
                 }
                 // ---- values
@@ -430,11 +414,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                             const uint2 y = spread(__byte_perm(codes[2][i], codes[3][i], sel));
                             const uint32_t x0 = mul2(x.x, f01), x1 = mul2(x.y, f01);
                             const uint32_t y0 = mul2(y.x, f23), y1 = mul2(y.y, f23);
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                mma16816(o[mt][4 * i + 2 * hi], w[mt], x0, y0, TP());
-                                mma16816(o[mt][4 * i + 2 * hi + 1], w[mt], x1, y1, TP());
-                            }
+                            mma16816(o[4 * i + 2 * hi], w, x0, y0, TP());
+                            mma16816(o[4 * i + 2 * hi + 1], w, x1, y1, TP());
                         }
                     }
                 } else {
@@ -469,11 +450,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     for (int j = 0; j < DP / 16; ++j) {
                         uint32_t b[4];
                         ldmatrix4_trans(from + (j >> 2) * args.panel + (((2 * (j & 3)) ^ y) << 4), b);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            mma16816(o[mt][2 * j], w[mt], b[0], b[1], TP());
-                            mma16816(o[mt][2 * j + 1], w[mt], b[2], b[3], TP());
-                        }
+                        mma16816(o[2 * j], w, b[0], b[1], TP());
+                        mma16816(o[2 * j + 1], w, b[2], b[3], TP());
                     }
                 }
                 __syncwarp();
@@ -486,7 +464,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             plan = plan_at(ctl, item + 1, wait_all);
             if (plan != nullptr) fetch(*plan);
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
                 if (c4 == 0) ctl.ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
@@ -561,14 +539,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             for (int j0 = 0; j0 < DP / 8; j0 += kStepsJ) {
                 if (!once && j0 > 0 && !(ok = meet())) break;
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     if (g + 8 * i >= rows) continue;
                     float* to = join + (warp * rows + g + 8 * i) * width + 2 * c4 + (once ? 8 * j0 : 0);
 #pragma unroll
                     for (int j = 0; j < kStepsJ; ++j)
                         *reinterpret_cast<float2*>(to + j * 8) =
-                            make_float2(o[i >> 1][j0 + j][2 * (i & 1)] * size,
-                                        o[i >> 1][j0 + j][2 * (i & 1) + 1] * size);
+                            make_float2(o[j0 + j][2 * i] * size,
+                                        o[j0 + j][2 * i + 1] * size);
                 }
                 if (!once) {
                     if (!(ok = meet())) break;

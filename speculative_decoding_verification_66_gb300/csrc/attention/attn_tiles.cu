@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         if (begun && __any_sync(0xFFFFFFFFu, grow || move)) {
                             // The slot's products so far are complete: s_full's
                             // commit came after them.
-                            const float keep = grow ? sv::ex2(m - mt) : 1.f;
+                            const float keep = grow ? sv::ex2(m - (mt - rise<T, E4M3>())) : 1.f;
 #pragma unroll 1
                             for (int x = 0; x < DP / 16; ++x) {
                                 float o[16];
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             }
                             l *= keep;
                         }
-                        if (grow) m = mt;
+                        if (grow) m = mt - rise<T, E4M3>();
                         begun = true;
                         const float shift = (m == ninf ? 0.f : -m) + static_cast<float>(lift);
                         float2 l0 = make_float2(0.f, 0.f), l1 = l0;

@@ -428,3 +428,35 @@ def test_refusals():
                dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(sv.SpecVerifyError):
             sv.sv_chunk_attention(q, *c.args(), **kw)
+
+
+@pytest.mark.parametrize("dtype,e4m3", TYPES)
+@pytest.mark.parametrize("T", [1, 8, 40])
+def test_many_small_weights_add_up(dtype, e4m3, T):
+    """One key takes most of the weight, 60000 others 2^-18.75 of it each and a seventh of the sum
+    together, the first tile's values 2^6 times the others'. 160 sequences on the same pages, so
+    that blocks work through whole ones."""
+    n, B = 60000, 160
+    c = Cache([n], [T], 1, 64, 64, dtype, False)
+    k = torch.zeros(c.parts[0].shape, dtype=c.dtype, device="cuda")
+    v = torch.ones_like(k)
+    p = torch.arange(128, device="cuda")
+    page, slot = c.table[0].long()[p // 64], p % 64
+    v[page, slot] = 64.0
+    k[page[0], 0], v[page[0], 0] = 1.625, 0.0  # scores 0.125 * 64 * 1.625 = 13, and 0
+    c.parts = [k, v]
+    if e4m3:
+        (kc, ke), (vc, ve) = quantise(k), quantise(v)
+        c.parts = [kc.view(torch.float8_e4m3fn), vc.view(torch.float8_e4m3fn)]
+        c.exps, c.e4m3 = [ke, ve], True
+    q = torch.ones(T, 4, 64, dtype=c.dtype, device="cuda")
+    ref, z, tol, tol_z = reference(c, q, 0.125)
+    out, lse = sv.sv_chunk_attention(
+        q.repeat(B, 1, 1), *c.parts, c.table.repeat(B, 1), c.cached.repeat(B),
+        torch.arange(0, B * T + 1, T, dtype=torch.int32, device="cuda"), **c.exp_args(),
+        scale=0.125, max_chunk=T, return_lse=True)
+    # (float16 weights keep 2^-27 of the largest at least, whatever the tile's values)
+    tol = tol - 2.0 ** -24 * (n + T + 127 * 64) + 2.0 ** -27 * (n + T + 127 * 64)
+    err = (out.view(B, T, 4, 64).double() - ref).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+    assert ((lse.view(B, T, 4).double() - z).abs() <= tol_z).all()
