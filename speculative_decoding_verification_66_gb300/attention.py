@@ -78,8 +78,8 @@ def _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps, v_ex
     if len(table) != 2 or table[0] != B or page_table.dtype != i32 or page_table.device != dev:
         raise ValueError("page_table must be int32 [B, max_pages]")
     row, step = page_table.stride()
-    if step != 1 and table[1] > 1:
-        raise ValueError("page_table's rows must be contiguous")
+    if (step != 1 and table[1] > 1) or (B > 1 and row < table[1]):
+        raise ValueError("page_table's rows must be contiguous and must not overlap")
     if chunk_starts.shape != (B + 1,) or chunk_starts.dtype != i32 \
             or not chunk_starts.is_contiguous() or chunk_starts.device != dev:
         raise ValueError("chunk_starts must be contiguous int32 [B + 1]")

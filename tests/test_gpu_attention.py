@@ -460,3 +460,14 @@ def test_many_small_weights_add_up(dtype, e4m3, T):
     err = (out.view(B, T, 4, 64).double() - ref).abs()
     assert (err <= tol).all(), float((err / tol).max())
     assert ((lse.view(B, T, 4).double() - z).abs() <= tol_z).all()
+
+
+def test_page_tables_that_overlap_are_refused():
+    c = Cache([4, 4], [2, 2], 2, 64, 8)
+    q = make_query(c, 4, 1)
+    k, v, table, cached, starts = c.args()
+    with pytest.raises(ValueError):
+        sv.sv_chunk_attention(q, k, v, table[:1].expand(2, -1), cached, starts)
+    # (one row has no distance to a next)
+    out = sv.sv_chunk_attention(q[:2], k, v, table[:1].expand(1, -1), cached[:1], starts[:2])
+    assert out.isfinite().all()
