@@ -10,7 +10,6 @@
 namespace {
 
 constexpr int64_t kMax31 = int64_t(1) << 31;
-constexpr int64_t kMaxTileDim = 128;  // the tile kernel's largest head size
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -187,8 +186,7 @@ SV_EXPORT int sv_chunk_attention_workspace_bytes(int64_t batch, int64_t tokens, 
     if (bytes == nullptr) return SV_ERR_ARG;
     const int rc = check_attention(batch, tokens, q_heads, kv_heads, head_dim, &max_chunk);
     if (rc != SV_OK) return rc;
-    *bytes = head_dim <= kMaxTileDim ? sva::tiles_workspace(max_chunk, q_heads / kv_heads, head_dim)
-                                     : 256;
+    *bytes = sva::tiles_workspace(max_chunk, q_heads / kv_heads, head_dim);
     return SV_OK;
 }
 
@@ -235,9 +233,9 @@ SV_EXPORT int sv_chunk_attention(const sv_paged_cache* cache, const void* query,
     a.scale_log2 = scale * 1.44269504088896341f;
     const bool f16 = dtype == SV_F16, e4m3 = cache->dtype == SV_E4M3;
     bool done = false;
-    if (a.c.D <= kMaxTileDim && a.c.num_pages > 0) {
-        const auto launch = max_chunk * a.G <= sva::kFewRows ? sva::launch_attention_few
-                                                             : sva::launch_attention_tiles;
+    if (a.c.num_pages > 0) {
+        const bool few = max_chunk * a.G <= sva::kFewRows || a.c.D > sva::kMaxTileDim;
+        const auto launch = few ? sva::launch_attention_few : sva::launch_attention_tiles;
         if (launch(a, f16, e4m3, workspace, s, &done) != cudaSuccess) return SV_ERR_CUDA;
     }
     if (!done && sva::launch_attention_rows(a, f16, e4m3, s) != cudaSuccess) return SV_ERR_CUDA;

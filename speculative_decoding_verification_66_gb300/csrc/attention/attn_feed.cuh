@@ -79,7 +79,7 @@ constexpr size_t kShareBytes = (sizeof(Share) * kMaxBlocks + 255) / 256 * 256;
 template <int DP>
 __device__ __forceinline__ int few_swizzle(int row, int ch, int swizzled)
 {
-    return swizzled ? (DP == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) : ch;
+    return DP <= 128 && swizzled ? (DP == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) : ch;
 }
 
 // Where the tiles of a segment lie in the ring: the order in which the products

@@ -163,33 +163,41 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         // The queries' operands, as the lanes will hold them: step w by warp w.
         // Fetched into registers while a segment's results are joined, stored after.
         constexpr bool kScaled = E4M3 && std::is_same<T, Bf16>::value;
-        static_assert(X::kSteps <= kWorkers, "a step a warp");
-        uint2 qv[2];       // rows g, g + 8
-        uint2 qrow[2];     // kScaled: elements 4 lane .. of rows warp, warp + 8
+        constexpr int kPer = (X::kSteps + kWorkers - 1) / kWorkers;  // steps of a warp
+        uint2 qv[kPer][2];    // rows g, g + 8
+        uint2 qrow[kPer][2];  // kScaled: elements 4 lane .. (and from 128 on) of rows warp, warp + 8
         auto fetch = [&](const Plan& p) {
             if (kScaled) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int r = warp + 8 * i;
-                    qrow[i] = make_uint2(0, 0);
-                    if (r < p.rows && lane * 4 < a.c.D)
-                        qrow[i] = *reinterpret_cast<const uint2*>(row_ptr(p, r) + lane * 8);
+#pragma unroll
+                    for (int z = 0; z < kPer; ++z) {
+                        qrow[z][i] = make_uint2(0, 0);
+                        if (r < p.rows && lane * 4 + 128 * z < a.c.D)
+                            qrow[z][i] = *reinterpret_cast<const uint2*>(row_ptr(p, r) + lane * 8 +
+                                                                         256 * z);
+                    }
                 }
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = g + 8 * i;
-                qv[i] = make_uint2(0, 0);
-                if (warp >= X::kSteps || r >= p.rows) continue;
-                const uint8_t* q = row_ptr(p, r);
-                if constexpr (E4M3) {
-                    // d = 16 (2 c + h) + 4 s (DP = 64: 16 c + 4 s)
-                    const int d = (DP == 128 ? 16 * (2 * c4 + (warp >> 2)) : 16 * c4) + 4 * (warp & 3);
-                    if (d < a.c.D) qv[i] = *reinterpret_cast<const uint2*>(q + d * 2);
-                } else if (16 * warp < a.c.D) {
-                    const int d = 16 * warp + 2 * c4;
-                    qv[i].x = *reinterpret_cast<const uint32_t*>(q + d * 2);
-                    qv[i].y = *reinterpret_cast<const uint32_t*>(q + d * 2 + 16);
+#pragma unroll
+                for (int z = 0; z < kPer; ++z) {
+                    const int step = warp + kWorkers * z;
+                    qv[z][i] = make_uint2(0, 0);
+                    if (step >= X::kSteps || r >= p.rows) continue;
+                    const uint8_t* q = row_ptr(p, r);
+                    if constexpr (E4M3) {
+                        // step (h, s): d = 16 (DP/64 c + h) + 4 s
+                        const int d = 16 * (DP / 64 * c4 + (step >> 2)) + 4 * (step & 3);
+                        if (d < a.c.D) qv[z][i] = *reinterpret_cast<const uint2*>(q + d * 2);
+                    } else if (16 * step < a.c.D) {
+                        const int d = 16 * step + 2 * c4;
+                        qv[z][i].x = *reinterpret_cast<const uint32_t*>(q + d * 2);
+                        qv[z][i].y = *reinterpret_cast<const uint32_t*>(q + d * 2 + 16);
+                    }
                 }
             }
         };
@@ -199,9 +207,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 // [2^14, 2^15).
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint2 u = qrow[i];
-                    uint32_t top = max(max(u.x << 16 & 0x7FFF0000u, u.x & 0x7FFF0000u),
-                                       max(u.y << 16 & 0x7FFF0000u, u.y & 0x7FFF0000u));
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int z = 0; z < kPer; ++z) {
+                        const uint2 u = qrow[z][i];
+                        top = max(top, max(max(u.x << 16 & 0x7FFF0000u, u.x & 0x7FFF0000u),
+                                           max(u.y << 16 & 0x7FFF0000u, u.y & 0x7FFF0000u)));
+                    }
                     top = __reduce_max_sync(0xFFFFFFFFu, top);
                     if (lane == 0)
                         ctl.q_scale[warp + 8 * i] = __uint_as_float(
@@ -212,13 +224,19 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t e = __float_as_uint(ctl.q_scale[g + 8 * i]) >> 23;
                     const float up = __uint_as_float((254u - e) << 23);
-                    qv[i].x = narrow2(sv::bf16_lo(qv[i].x) * up, sv::bf16_hi(qv[i].x) * up, F16());
-                    qv[i].y = narrow2(sv::bf16_lo(qv[i].y) * up, sv::bf16_hi(qv[i].y) * up, F16());
+#pragma unroll
+                    for (int z = 0; z < kPer; ++z) {
+                        uint2& x = qv[z][i];
+                        x.x = narrow2(sv::bf16_lo(x.x) * up, sv::bf16_hi(x.x) * up, F16());
+                        x.y = narrow2(sv::bf16_lo(x.y) * up, sv::bf16_hi(x.y) * up, F16());
+                    }
                 }
             }
-            if (warp < X::kSteps)
-                st_shared_v4(sq + (warp * 32 + lane) * 16,
-                             make_uint4(qv[0].x, qv[1].x, qv[0].y, qv[1].y));
+#pragma unroll
+            for (int z = 0; z < kPer; ++z)
+                if (warp + kWorkers * z < X::kSteps)
+                    st_shared_v4(sq + ((warp + kWorkers * z) * 32 + lane) * 16,
+                                 make_uint4(qv[z][0].x, qv[z][1].x, qv[z][0].y, qv[z][1].y));
             return meet();
         };
         Place<S> at;
@@ -273,7 +291,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         uint4 w[2];
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            const int row = key0 + 8 * t + g, ch = DP == 128 ? 2 * c4 + h : c4;
+                            const int row = key0 + 8 * t + g, ch = DP / 64 * c4 + h;
                             w[t] = make_uint4(0, 0, 0, 0);
                             if (ch * 16 < a.c.D) w[t] = ld_shared_v4(kt + row * a.c.D + few_swizzle<DP>(row, ch, args.swizzled) * 16);
                         }
@@ -378,32 +396,36 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
                 const uint32_t vt = st + at.stage * X::kTileBytes;
                 if constexpr (E4M3) {
-                    // Keys 2 c, 2 c + 1 and those eight further, as two pairs.
-                    constexpr int kWords = DP / 32;  // of four codes of a key to a lane
-                    uint32_t codes[4][kWords];
+                    // Keys 2 c, 2 c + 1 and those eight further, as two pairs; up to
+                    // 16 codes of a key at a time.
+                    constexpr int kWords = DP == 64 ? 2 : 4;  // of four codes
                     const uint16_t* factor =
                         reinterpret_cast<const uint16_t*>(&ctl.scale[at.stage][0]) + key0 + 2 * c4;
                     const uint32_t f01 = *reinterpret_cast<const uint32_t*>(factor);
                     const uint32_t f23 = *reinterpret_cast<const uint32_t*>(factor + 8);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const int row = key0 + 2 * c4 + (z & 1) + 8 * (z >> 1);
-                        const uint32_t from = vt + row * a.c.D;
-                        if constexpr (DP == 128) {
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (g * 16 < a.c.D) x = ld_shared_v4(from + few_swizzle<DP>(row, g, args.swizzled) * 16);
-                            codes[z][0] = x.x, codes[z][1] = x.y, codes[z][2] = x.z, codes[z][3] = x.w;
-                        } else {
-                            uint2 x = make_uint2(0, 0);
-                            if (g * 8 < a.c.D)
-                                x = ld_shared_v2(from + few_swizzle<DP>(row, g >> 1, args.swizzled) * 16 + (g & 1) * 8);
-                            codes[z][0] = x.x, codes[z][1] = x.y;
-                        }
-                        // (a factor of zero: hidden, whatever the codes are)
-                        if (edge && (((z >> 1 ? f23 : f01) >> (16 * (z & 1))) & 0xFFFFu) == 0u) {
+                    for (int part = 0; part < (DP == 256 ? 2 : 1); ++part) {
+                        uint32_t codes[4][kWords];
 #pragma unroll
-                            for (int i = 0; i < kWords; ++i) codes[z][i] = 0;
-                        }
+                        for (int z = 0; z < 4; ++z) {
+                            const int row = key0 + 2 * c4 + (z & 1) + 8 * (z >> 1);
+                            const uint32_t from = vt + row * a.c.D;
+                            if constexpr (DP >= 128) {
+                                const int ch = DP / 128 * g + part;
+                                uint4 x = make_uint4(0, 0, 0, 0);
+                                if (ch * 16 < a.c.D) x = ld_shared_v4(from + few_swizzle<DP>(row, ch, args.swizzled) * 16);
+                                codes[z][0] = x.x, codes[z][1] = x.y, codes[z][2] = x.z, codes[z][3] = x.w;
+                            } else {
+                                uint2 x = make_uint2(0, 0);
+                                if (g * 8 < a.c.D)
+                                    x = ld_shared_v2(from + few_swizzle<DP>(row, g >> 1, args.swizzled) * 16 + (g & 1) * 8);
+                                codes[z][0] = x.x, codes[z][1] = x.y;
+                            }
+                            // (a factor of zero: hidden, whatever the codes are)
+                            if (edge && (((z >> 1 ? f23 : f01) >> (16 * (z & 1))) & 0xFFFFu) == 0u) {
+#pragma unroll
+                                for (int i = 0; i < kWords; ++i) codes[z][i] = 0;
+                            }
                     }
 #pragma unroll
                     for (int i = 0; i < kWords; ++i) {
@@ -414,9 +436,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                             const uint2 y = spread(__byte_perm(codes[2][i], codes[3][i], sel));
                             const uint32_t x0 = mul2(x.x, f01), x1 = mul2(x.y, f01);
                             const uint32_t y0 = mul2(y.x, f23), y1 = mul2(y.y, f23);
-                            mma16816(o[4 * i + 2 * hi], w, x0, y0, TP());
-                            mma16816(o[4 * i + 2 * hi + 1], w, x1, y1, TP());
+                            mma16816(o[16 * part + 4 * i + 2 * hi], w, x0, y0, TP());
+                            mma16816(o[16 * part + 4 * i + 2 * hi + 1], w, x1, y1, TP());
                         }
+                    }
                     }
                 } else {
                     if (edge) {
@@ -610,14 +633,17 @@ cudaError_t launch_attention_few(const Attn& a, bool f16, bool e4m3, void* works
     CUtensorMap k, v;
     Tiles t;
     int blocks = 0;
-    const int64_t rows = a.max_chunk * a.G;
+    const int64_t rows = a.max_chunk * a.G < kFewRows ? a.max_chunk * a.G : kFewRows;
     cudaError_t e = set_up(a, f16, e4m3, rows, workspace, true, &k, &v, &t, &blocks, mapped);
     if (e != cudaSuccess || !*mapped) return e;
     if (a.c.D <= 64)
         return f16 ? launch_few_type<F16, 64>(k, v, t, blocks, rows, e4m3, s)
                    : launch_few_type<Bf16, 64>(k, v, t, blocks, rows, e4m3, s);
-    return f16 ? launch_few_type<F16, 128>(k, v, t, blocks, rows, e4m3, s)
-               : launch_few_type<Bf16, 128>(k, v, t, blocks, rows, e4m3, s);
+    if (a.c.D <= 128)
+        return f16 ? launch_few_type<F16, 128>(k, v, t, blocks, rows, e4m3, s)
+                   : launch_few_type<Bf16, 128>(k, v, t, blocks, rows, e4m3, s);
+    return f16 ? launch_few_type<F16, 256>(k, v, t, blocks, rows, e4m3, s)
+               : launch_few_type<Bf16, 256>(k, v, t, blocks, rows, e4m3, s);
 }
 
 }  // namespace sva

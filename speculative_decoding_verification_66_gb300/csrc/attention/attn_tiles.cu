@@ -803,15 +803,18 @@ cudaError_t launch_type(const CUtensorMap& k, const CUtensorMap& v, const Tiles&
 }
 
 // Rows of the largest item.
-int64_t item_rows(int64_t max_chunk, int64_t G) { return max_chunk * G < 256 ? max_chunk * G : 256; }
+int64_t item_rows(int64_t max_chunk, int64_t G, int64_t most)
+{
+    return max_chunk * G < most ? max_chunk * G : most;
+}
 
 }  // namespace
 
 size_t tiles_workspace(int64_t max_chunk, int64_t G, int64_t D)
 {
-    const int64_t dp = D <= 64 ? 64 : 128;
-    return kShareBytes + static_cast<size_t>(kMaxBlocks) * 2 * item_rows(max_chunk, G) * (dp + 4) *
-                             sizeof(float);
+    const int64_t dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+    const int64_t rows = item_rows(max_chunk, G, D <= kMaxTileDim ? 256 : kFewRows);
+    return kShareBytes + static_cast<size_t>(kMaxBlocks) * 2 * rows * (dp + 4) * sizeof(float);
 }
 
 cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* workspace,
@@ -820,7 +823,7 @@ cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* wor
     CUtensorMap k, v;
     Tiles t;
     int blocks = 0;
-    const int64_t rows = item_rows(a.max_chunk, a.G);
+    const int64_t rows = item_rows(a.max_chunk, a.G, 256);
     cudaError_t e = set_up(a, f16, e4m3, rows, workspace, false, &k, &v, &t, &blocks, mapped);
     if (e != cudaSuccess || !*mapped) return e;
     const bool pair = rows > 128;

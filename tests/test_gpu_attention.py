@@ -471,3 +471,48 @@ def test_page_tables_that_overlap_are_refused():
     # (one row has no distance to a next)
     out = sv.sv_chunk_attention(q[:2], k, v, table[:1].expand(1, -1), cached[:1], starts[:2])
     assert out.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,e4m3", TYPES)
+@pytest.mark.parametrize("d", [144, 192, 208, 256])
+def test_large_heads(dtype, e4m3, d):
+    """Head sizes past 128: 16 rows at a time, whatever the chunk is."""
+    run([0, 7, 250, 1025], [5, 1, 70, 4], 2, 4, d, 16, dtype, e4m3, seed=d)
+    run([3, 500], [1, 1], 1, 16, d, 128, dtype, e4m3, True, seed=d, max_chunk=1)
+    run([40, 700, 129], [9, 33, 4], 2, 3, d, 64, dtype, e4m3, window=100, seed=d)
+    run([9000, 20011], [3, 6], 1, 8, d, 64, dtype, e4m3, seed=d, max_chunk=6)
+    run([6000, 4100, 777], [17] * 3, 8, 4, d, 64, dtype, e4m3, seed=d, max_chunk=17)
+
+
+@pytest.mark.parametrize("dtype,e4m3", TYPES)
+@pytest.mark.parametrize("fill", [math.nan, math.inf])
+def test_large_heads_unused_slots_have_no_influence(dtype, e4m3, fill):
+    run([3, 100, 130, 517], [1, 9, 6, 40], 2, 4, 256, 16, dtype, e4m3, fill=fill)
+
+
+@pytest.mark.parametrize("dtype,e4m3", TYPES)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_large_heads_masked_values_have_no_influence(dtype, e4m3, bad):
+    """A bad value of a late position: rows before it do not see it, those from it on do."""
+    lens, T, at = 300, 12, 305
+    c = Cache([lens], [T], 2, 256, 16, dtype, False)
+    c.parts[1][c.table[0, at // 16], at % 16, :, 3] = bad
+    if e4m3:
+        for i in range(2):
+            code, c.exps[i] = quantise(c.parts[i])
+            c.parts[i] = code.view(torch.float8_e4m3fn)
+        c.e4m3 = True
+    q = make_query(c, 4, 2)
+    out, lse = attend(c, q, max_chunk=T)
+    check(out, lse, c, q, 256 ** -0.5, rows=slice(0, at - lens))
+    assert not out[at - lens:, :, 3].isfinite().any()
+
+
+def test_large_heads_bad_pages():
+    c = Cache([300, 200], [20, 20], 2, 256, 16)
+    q = make_query(c, 4, 2)
+    c.table[0, 3] = 10 ** 6
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out = sv.sv_chunk_attention(q, *c.args(), seq_status=status, max_chunk=20)
+    assert status.tolist() == [sv.SV_SEQ_BAD_PAGE, 0]
+    assert out[:20].isnan().all() and out[20:].isfinite().all()
