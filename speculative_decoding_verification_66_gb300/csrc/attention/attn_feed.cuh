@@ -63,14 +63,12 @@ struct Tiles {
     float* part;   // [blocks][2][rows][part_cols]: unnormalised O, then m and l
     Share* shares; // [blocks]
     int32_t part_rows;
-    // A tile in shared memory: rows of 128 bytes (64 elements), eight to a
-    // group; bytes from a group to the next, and to the next 64 elements.
-    int32_t group, panel;
-    // Copies of whole 128-element rows: pages and heads are one axis, a page
-    // page_heads steps, a head head_step. 0: a copy for each 64 elements.
-    int32_t page_heads, head_step;
     int32_t swizzled;  // e4m3 rows of 128 or 64 bytes lie swizzled (few rows)
 };
+
+// A tile of 16-bit elements in shared memory: panels of 64 elements of every row,
+// rows of 128 bytes, swizzled.
+constexpr int kPanel = kTile * 128;
 
 constexpr size_t kShareBytes = (sizeof(Share) * kMaxBlocks + 255) / 256 * 256;
 
@@ -242,12 +240,10 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
                  : "memory");
     return v;
 }
-// Byte offset of 16-byte chunk `chunk` of a row in a tile with the 128-byte
-// swizzle (group and panel: see Tiles).
-__device__ __forceinline__ uint32_t tile_chunk(int row, int chunk, int group, int panel)
+// Byte offset of 16-byte chunk `chunk` of a row in a tile (see kPanel).
+__device__ __forceinline__ uint32_t tile_chunk(int row, int chunk)
 {
-    return (row >> 3) * group + (chunk >> 3) * panel + (row & 7) * 128 +
-           (((chunk & 7) ^ (row & 7)) << 4);
+    return (chunk >> 3) * kPanel + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
 // Where this block starts, into ctl.start. True if some sequence's lengths are
@@ -389,8 +385,9 @@ __device__ __forceinline__ const Plan* plan_at(Ctl& ctl, int i, Wait& wait_all)
 // Copies of keys (kv = 0) or values (1), by a warp; the keys' warp also plans the
 // segments. e4m3: the factors that the codes are multiplied by (FEW: of keys, the
 // powers of two themselves; of values, as halves), and with the keys the largest
-// exponents of the tile's keys and values. The page of tile k + 2 and the
-// exponents of tile k + 1 are on their way while tile k is issued.
+// exponents of the tile's keys and values (FEW: with the values, of these). The
+// page of tile k + 2 and the exponents of tile k + 1 are on their way while tile k
+// is issued.
 template <class T, int DP, bool E4M3, int R, bool SPLIT, bool ALT, int FILL, bool FEW, class Ctl,
           class Wait>
 __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensorMap* map, int kv,
@@ -401,7 +398,7 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
     const int lane = threadIdx.x & 31;
     const int P = 1 << a.c.page_shift, box = min(P, kTile);
     const uint32_t box_bytes = E4M3 ? box * a.c.D : box * DP * 2;
-    const uint32_t lane_bytes = E4M3 ? lane * 4 * a.c.D : lane * 4 / 8 * args.group;
+    const uint32_t lane_bytes = E4M3 ? lane * 4 * a.c.D : lane * 4 * 128;
     const bool first_of_box = P >= kTile ? lane == 0 : ((lane * 4) & (P - 1)) == 0;
     const uint8_t* exps = kv ? a.c.exps[1] : a.c.exps[0];
     const int64_t exp_step = kv ? a.c.exp_slot_stride[1] : a.c.exp_slot_stride[0];
@@ -476,7 +473,7 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                 const uint8_t* e = exps_h + pg * exp_page + slot * exp_step;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x.e[i] = e[i * exp_step];
-                if (kv == 0) {
+                if (!FEW && kv == 0) {
                     const uint8_t* v = v_exps_h + pg * a.c.exp_page_stride[1] +
                                        slot * a.c.exp_slot_stride[1];
 #pragma unroll
@@ -527,9 +524,9 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     top = max(top, xc.e[i] == 255u ? 0u : xc.e[i]);
-                    if (kv == 0) v_top = max(v_top, xc.v[i] == 255u ? 0u : xc.v[i]);
+                    if (!FEW && kv == 0) v_top = max(v_top, xc.v[i] == 255u ? 0u : xc.v[i]);
                 }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                if (!FEW || kv == 1) top = __reduce_max_sync(0xFFFFFFFFu, top);
                 bool apart = false;  // further than float16 holds
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -554,7 +551,9 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                     *reinterpret_cast<uint4*>(&ctl.factor[at.stage][lane * 4]) =
                         make_uint4(f[0], f[1], f[2], f[3]);
                 }
-                if (kv == 0) {
+                if constexpr (FEW) {
+                    if (kv == 1 && lane == 0) ctl.top[at.stage] = top;
+                } else if (kv == 0) {
                     v_top = __reduce_max_sync(0xFFFFFFFFu, v_top);
                     if (lane == 0) ctl.top[at.stage] = make_uint2(top, v_top);
                 }
@@ -570,13 +569,10 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                 const uint32_t to = stages + at.stage * stage_bytes + lane_bytes;
                 if (E4M3) {
                     tma_load_4d(to, map, 0, c1, h, cur, &fullbar[at.stage]);
-                } else if (args.page_heads > 0) {
-                    tma_load_5d(to, map, 0, 0, 0, c1 >> 3, cur * args.page_heads + h * args.head_step,
-                                &fullbar[at.stage]);
                 } else {
 #pragma unroll
                     for (int q = 0; q < DP / 64; ++q)
-                        tma_load_4d(to + q * args.panel, map, q * 64, c1, h, cur, &fullbar[at.stage]);
+                        tma_load_4d(to + q * kPanel, map, q * 64, c1, h, cur, &fullbar[at.stage]);
                 }
             }
             __syncwarp();
@@ -756,56 +752,14 @@ bool make_map(CUtensorMap* map, const Cache& c, int kv, bool f16, bool e4m3, boo
            CUDA_SUCCESS;
 }
 
-// 16-bit rows of 128 elements, one copy a page for both halves of the rows:
-// [page and head][slot / 8][half][slot % 8][64 elements]. Pages and heads are one
-// axis, in steps of a head (one head: of a page); see heads_to_a_page.
-bool make_map5(CUtensorMap* map, const Cache& c, int kv, bool f16, int64_t page_heads)
-{
-    const EncodeTiled fn = encode_fn();
-    if (fn == nullptr) return false;
-    const int P = 1 << c.page_shift;
-    const int64_t step = c.Hkv > 1 ? c.head_stride[kv] : c.page_stride[kv];
-    const cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(P / 8),
-                                static_cast<cuuint64_t>((c.num_pages - 1) * page_heads + c.Hkv)};
-    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(c.slot_stride[kv]), 128,
-                                   static_cast<cuuint64_t>(c.slot_stride[kv]) * 8,
-                                   static_cast<cuuint64_t>(step)};
-    const cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>((P < kTile ? P : kTile) / 8), 1};
-    const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
-    return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
-              c.pages[kv], dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// How far apart pages are on make_map5's axis of pages and heads; 0 where it
-// cannot be used: the page stride has to be a multiple of the head stride, the
-// same in keys and values.
-int64_t heads_to_a_page(const Cache& c, bool e4m3)
-{
-    if (e4m3 || c.D != 128) return 0;
-    int64_t n = 1;
-    if (c.Hkv > 1) {
-        if (c.head_stride[0] <= 0 || c.page_stride[0] % c.head_stride[0] != 0) return 0;
-        n = c.page_stride[0] / c.head_stride[0];
-        if (n <= 0 || c.head_stride[1] <= 0 || c.page_stride[1] != n * c.head_stride[1]) return 0;
-    }
-    // (coordinates are 32 bits)
-    return n < (int64_t(1) << 31) / c.num_pages - c.Hkv ? n : 0;
-}
-
 // Maps, work description and number of blocks of a call; *mapped false where the
 // copies cannot describe the pages' strides. swizzle: e4m3 rows of 128 or 64 codes
 // may lie swizzled in shared memory.
 cudaError_t set_up(const Attn& a, bool f16, bool e4m3, int64_t rows, void* workspace, bool swizzle,
                    CUtensorMap* k, CUtensorMap* v, Tiles* t, int* blocks, bool* mapped)
 {
-    const int64_t page_heads = heads_to_a_page(a.c, e4m3);
-    const bool five = page_heads > 0 && make_map5(k, a.c, 0, f16, page_heads) &&
-                      make_map5(v, a.c, 1, f16, page_heads);
     const bool swizzled = swizzle && e4m3 && (a.c.D == 128 || a.c.D == 64);
-    *mapped = five || (make_map(k, a.c, 0, f16, e4m3, swizzled) &&
-                       make_map(v, a.c, 1, f16, e4m3, swizzled));
+    *mapped = make_map(k, a.c, 0, f16, e4m3, swizzled) && make_map(v, a.c, 1, f16, e4m3, swizzled);
     if (!*mapped) return cudaSuccess;
     int dev = 0, sms = 0;
     cudaError_t e;
@@ -817,10 +771,6 @@ cudaError_t set_up(const Attn& a, bool f16, bool e4m3, int64_t rows, void* works
                reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kShareBytes),
                static_cast<Share*>(workspace),
                static_cast<int32_t>(rows),
-               five ? 2048 : 1024,
-               five ? 1024 : kTile * 128,
-               five ? static_cast<int32_t>(page_heads) : 0,
-               a.c.Hkv > 1 ? 1 : 0,
                swizzled ? 1 : 0};
     return cudaSuccess;
 }

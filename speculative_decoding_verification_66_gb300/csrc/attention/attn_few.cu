@@ -57,10 +57,9 @@ struct FewControl {
     float2 ml[kWorkers][16];
     float q_scale[16];
     // e4m3, for every stage: the keys' powers of two, or the values' factors as
-    // halves; the largest exponents of its keys and of the values that belong to
-    // them.
+    // halves and their largest exponent.
     alignas(16) float scale[E4M3 ? STAGES : 1][E4M3 ? kTile : 4];
-    uint2 top[E4M3 ? STAGES : 1];
+    uint32_t top[E4M3 ? STAGES : 1];
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -316,22 +315,24 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     }
                 } else {
                     const int row = key0 + (lane & 7) + ((lane >> 4) << 3);
-                    const uint32_t from = kt + (row >> 3) * args.group + (row & 7) * 128;
+                    const uint32_t from = kt + row * 128;
                     const int y = ((lane >> 3) & 1) ^ (row & 7);
 #pragma unroll
                     for (int step = 0; step < X::kSteps; ++step) {
                         uint32_t b[4];
-                        ldmatrix4(from + (step >> 2) * args.panel + (((2 * (step & 3)) ^ y) << 4), b);
+                        ldmatrix4(from + (step >> 2) * kPanel + (((2 * (step & 3)) ^ y) << 4), b);
                         scores(step, b);
                     }
                 }
-                const int v_top = E4M3 ? static_cast<int>(ctl.top[at.stage].y) : 0;
                 __syncwarp();
                 if (lane == 0) sv::mbar_arrive(&ctl.empty[at.stage]);
                 at.advance(1);
                 // ---- weights
                 int lift = 0;  // e4m3: the tile's values above the outputs' exponent
                 if (E4M3) {
+                    // (the values' exponent comes with them)
+                    if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
+                    const int v_top = static_cast<int>(ctl.top[at.stage]);
                     if (moves(ref, v_top)) {
                         const float keep = moved(ref, v_top);
 #pragma unroll
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     }
                 }
                 // ---- values
-                if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
+                if (!E4M3 && !(ok = wait_all(&ctl.full[at.stage], at.round))) break;
                 const uint32_t vt = st + at.stage * X::kTileBytes;
                 if constexpr (E4M3) {
                     // Keys 2 c, 2 c + 1 and those eight further, as two pairs; up to
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll 1
                         for (int x = lane; x < 16 * kLanes; x += 32) {
                             const int row = key0 + x / kLanes, ch = x % kLanes, q = k * kTile + row;
-                            const uint32_t addr = vt + tile_chunk(row, ch, args.group, args.panel);
+                            const uint32_t addr = vt + tile_chunk(row, ch);
                             const bool outside = q < p.any_lo || q > p.any_hi;
                             const bool common = q >= p.all_lo && q <= p.all_hi;
                             bool special = false;
@@ -467,12 +468,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         __syncwarp();
                     }
                     const int row = key0 + (lane & 7) + (((lane >> 3) & 1) << 3);
-                    const uint32_t from = vt + (row >> 3) * args.group + (row & 7) * 128;
+                    const uint32_t from = vt + row * 128;
                     const int y = (lane >> 4) ^ (row & 7);
 #pragma unroll
                     for (int j = 0; j < DP / 16; ++j) {
                         uint32_t b[4];
-                        ldmatrix4_trans(from + (j >> 2) * args.panel + (((2 * (j & 3)) ^ y) << 4), b);
+                        ldmatrix4_trans(from + (j >> 2) * kPanel + (((2 * (j & 3)) ^ y) << 4), b);
                         mma16816(o[2 * j], w, b[0], b[1], TP());
                         mma16816(o[2 * j + 1], w, b[2], b[3], TP());
                     }

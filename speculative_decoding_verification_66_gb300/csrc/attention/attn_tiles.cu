@@ -82,7 +82,6 @@ struct Shape {
     // no more than the 640 threads are launched with, 96 each.
     static constexpr int kRegsRow = 104, kRegsOther = 88, kRegsLaunch = 96;
     static_assert(8 * kRegsRow + 12 * kRegsOther <= 20 * kRegsLaunch, "registers");
-    static constexpr int kPanel = kTile * 128;  // bytes of 64 elements of every row
     static constexpr int kTiles = kQBytes + kStages * kTileBytes + kRawStages * kRawBytes;
 };
 
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                 }
                 if (has)
                     st_shared_v4(sq + (r >> 7) * (128 * DP * 2) +
-                                     tile_chunk(r & 127, ch, 1024, X::kPanel),
+                                     tile_chunk(r & 127, ch),
                                  qv[i]);
             }
             fence_async_smem();
@@ -533,8 +532,8 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         constexpr uint32_t id_s = idesc<TP, kTile, false>(), id_o = idesc<TP, DP, true>();
         const int s = warp == 8 ? 0 : 1;
         const uint64_t dq = smem_desc(sq + (PAIR ? s * (128 * DP * 2) : 0), 16, 1024);
-        const uint64_t dk = smem_desc(st, 16, args.group), dv = smem_desc(st, args.panel, args.group);
-        const uint32_t panel = args.panel >> 4, v_step = args.group >> 3;  // 16 keys: two groups
+        const uint64_t dk = smem_desc(st, 16, 1024), dv = smem_desc(st, kPanel, 1024);
+        constexpr uint32_t panel = kPanel >> 4, v_step = 2048 >> 4;  // 16 keys: two groups of 8
         const uint32_t s_addr = tmem + s * 128, o_addr = tmem + 256 + s * DP;
         Place<S> at;
         uint32_t fixes = 0, tiles = 0;
@@ -607,7 +606,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < DP / 16; ++x) {
                                 const uint32_t o = (x & 3) * 2;
-                                mma_ss(s_addr, dq + o + (x >> 2) * (X::kPanel >> 4),
+                                mma_ss(s_addr, dq + o + (x >> 2) * panel,
                                        b + o + (x >> 2) * panel, id_s, x > 0);
                             }
                             mma_commit(&ctl.s_full[s]);
@@ -675,7 +674,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
 #pragma unroll 4
                         for (int x = tid; x < kTile * kLanes; x += kThreadsH) {
                             const int row = x / kLanes, ch = x % kLanes, p = k * kTile + row;
-                            const uint32_t addr = v + tile_chunk(row, ch, args.group, args.panel);
+                            const uint32_t addr = v + tile_chunk(row, ch);
                             const bool outside = p < g->any_lo || p > g->any_hi;
                             const bool common = p >= g->all_lo && p <= g->all_hi;
                             bool special = false;
@@ -710,7 +709,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const int piece = (tid & 3) + (kPieces > 4 ? (((tid >> 3) & 1) ^ odd) << 2 : 0);
                     const bool in_row = piece * 16 < a.c.D;
                     const uint32_t from = raw + row0 * a.c.D + (in_row ? piece * 16 : 0);
-                    const uint32_t to = dst + tile_chunk(row0, piece * 2, 1024, X::kPanel);
+                    const uint32_t to = dst + tile_chunk(row0, piece * 2);
                     const uint32_t* factor = &ctl.factor[raw_at.stage][row0];
                     if (!is_v && tid == 0) {
                         const uint2 top = ctl.top[raw_at.stage];
@@ -823,10 +822,14 @@ cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* wor
     CUtensorMap k, v;
     Tiles t;
     int blocks = 0;
-    const int64_t rows = item_rows(a.max_chunk, a.G, 256);
+    // PAIR where the sequences have more than 128 rows on average (their number is
+    // known, their lengths are not). 64 x 33 tokens of 4 heads: 265 us with, 365
+    // without; chunks from 1 to 33: 185 and 166, 32 x (1 to 17) of 8 heads: 500
+    // and 464: items of up to 128 rows leave the second slot idle.
+    const bool pair = a.max_chunk * a.G > 128 && a.tokens * a.G > 128 * static_cast<int64_t>(a.c.B);
+    const int64_t rows = item_rows(a.max_chunk, a.G, pair ? 256 : 128);
     cudaError_t e = set_up(a, f16, e4m3, rows, workspace, false, &k, &v, &t, &blocks, mapped);
     if (e != cudaSuccess || !*mapped) return e;
-    const bool pair = rows > 128;
     if (a.c.D <= 64)
         return f16 ? launch_type<F16, 64>(k, v, t, blocks, rows, e4m3, pair, s)
                    : launch_type<Bf16, 64>(k, v, t, blocks, rows, e4m3, pair, s);
