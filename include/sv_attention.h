@@ -23,6 +23,8 @@
  *   or an infinity is stored with e = 255. Every stored value is a bfloat16
  *   number; float16 sources are clamped to +-61440 first so that the stored
  *   value is a float16 number too (below 2^-14 up to float16's own rounding).
+ *   Codes 0x7F and 0xFF are never written, and must not be in a cache that was
+ *   written by something else.
  *
  * The chunks. Sequence b has cached_lens[b] tokens in the cache and
  * chunk_starts[b + 1] - chunk_starts[b] new ones (none is allowed), which are
@@ -112,7 +114,8 @@ int sv_kv_append(const sv_paged_cache* cache, const void* key, const void* value
  * Read positions cached_lens[b] + t back into the packed arrays
  * key, value [tokens, kv_heads, head_dim], contiguous, 16-byte aligned, of
  * `dtype`: the cache's own type, or either 16-bit type from SV_E4M3 (one
- * rounding). Rows of bad sequences or pages are NaN.
+ * rounding). Rows of bad sequences or pages, and of no sequence, are NaN.
+ * What was written to an e4m3 cache from bfloat16 may be too large for float16.
  * One launch (and a memset when seq_status is given).
  */
 int sv_kv_read(const sv_paged_cache* cache, void* key, void* value, int dtype, int64_t tokens,
@@ -127,8 +130,8 @@ int sv_kv_read(const sv_paged_cache* cache, void* key, void* value, int dtype, i
  * Query head h reads key/value head h / (q_heads / kv_heads). Values and
  * scores at positions that a query does not see have no influence on it,
  * whatever they are. Scores, softmax sums and outputs are accumulated in
- * float32; the softmax weights are rounded to the query's type for the second
- * product. Results do not depend on the order in which blocks run.
+ * float32; the softmax weights are rounded to the query's type (e4m3 caches: to
+ * float16) for the second product. bfloat16 values above 2^90 may overflow there. Results do not depend on the order in which blocks run.
  *   query       device [tokens, q_heads, head_dim] of `dtype` (SV_BF16 or
  *               SV_F16; the cache's own type unless the cache is SV_E4M3),
  *               16-byte aligned, strides in elements, multiples of 8.

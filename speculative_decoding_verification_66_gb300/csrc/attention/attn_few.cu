@@ -1,5 +1,7 @@
-// attn_few.cu -- attention over the paged cache for items of up to 16 rows (a
-// single token, a short draft), head sizes up to 128.
+// attn_few.cu -- attention over the paged cache by items of up to 16 rows: where a
+// sequence has no more to a key/value head (a single token, a short draft), and for
+// head sizes past 128, whose outputs would not fit attn_tiles.cu's tensor memory
+// beside two slots' scores.
 //
 // Such items are bound by the reads of the cache: 2 D (1 + rows) operations meet
 // 2 bytes of a key (or 1), far from the tensor cores' balance. The 128-row
@@ -11,14 +13,22 @@
 // A warp keeps a maximum, a sum and an output of its own for every row; they
 // are joined through shared memory at the end of a segment.
 //
+// Measured: 512 single tokens, 500 to 2000 cached, 16 heads of 64: 455 us, 5.8 TB/s
+// (with attn_tiles.cu 732 us); 4 tokens over 131000 e4m3 keys, 32 heads on 8: 230 us,
+// 4.7 TB/s (299 us); the reads bound the first, the reads and the conversions the
+// second (193 us with the loads alone). From 17 rows on the 128-row products win: 64
+// sequences of 20 rows 148 us against 156 here, of 32 rows 158 against 197. Heads of
+// 256: 64 x 5 tokens 341 us, a piece of 512 tokens 654 us (161 TFLOP/s), ten to
+// twenty times faster than a row at a time.
+//
 // Warps 0-7 work, 8 and 9 load keys and values (attn_feed.cuh). Masks, hidden
 // values and the sharing among blocks are those of attn_tiles.cu.
 //
 // e4m3. A lane reads 16 codes of a row at a time and expands them to float16 in
 // registers. Keys: the codes alone (the exponents multiply the scores' columns);
 // which d an operand's k slots stand for is free as long as the queries agree, so
-// slots 2c, 2c+1, 2c+8, 2c+9 of step (h, s) are d = 16 (2c + h) + 4 s + 0..3, four
-// neighbouring codes. Values, relative to their tile's largest exponent as in
+// slots 2c, 2c+1, 2c+8, 2c+9 of step (h, s) are d = 16 (DP/64 c + h) + 4 s + 0..3,
+// four neighbouring codes. Values, relative to their tile's largest exponent as in
 // attn_tiles.cu: lane (g, c) reads d = DP/8 g .. of its four keys and interleaves
 // the codes of two keys; the products' column n of step j is then d = DP/8 n + j.
 #include "attn_feed.cuh"
@@ -292,7 +302,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         for (int t = 0; t < 2; ++t) {
                             const int row = key0 + 8 * t + g, ch = DP / 64 * c4 + h;
                             w[t] = make_uint4(0, 0, 0, 0);
-                            if (ch * 16 < a.c.D) w[t] = ld_shared_v4(kt + row * a.c.D + few_swizzle<DP>(row, ch, args.swizzled) * 16);
+                            if (ch * 16 < a.c.D)
+                                w[t] = ld_shared_v4(kt + row * a.c.D +
+                                                    few_swizzle<DP>(row, ch, args.swizzled) * 16);
                         }
                         const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
                         const uint32_t w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
@@ -414,12 +426,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                             if constexpr (DP >= 128) {
                                 const int ch = DP / 128 * g + part;
                                 uint4 x = make_uint4(0, 0, 0, 0);
-                                if (ch * 16 < a.c.D) x = ld_shared_v4(from + few_swizzle<DP>(row, ch, args.swizzled) * 16);
-                                codes[z][0] = x.x, codes[z][1] = x.y, codes[z][2] = x.z, codes[z][3] = x.w;
+                                if (ch * 16 < a.c.D)
+                                    x = ld_shared_v4(from +
+                                                     few_swizzle<DP>(row, ch, args.swizzled) * 16);
+                                codes[z][0] = x.x, codes[z][1] = x.y;
+                                codes[z][2] = x.z, codes[z][3] = x.w;
                             } else {
                                 uint2 x = make_uint2(0, 0);
                                 if (g * 8 < a.c.D)
-                                    x = ld_shared_v2(from + few_swizzle<DP>(row, g >> 1, args.swizzled) * 16 + (g & 1) * 8);
+                                    x = ld_shared_v2(from + (g & 1) * 8 +
+                                                     few_swizzle<DP>(row, g >> 1, args.swizzled) * 16);
                                 codes[z][0] = x.x, codes[z][1] = x.y;
                             }
                             // (a factor of zero: hidden, whatever the codes are)
@@ -569,8 +585,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kStepsJ; ++j)
                         *reinterpret_cast<float2*>(to + j * 8) =
-                            make_float2(o[j0 + j][2 * i] * size,
-                                        o[j0 + j][2 * i + 1] * size);
+                            make_float2(o[j0 + j][2 * i] * size, o[j0 + j][2 * i + 1] * size);
                 }
                 if (!once) {
                     if (!(ok = meet())) break;

@@ -1,4 +1,8 @@
-// attn_rows.cu -- attention of the new tokens, one warp a query row.
+// attn_rows.cu -- attention of the new tokens, one warp a query row, one key at a
+// time. For caches that the tensor copies of the other kernels cannot describe: no
+// pages at all, or strides that a tensor map does not take. A row's keys come one
+// behind the other, so it is bound by the latency of its loads: 64 x 5 tokens take
+// 3.2 ms where attn_tiles.cu takes 0.13.
 #include "attn_internal.h"
 
 namespace sva {

@@ -19,7 +19,8 @@
 //   !PAIR   an item has up to 128 rows, both slots hold the same queries and
 //           take every second tile; their results are joined at the end.
 // PAIR halves the reads of a cache for chunks of more than 128 rows; !PAIR keeps
-// the tensor core busy where there are fewer (a draft, a single token).
+// the tensor core busy where there are fewer (launch_attention_tiles has the rule
+// and what it rests on).
 //
 // Warps:
 //   0-3, 4-7  softmax of slots 0 and 1 (row = tensor-memory lane = thread), the
@@ -29,9 +30,9 @@
 //             look after one slot's barriers while the other's products run.
 //   9, 10     load keys and values: page numbers, a bulk tensor copy a page,
 //             exponents. Warp 9 also plans the block's segments for all.
-//   12-..     helpers (4; e4m3: 8). 16-bit caches: make the values at a tile's hidden
-//             positions harmless. e4m3 caches: also expand every tile, exactly,
-//             into the stage that the products read.
+//   12-..     helpers (4; e4m3: 8). 16-bit caches: make the values at a tile's
+//             hidden positions harmless. e4m3 caches: expand every tile into the
+//             stage that the products read.
 // The next segment's queries are fetched while the last products of a segment
 // run, and its scores begin while the segment's results are written.
 //
@@ -58,11 +59,19 @@
 // Work is shared among one block per SM as attn_plan.cuh says; items that
 // several blocks share are joined by join_kernel in block order, so results
 // depend on the lengths and the number of blocks alone.
+//
+// What bounds it. 16-bit drafts: the reads of the cache (64 x 5 tokens, contexts
+// 1000 to 4000, 32 heads on 8: 133 us, 5.0 TB/s with both ends of a short call in
+// it; 32 x (1 to 17), 8000 to 32768, 64 on 8: 441 us, 6.1 TB/s of 6.8). Pieces of
+// prompts: the way from scores to weights to products, which the other slot covers
+// in part (2048 tokens after 6000: 218 us, 1.09 PFLOP/s of 1.91; the tensor pipe
+// runs half of the cycles). e4m3: the instructions that expand and weigh (256 x 9:
+// 680 us, 2.95 TB/s of codes, which are 5.9 TB/s of values; pieces of 1 to 700
+// tokens with a window: 175 us).
 #include "attn_feed.cuh"
 
 namespace sva {
 namespace {
-
 
 template <int DP, bool E4M3, bool PAIR>
 struct Shape {
@@ -186,16 +195,18 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
     };
     int item = 0;  // segments taken so far
 
+    if (E4M3 && warp >= 8)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kRegsOther));
     if (warp < 8) {
         // ------------------------------------------------------------------
         // Softmax of slot s; thread = row.
         // ------------------------------------------------------------------
         if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kRegsRow));
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-        // Columns of scores in registers at a time: 64 wait for fewer loads, and
-        // where every row exists that counts (a 2048-token piece: 210 us against
-        // 229); e4m3 has more code to keep in the instruction caches and fewer
-        // registers (256 x 9: 738 us against 1075 with 64).
+        // Columns of scores in registers at a time: 64 wait for fewer loads (a
+        // 2048-token piece 222 us against 228 with 32); e4m3 has more code to keep
+        // in the instruction caches and fewer registers (256 x 9: 738 us with 32,
+        // 1075 with 64, which spills).
         constexpr bool kWide = !E4M3;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t s_addr = lane_base + s * 128, o_addr = lane_base + 256 + s * DP;
@@ -522,9 +533,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             }
             if (lane == 0) sv::mbar_arrive(&ctl.o_free);
         }
-    } else {
-    if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kRegsOther));
-    if (warp == 8 || warp == 11) {
+    } else if (warp == 8 || warp == 11) {
         // ------------------------------------------------------------------
         // Products of slot s: the warp stays together, one lane issues. It
         // passes every tile in ring order, its own and the other slot's.
@@ -699,10 +708,9 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const uint32_t raw = sr + raw_at.stage * X::kRawBytes;
                     const uint32_t dst = st + at.stage * X::kTileBytes;
                     // A thread expands 16 codes of a row, the same piece of every
-                    // kStep-th row, four at a time. Eight neighbouring lanes take half of the
-                    // pieces of two rows, the other half of the second: their
-                    // 16-byte columns differ in the loads and, swizzled, in the
-                    // stores.
+                    // kStep-th row, four at a time. Eight neighbouring lanes take half
+                    // of the pieces of two rows, the other half of the second: their
+                    // 16-byte columns differ in the loads and, swizzled, in the stores.
                     constexpr int kPieces = DP / 16, kStep = kThreadsH / kPieces;
                     const int pair = tid / (2 * kPieces), odd = (tid >> 2) & 1;
                     const int row0 = pair * 2 + odd;
@@ -752,7 +760,6 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                 at.advance(1);
             }
         }
-    }
     }
     __syncthreads();
     if (threadIdx.x == 0) args.shares[blockIdx.x].failed = *stop;
