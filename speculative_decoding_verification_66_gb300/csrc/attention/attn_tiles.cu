@@ -225,23 +225,30 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         uint4 qv[kFetch];
         const int first = (threadIdx.x & 127) / kChunks + (PAIR ? 128 * s : 64 * s);
         const int ch = threadIdx.x % kChunks;
+        // From a row to the one that is kStep further, in tokens and heads.
+        constexpr int kStep = 128 / kChunks;
+        const int step_t = kStep / a.G, step_h = kStep - step_t * a.G;
         auto fetch = [&](const Plan& x) {
+            int t = (x.row0 + first) / a.G, head = x.row0 + first - t * a.G;
 #pragma unroll
             for (int i = 0; i < kFetch; ++i) {
-                const int r = first + i * (128 / kChunks);
                 qv[i] = make_uint4(0, 0, 0, 0);
-                if (r < x.rows && ch * 8 < a.c.D) {
-                    const int rr = x.row0 + r, t = rr / a.G;
+                if (first + i * kStep < x.rows && ch * 8 < a.c.D)
                     qv[i] = *reinterpret_cast<const uint4*>(
                         a.q + (static_cast<int64_t>(x.q0) + t) * a.q_token +
-                        static_cast<int64_t>(x.h * a.G + (rr - t * a.G)) * a.q_head + ch * 16);
+                        static_cast<int64_t>(x.h * a.G + head) * a.q_head + ch * 16);
+                t += step_t;
+                head += step_h;
+                if (head >= a.G) {
+                    head -= a.G;
+                    ++t;
                 }
             }
         };
         auto store = [&](const Plan& x, int at) {
 #pragma unroll
             for (int i = 0; i < kFetch; ++i) {
-                const int r = first + i * (128 / kChunks);
+                const int r = first + i * kStep;
                 const bool has = r < x.rows;
                 if constexpr (E4M3 && std::is_same<T, Bf16>::value) {
                     // To float16, scaled. The kChunks lanes of a row are neighbours.
@@ -460,16 +467,17 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             float* share = args.part + (static_cast<int64_t>(blockIdx.x) * 2 + (g.begins ? 1 : 0)) *
                                            args.part_rows * (DP + 4);
             if (live) {
-                // Columns of the row, kCols at a time: all, or the slot's half
-                // where both slots hold the row.
-                constexpr int kCols = PAIR ? 64 : DP / 2;
+                // Columns of the row, 32 at a time (more of both slots' would not
+                // stay in registers): all, or the slot's half where both slots hold
+                // the row.
+                constexpr int kCols = 32;
                 const int64_t orow = (static_cast<int64_t>(g.q0) + token) * a.Hq + g.h * a.G +
                                      (r - token * a.G);
                 const float inv = bad ? nan : (whole ? 1.f / l : 1.f) * (PAIR ? size : 1.f);
                 float* part = share + static_cast<int64_t>(slot_row) * (DP + 4);
 #pragma unroll 1
-                for (int x = 0; x < (PAIR ? DP / 64 : 1); ++x) {
-                    const int k0 = PAIR ? 64 * x : s * kCols;
+                for (int x = 0; x < DP / (PAIR ? kCols : 2 * kCols); ++x) {
+                    const int k0 = (PAIR ? 0 : s * (DP / 2)) + kCols * x;
                     float o[kCols];
                     __syncwarp();
                     if constexpr (PAIR) {
