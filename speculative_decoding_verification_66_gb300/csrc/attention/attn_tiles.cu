@@ -61,13 +61,14 @@
 // depend on the lengths and the number of blocks alone.
 //
 // What bounds it. 16-bit drafts: the reads of the cache (64 x 5 tokens, contexts
-// 1000 to 4000, 32 heads on 8: 133 us, 5.0 TB/s with both ends of a short call in
-// it; 32 x (1 to 17), 8000 to 32768, 64 on 8: 441 us, 6.1 TB/s of 6.8). Pieces of
+// 1000 to 4000, 32 heads on 8: 122 us, 5.4 TB/s with both ends of a short call in
+// it; 32 x (1 to 17), 8000 to 32768, 64 on 8: 434 us, 6.2 TB/s of 6.8). Pieces of
 // prompts: the way from scores to weights to products, which the other slot covers
-// in part (2048 tokens after 6000: 218 us, 1.09 PFLOP/s of 1.91; the tensor pipe
-// runs half of the cycles). e4m3: the instructions that expand and weigh (256 x 9:
-// 680 us, 2.95 TB/s of codes, which are 5.9 TB/s of values; pieces of 1 to 700
-// tokens with a window: 175 us).
+// in part (2048 tokens after 6000: 212 us, 1.11 PFLOP/s of 1.91; the tensor pipe
+// runs half of the cycles). e4m3: the chain of loads, expansion, scores, weights and
+// products, of which no part alone takes more than a sixth of the time (256 x 9:
+// 664 us, 3.0 TB/s of codes, which are 6.0 TB/s of values; pieces of 1 to 700 tokens
+// with a window: 161 us), and some 8 us from an item to the next.
 #include "attn_feed.cuh"
 
 namespace sva {
@@ -205,8 +206,8 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         // Columns of scores in registers at a time: 64 wait for fewer loads (a
         // 2048-token piece 222 us against 228 with 32); e4m3 has more code to keep
-        // in the instruction caches and fewer registers (256 x 9: 738 us with 32,
-        // 1075 with 64, which spills).
+        // in the instruction caches and fewer registers (256 x 9: 668 us with 32,
+        // 724 with 64 and 120 registers, which spill).
         constexpr bool kWide = !E4M3;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t s_addr = lane_base + s * 128, o_addr = lane_base + 256 + s * DP;
