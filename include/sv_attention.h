@@ -153,6 +153,24 @@ int sv_chunk_attention(const sv_paged_cache* cache, const void* query, int dtype
                        int32_t* seq_status, void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/*
+ * Test hook for the timeout path: sv_chunk_attention with the values' loads of
+ * one thread block held until the device int32 *gate becomes nonzero. That wait
+ * is bounded like every other wait in the kernels (about 2 s). When it runs out
+ * the thread block gives up and returns with no copy in flight, and every
+ * sequence of the call is reported as SV_SEQ_TIMEOUT. The context stays usable.
+ * A caller that sets *gate before the wait runs out gets the ordinary results.
+ *   block  the thread block, 0 .. SMs - 1; negative: all of them.
+ *   gate   device int32, 4-byte aligned (SV_ERR_ARG if NULL, SV_ERR_ALIGN).
+ * Other arguments as sv_chunk_attention.
+ */
+int sv_chunk_attention_gated(const sv_paged_cache* cache, const void* query, int dtype,
+                             int64_t tokens, int64_t q_heads, int64_t query_token_stride,
+                             int64_t query_head_stride, float scale, int64_t window,
+                             int64_t max_chunk, void* out, float* lse, int32_t* seq_status,
+                             void* workspace, size_t workspace_bytes, void* stream, int32_t block,
+                             const int32_t* gate);
+
 #ifdef __cplusplus
 }
 #endif

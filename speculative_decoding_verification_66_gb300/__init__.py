@@ -55,6 +55,7 @@ from .attention import (  # noqa: F401
     SV_SEQ_BAD_LENGTH,
     SV_SEQ_BAD_PAGE,
     sv_chunk_attention,
+    sv_chunk_attention_gated,
     sv_chunk_attention_workspace_bytes,
     sv_kv_append,
     sv_kv_read,

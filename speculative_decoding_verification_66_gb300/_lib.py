@@ -76,6 +76,8 @@ ATTENTION_SIGNATURES = {
                                                   ctypes.POINTER(_sz)]),
     "sv_chunk_attention": (_i32, [ctypes.c_char_p, _vp, _i32, _i64, _i64, _i64, _i64, _f32, _i64,
                                   _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sv_chunk_attention_gated": (_i32, [ctypes.c_char_p, _vp, _i32, _i64, _i64, _i64, _i64, _f32,
+                                        _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp, _i32, _vp]),
 }
 
 _lock = threading.Lock()

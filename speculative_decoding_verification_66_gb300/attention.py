@@ -226,6 +226,27 @@ def sv_chunk_attention(query, k_pages, v_pages, page_table, cached_lens, chunk_s
     ``scale`` defaults to head_dim ** -0.5. ``max_chunk``: an upper bound of the sequences' new
     tokens (0: tokens); a tight one lets the launches be planned for it. Returns out, or (out, lse)
     with ``return_lse`` or an ``lse`` tensor (float32 [tokens, q_heads])."""
+    return _attention(query, k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps, v_exps,
+                      scale, window, max_chunk, out, lse, return_lse, seq_status, workspace, stream)
+
+
+def sv_chunk_attention_gated(query, k_pages, v_pages, page_table, cached_lens, chunk_starts, gate, *,
+                             block: int = -1, k_exps=None, v_exps=None, scale=None,
+                             window: int = 0, max_chunk: int = 0, stream=None) -> dict:
+    """Test hook for the timeout path: sv_chunk_attention with the values' loads of one thread
+    ``block`` (negative: all) held until the device int32 ``gate`` (one element) is nonzero.
+    Returns out, lse and seq_status."""
+    if gate.dtype != torch.int32 or not gate.is_cuda or gate.numel() < 1:
+        raise ValueError("gate must be an int32 CUDA tensor")
+    status = torch.empty(cached_lens.shape, dtype=torch.int32, device=query.device)
+    out, lse = _attention(query, k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
+                          v_exps, scale, window, max_chunk, None, None, True, status, None, stream,
+                          (int(block), gate))
+    return {"out": out, "lse": lse, "seq_status": status}
+
+
+def _attention(query, k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps, v_exps, scale,
+               window, max_chunk, out, lse, return_lse, seq_status, workspace, stream, gate=None):
     cache, code, dev, B = _cache(k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps,
                                  v_exps)
     _, _, H, D = k_pages.shape
@@ -257,11 +278,16 @@ def sv_chunk_attention(query, k_pages, v_pages, page_table, cached_lens, chunk_s
         w = workspace
         if w is None:
             w = _workspace(dev, s, sv_chunk_attention_workspace_bytes(B, N, Hq, H, D, max_chunk))
-        _check(_lib.load_attention().sv_chunk_attention(
-            cache, query.data_ptr(), dtype, N, Hq, qs[0], qs[1], scale, window, max_chunk,
-            o.data_ptr(), None if z is None else z.data_ptr(), status, w.data_ptr(), w.numel(), s),
-            "sv_chunk_attention")
+        args = (cache, query.data_ptr(), dtype, N, Hq, qs[0], qs[1], scale, window, max_chunk,
+                o.data_ptr(), None if z is None else z.data_ptr(), status, w.data_ptr(), w.numel(),
+                s)
+        if gate is None:
+            _check(_lib.load_attention().sv_chunk_attention(*args), "sv_chunk_attention")
+        else:
+            _check(_lib.load_attention().sv_chunk_attention_gated(
+                *args, gate[0], gate[1].data_ptr()), "sv_chunk_attention_gated")
         return o if z is None else (o, z)
 
     return _on(dev, stream, call, (query, k_pages, v_pages, page_table, cached_lens, chunk_starts,
-                                   k_exps, v_exps, out, lse, seq_status, workspace))
+                                   k_exps, v_exps, out, lse, seq_status, workspace,
+                                   None if gate is None else gate[1]))

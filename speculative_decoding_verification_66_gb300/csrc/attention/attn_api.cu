@@ -190,11 +190,13 @@ SV_EXPORT int sv_chunk_attention_workspace_bytes(int64_t batch, int64_t tokens, 
     return SV_OK;
 }
 
-SV_EXPORT int sv_chunk_attention(const sv_paged_cache* cache, const void* query, int dtype,
-                                 int64_t tokens, int64_t q_heads, int64_t query_token_stride,
-                                 int64_t query_head_stride, float scale, int64_t window,
-                                 int64_t max_chunk, void* out, float* lse, int32_t* seq_status,
-                                 void* workspace, size_t workspace_bytes, void* stream)
+namespace {
+
+int attention(const sv_paged_cache* cache, const void* query, int dtype, int64_t tokens,
+              int64_t q_heads, int64_t query_token_stride, int64_t query_head_stride, float scale,
+              int64_t window, int64_t max_chunk, void* out, float* lse, int32_t* seq_status,
+              void* workspace, size_t workspace_bytes, void* stream, int32_t gate_block,
+              const int32_t* gate)
 {
     sva::Attn a{};
     int rc = check_cache(cache, &a.c);
@@ -231,6 +233,8 @@ SV_EXPORT int sv_chunk_attention(const sv_paged_cache* cache, const void* query,
     a.G = static_cast<int32_t>(q_heads / cache->kv_heads);
     a.scale = scale;
     a.scale_log2 = scale * 1.44269504088896341f;
+    a.gate = gate;
+    a.gate_block = gate_block;
     const bool f16 = dtype == SV_F16, e4m3 = cache->dtype == SV_E4M3;
     bool done = false;
     if (a.c.num_pages > 0) {
@@ -240,4 +244,32 @@ SV_EXPORT int sv_chunk_attention(const sv_paged_cache* cache, const void* query,
     }
     if (!done && sva::launch_attention_rows(a, f16, e4m3, s) != cudaSuccess) return SV_ERR_CUDA;
     return SV_OK;
+}
+
+}  // namespace
+
+SV_EXPORT int sv_chunk_attention(const sv_paged_cache* cache, const void* query, int dtype,
+                                 int64_t tokens, int64_t q_heads, int64_t query_token_stride,
+                                 int64_t query_head_stride, float scale, int64_t window,
+                                 int64_t max_chunk, void* out, float* lse, int32_t* seq_status,
+                                 void* workspace, size_t workspace_bytes, void* stream)
+{
+    return attention(cache, query, dtype, tokens, q_heads, query_token_stride, query_head_stride,
+                     scale, window, max_chunk, out, lse, seq_status, workspace, workspace_bytes,
+                     stream, -1, nullptr);
+}
+
+SV_EXPORT int sv_chunk_attention_gated(const sv_paged_cache* cache, const void* query, int dtype,
+                                       int64_t tokens, int64_t q_heads,
+                                       int64_t query_token_stride, int64_t query_head_stride,
+                                       float scale, int64_t window, int64_t max_chunk, void* out,
+                                       float* lse, int32_t* seq_status, void* workspace,
+                                       size_t workspace_bytes, void* stream, int32_t block,
+                                       const int32_t* gate)
+{
+    if (gate == nullptr) return SV_ERR_ARG;
+    if (!aligned(gate, 4)) return SV_ERR_ALIGN;
+    return attention(cache, query, dtype, tokens, q_heads, query_token_stride, query_head_stride,
+                     scale, window, max_chunk, out, lse, seq_status, workspace, workspace_bytes,
+                     stream, block, gate);
 }

@@ -185,6 +185,10 @@ struct Attn {
     int32_t Hq, G;
     float scale;       // the caller's
     float scale_log2;  // scale * log2(e): softmax runs in powers of two
+    // Test hook (nullptr in product calls): the values' loads of this thread block
+    // (negative: of all) are held until *gate != 0.
+    const int32_t* gate;
+    int32_t gate_block;
 };
 
 constexpr float kLn2 = 0.693147180559945309f;

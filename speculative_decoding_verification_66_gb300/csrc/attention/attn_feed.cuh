@@ -409,6 +409,19 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
     Share sh{};
     int64_t units = start.u0;
     bool ok = true;
+    if (kv == 1 && a.gate != nullptr &&
+        (a.gate_block < 0 || a.gate_block == static_cast<int>(blockIdx.x))) {
+        // Test hook: hold the values until *gate != 0, bounded like every other
+        // wait. Nothing sets it in the tests of the timeout path.
+        const volatile int32_t* gate = a.gate;
+        const long long t0 = clock64();
+        while (ok && *gate == 0) {
+            __nanosleep(1000);
+            ok = clock64() - t0 <= sv::kWaitLimitCycles;
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok) != 0;
+        if (!ok) *reinterpret_cast<volatile int*>(&ctl.stop) = 1;
+    }
     for (int item = 0; ok; ++item) {
         const Plan* g;
         if (kv == 0) {
@@ -589,11 +602,11 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
         sh.units = start.U;
         args.shares[blockIdx.x] = sh;
     }
-    if (!ok) {
-        // No copy may be under way when the block ends.
-        for (int i = 0; i < FILL; ++i)
-            if (used >> i & 1u) sv::mbar_wait_bounded(&fullbar[i], rounds >> i & 1u, nullptr);
-    }
+    // No copy may be under way when the block ends, whoever gave up a wait and when:
+    // this warp may have left at the end of its work, for lack of a plan, or before.
+    // (On the ordinary path the last tiles have come, or are about to be used.)
+    for (int i = 0; i < FILL; ++i)
+        if (used >> i & 1u) sv::mbar_wait_bounded(&fullbar[i], rounds >> i & 1u, nullptr);
 }
 
 // Joins the items that several blocks worked on, in block order: block x takes

@@ -170,3 +170,10 @@ def test_the_binding_refuses_host_tensors():
         sv.sv_chunk_attention(q, pages, pages, i32, i32[0], starts)
     with pytest.raises(ValueError):
         sv.sv_kv_append(q, q, pages, pages, i32, i32[0], starts)
+
+
+def test_the_gated_call_needs_its_gate(lib):
+    def gated(gate):
+        return lib.sv_chunk_attention_gated(cache(), P, BF16, 5, 32, 4096, 128, 0.1, 0, 0, P, 0, 0,
+                                            P, 1 << 40, 0, -1, gate)
+    assert gated(0) == ARG and gated(P + 2) == ALIGN
