@@ -404,7 +404,6 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
     const int64_t exp_step = kv ? a.c.exp_slot_stride[1] : a.c.exp_slot_stride[0];
     const int64_t exp_page = kv ? a.c.exp_page_stride[1] : a.c.exp_page_stride[0];
     Place<FILL> base_at;
-    uint32_t used = 0, rounds = 0;  // a stage's bit: filled by this warp; parity of the last fill
     Walk<R> walk(a, start);
     Share sh{};
     int64_t units = start.u0;
@@ -574,8 +573,10 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
             }
             const bool leader = needed && first_of_box;
             const unsigned boxes = __ballot_sync(0xFFFFFFFFu, leader);
-            if (lane == 0)
+            if (lane == 0) {
+                ctl.filled[at.stage] = at.round + 1;
                 sv::mbar_arrive_expect_tx(&fullbar[at.stage], __popc(boxes) * box_bytes);
+            }
             __syncwarp();
             if (leader) {
                 const int c1 = slot_of(k);
@@ -589,8 +590,6 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                 }
             }
             __syncwarp();
-            used |= 1u << at.stage;
-            rounds = (rounds & ~(1u << at.stage)) | (at.round & 1u) << at.stage;
             at.advance(kv ? ring_v_step<ALT>(k, n) : ring_k_step<ALT>(k));
             cur = next;
             next = then;
@@ -602,11 +601,18 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
         sh.units = start.U;
         args.shares[blockIdx.x] = sh;
     }
-    // No copy may be under way when the block ends, whoever gave up a wait and when:
-    // this warp may have left at the end of its work, for lack of a plan, or before.
-    // (On the ordinary path the last tiles have come, or are about to be used.)
-    for (int i = 0; i < FILL; ++i)
-        if (used >> i & 1u) sv::mbar_wait_bounded(&fullbar[i], rounds >> i & 1u, nullptr);
+}
+
+// No copy may be under way when the block ends. Where all waits came to their end
+// every tile has been used; where one ran out, whichever it was, the last copies to
+// every stage are waited for, whichever warp issued them. All threads come here when
+// the roles have met; the block's shared memory stays as long as one of them.
+template <int FILL, class Ctl>
+__device__ __forceinline__ void land(Ctl& ctl, uint64_t* fullbar)
+{
+    const int i = threadIdx.x;
+    if (ctl.stop != 0 && i < FILL && ctl.filled[i] > 0)
+        sv::mbar_wait_bounded(&fullbar[i], (ctl.filled[i] - 1) & 1u, nullptr);
 }
 
 // Joins the items that several blocks worked on, in block order: block x takes

@@ -57,6 +57,7 @@ template <int STAGES, bool E4M3>
 struct FewControl {
     uint64_t full[STAGES], empty[STAGES], sync;
     uint64_t plan_ready[kItems];
+    uint32_t filled[STAGES];  // how often the loads have filled a stage
     int stop;
     Start start;
     int64_t sums[kFewThreads / 32];
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     sv::pdl_trigger();
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
+            ctl.filled[i] = 0;
             sv::mbar_init(&ctl.full[i], 1);
             sv::mbar_init(&ctl.empty[i], kWorkers);
         }
@@ -612,6 +614,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     __syncthreads();
     if (threadIdx.x == 0) args.shares[blockIdx.x].failed = *stop;
+    land<S>(ctl, ctl.full);
 }
 
 template <class T, int DP, bool E4M3>

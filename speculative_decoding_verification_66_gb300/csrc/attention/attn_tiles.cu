@@ -102,6 +102,7 @@ struct Control {
     uint64_t raw_full[RAW > 0 ? RAW : 1], raw_empty[RAW > 0 ? RAW : 1];
     uint64_t s_full[2], p_ready[2], q_ready, q_free, o_full, o_free, s_free, ml_ready, done;
     uint64_t plan_ready[kItems];
+    uint32_t filled[RAW > 0 ? RAW : STAGES];  // how often the loads have filled a stage
     uint32_t tmem;
     int stop;
     int burst;  // PAIR: a slot's products are under way
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             sv::mbar_init(&ctl.raw_full[i], 1);
             sv::mbar_init(&ctl.raw_empty[i], X::kHelpers);
         }
+        for (int i = 0; i < kFill; ++i) ctl.filled[i] = 0;
         for (int i = 0; i < 2; ++i) {
             sv::mbar_init(&ctl.s_full[i], 1);
             sv::mbar_init(&ctl.p_ready[i], 4);
@@ -772,6 +774,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
     }
     __syncthreads();
     if (threadIdx.x == 0) args.shares[blockIdx.x].failed = *stop;
+    land<kFill>(ctl, E4M3 ? ctl.raw_full : ctl.full);
     if (warp == 8) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)

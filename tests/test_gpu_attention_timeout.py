@@ -52,6 +52,20 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(T, d, e4m3,
     assert torch.equal(r["out"], want[0]) and torch.equal(r["lse"], want[1])
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,d", SHAPES)
+def test_no_ordinary_call_waits_for_its_limit(T, d, e4m3):
+    c, q, kw = case(T, d, e4m3)
+    sv.sv_chunk_attention(q, *c.args(), **kw)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    for _ in range(3):
+        sv.sv_chunk_attention(q, *c.args(), **kw)
+    end.record()
+    torch.cuda.synchronize()
+    assert begin.elapsed_time(end) < 1000.0  # a wait's limit is about 2000
+
+
 def test_refusals():
     c, q, kw = case(1, 64, False)
     with pytest.raises(ValueError):
