@@ -41,6 +41,9 @@
  *   SV_SEQ_BAD_PAGE    a page outside [0, num_pages) among those needed.
  *                      Its tokens are not written; output rows that would read
  *                      it are NaN.
+ *   SV_SEQ_TIMEOUT     (spec_verify.h's) a wait inside the attention ran out
+ *                      (about 2 s; never in ordinary operation). It is reported
+ *                      for every sequence, and every output of the call is NaN.
  * seq_status, where given, receives 0 or these bits for every sequence.
  *
  * Return codes are spec_verify.h's SV_OK and SV_ERR_*. All calls are
@@ -157,8 +160,9 @@ int sv_chunk_attention(const sv_paged_cache* cache, const void* query, int dtype
  * Test hook for the timeout path: sv_chunk_attention with the values' loads of
  * one thread block held until the device int32 *gate becomes nonzero. That wait
  * is bounded like every other wait in the kernels (about 2 s). When it runs out
- * the thread block gives up and returns with no copy in flight, and every
- * sequence of the call is reported as SV_SEQ_TIMEOUT. The context stays usable.
+ * the thread block gives up and returns with no copy in flight, every sequence of
+ * the call is reported as SV_SEQ_TIMEOUT and every output is NaN. The context
+ * stays usable.
  * A caller that sets *gate before the wait runs out gets the ordinary results.
  *   block  the thread block, 0 .. SMs - 1; negative: all of them.
  *   gate   device int32, 4-byte aligned (SV_ERR_ARG if NULL, SV_ERR_ALIGN).

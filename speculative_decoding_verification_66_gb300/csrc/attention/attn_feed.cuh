@@ -62,6 +62,7 @@ struct Tiles {
     Attn a;
     float* part;   // [blocks][2][rows][part_cols]: unnormalised O, then m and l
     Share* shares; // [blocks]
+    int32_t* failed;  // [blocks]: a bounded wait ran out in this block
     int32_t part_rows;
     int32_t swizzled;  // e4m3 rows of 128 or 64 bytes lie swizzled (few rows)
 };
@@ -71,6 +72,7 @@ struct Tiles {
 constexpr int kPanel = kTile * 128;
 
 constexpr size_t kShareBytes = (sizeof(Share) * kMaxBlocks + 255) / 256 * 256;
+constexpr size_t kFailedBytes = (sizeof(int32_t) * kMaxBlocks + 255) / 256 * 256;
 
 // Which 16 bytes of a row of codes hold chunk `ch`: swizzled as bulk tensor copies
 // do it, rows of 128 bytes by the row, of 64 bytes by every second row.
@@ -617,7 +619,9 @@ __device__ __forceinline__ void land(Ctl& ctl, uint64_t* fullbar)
 
 // Joins the items that several blocks worked on, in block order: block x takes
 // the item that block x of the tile kernel began and did not finish, a warp a
-// row.
+// row. Where a wait ran out in block x, its column fills all outputs with NaN; no
+// other column may write then, so each looks at all blocks first (they lie side by
+// side: two loads a thread, which the share's covers).
 template <class T, int DP>
 __global__ void __launch_bounds__(128) join_kernel(const Tiles args, int blocks)
 {
@@ -625,8 +629,11 @@ __global__ void __launch_bounds__(128) join_kernel(const Tiles args, int blocks)
     const int lane = threadIdx.x & 31;
     sv::pdl_wait();
     const Share sh = args.shares[blockIdx.x];
+    const bool failed = args.failed[blockIdx.x] != 0;
+    bool any_failed = false;
+    for (int i = threadIdx.x; i < blocks; i += 128) any_failed |= args.failed[i] != 0;
     const float nan = __uint_as_float(0x7FFFFFFFu);
-    if (sh.failed) {
+    if (failed) {
         // A wait ran out: no output of this call can be trusted.
         const int64_t n = static_cast<int64_t>(gridDim.y) * blockDim.x;
         const int64_t i0 = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x;
@@ -638,7 +645,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Tiles args, int blocks)
             for (int64_t i = i0; i < a.c.B; i += n) atomicOr(a.status + i, kTimeout);
         return;
     }
-    if (!sh.leads) return;
+    if (!sh.leads || __syncthreads_or(any_failed)) return;
     const int r = blockIdx.y * (blockDim.x / 32) + (threadIdx.x >> 5);
     if (r >= sh.rows) return;
     constexpr int kPer = DP / 32;
@@ -787,8 +794,10 @@ cudaError_t set_up(const Attn& a, bool f16, bool e4m3, int64_t rows, void* works
         return e;
     *blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
     *t = Tiles{a,
-               reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kShareBytes),
+               reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kShareBytes +
+                                        kFailedBytes),
                static_cast<Share*>(workspace),
+               reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kShareBytes),
                static_cast<int32_t>(rows),
                swizzled ? 1 : 0};
     return cudaSuccess;

@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) args.shares[blockIdx.x].failed = *stop;
+    if (threadIdx.x == 0) args.failed[blockIdx.x] = *stop;
     land<S>(ctl, ctl.full);
 }
 

@@ -25,7 +25,6 @@ struct Share {
     int32_t b, h, row0, rows;
     int32_t q0;     // first packed row of the sequence
     int32_t last;   // the block that finished it
-    int32_t failed; // a bounded wait ran out in this block
     int64_t units;  // U
 };
 

@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) args.shares[blockIdx.x].failed = *stop;
+    if (threadIdx.x == 0) args.failed[blockIdx.x] = *stop;
     land<kFill>(ctl, E4M3 ? ctl.raw_full : ctl.full);
     if (warp == 8) {
         fence_after();
@@ -832,7 +832,8 @@ size_t tiles_workspace(int64_t max_chunk, int64_t G, int64_t D)
 {
     const int64_t dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
     const int64_t rows = item_rows(max_chunk, G, D <= kMaxTileDim ? 256 : kFewRows);
-    return kShareBytes + static_cast<size_t>(kMaxBlocks) * 2 * rows * (dp + 4) * sizeof(float);
+    return kShareBytes + kFailedBytes +
+           static_cast<size_t>(kMaxBlocks) * 2 * rows * (dp + 4) * sizeof(float);
 }
 
 cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* workspace,

@@ -66,6 +66,18 @@ def test_no_ordinary_call_waits_for_its_limit(T, d, e4m3):
     assert begin.elapsed_time(end) < 1000.0  # a wait's limit is about 2000
 
 
+@pytest.mark.parametrize("T,d", SHAPES)
+def test_one_block_that_gives_up_makes_every_output_nan(T, d):
+    """Also the rows that other blocks finished or join from that block's unwritten share, which the
+    call before left there."""
+    c, q, kw = case(T, d, False)
+    for block in (0, 33, 150):
+        sv.sv_chunk_attention(q, *c.args(), **kw)
+        gate = torch.zeros(1, dtype=torch.int32, device="cuda")
+        r = sv.sv_chunk_attention_gated(q, *c.args(), gate, block=block, **kw)
+        assert r["out"].isnan().all() and r["lse"].isnan().all()
+
+
 def test_refusals():
     c, q, kw = case(1, 64, False)
     with pytest.raises(ValueError):
