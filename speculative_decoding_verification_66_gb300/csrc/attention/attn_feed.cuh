@@ -215,6 +215,15 @@ __device__ __forceinline__ float moved(int ref, int top)
     return ref == 0 ? 1.f : exp_value(static_cast<uint32_t>(max(min(127 + ref - top, 227), 27)));
 }
 
+// The factor of a row's scores: the queries' and the keys' powers of two and the
+// scale. Where these multiply to nothing (a row of zeros, keys of zeros) a hidden
+// score's -inf times zero would be NaN. Scores are below 2^31 before this factor, so
+// the least normal number in the place of a smaller one moves none by 2^-95.
+__device__ __forceinline__ float score_factor(float c)
+{
+    return fmaxf(c, __uint_as_float(0x00800000u));
+}
+
 __device__ __forceinline__ bool any_special(uint4 w, uint32_t exponent)
 {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};

@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 pos[i] = p.cached + (p.row0 + r) / a.G;
                 low[i] = a.window > 0 ? pos[i] - static_cast<int>(a.window) + 1 : INT_MIN / 2;
                 cs[i] = a.scale_log2;
-                if constexpr (E4M3 && std::is_same<T, Bf16>::value) cs[i] *= ctl.q_scale[r];
+                if constexpr (E4M3 && std::is_same<T, Bf16>::value) cs[i] = score_factor(cs[i] * ctl.q_scale[r]);
                 m[i] = ninf;
                 l[i] = 0.f;
             }

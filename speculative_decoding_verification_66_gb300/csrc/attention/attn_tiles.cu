@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         bool move = false;
                         float keep_v = 1.f;
                         if (E4M3) {
-                            c = row_c * ctl.k_scale[(tiles_before + k) & 3];
+                            c = score_factor(row_c * ctl.k_scale[(tiles_before + k) & 3]);
                             const int top = ctl.v_top[(tiles_before + k) & 3];
                             if ((move = moves(ref, top))) {
                                 keep_v = moved(ref, top);

@@ -1,0 +1,128 @@
+"""sv_chunk_attention over e4m3 caches where sizes differ as far as the types allow: against the
+definition in 64 bits, every key with a bound from its own products."""
+import math
+
+import pytest
+import torch
+
+import speculative_decoding_verification_66_gb300 as sv
+from attention_util import Cache, half_step, quantise
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sv.load_attention()
+    torch.cuda.set_device(0)
+
+
+def reference(cache, query, scale, window=0):
+    """out, lse and their bounds, from the definition in 64 bits. With p the weights, A = sum p |v|,
+    n keys, d the head size, u half a step of the output's type:
+      ds_j = (d + 8) 2^-24 scale sum |q k_j|       the products' sum in float32
+             + 2^-22 |s_j|                        the scaling and the subtraction of the maximum
+             + 2^-38 scale max |q| sum |k_j|      bfloat16 queries held as float16
+      sum p (e^ds - 1) |v| + A sum p (e^ds - 1)   weights and normaliser
+      u |out| + u A                               the output's and the weights' rounding
+      ((n + d) 2^-23 + 2^-20) A                   sums, exponentials and the division
+      2^-27 sum |v|                               float16 weights far below the row's largest
+    and for lse: sum p ds + n 2^-24 + 2^-22 (1 + |lse|)."""
+    N, Hq, d = query.shape
+    G = Hq // cache.heads
+    out = torch.empty((N, Hq, d), dtype=torch.float64, device=query.device)
+    lse = torch.empty((N, Hq), dtype=torch.float64, device=query.device)
+    tol, tol_lse = torch.empty_like(out), torch.empty_like(lse)
+    u, r = half_step(query.dtype), 0
+    for b in range(len(cache.lens)):
+        total = cache.lens[b] + cache.chunks[b]
+        k, v = cache.dense(0, b, total), cache.dense(1, b, total)
+        for t in range(cache.chunks[b]):
+            p = cache.lens[b] + t
+            lo = max(0, p - window + 1) if window else 0
+            kk = k[lo:p + 1].repeat_interleave(G, 1)
+            vv = v[lo:p + 1].repeat_interleave(G, 1)
+            q = query[r].double()
+            prod = kk * q
+            s = prod.sum(-1) * scale
+            z = torch.logsumexp(s, 0)
+            w = torch.exp(s - z)
+            ds = (d + 8) * 2.0 ** -24 * scale * prod.abs().sum(-1) + 2.0 ** -22 * s.abs() \
+                + 2.0 ** -38 * scale * q.abs().amax(-1) * kk.abs().sum(-1)
+            o = (w.unsqueeze(-1) * vv).sum(0)
+            a = (w.unsqueeze(-1) * vv.abs()).sum(0)
+            off = w * torch.expm1(ds.clamp(max=50.0))
+            n = p + 1 - lo
+            out[r], lse[r] = o, z
+            tol[r] = (off.unsqueeze(-1) * vv.abs()).sum(0) + a * off.sum(0).unsqueeze(-1) \
+                + u * o.abs() + (u + (n + d) * 2.0 ** -23 + 2.0 ** -20) * a \
+                + 2.0 ** -27 * vv.abs().sum(0)
+            tol_lse[r] = (w * ds).sum(0) + n * 2.0 ** -24 + 2.0 ** -22 * (1 + z.abs())
+            r += 1
+    return out, lse, tol, tol_lse
+
+
+def quantised(c):
+    """The 16-bit cache c as an e4m3 cache."""
+    for i in range(2):
+        code, c.exps[i] = quantise(c.parts[i])
+        c.parts[i] = code.view(torch.float8_e4m3fn)
+    c.e4m3 = True
+    return c
+
+
+def places(c, b, n):
+    p = torch.arange(n, device="cuda")
+    return c.table[b].long()[p // c.page], p % c.page
+
+
+def scale_by(c, i, size):
+    """Position p of sequence 0's keys (i = 0) or values (1) times size[p]."""
+    at = places(c, 0, len(size))
+    x = c.parts[i][at].double() * size.double()[:, None, None]
+    c.parts[i][at] = x.to(c.dtype)
+
+
+def queries(c, G, spread=1.0, seed=3):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(c.tokens, c.heads * G, c.d, generator=g).double() * spread
+    return x.to(c.dtype).cuda()
+
+
+def agrees(c, q, T, window=0, scale=None):
+    scale = c.d ** -0.5 if scale is None else scale
+    status = torch.empty(len(c.lens), dtype=torch.int32, device="cuda")
+    out, lse = sv.sv_chunk_attention(q, *c.args(), **c.exp_args(), window=window, max_chunk=T,
+                                     scale=scale, return_lse=True, seq_status=status)
+    assert not status.any()
+    ref, z, tol, tol_z = reference(c, q, scale, window)
+    assert out.isfinite().all() and lse.isfinite().all()
+    err = (out.double() - ref).abs()
+    assert (err <= tol).all(), f"out: worst {float((err / tol).max()):.3g} x"
+    err = (lse.double() - z).abs()
+    assert (err <= tol_z).all(), f"lse: worst {float((err / tol_z).max()):.3g} x"
+
+
+# New tokens of four heads a key head, and the head size: 4, 16, 20 and 300 rows.
+ROWS = [(1, 128), (4, 64), (4, 128), (5, 64), (5, 128), (75, 128), (5, 256)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,d", ROWS)
+@pytest.mark.parametrize("keys", [0.0, 2.0 ** -14, 2.0 ** -60, 2.0 ** -112])
+def test_zero_and_tiny_queries_and_keys(dtype, T, d, keys):
+    """Rows of zeros, of 2^-20 and of ordinary size, over keys of zeros and next to nothing: the
+    weights are all alike, whatever the product of the scales is."""
+    c = Cache([290, 3], [T, T], 2, d, 16, dtype, False, seed=T)
+    for b in range(2):
+        at = places(c, b, c.lens[b] + T)
+        c.parts[0][at] = (c.parts[0][at].double() * keys).to(c.dtype)
+    q = queries(c, 4).double()
+    q[:, 0] = 0.0
+    q[:, 1] *= 2.0 ** -20
+    q[:, 5] = 0.0
+    agrees(quantised(c), q.to(c.dtype), T)
+    # A scale that is next to nothing.
+    agrees(c, q.to(c.dtype), T, scale=1e-37)
