@@ -36,7 +36,7 @@ __device__ __forceinline__ float rise()
 // outputs' reference, which follows the tiles when they are more than kLift above
 // or kSink below.
 constexpr int kLift = 7, kSink = 2;
-// Values of one tile may be this many powers of two apart (see code_factor).
+// Keys or values of one tile may be this many powers of two apart (see code_factor).
 constexpr int kSpread = 13;
 
 constexpr int kMaxBlocks = 160;  // shares in the workspace; grids are no larger
@@ -562,7 +562,9 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                     for (int i = 0; i < 4; ++i)
                         if (hidden >> i & 1u) f[i] = 0;
                 }
-                if (kv == 1 && apart) note(0, kNoted + 1);  // all rows again
+                // All rows again (FEW: the keys' codes go into the products as they
+                // are, each with a factor of its own).
+                if (apart && (kv == 1 || !FEW)) note(0, kNoted + 1);
                 if constexpr (FEW) {
                     if (kv == 0)
                         *reinterpret_cast<uint4*>(&ctl.scale[at.stage][lane * 4]) =

@@ -51,8 +51,9 @@
 // tile's exponents come back in where they cost nothing: the keys' in the scale of
 // the tile's scores, the values' in the exponent of its weights, which are
 // float16 too; O is kept relative to a reference exponent that follows the
-// tiles'. Values of a tile that are more than 2^13 apart would lose bits; a
-// segment that has such a tile computes its rows again, key by key. bfloat16
+// tiles'. Keys or values of a tile that are more than 2^13 apart would lose bits (a
+// key that a row does not see could take them from those that it does); a segment
+// that has such a tile computes its rows again, key by key. bfloat16
 // queries become float16, each row scaled by a power of two that brings its
 // largest element to [2^14, 2^15): exact down to 2^-38 of that.
 //

@@ -91,12 +91,17 @@ def queries(c, G, spread=1.0, seed=3):
     return x.to(c.dtype).cuda()
 
 
-def agrees(c, q, T, window=0, scale=None):
+def agrees(c, q, T, window=0, scale=None, times=1):
+    """The call on c's two sequences of T new tokens, `times` times over the same pages: with many a
+    thread block works through several tiles of one sequence, with few every tile has a block."""
     scale = c.d ** -0.5 if scale is None else scale
-    status = torch.empty(len(c.lens), dtype=torch.int32, device="cuda")
-    out, lse = sv.sv_chunk_attention(q, *c.args(), **c.exp_args(), window=window, max_chunk=T,
-                                     scale=scale, return_lse=True, seq_status=status)
+    status = torch.empty(2 * times, dtype=torch.int32, device="cuda")
+    starts = torch.arange(0, 2 * times * T + 1, T, dtype=torch.int32, device="cuda")
+    out, lse = sv.sv_chunk_attention(
+        q.repeat(times, 1, 1), *c.parts, c.table.repeat(times, 1), c.cached.repeat(times), starts,
+        **c.exp_args(), window=window, max_chunk=T, scale=scale, return_lse=True, seq_status=status)
     assert not status.any()
+    out, lse = out.view(times, *q.shape), lse.view(times, *q.shape[:2])
     ref, z, tol, tol_z = reference(c, q, scale, window)
     assert out.isfinite().all() and lse.isfinite().all()
     err = (out.double() - ref).abs()
@@ -126,3 +131,25 @@ def test_zero_and_tiny_queries_and_keys(dtype, T, d, keys):
     agrees(quantised(c), q.to(c.dtype), T)
     # A scale that is next to nothing.
     agrees(c, q.to(c.dtype), T, scale=1e-37)
+
+
+@pytest.mark.parametrize("T,d", ROWS)
+@pytest.mark.parametrize("k", [13, 14, 16, 24, 26, 30, 60])
+def test_a_key_far_above_the_others(T, d, k):
+    """One key 2^k times the others: seen by queries that are zero where it is large; and hidden from
+    the rows before it."""
+    c = Cache([290, 3], [T, T], 2, d, 16, "bf16", False, seed=k)
+    page, slot = c.table[0].long()[260 // 16], 260 % 16
+    c.parts[0][page, slot, :, 5] = 2.0 ** k
+    q = queries(c, 4)
+    q[:, :, 5] = 0.0
+    agrees(quantised(c), q, T)
+    c = Cache([290, 3], [T, T], 2, d, 16, "bf16", False, seed=k + 1)
+    size = torch.ones(290 + T, device="cuda")
+    size[-1] = 2.0 ** k
+    scale_by(c, 0, size)
+    q = queries(c, 4)
+    q[T - 1] = 0.0  # (the row that sees it: its score would be all there is)
+    agrees(quantised(c), q, T)
+    agrees(c, q, T, window=100)
+    agrees(c, q, T, times=100)
