@@ -203,12 +203,33 @@ __device__ __forceinline__ void expand(uint4 codes, uint32_t f, uint32_t (&o)[8]
         o[2 * i + 1] = mul2(s.y, f);
     }
 }
+// Exponent bytes up to kLeast stand for vectors of zeros, nearly always, and for
+// vectors of next to nothing (up to 448 2^-117). Zeros must not move a tile's or the
+// outputs' exponent, so these vectors are left out there and have the factor kUnless:
+// minus zero, which is right unless a code says otherwise. Whoever reads the codes
+// looks at those rows, and where one is not zero all rows are computed again.
+constexpr uint32_t kLeast = 10, kUnless = 0x8000u;
+// Codes under a factor (a half): zeros where the row is hidden, whatever they are, and
+// where the factor is kUnless; then true if they were no zeros.
+template <int N>
+__device__ __forceinline__ bool look_at_codes(uint32_t (&codes)[N], uint32_t factor)
+{
+    bool any = false;
+    if (factor == 0u || factor == kUnless) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            any |= (codes[i] & 0x7F7F7F7Fu) != 0;
+            codes[i] = 0;
+        }
+    }
+    return any && factor == kUnless;
+}
 // Whether the outputs' reference exponent (0: none yet) has to move to a tile's,
-// and the power of two that the outputs are then multiplied by. Tiles whose
-// values are all zero (exponent 10, or 0: none visible) do not count.
+// and the power of two that the outputs are then multiplied by. Tiles that have no
+// values above kLeast (0: none visible) do not count.
 __device__ __forceinline__ bool moves(int ref, int top)
 {
-    return top > 10 && (ref == 0 || top - ref > kLift || ref - top > kSink);
+    return top > static_cast<int>(kLeast) && (ref == 0 || top - ref > kLift || ref - top > kSink);
 }
 __device__ __forceinline__ float moved(int ref, int top)
 {
@@ -396,8 +417,8 @@ __device__ __forceinline__ const Plan* plan_at(Ctl& ctl, int i, Wait& wait_all)
 // Copies of keys (kv = 0) or values (1), by a warp; the keys' warp also plans the
 // segments. e4m3: the factors that the codes are multiplied by (FEW: of keys, the
 // powers of two themselves; of values, as halves), and with the keys the largest
-// exponents of the tile's keys and values (FEW: with the values, of these). The
-// page of tile k + 2 and the exponents of tile k + 1 are on their way while tile k
+// exponents of the tile's keys and values (FEW: with the values, of these), plus 256
+// where some row's codes have to be looked at (look_at_codes). The page of tile k + 2 and the exponents of tile k + 1 are on their way while tile k
 // is issued.
 template <class T, int DP, bool E4M3, int R, bool SPLIT, bool ALT, int FILL, bool FEW, class Ctl,
           class Wait>
@@ -551,17 +572,23 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                 }
                 if (!FEW || kv == 1) top = __reduce_max_sync(0xFFFFFFFFu, top);
                 bool apart = false;  // further than float16 holds
+                bool looks = false;  // some row's codes have to be looked at
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t e = xc.e[i];
                     f[i] = FEW && kv == 0 ? __float_as_uint(exp_value(e)) : code_factor(e, top);
-                    apart |= e > 10 && e + kSpread < top;
+                    const bool least = e <= kLeast && (kv == 1 || e + kSpread < top);
+                    if ((!FEW || kv == 1) && least) f[i] = both(kUnless);
+                    looks |= least;
+                    apart |= e > kLeast && e + kSpread < top;
                 }
                 if (hidden != 0) {
+                    looks = true;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (hidden >> i & 1u) f[i] = 0;
                 }
+                looks = __any_sync(0xFFFFFFFFu, looks) != 0;
                 // All rows again (FEW: the keys' codes go into the products as they
                 // are, each with a factor of its own).
                 if (apart && (kv == 1 || !FEW)) note(0, kNoted + 1);
@@ -577,10 +604,10 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                         make_uint4(f[0], f[1], f[2], f[3]);
                 }
                 if constexpr (FEW) {
-                    if (kv == 1 && lane == 0) ctl.top[at.stage] = top;
-                } else if (kv == 0) {
-                    v_top = __reduce_max_sync(0xFFFFFFFFu, v_top);
-                    if (lane == 0) ctl.top[at.stage] = make_uint2(top, v_top);
+                    if (kv == 1 && lane == 0) ctl.top[at.stage] = top | (looks ? 256u : 0u);
+                } else {
+                    if (kv == 0) v_top = __reduce_max_sync(0xFFFFFFFFu, v_top);
+                    if (lane == 0) ctl.top[at.stage] = make_uint2(top | (looks ? 256u : 0u), v_top);
                 }
                 __syncwarp();
             }

@@ -118,8 +118,8 @@ struct Control {
     // .. of the last four tiles: the keys' power of two, the values' exponent
     float k_scale[4];
     int v_top[4];
-    // e4m3, for every raw stage: the rows' factors; the exponents of its keys and
-    // of the values that belong to them.
+    // e4m3, for every raw stage: the rows' factors; the exponents of its keys (or
+    // values; plus 256: see look_at_codes) and of the values that belong to them.
     alignas(16) uint32_t factor[RAW > 0 ? RAW : 1][RAW > 0 ? kTile : 4];
     uint2 top[RAW > 0 ? RAW : 1];
 };
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                                 keep_v = moved(ref, top);
                                 ref = top;
                             }
-                            lift = top > 10 ? top - ref : 0;
+                            lift = top > static_cast<int>(kLeast) ? top - ref : 0;
                         }
                         if (masked) {
 #pragma unroll 1
@@ -731,12 +731,12 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const uint32_t from = raw + row0 * a.c.D + (in_row ? piece * 16 : 0);
                     const uint32_t to = dst + tile_chunk(row0, piece * 2);
                     const uint32_t* factor = &ctl.factor[raw_at.stage][row0];
+                    const uint2 top = ctl.top[raw_at.stage];
+                    const bool looks = top.x >= 256u;
                     if (!is_v && tid == 0) {
-                        const uint2 top = ctl.top[raw_at.stage];
-                        ctl.k_scale[k_tiles & 3] = exp_value(top.x);
+                        ctl.k_scale[k_tiles & 3] = exp_value(top.x & 255u);
                         ctl.v_top[k_tiles & 3] = static_cast<int>(top.y);
                     }
-                    const bool ragged = k < inner_lo || k > inner_hi;
                     constexpr int kBatch = kTile / kStep < 4 ? kTile / kStep : 4;
 #pragma unroll 1
                     for (int r = 0; r < kTile; r += kBatch * kStep) {
@@ -750,10 +750,10 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         }
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
-                            // (a factor of zero: hidden, whatever the codes are)
-                            if (ragged && f[u] == 0u) codes[u] = make_uint4(0, 0, 0, 0);
-                            uint32_t o[8];
-                            expand(codes[u], f[u], o);
+                            uint32_t c[4] = {codes[u].x, codes[u].y, codes[u].z, codes[u].w}, o[8];
+                            if (looks && look_at_codes(c, f[u] & 0xFFFFu))
+                                atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
+                            expand(make_uint4(c[0], c[1], c[2], c[3]), f[u], o);
                             // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
                             const uint32_t t = to + (r + u * kStep) * 128;
                             st_shared_v4(t, make_uint4(o[0], o[1], o[2], o[3]));

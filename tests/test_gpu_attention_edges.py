@@ -153,3 +153,35 @@ def test_a_key_far_above_the_others(T, d, k):
     agrees(quantised(c), q, T)
     agrees(c, q, T, window=100)
     agrees(c, q, T, times=100)
+
+
+@pytest.mark.parametrize("T,d", ROWS)
+@pytest.mark.parametrize("kind", ["all", "first", "last", "mixed"])
+@pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** -114])
+def test_values_next_to_nothing(T, d, kind, size):
+    """Values of 2^-110 and less, whose exponent is the least that a cache holds, alone, in tiles before and
+    after ordinary ones, and among them."""
+    n = 700 + T
+    c = Cache([700, 3], [T, T], 2, d, 16, "bf16", False, seed=5)
+    p = torch.arange(n, device="cuda")
+    tiny = {"all": p >= 0, "first": p < 300, "last": p >= 300, "mixed": p % 3 == 0}[kind]
+    scale_by(c, 1, torch.where(tiny, size, 1.0))
+    q = queries(c, 4)
+    agrees(quantised(c), q, T)
+    agrees(c, q, T, times=100)
+
+
+@pytest.mark.parametrize("T,d", ROWS)
+def test_keys_next_to_nothing_under_large_queries(T, d):
+    """Scores of ordinary size from keys of 2^-112 and queries of 2^110; the last key, of ordinary
+    size, is hidden from the rows before it."""
+    c = Cache([290, 3], [T, T], 2, d, 16, "bf16", False, seed=5)
+    size = torch.full((290 + T,), 2.0 ** -112, device="cuda")
+    if T > 1:
+        size[-1] = 1.0
+    scale_by(c, 0, size)
+    q = queries(c, 4, 2.0 ** 110)
+    q[T:] = (q[T:].double() * 2.0 ** -110).to(q.dtype)
+    if T > 1:
+        q[T - 1] = 0.0
+    agrees(quantised(c), q, T)
