@@ -38,6 +38,10 @@ __device__ __forceinline__ float rise()
 constexpr int kLift = 7, kSink = 2;
 // Keys or values of one tile may be this many powers of two apart (see code_factor).
 constexpr int kSpread = 13;
+// The values of a segment's tiles may be this many powers of two apart: outputs that
+// follow them stay below 2^127 (values 2^9, weights 2^8, 2^30 keys), and moved() is
+// exact. Beyond, the segment's rows are computed again.
+constexpr int kFar = 60;
 
 constexpr int kMaxBlocks = 160;  // shares in the workspace; grids are no larger
 constexpr size_t kMaxSmem = 232448;
@@ -503,6 +507,7 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                        ? a.c.table[page_row + (p >> a.c.page_shift)]
                        : INT_MIN;
         };
+        int v_low = 256, v_high = 0;  // e4m3: the values' exponents so far
         auto good = [&](int32_t page) { return page >= 0 && page < a.c.num_pages; };
         auto slot_of = [&](int k) { return (k * kTile + lane * 4 + in_page0) & (P - 1); };
         struct Exps {
@@ -592,6 +597,15 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                 // All rows again (FEW: the keys' codes go into the products as they
                 // are, each with a factor of its own).
                 if (apart && (kv == 1 || !FEW)) note(0, kNoted + 1);
+                if (!FEW && kv == 0) v_top = __reduce_max_sync(0xFFFFFFFFu, v_top);
+                if (kv == (FEW ? 1 : 0)) {
+                    const int of_values = static_cast<int>(FEW ? top : v_top);
+                    if (of_values > static_cast<int>(kLeast)) {
+                        v_low = min(v_low, of_values);
+                        v_high = max(v_high, of_values);
+                        if (lane == 0 && v_high - v_low > kFar) note(0, kNoted + 1);
+                    }
+                }
                 if constexpr (FEW) {
                     if (kv == 0)
                         *reinterpret_cast<uint4*>(&ctl.scale[at.stage][lane * 4]) =
@@ -606,7 +620,6 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                 if constexpr (FEW) {
                     if (kv == 1 && lane == 0) ctl.top[at.stage] = top | (looks ? 256u : 0u);
                 } else {
-                    if (kv == 0) v_top = __reduce_max_sync(0xFFFFFFFFu, v_top);
                     if (lane == 0) ctl.top[at.stage] = make_uint2(top | (looks ? 256u : 0u), v_top);
                 }
                 __syncwarp();

@@ -185,3 +185,19 @@ def test_keys_next_to_nothing_under_large_queries(T, d):
     if T > 1:
         q[T - 1] = 0.0
     agrees(quantised(c), q, T)
+
+
+@pytest.mark.parametrize("T,d", ROWS)
+@pytest.mark.parametrize("steps", [(80, -70), (-70, 80), (80, 30, -20, -70), (-70, -20, 30, 80),
+                                   (20, -38), (0, 80, 0)])
+@pytest.mark.parametrize("length", [300, 384])
+def test_tiles_of_values_far_apart(T, d, steps, length):
+    """Values of one size along 300 or 384 (three tiles of) tokens and of another, up to 2^150 times or
+    a part of it, along the next: the outputs are of the largest size."""
+    n = length * len(steps)
+    c = Cache([n - T, 3], [T, T], 2, d, 16, "bf16", False, seed=5)
+    p = torch.arange(n, device="cuda")
+    scale_by(c, 1, torch.exp2(torch.tensor(steps, device="cuda").double()[p // length]))
+    q = queries(c, 4)
+    agrees(quantised(c), q, T)
+    agrees(c, q, T, times=100)
