@@ -209,24 +209,16 @@ __device__ __forceinline__ void expand(uint4 codes, uint32_t f, uint32_t (&o)[8]
 }
 // Exponent bytes up to kLeast stand for vectors of zeros, nearly always, and for
 // vectors of next to nothing (up to 448 2^-117). Zeros must not move a tile's or the
-// outputs' exponent, so these vectors are left out there and have the factor kUnless:
-// minus zero, which is right unless a code says otherwise. Whoever reads the codes
-// looks at those rows, and where one is not zero all rows are computed again.
+// outputs' exponent, so these vectors are left out there. Somebody looks at their
+// codes, and where one is not zero all rows are computed again: with few rows the
+// loads, from memory, behind the workers' backs (131k keys 231 us; anywhere in the
+// workers' loop 240 and more, against 229 without); in the tile kernel, whose loading
+// warps have no registers for it (256 x 9 tokens 753 us), the helpers, whom a factor of
+// minus zero tells which rows (660, against 655 without).
 constexpr uint32_t kLeast = 10, kUnless = 0x8000u;
-// Codes under a factor (a half): zeros where the row is hidden, whatever they are, and
-// where the factor is kUnless; then true if they were no zeros.
-template <int N>
-__device__ __forceinline__ bool look_at_codes(uint32_t (&codes)[N], uint32_t factor)
+__device__ __forceinline__ bool not_zeros(uint4 codes)
 {
-    bool any = false;
-    if (factor == 0u || factor == kUnless) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            any |= (codes[i] & 0x7F7F7F7Fu) != 0;
-            codes[i] = 0;
-        }
-    }
-    return any && factor == kUnless;
+    return ((codes.x | codes.y | codes.z | codes.w) & 0x7F7F7F7Fu) != 0;
 }
 // Whether the outputs' reference exponent (0: none yet) has to move to a tile's,
 // and the power of two that the outputs are then multiplied by. Tiles that have no
@@ -422,7 +414,7 @@ __device__ __forceinline__ const Plan* plan_at(Ctl& ctl, int i, Wait& wait_all)
 // segments. e4m3: the factors that the codes are multiplied by (FEW: of keys, the
 // powers of two themselves; of values, as halves), and with the keys the largest
 // exponents of the tile's keys and values (FEW: with the values, of these), plus 256
-// where some row's codes have to be looked at (look_at_codes). The page of tile k + 2 and the exponents of tile k + 1 are on their way while tile k
+// where the codes of rows with the factor kUnless have to be looked at. The page of tile k + 2 and the exponents of tile k + 1 are on their way while tile k
 // is issued.
 template <class T, int DP, bool E4M3, int R, bool SPLIT, bool ALT, int FILL, bool FEW, class Ctl,
           class Wait>
@@ -577,23 +569,36 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                 }
                 if (!FEW || kv == 1) top = __reduce_max_sync(0xFFFFFFFFu, top);
                 bool apart = false;  // further than float16 holds
-                bool looks = false;  // some row's codes have to be looked at
+                bool looks = false;  // !FEW: some rows' codes have to be looked at
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t e = xc.e[i];
                     f[i] = FEW && kv == 0 ? __float_as_uint(exp_value(e)) : code_factor(e, top);
-                    const bool least = e <= kLeast && (kv == 1 || e + kSpread < top);
-                    if ((!FEW || kv == 1) && least) f[i] = both(kUnless);
-                    looks |= least;
                     apart |= e > kLeast && e + kSpread < top;
+                    if (!FEW && e <= kLeast && (kv == 1 || e + kSpread < top)) {
+                        f[i] = both(kUnless);
+                        looks = true;
+                    }
                 }
                 if (hidden != 0) {
-                    looks = true;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (hidden >> i & 1u) f[i] = 0;
                 }
-                looks = __any_sync(0xFFFFFFFFu, looks) != 0;
+                if (!FEW) looks = __any_sync(0xFFFFFFFFu, looks) != 0;
+                if (FEW && kv == 1 &&
+                    min(min(xc.e[0], xc.e[1]), min(xc.e[2], xc.e[3])) <= kLeast) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (xc.e[i] > kLeast || (hidden >> i & 1u)) continue;
+                        const uint8_t* codes = a.c.pages[1] + vec_at(a.c, 1, cur, slot_of(k) + i, h);
+                        bool any = false;
+#pragma unroll 1
+                        for (int d = 0; d < a.c.D; d += 16)
+                            any |= not_zeros(*reinterpret_cast<const uint4*>(codes + d));
+                        if (any) note(0, kNoted + 1);
+                    }
+                }
                 // All rows again (FEW: the keys' codes go into the products as they
                 // are, each with a factor of its own).
                 if (apart && (kv == 1 || !FEW)) note(0, kNoted + 1);
@@ -618,7 +623,7 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                         make_uint4(f[0], f[1], f[2], f[3]);
                 }
                 if constexpr (FEW) {
-                    if (kv == 1 && lane == 0) ctl.top[at.stage] = top | (looks ? 256u : 0u);
+                    if (kv == 1 && lane == 0) ctl.top[at.stage] = top;
                 } else {
                     if (lane == 0) ctl.top[at.stage] = make_uint2(top | (looks ? 256u : 0u), v_top);
                 }

@@ -68,7 +68,7 @@ struct FewControl {
     float2 ml[kWorkers][16];
     float q_scale[16];
     // e4m3, for every stage: the keys' powers of two, or the values' factors as
-    // halves and their largest exponent (plus 256: see look_at_codes).
+    // halves and their largest exponent.
     alignas(16) float scale[E4M3 ? STAGES : 1][E4M3 ? kTile : 4];
     uint32_t top[E4M3 ? STAGES : 1];
 };
@@ -343,12 +343,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 at.advance(1);
                 // ---- weights
                 int lift = 0;  // e4m3: the tile's values above the outputs' exponent
-                bool looks = false;
                 if (E4M3) {
                     // (the values' exponent comes with them)
                     if (!(ok = wait_all(&ctl.full[at.stage], at.round))) break;
-                    const int v_top = static_cast<int>(ctl.top[at.stage] & 255u);
-                    looks = ctl.top[at.stage] >= 256u;
+                    const int v_top = static_cast<int>(ctl.top[at.stage]);
                     if (moves(ref, v_top)) {
                         const float keep = moved(ref, v_top);
 #pragma unroll
@@ -442,9 +440,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                                                      few_swizzle<DP>(row, g >> 1, args.swizzled) * 16);
                                 codes[z][0] = x.x, codes[z][1] = x.y;
                             }
-                            if (looks && look_at_codes(codes[z], ((z >> 1 ? f23 : f01) >>
-                                                                  (16 * (z & 1))) & 0xFFFFu))
-                                atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
+                            // (a factor of zero: hidden, whatever the codes are)
+                            if (edge && (((z >> 1 ? f23 : f01) >> (16 * (z & 1))) & 0xFFFFu) == 0u) {
+#pragma unroll
+                                for (int i = 0; i < kWords; ++i) codes[z][i] = 0;
+                            }
                     }
 #pragma unroll
                     for (int i = 0; i < kWords; ++i) {

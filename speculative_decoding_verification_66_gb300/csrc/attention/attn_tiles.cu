@@ -119,7 +119,7 @@ struct Control {
     float k_scale[4];
     int v_top[4];
     // e4m3, for every raw stage: the rows' factors; the exponents of its keys (or
-    // values; plus 256: see look_at_codes) and of the values that belong to them.
+    // values; plus 256: see kUnless) and of the values that belong to them.
     alignas(16) uint32_t factor[RAW > 0 ? RAW : 1][RAW > 0 ? kTile : 4];
     uint2 top[RAW > 0 ? RAW : 1];
 };
@@ -731,12 +731,12 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const uint32_t from = raw + row0 * a.c.D + (in_row ? piece * 16 : 0);
                     const uint32_t to = dst + tile_chunk(row0, piece * 2);
                     const uint32_t* factor = &ctl.factor[raw_at.stage][row0];
-                    const uint2 top = ctl.top[raw_at.stage];
-                    const bool looks = top.x >= 256u;
                     if (!is_v && tid == 0) {
+                        const uint2 top = ctl.top[raw_at.stage];
                         ctl.k_scale[k_tiles & 3] = exp_value(top.x & 255u);
                         ctl.v_top[k_tiles & 3] = static_cast<int>(top.y);
                     }
+                    const bool ragged = k < inner_lo || k > inner_hi;
                     constexpr int kBatch = kTile / kStep < 4 ? kTile / kStep : 4;
 #pragma unroll 1
                     for (int r = 0; r < kTile; r += kBatch * kStep) {
@@ -750,15 +750,23 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                         }
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
-                            uint32_t c[4] = {codes[u].x, codes[u].y, codes[u].z, codes[u].w}, o[8];
-                            if (looks && look_at_codes(c, f[u] & 0xFFFFu))
-                                atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
-                            expand(make_uint4(c[0], c[1], c[2], c[3]), f[u], o);
+                            // (a factor of zero: hidden, whatever the codes are)
+                            if (ragged && f[u] == 0u) codes[u] = make_uint4(0, 0, 0, 0);
+                            uint32_t o[8];
+                            expand(codes[u], f[u], o);
                             // (chunk 2 c + 1 is chunk 2 c's neighbour under the swizzle too)
                             const uint32_t t = to + (r + u * kStep) * 128;
                             st_shared_v4(t, make_uint4(o[0], o[1], o[2], o[3]));
                             st_shared_v4(t ^ 16u, make_uint4(o[4], o[5], o[6], o[7]));
                         }
+                    }
+                    if (ctl.top[raw_at.stage].x >= 256u && in_row) {
+                        // (every thread those that it has expanded)
+#pragma unroll 1
+                        for (int row = 0; row < kTile; row += kStep)
+                            if (factor[row] == both(kUnless) &&
+                                not_zeros(ld_shared_v4(from + row * a.c.D)))
+                                atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
                     }
                     if (!is_v) ++k_tiles;
                     fence_async_smem();
