@@ -42,6 +42,10 @@ constexpr int kSpread = 13;
 // follow them stay below 2^127 (values 2^9, weights 2^8, 2^30 keys), and moved() is
 // exact. Beyond, the segment's rows are computed again.
 constexpr int kFar = 60;
+// A row's scores are below 2^31 before they are multiplied by its query's factor and
+// by the key's exponent, in either order: keys above 2^kLarge or a factor above 2^67
+// might overflow on the way where the product does not. All rows are computed again.
+constexpr uint32_t kLarge = 127 + 60;
 
 constexpr int kMaxBlocks = 160;  // shares in the workspace; grids are no larger
 constexpr size_t kMaxSmem = 232448;
@@ -232,10 +236,17 @@ __device__ __forceinline__ float moved(int ref, int top)
     return ref == 0 ? 1.f : exp_value(static_cast<uint32_t>(max(min(127 + ref - top, 227), 27)));
 }
 
-// The factor of a row's scores: the queries' and the keys' powers of two and the
-// scale. Where these multiply to nothing (a row of zeros, keys of zeros) a hidden
-// score's -inf times zero would be NaN. Scores are below 2^31 before this factor, so
-// the least normal number in the place of a smaller one moves none by 2^-95.
+// The query's part of the factor of a row's scores: the scale and its power of two.
+__device__ __forceinline__ float row_factor(float c, int* noted)
+{
+    if (c > __uint_as_float((127u + 67u) << 23)) atomicAdd(noted, kNoted + 1);  // (see kLarge)
+    return c;
+}
+// The factor of a row's scores: the above and the keys' power of two. Where these
+// multiply to nothing (a row of zeros, keys of zeros) a hidden score's -inf times zero
+// would be NaN. Scores are below 2^31 before this factor (few rows: times a key's
+// exponent, 2^91), so the least normal number in the place of a smaller one moves none
+// by 2^-95 (2^-35).
 __device__ __forceinline__ float score_factor(float c)
 {
     return fmaxf(c, __uint_as_float(0x00800000u));
@@ -600,8 +611,8 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                     }
                 }
                 // All rows again (FEW: the keys' codes go into the products as they
-                // are, each with a factor of its own).
-                if (apart && (kv == 1 || !FEW)) note(0, kNoted + 1);
+                // are, each with a factor of its own; `top` is the lane's).
+                if ((apart && (kv == 1 || !FEW)) || (kv == 0 && top > kLarge)) note(0, kNoted + 1);
                 if (!FEW && kv == 0) v_top = __reduce_max_sync(0xFFFFFFFFu, v_top);
                 if (kv == (FEW ? 1 : 0)) {
                     const int of_values = static_cast<int>(FEW ? top : v_top);

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
             }
         };
-        auto store = [&]() {
+        auto store = [&](int item) {
             if (kScaled) {
                 // To float16: powers of two that bring a row's largest element to
                 // [2^14, 2^15).
@@ -226,9 +226,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                                            max(u.y << 16 & 0x7FFF0000u, u.y & 0x7FFF0000u)));
                     }
                     top = __reduce_max_sync(0xFFFFFFFFu, top);
-                    if (lane == 0)
-                        ctl.q_scale[warp + 8 * i] = __uint_as_float(
+                    if (lane == 0) {
+                        const float size = __uint_as_float(
                             static_cast<uint32_t>(max(static_cast<int>(top >> 23), 15) - 14) << 23);
+                        ctl.q_scale[warp + 8 * i] = size;
+                        row_factor(a.scale_log2 * size, &ctl.noted[item % kItems]);
+                    }
                 }
                 if (!meet()) return false;
 #pragma unroll
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int item = 0; plan != nullptr; ++item) {
             const Plan& p = *plan;
             const int n = p.n, rows = p.rows;
-            if (!(ok = store())) break;
+            if (!(ok = store(item))) break;
 
             // This thread's rows: g + 8 i.
             int pos[2], low[2];
@@ -268,7 +271,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 pos[i] = p.cached + (p.row0 + r) / a.G;
                 low[i] = a.window > 0 ? pos[i] - static_cast<int>(a.window) + 1 : INT_MIN / 2;
                 cs[i] = a.scale_log2;
-                if constexpr (E4M3 && std::is_same<T, Bf16>::value) cs[i] = score_factor(cs[i] * ctl.q_scale[r]);
+                if constexpr (E4M3 && std::is_same<T, Bf16>::value)
+                    cs[i] = score_factor(cs[i] * ctl.q_scale[r]);
                 m[i] = ninf;
                 l[i] = 0.f;
             }

@@ -312,7 +312,9 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     if (live) {
                         fence_after();
                         if (E4M3 && std::is_same<T, Bf16>::value && !begun)
-                            row_c = a.scale_log2 * ctl.q_scale[item & 1][min(slot_row, rows - 1)];
+                            row_c = row_factor(
+                                a.scale_log2 * ctl.q_scale[item & 1][min(slot_row, rows - 1)],
+                                &ctl.noted[item % kItems]);
                         const int clo = low - k * kTile, chi = pos - k * kTile;
                         const bool masked =
                             __any_sync(0xFFFFFFFFu, clo > 0 || chi < kTile - 1) != 0;

@@ -201,3 +201,31 @@ def test_tiles_of_values_far_apart(T, d, steps, length):
     q = queries(c, 4)
     agrees(quantised(c), q, T)
     agrees(c, q, T, times=100)
+
+
+@pytest.mark.parametrize("T,d", ROWS)
+@pytest.mark.parametrize("e", [30, 60, 90, 105, 115])
+def test_large_keys_under_small_queries(T, d, e):
+    """Scores of ordinary size from keys of 2^e and queries of 2^-e, and the other way round."""
+    c = Cache([290, 3], [T, T], 2, d, 16, "bf16", False, seed=5)
+    scale_by(c, 0, torch.full((290 + T,), 2.0 ** e, device="cuda"))
+    q = queries(c, 4)
+    q[:T] = (q[:T].double() * 2.0 ** -e).to(q.dtype)
+    agrees(quantised(c), q, T)
+    if e <= 105:
+        c = Cache([290, 3], [T, T], 2, d, 16, "bf16", False, seed=5)
+        scale_by(c, 0, torch.full((290 + T,), 2.0 ** -e, device="cuda"))
+        q = queries(c, 4)
+        q[:T] = (q[:T].double() * 2.0 ** e).to(q.dtype)
+        agrees(quantised(c), q, T)
+    # Both large, in different elements: no product is.
+    c = Cache([290, 3], [T, T], 2, d, 16, "bf16", False, seed=6)
+    at = places(c, 0, 290 + T)
+    c.parts[0][at[0], at[1], :, 3] = 2.0 ** e
+    q = queries(c, 4)
+    q[:T, :, 3] = 0.0
+    q[:T, :, 7] = 2.0 ** e
+    x = c.parts[0][at]
+    x[:, :, 7] = 0.0
+    c.parts[0][at] = x
+    agrees(quantised(c), q, T)
