@@ -72,9 +72,10 @@ extern "C" {
 /*
  * A paged cache and the chunks of one call. Index 0 of the two-element fields
  * is the keys', index 1 the values'. Strides count elements; the innermost
- * (head_dim) stride is 1.
+ * (head_dim) stride is 1; the stride of a dimension of one element (one page, one
+ * head; in the packed arrays one token or head) is not looked at.
  *   pages        device, 16-byte aligned; page, slot and head strides are
- *                multiples of 16 bytes.
+ *                multiples of 16 bytes, below 2^40.
  *   exps         device bytes, SV_E4M3 only (NULL otherwise), any strides.
  *   num_pages    pages in each of the two arrays, 0 <= num_pages < 2^31.
  *   page_size    a power of two, 8 .. 1024.

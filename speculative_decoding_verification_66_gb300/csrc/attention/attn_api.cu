@@ -30,10 +30,16 @@ int check_cache(const sv_paged_cache* d, sva::Cache* c)
     const int es = d->dtype == SV_E4M3 ? 1 : 2;
     *c = sva::Cache{};
     for (int i = 0; i < 2; ++i) {
-        const int64_t st[3] = {d->page_stride[i], d->slot_stride[i], d->head_stride[i]};
-        for (int64_t s : st) {
-            if (s < 0 || s >= (int64_t(1) << 40)) return SV_ERR_ARG;
-            if (s * es % 16 != 0) return SV_ERR_ALIGN;
+        // Pages, slots, heads: elements, then bytes. Where there is one of a kind its
+        // stride says nothing (torch leaves any number there).
+        int64_t st[3] = {d->page_stride[i], d->slot_stride[i], d->head_stride[i]};
+        int64_t ex[3] = {d->exp_page_stride[i], d->exp_slot_stride[i], d->exp_head_stride[i]};
+        if (d->num_pages <= 1) st[0] = d->head_dim, ex[0] = 0;
+        if (d->kv_heads == 1) st[2] = d->head_dim, ex[2] = 0;
+        for (int64_t& s : st) {
+            if (s < 0 || s >= (int64_t(1) << 40) / es) return SV_ERR_ARG;
+            s *= es;
+            if (s % 16 != 0) return SV_ERR_ALIGN;
         }
         if (d->batch > 0 && d->num_pages > 0) {
             if (d->pages[i] == nullptr) return SV_ERR_ARG;
@@ -41,20 +47,17 @@ int check_cache(const sv_paged_cache* d, sva::Cache* c)
         }
         if (d->dtype != SV_E4M3 && d->exps[i] != nullptr) return SV_ERR_ARG;
         if (!aligned(d->pages[i], 16)) return SV_ERR_ALIGN;
-        if (d->dtype == SV_E4M3 &&
-            (d->exp_page_stride[i] < 0 || d->exp_slot_stride[i] < 0 || d->exp_head_stride[i] < 0 ||
-             d->exp_page_stride[i] >= (int64_t(1) << 40) ||
-             d->exp_slot_stride[i] >= (int64_t(1) << 40) ||
-             d->exp_head_stride[i] >= (int64_t(1) << 40)))
-            return SV_ERR_ARG;
+        if (d->dtype == SV_E4M3)
+            for (int64_t s : ex)
+                if (s < 0 || s >= (int64_t(1) << 40)) return SV_ERR_ARG;
         c->pages[i] = static_cast<uint8_t*>(d->pages[i]);
         c->exps[i] = d->exps[i];
-        c->page_stride[i] = d->page_stride[i] * es;
-        c->slot_stride[i] = d->slot_stride[i] * es;
-        c->head_stride[i] = d->head_stride[i] * es;
-        c->exp_page_stride[i] = d->exp_page_stride[i];
-        c->exp_slot_stride[i] = d->exp_slot_stride[i];
-        c->exp_head_stride[i] = d->exp_head_stride[i];
+        c->page_stride[i] = st[0];
+        c->slot_stride[i] = st[1];
+        c->head_stride[i] = st[2];
+        c->exp_page_stride[i] = ex[0];
+        c->exp_slot_stride[i] = ex[1];
+        c->exp_head_stride[i] = ex[2];
     }
     if (d->batch > 0) {
         if ((d->max_pages > 0 && d->page_table == nullptr) || d->cached_lens == nullptr ||
@@ -87,8 +90,12 @@ int check_dtype(int dtype, const sv_paged_cache* d)
     return SV_OK;
 }
 
-int check_rows(const void* x, int64_t tokens, int64_t token_stride, int64_t head_stride)
+// The strides of packed rows; those of one token or one head become 0.
+int check_rows(const void* x, int64_t tokens, int64_t heads, int64_t& token_stride,
+               int64_t& head_stride)
 {
+    if (tokens <= 1) token_stride = 0;
+    if (heads == 1) head_stride = 0;
     if (token_stride < 0 || head_stride < 0 || token_stride >= (int64_t(1) << 40) ||
         head_stride >= (int64_t(1) << 40))
         return SV_ERR_ARG;
@@ -117,8 +124,8 @@ SV_EXPORT int sv_kv_append(const sv_paged_cache* cache, const void* key, const v
     if (rc != SV_OK) return rc;
     if (tokens < 0) return SV_ERR_ARG;
     if (tokens >= kMax31) return SV_ERR_SIZE;
-    rc = check_rows(key, tokens, key_token_stride, key_head_stride);
-    if (rc == SV_OK) rc = check_rows(value, tokens, value_token_stride, value_head_stride);
+    rc = check_rows(key, tokens, c.Hkv, key_token_stride, key_head_stride);
+    if (rc == SV_OK) rc = check_rows(value, tokens, c.Hkv, value_token_stride, value_head_stride);
     if (rc == SV_OK && !aligned(seq_status, 4)) rc = SV_ERR_ALIGN;
     if (rc != SV_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -143,9 +150,9 @@ SV_EXPORT int sv_kv_read(const sv_paged_cache* cache, void* key, void* value, in
     if (rc != SV_OK) return rc;
     if (tokens < 0) return SV_ERR_ARG;
     if (tokens >= kMax31) return SV_ERR_SIZE;
-    const int64_t hs = c.D, ts = static_cast<int64_t>(c.Hkv) * c.D;
-    rc = check_rows(key, tokens, ts, hs);
-    if (rc == SV_OK) rc = check_rows(value, tokens, ts, hs);
+    int64_t hs = c.D, ts = static_cast<int64_t>(c.Hkv) * c.D;
+    rc = check_rows(key, tokens, c.Hkv, ts, hs);
+    if (rc == SV_OK) rc = check_rows(value, tokens, c.Hkv, ts, hs);
     if (rc == SV_OK && !aligned(seq_status, 4)) rc = SV_ERR_ALIGN;
     if (rc != SV_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -207,7 +214,7 @@ int attention(const sv_paged_cache* cache, const void* query, int dtype, int64_t
     if (rc != SV_OK) return rc;
     if (!(scale > 0.f) || !std::isfinite(scale * 1.44269504f)) return SV_ERR_ARG;
     if (window < 0 || window >= kMax31) return SV_ERR_ARG;
-    rc = check_rows(query, tokens, query_token_stride, query_head_stride);
+    rc = check_rows(query, tokens, q_heads, query_token_stride, query_head_stride);
     if (rc != SV_OK) return rc;
     if (tokens > 0 && out == nullptr) return SV_ERR_ARG;
     if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(seq_status, 4)) return SV_ERR_ALIGN;

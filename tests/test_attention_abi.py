@@ -177,3 +177,13 @@ def test_the_gated_call_needs_its_gate(lib):
         return lib.sv_chunk_attention_gated(cache(), P, BF16, 5, 32, 4096, 128, 0.1, 0, 0, P, 0, 0,
                                             P, 1 << 40, 0, -1, gate)
     assert gated(0) == ARG and gated(P + 2) == ALIGN
+
+
+def test_strides_of_single_elements_are_not_looked_at(lib):
+    one = dict(kv_heads=1, khs=3, vhs=-5, num_pages=1, kps=1 << 60, vps=7)
+    for c in (cache(**one), cache(dtype=E4M3, kehs=-1, veps=-2, **one)):
+        assert append(lib, c, tokens=0, strides=(3, 5, -7, 1)) == SV_OK
+        assert read(lib, c, tokens=0) == SV_OK
+        assert attend(lib, c, tokens=0, q_heads=1, ts=3, hs=-1) == SV_OK
+    assert append(lib, cache(kv_heads=1, khs=3, vhs=3, kss=1028), tokens=0) == ALIGN
+    assert append(lib, cache(kps=1 << 39), tokens=0) == ARG  # 2^40 bytes

@@ -516,3 +516,26 @@ def test_large_heads_bad_pages():
     out = sv.sv_chunk_attention(q, *c.args(), seq_status=status, max_chunk=20)
     assert status.tolist() == [sv.SV_SEQ_BAD_PAGE, 0]
     assert out[:20].isnan().all() and out[20:].isfinite().all()
+
+
+@pytest.mark.parametrize("T", [1, 30])
+def test_strides_of_single_elements_are_not_looked_at(T):
+    """One head, one page and one token with whatever stride torch may have left there."""
+    c = Cache([40 - T], [T], 1, 64, 64, "bf16", False, spare=0)
+    q, x = make_query(c, 1, 1), make_query(c, 1, 2)
+    want = sv.sv_chunk_attention(q, *c.args(), max_chunk=T)
+
+    def odd(t):
+        st = list(t.stride())
+        for i, n in enumerate(t.shape):
+            if n == 1:
+                st[i] = (1 << 39) + 3
+        return t.as_strided(t.shape, st)
+
+    k, v = (odd(t) for t in c.parts)
+    assert k.stride(0) == k.stride(2) == (1 << 39) + 3
+    out = sv.sv_chunk_attention(odd(q), k, v, *c.args()[2:], max_chunk=T)
+    assert torch.equal(out, want)
+    sv.sv_kv_append(odd(x), odd(q), k, v, *c.args()[2:])
+    key, value = sv.sv_kv_read(k, v, *c.args()[2:], T)
+    assert torch.equal(key, x) and torch.equal(value, q)
