@@ -28,7 +28,7 @@ SOURCES = ["row_stats.cu", "scan.cu", "sample.cu", "filter.cu", "hist.cu", "lmhe
 # The paged cache and its attention (csrc/attention).
 ATTENTION_LIB_PATH = os.path.join(PKG, "libsvattention.so")
 ATTENTION_CSRC = os.path.join(CSRC, "attention")
-ATTENTION_SOURCES = ["kv_cache.cu", "attn_rows.cu", "attn_few.cu", "attn_tiles.cu",
+ATTENTION_SOURCES = ["kv_cache.cu", "attn_no_pages.cu", "attn_few.cu", "attn_tiles.cu",
                      "attn_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -243,14 +243,12 @@ int attention(const sv_paged_cache* cache, const void* query, int dtype, int64_t
     a.gate = gate;
     a.gate_block = gate_block;
     const bool f16 = dtype == SV_F16, e4m3 = cache->dtype == SV_E4M3;
-    bool done = false;
-    if (a.c.num_pages > 0) {
-        const bool few = max_chunk * a.G <= sva::kFewRows || a.c.D > sva::kMaxTileDim;
-        const auto launch = few ? sva::launch_attention_few : sva::launch_attention_tiles;
-        if (launch(a, f16, e4m3, workspace, s, &done) != cudaSuccess) return SV_ERR_CUDA;
-    }
-    if (!done && sva::launch_attention_rows(a, f16, e4m3, s) != cudaSuccess) return SV_ERR_CUDA;
-    return SV_OK;
+    const bool few = max_chunk * a.G <= sva::kFewRows || a.c.D > sva::kMaxTileDim;
+    const auto launch = few ? sva::launch_attention_few : sva::launch_attention_tiles;
+    return (a.c.num_pages == 0 ? sva::launch_attention_no_pages(a, f16, s)
+                               : launch(a, f16, e4m3, workspace, s)) == cudaSuccess
+               ? SV_OK
+               : SV_ERR_CUDA;
 }
 
 }  // namespace

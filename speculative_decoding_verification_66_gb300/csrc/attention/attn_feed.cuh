@@ -845,15 +845,15 @@ bool make_map(CUtensorMap* map, const Cache& c, int kv, bool f16, bool e4m3, boo
            CUDA_SUCCESS;
 }
 
-// Maps, work description and number of blocks of a call; *mapped false where the
-// copies cannot describe the pages' strides. swizzle: e4m3 rows of 128 or 64 codes
-// may lie swizzled in shared memory.
+// Maps, work description and number of blocks of a call. swizzle: e4m3 rows of 128 or
+// 64 codes may lie swizzled in shared memory. (The encoder takes every stride that the
+// host's checks take, zero among them.)
 cudaError_t set_up(const Attn& a, bool f16, bool e4m3, int64_t rows, void* workspace, bool swizzle,
-                   CUtensorMap* k, CUtensorMap* v, Tiles* t, int* blocks, bool* mapped)
+                   CUtensorMap* k, CUtensorMap* v, Tiles* t, int* blocks)
 {
     const bool swizzled = swizzle && e4m3 && (a.c.D == 128 || a.c.D == 64);
-    *mapped = make_map(k, a.c, 0, f16, e4m3, swizzled) && make_map(v, a.c, 1, f16, e4m3, swizzled);
-    if (!*mapped) return cudaSuccess;
+    if (!make_map(k, a.c, 0, f16, e4m3, swizzled) || !make_map(v, a.c, 1, f16, e4m3, swizzled))
+        return cudaErrorInvalidValue;
     int dev = 0, sms = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;

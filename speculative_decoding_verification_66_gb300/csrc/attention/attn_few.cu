@@ -651,14 +651,14 @@ cudaError_t launch_few_type(const CUtensorMap& k, const CUtensorMap& v, const Ti
 }  // namespace
 
 cudaError_t launch_attention_few(const Attn& a, bool f16, bool e4m3, void* workspace,
-                                 cudaStream_t s, bool* mapped)
+                                 cudaStream_t s)
 {
     CUtensorMap k, v;
     Tiles t;
     int blocks = 0;
     const int64_t rows = a.max_chunk * a.G < kFewRows ? a.max_chunk * a.G : kFewRows;
-    cudaError_t e = set_up(a, f16, e4m3, rows, workspace, true, &k, &v, &t, &blocks, mapped);
-    if (e != cudaSuccess || !*mapped) return e;
+    cudaError_t e = set_up(a, f16, e4m3, rows, workspace, true, &k, &v, &t, &blocks);
+    if (e != cudaSuccess) return e;
     if (a.c.D <= 64)
         return f16 ? launch_few_type<F16, 64>(k, v, t, blocks, rows, e4m3, s)
                    : launch_few_type<Bf16, 64>(k, v, t, blocks, rows, e4m3, s);

@@ -16,19 +16,18 @@ struct Packed {
 cudaError_t launch_append(const Cache& c, const Packed& p, bool f16, bool e4m3, cudaStream_t s);
 cudaError_t launch_read(const Cache& c, const Packed& p, bool f16, bool e4m3, cudaStream_t s);
 
-// Head sizes up to kMaxTileDim; *mapped is false, and nothing is launched, where
-// the tensor copies cannot describe the pages' strides.
+// Head sizes up to kMaxTileDim.
 constexpr int64_t kMaxTileDim = 128;
 size_t tiles_workspace(int64_t max_chunk, int64_t G, int64_t D);
 cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* workspace,
-                                   cudaStream_t s, bool* mapped);
+                                   cudaStream_t s);
 
 // The same, kFewRows rows of a sequence and key/value head at a time, any head size.
 constexpr int64_t kFewRows = 16;
 cudaError_t launch_attention_few(const Attn& a, bool f16, bool e4m3, void* workspace,
-                                 cudaStream_t s, bool* mapped);
+                                 cudaStream_t s);
 
-// Any head size and strides, a row and a key at a time.
-cudaError_t launch_attention_rows(const Attn& a, bool f16, bool e4m3, cudaStream_t s);
+// A cache without pages.
+cudaError_t launch_attention_no_pages(const Attn& a, bool f16, cudaStream_t s);
 
 }  // namespace sva

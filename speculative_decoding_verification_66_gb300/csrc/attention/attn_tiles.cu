@@ -848,7 +848,7 @@ size_t tiles_workspace(int64_t max_chunk, int64_t G, int64_t D)
 }
 
 cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* workspace,
-                                   cudaStream_t s, bool* mapped)
+                                   cudaStream_t s)
 {
     CUtensorMap k, v;
     Tiles t;
@@ -859,8 +859,8 @@ cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* wor
     // and 464: items of up to 128 rows leave the second slot idle.
     const bool pair = a.max_chunk * a.G > 128 && a.tokens * a.G > 128 * static_cast<int64_t>(a.c.B);
     const int64_t rows = item_rows(a.max_chunk, a.G, pair ? 256 : 128);
-    cudaError_t e = set_up(a, f16, e4m3, rows, workspace, false, &k, &v, &t, &blocks, mapped);
-    if (e != cudaSuccess || !*mapped) return e;
+    cudaError_t e = set_up(a, f16, e4m3, rows, workspace, false, &k, &v, &t, &blocks);
+    if (e != cudaSuccess) return e;
     if (a.c.D <= 64)
         return f16 ? launch_type<F16, 64>(k, v, t, blocks, rows, e4m3, pair, s)
                    : launch_type<Bf16, 64>(k, v, t, blocks, rows, e4m3, pair, s);

@@ -539,3 +539,31 @@ def test_strides_of_single_elements_are_not_looked_at(T):
     sv.sv_kv_append(odd(x), odd(q), k, v, *c.args()[2:])
     key, value = sv.sv_kv_read(k, v, *c.args()[2:], T)
     assert torch.equal(key, x) and torch.equal(value, q)
+
+
+@pytest.mark.parametrize("dtype,e4m3", TYPES)
+@pytest.mark.parametrize("T", [1, 30])
+def test_a_cache_without_pages(dtype, e4m3, T):
+    c = Cache([8, 8, 0, 0], [T, 0, T, T], 2, 64, 8, dtype, e4m3, seed=9)
+    q = make_query(c, 4, 8)
+    for i in range(2):
+        c.parts[i] = c.parts[i][:0]
+        c.exps[i] = c.exps[i][:0] if e4m3 else None
+    c.cached[3] = -1
+    status = torch.full((4,), 99, dtype=torch.int32, device="cuda")
+    out, lse = attend(c, q, seq_status=status)
+    assert status.tolist() == [sv.SV_SEQ_BAD_PAGE, 0, sv.SV_SEQ_BAD_PAGE, sv.SV_SEQ_BAD_LENGTH]
+    assert out.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("T", [1, 30])
+def test_pages_and_heads_that_share_memory(T):
+    """Strides of zero: every page, or every head, is the same."""
+    c = Cache([200], [T], 2, 64, 16, "bf16", False, seed=9)
+    q = make_query(c, 4, 8)
+    for kind in ("pages", "heads"):
+        k, v = ((x[:1].expand(x.shape) if kind == "pages" else x[:, :, :1].expand(x.shape))
+                for x in c.parts)
+        out = sv.sv_chunk_attention(q, k, v, *c.args()[2:], max_chunk=T)
+        want = sv.sv_chunk_attention(q, k.contiguous(), v.contiguous(), *c.args()[2:], max_chunk=T)
+        assert torch.equal(out, want)
