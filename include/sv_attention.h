@@ -38,6 +38,10 @@
  *                      end beyond max_pages * page_size. The sequence is left
  *                      out: nothing is written to the cache, and its output
  *                      rows, where they lie in the packed arrays, are NaN.
+ *   SV_SEQ_OVERLAP     starts that are out of order (then some sequence has
+ *                      SV_SEQ_BAD_LENGTH too) give some of the sequence's rows to
+ *                      another one; no row has two owners. The sequence is left
+ *                      out as above, its rows that are another's excepted.
  *   SV_SEQ_BAD_PAGE    a page outside [0, num_pages) among those needed.
  *                      Its tokens are not written; output rows that would read
  *                      it are NaN.
@@ -68,6 +72,7 @@ extern "C" {
 /* seq_status bits besides spec_verify.h's. */
 #define SV_SEQ_BAD_PAGE 16
 #define SV_SEQ_BAD_LENGTH 32
+#define SV_SEQ_OVERLAP 64
 
 /*
  * A paged cache and the chunks of one call. Index 0 of the two-element fields

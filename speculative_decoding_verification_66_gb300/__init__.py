@@ -54,6 +54,7 @@ from .attention import (  # noqa: F401
     SV_F16,
     SV_SEQ_BAD_LENGTH,
     SV_SEQ_BAD_PAGE,
+    SV_SEQ_OVERLAP,
     sv_chunk_attention,
     sv_chunk_attention_gated,
     sv_chunk_attention_workspace_bytes,

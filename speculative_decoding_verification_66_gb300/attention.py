@@ -30,7 +30,7 @@ from . import _lib
 from .api import SV_BF16, _check
 
 SV_F16, SV_E4M3 = 2, 3
-SV_SEQ_BAD_PAGE, SV_SEQ_BAD_LENGTH = 16, 32
+SV_SEQ_BAD_PAGE, SV_SEQ_BAD_LENGTH, SV_SEQ_OVERLAP = 16, 32, 64
 
 _CODES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3}
 # struct sv_paged_cache

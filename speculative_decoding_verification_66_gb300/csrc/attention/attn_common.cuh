@@ -3,6 +3,7 @@
 // sequence's tokens lie.
 #pragma once
 
+#include <climits>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -14,6 +15,7 @@ namespace sva {
 constexpr int kBadPage = 16;    // == SV_SEQ_BAD_PAGE
 constexpr int kBadLength = 32;  // == SV_SEQ_BAD_LENGTH
 constexpr int kTimeout = 4;     // == SV_SEQ_TIMEOUT
+constexpr int kOverlap = 64;    // == SV_SEQ_OVERLAP
 
 // Element types of the kernels' template parameters.
 struct Bf16 {};
@@ -39,7 +41,7 @@ struct Cache {
 struct Seq {
     int64_t cached;
     int32_t start, count;
-    int32_t bad;  // 0 or kBadLength; then count is 0 unless the rows can be written
+    int32_t bad;  // 0, kBadLength or kOverlap; then count is 0 unless the rows can be written
 };
 
 __device__ __forceinline__ Seq seq_of(const Cache& c, int b, int64_t tokens, int64_t max_chunk)
@@ -58,21 +60,57 @@ __device__ __forceinline__ Seq seq_of(const Cache& c, int b, int64_t tokens, int
 
 // The sequence whose rows hold packed row t: the last b with starts[b] <= t,
 // found by a warp 32 boundaries at a time (two steps up to 1024 sequences).
-// A result only where the starts are in order; the caller checks that row t is
-// inside the sequence it gets.
-__device__ __forceinline__ int find_seq(const int32_t* starts, int B, int64_t t, int lane)
+// The caller checks that row t is inside the sequence it gets, and, as the starts may
+// be out of order, that it owns its rows.
+//
+// Sequence b owns its rows [s, e) if the search finds it for all of them, as it does
+// where the starts are in order: if every step goes the same way for s and for e - 1,
+// that is, if the boundaries taken (this lane's: *taken at most) are at most s and
+// those behind them (*passed at least) at least e. So a row has one owner at most,
+// whatever the starts are.
+__device__ __forceinline__ int find_seq(const int32_t* starts, int B, int64_t t, int lane,
+                                        int* taken, int* passed)
 {
     int lo = 0, n = B;  // the answer is in [lo, lo + n)
+    *taken = INT_MIN;
+    *passed = INT_MAX;
     while (n > 1) {
         const int step = (n + 31) / 32;
         const int i = lo + lane * step;
-        const bool le = lane * step < n && (lane == 0 || starts[i] <= t);
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, le);
+        const bool is = lane > 0 && lane * step < n;
+        const int x = is ? starts[i] : INT_MIN;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, lane == 0 || (is && x <= t));
         const int k = 31 - __clz(static_cast<int>(m));  // lane 0 always votes
+        if (lane == k) *taken = max(*taken, x);
+        if (is && lane > k) *passed = min(*passed, x);
         n = min(step, n - k * step);
         lo += k * step;
     }
     return lo;
+}
+
+// Whether sequence b owns its rows [s, e), s < e, by a thread.
+__device__ __forceinline__ bool owns_rows(const int32_t* starts, int B, int b, int64_t s, int64_t e)
+{
+    int lo = 0, n = B;
+    while (n > 1) {
+        const int step = (n + 31) / 32, k = (b - lo) / step;
+        if (k > 0 && starts[lo + k * step] > s) return false;
+        for (int j = k + 1; j < 32 && j * step < n; ++j)
+            if (starts[lo + j * step] < e) return false;
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    return true;
+}
+// seq_of, and kOverlap where some of the rows are not the sequence's own.
+__device__ __forceinline__ Seq own_seq_of(const Cache& c, int b, int64_t tokens, int64_t max_chunk)
+{
+    Seq q = seq_of(c, b, tokens, max_chunk);
+    if (!q.bad && q.count > 0 &&
+        !owns_rows(c.starts, c.B, b, q.start, static_cast<int64_t>(q.start) + q.count))
+        q.bad = kOverlap;
+    return q;
 }
 
 // The page of position pos of sequence b, or -1 (outside [0, num_pages)).
@@ -249,6 +287,18 @@ __device__ bool attend_row(const Attn& a, int b, int hkv, const uint8_t* q, int6
     *m_out = m;
     *l_out = l;
     return ok;
+}
+// Its result as output row `row` of [tokens, Hq].
+template <class T>
+__device__ __forceinline__ void write_row(const Attn& a, int64_t row, int lane, float m, float l,
+                                          const float (&o)[8])
+{
+    const float x = 1.f / l;
+    if (lane * 8 < a.c.D)
+        *reinterpret_cast<uint4*>(a.out + (row * a.c.D + lane * 8) * 2) =
+            make_uint4(narrow2(o[0] * x, o[1] * x, T()), narrow2(o[2] * x, o[3] * x, T()),
+                       narrow2(o[4] * x, o[5] * x, T()), narrow2(o[6] * x, o[7] * x, T()));
+    if (a.lse != nullptr && lane == 0) a.lse[row] = fmaf(m, kLn2, logf(l));
 }
 
 }  // namespace sva

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int i = 0; i < kItems; ++i) ctl.noted[i] = ctl.bad_page[i] = 0;
         sv::fence_barrier_init();
     }
-    if (find_start<R, kFewThreads>(a, ctl)) refuse_sequences<T>(a);
+    if (find_start<R, kFewThreads>(a, ctl)) refuse_sequences<T, E4M3>(a, ctl);
     __syncthreads();
     const Start start = ctl.start;
     volatile int* stop = &ctl.stop;

@@ -14,7 +14,7 @@ __global__ void __launch_bounds__(kThreads) no_pages_kernel(const Attn a)
     const float nan = __uint_as_float(0x7FFFFFFFu);
     const uint32_t nan2 = narrow2(nan, nan, T());
     for (int64_t b = blockIdx.x; b < a.c.B; b += gridDim.x) {
-        const Seq q = seq_of(a.c, static_cast<int>(b), a.tokens, a.max_chunk);
+        const Seq q = own_seq_of(a.c, static_cast<int>(b), a.tokens, a.max_chunk);
         if (a.status != nullptr && threadIdx.x == 0)
             a.status[b] = q.bad ? q.bad : q.count > 0 ? kBadPage : 0;
         const int64_t row0 = static_cast<int64_t>(q.start) * a.Hq;

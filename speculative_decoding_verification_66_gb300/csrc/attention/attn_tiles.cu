@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
 
-    if (find_start<R, X::kThreads>(a, ctl)) refuse_sequences<T>(a);
+    if (find_start<R, X::kThreads>(a, ctl)) refuse_sequences<T, E4M3>(a, ctl);
     __syncthreads();
     fence_after();
     const uint32_t tmem = ctl.tmem;

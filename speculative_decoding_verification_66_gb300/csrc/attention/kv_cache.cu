@@ -74,17 +74,19 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const Cache c, const Pac
     if (p.status != nullptr)
         for (int64_t b = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; b < c.B;
              b += static_cast<int64_t>(gridDim.x) * kThreads) {
-            const int bad = seq_of(c, static_cast<int>(b), p.tokens, p.tokens).bad;
+            const int bad = own_seq_of(c, static_cast<int>(b), p.tokens, p.tokens).bad;
             if (bad) atomicOr(p.status + b, bad);
         }
     const int64_t w = blockIdx.x * static_cast<int64_t>(kThreads / 32) + (threadIdx.x >> 5);
     const int64_t t = w / parts;
     const int part = static_cast<int>(w - t * parts);
     if (t >= p.tokens) return;
-    const int b = find_seq(c.starts, c.B, t, lane);
+    int taken, passed;
+    const int b = find_seq(c.starts, c.B, t, lane, &taken, &passed);
     const Seq q = seq_of(c, b, p.tokens, p.tokens);
     int32_t page = -1, slot = 0;
-    if (!q.bad && t >= q.start && t - q.start < q.count) {
+    if (!q.bad && t >= q.start && t - q.start < q.count &&
+        __all_sync(0xFFFFFFFFu, taken <= q.start && passed - q.start >= q.count)) {
         const int64_t pos = q.cached + (t - q.start);
         page = page_of(c, b, pos);
         slot = static_cast<int32_t>(pos) & ((1 << c.page_shift) - 1);
