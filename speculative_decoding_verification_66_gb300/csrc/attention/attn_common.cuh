@@ -41,7 +41,7 @@ struct Cache {
 struct Seq {
     int64_t cached;
     int32_t start, count;
-    int32_t bad;  // 0, kBadLength or kOverlap; then count is 0 unless the rows can be written
+    int32_t bad;  // 0, kBadLength or kOverlap
 };
 
 __device__ __forceinline__ Seq seq_of(const Cache& c, int b, int64_t tokens, int64_t max_chunk)
@@ -103,13 +103,20 @@ __device__ __forceinline__ bool owns_rows(const int32_t* starts, int B, int b, i
     }
     return true;
 }
-// seq_of, and kOverlap where some of the rows are not the sequence's own.
+// seq_of, and kOverlap where some of the rows are not the sequence's own. A bad
+// sequence's rows are those of its that lie in the packed arrays.
 __device__ __forceinline__ Seq own_seq_of(const Cache& c, int b, int64_t tokens, int64_t max_chunk)
 {
     Seq q = seq_of(c, b, tokens, max_chunk);
     if (!q.bad && q.count > 0 &&
         !owns_rows(c.starts, c.B, b, q.start, static_cast<int64_t>(q.start) + q.count))
         q.bad = kOverlap;
+    if (q.bad) {
+        const int64_t s = min(max(static_cast<int64_t>(c.starts[b]), int64_t(0)), tokens);
+        const int64_t e = min(max(static_cast<int64_t>(c.starts[b + 1]), s), tokens);
+        q.start = static_cast<int32_t>(s);
+        q.count = static_cast<int32_t>(e - s);
+    }
     return q;
 }
 

@@ -127,3 +127,40 @@ def test_append_and_read(starts):
     for t, b in enumerate(own):
         for x, y in ((key, k), (value, v)):
             assert torch.equal(x[t], y[t]) if b is not None else x[t].isnan().all()
+
+
+@pytest.mark.parametrize("starts", [[2, 5, 9, 99], [-4, 5, 9, 20], [0, 99, 4, 20], [0, 5, 21, 30],
+                                    [-9, -2, 4, 20], [0, 5, 10, -3]])
+@pytest.mark.parametrize("d,max_chunk", [(64, 0), (64, 1), (256, 0)])
+def test_rows_of_sequences_that_leave_the_arrays_are_nan(starts, d, max_chunk):
+    c = Cache([8, 8, 8], [N] * 3, 2, d, 32, "bf16", False, seed=9)
+    c.starts = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    q = torch.randn(N, 8, d, device="cuda").bfloat16()
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    status = torch.empty(3, dtype=torch.int32, device="cuda")
+    sv.sv_chunk_attention(q, *c.args(), out=out, lse=lse, max_chunk=max_chunk, seq_status=status)
+    kind = [7.0] * N
+    for b in range(3):
+        for t in range(max(0, starts[b]), min(N, starts[b + 1])):
+            kind[t] = "nan"
+    for b, s in enumerate(status.tolist()):
+        if s == 0:
+            kind[starts[b]:starts[b + 1]] = ["good"] * (starts[b + 1] - starts[b])
+    for t in range(N):
+        if kind[t] == "good":
+            assert out[t].isfinite().all() and lse[t].isfinite().all()
+        elif kind[t] == "nan":
+            assert out[t].isnan().all() and lse[t].isnan().all()
+        else:
+            assert (out[t] == 7.0).all() and (lse[t] == 7.0).all()
+    # Nothing of the bad ones is written to the cache.
+    before = [x.clone() for x in c.parts]
+    k = torch.randn(N, 2, d, device="cuda").bfloat16()
+    sv.sv_kv_append(k, k, *c.args(), seq_status=status)
+    for b, s in enumerate(status.tolist()):
+        if s == 0:
+            for t in range(starts[b], starts[b + 1]):
+                p = 8 + t - starts[b]
+                for x in before:
+                    x[c.pages_of[b][p // 32], p % 32] = k[t]
+    assert all(torch.equal(x, y) for x, y in zip(before, c.parts))
