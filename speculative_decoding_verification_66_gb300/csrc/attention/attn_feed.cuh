@@ -442,6 +442,19 @@ __device__ __noinline__ void again_row(const Tiles& args, const Plan& g, int r, 
     }
 }
 
+// Whether row r of a segment sees a position in it whose page is out of range: asked
+// only where some page of the segment is.
+__device__ __noinline__ bool meets_bad_page(const Attn& a, const Plan& g, int r)
+{
+    const int64_t origin = static_cast<int64_t>(g.tile0) << kTileShift;
+    const int64_t pos = origin + g.cached + (g.row0 + r) / a.G;
+    const int64_t hi = min(pos + 1, origin + (static_cast<int64_t>(g.n) << kTileShift));
+    for (int64_t p = max(first_key(a, pos), origin); p < hi;
+         p = ((p >> a.c.page_shift) + 1) << a.c.page_shift)
+        if (page_of(a.c, g.b, p) < 0) return true;
+    return false;
+}
+
 // The plan of segment i, or nullptr when there is none or a wait ran out.
 template <class Ctl, class Wait>
 __device__ __forceinline__ const Plan* plan_at(Ctl& ctl, int i, Wait& wait_all)
@@ -572,7 +585,9 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
             const int32_t then = entry(k + 2);
             const Exps xn = exps_of(k + 1, next);
             const bool needed = cur != INT_MIN;
-            // A page out of range: page 0 in its place, and NaN for the item.
+            // A page out of range: page 0 in its place, and NaN for the rows that see
+            // a position of it; e4m3: hidden for the others, as what is there would
+            // count for the tile's exponents.
             const bool bad = needed && !good(cur);
             if (at.round > 0 && !(ok = wait_all(&emptybar[at.stage], at.round - 1))) break;
             if (bad) {
@@ -589,7 +604,10 @@ __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensor
                     const int x = atomicAdd(&ctl.noted[item % kItems], times);
                     if (x < kNoted) ctl.note[item % kItems][x] = p;
                 };
-                if (k < g->inner_lo || k > g->inner_hi) {
+                if (bad) {
+                    hidden = 15u;
+                    xc = Exps{};
+                } else if (k < g->inner_lo || k > g->inner_hi) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int p = k * kTile + lane * 4 + i;

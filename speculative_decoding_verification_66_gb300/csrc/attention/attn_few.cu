@@ -65,6 +65,7 @@ struct FewControl {
     int noted[kItems];
     int note[kItems][kNoted];
     int bad_page[kItems];
+    uint32_t bad_rows[kWorkers];  // of a segment with pages out of range: by the warps
     float2 ml[kWorkers][16];
     float q_scale[16];
     // e4m3, for every stage: the keys' powers of two, or the values' factors as
@@ -522,10 +523,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             // Every warp's rows, `width` columns of them from step j0 on, lie in
             // shared memory: added up, weighted, and written.
             int noted = 0;
-            bool bad = false;
+            // Rows that see a position of a page out of range.
+            uint32_t bad_rows = 0;
+            if (*reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0) {
+                for (int r = warp; r < rows; r += kWorkers)
+                    bad_rows |= meets_bad_page(a, p, r) ? 1u << r : 0u;
+                if (lane == 0) ctl.bad_rows[warp] = bad_rows;
+                if (!(ok = meet())) break;
+                for (int i = 0; i < kWorkers; ++i) bad_rows |= ctl.bad_rows[i];
+            }
             // A row that sees a noted position is computed again below.
             auto again = [&](int r) {
-                if (noted == 0 || bad) return false;
+                if (noted == 0 || (bad_rows >> r & 1u)) return false;
                 const int at_row = p.cached + (p.row0 + r) / a.G;
                 const int from = a.window > 0 ? at_row - static_cast<int>(a.window) + 1 : INT_MIN / 2;
                 bool x = noted > kNoted;
@@ -537,11 +546,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             };
             auto add_up = [&](int j0, int width) {
                 noted = *reinterpret_cast<volatile int*>(&ctl.noted[item % kItems]);
-                bad = *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0;
                 const int steps = width >> 3;
                 for (int x = threadIdx.x; x < rows * width; x += kWorkers * 32) {
                     const int r = x / width, y = x - r * width;
                     if (again(r)) continue;
+                    const bool bad = (bad_rows >> r & 1u) != 0;
                     // e4m3: column n of step j is d = DP / 8 n + j
                     const int col = E4M3 ? y / steps : y & 7;
                     const int j = E4M3 ? y - col * steps : y >> 3;
@@ -600,7 +609,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             if (ok && once && (ok = meet())) add_up(0, width);
             if (!ok) break;
-            if (noted != 0 && !bad) {
+            if (noted != 0) {
                 for (int r = warp; r < rows; r += kWorkers) {
                     __syncwarp();
                     if (again(r))

@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             const bool whole = g.whole != 0, valid = slot_row < rows;
             // A row that sees a noted position is computed again below.
             const int noted = *reinterpret_cast<volatile int*>(&ctl.noted[item % kItems]);
-            const bool bad = *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0;
+            const bool bad = *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0 &&
+                             meets_bad_page(a, g, min(slot_row, rows - 1));
             const int r = g.row0 + min(slot_row, rows - 1), token = r / a.G;
             bool again = noted > kNoted;
             if (noted > 0) {

@@ -567,3 +567,41 @@ def test_pages_and_heads_that_share_memory(T):
         out = sv.sv_chunk_attention(q, k, v, *c.args()[2:], max_chunk=T)
         want = sv.sv_chunk_attention(q, k.contiguous(), v.contiguous(), *c.args()[2:], max_chunk=T)
         assert torch.equal(out, want)
+
+
+def with_page_0_unused(*args, **kw):
+    """A cache whose page 0, which takes the place of pages out of range, is a spare one."""
+    for seed in range(100):
+        c = Cache(*args, seed=seed, spare=20, **kw)
+        if 0 in c.unused:
+            return c
+
+
+@pytest.mark.parametrize("dtype,e4m3", TYPES)
+@pytest.mark.parametrize("T,d", [(4, 64), (4, 128), (20, 128), (75, 64), (75, 128), (12, 256)])
+@pytest.mark.parametrize("at,window", [(304, 0), (288, 10), (256, 40), (307, 3)])
+def test_a_bad_page_reaches_only_the_rows_that_see_it(dtype, e4m3, T, d, at, window):
+    """A page out of range among the new tokens' own, or one that the window passes."""
+    c = with_page_0_unused([300, 4000], [T, T], 2, d, 16, dtype, e4m3, fill=math.inf)
+    q = make_query(c, 4, 1)
+    for b, shift in ((0, 0), (1, 3696)):
+        c.table[b, (at + shift) // 16] = 10 ** 6
+    status = torch.empty(2, dtype=torch.int32, device="cuda")
+    out, lse = attend(c, q, window, max_chunk=T, seq_status=status)
+    lo, hi = at // 16 * 16, at // 16 * 16 + 15  # the page's positions (of sequence 0)
+    seen = torch.tensor([p >= lo and (window == 0 or p - window + 1 <= hi)
+                         for p in range(300, 300 + T)]).repeat(2)
+    # (sequence 1's positions are 3700 on, and its page's 3696 further: 3996 and so on)
+    first = 4000 - 300 - 3696
+    for t in range(T):
+        p = 4000 + t - 3696
+        seen[T + t] = p >= lo and (window == 0 or p - window + 1 <= hi)
+    assert first == 4
+    assert status.tolist() == [sv.SV_SEQ_BAD_PAGE if seen[b * T:b * T + T].any() else 0
+                               for b in range(2)]
+    assert out[seen.cuda()].isnan().all() and lse[seen.cuda()].isnan().all()
+    good = (~seen).nonzero().squeeze(1).cuda()
+    if len(good):
+        for b in range(2):  # (never read by the good rows: any page will do for the reference)
+            c.table[b, (at + (0, 3696)[b]) // 16] = c.unused[0]
+        check(out, lse, c, q, d ** -0.5, window, rows=good)
