@@ -246,3 +246,17 @@ def test_refusals():
         flat = torch.zeros(2 * 2 * 64 + 4, dtype=torch.bfloat16, device="cuda")
         x = flat[4:].view(2, 2, 64)
         sv.sv_kv_append(x, x, *c.args())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_read_of_no_sequences_is_nan(e4m3):
+    c = Cache([4], [2], 2, 64, 8, "bf16", e4m3)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    key, value = (torch.full((5, 2, 64), 7.0, device="cuda").bfloat16() for _ in range(2))
+    args = (c.parts[0], c.parts[1], torch.empty((0, 4), **i32), torch.empty(0, **i32),
+            torch.zeros(1, **i32))
+    sv.sv_kv_read(*args, 5, **c.exp_args(), key=key, value=value)
+    assert key.isnan().all() and value.isnan().all()
+    before = [x.clone() for x in c.parts]
+    sv.sv_kv_append(key, value, *args, **c.exp_args())
+    assert all(torch.equal(bits(x), bits(y)) for x, y in zip(before, c.parts))
