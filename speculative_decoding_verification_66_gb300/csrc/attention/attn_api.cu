@@ -226,7 +226,7 @@ int attention(const sv_paged_cache* cache, const void* query, int dtype, int64_t
         return SV_ERR_WORKSPACE;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((rc = clear_status(seq_status, cache->batch, s)) != SV_OK) return rc;
-    if (tokens == 0 || cache->batch == 0) return SV_OK;
+    if (cache->batch == 0 || (tokens == 0 && seq_status == nullptr)) return SV_OK;
     a.q = static_cast<const uint8_t*>(query);
     a.q_token = query_token_stride * 2;
     a.q_head = query_head_stride * 2;
@@ -245,8 +245,9 @@ int attention(const sv_paged_cache* cache, const void* query, int dtype, int64_t
     const bool f16 = dtype == SV_F16, e4m3 = cache->dtype == SV_E4M3;
     const bool few = max_chunk * a.G <= sva::kFewRows || a.c.D > sva::kMaxTileDim;
     const auto launch = few ? sva::launch_attention_few : sva::launch_attention_tiles;
-    return (a.c.num_pages == 0 ? sva::launch_attention_no_pages(a, f16, s)
-                               : launch(a, f16, e4m3, workspace, s)) == cudaSuccess
+    // (without rows there are only statuses to find)
+    return (a.c.num_pages == 0 || tokens == 0 ? sva::launch_attention_no_pages(a, f16, s)
+                                              : launch(a, f16, e4m3, workspace, s)) == cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;
 }

@@ -1,6 +1,6 @@
 // attn_no_pages.cu -- attention over a cache without pages: there is nothing to attend
 // to, and no tensor map for the other kernels' copies. Rows of every sequence
-// become NaN, and the statuses say why.
+// become NaN, and the statuses say why. Also the statuses of calls without rows.
 #include "attn_internal.h"
 
 namespace sva {

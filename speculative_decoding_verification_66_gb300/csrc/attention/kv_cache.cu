@@ -192,7 +192,8 @@ cudaError_t launch_lanes(const Cache& c, const Packed& p, cudaStream_t s)
 {
     constexpr int per = 32 / LV * kRounds;
     const int parts = (2 * c.Hkv + per - 1) / per;
-    const int64_t blocks = (p.tokens * parts + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t work = (p.tokens * parts + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t blocks = work > 0 ? work : 1;  // (one for the statuses)
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     move_kernel<T, E4M3, READ, LV><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(c, p, parts);
     return cudaGetLastError();
@@ -213,7 +214,8 @@ cudaError_t launch_move(const Cache& c, const Packed& p, cudaStream_t s)
 template <bool READ>
 cudaError_t launch_any(const Cache& c, const Packed& p, bool f16, bool e4m3, cudaStream_t s)
 {
-    if (p.tokens == 0 || (c.B == 0 && !READ)) return cudaSuccess;
+    if (p.tokens == 0 && (c.B == 0 || p.status == nullptr)) return cudaSuccess;
+    if (c.B == 0 && !READ) return cudaSuccess;
     if (!e4m3) return launch_move<Bf16, false, READ>(c, p, s);  // 16-bit elements move as they are
     return f16 ? launch_move<F16, true, READ>(c, p, s) : launch_move<Bf16, true, READ>(c, p, s);
 }

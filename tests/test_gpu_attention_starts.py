@@ -164,3 +164,19 @@ def test_rows_of_sequences_that_leave_the_arrays_are_nan(starts, d, max_chunk):
                 for x in before:
                     x[c.pages_of[b][p // 32], p % 32] = k[t]
     assert all(torch.equal(x, y) for x, y in zip(before, c.parts))
+
+
+def test_statuses_of_calls_without_rows():
+    """No rows in the packed arrays: starts other than 0 and negative lengths are still bad."""
+    c, q, k, v = call([0, 0, 0, 0, 5])
+    c.cached[1] = -3
+    want = [0, sv.SV_SEQ_BAD_LENGTH, 0, sv.SV_SEQ_BAD_LENGTH]
+    status = torch.full((4,), 99, dtype=torch.int32, device="cuda")
+    sv.sv_chunk_attention(q[:0], *c.args(), seq_status=status)
+    assert status.tolist() == want
+    status.fill_(99)
+    sv.sv_kv_append(k[:0], v[:0], *c.args(), seq_status=status)
+    assert status.tolist() == want
+    status.fill_(99)
+    sv.sv_kv_read(*c.args(), 0, seq_status=status)
+    assert status.tolist() == want
