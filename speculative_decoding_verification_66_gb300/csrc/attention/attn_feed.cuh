@@ -59,6 +59,7 @@ struct Plan {
     int32_t b, h, q0, row0, rows;
     int32_t tile0;                     // the first tile's number in the sequence
     int32_t cached;                    // row r stands at position cached + r / G
+    int32_t low;                       // .. and sees positions from low + r / G on
     int32_t lo0, hi0, lo1, hi1;        // split in two slots of 128 rows: their tiles
     int32_t any_lo, any_hi;            // positions that some row sees
     int32_t all_lo, all_hi;            // positions that every row sees
@@ -125,6 +126,7 @@ struct Place {
     }
 };
 
+// Positions of a segment are far below 2^30; those outside need not be told apart.
 __device__ __forceinline__ int clamp32(int64_t v)
 {
     return static_cast<int>(max(min(v, int64_t(INT_MAX / 2)), int64_t(INT_MIN / 2)));
@@ -145,6 +147,7 @@ __device__ __forceinline__ Plan plan_of(const Attn& a, const Segment& g)
     p.rows = g.rows;
     p.tile0 = g.t.lo;
     p.cached = clamp32(g.cached - origin);
+    p.low = a.window > 0 ? clamp32(g.cached - a.window + 1 - origin) : INT_MIN / 2;
     p.any_lo = clamp32(first_key(a, p0) - origin);
     p.any_hi = clamp32(p1 - origin);
     p.all_lo = clamp32(first_key(a, p1) - origin);
@@ -422,9 +425,9 @@ __device__ __noinline__ void again_row(const Tiles& args, const Plan& g, int r, 
     const int lane = threadIdx.x & 31;
     const int64_t origin = static_cast<int64_t>(g.tile0) << kTileShift;
     const int t = (g.row0 + r) / a.G, hq = g.h * a.G + (g.row0 + r - t * a.G);
-    const int64_t pos = origin + g.cached + t, token = static_cast<int64_t>(g.q0) + t;
-    const int64_t lo = max(first_key(a, pos), origin);
-    const int64_t hi = min(pos + 1, origin + (static_cast<int64_t>(g.n) << kTileShift));
+    const int64_t token = static_cast<int64_t>(g.q0) + t;
+    const int64_t lo = origin + max(g.low + t, 0);
+    const int64_t hi = min(origin + g.cached + t + 1, origin + (static_cast<int64_t>(g.n) << kTileShift));
     const int64_t orow = token * a.Hq + hq;
     float m, l, o[8];
     attend_row<T, E4M3>(a, g.b, g.h, a.q + token * a.q_token + hq * a.q_head, lo, hi, lane, &m, &l, o);
@@ -447,9 +450,10 @@ __device__ __noinline__ void again_row(const Tiles& args, const Plan& g, int r, 
 __device__ __noinline__ bool meets_bad_page(const Attn& a, const Plan& g, int r)
 {
     const int64_t origin = static_cast<int64_t>(g.tile0) << kTileShift;
-    const int64_t pos = origin + g.cached + (g.row0 + r) / a.G;
-    const int64_t hi = min(pos + 1, origin + (static_cast<int64_t>(g.n) << kTileShift));
-    for (int64_t p = max(first_key(a, pos), origin); p < hi;
+    const int t = (g.row0 + r) / a.G;
+    const int64_t hi = origin + min(static_cast<int64_t>(g.cached) + t + 1,
+                                    static_cast<int64_t>(g.n) << kTileShift);
+    for (int64_t p = origin + max(g.low + t, 0); p < hi;
          p = ((p >> a.c.page_shift) + 1) << a.c.page_shift)
         if (page_of(a.c, g.b, p) < 0) return true;
     return false;

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             for (int i = 0; i < 2; ++i) {
                 const int r = min(g + 8 * i, rows - 1);
                 pos[i] = p.cached + (p.row0 + r) / a.G;
-                low[i] = a.window > 0 ? pos[i] - static_cast<int>(a.window) + 1 : INT_MIN / 2;
+                low[i] = p.low + (p.row0 + r) / a.G;
                 cs[i] = a.scale_log2;
                 if constexpr (E4M3 && std::is_same<T, Bf16>::value)
                     cs[i] = score_factor(cs[i] * ctl.q_scale[r]);
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             auto again = [&](int r) {
                 if (noted == 0 || (bad_rows >> r & 1u)) return false;
                 const int at_row = p.cached + (p.row0 + r) / a.G;
-                const int from = a.window > 0 ? at_row - static_cast<int>(a.window) + 1 : INT_MIN / 2;
+                const int from = p.low + (p.row0 + r) / a.G;
                 bool x = noted > kNoted;
                 for (int i = 0; i < min(noted, kNoted); ++i) {
                     const int q = *reinterpret_cast<volatile int*>(&ctl.note[item % kItems][i]);

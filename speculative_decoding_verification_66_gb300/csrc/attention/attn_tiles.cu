@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             bool begun = false;
             {
                 // The last position that the row sees, and the first.
-                const int pos = g.cached + (g.row0 + min(slot_row, rows - 1)) / a.G;
-                const int low = a.window > 0 ? pos - static_cast<int>(a.window) + 1 : INT_MIN / 2;
+                const int of = (g.row0 + min(slot_row, rows - 1)) / a.G;
+                const int pos = g.cached + of, low = g.low + of;
                 const int k0 = PAIR ? (s ? g.lo1 : g.lo0) : s;
                 const int k1 = PAIR ? (s ? g.hi1 : g.hi0) : g.n;
                 float row_c = a.scale_log2, c = row_c;
@@ -462,8 +462,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             const int r = g.row0 + min(slot_row, rows - 1), token = r / a.G;
             bool again = noted > kNoted;
             if (noted > 0) {
-                const int pos = g.cached + token;
-                const int low = a.window > 0 ? pos - static_cast<int>(a.window) + 1 : INT_MIN / 2;
+                const int pos = g.cached + token, low = g.low + token;
                 for (int i = 0; i < min(noted, kNoted); ++i) {
                     const int p = *reinterpret_cast<volatile int*>(&ctl.note[item % kItems][i]);
                     again |= p >= low && p <= pos;

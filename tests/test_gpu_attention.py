@@ -605,3 +605,29 @@ def test_a_bad_page_reaches_only_the_rows_that_see_it(dtype, e4m3, T, d, at, win
         for b in range(2):  # (never read by the good rows: any page will do for the reference)
             c.table[b, (at + (0, 3696)[b]) // 16] = c.unused[0]
         check(out, lse, c, q, d ** -0.5, window, rows=good)
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_windows_longer_than_30_bits(T):
+    """A window of 2^30 + 2^29 positions on two pages, one of which is nearly all of them; weights are
+    all alike but for a key right before the first row's window and one that the first rows see."""
+    window, P = (1 << 30) + (1 << 29), 1024
+    low = (1 << 28) + 500
+    cached = low + window - 1
+    assert low % P == 500 and 500 % 128 < 124 and cached + T < 1 << 31
+    pages = torch.zeros(2, P, 1, 16, device="cuda").bfloat16()
+    values = torch.ones_like(pages)
+    pages[1, 499], pages[1, 503] = 8.0, 8.0  # scores of 32 under queries of ones
+    values[1, 499], values[1, 503] = 100.0, 5.0
+    table = torch.zeros(1, 1 << 21, dtype=torch.int32, device="cuda")
+    table[0, low // P] = 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.ones(T, 1, 16, device="cuda").bfloat16()
+    out, lse = sv.sv_chunk_attention(q, pages, values, table, torch.tensor([cached], **i32),
+                                     torch.tensor([0, T], **i32), window=window, max_chunk=T,
+                                     return_lse=True)
+    # Row t sees position low + t on: the key of 32 at low + 3 weighs e^32 = 8e13 against 1.6e9.
+    for t in range(T):
+        want = 5.0 if t <= 3 else 1.0
+        assert (out[t].float() - want).abs().max() <= 2.0 ** -8 * want + 4.0 * window / math.exp(32)
+        assert abs(float(lse[t, 0]) - (32.0 if t <= 3 else math.log(window))) < 1e-3
