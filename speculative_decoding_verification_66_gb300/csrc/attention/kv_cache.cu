@@ -81,13 +81,10 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const Cache c, const Pac
     const int64_t t = w / parts;
     const int part = static_cast<int>(w - t * parts);
     if (t >= p.tokens) return;
+    int taken, passed;
+    const int b = find_seq(c.starts, c.B, t, lane, &taken, &passed);
+    const Seq q = seq_of(c, b, p.tokens, p.tokens);
     int32_t page = -1, slot = 0;
-    int b = 0, taken = 0, passed = 0;
-    Seq q{0, 0, 0, 0};
-    if (c.B > 0) {  // (a read of no sequences: all rows are NaN)
-        b = find_seq(c.starts, c.B, t, lane, &taken, &passed);
-        q = seq_of(c, b, p.tokens, p.tokens);
-    }
     if (!q.bad && t >= q.start && t - q.start < q.count &&
         __all_sync(0xFFFFFFFFu, taken <= q.start && passed - q.start >= q.count)) {
         const int64_t pos = q.cached + (t - q.start);
@@ -214,8 +211,15 @@ cudaError_t launch_move(const Cache& c, const Packed& p, cudaStream_t s)
 template <bool READ>
 cudaError_t launch_any(const Cache& c, const Packed& p, bool f16, bool e4m3, cudaStream_t s)
 {
-    if (p.tokens == 0 && (c.B == 0 || p.status == nullptr)) return cudaSuccess;
-    if (c.B == 0 && !READ) return cudaSuccess;
+    if (c.B == 0) {
+        // Rows of no sequence: NaN of either type.
+        const size_t bytes = static_cast<size_t>(p.tokens) * c.Hkv * c.D * 2;
+        cudaError_t e = cudaSuccess;
+        for (int i = 0; READ && bytes > 0 && i < 2 && e == cudaSuccess; ++i)
+            e = cudaMemsetAsync(p.x[i], 0xFF, bytes, s);
+        return e;
+    }
+    if (p.tokens == 0 && p.status == nullptr) return cudaSuccess;
     if (!e4m3) return launch_move<Bf16, false, READ>(c, p, s);  // 16-bit elements move as they are
     return f16 ? launch_move<F16, true, READ>(c, p, s) : launch_move<Bf16, true, READ>(c, p, s);
 }
