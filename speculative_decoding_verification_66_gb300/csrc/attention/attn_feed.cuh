@@ -255,6 +255,16 @@ __device__ __forceinline__ float score_factor(float c)
     return fmaxf(c, __uint_as_float(0x00800000u));
 }
 
+// A weight is 2^(s c - m), by one rounding, with m the rounded product of the largest
+// score: where that is so large that its own rounding counts, the largest weight would
+// be anything up to infinity. Such rows are computed again, where scores are rounded
+// before they are compared. (Below 2^22 the weights are off by the square root of 2 at
+// most, which their types have room for.)
+__device__ __forceinline__ bool too_far(float m)
+{
+    return fabsf(m) > 4194304.f && m != __uint_as_float(sv::kF32NegInfBits);
+}
+
 __device__ __forceinline__ bool any_special(uint4 w, uint32_t exponent)
 {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};

@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             // The slot's products so far are complete: s_full's
                             // commit came after them.
                             const float keep = grow ? sv::ex2(m - (mt - rise<T, E4M3>())) : 1.f;
+                            if (grow && too_far(m)) atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
 #pragma unroll 1
                             for (int x = 0; x < DP / 16; ++x) {
                                 float o[16];
@@ -426,6 +427,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             // O's true size: e4m3, its reference exponent.
             const float size = E4M3 && ref != 0 ? exp_value(static_cast<uint32_t>(ref)) : 1.f;
             float w0 = size, w1 = 0.f;
+            bool far = too_far(m);
             if (!PAIR) {
                 // The slots exchange their rows' maxima and sums through the
                 // scores' columns, which the products have done with.
@@ -442,6 +444,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     float om, ol, osize, none;
                     tmem_ld4(lane_base + (1 - s) * 128, om, ol, osize, none);
                     fence_before();
+                    far |= too_far(om);
                     const float top = fmaxf(m, om);
                     const float wm = m == top ? 1.f : sv::ex2(m - top);
                     const float wo = om == top ? 1.f : sv::ex2(om - top);
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             const bool bad = *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0 &&
                              meets_bad_page(a, g, min(slot_row, rows - 1));
             const int r = g.row0 + min(slot_row, rows - 1), token = r / a.G;
-            bool again = noted > kNoted;
+            bool again = far || noted > kNoted;
             if (noted > 0) {
                 const int pos = g.cached + token, low = g.low + token;
                 for (int i = 0; i < min(noted, kNoted); ++i) {

@@ -229,3 +229,26 @@ def test_large_keys_under_small_queries(T, d, e):
     x[:, :, 7] = 0.0
     c.parts[0][at] = x
     agrees(quantised(c), q, T)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("T,d", ROWS)
+@pytest.mark.parametrize("size", [1e6, 1e7, 1e8, 1e9, 1e10, 1e12])
+@pytest.mark.parametrize("sign", [1, -1, 0])
+def test_scores_far_beyond_any_models(cache, T, d, size, sign):
+    """Scores of up to 10^12 of one or of both signs, in falling or rising order or none: one key takes
+    all the weight, and the rounding of scores that large is no exponent."""
+    n = 900 + T
+    c = Cache([900, 3], [T, T], 2, d, 16, "fp16" if cache == "fp16" else "bf16", False, seed=2)
+    at = places(c, 0, n)
+    ramp = torch.linspace(1.0, 2.0, n, device="cuda").double()
+    along = {1: ramp, -1: -ramp, 0: ramp * torch.where(torch.arange(n, device="cuda") % 2 == 0, 1, -1)}
+    x = c.parts[0][at].double() * 2.0 ** -9
+    x[:, :, 5] = along[sign][:, None]
+    c.parts[0][at] = x.to(c.dtype)
+    q = queries(c, 4)
+    q[:, :, 5] = 1.0
+    if cache == "e4m3":
+        c = quantised(c)
+    agrees(c, q, T, scale=size)
+    agrees(c, q, T, scale=size, times=100)
