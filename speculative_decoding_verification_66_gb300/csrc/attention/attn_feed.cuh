@@ -37,12 +37,12 @@ __device__ __forceinline__ float rise()
 // or kSink below.
 constexpr int kLift = 7, kSink = 2;
 // Keys or values of one tile may be this many powers of two apart (see code_factor).
-constexpr int kSpread = 13;
+constexpr int kSpread = 22;
 // The values of a segment's tiles may be this many powers of two apart: outputs that
-// follow them stay below 2^127 (values 2^9, weights 2^8, 2^30 keys), and moved() is
+// follow them stay below 2^127 (values 2^16, weights 2^15, 2^30 keys), and moved() is
 // exact. Beyond, the segment's rows are computed again.
 constexpr int kFar = 60;
-// A row's scores are below 2^31 before they are multiplied by its query's factor and
+// A row's scores are below 2^38 before they are multiplied by its query's factor and
 // by the key's exponent, in either order: keys above 2^kLarge or a factor above 2^67
 // might overflow on the way where the product does not. All rows are computed again.
 constexpr uint32_t kLarge = 127 + 60;
@@ -174,11 +174,14 @@ __device__ __forceinline__ Plan plan_of(const Attn& a, const Segment& g)
 
 // ---------------------------------------------------------------------------
 // Expanding e4m3 to float16, relative to the largest exponent `top` of a tile:
-// code 2^(e - top), the conversion and one multiplication for two values. Codes
-// have three mantissa bits and a least step of 2^-9, so this is exact for
-// top - e <= kSpread = 13 (2^-22, where float16 has 2^-24) and off by at most
-// 2^-25 below that.
+// code 2^(kUp + e - top), the conversion and one multiplication for two values. Codes
+// have three mantissa bits, a least step of 2^-9 and are at most 448, which kUp = 7
+// brings to 57344: this is exact for top - e <= kSpread = 22 (2^-24, float16's least).
+// Rows of tiles whose vectors lie further apart are computed again, key by key, which
+// takes a hundred times as long and more; so the range counts.
 // ---------------------------------------------------------------------------
+constexpr int kUp = 7;
+constexpr float kDown = 1.f / (1 << kUp);
 __device__ __forceinline__ uint32_t both(uint32_t h) { return h | (h << 16); }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
 {
@@ -201,7 +204,9 @@ __device__ __forceinline__ uint32_t code_factor(uint32_t e, uint32_t top)
 {
     if (e == 255u) return both(0x7FFFu);
     const int d = static_cast<int>(top) - static_cast<int>(e);
-    return both(d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u);
+    return both(d <= 14 + kUp   ? static_cast<uint32_t>(15 + kUp - d) << 10
+                : d <= 24 + kUp ? 1u << (24 + kUp - d)
+                                : 0u);
 }
 // 16 codes times a factor, as sixteen float16 values.
 __device__ __forceinline__ void expand(uint4 codes, uint32_t f, uint32_t (&o)[8])
@@ -214,15 +219,15 @@ __device__ __forceinline__ void expand(uint4 codes, uint32_t f, uint32_t (&o)[8]
         o[2 * i + 1] = mul2(s.y, f);
     }
 }
-// Exponent bytes up to kLeast stand for vectors of zeros, nearly always, and for
-// vectors of next to nothing (up to 448 2^-117). Zeros must not move a tile's or the
+// Exponent bytes up to kLeast stand for vectors of zeros, nearly always (10), and for
+// vectors of next to nothing (up to 448 2^-87). Zeros must not move a tile's or the
 // outputs' exponent, so these vectors are left out there. Somebody looks at their
 // codes, and where one is not zero all rows are computed again: with few rows the
 // loads, from memory, behind the workers' backs (131k keys 231 us; anywhere in the
 // workers' loop 240 and more, against 229 without); in the tile kernel, whose loading
 // warps have no registers for it (256 x 9 tokens 753 us), the helpers, whom a factor of
 // minus zero tells which rows (660, against 655 without).
-constexpr uint32_t kLeast = 10, kUnless = 0x8000u;
+constexpr uint32_t kLeast = 40, kUnless = 0x8000u;
 __device__ __forceinline__ bool not_zeros(uint4 codes)
 {
     return ((codes.x | codes.y | codes.z | codes.w) & 0x7F7F7F7Fu) != 0;
@@ -247,9 +252,9 @@ __device__ __forceinline__ float row_factor(float c, int* noted)
 }
 // The factor of a row's scores: the above and the keys' power of two. Where these
 // multiply to nothing (a row of zeros, keys of zeros) a hidden score's -inf times zero
-// would be NaN. Scores are below 2^31 before this factor (few rows: times a key's
+// would be NaN. Scores are below 2^38 before this factor (few rows: times a key's
 // exponent, 2^91), so the least normal number in the place of a smaller one moves none
-// by 2^-95 (2^-35).
+// by 2^-88 (2^-35).
 __device__ __forceinline__ float score_factor(float c)
 {
     return fmaxf(c, __uint_as_float(0x00800000u));

@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     }
                 }
             };
-            const float size = E4M3 && ref != 0 ? exp_value(static_cast<uint32_t>(ref)) : 1.f;
+            const float size = E4M3 && ref != 0 ? exp_value(static_cast<uint32_t>(ref)) * kDown : 1.f;
             // All columns at one time where they fit, else kJoin at a time.
             const bool once = rows * DP <= X::kRows * X::kJoin;
             const int width = once ? DP : X::kJoin;

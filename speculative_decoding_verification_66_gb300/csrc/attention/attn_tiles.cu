@@ -51,7 +51,7 @@
 // tile's exponents come back in where they cost nothing: the keys' in the scale of
 // the tile's scores, the values' in the exponent of its weights, which are
 // float16 too; O is kept relative to a reference exponent that follows the
-// tiles'. Keys or values of a tile that are more than 2^13 apart would lose bits (a
+// tiles'. Keys or values of a tile that are more than 2^22 apart would lose bits (a
 // key that a row does not see could take them from those that it does); a segment
 // that has such a tile computes its rows again, key by key. bfloat16
 // queries become float16, each row scaled by a power of two that brings its
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             if (!(ok = wait_all(&ctl.o_full, item))) break;
             fence_after();
             // O's true size: e4m3, its reference exponent.
-            const float size = E4M3 && ref != 0 ? exp_value(static_cast<uint32_t>(ref)) : 1.f;
+            const float size = E4M3 && ref != 0 ? exp_value(static_cast<uint32_t>(ref)) * kDown : 1.f;
             float w0 = size, w1 = 0.f;
             bool far = too_far(m);
             if (!PAIR) {
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     const uint32_t* factor = &ctl.factor[raw_at.stage][row0];
                     if (!is_v && tid == 0) {
                         const uint2 top = ctl.top[raw_at.stage];
-                        ctl.k_scale[k_tiles & 3] = exp_value(top.x & 255u);
+                        ctl.k_scale[k_tiles & 3] = exp_value(top.x & 255u) * kDown;
                         ctl.v_top[k_tiles & 3] = static_cast<int>(top.y);
                     }
                     const bool ragged = k < inner_lo || k > inner_hi;

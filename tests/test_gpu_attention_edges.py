@@ -252,3 +252,47 @@ def test_scores_far_beyond_any_models(cache, T, d, size, sign):
         c = quantised(c)
     agrees(c, q, T, scale=size)
     agrees(c, q, T, scale=size, times=100)
+
+
+@pytest.mark.parametrize("dtype,k", [("bf16", k) for k in (12, 13, 14, 20, 21, 22, 23, 24, 30)]
+                         + [("fp16", k) for k in (12, 13)])  # (as far as float16 sources reach)
+@pytest.mark.parametrize("T,d", ROWS)
+def test_vectors_of_a_tile_far_apart(dtype, k, T, d):
+    """Every third key and value 2^-k times the others, and the weight on these: the queries are along
+    the small keys' own channel, which the large ones do not have."""
+    n = 290 + T
+    c = Cache([290, 3], [T, T], 2, d, 16, dtype, False, seed=k)
+    small = torch.arange(n, device="cuda") % 3 == 0
+    at = places(c, 0, n)
+    x = c.parts[0][at].double() * torch.where(small, 2.0 ** -k, 1.0).double()[:, None, None]
+    x[~small, :, 5] = 0.0
+    x[small, :, 5] = 4.0 * 2.0 ** -k
+    c.parts[0][at] = x.to(c.dtype)
+    scale_by(c, 1, torch.where(small, 2.0 ** -k, 1.0))
+    q = torch.zeros(2 * T, 8, d, dtype=c.dtype, device="cuda")
+    q[:, :, 5] = 16.0
+    agrees(quantised(c), q, T, scale=2.0 ** k / 4 if dtype == "bf16" else 2.0 ** k / 8)
+    agrees(c, q, T, scale=2.0 ** k / 4 if dtype == "bf16" else 2.0 ** k / 8, times=100)
+
+
+@pytest.mark.parametrize("T", [1, 5])
+def test_vectors_far_apart_take_the_ordinary_time(T):
+    """A value 2^-20 times its neighbours is expanded like the others: no row is computed again."""
+    c = quantised(Cache([20000, 3], [T, T], 2, 128, 16, "bf16", False, seed=1))
+    q = queries(c, 4)
+
+    def time():
+        ms = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            sv.sv_chunk_attention(q, *c.args(), **c.exp_args(), max_chunk=T)
+            b.record()
+            torch.cuda.synchronize()
+            ms.append(a.elapsed_time(b))
+        return min(ms)
+
+    ordinary = time()
+    page, slot = places(c, 0, 20000)
+    c.exps[1][page[5000], slot[5000]] -= 20
+    assert time() < 3 * ordinary + 0.1
