@@ -357,7 +357,9 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             // The slot's products so far are complete: s_full's
                             // commit came after them.
                             const float keep = grow ? sv::ex2(m - (mt - rise<T, E4M3>())) : 1.f;
-                            if (grow && too_far(m)) atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
+                            // (lanes without a row have scores of whatever lies in its place)
+                            if (grow && slot_row < rows && too_far(m))
+                                atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
 #pragma unroll 1
                             for (int x = 0; x < DP / 16; ++x) {
                                 float o[16];

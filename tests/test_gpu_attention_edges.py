@@ -296,3 +296,31 @@ def test_vectors_far_apart_take_the_ordinary_time(T):
     page, slot = places(c, 0, 20000)
     c.exps[1][page[5000], slot[5000]] -= 20
     assert time() < 3 * ordinary + 0.1
+
+
+@pytest.mark.parametrize("T", [5, 7, 31, 33, 37, 65])
+@pytest.mark.parametrize("cache", ["bf16", "fp16", "e4m3"])
+def test_rows_that_do_not_exist_cost_nothing(T, cache):
+    """Items whose last rows are missing, behind a call that leaves large queries in shared memory: no
+    row is computed again for what lies in the missing ones' places."""
+    def calls(T, size):
+        c = Cache([3000, 2000], [T, T], 2, 128, 64, "fp16" if cache == "fp16" else "bf16", False, seed=1,
+                  spread=1000.0)
+        c = quantised(c) if cache == "e4m3" else c
+        q = queries(c, 4, size)
+        q = q.repeat(8, 1, 1)
+        starts = torch.arange(0, 16 * T + 1, T, dtype=torch.int32, device="cuda")
+        args = (q, *c.parts, c.table.repeat(8, 1), c.cached.repeat(8), starts)
+        return lambda: sv.sv_chunk_attention(*args, **c.exp_args(), max_chunk=T)
+
+    large, some = calls(64, 8000.0), calls(T, 0.001)
+    ms = []
+    for _ in range(3):
+        large()
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        some()
+        b.record()
+        torch.cuda.synchronize()
+        ms.append(a.elapsed_time(b))
+    assert min(ms) < 5.0, ms  # some 0.1; rows computed again take 20 and more
