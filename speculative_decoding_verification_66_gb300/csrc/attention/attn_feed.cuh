@@ -265,9 +265,17 @@ __device__ __forceinline__ float score_factor(float c)
 // be anything up to infinity. Such rows are computed again, where scores are rounded
 // before they are compared. (Below 2^22 the weights are off by the square root of 2 at
 // most, which their types have room for.)
+// Asked whenever m moves; it is finite or inf then.
 __device__ __forceinline__ bool too_far(float m)
 {
-    return fabsf(m) > 4194304.f && m != __uint_as_float(sv::kF32NegInfBits);
+    return fabsf(m) > 4194304.f;
+}
+
+// Notes that all rows of a segment have to be computed again. (A plain store: the
+// number only has to stay above kNoted.)
+__device__ __forceinline__ void note_all(int* noted)
+{
+    *reinterpret_cast<volatile int*>(noted) = kNoted + 1;
 }
 
 __device__ __forceinline__ bool any_special(uint4 w, uint32_t exponent)

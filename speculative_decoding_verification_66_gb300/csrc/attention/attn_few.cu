@@ -390,7 +390,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         if (x > m[i] + slack<T, E4M3>()) {
                             x -= rise<T, E4M3>();
                             const float keep = sv::ex2(m[i] - x);
-                            if (too_far(m[i])) atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
                             l[i] *= keep;
 #pragma unroll
                             for (int j = 0; j < DP / 8; ++j) {
@@ -398,6 +397,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                                 o[j][2 * i + 1] *= keep;
                             }
                             m[i] = x;
+                            if (too_far(x)) note_all(&ctl.noted[item % kItems]);
                         }
                     }
                 }
@@ -515,10 +515,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             for (int i = 0; i < 2; ++i) {
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-                if (c4 == 0) {
-                    ctl.ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
-                    if (too_far(m[i])) atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
-                }
+                if (c4 == 0) ctl.ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
             }
             const bool whole = p.whole != 0;
             const float nan = __uint_as_float(0x7FFFFFFFu);

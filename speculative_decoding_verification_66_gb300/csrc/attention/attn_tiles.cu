@@ -357,9 +357,6 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             // The slot's products so far are complete: s_full's
                             // commit came after them.
                             const float keep = grow ? sv::ex2(m - (mt - rise<T, E4M3>())) : 1.f;
-                            // (lanes without a row have scores of whatever lies in its place)
-                            if (grow && slot_row < rows && too_far(m))
-                                atomicAdd(&ctl.noted[item % kItems], kNoted + 1);
 #pragma unroll 1
                             for (int x = 0; x < DP / 16; ++x) {
                                 float o[16];
@@ -370,7 +367,11 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                             }
                             l *= keep;
                         }
-                        if (grow) m = mt - rise<T, E4M3>();
+                        if (grow) {
+                            m = mt - rise<T, E4M3>();
+                            // (lanes without a row have scores of whatever lies in its place)
+                            if (too_far(m) && slot_row < rows) note_all(&ctl.noted[item % kItems]);
+                        }
                         begun = true;
                         const float shift = (m == ninf ? 0.f : -m) + static_cast<float>(lift);
                         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
@@ -429,7 +430,6 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             // O's true size: e4m3, its reference exponent.
             const float size = E4M3 && ref != 0 ? exp_value(static_cast<uint32_t>(ref)) * kDown : 1.f;
             float w0 = size, w1 = 0.f;
-            bool far = too_far(m);
             if (!PAIR) {
                 // The slots exchange their rows' maxima and sums through the
                 // scores' columns, which the products have done with.
@@ -446,7 +446,6 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     float om, ol, osize, none;
                     tmem_ld4(lane_base + (1 - s) * 128, om, ol, osize, none);
                     fence_before();
-                    far |= too_far(om);
                     const float top = fmaxf(m, om);
                     const float wm = m == top ? 1.f : sv::ex2(m - top);
                     const float wo = om == top ? 1.f : sv::ex2(om - top);
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
             const bool bad = *reinterpret_cast<volatile int*>(&ctl.bad_page[item % kItems]) != 0 &&
                              meets_bad_page(a, g, min(slot_row, rows - 1));
             const int r = g.row0 + min(slot_row, rows - 1), token = r / a.G;
-            bool again = far || noted > kNoted;
+            bool again = noted > kNoted;
             if (noted > 0) {
                 const int pos = g.cached + token, low = g.low + token;
                 for (int i = 0; i < min(noted, kNoted); ++i) {
