@@ -224,7 +224,9 @@ def sv_chunk_attention(query, k_pages, v_pages, page_table, cached_lens, chunk_s
     to its own, cached_lens[b] + t, and with a ``window`` only the last ``window`` of them.
 
     ``scale`` defaults to head_dim ** -0.5. ``max_chunk``: an upper bound of the sequences' new
-    tokens (0: tokens); a tight one lets the launches be planned for it. Returns out, or (out, lse)
+    tokens (0: tokens); a tight one lets the launches be planned for it (512 single tokens take half
+    as long again without). A workspace (up to 43 MB) is kept for the thread and stream
+    unless one is given (``sv_chunk_attention_workspace_bytes``). Returns out, or (out, lse)
     with ``return_lse`` or an ``lse`` tensor (float32 [tokens, q_heads])."""
     return _attention(query, k_pages, v_pages, page_table, cached_lens, chunk_starts, k_exps, v_exps,
                       scale, window, max_chunk, out, lse, return_lse, seq_status, workspace, stream)

@@ -13,13 +13,14 @@
 // A warp keeps a maximum, a sum and an output of its own for every row; they
 // are joined through shared memory at the end of a segment.
 //
-// Measured: 512 single tokens, 500 to 2000 cached, 16 heads of 64: 455 us, 5.8 TB/s
-// (with attn_tiles.cu 732 us); 4 tokens over 131000 e4m3 keys, 32 heads on 8: 230 us,
-// 4.7 TB/s (299 us); the reads bound the first, the reads and the conversions the
-// second (193 us with the loads alone). From 17 rows on the 128-row products win: 64
-// sequences of 20 rows 148 us against 156 here, of 32 rows 158 against 197. Heads of
-// 256: 64 x 5 tokens 341 us, a piece of 512 tokens 654 us (161 TFLOP/s), ten to
-// twenty times faster than a row at a time.
+// Measured: 512 single tokens, 500 to 2000 cached, 16 heads of 64: 467 us, 5.6 TB/s
+// (with attn_tiles.cu 712 us); 4 tokens over 131000 e4m3 keys, 32 heads on 8: 233 us,
+// 4.6 TB/s (300 us); the reads bound the first, the reads and the conversions the
+// second (193 us with the loads alone). At 16 rows (64 x 4 tokens after 4000, 32 heads
+// on 8) bfloat16 heads of 128 take 177 us here and 173 there, of 64 148 and 138, e4m3
+// 173 and 190, 150 and 170. At 20 rows, which are two items here, 325 and 174, 268 and
+// 140, e4m3 309 and 190, 275 and 170: up to 16, whatever the cache. Heads of 256: 64 x
+// (1 to 5) tokens 344 us, a piece of 512 tokens after 3000 455 us (120 TFLOP/s).
 //
 // Warps 0-7 work, 8 and 9 load keys and values (attn_feed.cuh). Masks, hidden
 // values and the sharing among blocks are those of attn_tiles.cu.

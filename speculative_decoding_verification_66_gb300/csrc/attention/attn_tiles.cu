@@ -8,8 +8,14 @@
 // chip. S, P and O live in tensor memory, a row to a lane: a thread owns a row,
 // so the maximum and the sum need no exchange between threads. O is rescaled
 // only when the maximum has grown by more than slack() powers of two since the
-// last time: the weights stay below 2^slack(), which is what their type holds
-// without loss, and hardly any tile after the first needs it.
+// last time: the weights stay below 2^slack(), which their type holds, and hardly any
+// tile after the first needs it.
+//
+// P is rounded to the values' type, since a product's operands have to be of one type:
+// by at most 2^-8 each in bfloat16, which takes the outputs' error from 0.0017 of their
+// size, their own rounding, to 0.0023; in float16 (e4m3 caches too) by 2^-11, next to
+// nothing. Two products, with P as the sum of two bfloat16, would take that away for
+// half as much again of the tensor core's time.
 //
 // Two slots, each with its own S, O and softmax warpgroup, take turns on the
 // tensor core: while one slot's rows go through the softmax, the other's
@@ -62,14 +68,14 @@
 // depend on the lengths and the number of blocks alone.
 //
 // What bounds it. 16-bit drafts: the reads of the cache (64 x 5 tokens, contexts
-// 1000 to 4000, 32 heads on 8: 122 us, 5.4 TB/s with both ends of a short call in
-// it; 32 x (1 to 17), 8000 to 32768, 64 on 8: 434 us, 6.2 TB/s of 6.8). Pieces of
+// 1000 to 4000, 32 heads on 8: 123 us, 5.4 TB/s with both ends of a short call in
+// it; 32 x (1 to 17), 8000 to 32768, 64 on 8: 436 us, 6.2 TB/s of 6.8). Pieces of
 // prompts: the way from scores to weights to products, which the other slot covers
-// in part (2048 tokens after 6000: 212 us, 1.11 PFLOP/s of 1.91; the tensor pipe
+// in part (2048 tokens after 6000: 213 us, 1.11 PFLOP/s of 1.91; the tensor pipe
 // runs half of the cycles). e4m3: the chain of loads, expansion, scores, weights and
 // products, of which no part alone takes more than a sixth of the time (256 x 9:
-// 664 us, 3.0 TB/s of codes, which are 6.0 TB/s of values; pieces of 1 to 700 tokens
-// with a window: 161 us), and some 8 us from an item to the next.
+// 660 us, 3.0 TB/s of codes, which are 6.0 TB/s of values; pieces of 1 to 700 tokens
+// with a window: 169 us), and some 8 us from an item to the next.
 #include "attn_feed.cuh"
 
 namespace sva {
@@ -207,10 +213,10 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
         // ------------------------------------------------------------------
         if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kRegsRow));
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-        // Columns of scores in registers at a time: 64 wait for fewer loads (a
-        // 2048-token piece 222 us against 228 with 32); e4m3 has more code to keep
-        // in the instruction caches and fewer registers (256 x 9: 668 us with 32,
-        // 724 with 64 and 120 registers, which spill).
+        // Columns of scores in registers at a time: 64 wait for fewer loads (when
+        // this was chosen, a 2048-token piece 222 us against 228 with 32); e4m3 has
+        // more code to keep in the instruction caches and fewer registers (256 x 9:
+        // 668 us with 32, 724 with 64 and 120 registers, which spill).
         constexpr bool kWide = !E4M3;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t s_addr = lane_base + s * 128, o_addr = lane_base + 256 + s * DP;
@@ -858,9 +864,10 @@ cudaError_t launch_attention_tiles(const Attn& a, bool f16, bool e4m3, void* wor
     Tiles t;
     int blocks = 0;
     // PAIR where the sequences have more than 128 rows on average (their number is
-    // known, their lengths are not). 64 x 33 tokens of 4 heads: 265 us with, 365
-    // without; chunks from 1 to 33: 185 and 166, 32 x (1 to 17) of 8 heads: 500
-    // and 464: items of up to 128 rows leave the second slot idle.
+    // known, their lengths are not). 64 x 33 tokens of 4 heads after 4000: 262 us
+    // with, 338 without, 64 x 64: 269 and 353, a piece of 2048: 214 and 228; chunks
+    // from 1 to 33: 165 and 138, 32 x (1 to 17) of 8 heads: 476 and 440: items of up
+    // to 128 rows leave the second slot idle.
     const bool pair = a.max_chunk * a.G > 128 && a.tokens * a.G > 128 * static_cast<int64_t>(a.c.B);
     const int64_t rows = item_rows(a.max_chunk, a.G, pair ? 256 : 128);
     cudaError_t e = set_up(a, f16, e4m3, rows, workspace, false, &k, &v, &t, &blocks);
