@@ -244,6 +244,13 @@ __device__ __forceinline__ float moved(int ref, int top)
     return ref == 0 ? 1.f : exp_value(static_cast<uint32_t>(max(min(127 + ref - top, 227), 27)));
 }
 
+// The exponent (biased) that a bfloat16 query row is scaled by, from the bits of its
+// largest element. A row with an infinity or a NaN has nothing to lose: its size is 1.
+__device__ __forceinline__ int row_exponent(uint32_t top)
+{
+    const int e = max(static_cast<int>(top >> 23), 15);
+    return e == 255 ? 127 + 14 : e;
+}
 // The query's part of the factor of a row's scores: the scale and its power of two.
 __device__ __forceinline__ float row_factor(float c, int* noted)
 {
@@ -265,10 +272,10 @@ __device__ __forceinline__ float score_factor(float c)
 // be anything up to infinity. Such rows are computed again, where scores are rounded
 // before they are compared. (Below 2^22 the weights are off by the square root of 2 at
 // most, which their types have room for.)
-// Asked whenever m moves; it is finite or inf then.
+// Asked whenever m moves. Where it is infinite the row is NaN either way.
 __device__ __forceinline__ bool too_far(float m)
 {
-    return fabsf(m) > 4194304.f;
+    return fabsf(m) > 4194304.f && m < __uint_as_float(0x7F800000u);
 }
 
 // Notes that all rows of a segment have to be computed again. (A plain store: the

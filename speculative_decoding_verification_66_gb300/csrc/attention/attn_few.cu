@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     }
                     top = __reduce_max_sync(0xFFFFFFFFu, top);
                     if (lane == 0) {
-                        const float size = __uint_as_float(
-                            static_cast<uint32_t>(max(static_cast<int>(top >> 23), 15) - 14) << 23);
+                        const float size =
+                            __uint_as_float(static_cast<uint32_t>(row_exponent(top) - 14) << 23);
                         ctl.q_scale[warp + 8 * i] = size;
                         row_factor(a.scale_log2 * size, &ctl.noted[item % kItems]);
                     }

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(Shape<DP, E4M3, PAIR>::kThreads, 1)
                     for (int d = kChunks / 2; d > 0; d >>= 1)
                         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
                     // 2^(14 - exponent), at most 2^126
-                    const int e = max(static_cast<int>(top >> 23), 15);
+                    const int e = row_exponent(top);
                     const float up = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
                     uint32_t h[4];
 #pragma unroll

@@ -324,3 +324,48 @@ def test_rows_that_do_not_exist_cost_nothing(T, cache):
         torch.cuda.synchronize()
         ms.append(a.elapsed_time(b))
     assert min(ms) < 5.0, ms  # some 0.1; rows computed again take 20 and more
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("T", [1, 5, 40])
+@pytest.mark.parametrize("cache", ["bf16", "fp16", "e4m3"])
+def test_a_sequence_that_is_not_finite_costs_nothing(T, cache, bad):
+    """A query, and a cached key that every row sees, that are NaN or infinite: their rows are NaN, the
+    others as they were, and nothing is computed again."""
+    c = Cache([3000, 2000], [T, T], 2, 128, 64, "fp16" if cache == "fp16" else "bf16", False, seed=1)
+    q = queries(c, 4)
+    k = c.parts[0].clone()
+    page, slot = places(c, 0, 3000)
+    for kind in ("query", "key"):
+        c.parts[0].copy_(k)
+        x = q.clone()
+        if kind == "query":
+            x[T - 1, 5, 7] = bad
+        else:
+            c.parts[0][page[1500], slot[1500], 1, 7] = bad
+        e = Cache([3000, 2000], [T, T], 2, 128, 64, "bf16", False, seed=1) if cache == "e4m3" else c
+        if cache == "e4m3":
+            e.parts[0].copy_(c.parts[0])
+            e = quantised(e)
+        ms = []
+        for _ in range(3):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            out, lse = sv.sv_chunk_attention(x, *e.args(), **e.exp_args(), max_chunk=T, return_lse=True)
+            b.record()
+            torch.cuda.synchronize()
+            ms.append(a.elapsed_time(b))
+        hit = torch.zeros(2 * T, 8, dtype=torch.bool, device="cuda")
+        if kind == "query":
+            hit[T - 1, 5] = True
+        else:
+            hit[:T, 4:] = True
+        ref, _, tol, _ = reference(e, torch.where(hit[..., None], torch.zeros_like(x), x)
+                                   if kind == "query" else x, 128 ** -0.5)
+        err = (out.double() - ref).abs()
+        assert (err <= tol)[~hit].all()
+        # (an infinite key takes nothing from rows whose product with it is -inf)
+        sure = hit if kind == "query" or math.isnan(bad) or cache == "e4m3" else \
+            hit & (x[:, :, 7].float() * bad > 0)
+        assert out[sure].isnan().all()
+        assert min(ms) < 2.0, ms
