@@ -43,8 +43,9 @@ constexpr int kSpread = 22;
 // exact. Beyond, the segment's rows are computed again.
 constexpr int kFar = 60;
 // A row's scores are below 2^38 before they are multiplied by its query's factor and
-// by the key's exponent, in either order: keys above 2^kLarge or a factor above 2^67
-// might overflow on the way where the product does not. All rows are computed again.
+// by the key's exponent, in either order: exponent bytes above kLarge (2^60) or a
+// factor above 2^67 might overflow on the way where the product does not. All rows
+// are computed again.
 constexpr uint32_t kLarge = 127 + 60;
 
 constexpr int kMaxBlocks = 160;  // shares in the workspace; grids are no larger
@@ -502,8 +503,8 @@ __device__ __forceinline__ const Plan* plan_at(Ctl& ctl, int i, Wait& wait_all)
 // segments. e4m3: the factors that the codes are multiplied by (FEW: of keys, the
 // powers of two themselves; of values, as halves), and with the keys the largest
 // exponents of the tile's keys and values (FEW: with the values, of these), plus 256
-// where the codes of rows with the factor kUnless have to be looked at. The page of tile k + 2 and the exponents of tile k + 1 are on their way while tile k
-// is issued.
+// where the codes of rows with the factor kUnless have to be looked at. The page of
+// tile k + 2 and the exponents of tile k + 1 are on their way while tile k is issued.
 template <class T, int DP, bool E4M3, int R, bool SPLIT, bool ALT, int FILL, bool FEW, class Ctl,
           class Wait>
 __device__ __forceinline__ void feed(const Tiles& args, Ctl& ctl, const CUtensorMap* map, int kv,
