@@ -11,6 +11,11 @@ library; there is no CPU or eager fallback.
 libsvattention.so) are the step before it in the target model: the new
 positions' keys and values go into a paged cache, 16-bit or e4m3, and their
 queries attend to it.
+
+``sv_token_logprobs`` and ``sv_distill_loss`` (include/sv_logprobs.h,
+libsvlogprobs.so) stand beside it: the log probabilities, entropies and
+alternatives of the tokens that a round emits, and the distillation of the
+target's top alternatives into the draft model, with their gradients.
 """
 from .api import (  # noqa: F401
     SV_BF16,
@@ -61,4 +66,22 @@ from .attention import (  # noqa: F401
     sv_kv_append,
     sv_kv_read,
 )
-from ._lib import LIB_PATH, LibraryMissing, load, load_attention  # noqa: F401
+from .logprobs import (  # noqa: F401
+    SV_MAX_TOP,
+    SV_MAX_TOP_VOCAB,
+    SV_TAIL_BUCKET,
+    SV_TAIL_RENORMALISE,
+    TokenLogprobs,
+    sv_distill,
+    sv_distill_backward,
+    sv_distill_loss,
+    sv_token_logprobs,
+    sv_token_logprobs_backward,
+)
+from ._lib import (  # noqa: F401
+    LIB_PATH,
+    LibraryMissing,
+    load,
+    load_attention,
+    load_logprobs,
+)

@@ -1,8 +1,9 @@
-"""Build libspecverify.so and libsvattention.so in-tree for sm_103a (GB300) with nvcc.
+"""Build libspecverify.so, libsvattention.so and libsvlogprobs.so in-tree for sm_103a (GB300)
+with nvcc.
 
 Each .cu under csrc/ compiles to its own object in parallel, then nvcc links
 them into a shared library beside this file. Only the names the public headers
-(include/spec_verify.h, include/sv_attention.h) declare are exported
+(include/spec_verify.h, include/sv_attention.h, include/sv_logprobs.h) declare are exported
 (-fvisibility=hidden plus explicit default visibility).
 """
 from __future__ import annotations
@@ -30,6 +31,10 @@ ATTENTION_LIB_PATH = os.path.join(PKG, "libsvattention.so")
 ATTENTION_CSRC = os.path.join(CSRC, "attention")
 ATTENTION_SOURCES = ["kv_cache.cu", "attn_no_pages.cu", "attn_few.cu", "attn_tiles.cu",
                      "attn_api.cu"]
+# Log probabilities and distillation (csrc/logprobs).
+LOGPROBS_LIB_PATH = os.path.join(PKG, "libsvlogprobs.so")
+LOGPROBS_CSRC = os.path.join(CSRC, "logprobs")
+LOGPROBS_SOURCES = ["logprobs.cu", "distill.cu", "rows_grad.cu", "lp_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -90,6 +95,18 @@ def build_attention(force: bool = False, verbose: bool = False, extra_flags=()) 
                     ATTENTION_LIB_PATH, verbose, extra_flags)
 
 
+def build_logprobs(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Compile (if needed) libsvlogprobs.so and return its path."""
+    files = [os.path.join(LOGPROBS_CSRC, f) for f in os.listdir(LOGPROBS_CSRC)]
+    files += [os.path.join(CSRC, "sv_device.cuh"), os.path.join(INCLUDE, "spec_verify.h"),
+              os.path.join(INCLUDE, "sv_logprobs.h")]
+    if not force and os.path.exists(LOGPROBS_LIB_PATH) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(LOGPROBS_LIB_PATH) for f in files):
+        return LOGPROBS_LIB_PATH
+    return _compile(LOGPROBS_CSRC, LOGPROBS_SOURCES, os.path.join(BUILD_DIR, "logprobs"),
+                    LOGPROBS_LIB_PATH, verbose, extra_flags)
+
+
 def _compile(csrc, sources, build_dir, lib_path, verbose, extra_flags) -> str:
     os.makedirs(build_dir, exist_ok=True)
     cc = nvcc()
@@ -125,3 +142,4 @@ if __name__ == "__main__":
     import sys
     print(build(force=True, verbose="-v" in sys.argv, debug="--debug" in sys.argv))
     print(build_attention(force=True, verbose="-v" in sys.argv))
+    print(build_logprobs(force=True, verbose="-v" in sys.argv))

@@ -1,4 +1,5 @@
-"""ctypes loaders for libspecverify.so and libsvattention.so (argument types only; no logic)."""
+"""ctypes loaders for libspecverify.so, libsvattention.so and libsvlogprobs.so (argument types
+only; no logic)."""
 from __future__ import annotations
 
 import ctypes
@@ -80,9 +81,23 @@ ATTENTION_SIGNATURES = {
                                         _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp, _i32, _vp]),
 }
 
+# The same for libsvlogprobs.so and include/sv_logprobs.h, passed the same way.
+LOGPROBS_PATH = os.path.join(_DIR, "libsvlogprobs.so")
+LOGPROBS_SIGNATURES = {
+    "sv_token_logprobs": (_i32, [ctypes.c_char_p, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _vp]),
+    "sv_token_logprobs_backward": (_i32, [ctypes.c_char_p, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                                          _vp]),
+    "sv_distill": (_i32, [ctypes.c_char_p, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _vp,
+                          _vp, _vp]),
+    "sv_distill_backward": (_i32, [ctypes.c_char_p, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64,
+                                   _vp]),
+}
+
 _lock = threading.Lock()
 _lib = None
 _attention = None
+_logprobs = None
 
 
 class LibraryMissing(RuntimeError):
@@ -127,3 +142,18 @@ def load_attention() -> ctypes.CDLL:
                         "(nvcc, sm_103a). The attention has no CPU fallback.")
                 _attention = _open(ATTENTION_PATH, ATTENTION_SIGNATURES)
     return _attention
+
+
+def load_logprobs() -> ctypes.CDLL:
+    """Load the in-tree library of the log probabilities and of distillation,
+    which has no fallback either."""
+    global _logprobs
+    if _logprobs is None:
+        with _lock:
+            if _logprobs is None:
+                if not os.path.exists(LOGPROBS_PATH):
+                    raise LibraryMissing(
+                        f"{LOGPROBS_PATH} is missing: build it with __graft_entry__.build() "
+                        "(nvcc, sm_103a). The log probabilities have no CPU fallback.")
+                _logprobs = _open(LOGPROBS_PATH, LOGPROBS_SIGNATURES)
+    return _logprobs

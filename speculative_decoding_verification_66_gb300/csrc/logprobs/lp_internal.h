@@ -1,0 +1,51 @@
+// lp_internal.h -- launchers of libsvlogprobs' translation units.
+#pragma once
+
+#include "lp_common.cuh"
+
+namespace svl {
+
+struct LogprobArgs {
+    Rows r;
+    const int32_t* tokens;
+    int32_t k;
+    float* logprobs;
+    float* entropy;
+    float* lse;
+    int32_t* rank;
+    int32_t* top_tokens;
+    float* top_logprobs;
+    float4* stats;
+    int32_t* status;
+};
+
+struct LogprobGradArgs {
+    Rows r;
+    const int32_t* tokens;
+    const float4* stats;
+    const float* a;  // gradients of log probability, entropy and lse
+    const float* b;
+    const float* c;
+    RowAt grad;
+};
+
+struct DistillArgs {
+    Rows r;
+    const int32_t* ids;
+    const float* logp;
+    int32_t k;
+    int32_t bucket;
+    const float* weights;
+    float* loss;
+    RowAt grad;       // base NULL: no gradient
+    float4* stats;
+    int32_t* status;
+};
+
+cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_distill(const DistillArgs& a, int dtype, cudaStream_t s);
+// (a.weights: the loss's gradient)
+cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t s);
+
+}  // namespace svl

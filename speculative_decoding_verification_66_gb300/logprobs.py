@@ -1,0 +1,332 @@
+"""Python binding of the log probabilities of given tokens and of distillation
+(include/sv_logprobs.h): the same names, torch tensors in, and autograd.
+
+Argument marshalling only, as in api.py. Logits are [V], [rows, V] or
+[B, rows, V], bfloat16, float16 or float32, with any strides but the last (a
+slice of positions or of a padded vocabulary is read where it lies). What is
+given or returned for each row has the logits' shape without V.
+
+``sv_token_logprobs`` and ``sv_distill_loss`` are differentiable in the logits.
+``sv_distill`` gives loss and gradient at once, in one pass over the logits, for
+training that calls ``logits.backward(grad)`` itself; the ``_backward`` calls are
+the gradients alone. Everything can be captured into a CUDA graph. (What torch
+asks of a captured backward pass holds: gradients that are accumulated into leaves
+need a warm-up on the capturing stream and no eager graph of the same leaves that
+is still alive; ``torch.autograd.grad`` and ``sv_distill`` need neither.)
+"""
+from __future__ import annotations
+
+import struct
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _lib
+from .api import SV_BF16, SV_F32, _check
+from .attention import SV_F16, _on
+
+SV_MAX_TOP, SV_MAX_TOP_VOCAB = 128, 1 << 20
+SV_TAIL_RENORMALISE, SV_TAIL_BUCKET = 0, 1
+
+_CODES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+_TAILS = {"renormalise": SV_TAIL_RENORMALISE, "bucket": SV_TAIL_BUCKET}
+# struct sv_logit_rows
+_ROWS = struct.Struct("@P5qif")
+
+
+class TokenLogprobs(NamedTuple):
+    """What ``sv_token_logprobs`` returns; None where it was not asked for."""
+    logprobs: Optional[torch.Tensor]
+    rank: Optional[torch.Tensor]
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_tokens: Optional[torch.Tensor]
+    top_logprobs: Optional[torch.Tensor]
+
+
+def _strides(x):
+    """(outer, inner, outer stride, inner stride) of the rows of x."""
+    shape, st = x.shape, x.stride()
+    if len(shape) == 3:
+        return shape[0], shape[1], st[0], st[1]
+    if len(shape) == 2:
+        return 1, shape[0], 0, st[0]
+    return 1, 1, 0, 0
+
+
+def _describe(logits, temperature):
+    """(packed struct sv_logit_rows, device, shape of the rows)."""
+    shape = logits.shape
+    if not logits.is_cuda or not 1 <= len(shape) <= 3:
+        raise ValueError("logits must be a CUDA tensor [V], [rows, V] or [B, rows, V]")
+    code = _CODES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    if shape[-1] < 1 or (shape[-1] > 1 and logits.stride(-1) != 1):
+        raise ValueError("logits must be contiguous along a vocabulary of at least one token")
+    packed = _ROWS.pack(logits.data_ptr(), *_strides(logits), shape[-1], code, temperature)
+    return packed, logits.device, shape[:-1]
+
+
+def _per_row(x, name, shape, dtype, dev, last=()):
+    """Address of a contiguous array for each row, or None."""
+    if x is None:
+        return None
+    if x.dtype != dtype or x.shape != (*shape, *last) or not x.is_contiguous() or x.device != dev:
+        kind = str(dtype).replace("torch.", "")
+        raise ValueError(f"{name} must be contiguous {kind} {list((*shape, *last))} on the logits' "
+                         "device")
+    return x.data_ptr()
+
+
+def _grad_like(logits):
+    """An uninitialised gradient. Its rows begin as far from 16-byte boundaries as the logits' do,
+    which lets both be moved by whole vectors; so rows that are padded stay padded."""
+    shape, V = logits.shape, logits.shape[-1]
+    vector = 16 // logits.element_size()
+    if V % vector == 0 or logits.is_contiguous() or \
+            any(s % vector for s, n in zip(logits.stride()[:-1], shape[:-1]) if n > 1):
+        return torch.empty(shape, dtype=logits.dtype, device=logits.device)
+    padded = torch.empty((*shape[:-1], V + -V % vector), dtype=logits.dtype, device=logits.device)
+    return padded[..., :V]
+
+
+def _span(x):
+    """Bytes [first, end) that the elements of x lie in."""
+    last = sum((n - 1) * s for n, s in zip(x.shape, x.stride()))
+    return x.data_ptr(), x.data_ptr() + (last + 1) * x.element_size()
+
+
+def _check_grad(grad, logits):
+    if grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != logits.device \
+            or (grad.shape[-1] > 1 and grad.stride(-1) != 1):
+        raise ValueError("grad must have the logits' shape, dtype and device, and be contiguous "
+                         "along the vocabulary")
+    if grad.numel() == 0:
+        return
+    a, b = _span(grad), _span(logits)
+    if a[0] < b[1] and b[0] < a[1] and (a[0] != b[0] or _strides(grad) != _strides(logits)):
+        raise ValueError("grad must be the logits themselves or lie apart from them")
+
+
+def _logprobs(described, logits, tokens, top_k, row_stats, row_status):
+    rows, dev, shape = described
+    i32, f32 = torch.int32, torch.float32
+    token_ptr = _per_row(tokens, "tokens", shape, i32, dev)
+    stats_ptr = _per_row(row_stats, "row_stats", shape, f32, dev, (4,))
+    status_ptr = _per_row(row_status, "row_status", shape, i32, dev)
+    if not 0 <= top_k <= min(SV_MAX_TOP, logits.shape[-1]):
+        raise ValueError(f"top_k must be from 0 to {SV_MAX_TOP} and at most the vocabulary")
+    entropy = torch.empty(shape, dtype=f32, device=dev)
+    lse = torch.empty_like(entropy)
+    logprobs = rank = top_tokens = top_logprobs = None
+    if tokens is not None:
+        logprobs = torch.empty_like(entropy)
+        rank = torch.empty(shape, dtype=i32, device=dev)
+    if top_k:
+        top_tokens = torch.empty((*shape, top_k), dtype=i32, device=dev)
+        top_logprobs = torch.empty((*shape, top_k), dtype=f32, device=dev)
+
+    def ptr(x):
+        return None if x is None else x.data_ptr()
+
+    _check(_lib.load_logprobs().sv_token_logprobs(
+        rows, token_ptr, top_k, ptr(logprobs), entropy.data_ptr(), lse.data_ptr(), ptr(rank),
+        ptr(top_tokens), ptr(top_logprobs), stats_ptr, status_ptr,
+        torch._C._cuda_getCurrentRawStream(dev.index)), "sv_token_logprobs")
+    return TokenLogprobs(logprobs, rank, entropy, lse, top_tokens, top_logprobs)
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, described, logits, tokens, temperature, top_k, row_stats, row_status):
+        if row_stats is None:
+            row_stats = torch.empty((*logits.shape[:-1], 4), dtype=torch.float32,
+                                    device=logits.device)
+        out = _logprobs(described, logits, tokens, top_k, row_stats, row_status)
+        ctx.save_for_backward(logits, tokens, row_stats)
+        ctx.temperature = temperature
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*(x for x in (out.rank, out.top_tokens, out.top_logprobs)
+                                      if x is not None))
+        return tuple(out)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_logprobs, _rank, grad_entropy, grad_lse, _tokens, _logprobs):
+        logits, tokens, row_stats = ctx.saved_tensors
+        grad = sv_token_logprobs_backward(
+            logits, row_stats, tokens=tokens, temperature=ctx.temperature,
+            **{name: None if g is None else g.contiguous() for name, g in
+               (("grad_logprobs", grad_logprobs), ("grad_entropy", grad_entropy),
+                ("grad_lse", grad_lse))})
+        return None, grad, None, None, None, None, None
+
+
+def sv_token_logprobs(logits, tokens=None, *, temperature: float = 1.0, top_k: int = 0,
+                      row_stats=None, row_status=None, stream=None) -> TokenLogprobs:
+    """Log probabilities of ``tokens`` (int32, one for each row) under softmax(logits / temperature),
+    their ranks (how many tokens are ahead; ties go to the lower index), the rows' entropies and
+    log-sum-exps, and with ``top_k`` the first tokens in order with their log probabilities.
+
+    A token of -1, as ``spec_verify`` leaves behind a sequence's last one, asks nothing of its row:
+    the row is not read and gets zeros, rank and top tokens -1, top log probabilities -inf. Without
+    ``tokens`` there are no log probabilities and ranks. ``row_status``: int32, receives SV_SEQ_BAD_TOKEN
+    and SV_SEQ_NONFINITE for rows whose results are NaN. ``row_stats``: float32 [..., 4], receives
+    what ``sv_token_logprobs_backward`` needs. Differentiable in the logits (logprobs, entropy and
+    lse). Asynchronous on ``stream`` (default: the current stream of the logits' device)."""
+    described = _describe(logits, temperature)
+
+    def call(_):
+        if logits.requires_grad and torch.is_grad_enabled():
+            return TokenLogprobs(*_TokenLogprobs.apply(described, logits, tokens, temperature, top_k,
+                                                       row_stats, row_status))
+        return _logprobs(described, logits, tokens, top_k, row_stats, row_status)
+
+    return _on(logits.device, stream, call, (logits, tokens, row_stats, row_status))
+
+
+def sv_token_logprobs_backward(logits, row_stats, *, tokens=None, grad_logprobs=None,
+                               grad_entropy=None, grad_lse=None, temperature: float = 1.0,
+                               grad=None, stream=None):
+    """The logits' gradient from those of ``sv_token_logprobs``' log probabilities, entropies and
+    log-sum-exps (float32, one for each row; None: zeros), with the ``row_stats`` that it filled.
+    ``grad`` may be the logits themselves, whose values are then gone."""
+    rows, dev, shape = _describe(logits, temperature)
+    f32 = torch.float32
+    ptrs = [_per_row(tokens, "tokens", shape, torch.int32, dev),
+            _per_row(row_stats, "row_stats", shape, f32, dev, (4,)),
+            _per_row(grad_logprobs, "grad_logprobs", shape, f32, dev),
+            _per_row(grad_entropy, "grad_entropy", shape, f32, dev),
+            _per_row(grad_lse, "grad_lse", shape, f32, dev)]
+    if grad is not None:
+        _check_grad(grad, logits)
+
+    def call(s):
+        g = _grad_like(logits) if grad is None else grad
+        _check(_lib.load_logprobs().sv_token_logprobs_backward(
+            rows, *ptrs, g.data_ptr(), *_strides(g)[2:], s), "sv_token_logprobs_backward")
+        return g
+
+    return _on(dev, stream, call, (logits, row_stats, tokens, grad_logprobs, grad_entropy, grad_lse,
+                                   grad))
+
+
+def _teacher(teacher_tokens, teacher_logprobs, shape, dev, tail):
+    """(address of tokens, of log probabilities, entries a row, code of tail)."""
+    if teacher_tokens.dim() != len(shape) + 1:
+        raise ValueError("teacher_tokens must be [..., k], beside logits [..., V]")
+    k = teacher_tokens.shape[-1]
+    if not 1 <= k <= SV_MAX_TOP:
+        raise ValueError(f"a teacher has from 1 to {SV_MAX_TOP} entries a row")
+    if tail not in _TAILS:
+        raise ValueError(f"tail must be one of {sorted(_TAILS)}, got {tail!r}")
+    return (_per_row(teacher_tokens, "teacher_tokens", shape, torch.int32, dev, (k,)),
+            _per_row(teacher_logprobs, "teacher_logprobs", shape, torch.float32, dev, (k,)), k,
+            _TAILS[tail])
+
+
+def _distill(described, teacher_tokens, teacher_logprobs, weights, tail, loss, grad, row_stats,
+             row_status):
+    """Calls sv_distill on the current stream; grad: a tensor or None."""
+    rows, dev, shape = described
+    teacher = _teacher(teacher_tokens, teacher_logprobs, shape, dev, tail)
+    f32 = torch.float32
+    weights_ptr = _per_row(weights, "weights", shape, f32, dev)
+    if loss is None:
+        loss = torch.empty(shape, dtype=f32, device=dev)
+    ptrs = (_per_row(loss, "loss", shape, f32, dev), None, 0, 0)
+    if grad is not None:
+        ptrs = (ptrs[0], grad.data_ptr(), *_strides(grad)[2:])
+    _check(_lib.load_logprobs().sv_distill(
+        rows, *teacher, weights_ptr, *ptrs,
+        _per_row(row_stats, "row_stats", shape, f32, dev, (4,)),
+        _per_row(row_status, "row_status", shape, torch.int32, dev),
+        torch._C._cuda_getCurrentRawStream(dev.index)), "sv_distill")
+    return loss
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, described, logits, teacher_tokens, teacher_logprobs, temperature, tail,
+                row_status):
+        row_stats = torch.empty((*logits.shape[:-1], 4), dtype=torch.float32, device=logits.device)
+        loss = _distill(described, teacher_tokens, teacher_logprobs, None, tail, None, None,
+                        row_stats, row_status)
+        ctx.save_for_backward(logits, teacher_tokens, teacher_logprobs, row_stats)
+        ctx.args = temperature, tail
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss):
+        logits, teacher_tokens, teacher_logprobs, row_stats = ctx.saved_tensors
+        temperature, tail = ctx.args
+        grad = sv_distill_backward(logits, teacher_tokens, teacher_logprobs, row_stats,
+                                   grad_loss.contiguous(), temperature=temperature, tail=tail)
+        return None, grad, None, None, None, None, None
+
+
+def sv_distill_loss(logits, teacher_tokens, teacher_logprobs, *, temperature: float = 1.0,
+                    tail: str = "renormalise", row_status=None, stream=None):
+    """Divergence (float32, one for each row) of a teacher from softmax(logits / temperature),
+    differentiable in the logits. The teacher's rows are k tokens (int32, -1 for none; a token given
+    twice has both probabilities) and their log probabilities (float32): ``sv_token_logprobs``'
+    ``top_tokens`` and ``top_logprobs``, at the same temperature. ``tail`` says what becomes of the
+    probability that they leave: "renormalise" scales the k to sum 1 (their logits over the
+    temperature do as well, then), "bucket" makes one outcome of all other tokens. Rows without a
+    teacher have loss 0 and are not read. ``row_status`` as in ``sv_token_logprobs``."""
+    described = _describe(logits, temperature)
+
+    def call(_):
+        if logits.requires_grad and torch.is_grad_enabled():
+            return _DistillLoss.apply(described, logits, teacher_tokens, teacher_logprobs,
+                                      temperature, tail, row_status)
+        return _distill(described, teacher_tokens, teacher_logprobs, None, tail, None, None, None,
+                        row_status)
+
+    return _on(logits.device, stream, call, (logits, teacher_tokens, teacher_logprobs, row_status))
+
+
+def sv_distill(logits, teacher_tokens, teacher_logprobs, *, weights=None, temperature: float = 1.0,
+               tail: str = "renormalise", loss=None, grad=None, row_stats=None, row_status=None,
+               stream=None):
+    """``sv_distill_loss`` and its gradient at once: (loss, grad), grad being the logits' gradient of
+    the sum of ``weights`` (float32, one for each row; default 1) times the losses. Rows are read
+    once. Continue with ``logits.backward(grad)``, or with the head's products. ``grad`` may be the
+    logits themselves, whose values are then gone. Arguments otherwise as in
+    ``sv_distill_loss``; ``row_stats`` (float32 [..., 4]) receives what ``sv_distill_backward``
+    needs."""
+    described = _describe(logits, temperature)
+    if grad is not None:
+        _check_grad(grad, logits)
+
+    def call(_):
+        g = _grad_like(logits) if grad is None else grad
+        return _distill(described, teacher_tokens, teacher_logprobs, weights, tail, loss, g,
+                        row_stats, row_status), g
+
+    return _on(logits.device, stream, call, (logits, teacher_tokens, teacher_logprobs, weights, loss,
+                                             grad, row_stats, row_status))
+
+
+def sv_distill_backward(logits, teacher_tokens, teacher_logprobs, row_stats, grad_loss, *,
+                        temperature: float = 1.0, tail: str = "renormalise", grad=None,
+                        stream=None):
+    """The logits' gradient from that of ``sv_distill``'s losses (float32, one for each row), with the
+    ``row_stats`` that it filled for the same logits and teacher."""
+    rows, dev, shape = _describe(logits, temperature)
+    teacher = _teacher(teacher_tokens, teacher_logprobs, shape, dev, tail)
+    ptrs = (_per_row(row_stats, "row_stats", shape, torch.float32, dev, (4,)),
+            _per_row(grad_loss, "grad_loss", shape, torch.float32, dev))
+    if grad is not None:
+        _check_grad(grad, logits)
+
+    def call(s):
+        g = _grad_like(logits) if grad is None else grad
+        _check(_lib.load_logprobs().sv_distill_backward(
+            rows, *teacher, *ptrs, g.data_ptr(), *_strides(g)[2:], s), "sv_distill_backward")
+        return g
+
+    return _on(dev, stream, call, (logits, teacher_tokens, teacher_logprobs, row_stats, grad_loss,
+                                   grad))
