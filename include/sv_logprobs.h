@@ -52,6 +52,9 @@ extern "C" {
 /* Largest vocabulary whose top alternatives are given. */
 #define SV_MAX_TOP_VOCAB (1 << 20)
 
+/* Floats that the forward calls keep of a row for the backward ones. */
+#define SV_ROW_STATS 8
+
 /* What is made of the teacher's probability that its entries leave:
  * SV_TAIL_RENORMALISE  the entries are scaled to sum 1 (their log
  *                      probabilities may be off by a constant, as logits are).
@@ -94,7 +97,7 @@ typedef struct sv_logit_rows {
  *   entropy, lse  device float [rows].
  *   top_tokens, top_logprobs  device int32 and float [rows][top_k]: the first
  *                 top_k tokens in order, and their log p. Both or neither.
- *   row_stats     device float [rows][4], 16-byte aligned: what the backward call
+ *   row_stats     device float [rows][SV_ROW_STATS], 16-byte aligned: what the backward call
  *                 needs of this one.
  * Each output may be NULL. One launch.
  */
@@ -138,7 +141,7 @@ int sv_token_logprobs_backward(const sv_logit_rows* rows, const int32_t* tokens,
  *               gradients (not of their losses).
  *   loss        device float [rows], or NULL.
  *   grad        as in sv_token_logprobs_backward, or NULL.
- *   row_stats   device float [rows][4], 16-byte aligned, or NULL.
+ *   row_stats   device float [rows][SV_ROW_STATS], 16-byte aligned, or NULL.
  * One launch.
  */
 int sv_distill(const sv_logit_rows* rows, const int32_t* teacher_tokens,

@@ -69,6 +69,7 @@ from .attention import (  # noqa: F401
 from .logprobs import (  # noqa: F401
     SV_MAX_TOP,
     SV_MAX_TOP_VOCAB,
+    SV_ROW_STATS,
     SV_TAIL_BUCKET,
     SV_TAIL_RENORMALISE,
     TokenLogprobs,

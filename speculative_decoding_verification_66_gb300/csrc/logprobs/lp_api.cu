@@ -5,6 +5,8 @@
 
 #define SV_EXPORT extern "C" __attribute__((visibility("default")))
 
+static_assert(sizeof(svl::RowStats) == SV_ROW_STATS * sizeof(float), "as the header says");
+
 namespace {
 
 constexpr int64_t kMax31 = int64_t(1) << 31;
@@ -109,7 +111,7 @@ SV_EXPORT int sv_token_logprobs(const sv_logit_rows* rows, const int32_t* tokens
     a.rank = rank;
     a.top_tokens = top_tokens;
     a.top_logprobs = top_logprobs;
-    a.stats = reinterpret_cast<float4*>(row_stats);
+    a.stats = reinterpret_cast<svl::RowStats*>(row_stats);
     a.status = row_status;
     return done(svl::launch_logprobs(a, rows->dtype, static_cast<cudaStream_t>(stream)));
 }
@@ -132,7 +134,7 @@ SV_EXPORT int sv_token_logprobs_backward(const sv_logit_rows* rows, const int32_
         return SV_ERR_ALIGN;
     if (a.r.rows == 0) return SV_OK;
     a.tokens = tokens;
-    a.stats = reinterpret_cast<const float4*>(row_stats);
+    a.stats = reinterpret_cast<const svl::RowStats*>(row_stats);
     a.a = grad_logprobs;
     a.b = grad_entropy;
     a.c = grad_lse;
@@ -161,7 +163,7 @@ SV_EXPORT int sv_distill(const sv_logit_rows* rows, const int32_t* teacher_token
     a.bucket = tail == SV_TAIL_BUCKET;
     a.weights = weights;
     a.loss = loss;
-    a.stats = reinterpret_cast<float4*>(row_stats);
+    a.stats = reinterpret_cast<svl::RowStats*>(row_stats);
     a.status = row_status;
     return done(svl::launch_distill(a, rows->dtype, static_cast<cudaStream_t>(stream)));
 }
@@ -185,6 +187,6 @@ SV_EXPORT int sv_distill_backward(const sv_logit_rows* rows, const int32_t* teac
     a.k = static_cast<int32_t>(k);
     a.bucket = tail == SV_TAIL_BUCKET;
     a.weights = grad_loss;
-    a.stats = reinterpret_cast<float4*>(const_cast<float*>(row_stats));
+    a.stats = reinterpret_cast<svl::RowStats*>(const_cast<float*>(row_stats));
     return done(svl::launch_distill_grad(a, rows->dtype, static_cast<cudaStream_t>(stream)));
 }

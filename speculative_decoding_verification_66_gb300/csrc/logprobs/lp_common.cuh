@@ -64,9 +64,6 @@ __device__ __forceinline__ void store_one(uint8_t* row, int64_t v, float g)
         reinterpret_cast<__half*>(row)[v] = __float2half_rn(g);
 }
 
-// What the backward pass is told of a row, in its four floats' last place.
-enum RowKind { kRowGood = 0, kRowSkipped = 1, kRowBad = 2 };
-
 // Whole numbers in the floats' order (one zero; no NaN).
 __device__ __forceinline__ uint32_t ordered(float x)
 {

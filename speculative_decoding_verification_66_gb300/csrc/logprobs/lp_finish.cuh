@@ -10,6 +10,7 @@
 #pragma once
 
 #include "lp_internal.h"
+#include "lp_vec.cuh"
 
 namespace svl {
 
@@ -28,7 +29,7 @@ __device__ __forceinline__ void finish_plain(const LogprobArgs& a, int32_t row, 
     if (a.entropy != nullptr) a.entropy[row] = f;
     if (a.lse != nullptr) a.lse[row] = f;
     if (a.rank != nullptr) a.rank[row] = -1;
-    if (a.stats != nullptr) a.stats[row] = make_float4(0.f, 0.f, 0.f, static_cast<float>(kind));
+    if (a.stats != nullptr) a.stats[row].kind = kind;
     if (a.status != nullptr) a.status[row] = status;
 }
 
@@ -41,8 +42,7 @@ __device__ __forceinline__ void finish_plain_top(const LogprobArgs& a, int32_t r
     }
 }
 
-// Results of a good row (x_t, rank: the token's, where there is one). For the backward
-// pass: M, 1 / S and the entropy less log S.
+// Results of a good row (x_t, rank: the token's, where there is one).
 __device__ __forceinline__ void finish_row(const LogprobArgs& a, int32_t row, float M, float S,
                                            float E, float x_t, int rank, double log_s)
 {
@@ -54,168 +54,230 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, int32_t row, fl
     if (a.lse != nullptr)
         a.lse[row] = static_cast<float>(static_cast<double>(M) * a.r.inv_t + log_s);
     if (a.stats != nullptr)
-        a.stats[row] = make_float4(M, 1.0f / S, static_cast<float>(-mean), kRowGood);
+        a.stats[row] = {M, 1.0f / S, static_cast<float>(-mean), 0.f, 0.f, 0.f, 0.f, kRowGood};
     if (a.status != nullptr) a.status[row] = 0;
 }
 
 // A row's teacher in shared memory: the tokens that have entries, each once.
+constexpr int kChunks = SV_MAX_TOP / 32;
 struct Teacher {
     int32_t id[SV_MAX_TOP];      // -1 where there is none, or where it came before
     float x[SV_MAX_TOP];         // the student's logit
     float p[SV_MAX_TOP];         // probability (finish_distill renormalises)
     float logp[SV_MAX_TOP];      // as given
-    double part[4], part2[4];    // sums of four warps
-    float top[4];
-    int count[4];
+    double part[kChunks], part2[kChunks];  // sums of 32 entries
+    float top[kChunks];
+    int count[kChunks];
     double mass;                 // the entries' sum, before they are renormalised
+    float shift;                 // what was taken off their log probabilities
     int distinct;
     int status;
-    float listed, others;        // what finish_distill leaves: factors of 2^((x - M) c)
+    // What finish_distill leaves: the gradient is, times the row's weight over T,
+    //   scale 2^((x - M) c)                for tokens without entries
+    //   listed 2^((x - listed_M) c) - p    for tokens with
+    float M, scale, listed_M, listed;
 };
 
-// Fills in all but x; called by all threads of a block of at least 128. Ends with a
-// barrier.
-__device__ __forceinline__ void load_teacher(Teacher& t, const DistillArgs& a, int32_t row)
+// Sum of the 32 lanes of a warp.
+template <typename N>
+__device__ __forceinline__ N warp_sum(N x)
 {
-    const int j = threadIdx.x;
-    if (j == 0) t.status = 0;
-    __syncthreads();
-    const int warp = j >> 5;
-    int32_t id = -1;
-    float lp = -inf();
-    if (j < SV_MAX_TOP) {
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+    return x;
+}
+
+// Sum over the chunks in use, in one order.
+template <typename N>
+__device__ __forceinline__ N chunk_sum(const N* part, int chunks)
+{
+    N s = part[0];
+    for (int i = 1; i < chunks; ++i) s += part[i];
+    return s;
+}
+
+// Takes the row's entries and says whether there is anything to do with it (an entry, or a
+// fault); called by all threads, with a barrier inside and at its end.
+__device__ __forceinline__ bool read_teacher(Teacher& t, const DistillArgs& a, int32_t row)
+{
+    int any = 0;
+    for (int j = threadIdx.x; j < SV_MAX_TOP; j += blockDim.x) {
+        int32_t id = -1;
+        float lp = -inf();
         if (j < a.k) {
             const int64_t at = static_cast<int64_t>(row) * a.k + j;
             id = a.ids[at];
             lp = a.logp[at];
-            int bad = 0;
-            if (id < -1 || id >= a.r.V) bad = SV_SEQ_BAD_TOKEN;
-            if (lp != lp || lp == inf()) bad |= SV_SEQ_NONFINITE;
-            if (bad != 0) {
-                atomicOr(&t.status, bad);
-                id = -1;
-            }
-            if (id < 0) lp = -inf();
         }
+        any |= id != -1 || lp != lp || lp == inf();
         t.id[j] = id;
         t.logp[j] = lp;
-        float top = lp;
-        for (int off = 16; off > 0; off >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-        if ((j & 31) == 0) t.top[warp] = top;
+    }
+    if (threadIdx.x == 0) t.status = 0;
+    return __syncthreads_or(any) != 0;
+}
+
+// The rest of the teacher but the student's logits, after read_teacher. Ends with a barrier.
+__device__ __forceinline__ void make_teacher(Teacher& t, const DistillArgs& a)
+{
+    const int end = (a.k + 31) & ~31, chunks = end >> 5;
+    for (int j = threadIdx.x; j < end; j += blockDim.x) {
+        int32_t id = t.id[j];
+        float lp = t.logp[j];
+        int bad = 0;
+        if (id < -1 || id >= a.r.V) bad = SV_SEQ_BAD_TOKEN;
+        if (lp != lp || lp == inf()) bad |= SV_SEQ_NONFINITE;
+        if (bad != 0) {
+            atomicOr(&t.status, bad);
+            id = -1;
+        }
+        if (id < 0) lp = -inf();
+        t.id[j] = id;
+        t.logp[j] = lp;
+        const float top = warp_max(lp);
+        if ((j & 31) == 0) t.top[j >> 5] = top;
     }
     __syncthreads();
-    if (j < SV_MAX_TOP) {
-        // Renormalised probabilities are taken from the largest one, so that none
-        // overflows.
-        float shift = 0.f;
-        if (!a.bucket) {
-            shift = fmaxf(fmaxf(t.top[0], t.top[1]), fmaxf(t.top[2], t.top[3]));
-            if (shift == -inf()) shift = 0.f;
-        }
+    // Renormalised probabilities are taken from the largest one, so that none overflows.
+    float shift = 0.f;
+    if (!a.bucket) {
+        shift = t.top[0];
+        for (int i = 1; i < chunks; ++i) shift = fmaxf(shift, t.top[i]);
+        if (shift == -inf()) shift = 0.f;
+    }
+    uint32_t again = 0;  // (entries of this thread whose token came before)
+    int turn = 0;
+    for (int j = threadIdx.x; j < end; j += blockDim.x, ++turn) {
+        const int32_t id = t.id[j];
         bool first = id >= 0;
         float p = 0.f;
-        for (int i = 0; i < a.k; ++i)
-            if (t.id[i] == id) {
-                if (i < j) first = false;
-                p += expf(t.logp[i] - shift);
-            }
-        if (!first) p = 0.f;
-        double sum = p;
-        int n = first;
-        for (int off = 16; off > 0; off >>= 1) {
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-            n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
+        if (id >= 0)
+            for (int i = 0; i < a.k; ++i)
+                if (t.id[i] == id) {
+                    if (i < j) first = false;
+                    p += expf(t.logp[i] - shift);
+                }
+        if (!first) {
+            p = 0.f;
+            again |= 1u << turn;
         }
+        const double sum = warp_sum(static_cast<double>(p));
+        const int n = warp_sum(first ? 1 : 0);
         if ((j & 31) == 0) {
-            t.part[warp] = sum;
-            t.count[warp] = n;
+            t.part[j >> 5] = sum;
+            t.count[j >> 5] = n;
         }
         t.p[j] = p;
-        id = first ? id : -1;
     }
     __syncthreads();
-    if (j < SV_MAX_TOP) t.id[j] = id;
-    if (j == 0) {
-        t.mass = (t.part[0] + t.part[1]) + (t.part[2] + t.part[3]);
-        t.distinct = (t.count[0] + t.count[1]) + (t.count[2] + t.count[3]);
+    turn = 0;
+    for (int j = threadIdx.x; j < end; j += blockDim.x, ++turn)
+        if (again >> turn & 1) t.id[j] = -1;
+    if (threadIdx.x == 0) {
+        t.shift = shift;
+        t.mass = chunk_sum(t.part, chunks);
+        t.distinct = chunk_sum(t.count, chunks);
         if (!a.bucket && t.distinct > 0 && !(t.mass > 0.0)) t.status |= SV_SEQ_NONFINITE;
     }
     __syncthreads();
 }
 
-// Loss and gradient factors of a good row, from M, the largest logit, and the sum S_o of
-// 2^((x - M) c) over the tokens without entries; the entries' logits are in t.x. The
-// gradient is then, times the row's weight over T,
-//   listed 2^((x - M) c) - p   for tokens with entries,   others 2^((x - M) c)   for others:
-// with S the sum over all tokens and m the entries' probabilities' sum,
-//   listed = 1 / S, others = 1 / S                          renormalised
+// Loss and gradient factors of a row, from the largest logit M_o and the sum S_o of
+// 2^((x - M_o) c) over the tokens without entries (-inf and 0: none, or all of them are
+// -inf); the entries' logits are in t.x. With M the largest of all, S the sum over all of
+// 2^((x - M) c), q_e the entries' share of it and m the sum of their probabilities:
+//   listed = 1 / S, scale = 2^((M_o - M) c) / S             renormalised
 //   listed = max(m, 1) / S                                  bucket
-//   others = (1 - P_o / q_o) / S = (m - q_e) / S_o          .. where m <= 1 (q_e = 1 - q_o)
-// Called by all threads; ends with a barrier.
-__device__ __forceinline__ void finish_distill(Teacher& t, const DistillArgs& a, int32_t row,
-                                               float M, float S_o)
+//   scale  = (1 - P_o / q_o) 2^((M_o - M) c) / S = (m - q_e) / S_o     .. where m <= 1
+// so that the others' gradient keeps its digits however small their share is. Called by
+// all threads; `lead` writes the results. Returns the row's kind; ends with a barrier.
+__device__ __forceinline__ int finish_distill(Teacher& t, const DistillArgs& a, int32_t row,
+                                              float M_o, float S_o, bool lead)
 {
-    const int j = threadIdx.x, warp = j >> 5;
-    float e = 0.f;
-    if (j < SV_MAX_TOP) {
-        if (t.id[j] >= 0) e = ex2((t.x[j] - M) * a.r.c);
-        double sum = e;
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-        if ((j & 31) == 0) t.part[warp] = sum;
+    const int end = (a.k + 31) & ~31, chunks = end >> 5;
+    const float c = a.r.c;
+    for (int j = threadIdx.x; j < end; j += blockDim.x) {
+        const float top = warp_max(t.id[j] >= 0 ? t.x[j] : -inf());
+        if ((j & 31) == 0) t.top[j >> 5] = top;
     }
     __syncthreads();
-    const double S_e = (t.part[0] + t.part[1]) + (t.part[2] + t.part[3]);
-    const double S = S_e + S_o;
-    const bool has_others = t.distinct < a.r.V;
-    if (j < SV_MAX_TOP) {
-        const double log_s = log_wide(static_cast<float>(S));
+    float M = M_o;
+    for (int i = 0; i < chunks; ++i) M = fmax_nan(M, t.top[i]);
+    const bool good = fabsf(M) < inf() && t.status == 0;
+    if (!good) {
+        if (lead && threadIdx.x == 0) {
+            const int status = t.status | (fabsf(M) < inf() ? 0 : SV_SEQ_NONFINITE);
+            if (a.loss != nullptr) a.loss[row] = nan();
+            if (a.stats != nullptr) a.stats[row].kind = kRowBad;
+            if (a.status != nullptr) a.status[row] = status;
+        }
+        return kRowBad;
+    }
+    for (int j = threadIdx.x; j < end; j += blockDim.x) {
+        const float e = t.id[j] >= 0 ? ex2((t.x[j] - M) * c) : 0.f;
+        const double sum = warp_sum(static_cast<double>(e));
+        if ((j & 31) == 0) t.part[j >> 5] = sum;
+    }
+    __syncthreads();
+    const float fall = S_o > 0.f ? ex2((M_o - M) * c) : 0.f;
+    const double S_e = chunk_sum(t.part, chunks);
+    const double S = S_e + static_cast<double>(S_o) * fall;
+    const double log_s = log_wide(static_cast<float>(S));
+    for (int j = threadIdx.x; j < end; j += blockDim.x) {
         double term = 0.0;
         const float p = t.p[j];
         if (t.id[j] >= 0 && p > 0.f) {
             const double log_m = a.bucket ? 0.0 : log_wide(static_cast<float>(t.mass));
             const double P = a.bucket ? p : p / t.mass;
-            term = P * (log_wide(p) - log_m - log_prob(t.x[j], M, a.r.c, log_s));
+            term = P * (log_wide(p) - log_m - log_prob(t.x[j], M, c, log_s));
             t.p[j] = static_cast<float>(P);
         }
-        for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, off);
-        if ((j & 31) == 0) t.part2[warp] = term;
+        term = warp_sum(term);
+        if ((j & 31) == 0) t.part2[j >> 5] = term;
     }
     __syncthreads();
-    if (j == 0) {
-        double loss = (t.part2[0] + t.part2[1]) + (t.part2[2] + t.part2[3]);
-        const float m = static_cast<float>(t.mass);
-        const float q_e = static_cast<float>(S_e / S);
-        t.listed = t.others = static_cast<float>(1.0 / S);
+    if (threadIdx.x == 0) {
+        double loss = chunk_sum(t.part2, chunks);
+        const double q_e = S_e / S;
+        t.M = S_o > 0.f ? M_o : 0.f;  // (nothing finite: any finite number)
+        t.listed_M = M;
+        t.listed = static_cast<float>(1.0 / S);
+        t.scale = t.listed * fall;
         if (a.bucket) {
-            const double P_o = has_others ? fmax(0.0, 1.0 - t.mass) : 0.0;
+            const double P_o = t.distinct < a.r.V ? fmax(0.0, 1.0 - t.mass) : 0.0;
             if (P_o > 0.0) {
+                const float m = static_cast<float>(t.mass);
                 const double log_P = m < 0.5f ? log1pf(-m) : logf(static_cast<float>(P_o));
-                const double log_q = q_e < 0.5f ? static_cast<double>(log1pf(-q_e))
-                                                : log_wide(S_o) - log_wide(static_cast<float>(S));
+                const double log_q = q_e < 0.5 ? static_cast<double>(log1pf(-static_cast<float>(q_e)))
+                                               : log_prob(M_o, M, c, log_s) + log_wide(S_o);
                 loss += P_o * (log_P - log_q);
             }
-            const double total = t.mass + P_o;
-            t.listed = static_cast<float>(total / S);
-            // (no token left, or all of probability 0: their gradient is 0)
-            t.others = !(S_o > 0.f)   ? 0.f
-                       : t.mass <= 1.0 ? static_cast<float>((t.mass - S_e / S) / S_o)
-                                       : t.listed;
+            t.listed = static_cast<float>((t.mass + P_o) / S);
+            // (no other token, or all of probability 0: their gradient is 0)
+            t.scale = !(S_o > 0.f)    ? 0.f
+                      : t.mass <= 1.0 ? static_cast<float>((t.mass - q_e) / S_o)
+                                      : t.listed * fall;
         }
-        if (a.loss != nullptr) a.loss[row] = static_cast<float>(loss);
-        if (a.stats != nullptr) a.stats[row] = make_float4(M, t.listed, t.others, kRowGood);
-        if (a.status != nullptr) a.status[row] = 0;
+        if (lead) {
+            if (a.loss != nullptr) a.loss[row] = static_cast<float>(loss);
+            if (a.stats != nullptr)
+                a.stats[row] = {t.M,     t.scale,
+                                0.f,     t.listed_M,
+                                t.listed, t.shift,
+                                a.bucket ? 1.f : static_cast<float>(1.0 / t.mass),
+                                kRowGood};
+            if (a.status != nullptr) a.status[row] = 0;
+        }
     }
     __syncthreads();
+    return kRowGood;
 }
 
-// The same for a row without entries, or a bad one.
-__device__ __forceinline__ void finish_distill_plain(const DistillArgs& a, int32_t row, int kind,
-                                                     int status)
+// The same for a row without entries.
+__device__ __forceinline__ void finish_distill_skipped(const DistillArgs& a, int32_t row)
 {
-    if (a.loss != nullptr) a.loss[row] = kind == kRowBad ? nan() : 0.f;
-    if (a.stats != nullptr) a.stats[row] = make_float4(0.f, 0.f, 0.f, static_cast<float>(kind));
-    if (a.status != nullptr) a.status[row] = status;
+    if (a.loss != nullptr) a.loss[row] = 0.f;
+    if (a.stats != nullptr) a.stats[row].kind = kRowSkipped;
+    if (a.status != nullptr) a.status[row] = 0;
 }
 
 }  // namespace svl

@@ -5,6 +5,18 @@
 
 namespace svl {
 
+// What the backward pass is told of a row (SV_ROW_STATS floats).
+enum RowKind { kRowGood = 0, kRowSkipped = 1, kRowBad = 2 };
+struct __align__(16) RowStats {
+    float M;           // the largest logit; distillation: of the tokens without entries
+    float scale;       // factor of 2^((x - M) c)
+    float mean;        // log probabilities: entropy less log S
+    float listed_M;    // distillation: the largest logit of all,
+    float listed;      //   the factor of 2^((x - listed_M) c) for tokens with entries,
+    float shift, inv;  //   and their probabilities: exp(log probability - shift) inv
+    float kind;
+};
+
 struct LogprobArgs {
     Rows r;
     const int32_t* tokens;
@@ -15,14 +27,14 @@ struct LogprobArgs {
     int32_t* rank;
     int32_t* top_tokens;
     float* top_logprobs;
-    float4* stats;
+    RowStats* stats;
     int32_t* status;
 };
 
 struct LogprobGradArgs {
     Rows r;
     const int32_t* tokens;
-    const float4* stats;
+    const RowStats* stats;
     const float* a;  // gradients of log probability, entropy and lse
     const float* b;
     const float* c;
@@ -38,7 +50,7 @@ struct DistillArgs {
     const float* weights;
     float* loss;
     RowAt grad;       // base NULL: no gradient
-    float4* stats;
+    RowStats* stats;
     int32_t* status;
 };
 

@@ -25,7 +25,7 @@ from . import _lib
 from .api import SV_BF16, SV_F32, _check
 from .attention import SV_F16, _on
 
-SV_MAX_TOP, SV_MAX_TOP_VOCAB = 128, 1 << 20
+SV_MAX_TOP, SV_MAX_TOP_VOCAB, SV_ROW_STATS = 128, 1 << 20, 8
 SV_TAIL_RENORMALISE, SV_TAIL_BUCKET = 0, 1
 
 _CODES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}
@@ -113,7 +113,7 @@ def _logprobs(described, logits, tokens, top_k, row_stats, row_status):
     rows, dev, shape = described
     i32, f32 = torch.int32, torch.float32
     token_ptr = _per_row(tokens, "tokens", shape, i32, dev)
-    stats_ptr = _per_row(row_stats, "row_stats", shape, f32, dev, (4,))
+    stats_ptr = _per_row(row_stats, "row_stats", shape, f32, dev, (SV_ROW_STATS,))
     status_ptr = _per_row(row_status, "row_status", shape, i32, dev)
     if not 0 <= top_k <= min(SV_MAX_TOP, logits.shape[-1]):
         raise ValueError(f"top_k must be from 0 to {SV_MAX_TOP} and at most the vocabulary")
@@ -141,7 +141,7 @@ class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, described, logits, tokens, temperature, top_k, row_stats, row_status):
         if row_stats is None:
-            row_stats = torch.empty((*logits.shape[:-1], 4), dtype=torch.float32,
+            row_stats = torch.empty((*logits.shape[:-1], SV_ROW_STATS), dtype=torch.float32,
                                     device=logits.device)
         out = _logprobs(described, logits, tokens, top_k, row_stats, row_status)
         ctx.save_for_backward(logits, tokens, row_stats)
@@ -172,7 +172,7 @@ def sv_token_logprobs(logits, tokens=None, *, temperature: float = 1.0, top_k: i
     A token of -1, as ``spec_verify`` leaves behind a sequence's last one, asks nothing of its row:
     the row is not read and gets zeros, rank and top tokens -1, top log probabilities -inf. Without
     ``tokens`` there are no log probabilities and ranks. ``row_status``: int32, receives SV_SEQ_BAD_TOKEN
-    and SV_SEQ_NONFINITE for rows whose results are NaN. ``row_stats``: float32 [..., 4], receives
+    and SV_SEQ_NONFINITE for rows whose results are NaN. ``row_stats``: float32 [..., SV_ROW_STATS], receives
     what ``sv_token_logprobs_backward`` needs. Differentiable in the logits (logprobs, entropy and
     lse). Asynchronous on ``stream`` (default: the current stream of the logits' device)."""
     described = _describe(logits, temperature)
@@ -195,7 +195,7 @@ def sv_token_logprobs_backward(logits, row_stats, *, tokens=None, grad_logprobs=
     rows, dev, shape = _describe(logits, temperature)
     f32 = torch.float32
     ptrs = [_per_row(tokens, "tokens", shape, torch.int32, dev),
-            _per_row(row_stats, "row_stats", shape, f32, dev, (4,)),
+            _per_row(row_stats, "row_stats", shape, f32, dev, (SV_ROW_STATS,)),
             _per_row(grad_logprobs, "grad_logprobs", shape, f32, dev),
             _per_row(grad_entropy, "grad_entropy", shape, f32, dev),
             _per_row(grad_lse, "grad_lse", shape, f32, dev)]
@@ -240,7 +240,7 @@ def _distill(described, teacher_tokens, teacher_logprobs, weights, tail, loss, g
         ptrs = (ptrs[0], grad.data_ptr(), *_strides(grad)[2:])
     _check(_lib.load_logprobs().sv_distill(
         rows, *teacher, weights_ptr, *ptrs,
-        _per_row(row_stats, "row_stats", shape, f32, dev, (4,)),
+        _per_row(row_stats, "row_stats", shape, f32, dev, (SV_ROW_STATS,)),
         _per_row(row_status, "row_status", shape, torch.int32, dev),
         torch._C._cuda_getCurrentRawStream(dev.index)), "sv_distill")
     return loss
@@ -250,7 +250,7 @@ class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, described, logits, teacher_tokens, teacher_logprobs, temperature, tail,
                 row_status):
-        row_stats = torch.empty((*logits.shape[:-1], 4), dtype=torch.float32, device=logits.device)
+        row_stats = torch.empty((*logits.shape[:-1], SV_ROW_STATS), dtype=torch.float32, device=logits.device)
         loss = _distill(described, teacher_tokens, teacher_logprobs, None, tail, None, None,
                         row_stats, row_status)
         ctx.save_for_backward(logits, teacher_tokens, teacher_logprobs, row_stats)
@@ -295,7 +295,7 @@ def sv_distill(logits, teacher_tokens, teacher_logprobs, *, weights=None, temper
     the sum of ``weights`` (float32, one for each row; default 1) times the losses. Rows are read
     once. Continue with ``logits.backward(grad)``, or with the head's products. ``grad`` may be the
     logits themselves, whose values are then gone. Arguments otherwise as in
-    ``sv_distill_loss``; ``row_stats`` (float32 [..., 4]) receives what ``sv_distill_backward``
+    ``sv_distill_loss``; ``row_stats`` (float32 [..., SV_ROW_STATS]) receives what ``sv_distill_backward``
     needs."""
     described = _describe(logits, temperature)
     if grad is not None:
@@ -317,7 +317,7 @@ def sv_distill_backward(logits, teacher_tokens, teacher_logprobs, row_stats, gra
     ``row_stats`` that it filled for the same logits and teacher."""
     rows, dev, shape = _describe(logits, temperature)
     teacher = _teacher(teacher_tokens, teacher_logprobs, shape, dev, tail)
-    ptrs = (_per_row(row_stats, "row_stats", shape, torch.float32, dev, (4,)),
+    ptrs = (_per_row(row_stats, "row_stats", shape, torch.float32, dev, (SV_ROW_STATS,)),
             _per_row(grad_loss, "grad_loss", shape, torch.float32, dev))
     if grad is not None:
         _check_grad(grad, logits)

@@ -209,7 +209,7 @@ def test_gradients_of_any_layout(dtype, V):
         loss, g = sv.sv_distill(x, ids, lp, grad=grad)
         assert g is grad
         check(x, ids, lp, 1.0, "renormalise", loss, g)
-        stats = torch.empty(4, 3, 4, device="cuda")
+        stats = torch.empty(4, 3, sv.SV_ROW_STATS, device="cuda")
         w = torch.rand(4, 3, device="cuda")
         sv.sv_distill(x, ids, lp, row_stats=stats)
         g = sv.sv_distill_backward(x, ids, lp, stats, w, grad=grad)

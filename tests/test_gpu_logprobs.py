@@ -265,7 +265,7 @@ def test_the_same_gradient_twice_and_second_derivatives_refused():
 def test_backward_into_the_logits_themselves():
     x = draw((9, 3001), "bf16")
     tokens = draw_tokens((9,), 3001)
-    stats = torch.empty(9, 4, device="cuda")
+    stats = torch.empty(9, sv.SV_ROW_STATS, device="cuda")
     sv.sv_token_logprobs(x, tokens, row_stats=stats)
     a = torch.randn(9, device="cuda")
     want = sv.sv_token_logprobs_backward(x, stats, tokens=tokens, grad_logprobs=a)
@@ -347,7 +347,7 @@ def test_refusals():
     for y in (x.t(), x.double(), x.int(), x[None, None], x[:, :0], x.cpu()):
         with pytest.raises((ValueError, TypeError)):
             sv.sv_token_logprobs(y)
-    stats = torch.zeros(4, 4, device="cuda")
+    stats = torch.zeros(4, sv.SV_ROW_STATS, device="cuda")
     with pytest.raises(ValueError):
         sv.sv_token_logprobs_backward(x, stats, grad=x[:, 1:])
     big = draw((5, 100), "bf16")
