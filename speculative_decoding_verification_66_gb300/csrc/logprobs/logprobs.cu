@@ -1,10 +1,7 @@
 // logprobs.cu -- log probabilities of given tokens, entropy and top alternatives,
 // in one read of the row.
 //
-// Sums. A thread adds 2^t and 2^t t with t = (x - r) c against a reference r that is one
-// of its logits, and moves r only when a logit passes it by 2^16: hardly ever, and then with
-// one rounding. Differences are taken before they are scaled, so logits far from zero lose
-// nothing.
+// Sums: lp_stream.cuh.
 //
 // Rank. A vector's largest element is known for the sums' sake; its elements are only
 // compared with the given token's where that one reaches it, which is rare for tokens that
@@ -23,13 +20,13 @@
 //
 // Bound by memory for many rows (some six to seven instructions an element).
 #include "lp_finish.cuh"
+#include "lp_stream.cuh"
 
 namespace svl {
 namespace {
 
 constexpr int kMaxThreads = 256;
 constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 4;               // vectors that a thread has in flight
 constexpr int kCandidates = 1024;        // elements kept for the last choice: 8 SV_MAX_TOP
 static_assert(kCandidates >= 8 * SV_MAX_TOP, "a vector of each of the first k");
 
@@ -37,48 +34,6 @@ struct LogprobPlan {
     int32_t cluster;    // blocks of a row
     int32_t groups;     // room for maxima, of groups and later of vectors
 };
-
-struct RowSum {
-    float m;            // largest logit (NaN, +inf: a bad row)
-    float s, e;         // sums of 2^((x - m) c) and of that times (x - m) c
-    float ahead;        // (a count's bits)
-};
-
-// A thread's sums; the reference is behind the largest logit by 2^16 at most.
-struct Running {
-    float r;            // -inf: nothing yet
-    float limit;        // a logit above this moves the reference
-    float m;
-    uint64_t s, e;      // two sums each
-    int32_t ahead;
-};
-
-// Sums against another reference, d = (old - new) c further down.
-__device__ __forceinline__ void rebase(float& s, float& e, float d)
-{
-    d = fmaxf(d, -1000.f);
-    const float f = ex2(d);
-    e = (e + s * d) * f;
-    s *= f;
-}
-
-__device__ __forceinline__ void move_reference(Running& st, float to, float c, float step)
-{
-    if (st.r == -inf()) {
-        st.r = to;
-    } else {
-        float s0, s1, e0, e1;
-        unpack2(st.s, s0, s1);
-        unpack2(st.e, e0, e1);
-        const float d = (st.r - to) * c;
-        rebase(s0, e0, d);
-        rebase(s1, e1, d);
-        st.s = pack2(s0, s1);
-        st.e = pack2(e0, e1);
-        st.r = to;
-    }
-    st.limit = to + step;
-}
 
 // The first float above x (for finite x or -inf).
 __device__ __forceinline__ float next_up(float x)
@@ -104,69 +59,6 @@ __device__ __noinline__ int count_ahead(uint4 v, float x_t, float above, int64_t
         n += b >= (2 * i + 1 < last ? x_t : above);
     }
     return n;
-}
-
-// One turn of vectors into a thread's sums.
-template <int DT, bool TOP>
-__device__ __forceinline__ void take(Running& st, const uint4 (&v)[kUnroll], const int32_t (&at)[kUnroll],
-                                     float* maxima, int32_t n, const Vecs& in, float c, float step,
-                                     float x_t, float above, int32_t token)
-{
-    float top;
-    if (TOP) {
-        top = -inf();
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const float t = halves_max<DT>(vec_max<DT>(v[u]));
-            const float g = warp_max(t);
-            if ((threadIdx.x & 31) == 0 && at[u] < n) maxima[at[u] >> 5] = g;
-            top = fmax_nan(top, t);
-        }
-    } else {
-        uint32_t t = vec_max<DT>(v[0]);
-#pragma unroll
-        for (int u = 1; u < kUnroll; ++u) t = packed_max<DT>(t, vec_max<DT>(v[u]));
-        top = halves_max<DT>(t);
-    }
-    st.m = fmax_nan(st.m, top);
-    if (top >= x_t) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (halves_max<DT>(vec_max<DT>(v[u])) >= x_t)
-                st.ahead += count_ahead<DT>(v[u], x_t, above, token - first_of<DT>(in, at[u]));
-    }
-    if (top > st.limit) move_reference(st, top, c, step);
-    if (st.r == -inf()) return;  // only -inf so far
-    const uint64_t r2 = pack2(-st.r, -st.r), c2 = pack2(c, c);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        uint64_t p[kPerVec<DT> / 2];
-        widen<DT>(v[u], p);
-#pragma unroll
-        for (int i = 0; i < kPerVec<DT> / 2; ++i) {
-            float t0, t1;
-            unpack2(mul2(add2(p[i], r2), c2), t0, t1);
-            // (masked logits: 0 times a number and not times -inf)
-            t0 = fmaxf(t0, -1000.f);
-            t1 = fmaxf(t1, -1000.f);
-            const uint64_t e = pack2(ex2(t0), ex2(t1));
-            st.s = add2(st.s, e);
-            st.e = fma2(e, pack2(t0, t1), st.e);
-        }
-    }
-}
-
-// Sums of two parts of a row, against the larger maximum.
-__device__ __forceinline__ RowSum join(RowSum a, RowSum b, float c)
-{
-    RowSum r;
-    r.m = fmax_nan(a.m, b.m);
-    if (a.s > 0.f) rebase(a.s, a.e, (a.m - r.m) * c);
-    if (b.s > 0.f) rebase(b.s, b.e, (b.m - r.m) * c);
-    r.s = a.s + b.s;
-    r.e = a.e + b.e;
-    r.ahead = __int_as_float(__float_as_int(a.ahead) + __float_as_int(b.ahead));
-    return r;
 }
 
 // The k that come first of n keys (larger first, then lower index), by one warp: their
@@ -349,40 +241,43 @@ __global__ void __launch_bounds__(kMaxThreads)
         a.tokens == nullptr ? inf() : load_one<DT>(in.a0 + in.head * kElem<DT>, token);
     const float above = next_up(x_t);
     const float step = 16.f / c;
+    const float low = lowest_of<DT>(c);
     Running st;
-    st.r = st.limit = st.m = -inf();
-    st.s = st.e = pack2(0.f, 0.f);
-    st.ahead = 0;
-    const int32_t turn = kUnroll * blockDim.x;
-    for (int64_t j0 = static_cast<int64_t>(rank) * turn; j0 < in.n; j0 += static_cast<int64_t>(C) * turn) {
-        uint4 v[kUnroll];
-        int32_t at[kUnroll];
+    start(st);
+    int32_t ahead = 0;
+    const int32_t tiles = tiles_of(in.n);
+    for (int32_t tile = rank * warps + warp; tile < tiles; tile += C * warps) {
+        const int32_t base = tile * kTile;
+        uint4 v[kInFlight];
+        ld_tile<DT>(v, in, base, lane, V);
+        float top;
+        if (TOP) {
+            float tops[kInFlight], groups[kInFlight];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            at[u] = static_cast<int32_t>(min(j0 + u * blockDim.x + tid, int64_t(INT32_MAX)));
-            v[u] = ld_vec<DT>(in, at[u], V);
+            for (int u = 0; u < kInFlight; ++u) {
+                tops[u] = halves_max<DT>(vec_max<DT>(v[u]));
+                groups[u] = warp_max(tops[u]);
+            }
+            if (lane == 0)
+                reinterpret_cast<float4*>(maxima)[tile] =
+                    make_float4(groups[0], groups[1], groups[2], groups[3]);
+            top = fmax_nan(fmax_nan(tops[0], tops[1]), fmax_nan(tops[2], tops[3]));
+        } else {
+            uint32_t t = vec_max<DT>(v[0]);
+#pragma unroll
+            for (int u = 1; u < kInFlight; ++u) t = packed_max<DT>(t, vec_max<DT>(v[u]));
+            top = halves_max<DT>(t);
         }
-        take<DT, TOP>(st, v, at, maxima, in.n, in, c, step, x_t, above, token);
+        if (top >= x_t) {
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u)
+                if (halves_max<DT>(vec_max<DT>(v[u])) >= x_t)
+                    ahead += count_ahead<DT>(v[u], x_t, above,
+                                             token - first_of<DT>(in, base + lane + u * 32));
+        }
+        take<DT, true>(st, v, top, c, step, low);
     }
-    RowSum mine;
-    mine.m = st.m;
-    {
-        float s0, s1, e0, e1;
-        unpack2(st.s, s0, s1);
-        unpack2(st.e, e0, e1);
-        mine.s = s0 + s1;
-        mine.e = e0 + e1;
-        if (mine.s > 0.f) rebase(mine.s, mine.e, (st.r - st.m) * c);
-        mine.ahead = __int_as_float(st.ahead);
-    }
-    for (int off = 16; off > 0; off >>= 1) {
-        RowSum o;
-        o.m = __shfl_xor_sync(0xFFFFFFFFu, mine.m, off);
-        o.s = __shfl_xor_sync(0xFFFFFFFFu, mine.s, off);
-        o.e = __shfl_xor_sync(0xFFFFFFFFu, mine.e, off);
-        o.ahead = __shfl_xor_sync(0xFFFFFFFFu, mine.ahead, off);
-        mine = join(mine, o, c);
-    }
+    const RowSum mine = warp_join(st, ahead, c);
     if (C == 1) {
         if (lane == 0) part[warp] = mine;
         __syncthreads();
@@ -393,15 +288,14 @@ __global__ void __launch_bounds__(kMaxThreads)
             st_cluster(&slot->m, 0, mine.m);
             st_cluster(&slot->s, 0, mine.s);
             st_cluster(&slot->e, 0, mine.e);
-            st_cluster(&slot->ahead, 0, mine.ahead);
+            st_cluster(&slot->ahead, 0, __int_as_float(mine.ahead));
         }
         if (TOP && rank != 0) {
             // This block's maxima, those that its own warps wrote among them.
             __syncthreads();
-            const int32_t groups = (in.n + 31) >> 5;
-            const int32_t per_turn = turn >> 5;
-            for (int32_t g0 = rank * per_turn; g0 < groups; g0 += C * per_turn)
-                for (int32_t g = g0 + tid; g < min(g0 + per_turn, groups); g += blockDim.x)
+            for (int32_t t0 = rank * warps; t0 < tiles; t0 += C * warps)
+                for (int32_t g = t0 * kInFlight + tid; g < min(t0 + warps, tiles) * kInFlight;
+                     g += blockDim.x)
                     st_cluster(&maxima[g], 0, maxima[g]);
         }
         cluster_arrive();
@@ -418,7 +312,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     const double log_s = log_wide(all.s);
     if (tid == 0) {
         // (the -inf that stand for what is before the row were counted as ties of a masked token)
-        const int ahead = __float_as_int(all.ahead) - (x_t == -inf() ? in.head : 0);
+        const int ahead = all.ahead - (x_t == -inf() ? in.head : 0);
         finish_row(a, row, all.m, all.s, all.e, x_t, ahead, log_s);
     }
     if (TOP)
@@ -430,21 +324,21 @@ template <int DT, bool TOP>
 cudaError_t launch(const LogprobArgs& a, cudaStream_t s)
 {
     constexpr int64_t kBlocks = 304;
-    const int64_t n = (a.r.V + kPerVec<DT> - 1) / kPerVec<DT> + 1;
-    int threads = 32;
-    while (threads < kMaxThreads && threads * kUnroll < n) threads *= 2;
+    const int64_t tiles = tiles_of((a.r.V + kPerVec<DT> - 1) / kPerVec<DT> + 1);
+    int warps = 1;
+    while (warps * 32 < kMaxThreads && warps < tiles) warps *= 2;
     // A cluster where there are fewer rows than two blocks an SM, and a turn for each block.
     int64_t C = 1;
-    while (C < kMaxCluster && a.r.rows * C < kBlocks && n > C * threads * kUnroll) C *= 2;
+    while (C < kMaxCluster && a.r.rows * C < kBlocks && tiles > C * warps) C *= 2;
     LogprobPlan p;
     p.cluster = static_cast<int32_t>(C);
-    // Maxima of groups, and of the chosen groups' vectors; 16-byte steps.
-    const int64_t groups = (n + 31) / 32;
+    // Maxima of groups, and of the chosen groups' vectors.
+    const int64_t groups = tiles * kInFlight;
     const int64_t again = 32 * (a.k < groups ? a.k : groups);
-    p.groups = static_cast<int32_t>(((groups > again ? groups : again) + 3) & ~int64_t(3));
+    p.groups = static_cast<int32_t>(groups > again ? groups : again);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.r.rows * C));
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = dim3(warps * 32);
     cfg.dynamicSmemBytes = TOP ? p.groups * 4 + sizeof(Top) : 0;
     cfg.stream = s;
     cudaLaunchAttribute at[1];

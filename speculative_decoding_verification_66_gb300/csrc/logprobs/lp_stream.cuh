@@ -1,0 +1,310 @@
+// lp_stream.cuh -- a row of logits through a block: its sums, and its gradient.
+//
+// A warp takes 128 vectors of 16 bytes at a time, four for each lane, and loads all of them
+// before it uses the first. Vectors at a row's ends are looked at only where a warp's tile
+// is not wholly inside; everywhere else a vector costs its load, a quarter of the loop's
+// counting, and the arithmetic: five instructions an element for a sum with its entropy
+// (pairs of float32 in one instruction where there is one), of the ten that there is time
+// for at the memory's rate.
+#pragma once
+
+#include "lp_vec.cuh"
+
+namespace svl {
+
+constexpr int kInFlight = 4;                // vectors of a lane's turn
+constexpr int kTile = 32 * kInFlight;       // vectors of a warp's turn
+
+// The largest |x c| that is taken off in one instruction with the product (t = x c - o).
+// Rows of logits further from 0 subtract first, since o would be rounded to a multiple of
+// something that matters.
+constexpr float kNear = 1048576.f;
+
+// A thread's sums of 2^t and 2^t t, t = x c - o, where o is (about) the largest x c seen,
+// behind it by 16 at most: it moves hardly ever, and a move costs one rounding.
+struct Running {
+    float m;            // largest logit (NaN if there is one)
+    float r;            // the logit that o stands for; -inf: none yet
+    float limit;        // a logit above this moves it
+    float o;            // r c rounded
+    bool near;          // or, far from 0: t = (x - r) c
+    uint64_t s, e;      // two sums each
+};
+
+__device__ __forceinline__ void start(Running& st)
+{
+    st.m = st.r = st.limit = -inf();
+    st.o = 0.f;
+    st.near = false;
+    st.s = st.e = pack2(0.f, 0.f);
+}
+
+// What t is relative to, exactly.
+__device__ __forceinline__ double reference(const Running& st, float c)
+{
+    return st.near ? static_cast<double>(st.o) : static_cast<double>(st.r) * c;
+}
+
+// Sums against another reference, d = old - new further down (or, on the last step, up by
+// no more than 16).
+__device__ __forceinline__ void rebase(float& s, float& e, float d)
+{
+    d = fmaxf(d, -1000.f);
+    const float f = ex2(d);
+    e = fmaf(s, d, e) * f;
+    s *= f;
+}
+
+static __device__ __noinline__ Running moved(Running st, float to, float c, float step, float low)
+{
+    const double before = reference(st, c);
+    const bool first = st.r == -inf();
+    st.r = to;
+    st.o = to * c;
+    st.limit = to + step;
+    st.near = fabsf(st.o) < kNear && (to - low) * c > 256.f;
+    if (!first) {
+        const float d = static_cast<float>(before - reference(st, c));
+        float s0, s1, e0, e1;
+        unpack2(st.s, s0, s1);
+        unpack2(st.e, e0, e1);
+        rebase(s0, e0, d);
+        rebase(s1, e1, d);
+        st.s = pack2(s0, s1);
+        st.e = pack2(e0, e1);
+    }
+    return st;
+}
+
+// A logit below this has no share in a sum whose reference is near 0 (and 256 / c above it,
+// which float16's end may not be), and t is finite for it: masked logits, -inf among them, are
+// raised to it, or 2^t t would be 0 times infinity.
+template <int DT>
+__device__ __forceinline__ float lowest_of(float c)
+{
+    const float l = -2.f * kNear / c;
+    const float end = DT == SV_F16 ? -65504.f : -3.3895314e38f;
+    const float x = fmaxf(l, end);
+    return DT == SV_F32 ? x : DT == SV_BF16 ? __bfloat162float(__float2bfloat16_rn(x))
+                                            : __half2float(__float2half_rn(x));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pair_of(float x)
+{
+    if (DT == SV_F32) return __float_as_uint(x);
+    const uint32_t h = DT == SV_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x))
+                                     : __half_as_ushort(__float2half_rn(x));
+    return h | h << 16;
+}
+// (not the maximum that hands NaN on: rows with NaN are told by their maximum)
+template <int DT>
+__device__ __forceinline__ uint32_t raised(uint32_t w, uint32_t low)
+{
+    uint32_t r;
+    if (DT == SV_F32)
+        asm("max.f32 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(low));
+    else if (DT == SV_BF16)
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(low));
+    else
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(low));
+    return r;
+}
+
+template <int DT, bool ENTROPY>
+__device__ __forceinline__ void add_tile(Running& st, const uint4 (&v)[kInFlight], float c,
+                                         uint32_t low)
+{
+    const uint64_t o2 = pack2(-st.o, -st.o), c2 = pack2(c, c);
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+        uint4 w = v[u];
+        if (ENTROPY)
+            w = make_uint4(raised<DT>(w.x, low), raised<DT>(w.y, low), raised<DT>(w.z, low),
+                           raised<DT>(w.w, low));
+        uint64_t p[kPerVec<DT> / 2];
+        widen<DT>(w, p);
+#pragma unroll
+        for (int i = 0; i < kPerVec<DT> / 2; ++i) {
+            const uint64_t t = fma2(p[i], c2, o2);
+            float a, b;
+            unpack2(t, a, b);
+            const uint64_t e = pack2(ex2(a), ex2(b));
+            st.s = add2(st.s, e);
+            if (ENTROPY) st.e = fma2(e, t, st.e);
+        }
+    }
+}
+
+// The same for a reference far from 0.
+template <int DT>
+__device__ __noinline__ void add_far(Running* st, uint4 v, float c)
+{
+    const uint64_t r2 = pack2(-st->r, -st->r), c2 = pack2(c, c);
+    uint64_t p[kPerVec<DT> / 2];
+    widen<DT>(v, p);
+#pragma unroll
+    for (int i = 0; i < kPerVec<DT> / 2; ++i) {
+        float a, b;
+        unpack2(mul2(add2(p[i], r2), c2), a, b);
+        a = fmaxf(a, -1000.f);
+        b = fmaxf(b, -1000.f);
+        const uint64_t e = pack2(ex2(a), ex2(b));
+        st->s = add2(st->s, e);
+        st->e = fma2(e, pack2(a, b), st->e);
+    }
+}
+
+// One turn's vectors, whose largest element is `top`, into a thread's sums.
+template <int DT, bool ENTROPY>
+__device__ __forceinline__ void take(Running& st, const uint4 (&v)[kInFlight], float top, float c,
+                                     float step, float low)
+{
+    st.m = fmax_nan(st.m, top);
+    if (top > st.limit) st = moved(st, top, c, step, low);
+    if (st.near) {
+        add_tile<DT, ENTROPY>(st, v, c, pair_of<DT>(low));
+    } else if (st.r != -inf()) {  // (-inf: nothing but that so far)
+        Running copy = st;
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) add_far<DT>(&copy, v[u], c);
+        st = copy;
+    }
+}
+
+// A warp's turn lies wholly inside a row.
+__device__ __forceinline__ bool whole(const Vecs& r, int32_t base)
+{
+    return base >= r.full && base + kTile <= r.full_end;
+}
+
+// Vectors j, j + 32, .. of a row; -inf where it has none.
+template <int DT>
+__device__ __forceinline__ void ld_tile(uint4 (&v)[kInFlight], const Vecs& in, int32_t base, int lane,
+                                        int32_t V)
+{
+    if (whole(in, base)) {
+        const uint8_t* p = in.a0 + static_cast<int64_t>(base + lane) * 16;
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) v[u] = ld_stream(p + u * 512);
+    } else {
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) v[u] = ld_vec<DT>(in, base + lane + u * 32, V);
+    }
+}
+
+// What is known of (a part of) a row: sums of 2^t and 2^t t with t = (x - m) c.
+struct RowSum {
+    float m;            // largest logit (NaN, +inf: a bad row; -inf: nothing else)
+    float s, e;
+    int32_t ahead;      // tokens ahead of the given one
+};
+
+__device__ __forceinline__ RowSum join(RowSum a, RowSum b, float c)
+{
+    RowSum r;
+    r.m = fmax_nan(a.m, b.m);
+    if (a.s > 0.f) rebase(a.s, a.e, (a.m - r.m) * c);
+    if (b.s > 0.f) rebase(b.s, b.e, (b.m - r.m) * c);
+    r.s = a.s + b.s;
+    r.e = a.e + b.e;
+    r.ahead = a.ahead + b.ahead;
+    return r;
+}
+
+// The sums of a warp's threads, in all lanes.
+__device__ __forceinline__ RowSum warp_join(const Running& st, int32_t ahead, float c)
+{
+    RowSum r;
+    r.m = warp_max(st.m);
+    float s0, s1, e0, e1;
+    unpack2(st.s, s0, s1);
+    unpack2(st.e, e0, e1);
+    r.s = s0 + s1;
+    r.e = e0 + e1;
+    if (r.s > 0.f)
+        rebase(r.s, r.e, static_cast<float>(reference(st, c) - static_cast<double>(r.m) * c));
+    for (int off = 16; off > 0; off >>= 1) {
+        r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, off);
+        r.e += __shfl_xor_sync(0xFFFFFFFFu, r.e, off);
+    }
+    r.ahead = __reduce_add_sync(0xFFFFFFFFu, ahead);
+    return r;
+}
+
+// e (A + B t) with t = (x - M) c and e = 2^t, for the vectors of a gradient's row that are in
+// the warps' turns first_tile, first_tile + step, .. before end_tile.
+template <int DT, bool LINEAR>
+__device__ __forceinline__ void grad_tiles(const Vecs& in, const Vecs& out, int32_t first_tile,
+                                           int32_t step, int32_t end_tile, int32_t V, float M,
+                                           float c, float A, float B)
+{
+    constexpr int P = kPerVec<DT> / 2;
+    const int lane = threadIdx.x & 31;
+    const Shift sh = shift_of<DT>(in, out);
+    const uint64_t m2 = pack2(-M, -M), c2 = pack2(c, c), A2 = pack2(A, A), B2 = pack2(B, B);
+    for (int32_t tile = first_tile; tile < end_tile; tile += step) {
+        const int32_t base = tile * kTile;
+        const bool inside = whole(out, base);
+        uint4 v[kInFlight];
+        if (sh.shift == 0) {
+            ld_tile<DT>(v, in, base, lane, V);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u) {
+                const int32_t i = base + lane + u * 32 + sh.step;
+                // (vectors around the row's: -inf, nothing is loaded)
+                const uint4 a = ld_vec<DT>(in, i < 0 ? in.n : i, V);
+                const uint4 b = ld_vec<DT>(in, i + 1, V);
+                v[u] = shifted(a, b, sh.shift * kElem<DT>);
+            }
+        }
+        uint8_t* g = out.a0 + static_cast<int64_t>(base + lane) * 16;
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            uint64_t p[P];
+            widen<DT>(v[u], p);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                uint64_t t = mul2(add2(p[i], m2), c2);
+                float t0, t1;
+                unpack2(t, t0, t1);
+                if (LINEAR) {
+                    // (masked logits: 0 times a number and not times -inf)
+                    t0 = fmaxf(t0, -1000.f);
+                    t1 = fmaxf(t1, -1000.f);
+                    t = pack2(t0, t1);
+                }
+                const uint64_t e = pack2(ex2(t0), ex2(t1));
+                p[i] = mul2(e, LINEAR ? fma2(B2, t, A2) : A2);
+            }
+            const uint4 w = narrow<DT>(p);
+            if (inside)
+                st_stream(g + u * 512, w);
+            else
+                st_vec<DT>(out, base + lane + u * 32, V, w);
+        }
+    }
+}
+
+// One value throughout the same vectors.
+template <int DT>
+__device__ __forceinline__ void fill_tiles(const Vecs& out, int32_t first_tile, int32_t step,
+                                           int32_t end_tile, int32_t V, float value)
+{
+    const uint64_t f = pack2(value, value);
+    uint64_t p[kPerVec<DT> / 2];
+#pragma unroll
+    for (int i = 0; i < kPerVec<DT> / 2; ++i) p[i] = f;
+    const uint4 v = narrow<DT>(p);
+    for (int32_t tile = first_tile; tile < end_tile; tile += step)
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u)
+            st_vec<DT>(out, tile * kTile + (threadIdx.x & 31) + u * 32, V, v);
+}
+
+__host__ __device__ __forceinline__ int32_t tiles_of(int64_t vectors)
+{
+    return static_cast<int32_t>((vectors + kTile - 1) / kTile);
+}
+
+}  // namespace svl

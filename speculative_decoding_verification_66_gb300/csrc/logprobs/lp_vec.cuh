@@ -222,19 +222,6 @@ __device__ __forceinline__ void st_vec(const Vecs& r, int32_t i, int32_t V, uint
         st_edge<DT>(r.a0, i, r.head, V, v);
 }
 
-// One value throughout vectors [first, end) of a row, by a block.
-template <int DT>
-__device__ __forceinline__ void fill(const Vecs& out, int32_t first, int32_t end, int32_t V,
-                                     float value)
-{
-    const uint64_t f = pack2(value, value);
-    uint64_t p[kPerVec<DT> / 2];
-#pragma unroll
-    for (int i = 0; i < kPerVec<DT> / 2; ++i) p[i] = f;
-    const uint4 v = narrow<DT>(p);
-    for (int32_t j = first + threadIdx.x; j < end; j += blockDim.x) st_vec<DT>(out, j, V, v);
-}
-
 // Largest element of a vector (NaN if one is).
 template <int DT>
 __device__ __forceinline__ uint32_t packed_max(uint32_t a, uint32_t b)

@@ -10,83 +10,33 @@
 // One read and one write of 16-byte vectors and some seven instructions an element:
 // bound by memory. A block takes a piece of a row.
 #include "lp_finish.cuh"
+#include "lp_stream.cuh"
 
 namespace svl {
 namespace {
 
 constexpr int kMaxThreads = 256;
-constexpr int kUnroll = 4;      // vectors that a thread has in flight
-
-// This block's piece of a row.
-struct Piece {
-    int32_t row;
-    int32_t first, end;      // vectors of the gradient's row
-};
 
 struct GradPlan {
     int32_t pieces;          // of a row
-    int32_t piece;           // vectors
+    int32_t piece;           // warps' turns in a piece
 };
 
-// The logits under vector j of the gradient.
-template <int DT>
-__device__ __forceinline__ uint4 ld_under(const Vecs& in, const Vecs& out, Shift sh, int32_t j,
-                                          int32_t V)
-{
-    if (sh.shift == 0) return ld_vec<DT>(in, j, V);
-    const int32_t i = j + sh.step;
-    // (vectors around the row's: -inf, nothing is loaded)
-    const uint4 a = i < 0 ? ld_vec<DT>(in, in.n, V) : ld_vec<DT>(in, i, V);
-    const uint4 b = ld_vec<DT>(in, i + 1, V);
-    return shifted(a, b, sh.shift * kElem<DT>);
-}
+// This block's turns in its row.
+struct Piece {
+    int32_t first, end;      // of the block
+    int32_t mine, step;      // of the warp
+};
 
-// e (A + B t) over a piece.
-template <int DT, bool LINEAR>
-__device__ __forceinline__ void grad_piece(const Vecs& in, const Vecs& out, int32_t first,
-                                           int32_t end, int32_t V, float M, float c, float A,
-                                           float B)
-{
-    constexpr int P = kPerVec<DT> / 2;
-    const Shift sh = shift_of<DT>(in, out);
-    const uint64_t m2 = pack2(-M, -M), c2 = pack2(c, c), A2 = pack2(A, A), B2 = pack2(B, B);
-    for (int32_t j0 = first + threadIdx.x; j0 < end; j0 += kUnroll * blockDim.x) {
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int32_t j = j0 + u * blockDim.x;
-            if (j < end) v[u] = ld_under<DT>(in, out, sh, j, V);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int32_t j = j0 + u * blockDim.x;
-            if (j >= end) break;
-            uint64_t p[P];
-            widen<DT>(v[u], p);
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                float t0, t1;
-                unpack2(mul2(add2(p[i], m2), c2), t0, t1);
-                if (LINEAR) {
-                    // (masked logits: 0 times a number and not times -inf)
-                    t0 = fmaxf(t0, -1000.f);
-                    t1 = fmaxf(t1, -1000.f);
-                }
-                const uint64_t e = pack2(ex2(t0), ex2(t1));
-                p[i] = mul2(e, LINEAR ? fma2(B2, pack2(t0, t1), A2) : A2);
-            }
-            st_vec<DT>(out, j, V, narrow<DT>(p));
-        }
-    }
-}
-
-__device__ __forceinline__ Piece my_piece(const GradPlan& g, int32_t n)
+__device__ __forceinline__ Piece my_piece(const GradPlan& g, int32_t row, int32_t vectors)
 {
     Piece p;
-    p.row = blockIdx.x / g.pieces;
-    const int64_t first = static_cast<int64_t>(blockIdx.x - p.row * g.pieces) * g.piece;
-    p.first = static_cast<int32_t>(min(first, static_cast<int64_t>(n)));
-    p.end = static_cast<int32_t>(min(first + g.piece, static_cast<int64_t>(n)));
+    const int32_t tiles = tiles_of(vectors);
+    const int64_t first = static_cast<int64_t>(blockIdx.x - row * g.pieces) * g.piece;
+    p.first = static_cast<int32_t>(min(first, static_cast<int64_t>(tiles)));
+    p.end = static_cast<int32_t>(min(first + g.piece, static_cast<int64_t>(tiles)));
+    p.mine = p.first + (threadIdx.x >> 5);
+    p.step = blockDim.x >> 5;
     return p;
 }
 
@@ -97,10 +47,10 @@ __global__ void __launch_bounds__(kMaxThreads)
     const int32_t row = blockIdx.x / plan.pieces, V = a.r.V;
     const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
     const Vecs out = vectors_of<DT>(row_begin(a.grad, a.r.inner, row), V);
-    const Piece pc = my_piece(plan, out.n);
+    const Piece pc = my_piece(plan, row, out.n);
     const RowStats st = a.stats[row];
     if (st.kind != kRowGood) {
-        fill<DT>(out, pc.first, pc.end, V, st.kind == kRowBad ? nan() : 0.f);
+        fill_tiles<DT>(out, pc.mine, pc.step, pc.end, V, st.kind == kRowBad ? nan() : 0.f);
         return;
     }
     const float da = a.a == nullptr ? 0.f : a.a[row];
@@ -111,7 +61,8 @@ __global__ void __launch_bounds__(kMaxThreads)
     // The token's own gradient, where it is in this piece: its logit is read before anything
     // is written, over the logits perhaps.
     const int32_t token = a.tokens == nullptr ? -1 : a.tokens[row];
-    const int64_t at = token < 0 ? -1 : (static_cast<int64_t>(token) + out.head) / kPerVec<DT>;
+    const int64_t at =
+        token < 0 ? -1 : (static_cast<int64_t>(token) + out.head) / (kPerVec<DT> * kTile);
     const bool mine = at >= pc.first && at < pc.end;
     float own = 0.f;
     if (mine) {
@@ -121,9 +72,9 @@ __global__ void __launch_bounds__(kMaxThreads)
         __syncthreads();
     }
     if (db == 0.f)
-        grad_piece<DT, false>(in, out, pc.first, pc.end, V, st.M, a.r.c, A, 0.f);
+        grad_tiles<DT, false>(in, out, pc.mine, pc.step, pc.end, V, st.M, a.r.c, A, 0.f);
     else
-        grad_piece<DT, true>(in, out, pc.first, pc.end, V, st.M, a.r.c, A, B);
+        grad_tiles<DT, true>(in, out, pc.mine, pc.step, pc.end, V, st.M, a.r.c, A, B);
     if (mine) {
         __syncthreads();
         if (threadIdx.x == 0) store_one<DT>(out.a0 + out.head * kElem<DT>, token, own);
@@ -140,10 +91,10 @@ __global__ void __launch_bounds__(kMaxThreads)
     const int32_t row = blockIdx.x / plan.pieces, V = a.r.V;
     const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
     const Vecs out = vectors_of<DT>(row_begin(a.grad, a.r.inner, row), V);
-    const Piece pc = my_piece(plan, out.n);
+    const Piece pc = my_piece(plan, row, out.n);
     const RowStats st = a.stats[row];
     if (st.kind != kRowGood) {
-        fill<DT>(out, pc.first, pc.end, V, st.kind == kRowBad ? nan() : 0.f);
+        fill_tiles<DT>(out, pc.mine, pc.step, pc.end, V, st.kind == kRowBad ? nan() : 0.f);
         return;
     }
     const float w = a.weights[row] * a.r.inv_t;
@@ -153,8 +104,8 @@ __global__ void __launch_bounds__(kMaxThreads)
         const int64_t at = static_cast<int64_t>(row) * a.k + j;
         int32_t v = a.ids[at];
         logp[j] = a.logp[at];
-        const int64_t vec = (static_cast<int64_t>(v) + out.head) / kPerVec<DT>;
-        if (v < 0 || v >= V || vec < pc.first || vec >= pc.end) v = -1;
+        const int64_t tile = (static_cast<int64_t>(v) + out.head) / (kPerVec<DT> * kTile);
+        if (v < 0 || v >= V || tile < pc.first || tile >= pc.end) v = -1;
         id[j] = v;
         some |= v >= 0;
     }
@@ -172,7 +123,7 @@ __global__ void __launch_bounds__(kMaxThreads)
         }
         __syncthreads();
     }
-    grad_piece<DT, false>(in, out, pc.first, pc.end, V, st.M, a.r.c, w * st.scale, 0.f);
+    grad_tiles<DT, false>(in, out, pc.mine, pc.step, pc.end, V, st.M, a.r.c, w * st.scale, 0.f);
     if (some) {
         __syncthreads();
         for (int j = threadIdx.x; j < a.k; j += blockDim.x)
@@ -180,23 +131,23 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
 }
 
-// A thread moves up to eight vectors, in blocks of 32 to 256 threads: short rows leave few
-// threads idle, long ones are cut where a block's start no longer shows.
+// A warp has up to two turns, in blocks of one to eight warps: short rows leave few threads
+// idle, long ones are cut where a block's start no longer shows.
 template <typename Kernel, typename Args>
 cudaError_t launch(Kernel k, const Args& a, int per_vec, cudaStream_t s)
 {
-    const int64_t n = (a.r.V + per_vec - 1) / per_vec + 1;
-    int threads = 32;
-    while (threads < kMaxThreads && threads * kUnroll < n) threads *= 2;
+    const int64_t tiles = tiles_of((a.r.V + per_vec - 1) / per_vec + 1);
+    int warps = 1;
+    while (warps * 32 < kMaxThreads && warps < tiles) warps *= 2;
     GradPlan g;
-    g.piece = threads * 2 * kUnroll;
-    int64_t pieces = (n + g.piece - 1) / g.piece;
+    g.piece = warps * 2;
+    int64_t pieces = (tiles + g.piece - 1) / g.piece;
     while (pieces * a.r.rows >= (int64_t(1) << 31)) {
         g.piece *= 2;
-        pieces = (n + g.piece - 1) / g.piece;
+        pieces = (tiles + g.piece - 1) / g.piece;
     }
     g.pieces = static_cast<int32_t>(pieces);
-    k<<<static_cast<unsigned>(pieces * a.r.rows), threads, 0, s>>>(a, g);
+    k<<<static_cast<unsigned>(pieces * a.r.rows), warps * 32, 0, s>>>(a, g);
     return cudaGetLastError();
 }
 

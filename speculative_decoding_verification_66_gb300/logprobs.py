@@ -139,7 +139,8 @@ def _logprobs(described, logits, tokens, top_k, row_stats, row_status):
 
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, described, logits, tokens, temperature, top_k, row_stats, row_status):
+    def forward(ctx, described, logits, tokens, temperature, top_k, row_stats, row_status, rest):
+        """The differentiable results; the others go to the list `rest`."""
         if row_stats is None:
             row_stats = torch.empty((*logits.shape[:-1], SV_ROW_STATS), dtype=torch.float32,
                                     device=logits.device)
@@ -147,20 +148,28 @@ class _TokenLogprobs(torch.autograd.Function):
         ctx.save_for_backward(logits, tokens, row_stats)
         ctx.temperature = temperature
         ctx.set_materialize_grads(False)
-        ctx.mark_non_differentiable(*(x for x in (out.rank, out.top_tokens, out.top_logprobs)
-                                      if x is not None))
-        return tuple(out)
+        rest += (out.rank, out.top_tokens, out.top_logprobs)
+        return out.logprobs, out.entropy, out.lse
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, grad_logprobs, _rank, grad_entropy, grad_lse, _tokens, _logprobs):
-        logits, tokens, row_stats = ctx.saved_tensors
-        grad = sv_token_logprobs_backward(
-            logits, row_stats, tokens=tokens, temperature=ctx.temperature,
-            **{name: None if g is None else g.contiguous() for name, g in
-               (("grad_logprobs", grad_logprobs), ("grad_entropy", grad_entropy),
-                ("grad_lse", grad_lse))})
-        return None, grad, None, None, None, None, None
+    def backward(ctx, *grads):
+        return (_logprobs_backward_once if torch.is_grad_enabled() else _logprobs_backward)(
+            ctx, *grads)
+
+
+def _logprobs_backward(ctx, grad_logprobs, grad_entropy, grad_lse):
+    logits, tokens, row_stats = ctx.saved_tensors
+    grad = sv_token_logprobs_backward(
+        logits, row_stats, tokens=tokens, temperature=ctx.temperature,
+        grad_logprobs=None if grad_logprobs is None else grad_logprobs.contiguous(),
+        grad_entropy=None if grad_entropy is None else grad_entropy.contiguous(),
+        grad_lse=None if grad_lse is None else grad_lse.contiguous())
+    return None, grad, None, None, None, None, None, None
+
+
+# (refuses second derivatives; only where a graph of the backward pass is asked for, since it takes
+# its time)
+_logprobs_backward_once = torch.autograd.function.once_differentiable(_logprobs_backward)
 
 
 def sv_token_logprobs(logits, tokens=None, *, temperature: float = 1.0, top_k: int = 0,
@@ -179,8 +188,10 @@ def sv_token_logprobs(logits, tokens=None, *, temperature: float = 1.0, top_k: i
 
     def call(_):
         if logits.requires_grad and torch.is_grad_enabled():
-            return TokenLogprobs(*_TokenLogprobs.apply(described, logits, tokens, temperature, top_k,
-                                                       row_stats, row_status))
+            rest = []
+            logprobs, entropy, lse = _TokenLogprobs.apply(described, logits, tokens, temperature,
+                                                          top_k, row_stats, row_status, rest)
+            return TokenLogprobs(logprobs, rest[0], entropy, lse, rest[1], rest[2])
         return _logprobs(described, logits, tokens, top_k, row_stats, row_status)
 
     return _on(logits.device, stream, call, (logits, tokens, row_stats, row_status))
@@ -258,13 +269,20 @@ class _DistillLoss(torch.autograd.Function):
         return loss
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
-        logits, teacher_tokens, teacher_logprobs, row_stats = ctx.saved_tensors
-        temperature, tail = ctx.args
-        grad = sv_distill_backward(logits, teacher_tokens, teacher_logprobs, row_stats,
-                                   grad_loss.contiguous(), temperature=temperature, tail=tail)
-        return None, grad, None, None, None, None, None
+        return (_distill_backward_once if torch.is_grad_enabled() else _distill_backward)(
+            ctx, grad_loss)
+
+
+def _distill_backward(ctx, grad_loss):
+    logits, teacher_tokens, teacher_logprobs, row_stats = ctx.saved_tensors
+    temperature, tail = ctx.args
+    grad = sv_distill_backward(logits, teacher_tokens, teacher_logprobs, row_stats,
+                               grad_loss.contiguous(), temperature=temperature, tail=tail)
+    return None, grad, None, None, None, None, None
+
+
+_distill_backward_once = torch.autograd.function.once_differentiable(_distill_backward)
 
 
 def sv_distill_loss(logits, teacher_tokens, teacher_logprobs, *, temperature: float = 1.0,
