@@ -27,8 +27,15 @@
  * Sums and statistics are float32, gradients are rounded to the logits' type
  * once. Results do not depend on the order in which blocks run: the same
  * inputs give the same bits. Return codes are spec_verify.h's SV_OK and
- * SV_ERR_*. All calls are asynchronous on `stream`, allocate nothing, need no
- * workspace and may be captured into a CUDA graph.
+ * SV_ERR_*. All calls are asynchronous on `stream`, allocate nothing and may be
+ * captured into a CUDA graph.
+ *
+ * Workspace. Rows are cut into pieces whose blocks leave one another their sums.
+ *   workspace  device, 256-byte aligned, at least sv_logprobs_workspace_bytes (which
+ *              may be 0: then it may be NULL). Its first SV_LOGPROBS_COUNTER_BYTES
+ *              must be 0 before it is used for the first time, with rows of whatever
+ *              sizes; every call leaves them 0. Calls that share a workspace must be
+ *              ordered (one stream, or events); a captured call's replays too.
  */
 #ifndef SV_LOGPROBS_H
 #define SV_LOGPROBS_H
@@ -51,6 +58,9 @@ extern "C" {
 #define SV_MAX_TOP 128
 /* Largest vocabulary whose top alternatives are given. */
 #define SV_MAX_TOP_VOCAB (1 << 20)
+
+/* The part of a workspace that has to be 0 before its first use. */
+#define SV_LOGPROBS_COUNTER_BYTES 262144
 
 /* Floats that the forward calls keep of a row for the backward ones. */
 #define SV_ROW_STATS 8
@@ -85,6 +95,12 @@ typedef struct sv_logit_rows {
 } sv_logit_rows;
 
 /*
+ * Workspace for any of these calls on such rows, with up to top_k alternatives.
+ * rows->logits and the strides are not looked at. Host only.
+ */
+int sv_logprobs_workspace_bytes(const sv_logit_rows* rows, int64_t top_k, size_t* bytes);
+
+/*
  * Log probabilities, entropy and top alternatives of rows of logits, which are
  * read once.
  *   tokens        device int32 [rows], or NULL. -1: nothing is asked of the row,
@@ -104,7 +120,7 @@ typedef struct sv_logit_rows {
 int sv_token_logprobs(const sv_logit_rows* rows, const int32_t* tokens, int64_t top_k,
                       float* logprobs, float* entropy, float* lse, int32_t* rank,
                       int32_t* top_tokens, float* top_logprobs, float* row_stats,
-                      int32_t* row_status, void* stream);
+                      int32_t* row_status, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * The logits' gradient, from gradients a, b and c of log probability, entropy and
@@ -142,12 +158,13 @@ int sv_token_logprobs_backward(const sv_logit_rows* rows, const int32_t* tokens,
  *   loss        device float [rows], or NULL.
  *   grad        as in sv_token_logprobs_backward, or NULL.
  *   row_stats   device float [rows][SV_ROW_STATS], 16-byte aligned, or NULL.
- * One launch.
+ * One launch, and one more for the gradient.
  */
 int sv_distill(const sv_logit_rows* rows, const int32_t* teacher_tokens,
                const float* teacher_logprobs, int64_t k, int tail, const float* weights,
                float* loss, void* grad, int64_t grad_outer_stride, int64_t grad_inner_stride,
-               float* row_stats, int32_t* row_status, void* stream);
+               float* row_stats, int32_t* row_status, void* workspace, size_t workspace_bytes,
+               void* stream);
 
 /*
  * The gradient alone, from row_stats of a sv_distill call on the same rows and

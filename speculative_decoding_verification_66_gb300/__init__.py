@@ -67,6 +67,7 @@ from .attention import (  # noqa: F401
     sv_kv_read,
 )
 from .logprobs import (  # noqa: F401
+    SV_LOGPROBS_COUNTER_BYTES,
     SV_MAX_TOP,
     SV_MAX_TOP_VOCAB,
     SV_ROW_STATS,
@@ -76,6 +77,7 @@ from .logprobs import (  # noqa: F401
     sv_distill,
     sv_distill_backward,
     sv_distill_loss,
+    sv_logprobs_workspace_bytes,
     sv_token_logprobs,
     sv_token_logprobs_backward,
 )

@@ -84,12 +84,13 @@ ATTENTION_SIGNATURES = {
 # The same for libsvlogprobs.so and include/sv_logprobs.h, passed the same way.
 LOGPROBS_PATH = os.path.join(_DIR, "libsvlogprobs.so")
 LOGPROBS_SIGNATURES = {
+    "sv_logprobs_workspace_bytes": (_i32, [ctypes.c_char_p, _i64, ctypes.POINTER(_sz)]),
     "sv_token_logprobs": (_i32, [ctypes.c_char_p, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
-                                 _vp]),
+                                 _vp, _sz, _vp]),
     "sv_token_logprobs_backward": (_i32, [ctypes.c_char_p, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
                                           _vp]),
     "sv_distill": (_i32, [ctypes.c_char_p, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _vp,
-                          _vp, _vp]),
+                          _vp, _vp, _sz, _vp]),
     "sv_distill_backward": (_i32, [ctypes.c_char_p, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64,
                                    _vp]),
 }

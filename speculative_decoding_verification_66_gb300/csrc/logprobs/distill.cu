@@ -1,11 +1,5 @@
-// distill.cu -- divergence of a teacher's entries from rows of logits, and its
-// gradient, in one read of memory and one write.
-//
-// The gradient of an element needs the sum over its whole row first. A block goes through
-// its row twice, and the second time finds it in L2: what the resident blocks have of rows
-// is kept below the cache's size. (Rows held in a cluster's shared memory, 64 KB a block,
-// read L2 once less and took more than twice as long: what a row waits for -- its teacher,
-// barriers, a few logarithms -- has little to hide behind where a row fills an SM.)
+// distill.cu -- divergence of a teacher's entries from rows of logits, and what its
+// gradient needs (rows_grad.cu has that).
 //
 // With SV_TAIL_BUCKET the sum over the tokens without entries must not be a difference:
 // where a teacher's few tokens have nearly all of the student's probability too, nothing
@@ -13,39 +7,210 @@
 // vector of eight; a warp looks at its vectors' bytes and takes out what is marked, which is
 // rare. (Renormalised or not: the sum is over the others, and the entries are added.)
 //
-// The entries' gradients are written over what the loop wrote for them, a barrier later.
-//
-// A row is taken by a block, or by a cluster of up to eight where there are few rows or they
-// are long: each block tells all others its part's maximum and sum, and all find the row's
-// few logarithms for themselves (one barrier over the cluster; an answer would take two).
+// A row is cut into pieces as in logprobs.cu. One warp of the block that is a row's last takes
+// the teacher into its lanes' registers and finds the row's few logarithms; a duplicate token
+// shows by its mark being there already, and only then the entries are compared with one
+// another.
 #include "lp_finish.cuh"
 #include "lp_stream.cuh"
 
 namespace svl {
 namespace {
 
-constexpr int kMaxThreads = 512;
-constexpr int kMaxCluster = 8;
-// A bitmap's words, and the elements that they are for: longer rows take turns with it.
-constexpr int32_t kMapWords = 8192;
+constexpr int kMaxWarps = 4;
+// Turns that a block's bitmap of entries is for.
+constexpr int32_t kSpan = kMostTurns;
 
 struct DistillPlan {
-    int32_t cluster;     // blocks of a row
-    int32_t words;       // of the bitmap
+    int32_t pieces;      // of a row, a block each
+    int32_t piece;       // warps' turns in a piece
+    Split split;         // with more than one piece
 };
 
-// Sets or clears the marks of the entries from position `begin` on.
-template <bool SET>
-__device__ __forceinline__ void mark(uint32_t* map, const Teacher& t, int32_t k, int32_t head,
-                                     int64_t begin, int32_t words)
+// The teacher in its warp: entry lane + 32 q is the lane's q-th.
+constexpr int kEach = SV_MAX_TOP / 32;
+struct Teacher {
+    int32_t id[kEach];   // -1 where there is none, or where its token came before
+    float x[kEach];      // the student's logit
+    float p[kEach];      // probability, before they are renormalised
+    double mass;         // their sum
+    float shift;         // what was taken off their logarithms
+    int32_t distinct;
+    int32_t status;
+};
+
+// Room for looking for entries of one token.
+struct Entries {
+    int32_t id[SV_MAX_TOP];
+    float p[SV_MAX_TOP];
+};
+
+template <typename N>
+__device__ __forceinline__ N warp_sum(N x)
 {
-    for (int j = threadIdx.x; j < k; j += blockDim.x) {
-        const int64_t at = static_cast<int64_t>(t.id[j]) + head - begin;
-        if (t.id[j] < 0 || at < 0 || at >= static_cast<int64_t>(words) * 32) continue;
-        if (SET)
-            atomicOr(&map[at >> 5], 1u << (at & 31));
-        else
-            map[at >> 5] = 0u;
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+    return x;
+}
+
+// Takes the row's entries and their logits.
+template <int DT>
+__device__ __forceinline__ void read_teacher(Teacher& t, const DistillArgs& a, int32_t row,
+                                             const uint8_t* x, int lane)
+{
+    int bad = 0;
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+        const int j = lane + 32 * q;
+        int32_t id = -1;
+        float lp = -inf();
+        if (j < a.k) {
+            const int64_t at = static_cast<int64_t>(row) * a.k + j;
+            id = a.ids[at];
+            lp = a.logp[at];
+        }
+        const bool nonfinite = lp != lp || lp == inf();
+        if (id < -1 || id >= a.r.V) bad |= SV_SEQ_BAD_TOKEN;
+        if (nonfinite) bad |= SV_SEQ_NONFINITE;
+        if (id < 0 || id >= a.r.V || nonfinite) {
+            id = -1;
+            lp = -inf();
+        }
+        t.id[q] = id;
+        t.p[q] = lp;   // (its logarithm so far)
+        t.x[q] = id >= 0 ? load_one<DT>(x, id) : 0.f;
+    }
+    t.status = __reduce_or_sync(0xFFFFFFFFu, bad);
+}
+
+// The entries' probabilities. `twice`: some token may have two entries.
+__device__ __forceinline__ void make_teacher(Teacher& t, Entries& s, const DistillArgs& a, int lane,
+                                             bool twice)
+{
+    // Renormalised probabilities are taken from the largest one, so that none overflows.
+    t.shift = 0.f;
+    if (!a.bucket) {
+        float top = t.p[0];
+#pragma unroll
+        for (int q = 1; q < kEach; ++q) top = fmaxf(top, t.p[q]);
+        top = warp_max(top);
+        if (top != -inf()) t.shift = top;
+    }
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) t.p[q] = t.id[q] >= 0 ? expf(t.p[q] - t.shift) : 0.f;
+    if (twice) {
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            s.id[lane + 32 * q] = t.id[q];
+            s.p[lane + 32 * q] = t.p[q];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            if (t.id[q] < 0) continue;
+            float p = 0.f;
+            bool first = true;
+            for (int i = 0; i < a.k; ++i)
+                if (s.id[i] == t.id[q]) {
+                    first &= i >= lane + 32 * q;
+                    p += s.p[i];
+                }
+            t.p[q] = first ? p : 0.f;
+            if (!first) t.id[q] = -1;
+        }
+    }
+    double mass = 0.0;
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+        mass += t.p[q];
+        n += t.id[q] >= 0;
+    }
+    t.mass = warp_sum(mass);
+    t.distinct = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (!a.bucket && t.distinct > 0 && !(t.mass > 0.0)) t.status |= SV_SEQ_NONFINITE;
+}
+
+// 1 / x to some 2^-40, for x in the range of floats.
+__device__ __forceinline__ double inverse(double x)
+{
+    const double r = 1.0f / static_cast<float>(x);
+    return r * (2.0 - x * r);
+}
+
+// Loss and gradient factors of a row, from the largest logit M_o and the sum S_o of
+// 2^((x - M_o) c) over the tokens without entries (-inf and 0: none, or all of them are
+// -inf). With M the largest of all, S the sum over all of 2^((x - M) c), q_e the entries'
+// share of it and m the sum of their probabilities:
+//   listed = 1 / S, scale = 2^((M_o - M) c) / S             renormalised
+//   listed = max(m, 1) / S                                  bucket
+//   scale  = (1 - P_o / q_o) 2^((M_o - M) c) / S = (m - q_e) / S_o     .. where m <= 1
+// so that the others' gradient keeps its digits however small their share is.
+__device__ __forceinline__ void finish(const Teacher& t, const DistillArgs& a, int32_t row, float M_o,
+                                       float S_o, int lane)
+{
+    const float c = a.r.c;
+    float M = -inf();
+#pragma unroll
+    for (int q = 0; q < kEach; ++q)
+        if (t.id[q] >= 0) M = fmax_nan(M, t.x[q]);
+    M = fmax_nan(warp_max(M), M_o);
+    if (!(fabsf(M) < inf()) || t.status != 0) {
+        if (lane == 0) {
+            if (a.loss != nullptr) a.loss[row] = nan();
+            if (a.stats != nullptr) a.stats[row].kind = kRowBad;
+            if (a.status != nullptr)
+                a.status[row] = t.status | (fabsf(M) < inf() ? 0 : SV_SEQ_NONFINITE);
+        }
+        return;
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int q = 0; q < kEach; ++q)
+        if (t.id[q] >= 0) sum += ex2((t.x[q] - M) * c);
+    const double S_e = warp_sum(sum);
+    const float fall = S_o > 0.f ? ex2((M_o - M) * c) : 0.f;
+    const double S = S_e + static_cast<double>(S_o) * fall;
+    const double log_s = log_wide(static_cast<float>(S));
+    const double over_mass = a.bucket ? 1.0 : inverse(t.mass);
+    const double log_m = a.bucket ? 0.0 : log_wide(static_cast<float>(t.mass));
+    double loss = 0.0;
+#pragma unroll
+    for (int q = 0; q < kEach; ++q)
+        if (t.id[q] >= 0 && t.p[q] > 0.f)
+            loss += t.p[q] * over_mass *
+                    (log_wide(t.p[q]) - log_m - log_prob(t.x[q], M, c, log_s));
+    loss = warp_sum(loss);
+    const double over_S = inverse(S);
+    float listed = static_cast<float>(over_S);
+    float scale = listed * fall;
+    if (a.bucket) {
+        const double q_e = S_e * over_S;
+        const double P_o = t.distinct < a.r.V ? fmax(0.0, 1.0 - t.mass) : 0.0;
+        if (P_o > 0.0) {
+            const float m = static_cast<float>(t.mass);
+            const double log_P = m < 0.5f ? log1pf(-m) : logf(static_cast<float>(P_o));
+            const double log_q = q_e < 0.5 ? static_cast<double>(log1pf(-static_cast<float>(q_e)))
+                                           : log_prob(M_o, M, c, log_s) + log_wide(S_o);
+            loss += P_o * (log_P - log_q);
+        }
+        listed = static_cast<float>((t.mass + P_o) * over_S);
+        // (no other token, or all of probability 0: their gradient is 0)
+        scale = !(S_o > 0.f)    ? 0.f
+                : t.mass <= 1.0 ? static_cast<float>(t.mass - q_e) / S_o
+                                : listed * fall;
+    }
+    if (lane == 0) {
+        if (a.loss != nullptr) a.loss[row] = static_cast<float>(loss);
+        if (a.stats != nullptr)  // (M_o where nothing is finite: any finite number)
+            a.stats[row] = {S_o > 0.f ? M_o : 0.f,
+                            scale,
+                            0.f,
+                            M,
+                            listed,
+                            t.shift,
+                            static_cast<float>(over_mass),
+                            kRowGood};
+        if (a.status != nullptr) a.status[row] = 0;
     }
 }
 
@@ -74,146 +239,125 @@ __device__ __forceinline__ uint32_t marks_of(const uint32_t* map, int32_t i)
     return DT == SV_F32 ? b[i >> 1] >> ((i & 1) * 4) & 15u : b[i];
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kMaxThreads)
-    distill_kernel(const __grid_constant__ DistillArgs a, const DistillPlan plan)
+// A piece of a row to a block. SPLIT: of several.
+template <int DT, bool SPLIT>
+__global__ void __launch_bounds__(kMaxWarps * 32, 10)
+    distill_kernel(const __grid_constant__ DistillArgs a, const __grid_constant__ DistillPlan plan)
 {
-    extern __shared__ __align__(16) uint32_t map[];
-    __shared__ Teacher t;
-    __shared__ float part_m[kMaxThreads / 32], part_s[kMaxThreads / 32];
-    __shared__ float from_m[kMaxCluster], from_s[kMaxCluster];
-    const int C = plan.cluster;
-    const int32_t row = blockIdx.x / C, rank = blockIdx.x - row * C, V = a.r.V;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    constexpr int32_t kBits = kSpan * kTile * kPerVec<DT>;
+    __shared__ uint32_t map[kBits / 32];
+    __shared__ RowSum part[kMaxWarps];
+    __shared__ Entries entries;
+    __shared__ uint32_t flag;
+    const int32_t row = SPLIT ? blockIdx.x / plan.pieces : blockIdx.x;
+    const int32_t piece = SPLIT ? blockIdx.x - row * plan.pieces : 0, V = a.r.V;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const float c = a.r.c;
-    const int32_t first_tile = rank * warps + warp, step_tiles = C * warps;
-    // (that all blocks of the cluster run is known to each before it writes to another)
-    if (C > 1) cluster_arrive();
-    const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
-    const bool has_grad = a.grad.base != nullptr;
-    const Vecs out = has_grad ? vectors_of<DT>(row_begin(a.grad, a.r.inner, row), V) : in;
-    for (int i = threadIdx.x; i < plan.words; i += blockDim.x) map[i] = 0u;
-    int kind = kRowSkipped;
-    if (!read_teacher(t, a, row)) {
-        if (rank == 0 && threadIdx.x == 0) finish_distill_skipped(a, row);
-        if (C > 1) cluster_wait();
-    } else {
-        make_teacher(t, a);
-        const uint8_t* x = in.a0 + in.head * kElem<DT>;
-        for (int j = threadIdx.x; j < a.k; j += blockDim.x)
-            if (t.id[j] >= 0) t.x[j] = load_one<DT>(x, t.id[j]);
-        Running st;
-        start(st);
-        const float step = 16.f / c, low = lowest_of<DT>(c);
-        const int32_t tiles = tiles_of(in.n);
-        const int32_t span = plan.words * 32 / (kPerVec<DT> * kTile);  // turns of one bitmap
-        for (int32_t t0 = 0; t0 < tiles; t0 += span) {
-            const int64_t begin = static_cast<int64_t>(t0) * kTile * kPerVec<DT>;
-            if (t0 > 0) {
-                __syncthreads();
-                mark<false>(map, t, a.k, in.head, begin - static_cast<int64_t>(plan.words) * 32,
-                            plan.words);
-                __syncthreads();
-            }
-            mark<true>(map, t, a.k, in.head, begin, plan.words);
-            __syncthreads();
-            int32_t tile = t0 + (first_tile - t0 % step_tiles + step_tiles) % step_tiles;
-            for (; tile < min(t0 + span, tiles); tile += step_tiles) {
-                const int32_t base = tile * kTile;
-                uint4 v[kInFlight];
-                ld_tile<DT>(v, in, base, lane, V);
-                uint32_t marks[kInFlight];
-#pragma unroll
-                for (int u = 0; u < kInFlight; ++u)
-                    marks[u] = marks_of<DT>(map, base - t0 * kTile + lane + u * 32);
-                if ((marks[0] | marks[1] | marks[2] | marks[3]) != 0) {
-#pragma unroll
-                    for (int u = 0; u < kInFlight; ++u)
-                        if (marks[u] != 0) v[u] = without<DT>(v[u], marks[u]);
-                }
-                uint32_t top = vec_max<DT>(v[0]);
-#pragma unroll
-                for (int u = 1; u < kInFlight; ++u) top = packed_max<DT>(top, vec_max<DT>(v[u]));
-                take<DT, false>(st, v, halves_max<DT>(top), c, step, low);
-            }
-        }
-        const RowSum mine = warp_join(st, 0, c);
-        if (lane == 0) {
-            part_m[warp] = mine.m;
-            part_s[warp] = mine.s;
-        }
-        if (C > 1) cluster_wait();
-        __syncthreads();
-        RowSum all{part_m[0], part_s[0], 0.f, 0};
-        for (int w = 1; w < warps; ++w) all = join(all, {part_m[w], part_s[w], 0.f, 0}, c);
-        if (C > 1) {
-            if (threadIdx.x < C) {
-                st_cluster(&from_m[rank], threadIdx.x, all.m);
-                st_cluster(&from_s[rank], threadIdx.x, all.s);
-            }
-            cluster_arrive();
-            cluster_wait();
-            all = {from_m[0], from_s[0], 0.f, 0};
-            for (int r = 1; r < C; ++r) all = join(all, {from_m[r], from_s[r], 0.f, 0}, c);
-        }
-        kind = finish_distill(t, a, row, all.m, all.s, rank == 0);
+    // Is there an entry, or a fault?
+    int any = 0;
+    for (int j = tid; j < a.k; j += blockDim.x) {
+        const int64_t at = static_cast<int64_t>(row) * a.k + j;
+        const float lp = a.logp[at];
+        any |= a.ids[at] != -1 || lp != lp || lp == inf();
     }
-    if (!has_grad) return;
-    const int32_t out_tiles = tiles_of(out.n);
-    if (kind != kRowGood) {
-        fill_tiles<DT>(out, first_tile, step_tiles, out_tiles, V, kind == kRowBad ? nan() : 0.f);
+    if (!__syncthreads_or(any)) {
+        if (piece == 0 && tid == 0) {
+            if (a.loss != nullptr) a.loss[row] = 0.f;
+            if (a.stats != nullptr) a.stats[row].kind = kRowSkipped;
+            if (a.status != nullptr) a.status[row] = 0;
+        }
         return;
     }
-    const float w = (a.weights == nullptr ? 1.f : a.weights[row]) * a.r.inv_t;
-    grad_tiles<DT, false>(in, out, first_tile, step_tiles, out_tiles, V, t.M, c, w * t.scale, 0.f);
-    __syncthreads();
-    // The entries in this block's turns.
-    for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
-        if (t.id[j] < 0) continue;
-        const int64_t tile = (static_cast<int64_t>(t.id[j]) + out.head) / (kPerVec<DT> * kTile);
-        if (tile / warps % C != rank) continue;
-        store_one<DT>(out.a0 + out.head * kElem<DT>, t.id[j],
-                      w * (t.listed * ex2((t.x[j] - t.listed_M) * c) - t.p[j]));
+    const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
+    const float step = 16.f / c, low = lowest_of<DT>(c);
+    const int32_t tiles = tiles_of(in.n);
+    const int32_t first = SPLIT ? piece * plan.piece : 0;
+    const int32_t end = SPLIT ? min(first + plan.piece, tiles) : tiles;
+    Running st;
+    start(st);
+    int32_t twice = 0;
+    for (int32_t t0 = first; t0 < end; t0 += kSpan) {
+        if (t0 > first) __syncthreads();
+        for (int i = tid; i < kBits / 32; i += blockDim.x) map[i] = 0u;
+        __syncthreads();
+        const int64_t begin = static_cast<int64_t>(t0) * kTile * kPerVec<DT> - in.head;
+        for (int j = tid; j < a.k; j += blockDim.x) {
+            const int32_t id = a.ids[static_cast<int64_t>(row) * a.k + j];
+            const int64_t at = id - begin;
+            if (id < 0 || id >= V || at < 0 || at >= kBits) continue;
+            const uint32_t was = atomicOr(&map[at >> 5], 1u << (at & 31));
+            twice |= was >> (at & 31) & 1;
+        }
+        __syncthreads();
+        const int32_t stop = min(t0 + kSpan, end);
+        for (int32_t tile = t0 + warp; tile < stop; tile += warps) {
+            uint4 v[kInFlight];
+            ld_tile<DT>(v, in, tile * kTile, lane, V);
+            uint32_t marks[kInFlight];
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u)
+                marks[u] = marks_of<DT>(map, (tile - t0) * kTile + lane + u * 32);
+            if ((marks[0] | marks[1] | marks[2] | marks[3]) != 0) {
+#pragma unroll
+                for (int u = 0; u < kInFlight; ++u)
+                    if (marks[u] != 0) v[u] = without<DT>(v[u], marks[u]);
+            }
+            uint32_t top = vec_max<DT>(v[0]);
+#pragma unroll
+            for (int u = 1; u < kInFlight; ++u) top = packed_max<DT>(top, vec_max<DT>(v[u]));
+            take<DT, false>(st, v, halves_max<DT>(top), c, step, low);
+        }
     }
+    const RowSum mine = warp_join(st, twice, c);
+    if (lane == 0) part[warp] = mine;
+    __syncthreads();
+    RowSum all = part[0];
+    for (int w = 1; w < warps; ++w) all = join(all, part[w], c);
+    if (SPLIT && !last_piece(plan.split, row, piece, plan.pieces, all, &flag)) return;
+    if (warp != 0) return;
+    if (SPLIT) all = join_pieces(plan.split, row, plan.pieces, c, lane);
+    Teacher t;
+    read_teacher<DT>(t, a, row, in.a0 + in.head * kElem<DT>, lane);
+    make_teacher(t, entries, a, lane, all.ahead != 0);
+    finish(t, a, row, all.m, all.s, lane);
 }
 
 template <int DT>
-cudaError_t launch(const DistillArgs& a, cudaStream_t s)
+DistillPlan plan_of(const Rows& r, int* warps)
 {
-    constexpr int64_t kBlocks = 304;               // two an SM
-    constexpr int64_t kPart = int64_t(280) << 10;  // a block's share: twice 152 of it fit in L2
-    const int64_t n = (a.r.V + kPerVec<DT> - 1) / kPerVec<DT> + 1;
-    const int64_t tiles = tiles_of(n);
+    DistillPlan p{};
+    const int32_t tiles = tiles_of((static_cast<int64_t>(r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
+    p.pieces = pieces_of(r.rows, tiles, kMaxWarps, &p.piece);
+    *warps = 1;
+    while (*warps < kMaxWarps && *warps < p.piece) *warps *= 2;
+    return p;
+}
+
+template <int DT>
+cudaError_t launch(const DistillArgs& a, void* workspace, cudaStream_t s)
+{
     int warps = 1;
-    while (warps * 32 < kMaxThreads && warps < tiles) warps *= 2;
-    int64_t C = 1;
-    while (C < kMaxCluster && a.r.rows * C * 2 < (int64_t(1) << 31) &&
-           (n * 16 / C > kPart || (a.r.rows * C < kBlocks && tiles > C * warps)))
-        C *= 2;
-    DistillPlan p;
-    p.cluster = static_cast<int32_t>(C);
-    const int64_t words = tiles * kTile * kPerVec<DT> / 32;
-    p.words = static_cast<int32_t>(words < kMapWords ? words : kMapWords);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.r.rows * C));
-    cfg.blockDim = dim3(warps * 32);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.words) * 4;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(C);
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = C > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, distill_kernel<DT>, a, p);
+    DistillPlan p = plan_of<DT>(a.r, &warps);
+    if (p.pieces > 1) p.split = split_of(workspace, a.r.rows, p.pieces);
+    const auto k = p.pieces > 1 ? distill_kernel<DT, true> : distill_kernel<DT, false>;
+    k<<<static_cast<unsigned>(static_cast<int64_t>(p.pieces) * a.r.rows), warps * 32, 0, s>>>(a, p);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_distill(const DistillArgs& a, int dtype, cudaStream_t s)
+size_t distill_workspace(const Rows& r, int dtype)
 {
-    return dtype == SV_F32 ? launch<SV_F32>(a, s) : dtype == SV_BF16 ? launch<SV_BF16>(a, s)
-                                                                      : launch<SV_F16>(a, s);
+    int warps;
+    const DistillPlan p = dtype == SV_F32 ? plan_of<SV_F32>(r, &warps) : plan_of<SV_BF16>(r, &warps);
+    return p.pieces > 1 ? split_bytes(r.rows, p.pieces, 0) : 0;
+}
+
+cudaError_t launch_distill(const DistillArgs& a, int dtype, void* workspace, cudaStream_t s)
+{
+    return dtype == SV_F32    ? launch<SV_F32>(a, workspace, s)
+           : dtype == SV_BF16 ? launch<SV_BF16>(a, workspace, s)
+                              : launch<SV_F16>(a, workspace, s);
 }
 
 }  // namespace svl

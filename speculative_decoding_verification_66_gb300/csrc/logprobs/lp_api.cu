@@ -2,9 +2,11 @@
 #include <cmath>
 
 #include "lp_internal.h"
+#include "lp_stream.cuh"
 
 #define SV_EXPORT extern "C" __attribute__((visibility("default")))
 
+static_assert(svl::kMaxSplitRows * 4 == SV_LOGPROBS_COUNTER_BYTES, "as the header says");
 static_assert(sizeof(svl::RowStats) == SV_ROW_STATS * sizeof(float), "as the header says");
 
 namespace {
@@ -17,7 +19,7 @@ bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 int element_size(int dtype) { return dtype == SV_F32 ? 4 : 2; }
 
 // Host checks of a description of rows, and the kernels' form of it.
-int check_rows(const sv_logit_rows* d, svl::Rows* r)
+int check_rows(const sv_logit_rows* d, svl::Rows* r, bool pointers = true)
 {
     if (d == nullptr) return SV_ERR_ARG;
     if (d->dtype != SV_F32 && d->dtype != SV_BF16 && d->dtype != SV_F16) return SV_ERR_DTYPE;
@@ -32,11 +34,11 @@ int check_rows(const sv_logit_rows* d, svl::Rows* r)
         return SV_ERR_ARG;
     const int64_t rows = d->outer * d->inner;
     const int es = element_size(d->dtype);
-    const int64_t so = d->outer <= 1 ? 0 : d->outer_stride;
-    const int64_t si = d->inner <= 1 ? 0 : d->inner_stride;
+    const int64_t so = d->outer <= 1 || !pointers ? 0 : d->outer_stride;
+    const int64_t si = d->inner <= 1 || !pointers ? 0 : d->inner_stride;
     if (so < 0 || si < 0 || so > kMaxStride || si > kMaxStride) return SV_ERR_ARG;
-    if (rows > 0 && d->logits == nullptr) return SV_ERR_ARG;
-    if (!aligned(d->logits, es)) return SV_ERR_ALIGN;
+    if (pointers && rows > 0 && d->logits == nullptr) return SV_ERR_ARG;
+    if (pointers && !aligned(d->logits, es)) return SV_ERR_ALIGN;
     r->x = {static_cast<uint8_t*>(const_cast<void*>(d->logits)), so * es, si * es};
     r->inner = static_cast<int32_t>(d->inner > 0 ? d->inner : 1);
     r->rows = static_cast<int32_t>(rows);
@@ -77,14 +79,49 @@ int check_teacher(const svl::Rows& r, const int32_t* ids, const float* logp, int
     return aligned(ids, 4) && aligned(logp, 4) ? SV_OK : SV_ERR_ALIGN;
 }
 
+size_t up(size_t n) { return (n + 255) & ~size_t(255); }
+
+bool enough(const void* workspace, size_t bytes, size_t need)
+{
+    return need == 0 || (workspace != nullptr && bytes >= need && aligned(workspace, 256));
+}
+
+// Where in a workspace the rows' statistics are: behind the pieces', and the counters in any
+// case, which other calls find 0.
+size_t stats_offset(const svl::Rows& r, int dtype)
+{
+    const size_t pieces = svl::distill_workspace(r, dtype);
+    return up(pieces > SV_LOGPROBS_COUNTER_BYTES ? pieces : SV_LOGPROBS_COUNTER_BYTES);
+}
+
+size_t distill_bytes(const svl::Rows& r, int dtype, bool grad)
+{
+    return grad ? stats_offset(r, dtype) + static_cast<size_t>(r.rows) * sizeof(svl::RowStats)
+                : svl::distill_workspace(r, dtype);
+}
+
 int done(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 
 }  // namespace
 
+SV_EXPORT int sv_logprobs_workspace_bytes(const sv_logit_rows* rows, int64_t top_k, size_t* bytes)
+{
+    svl::Rows r;
+    const int rc = check_rows(rows, &r, false);
+    if (rc != SV_OK) return rc;
+    if (bytes == nullptr || top_k < 0 || top_k > r.V) return SV_ERR_ARG;
+    if (top_k > SV_MAX_TOP || (top_k > 0 && r.V > SV_MAX_TOP_VOCAB)) return SV_ERR_SIZE;
+    const size_t a = svl::logprobs_workspace(r, rows->dtype, static_cast<int32_t>(top_k));
+    const size_t b = distill_bytes(r, rows->dtype, true);
+    *bytes = a > b ? a : b;
+    return SV_OK;
+}
+
 SV_EXPORT int sv_token_logprobs(const sv_logit_rows* rows, const int32_t* tokens, int64_t top_k,
                                 float* logprobs, float* entropy, float* lse, int32_t* rank,
                                 int32_t* top_tokens, float* top_logprobs, float* row_stats,
-                                int32_t* row_status, void* stream)
+                                int32_t* row_status, void* workspace, size_t workspace_bytes,
+                                void* stream)
 {
     svl::LogprobArgs a{};
     const int rc = check_rows(rows, &a.r);
@@ -103,6 +140,9 @@ SV_EXPORT int sv_token_logprobs(const sv_logit_rows* rows, const int32_t* tokens
         if (!aligned(p, 4)) return SV_ERR_ALIGN;
     if (!aligned(row_stats, 16)) return SV_ERR_ALIGN;
     if (a.r.rows == 0) return SV_OK;
+    if (!enough(workspace, workspace_bytes,
+                svl::logprobs_workspace(a.r, rows->dtype, static_cast<int32_t>(top_k))))
+        return SV_ERR_WORKSPACE;
     a.tokens = tokens;
     a.k = static_cast<int32_t>(top_k);
     a.logprobs = logprobs;
@@ -113,7 +153,7 @@ SV_EXPORT int sv_token_logprobs(const sv_logit_rows* rows, const int32_t* tokens
     a.top_logprobs = top_logprobs;
     a.stats = reinterpret_cast<svl::RowStats*>(row_stats);
     a.status = row_status;
-    return done(svl::launch_logprobs(a, rows->dtype, static_cast<cudaStream_t>(stream)));
+    return done(svl::launch_logprobs(a, rows->dtype, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 SV_EXPORT int sv_token_logprobs_backward(const sv_logit_rows* rows, const int32_t* tokens,
@@ -145,7 +185,7 @@ SV_EXPORT int sv_distill(const sv_logit_rows* rows, const int32_t* teacher_token
                          const float* teacher_logprobs, int64_t k, int tail, const float* weights,
                          float* loss, void* grad, int64_t grad_outer_stride,
                          int64_t grad_inner_stride, float* row_stats, int32_t* row_status,
-                         void* stream)
+                         void* workspace, size_t workspace_bytes, void* stream)
 {
     svl::DistillArgs a{};
     int rc = check_rows(rows, &a.r);
@@ -165,7 +205,15 @@ SV_EXPORT int sv_distill(const sv_logit_rows* rows, const int32_t* teacher_token
     a.loss = loss;
     a.stats = reinterpret_cast<svl::RowStats*>(row_stats);
     a.status = row_status;
-    return done(svl::launch_distill(a, rows->dtype, static_cast<cudaStream_t>(stream)));
+    if (!enough(workspace, workspace_bytes, distill_bytes(a.r, rows->dtype, grad != nullptr)))
+        return SV_ERR_WORKSPACE;
+    if (grad != nullptr && row_stats == nullptr)
+        a.stats = reinterpret_cast<svl::RowStats*>(static_cast<uint8_t*>(workspace) +
+                                                   stats_offset(a.r, rows->dtype));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int rc2 = done(svl::launch_distill(a, rows->dtype, workspace, s));
+    if (rc2 != SV_OK || grad == nullptr) return rc2;
+    return done(svl::launch_distill_grad(a, rows->dtype, s));
 }
 
 SV_EXPORT int sv_distill_backward(const sv_logit_rows* rows, const int32_t* teacher_tokens,

@@ -49,15 +49,19 @@ struct DistillArgs {
     int32_t bucket;
     const float* weights;
     float* loss;
-    RowAt grad;       // base NULL: no gradient
+    RowAt grad;
     RowStats* stats;
     int32_t* status;
 };
 
-cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, cudaStream_t s);
+// (bytes of workspace, 0: none is used)
+size_t logprobs_workspace(const Rows& r, int dtype, int32_t k);
+size_t distill_workspace(const Rows& r, int dtype);
+cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, void* workspace, cudaStream_t s);
 cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, int dtype, cudaStream_t s);
-cudaError_t launch_distill(const DistillArgs& a, int dtype, cudaStream_t s);
-// (a.weights: the loss's gradient)
+// (without the gradient)
+cudaError_t launch_distill(const DistillArgs& a, int dtype, void* workspace, cudaStream_t s);
+// (a.weights: the loss's gradient, NULL for ones)
 cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t s);
 
 }  // namespace svl

@@ -193,7 +193,7 @@ __device__ __forceinline__ void ld_tile(uint4 (&v)[kInFlight], const Vecs& in, i
 }
 
 // What is known of (a part of) a row: sums of 2^t and 2^t t with t = (x - m) c.
-struct RowSum {
+struct __align__(16) RowSum {
     float m;            // largest logit (NaN, +inf: a bad row; -inf: nothing else)
     float s, e;
     int32_t ahead;      // tokens ahead of the given one
@@ -221,8 +221,8 @@ __device__ __forceinline__ RowSum warp_join(const Running& st, int32_t ahead, fl
     unpack2(st.e, e0, e1);
     r.s = s0 + s1;
     r.e = e0 + e1;
-    if (r.s > 0.f)
-        rebase(r.s, r.e, static_cast<float>(reference(st, c) - static_cast<double>(r.m) * c));
+    if (r.s > 0.f)  // (o - m c, rounded once)
+        rebase(r.s, r.e, st.near ? fmaf(-r.m, c, st.o) : (st.r - r.m) * c);
     for (int off = 16; off > 0; off >>= 1) {
         r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, off);
         r.e += __shfl_xor_sync(0xFFFFFFFFu, r.e, off);
@@ -305,6 +305,88 @@ __device__ __forceinline__ void fill_tiles(const Vecs& out, int32_t first_tile, 
 __host__ __device__ __forceinline__ int32_t tiles_of(int64_t vectors)
 {
     return static_cast<int32_t>((vectors + kTile - 1) / kTile);
+}
+
+// Rows in pieces, a block each. What the pieces leave for one another lies in the workspace: a
+// counter a row, in a place of their own that other calls' workspaces have too, since the
+// counters are 0 between calls; then the pieces' sums; then the groups' maxima.
+constexpr int64_t kMaxSplitRows = 65536;   // more rows are enough blocks as they are
+constexpr int32_t kMostTurns = 32;         // of a piece: 64 KB
+constexpr int64_t kEnoughBlocks = 1216;    // eight an SM
+
+struct Split {
+    uint32_t* counters;
+    RowSum* sums;
+    float* maxima;
+};
+
+// Pieces of a row of so many turns, and their turns: 32 where that makes blocks enough, down to
+// one a warp where it does not.
+inline int32_t pieces_of(int64_t rows, int32_t tiles, int32_t warps, int32_t* piece)
+{
+    *piece = tiles;
+    if (rows > kMaxSplitRows || tiles <= warps) return 1;
+    int32_t most = kMostTurns;
+    while (most > warps && rows * ((tiles + most - 1) / most) < kEnoughBlocks) most /= 2;
+    const int32_t n = (tiles + most - 1) / most;
+    *piece = (tiles + n - 1) / n;               // evenly, in whole turns of all warps
+    *piece = (*piece + warps - 1) / warps * warps;
+    return (tiles + *piece - 1) / *piece;
+}
+
+inline size_t split_bytes(int64_t rows, int64_t pieces, int64_t groups)
+{
+    return kMaxSplitRows * 4 + static_cast<size_t>(rows) * pieces * sizeof(RowSum) +
+           static_cast<size_t>(rows) * groups * 4;
+}
+
+inline Split split_of(void* workspace, int64_t rows, int64_t pieces)
+{
+    Split s;
+    s.counters = static_cast<uint32_t*>(workspace);
+    s.sums = reinterpret_cast<RowSum*>(s.counters + kMaxSplitRows);
+    s.maxima = reinterpret_cast<float*>(s.sums + rows * pieces);
+    return s;
+}
+
+// Leaves a piece's sums (those of thread 0) and says whether all of the row's are there now;
+// everything that the block's threads wrote before is then visible to the block that is told so,
+// past the first-level cache.
+__device__ __forceinline__ bool last_piece(const Split& s, int32_t row, int32_t piece, int32_t pieces,
+                                           const RowSum& mine, uint32_t* shared)
+{
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __stcg(reinterpret_cast<float4*>(s.sums + static_cast<int64_t>(row) * pieces + piece),
+               make_float4(mine.m, mine.s, mine.e, __int_as_float(mine.ahead)));
+        __threadfence();
+        *shared = atomicInc(s.counters + row, pieces - 1) == static_cast<uint32_t>(pieces - 1);
+        __threadfence();
+    }
+    __syncthreads();
+    return *shared != 0;
+}
+
+// A row's sums from its pieces', in all threads; by each warp for itself, in one order.
+__device__ __forceinline__ RowSum join_pieces(const Split& s, int32_t row, int32_t pieces, float c,
+                                              int lane)
+{
+    RowSum r{-inf(), 0.f, 0.f, 0};
+    const float4* p = reinterpret_cast<const float4*>(s.sums + static_cast<int64_t>(row) * pieces);
+    for (int32_t i = lane; i < pieces; i += 32) {
+        const float4 f = __ldcg(p + i);
+        r = join(r, {f.x, f.y, f.z, __float_as_int(f.w)}, c);
+    }
+    const float m = warp_max(r.m);
+    if (r.s > 0.f) rebase(r.s, r.e, (r.m - m) * c);
+    r.m = m;
+    for (int off = 16; off > 0; off >>= 1) {
+        r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, off);
+        r.e += __shfl_xor_sync(0xFFFFFFFFu, r.e, off);
+        r.ahead += __shfl_xor_sync(0xFFFFFFFFu, r.ahead, off);
+    }
+    return r;
 }
 
 }  // namespace svl

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kMaxThreads)
         fill_tiles<DT>(out, pc.mine, pc.step, pc.end, V, st.kind == kRowBad ? nan() : 0.f);
         return;
     }
-    const float w = a.weights[row] * a.r.inv_t;
+    const float w = (a.weights == nullptr ? 1.f : a.weights[row]) * a.r.inv_t;
     // Entries in this piece. (The row is good: its tokens are in range.)
     int some = 0;
     for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
 }
 
-// A warp has up to two turns, in blocks of one to eight warps: short rows leave few threads
+// A warp has up to four turns, in blocks of one to eight warps: short rows leave few threads
 // idle, long ones are cut where a block's start no longer shows.
 template <typename Kernel, typename Args>
 cudaError_t launch(Kernel k, const Args& a, int per_vec, cudaStream_t s)
@@ -140,7 +140,7 @@ cudaError_t launch(Kernel k, const Args& a, int per_vec, cudaStream_t s)
     int warps = 1;
     while (warps * 32 < kMaxThreads && warps < tiles) warps *= 2;
     GradPlan g;
-    g.piece = warps * 2;
+    g.piece = warps * 4;
     int64_t pieces = (tiles + g.piece - 1) / g.piece;
     while (pieces * a.r.rows >= (int64_t(1) << 31)) {
         g.piece *= 2;

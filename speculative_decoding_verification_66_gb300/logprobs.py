@@ -16,7 +16,10 @@ is still alive; ``torch.autograd.grad`` and ``sv_distill`` need neither.)
 """
 from __future__ import annotations
 
+import ctypes
 import struct
+import threading
+from functools import lru_cache
 from typing import NamedTuple, Optional
 
 import torch
@@ -26,6 +29,7 @@ from .api import SV_BF16, SV_F32, _check
 from .attention import SV_F16, _on
 
 SV_MAX_TOP, SV_MAX_TOP_VOCAB, SV_ROW_STATS = 128, 1 << 20, 8
+SV_LOGPROBS_COUNTER_BYTES = 262144
 SV_TAIL_RENORMALISE, SV_TAIL_BUCKET = 0, 1
 
 _CODES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}
@@ -66,6 +70,54 @@ def _describe(logits, temperature):
         raise ValueError("logits must be contiguous along a vocabulary of at least one token")
     packed = _ROWS.pack(logits.data_ptr(), *_strides(logits), shape[-1], code, temperature)
     return packed, logits.device, shape[:-1]
+
+
+@lru_cache(maxsize=256)
+def _workspace_bytes(rows, V, code, top_k):
+    n = ctypes.c_size_t(0)
+    _check(_lib.load_logprobs().sv_logprobs_workspace_bytes(
+        _ROWS.pack(0, 1, rows, 0, 0, V, code, 1.0), top_k, ctypes.byref(n)),
+        "sv_logprobs_workspace_bytes")
+    return n.value
+
+
+def sv_logprobs_workspace_bytes(rows: int, V: int, dtype, top_k: int = 0) -> int:
+    """Workspace that ``sv_token_logprobs``, ``sv_distill`` and ``sv_distill_loss`` need for so many
+    rows, with up to ``top_k`` alternatives; 0 where none is used."""
+    if dtype not in _CODES:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {dtype}")
+    return _workspace_bytes(rows, V, _CODES[dtype], top_k)
+
+
+_kept = threading.local()
+
+
+def _workspace(given, logits, rows, top_k, stream):
+    """(address, bytes) of a workspace: the one given, or one that is kept for this thread's calls on
+    this stream, which the stream puts in order. A call that is being captured gets one of its own,
+    from the graph's pool: its replays may run beside anything."""
+    dev = logits.device
+    if given is not None:
+        if given.device != dev or given.dtype != torch.uint8 or not given.is_contiguous():
+            raise ValueError("workspace must be contiguous uint8 on the logits' device")
+        return given.data_ptr(), given.numel()
+    need = _workspace_bytes(rows, logits.shape[-1], _CODES[logits.dtype], top_k)
+    if need == 0:
+        return None, 0
+    if torch.cuda.is_current_stream_capturing():
+        w = _zeroed(need, dev)
+    else:
+        kept = _kept.__dict__
+        w = kept.get((dev.index, stream))
+        if w is None or w.numel() < need:
+            w = kept[(dev.index, stream)] = _zeroed(need, dev)
+    return w.data_ptr(), w.numel()
+
+
+def _zeroed(nbytes, dev):
+    w = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    w[:SV_LOGPROBS_COUNTER_BYTES].zero_()
+    return w
 
 
 def _per_row(x, name, shape, dtype, dev, last=()):
@@ -109,8 +161,9 @@ def _check_grad(grad, logits):
         raise ValueError("grad must be the logits themselves or lie apart from them")
 
 
-def _logprobs(described, logits, tokens, top_k, row_stats, row_status):
+def _logprobs(described, logits, tokens, top_k, row_stats, row_status, workspace):
     rows, dev, shape = described
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
     i32, f32 = torch.int32, torch.float32
     token_ptr = _per_row(tokens, "tokens", shape, i32, dev)
     stats_ptr = _per_row(row_stats, "row_stats", shape, f32, dev, (SV_ROW_STATS,))
@@ -133,18 +186,19 @@ def _logprobs(described, logits, tokens, top_k, row_stats, row_status):
     _check(_lib.load_logprobs().sv_token_logprobs(
         rows, token_ptr, top_k, ptr(logprobs), entropy.data_ptr(), lse.data_ptr(), ptr(rank),
         ptr(top_tokens), ptr(top_logprobs), stats_ptr, status_ptr,
-        torch._C._cuda_getCurrentRawStream(dev.index)), "sv_token_logprobs")
+        *_workspace(workspace, logits, shape.numel(), top_k, stream), stream), "sv_token_logprobs")
     return TokenLogprobs(logprobs, rank, entropy, lse, top_tokens, top_logprobs)
 
 
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, described, logits, tokens, temperature, top_k, row_stats, row_status, rest):
+    def forward(ctx, described, logits, tokens, temperature, top_k, row_stats, row_status, workspace,
+                rest):
         """The differentiable results; the others go to the list `rest`."""
         if row_stats is None:
             row_stats = torch.empty((*logits.shape[:-1], SV_ROW_STATS), dtype=torch.float32,
                                     device=logits.device)
-        out = _logprobs(described, logits, tokens, top_k, row_stats, row_status)
+        out = _logprobs(described, logits, tokens, top_k, row_stats, row_status, workspace)
         ctx.save_for_backward(logits, tokens, row_stats)
         ctx.temperature = temperature
         ctx.set_materialize_grads(False)
@@ -164,7 +218,7 @@ def _logprobs_backward(ctx, grad_logprobs, grad_entropy, grad_lse):
         grad_logprobs=None if grad_logprobs is None else grad_logprobs.contiguous(),
         grad_entropy=None if grad_entropy is None else grad_entropy.contiguous(),
         grad_lse=None if grad_lse is None else grad_lse.contiguous())
-    return None, grad, None, None, None, None, None, None
+    return None, grad, None, None, None, None, None, None, None
 
 
 # (refuses second derivatives; only where a graph of the backward pass is asked for, since it takes
@@ -173,7 +227,8 @@ _logprobs_backward_once = torch.autograd.function.once_differentiable(_logprobs_
 
 
 def sv_token_logprobs(logits, tokens=None, *, temperature: float = 1.0, top_k: int = 0,
-                      row_stats=None, row_status=None, stream=None) -> TokenLogprobs:
+                      row_stats=None, row_status=None, workspace=None,
+                      stream=None) -> TokenLogprobs:
     """Log probabilities of ``tokens`` (int32, one for each row) under softmax(logits / temperature),
     their ranks (how many tokens are ahead; ties go to the lower index), the rows' entropies and
     log-sum-exps, and with ``top_k`` the first tokens in order with their log probabilities.
@@ -183,18 +238,21 @@ def sv_token_logprobs(logits, tokens=None, *, temperature: float = 1.0, top_k: i
     ``tokens`` there are no log probabilities and ranks. ``row_status``: int32, receives SV_SEQ_BAD_TOKEN
     and SV_SEQ_NONFINITE for rows whose results are NaN. ``row_stats``: float32 [..., SV_ROW_STATS], receives
     what ``sv_token_logprobs_backward`` needs. Differentiable in the logits (logprobs, entropy and
-    lse). Asynchronous on ``stream`` (default: the current stream of the logits' device)."""
+    lse). A workspace is kept for the thread and stream unless one is given
+    (``sv_logprobs_workspace_bytes``, its first SV_LOGPROBS_COUNTER_BYTES zeros when it is new).
+    Asynchronous on ``stream`` (default: the current stream of the logits' device)."""
     described = _describe(logits, temperature)
 
     def call(_):
         if logits.requires_grad and torch.is_grad_enabled():
             rest = []
             logprobs, entropy, lse = _TokenLogprobs.apply(described, logits, tokens, temperature,
-                                                          top_k, row_stats, row_status, rest)
+                                                          top_k, row_stats, row_status, workspace,
+                                                          rest)
             return TokenLogprobs(logprobs, rest[0], entropy, lse, rest[1], rest[2])
-        return _logprobs(described, logits, tokens, top_k, row_stats, row_status)
+        return _logprobs(described, logits, tokens, top_k, row_stats, row_status, workspace)
 
-    return _on(logits.device, stream, call, (logits, tokens, row_stats, row_status))
+    return _on(logits.device, stream, call, (logits, tokens, row_stats, row_status, workspace))
 
 
 def sv_token_logprobs_backward(logits, row_stats, *, tokens=None, grad_logprobs=None,
@@ -237,10 +295,11 @@ def _teacher(teacher_tokens, teacher_logprobs, shape, dev, tail):
             _TAILS[tail])
 
 
-def _distill(described, teacher_tokens, teacher_logprobs, weights, tail, loss, grad, row_stats,
-             row_status):
+def _distill(described, logits, teacher_tokens, teacher_logprobs, weights, tail, loss, grad,
+             row_stats, row_status, workspace):
     """Calls sv_distill on the current stream; grad: a tensor or None."""
     rows, dev, shape = described
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
     teacher = _teacher(teacher_tokens, teacher_logprobs, shape, dev, tail)
     f32 = torch.float32
     weights_ptr = _per_row(weights, "weights", shape, f32, dev)
@@ -253,17 +312,17 @@ def _distill(described, teacher_tokens, teacher_logprobs, weights, tail, loss, g
         rows, *teacher, weights_ptr, *ptrs,
         _per_row(row_stats, "row_stats", shape, f32, dev, (SV_ROW_STATS,)),
         _per_row(row_status, "row_status", shape, torch.int32, dev),
-        torch._C._cuda_getCurrentRawStream(dev.index)), "sv_distill")
+        *_workspace(workspace, logits, shape.numel(), 0, stream), stream), "sv_distill")
     return loss
 
 
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, described, logits, teacher_tokens, teacher_logprobs, temperature, tail,
-                row_status):
+                row_status, workspace):
         row_stats = torch.empty((*logits.shape[:-1], SV_ROW_STATS), dtype=torch.float32, device=logits.device)
-        loss = _distill(described, teacher_tokens, teacher_logprobs, None, tail, None, None,
-                        row_stats, row_status)
+        loss = _distill(described, logits, teacher_tokens, teacher_logprobs, None, tail, None, None,
+                        row_stats, row_status, workspace)
         ctx.save_for_backward(logits, teacher_tokens, teacher_logprobs, row_stats)
         ctx.args = temperature, tail
         return loss
@@ -279,36 +338,38 @@ def _distill_backward(ctx, grad_loss):
     temperature, tail = ctx.args
     grad = sv_distill_backward(logits, teacher_tokens, teacher_logprobs, row_stats,
                                grad_loss.contiguous(), temperature=temperature, tail=tail)
-    return None, grad, None, None, None, None, None
+    return None, grad, None, None, None, None, None, None
 
 
 _distill_backward_once = torch.autograd.function.once_differentiable(_distill_backward)
 
 
 def sv_distill_loss(logits, teacher_tokens, teacher_logprobs, *, temperature: float = 1.0,
-                    tail: str = "renormalise", row_status=None, stream=None):
+                    tail: str = "renormalise", row_status=None, workspace=None, stream=None):
     """Divergence (float32, one for each row) of a teacher from softmax(logits / temperature),
     differentiable in the logits. The teacher's rows are k tokens (int32, -1 for none; a token given
     twice has both probabilities) and their log probabilities (float32): ``sv_token_logprobs``'
     ``top_tokens`` and ``top_logprobs``, at the same temperature. ``tail`` says what becomes of the
     probability that they leave: "renormalise" scales the k to sum 1 (their logits over the
     temperature do as well, then), "bucket" makes one outcome of all other tokens. Rows without a
-    teacher have loss 0 and are not read. ``row_status`` as in ``sv_token_logprobs``."""
+    teacher have loss 0 and are not read. ``row_status`` and ``workspace`` as in
+    ``sv_token_logprobs``."""
     described = _describe(logits, temperature)
 
     def call(_):
         if logits.requires_grad and torch.is_grad_enabled():
             return _DistillLoss.apply(described, logits, teacher_tokens, teacher_logprobs,
-                                      temperature, tail, row_status)
-        return _distill(described, teacher_tokens, teacher_logprobs, None, tail, None, None, None,
-                        row_status)
+                                      temperature, tail, row_status, workspace)
+        return _distill(described, logits, teacher_tokens, teacher_logprobs, None, tail, None, None,
+                        None, row_status, workspace)
 
-    return _on(logits.device, stream, call, (logits, teacher_tokens, teacher_logprobs, row_status))
+    return _on(logits.device, stream, call, (logits, teacher_tokens, teacher_logprobs, row_status,
+                                             workspace))
 
 
 def sv_distill(logits, teacher_tokens, teacher_logprobs, *, weights=None, temperature: float = 1.0,
                tail: str = "renormalise", loss=None, grad=None, row_stats=None, row_status=None,
-               stream=None):
+               workspace=None, stream=None):
     """``sv_distill_loss`` and its gradient at once: (loss, grad), grad being the logits' gradient of
     the sum of ``weights`` (float32, one for each row; default 1) times the losses. Rows are read
     once. Continue with ``logits.backward(grad)``, or with the head's products. ``grad`` may be the
@@ -321,11 +382,11 @@ def sv_distill(logits, teacher_tokens, teacher_logprobs, *, weights=None, temper
 
     def call(_):
         g = _grad_like(logits) if grad is None else grad
-        return _distill(described, teacher_tokens, teacher_logprobs, weights, tail, loss, g,
-                        row_stats, row_status), g
+        return _distill(described, logits, teacher_tokens, teacher_logprobs, weights, tail, loss, g,
+                        row_stats, row_status, workspace), g
 
     return _on(logits.device, stream, call, (logits, teacher_tokens, teacher_logprobs, weights, loss,
-                                             grad, row_stats, row_status))
+                                             grad, row_stats, row_status, workspace))
 
 
 def sv_distill_backward(logits, teacher_tokens, teacher_logprobs, row_stats, grad_loss, *,

@@ -1,5 +1,6 @@
 """libsvlogprobs without a GPU: it exports what include/sv_logprobs.h declares, its calls refuse bad
 arguments on the host before any CUDA call, and the plain forms that the GPU tests use are right."""
+import ctypes
 import math
 import os
 import re
@@ -14,7 +15,7 @@ import logprobs_util as u
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "sv_logprobs.h")
-SV_OK, ARG, DTYPE, ALIGN, SIZE = 0, -1, -2, -3, -6
+SV_OK, ARG, DTYPE, ALIGN, WORKSPACE, SIZE = 0, -1, -2, -3, -4, -6
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 
 
@@ -78,9 +79,9 @@ def rows(**kw):
 
 
 def logprobs(lib, r, tokens=P, k=5, logprobs=P, entropy=P, lse=P, rank=P, top=P, top_lp=P, stats=P,
-             status=P):
+             status=P, ws=P, ws_bytes=1 << 40):
     return lib.sv_token_logprobs(r, tokens, k, logprobs, entropy, lse, rank, top, top_lp, stats,
-                                 status, 0)
+                                 status, ws, ws_bytes, 0)
 
 
 def logprobs_grad(lib, r, tokens=P, stats=P, a=P, b=P, c=P, grad=P, so=300, si=100):
@@ -88,8 +89,9 @@ def logprobs_grad(lib, r, tokens=P, stats=P, a=P, b=P, c=P, grad=P, so=300, si=1
 
 
 def distill(lib, r, ids=P, lp=P, k=5, tail=0, weights=P, loss=P, grad=P, so=300, si=100, stats=P,
-            status=P):
-    return lib.sv_distill(r, ids, lp, k, tail, weights, loss, grad, so, si, stats, status, 0)
+            status=P, ws=P, ws_bytes=1 << 40):
+    return lib.sv_distill(r, ids, lp, k, tail, weights, loss, grad, so, si, stats, status, ws,
+                          ws_bytes, 0)
 
 
 def distill_grad(lib, r, ids=P, lp=P, k=5, tail=0, stats=P, up=P, grad=P, so=300, si=100):
@@ -115,9 +117,9 @@ def test_no_rows(lib):
     for call in CALLS:
         assert call(lib, None) == ARG
     for kw in (dict(outer=0), dict(inner=0), dict(outer=0, inner=0, logits=0)):
-        assert logprobs(lib, rows(**kw), 0, 5, 0, 0, 0, 0, 0, 0, 0, 0) == SV_OK
+        assert logprobs(lib, rows(**kw), 0, 5, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) == SV_OK
         assert logprobs_grad(lib, rows(**kw), 0, 0, 0, 0, 0, 0) == SV_OK
-        assert distill(lib, rows(**kw), 0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0) == SV_OK
+        assert distill(lib, rows(**kw), 0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) == SV_OK
         assert distill_grad(lib, rows(**kw), 0, 0, 1, 0, 0, 0, 0) == SV_OK
 
 
@@ -162,6 +164,30 @@ def test_bad_distillations(lib, kw, code):
 @pytest.mark.parametrize("kw,code", TEACHERS + GRADS + [(dict(up=0), ARG), (dict(up=P + 2), ALIGN)])
 def test_bad_distillation_gradients(lib, kw, code):
     assert distill_grad(lib, rows(), **kw) == code
+
+
+def workspace_bytes(lib, r, k=0):
+    n = ctypes.c_size_t(77)
+    rc = lib.sv_logprobs_workspace_bytes(r, k, ctypes.byref(n))
+    return n.value if rc == SV_OK else rc
+
+
+def test_workspaces(lib):
+    big = dict(vocab=128256, so=3 * 128256, si=128256, dtype=BF16)
+    need = workspace_bytes(lib, rows(**big), 20)
+    assert need > 262144  # (the counters)
+    assert workspace_bytes(lib, rows(logits=0, so=-5, si=-5, vocab=128256), 20) == need
+    assert 262144 <= workspace_bytes(lib, rows(vocab=5)) <= 262144 + 4096
+    assert lib.sv_logprobs_workspace_bytes(rows(), 0, None) == ARG
+    assert workspace_bytes(lib, None) == ARG and workspace_bytes(lib, rows(), -1) == ARG
+    assert workspace_bytes(lib, rows(), 101) == ARG and workspace_bytes(lib, rows(vocab=500), 129) == SIZE
+    for kw in (dict(ws=0), dict(ws=P + 16), dict(ws_bytes=1000), dict(ws_bytes=0)):
+        assert logprobs(lib, rows(**big), k=20, **kw) == WORKSPACE
+        assert distill(lib, rows(**big), so=3 * 128256, si=128256, **kw) == WORKSPACE
+    import speculative_decoding_verification_66_gb300 as sv
+    assert sv.sv_logprobs_workspace_bytes(6, 128256, torch.bfloat16, 20) == need
+    with pytest.raises(TypeError):
+        sv.sv_logprobs_workspace_bytes(6, 128256, torch.float64)
 
 
 def test_the_binding_refuses_host_tensors():
