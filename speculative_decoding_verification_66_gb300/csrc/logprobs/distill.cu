@@ -145,9 +145,11 @@ __device__ __forceinline__ double inverse(double x)
 //   listed = max(m, 1) / S                                  bucket
 //   scale  = (1 - P_o / q_o) 2^((M_o - M) c) / S = (m - q_e) / S_o     .. where m <= 1
 // so that the others' gradient keeps its digits however small their share is.
-__device__ __forceinline__ void finish(const Teacher& t, const DistillArgs& a, int32_t row, float M_o,
-                                       float S_o, int lane)
+__device__ __forceinline__ RowStats finish(const Teacher& t, const DistillArgs& a, int32_t row,
+                                           float M_o, float S_o, int lane)
 {
+    RowStats st{};
+    st.kind = kRowBad;
     const float c = a.r.c;
     float M = -inf();
 #pragma unroll
@@ -161,7 +163,7 @@ __device__ __forceinline__ void finish(const Teacher& t, const DistillArgs& a, i
             if (a.status != nullptr)
                 a.status[row] = t.status | (fabsf(M) < inf() ? 0 : SV_SEQ_NONFINITE);
         }
-        return;
+        return st;
     }
     double sum = 0.0;
 #pragma unroll
@@ -199,19 +201,21 @@ __device__ __forceinline__ void finish(const Teacher& t, const DistillArgs& a, i
                 : t.mass <= 1.0 ? static_cast<float>(t.mass - q_e) / S_o
                                 : listed * fall;
     }
+    // (M_o where nothing is finite: any finite number)
+    st = {S_o > 0.f ? M_o : 0.f,
+          scale,
+          0.f,
+          M,
+          listed,
+          t.shift,
+          static_cast<float>(over_mass),
+          kRowGood};
     if (lane == 0) {
         if (a.loss != nullptr) a.loss[row] = static_cast<float>(loss);
-        if (a.stats != nullptr)  // (M_o where nothing is finite: any finite number)
-            a.stats[row] = {S_o > 0.f ? M_o : 0.f,
-                            scale,
-                            0.f,
-                            M,
-                            listed,
-                            t.shift,
-                            static_cast<float>(over_mass),
-                            kRowGood};
+        if (a.stats != nullptr) a.stats[row] = st;
         if (a.status != nullptr) a.status[row] = 0;
     }
+    return st;
 }
 
 // -inf for the marked elements of a vector.
@@ -239,9 +243,9 @@ __device__ __forceinline__ uint32_t marks_of(const uint32_t* map, int32_t i)
     return DT == SV_F32 ? b[i >> 1] >> ((i & 1) * 4) & 15u : b[i];
 }
 
-// A piece of a row to a block. SPLIT: of several.
-template <int DT, bool SPLIT>
-__global__ void __launch_bounds__(kMaxWarps * 32, 10)
+// A piece of a row to a block. SPLIT: of several. GRAD: a whole row, and its gradient after it.
+template <int DT, bool SPLIT, bool GRAD>
+__global__ void __launch_bounds__(kMaxWarps * 32, 8)
     distill_kernel(const __grid_constant__ DistillArgs a, const __grid_constant__ DistillPlan plan)
 {
     constexpr int32_t kBits = kSpan * kTile * kPerVec<DT>;
@@ -249,6 +253,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 10)
     __shared__ RowSum part[kMaxWarps];
     __shared__ Entries entries;
     __shared__ uint32_t flag;
+    // (GRAD: in shared memory, so that the loops' registers are not laid out for it)
+    __shared__ Teacher teacher[GRAD ? 32 : 1];
+    __shared__ RowStats done;
     const int32_t row = SPLIT ? blockIdx.x / plan.pieces : blockIdx.x;
     const int32_t piece = SPLIT ? blockIdx.x - row * plan.pieces : 0, V = a.r.V;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
@@ -265,6 +272,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 10)
             if (a.loss != nullptr) a.loss[row] = 0.f;
             if (a.stats != nullptr) a.stats[row].kind = kRowSkipped;
             if (a.status != nullptr) a.status[row] = 0;
+        }
+        if (GRAD) {
+            const Vecs out = vectors_of<DT>(row_begin(a.grad, a.r.inner, row), V);
+            fill_tiles<DT>(out, warp, warps, tiles_of(out.n), V, 0.f);
         }
         return;
     }
@@ -308,39 +319,73 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 10)
             take<DT, false>(st, v, halves_max<DT>(top), c, step, low);
         }
     }
-    const RowSum mine = warp_join(st, twice, c);
-    if (lane == 0) part[warp] = mine;
-    __syncthreads();
-    RowSum all = part[0];
-    for (int w = 1; w < warps; ++w) all = join(all, part[w], c);
+    RowSum all = block_join(part, warp_join(st, twice, c), c);
     if (SPLIT && !last_piece(plan.split, row, piece, plan.pieces, all, &flag)) return;
+    if (!GRAD) {
+        if (warp != 0) return;
+        if (SPLIT) all = join_pieces(plan.split, row, plan.pieces, c, lane);
+        Teacher t;
+        read_teacher<DT>(t, a, row, in.a0 + in.head * kElem<DT>, lane);
+        make_teacher(t, entries, a, lane, all.ahead != 0);
+        finish(t, a, row, all.m, all.s, lane);
+        return;
+    }
+    Teacher& t = teacher[lane];
+    if (warp == 0) {
+        read_teacher<DT>(t, a, row, in.a0 + in.head * kElem<DT>, lane);
+        make_teacher(t, entries, a, lane, all.ahead != 0);
+        const RowStats st = finish(t, a, row, all.m, all.s, lane);
+        if (lane == 0) done = st;
+    }
+    __syncthreads();
+    const Vecs out = vectors_of<DT>(row_begin(a.grad, a.r.inner, row), V);
+    const float w = (a.weights == nullptr ? 1.f : a.weights[row]) * a.r.inv_t;
+    if (done.kind != kRowGood) {
+        fill_tiles<DT>(out, warp, warps, tiles_of(out.n), V, nan());
+        return;
+    }
+    grad_tiles<DT, false>(in, out, warp, warps, tiles_of(out.n), V, done.M, c, w * done.scale, 0.f);
+    __syncthreads();
     if (warp != 0) return;
-    if (SPLIT) all = join_pieces(plan.split, row, plan.pieces, c, lane);
-    Teacher t;
-    read_teacher<DT>(t, a, row, in.a0 + in.head * kElem<DT>, lane);
-    make_teacher(t, entries, a, lane, all.ahead != 0);
-    finish(t, a, row, all.m, all.s, lane);
+#pragma unroll
+    for (int q = 0; q < kEach; ++q)
+        if (t.id[q] >= 0)
+            store_one<DT>(out.a0 + out.head * kElem<DT>, t.id[q],
+                          w * (done.listed * ex2((t.x[q] - done.listed_M) * c) - t.p[q] * done.inv));
 }
 
+// Loss and gradient by one block a row, in one launch: rows of up to 64 KB, which are in L2 (and
+// half of them in the SM's own cache) when the block comes to them again, and as many as run at
+// a time are two thirds of L2.
+inline bool one_block(int32_t tiles, bool grad) { return grad && tiles <= 33; }
+
 template <int DT>
-DistillPlan plan_of(const Rows& r, int* warps)
+DistillPlan plan_of(const Rows& r, bool grad, int* warps)
 {
     DistillPlan p{};
     const int32_t tiles = tiles_of((static_cast<int64_t>(r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
-    p.pieces = pieces_of(r.rows, tiles, kMaxWarps, &p.piece);
+    p.pieces = 1;
+    p.piece = tiles;
+    if (!one_block(tiles, grad)) p.pieces = pieces_of(r.rows, tiles, kMaxWarps, &p.piece);
     *warps = 1;
     while (*warps < kMaxWarps && *warps < p.piece) *warps *= 2;
     return p;
 }
 
 template <int DT>
-cudaError_t launch(const DistillArgs& a, void* workspace, cudaStream_t s)
+cudaError_t launch(const DistillArgs& a, void* workspace, bool* all_done, cudaStream_t s)
 {
     int warps = 1;
-    DistillPlan p = plan_of<DT>(a.r, &warps);
+    const bool grad = a.grad.base != nullptr;
+    DistillPlan p = plan_of<DT>(a.r, grad, &warps);
     if (p.pieces > 1) p.split = split_of(workspace, a.r.rows, p.pieces);
-    const auto k = p.pieces > 1 ? distill_kernel<DT, true> : distill_kernel<DT, false>;
+    const int32_t tiles = tiles_of((static_cast<int64_t>(a.r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
+    const bool one = one_block(tiles, grad);
+    const auto k = one             ? distill_kernel<DT, false, true>
+                   : p.pieces > 1 ? distill_kernel<DT, true, false>
+                                  : distill_kernel<DT, false, false>;
     k<<<static_cast<unsigned>(static_cast<int64_t>(p.pieces) * a.r.rows), warps * 32, 0, s>>>(a, p);
+    *all_done = one || !grad;
     return cudaGetLastError();
 }
 
@@ -349,15 +394,17 @@ cudaError_t launch(const DistillArgs& a, void* workspace, cudaStream_t s)
 size_t distill_workspace(const Rows& r, int dtype)
 {
     int warps;
-    const DistillPlan p = dtype == SV_F32 ? plan_of<SV_F32>(r, &warps) : plan_of<SV_BF16>(r, &warps);
+    const DistillPlan p = dtype == SV_F32 ? plan_of<SV_F32>(r, false, &warps)
+                                          : plan_of<SV_BF16>(r, false, &warps);
     return p.pieces > 1 ? split_bytes(r.rows, p.pieces, 0) : 0;
 }
 
-cudaError_t launch_distill(const DistillArgs& a, int dtype, void* workspace, cudaStream_t s)
+cudaError_t launch_distill(const DistillArgs& a, int dtype, void* workspace, bool* all_done,
+                           cudaStream_t s)
 {
-    return dtype == SV_F32    ? launch<SV_F32>(a, workspace, s)
-           : dtype == SV_BF16 ? launch<SV_BF16>(a, workspace, s)
-                              : launch<SV_F16>(a, workspace, s);
+    return dtype == SV_F32    ? launch<SV_F32>(a, workspace, all_done, s)
+           : dtype == SV_BF16 ? launch<SV_BF16>(a, workspace, all_done, s)
+                              : launch<SV_F16>(a, workspace, all_done, s);
 }
 
 }  // namespace svl

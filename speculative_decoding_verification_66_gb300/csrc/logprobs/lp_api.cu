@@ -211,8 +211,9 @@ SV_EXPORT int sv_distill(const sv_logit_rows* rows, const int32_t* teacher_token
         a.stats = reinterpret_cast<svl::RowStats*>(static_cast<uint8_t*>(workspace) +
                                                    stats_offset(a.r, rows->dtype));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int rc2 = done(svl::launch_distill(a, rows->dtype, workspace, s));
-    if (rc2 != SV_OK || grad == nullptr) return rc2;
+    bool all_done = true;
+    rc = done(svl::launch_distill(a, rows->dtype, workspace, &all_done, s));
+    if (rc != SV_OK || all_done) return rc;
     return done(svl::launch_distill_grad(a, rows->dtype, s));
 }
 

@@ -49,7 +49,7 @@ struct DistillArgs {
     int32_t bucket;
     const float* weights;
     float* loss;
-    RowAt grad;
+    RowAt grad;       // base NULL: no gradient
     RowStats* stats;
     int32_t* status;
 };
@@ -59,8 +59,9 @@ size_t logprobs_workspace(const Rows& r, int dtype, int32_t k);
 size_t distill_workspace(const Rows& r, int dtype);
 cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, void* workspace, cudaStream_t s);
 cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, int dtype, cudaStream_t s);
-// (without the gradient)
-cudaError_t launch_distill(const DistillArgs& a, int dtype, void* workspace, cudaStream_t s);
+// (all_done: false if the gradient that is asked for has still to be launched)
+cudaError_t launch_distill(const DistillArgs& a, int dtype, void* workspace, bool* all_done,
+                           cudaStream_t s);
 // (a.weights: the loss's gradient, NULL for ones)
 cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t s);
 

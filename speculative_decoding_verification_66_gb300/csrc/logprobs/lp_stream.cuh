@@ -57,14 +57,15 @@ __device__ __forceinline__ void rebase(float& s, float& e, float d)
 
 static __device__ __noinline__ Running moved(Running st, float to, float c, float step, float low)
 {
-    const double before = reference(st, c);
-    const bool first = st.r == -inf();
+    const Running old = st;
     st.r = to;
     st.o = to * c;
     st.limit = to + step;
     st.near = fabsf(st.o) < kNear && (to - low) * c > 256.f;
-    if (!first) {
-        const float d = static_cast<float>(before - reference(st, c));
+    if (old.r != -inf()) {
+        const float d = old.near && st.near
+                            ? old.o - st.o
+                            : static_cast<float>(reference(old, c) - reference(st, c));
         float s0, s1, e0, e1;
         unpack2(st.s, s0, s1);
         unpack2(st.e, e0, e1);
@@ -211,7 +212,21 @@ __device__ __forceinline__ RowSum join(RowSum a, RowSum b, float c)
     return r;
 }
 
-// The sums of a warp's threads, in all lanes.
+// The sums of a warp's lanes, in all of them.
+__device__ __forceinline__ RowSum lanes_join(RowSum r, float c)
+{
+    const float m = warp_max(r.m);
+    if (r.s > 0.f) rebase(r.s, r.e, (r.m - m) * c);
+    r.m = m;
+    for (int off = 16; off > 0; off >>= 1) {
+        r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, off);
+        r.e += __shfl_xor_sync(0xFFFFFFFFu, r.e, off);
+    }
+    r.ahead = __reduce_add_sync(0xFFFFFFFFu, r.ahead);
+    return r;
+}
+
+// The same of their running sums.
 __device__ __forceinline__ RowSum warp_join(const Running& st, int32_t ahead, float c)
 {
     RowSum r;
@@ -311,7 +326,7 @@ __host__ __device__ __forceinline__ int32_t tiles_of(int64_t vectors)
 // counter a row, in a place of their own that other calls' workspaces have too, since the
 // counters are 0 between calls; then the pieces' sums; then the groups' maxima.
 constexpr int64_t kMaxSplitRows = 65536;   // more rows are enough blocks as they are
-constexpr int32_t kMostTurns = 32;         // of a piece: 64 KB
+constexpr int32_t kMostTurns = 32;         // of a bitmap of entries
 constexpr int64_t kEnoughBlocks = 1216;    // eight an SM
 
 struct Split {
@@ -320,16 +335,23 @@ struct Split {
     float* maxima;
 };
 
-// Pieces of a row of so many turns, and their turns: 32 where that makes blocks enough, down to
-// one a warp where it does not.
+// Pieces of a row of so many turns, and their turns. As many as make one wave of blocks, with two
+// turns a warp at least: more blocks than run at a time end in a wave that is not full, and a
+// block's beginning and end cost as much as three turns a warp. For 1024 rows of 128256
+// (bfloat16, without alternatives): one piece 52 us, two 62, four 56, eight 58; 544 rows: 41, 35,
+// 38, 38; 40 rows: 35, 23, 17, 15. Two where there are somewhat more long rows than blocks run
+// at a time, some of which may have nothing to do: 1280 rows with 20 alternatives, one piece 99,
+// two 87; 2304 rows 124 and 134; but 2000 rows of 64 KB 31 and 33.
 inline int32_t pieces_of(int64_t rows, int32_t tiles, int32_t warps, int32_t* piece)
 {
     *piece = tiles;
-    if (rows > kMaxSplitRows || tiles <= warps) return 1;
-    int32_t most = kMostTurns;
-    while (most > warps && rows * ((tiles + most - 1) / most) < kEnoughBlocks) most /= 2;
-    const int32_t n = (tiles + most - 1) / most;
-    *piece = (tiles + n - 1) / n;               // evenly, in whole turns of all warps
+    if (rows > kMaxSplitRows || rows == 0) return 1;
+    int64_t n = rows <= kEnoughBlocks                        ? kEnoughBlocks / rows
+                : rows < 4 * kEnoughBlocks && tiles >= 64 ? 2
+                                                          : 1;
+    if (n > tiles / (2 * warps)) n = tiles / (2 * warps);
+    if (n <= 1) return 1;
+    *piece = static_cast<int32_t>((tiles + n - 1) / n);  // evenly, in whole turns of all warps
     *piece = (*piece + warps - 1) / warps * warps;
     return (tiles + *piece - 1) / *piece;
 }
@@ -349,20 +371,38 @@ inline Split split_of(void* workspace, int64_t rows, int64_t pieces)
     return s;
 }
 
+// The sums of a block's warps, in the first warp's lanes (part: a place for each warp; `mine`:
+// in all lanes). Ends after a barrier.
+__device__ __forceinline__ RowSum block_join(RowSum* part, const RowSum& mine, float c)
+{
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) part[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    RowSum r{-inf(), 0.f, 0.f, 0};
+    if (threadIdx.x < 32) {
+        if (lane < warps) r = part[lane];
+        r = lanes_join(r, c);
+    }
+    return r;
+}
+
 // Leaves a piece's sums (those of thread 0) and says whether all of the row's are there now;
 // everything that the block's threads wrote before is then visible to the block that is told so,
 // past the first-level cache.
 __device__ __forceinline__ bool last_piece(const Split& s, int32_t row, int32_t piece, int32_t pieces,
                                            const RowSum& mine, uint32_t* shared)
 {
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
         __stcg(reinterpret_cast<float4*>(s.sums + static_cast<int64_t>(row) * pieces + piece),
                make_float4(mine.m, mine.s, mine.e, __int_as_float(mine.ahead)));
-        __threadfence();
-        *shared = atomicInc(s.counters + row, pieces - 1) == static_cast<uint32_t>(pieces - 1);
-        __threadfence();
+        // (releases what the barrier has shown this thread of the others' writes too)
+        uint32_t before;
+        asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                     : "=r"(before)
+                     : "l"(s.counters + row), "r"(static_cast<uint32_t>(pieces - 1))
+                     : "memory");
+        *shared = before == static_cast<uint32_t>(pieces - 1);
     }
     __syncthreads();
     return *shared != 0;
@@ -378,15 +418,7 @@ __device__ __forceinline__ RowSum join_pieces(const Split& s, int32_t row, int32
         const float4 f = __ldcg(p + i);
         r = join(r, {f.x, f.y, f.z, __float_as_int(f.w)}, c);
     }
-    const float m = warp_max(r.m);
-    if (r.s > 0.f) rebase(r.s, r.e, (r.m - m) * c);
-    r.m = m;
-    for (int off = 16; off > 0; off >>= 1) {
-        r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, off);
-        r.e += __shfl_xor_sync(0xFFFFFFFFu, r.e, off);
-        r.ahead += __shfl_xor_sync(0xFFFFFFFFu, r.ahead, off);
-    }
-    return r;
+    return lanes_join(r, c);
 }
 
 }  // namespace svl

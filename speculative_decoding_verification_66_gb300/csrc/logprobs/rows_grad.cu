@@ -28,11 +28,17 @@ struct Piece {
     int32_t mine, step;      // of the warp
 };
 
-__device__ __forceinline__ Piece my_piece(const GradPlan& g, int32_t row, int32_t vectors)
+// The last row first: the forward pass has read it last, and has left it in L2.
+__device__ __forceinline__ int32_t row_of(const GradPlan& g, int32_t rows)
+{
+    return rows - 1 - static_cast<int32_t>(blockIdx.x / g.pieces);
+}
+
+__device__ __forceinline__ Piece my_piece(const GradPlan& g, int32_t vectors)
 {
     Piece p;
     const int32_t tiles = tiles_of(vectors);
-    const int64_t first = static_cast<int64_t>(blockIdx.x - row * g.pieces) * g.piece;
+    const int64_t first = static_cast<int64_t>(blockIdx.x % g.pieces) * g.piece;
     p.first = static_cast<int32_t>(min(first, static_cast<int64_t>(tiles)));
     p.end = static_cast<int32_t>(min(first + g.piece, static_cast<int64_t>(tiles)));
     p.mine = p.first + (threadIdx.x >> 5);
@@ -44,10 +50,10 @@ template <int DT>
 __global__ void __launch_bounds__(kMaxThreads)
     logprobs_grad_kernel(const __grid_constant__ LogprobGradArgs a, const GradPlan plan)
 {
-    const int32_t row = blockIdx.x / plan.pieces, V = a.r.V;
+    const int32_t row = row_of(plan, a.r.rows), V = a.r.V;
     const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
     const Vecs out = vectors_of<DT>(row_begin(a.grad, a.r.inner, row), V);
-    const Piece pc = my_piece(plan, row, out.n);
+    const Piece pc = my_piece(plan, out.n);
     const RowStats st = a.stats[row];
     if (st.kind != kRowGood) {
         fill_tiles<DT>(out, pc.mine, pc.step, pc.end, V, st.kind == kRowBad ? nan() : 0.f);
@@ -88,10 +94,10 @@ __global__ void __launch_bounds__(kMaxThreads)
     __shared__ int32_t id[SV_MAX_TOP];
     __shared__ float logp[SV_MAX_TOP];
     __shared__ float own[SV_MAX_TOP];
-    const int32_t row = blockIdx.x / plan.pieces, V = a.r.V;
+    const int32_t row = row_of(plan, a.r.rows), V = a.r.V;
     const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
     const Vecs out = vectors_of<DT>(row_begin(a.grad, a.r.inner, row), V);
-    const Piece pc = my_piece(plan, row, out.n);
+    const Piece pc = my_piece(plan, out.n);
     const RowStats st = a.stats[row];
     if (st.kind != kRowGood) {
         fill_tiles<DT>(out, pc.mine, pc.step, pc.end, V, st.kind == kRowBad ? nan() : 0.f);

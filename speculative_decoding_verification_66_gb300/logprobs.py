@@ -161,7 +161,7 @@ def _check_grad(grad, logits):
         raise ValueError("grad must be the logits themselves or lie apart from them")
 
 
-def _logprobs(described, logits, tokens, top_k, row_stats, row_status, workspace):
+def _logprobs(described, logits, tokens, top_k, row_status, workspace, row_stats):
     rows, dev, shape = described
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
     i32, f32 = torch.int32, torch.float32
@@ -190,19 +190,33 @@ def _logprobs(described, logits, tokens, top_k, row_stats, row_status, workspace
     return TokenLogprobs(logprobs, rank, entropy, lse, top_tokens, top_logprobs)
 
 
+class _Call:
+    """What a differentiable call's backward pass needs beside the logits. (One object in place of
+    arguments and saved tensors: autograd takes its time for each of those. Inputs that were
+    changed in between are noticed here, as autograd notices it of the logits.)"""
+    __slots__ = ("described", "inputs", "versions", "row_stats", "results", "args")
+
+    def __init__(self, described, inputs, row_stats, args):
+        self.described, self.inputs = described, inputs
+        self.versions = [x._version for x in inputs]
+        self.row_stats, self.args, self.results = row_stats, args, None
+
+    def check(self):
+        if [x._version for x in self.inputs] != self.versions:
+            raise RuntimeError("an input of the forward call has been changed in place since")
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, described, logits, tokens, temperature, top_k, row_stats, row_status, workspace,
-                rest):
-        """The differentiable results; the others go to the list `rest`."""
-        if row_stats is None:
-            row_stats = torch.empty((*logits.shape[:-1], SV_ROW_STATS), dtype=torch.float32,
-                                    device=logits.device)
-        out = _logprobs(described, logits, tokens, top_k, row_stats, row_status, workspace)
-        ctx.save_for_backward(logits, tokens, row_stats)
-        ctx.temperature = temperature
+    def forward(ctx, logits, call):
+        """The differentiable results; the others are in call.results."""
+        if call.row_stats is None:
+            call.row_stats = torch.empty((*call.described[2], SV_ROW_STATS), dtype=torch.float32,
+                                         device=logits.device)
+        call.results = out = _logprobs(call.described, logits, *call.args, call.row_stats)
+        ctx.save_for_backward(logits)
+        ctx.call = call
         ctx.set_materialize_grads(False)
-        rest += (out.rank, out.top_tokens, out.top_logprobs)
         return out.logprobs, out.entropy, out.lse
 
     @staticmethod
@@ -212,13 +226,16 @@ class _TokenLogprobs(torch.autograd.Function):
 
 
 def _logprobs_backward(ctx, grad_logprobs, grad_entropy, grad_lse):
-    logits, tokens, row_stats = ctx.saved_tensors
-    grad = sv_token_logprobs_backward(
-        logits, row_stats, tokens=tokens, temperature=ctx.temperature,
-        grad_logprobs=None if grad_logprobs is None else grad_logprobs.contiguous(),
-        grad_entropy=None if grad_entropy is None else grad_entropy.contiguous(),
-        grad_lse=None if grad_lse is None else grad_lse.contiguous())
-    return None, grad, None, None, None, None, None, None, None
+    (logits,), call = ctx.saved_tensors, ctx.call
+    call.check()
+    rows, dev, _ = call.described
+    grads = [None if g is None else g.contiguous() for g in (grad_logprobs, grad_entropy, grad_lse)]
+    out = _grad_like(logits)
+    _check(_lib.load_logprobs().sv_token_logprobs_backward(
+        rows, call.inputs[0].data_ptr() if call.inputs else None, call.row_stats.data_ptr(),
+        *[None if g is None else g.data_ptr() for g in grads], out.data_ptr(), *_strides(out)[2:],
+        torch._C._cuda_getCurrentRawStream(dev.index)), "sv_token_logprobs_backward")
+    return out, None
 
 
 # (refuses second derivatives; only where a graph of the backward pass is asked for, since it takes
@@ -245,12 +262,13 @@ def sv_token_logprobs(logits, tokens=None, *, temperature: float = 1.0, top_k: i
 
     def call(_):
         if logits.requires_grad and torch.is_grad_enabled():
-            rest = []
-            logprobs, entropy, lse = _TokenLogprobs.apply(described, logits, tokens, temperature,
-                                                          top_k, row_stats, row_status, workspace,
-                                                          rest)
-            return TokenLogprobs(logprobs, rest[0], entropy, lse, rest[1], rest[2])
-        return _logprobs(described, logits, tokens, top_k, row_stats, row_status, workspace)
+            c = _Call(described, () if tokens is None else (tokens,), row_stats,
+                      (tokens, top_k, row_status, workspace))
+            logprobs, entropy, lse = _TokenLogprobs.apply(logits, c)
+            _, rank, _, _, top_tokens, top_logprobs = c.results
+            c.results = None
+            return TokenLogprobs(logprobs, rank, entropy, lse, top_tokens, top_logprobs)
+        return _logprobs(described, logits, tokens, top_k, row_status, workspace, row_stats)
 
     return _on(logits.device, stream, call, (logits, tokens, row_stats, row_status, workspace))
 
@@ -318,14 +336,14 @@ def _distill(described, logits, teacher_tokens, teacher_logprobs, weights, tail,
 
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, described, logits, teacher_tokens, teacher_logprobs, temperature, tail,
-                row_status, workspace):
-        row_stats = torch.empty((*logits.shape[:-1], SV_ROW_STATS), dtype=torch.float32, device=logits.device)
-        loss = _distill(described, logits, teacher_tokens, teacher_logprobs, None, tail, None, None,
-                        row_stats, row_status, workspace)
-        ctx.save_for_backward(logits, teacher_tokens, teacher_logprobs, row_stats)
-        ctx.args = temperature, tail
-        return loss
+    def forward(ctx, logits, call):
+        tail, row_status, workspace = call.args
+        call.row_stats = torch.empty((*call.described[2], SV_ROW_STATS), dtype=torch.float32,
+                                     device=logits.device)
+        ctx.save_for_backward(logits)
+        ctx.call = call
+        return _distill(call.described, logits, *call.inputs, None, tail, None, None, call.row_stats,
+                        row_status, workspace)
 
     @staticmethod
     def backward(ctx, grad_loss):
@@ -334,11 +352,16 @@ class _DistillLoss(torch.autograd.Function):
 
 
 def _distill_backward(ctx, grad_loss):
-    logits, teacher_tokens, teacher_logprobs, row_stats = ctx.saved_tensors
-    temperature, tail = ctx.args
-    grad = sv_distill_backward(logits, teacher_tokens, teacher_logprobs, row_stats,
-                               grad_loss.contiguous(), temperature=temperature, tail=tail)
-    return None, grad, None, None, None, None, None, None
+    (logits,), call = ctx.saved_tensors, ctx.call
+    call.check()
+    rows, dev, _ = call.described
+    tokens, logprobs = call.inputs
+    grad_loss, out = grad_loss.contiguous(), _grad_like(logits)
+    _check(_lib.load_logprobs().sv_distill_backward(
+        rows, tokens.data_ptr(), logprobs.data_ptr(), tokens.shape[-1], _TAILS[call.args[0]],
+        call.row_stats.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), *_strides(out)[2:],
+        torch._C._cuda_getCurrentRawStream(dev.index)), "sv_distill_backward")
+    return out, None
 
 
 _distill_backward_once = torch.autograd.function.once_differentiable(_distill_backward)
@@ -358,8 +381,8 @@ def sv_distill_loss(logits, teacher_tokens, teacher_logprobs, *, temperature: fl
 
     def call(_):
         if logits.requires_grad and torch.is_grad_enabled():
-            return _DistillLoss.apply(described, logits, teacher_tokens, teacher_logprobs,
-                                      temperature, tail, row_status, workspace)
+            return _DistillLoss.apply(logits, _Call(
+                described, (teacher_tokens, teacher_logprobs), None, (tail, row_status, workspace)))
         return _distill(described, logits, teacher_tokens, teacher_logprobs, None, tail, None, None,
                         None, row_status, workspace)
 
