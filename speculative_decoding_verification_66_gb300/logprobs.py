@@ -9,10 +9,11 @@ given or returned for each row has the logits' shape without V.
 ``sv_token_logprobs`` and ``sv_distill_loss`` are differentiable in the logits.
 ``sv_distill`` gives loss and gradient at once, in one pass over the logits, for
 training that calls ``logits.backward(grad)`` itself; the ``_backward`` calls are
-the gradients alone. Everything can be captured into a CUDA graph. (What torch
-asks of a captured backward pass holds: gradients that are accumulated into leaves
-need a warm-up on the capturing stream and no eager graph of the same leaves that
-is still alive; ``torch.autograd.grad`` and ``sv_distill`` need neither.)
+the gradients alone. All of these can be captured into a CUDA graph. Of a backward
+pass through autograd torch asks that no eager graph of the same leaf is alive when
+it is captured: that graph has bound the leaf to its own stream, and the capture ends
+in an error (``torch.autograd.grad`` included). ``sv_distill`` and the ``_backward``
+calls go without autograd, and are captured beside anything.
 """
 from __future__ import annotations
 

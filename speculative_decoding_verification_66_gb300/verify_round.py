@@ -9,7 +9,12 @@ states go to ``spec_verify_lmhead``. What is rejected is taken back by passing
 the shorter cached length to the next round: nothing is copied or cleared, and
 no length ever comes to the host.
 
-    python -m speculative_decoding_verification_66_gb300.verify_round --rounds 8
+With ``--logprobs`` every emitted token comes with its log probability
+(``sv_token_logprobs``); with ``--learn`` the draft model's head learns, after every
+round, from what the target thought of the positions that it verified: the
+target's top alternatives are the teacher of ``sv_distill``.
+
+    python -m speculative_decoding_verification_66_gb300.verify_round --rounds 8 --learn 0.5
 """
 from __future__ import annotations
 
@@ -20,6 +25,7 @@ import torch
 
 from .api import spec_verify_lmhead, sv_lmhead_logits
 from .attention import sv_chunk_attention, sv_kv_append, sv_kv_read
+from .logprobs import sv_distill, sv_token_logprobs
 
 
 class Model:
@@ -80,9 +86,33 @@ def ramp(batch, step, device):
     return torch.arange(0, batch * step + 1, step, dtype=torch.int32, device=device)
 
 
-def generate(target, draft, prompt, rounds, K, mode="greedy", temperature=1.0, seed=1):
+def learn_step(head, hidden, teacher_tokens, teacher_logprobs, rate, temperature=1.0, err=None):
+    """One step of a draft model's head [V, width] towards a teacher's top alternatives
+    [B, K, top] at the positions of its hidden states [B, K, width]; the unlisted tokens count as
+    one outcome. The head is changed in place, by ``rate`` times the gradient of the mean divergence.
+    Returns the divergences [B, K] before the step (0 where there is no teacher) and the gradient."""
+    B, K, width = hidden.shape
+    rows = hidden.reshape(B * K, width)
+    logits = sv_lmhead_logits(rows, head, err=err).view(B, K, -1)
+    taught = (teacher_tokens >= 0).any(-1)
+    weights = taught / taught.sum().clamp(min=1)
+    # (the logits are not needed again: their gradient takes their place)
+    loss, grad = sv_distill(logits, teacher_tokens, teacher_logprobs, weights=weights,
+                            temperature=temperature, tail="bucket", grad=logits)
+    step = grad.view(B * K, -1).t().to(head.dtype) @ rows
+    head.sub_(step, alpha=rate)
+    return loss, step
+
+
+def generate(target, draft, prompt, rounds, K, mode="greedy", temperature=1.0, seed=1, learn=0.0,
+             top=32, details=None):
     """Rounds of K drafts for prompt [B, L] (L >= 2). Returns the emitted tokens [rounds, B, K + 1]
-    (-1 where a round emitted fewer), the numbers of drafts kept [rounds, B] and the cached lengths."""
+    (-1 where a round emitted fewer), the numbers of drafts kept [rounds, B] and the cached lengths.
+
+    ``details``: a list that receives, for every round, a dict of the emitted tokens' ``logprobs``
+    [B, K + 1] (0 behind the last one) and, where the draft's head learns (at rate ``learn``, from
+    ``top`` alternatives of the target, up to the first position that was not kept), of its
+    divergences ``loss`` [B, K]."""
     B, L = prompt.shape
     dev = prompt.device
     g = torch.Generator(device=dev).manual_seed(seed)
@@ -95,7 +125,7 @@ def generate(target, draft, prompt, rounds, K, mode="greedy", temperature=1.0, s
     one, chunk = ramp(B, 1, dev), ramp(B, K + 1, dev)
     err = torch.zeros(1, dtype=torch.int32, device=dev)
     emitted, kept = [], []
-    for r in range(rounds):
+    for n in range(rounds):
         tokens, hidden = [last], []
         for i in range(K):
             h = draft.forward(tokens[-1], cached + i, one, 1)
@@ -114,7 +144,19 @@ def generate(target, draft, prompt, rounds, K, mode="greedy", temperature=1.0, s
         h = target.forward(tokens.reshape(-1), cached, chunk, K + 1).view(B, K + 1, -1)
         out, accepted = spec_verify_lmhead(
             h, target.head, torch.stack(hidden, 1).contiguous(), draft.head,
-            tokens[:, 1:].contiguous(), temperature, seed + r, mode)
+            tokens[:, 1:].contiguous(), temperature, seed + n, mode)
+        if learn or details is not None:
+            # Rows behind the last emitted token (-1) are not read, and teach nothing.
+            logits = sv_lmhead_logits(h.view(B * (K + 1), -1), target.head, err=err)
+            r = sv_token_logprobs(logits.view(B, K + 1, -1), out, temperature=temperature,
+                                  top_k=min(top, logits.shape[-1]) if learn else 0)
+            report = {"logprobs": r.logprobs}
+            if learn:
+                report["loss"], _ = learn_step(
+                    draft.head, torch.stack(hidden, 1), r.top_tokens[:, :K].contiguous(),
+                    r.top_logprobs[:, :K].contiguous(), learn, temperature, err)
+            if details is not None:
+                details.append(report)
         emitted.append(out)
         kept.append(accepted)
         last = out.gather(1, accepted.long()[:, None]).squeeze(1)
@@ -132,6 +174,8 @@ def main():
     ap.add_argument("--drafts", type=int, default=4)
     ap.add_argument("--mode", choices=("greedy", "sample"), default="sample")
     ap.add_argument("--cache", choices=("bf16", "e4m3"), default="e4m3")
+    ap.add_argument("--logprobs", action="store_true")
+    ap.add_argument("--learn", type=float, default=0.0, metavar="RATE")
     a = ap.parse_args()
     V, max_len = 32000, a.prompt + a.rounds * (a.drafts + 1) + 1
     e4m3 = a.cache == "e4m3"
@@ -140,8 +184,10 @@ def main():
     prompt = torch.randint(0, V, (a.batch, a.prompt), dtype=torch.int32, device="cuda")
     generate(target, draft, prompt, 1, a.drafts, a.mode)  # warm-up
     torch.cuda.synchronize()
+    details = [] if a.logprobs or a.learn else None
     t = time.perf_counter()
-    out, kept, cached = generate(target, draft, prompt, a.rounds, a.drafts, a.mode)
+    out, kept, cached = generate(target, draft, prompt, a.rounds, a.drafts, a.mode, learn=a.learn,
+                                 details=details)
     torch.cuda.synchronize()
     t = time.perf_counter() - t
     tokens = int((out >= 0).sum())
@@ -152,6 +198,14 @@ def main():
     print(f"{a.batch} sequences, {a.rounds} rounds of {a.drafts} drafts: {tokens} tokens in "
           f"{t * 1e3:.1f} ms, {float(kept.float().mean()):.2f} drafts kept a round; the first "
           f"layer's keys read back: {tuple(k.shape)}")
+
+    if details:
+        lp = torch.stack([d["logprobs"] for d in details])
+        print(f"mean log probability of an emitted token: {float(lp.sum()) / max(tokens, 1):.3f}")
+    if a.learn:
+        loss = [float(d["loss"].sum() / (d["loss"] != 0).sum().clamp(min=1)) for d in details]
+        print(f"divergence of the draft from the target: {loss[0]:.4f} in the first round, "
+              f"{loss[-1]:.4f} in the last")
 
 
 if __name__ == "__main__":

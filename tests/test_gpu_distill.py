@@ -344,3 +344,62 @@ def test_refusals():
         sv.sv_distill(big[:4], ids, lp, grad=big[1:])
     with pytest.raises(sv.SpecVerifyError):
         sv.sv_distill(x, ids, lp, temperature=0.0)
+
+
+@pytest.mark.parametrize("tail", TAILS)
+def test_certain_students_keep_finite_losses_and_gradients(tail):
+    """A logit 200 above all others: the others' probabilities are below float32's least, their
+    logarithms and (as one outcome) their shares of one another are not."""
+    V = 3001
+    x, ids, lp = teacher((3,), V, 5, 8, missing=0.0, none=0.0)
+    x[0, ids[0, 0].long()] = 200.0
+    x[1, ids[1, 4].long()] = 500.0
+    x[2, (ids[2, 0].long() + 1) % V] = 300.0     # (certain of a token that is not listed)
+    loss, g = both(x, ids, lp, 1.0, tail)
+    assert loss.isfinite().all() and (loss > 20).all()
+
+
+@pytest.mark.parametrize("tail", TAILS)
+@pytest.mark.parametrize("dtype,rows,V", [("bf16", 70000, 300), ("bf16", 5000, 40000),
+                                          ("fp16", 700, 70001), ("f32", 1300, 33001)])
+def test_many_rows(dtype, rows, V, tail):
+    x = torch.empty((rows, V), dtype=u.DTYPES[dtype], device="cuda")
+    ids = torch.empty((rows, 7), dtype=torch.int32, device="cuda")
+    lp = torch.empty((rows, 7), device="cuda")
+    step = max(1, 20_000_000 // V)
+    for n, i in enumerate(range(0, rows, step)):
+        s = slice(i, min(i + step, rows))
+        x[s], ids[s], lp[s] = teacher((s.stop - s.start,), V, 7, n)
+    loss, grad = sv.sv_distill(x, ids, lp, tail=tail)
+    y = x.detach().requires_grad_()
+    l2 = sv.sv_distill_loss(y, ids, lp, tail=tail)
+    g2, = torch.autograd.grad(l2.sum(), y)
+    for i in list(range(0, rows, step))[::4] + [max(0, rows - step)]:
+        s = slice(i, i + step)
+        check(x[s], ids[s], lp[s], 1.0, tail, loss[s], grad[s])
+        check(x[s], ids[s], lp[s], 1.0, tail, l2[s], g2[s])
+
+
+def test_entries_in_every_turn_and_twice_across_them():
+    """Entries at the ends of turns of 1024 elements, some tokens twice, at odd alignments."""
+    V = 70 * 1024 + 3
+    x, _, _ = teacher((4,), V, 1, 3)
+    at = torch.tensor([t + d for t in range(0, V - 1, 1200) for d in (0, 1)])[:110]
+    ids = at.repeat(4, 1).to(torch.int32).cuda()
+    ids[1, :55] = ids[1, 55:]
+    ids[2, 1::2] = ids[2, ::2]
+    lp = torch.full(ids.shape, -6.0, device="cuda") - torch.rand(ids.shape, device="cuda")
+    for dtype in ("bf16", "f32"):
+        room = torch.zeros(4, V + 9, dtype=u.DTYPES[dtype], device="cuda")
+        room[:, 3:V + 3] = x
+        for tail in TAILS:
+            both(room[:, 3:V + 3], ids, lp, 1.0, tail)
+
+
+def test_inputs_changed_before_the_backward_pass_are_noticed():
+    x, ids, lp = teacher((4,), 500, 5, 1)
+    x.requires_grad_()
+    loss = sv.sv_distill_loss(x, ids, lp)
+    lp.mul_(1.0)
+    with pytest.raises(RuntimeError):
+        loss.sum().backward()

@@ -358,3 +358,116 @@ def test_refusals():
                                                                  dtype=x.dtype).expand(4, 100))
     with pytest.raises(sv.SpecVerifyError):  # a gradient of log probabilities of no tokens
         sv.sv_token_logprobs_backward(x, stats, grad_logprobs=stats[:, 0].contiguous())
+
+
+@pytest.mark.parametrize("dtype,rows,V", [("bf16", 70000, 300), ("f32", 66000, 130), ("bf16", 5000, 40000),
+                                          ("fp16", 700, 70001), ("f32", 1300, 33001),
+                                          ("bf16", 2500, 66000)])
+def test_many_rows(dtype, rows, V):
+    """More rows than are cut into pieces, rows of more turns than one piece has, and rows in two."""
+    x = draw((rows, V), dtype, V)
+    tokens = draw_tokens((rows,), V)
+    status = torch.full((rows,), 77, dtype=torch.int32, device="cuda")
+    r = sv.sv_token_logprobs(x, tokens, temperature=0.9, top_k=11, row_status=status)
+    step = max(1, 20_000_000 // V)
+    for i in list(range(0, rows, step))[::4] + [rows - step]:
+        s = slice(max(i, 0), max(i, 0) + step)
+        part = sv.TokenLogprobs(*(t[s] for t in r))
+        u.check_logprobs(x[s], tokens[s], 0.9, 11, part, status[s])
+
+
+def test_tokens_around_turns_and_pieces():
+    """Tokens on both sides of every boundary of a turn of 1024 elements, tied with their
+    neighbours."""
+    V = 20 * 1024 + 5
+    row = (torch.arange(V) // 3 % 50).float()
+    tokens = torch.tensor([t + d for t in range(0, V, 1024) for d in (-1, 0, 1)][1:],
+                          dtype=torch.int32, device="cuda")
+    for offset in (0, 3):
+        base = torch.zeros(V + 8, device="cuda", dtype=torch.bfloat16)
+        base[offset:offset + V] = row
+        x = base[offset:offset + V].expand(len(tokens), V)
+        call(x, tokens, 1.0, 3)
+
+
+def test_a_given_workspace():
+    """Calls of different sizes share one; its counters are zeros between them."""
+    big, small = draw((40, 128256), "bf16"), draw((9, 20000), "f32")
+    n = max(sv.sv_logprobs_workspace_bytes(40, 128256, torch.bfloat16, 20),
+            sv.sv_logprobs_workspace_bytes(9, 20000, torch.float32, 20))
+    w = torch.full((n,), 123, dtype=torch.uint8, device="cuda")
+    w[:sv.SV_LOGPROBS_COUNTER_BYTES] = 0
+    for x in (big, small, big, small):
+        tokens = draw_tokens(x.shape[:1], x.shape[1])
+        r = sv.sv_token_logprobs(x, tokens, top_k=20, workspace=w)
+        u.check_logprobs(x, tokens, 1.0, 20, r)
+        assert (w[:sv.SV_LOGPROBS_COUNTER_BYTES] == 0).all()
+        ids = r.top_tokens.clone()
+        loss, grad = sv.sv_distill(x, ids, r.top_logprobs, tail="bucket", workspace=w)
+        assert loss.abs().max() < 1e-4
+        assert (w[:sv.SV_LOGPROBS_COUNTER_BYTES] == 0).all()
+    for bad in (w.float(), w.cpu(), w[::2]):
+        with pytest.raises(ValueError):
+            sv.sv_token_logprobs(big, workspace=bad)
+    with pytest.raises(sv.SpecVerifyError) as e:
+        sv.sv_token_logprobs(big, top_k=20, workspace=w[:1024])
+    assert e.value.code == -4
+
+
+def test_two_streams_and_two_graphs_at_once():
+    """Calls on two streams and replays of two graphs run beside one another; each has its own
+    workspace."""
+    xs = [draw((60, 128256), "bf16", s) for s in (1, 2)]
+    tokens = [draw_tokens((60,), 128256, s) for s in (3, 4)]
+    want = [sv.sv_token_logprobs(x, t, top_k=20) for x, t in zip(xs, tokens)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            got[i].append(sv.sv_token_logprobs(xs[i], tokens[i], top_k=20, stream=streams[i]))
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(sv.sv_token_logprobs(xs[i], tokens[i], top_k=20))
+        graphs.append(graph)
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i] + [outs[i]]:
+            for p, q in zip(want[i], r):
+                assert torch.equal(p, q)
+
+
+def test_a_captured_gradient_beside_an_eager_graph_of_the_same_leaf():
+    x = draw((20, 9001), "f32").requires_grad_()
+    tokens = draw_tokens((20,), 9001)
+    a = torch.randn(20, device="cuda")
+    alive = sv.sv_token_logprobs(x, tokens)
+    want, = torch.autograd.grad(alive.logprobs, x, a, retain_graph=True)
+    stats = torch.empty(20, sv.SV_ROW_STATS, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with torch.no_grad():
+            sv.sv_token_logprobs(x, tokens, row_stats=stats)
+            got = sv.sv_token_logprobs_backward(x.detach(), stats, tokens=tokens, grad_logprobs=a)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    again, = torch.autograd.grad(alive.logprobs, x, a)
+    assert torch.equal(again, want)
+
+
+def test_inputs_changed_before_the_backward_pass_are_noticed():
+    x = draw((3, 500), "f32").requires_grad_()
+    tokens = draw_tokens((3,), 500)
+    r = sv.sv_token_logprobs(x, tokens)
+    tokens.add_(0)
+    with pytest.raises(RuntimeError):
+        r.logprobs.sum().backward()
