@@ -354,9 +354,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 8)
                           w * (done.listed * ex2((t.x[q] - done.listed_M) * c) - t.p[q] * done.inv));
 }
 
-// Loss and gradient by one block a row, in one launch: rows of up to 64 KB, which are in L2 (and
-// half of them in the SM's own cache) when the block comes to them again, and as many as run at
-// a time are two thirds of L2.
+// Loss and gradient by one block a row, in one launch: rows of up to 64 KB, some of which are
+// still in L2 when the block comes to them again. 512, 2000 and 8192 rows of 32000 (bfloat16):
+// 31, 78 and 272 us; in two launches 37, 86 and 281. Rows of 50257: 45, 117 and (5000 rows) 272;
+// 49, 119 and 268. Of 128256, 512 and 2048 rows: 88 and 262; 82 and 264.
 inline bool one_block(int32_t tiles, bool grad) { return grad && tiles <= 33; }
 
 template <int DT>

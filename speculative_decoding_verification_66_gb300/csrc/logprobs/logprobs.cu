@@ -16,9 +16,8 @@
 // Should they be many (ties, or a sorted row), the same argument is applied once more, to
 // the vectors of 16 bytes in those groups, and leaves 8 k elements at most.
 //
-// A row is cut into pieces of up to 64 KB, a block each: many small blocks load the memory
-// evenly to the end, and one row alone is read by thirty SMs. A piece leaves its sums and its
-// groups' maxima in the workspace; the block that is the last of its row to do so (a counter a
+// Few rows are cut into pieces, a block each (pieces_of; one row of 128256 bfloat16 is read by
+// fifteen SMs). A piece leaves its sums and its groups' maxima in the workspace; the block that is the last of its row to do so (a counter a
 // row, which starts at 0 and is 0 again afterwards) finishes the row while others read on.
 // Pieces are joined in order, so that who is last makes no difference.
 //

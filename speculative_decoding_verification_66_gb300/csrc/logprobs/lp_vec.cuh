@@ -1,5 +1,5 @@
-// lp_vec.cuh -- rows as 16-byte vectors, packed arithmetic, and the pieces of
-// clusters that CUDA C++ does not name.
+// lp_vec.cuh -- rows as 16-byte vectors, and packed arithmetic that CUDA C++ does
+// not name.
 #pragma once
 
 #include "lp_common.cuh"
@@ -255,24 +255,6 @@ __device__ __forceinline__ float warp_max(float x)
     float r;
     asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
-}
-
-// Clusters: this block's place, the barrier over all of a cluster's threads (a hardware
-// barrier: blocks of a cluster run at the same time), and stores to another block's shared
-// memory.
-__device__ __forceinline__ void cluster_arrive()
-{
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait()
-{
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ void st_cluster(const void* local, uint32_t rank, float v)
-{
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(sv::smem_addr(local)), "r"(rank));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
 }  // namespace svl

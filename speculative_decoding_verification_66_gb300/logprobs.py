@@ -7,8 +7,7 @@ slice of positions or of a padded vocabulary is read where it lies). What is
 given or returned for each row has the logits' shape without V.
 
 ``sv_token_logprobs`` and ``sv_distill_loss`` are differentiable in the logits.
-``sv_distill`` gives loss and gradient at once, in one pass over the logits, for
-training that calls ``logits.backward(grad)`` itself; the ``_backward`` calls are
+``sv_distill`` gives loss and gradient at once, for training that calls ``logits.backward(grad)`` itself; the ``_backward`` calls are
 the gradients alone. All of these can be captured into a CUDA graph. Of a backward
 pass through autograd torch asks that no eager graph of the same leaf is alive when
 it is captured: that graph has bound the leaf to its own stream, and the capture ends
@@ -395,8 +394,7 @@ def sv_distill(logits, teacher_tokens, teacher_logprobs, *, weights=None, temper
                tail: str = "renormalise", loss=None, grad=None, row_stats=None, row_status=None,
                workspace=None, stream=None):
     """``sv_distill_loss`` and its gradient at once: (loss, grad), grad being the logits' gradient of
-    the sum of ``weights`` (float32, one for each row; default 1) times the losses. Rows are read
-    once. Continue with ``logits.backward(grad)``, or with the head's products. ``grad`` may be the
+    the sum of ``weights`` (float32, one for each row; default 1) times the losses. Continue with ``logits.backward(grad)``, or with the head's products. ``grad`` may be the
     logits themselves, whose values are then gone. Arguments otherwise as in
     ``sv_distill_loss``; ``row_stats`` (float32 [..., SV_ROW_STATS]) receives what ``sv_distill_backward``
     needs."""
