@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 8)
     const int32_t piece = SPLIT ? blockIdx.x - row * plan.pieces : 0, V = a.r.V;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const float c = a.r.c;
+    if (!GRAD) sv::pdl_trigger();   // (the gradient's blocks, if there are to be any, may be launched)
     // Is there an entry, or a fault?
     int any = 0;
     for (int j = tid; j < a.k; j += blockDim.x) {

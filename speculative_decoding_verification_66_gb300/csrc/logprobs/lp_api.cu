@@ -214,7 +214,7 @@ SV_EXPORT int sv_distill(const sv_logit_rows* rows, const int32_t* teacher_token
     bool all_done = true;
     rc = done(svl::launch_distill(a, rows->dtype, workspace, &all_done, s));
     if (rc != SV_OK || all_done) return rc;
-    return done(svl::launch_distill_grad(a, rows->dtype, s));
+    return done(svl::launch_distill_grad(a, rows->dtype, true, s));
 }
 
 SV_EXPORT int sv_distill_backward(const sv_logit_rows* rows, const int32_t* teacher_tokens,
@@ -237,5 +237,6 @@ SV_EXPORT int sv_distill_backward(const sv_logit_rows* rows, const int32_t* teac
     a.bucket = tail == SV_TAIL_BUCKET;
     a.weights = grad_loss;
     a.stats = reinterpret_cast<svl::RowStats*>(const_cast<float*>(row_stats));
-    return done(svl::launch_distill_grad(a, rows->dtype, static_cast<cudaStream_t>(stream)));
+    return done(
+        svl::launch_distill_grad(a, rows->dtype, false, static_cast<cudaStream_t>(stream)));
 }

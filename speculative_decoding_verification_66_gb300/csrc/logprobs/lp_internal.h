@@ -62,7 +62,8 @@ cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, int dtype, cudaStream
 // (all_done: false if the gradient that is asked for has still to be launched)
 cudaError_t launch_distill(const DistillArgs& a, int dtype, void* workspace, bool* all_done,
                            cudaStream_t s);
-// (a.weights: the loss's gradient, NULL for ones)
-cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t s);
+// (a.weights: the loss's gradient, NULL for ones; behind: launch_distill is just before it in the
+// stream)
+cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, bool behind, cudaStream_t s);
 
 }  // namespace svl

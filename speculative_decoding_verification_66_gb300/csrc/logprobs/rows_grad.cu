@@ -46,6 +46,14 @@ __device__ __forceinline__ Piece my_piece(const GradPlan& g, int32_t vectors)
     return p;
 }
 
+// (not through the read-only path: another kernel may still have been writing when this one began)
+__device__ __forceinline__ RowStats load_stats(const RowStats* p)
+{
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+    return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kMaxThreads)
     logprobs_grad_kernel(const __grid_constant__ LogprobGradArgs a, const GradPlan plan)
@@ -98,7 +106,8 @@ __global__ void __launch_bounds__(kMaxThreads)
     const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
     const Vecs out = vectors_of<DT>(row_begin(a.grad, a.r.inner, row), V);
     const Piece pc = my_piece(plan, out.n);
-    const RowStats st = a.stats[row];
+    sv::pdl_wait();   // (behind sv_distill's sums this kernel is launched before they end)
+    const RowStats st = load_stats(a.stats + row);
     if (st.kind != kRowGood) {
         fill_tiles<DT>(out, pc.mine, pc.step, pc.end, V, st.kind == kRowBad ? nan() : 0.f);
         return;
@@ -140,7 +149,7 @@ __global__ void __launch_bounds__(kMaxThreads)
 // A warp has up to four turns, in blocks of one to eight warps: short rows leave few threads
 // idle, long ones are cut where a block's start no longer shows.
 template <typename Kernel, typename Args>
-cudaError_t launch(Kernel k, const Args& a, int per_vec, cudaStream_t s)
+cudaError_t launch(Kernel k, const Args& a, int per_vec, cudaStream_t s, bool early = false)
 {
     const int64_t tiles = tiles_of((a.r.V + per_vec - 1) / per_vec + 1);
     int warps = 1;
@@ -153,8 +162,16 @@ cudaError_t launch(Kernel k, const Args& a, int per_vec, cudaStream_t s)
         pieces = (tiles + g.piece - 1) / g.piece;
     }
     g.pieces = static_cast<int32_t>(pieces);
-    k<<<static_cast<unsigned>(pieces * a.r.rows), warps * 32, 0, s>>>(a, g);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(pieces * a.r.rows));
+    cfg.blockDim = dim3(warps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, a, g);
 }
 
 }  // namespace
@@ -166,11 +183,11 @@ cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, int dtype, cudaStream
     return launch(logprobs_grad_kernel<SV_F16>, a, 8, s);
 }
 
-cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t s)
+cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, bool behind, cudaStream_t s)
 {
-    if (dtype == SV_F32) return launch(distill_grad_kernel<SV_F32>, a, 4, s);
-    if (dtype == SV_BF16) return launch(distill_grad_kernel<SV_BF16>, a, 8, s);
-    return launch(distill_grad_kernel<SV_F16>, a, 8, s);
+    if (dtype == SV_F32) return launch(distill_grad_kernel<SV_F32>, a, 4, s, behind);
+    if (dtype == SV_BF16) return launch(distill_grad_kernel<SV_BF16>, a, 8, s, behind);
+    return launch(distill_grad_kernel<SV_F16>, a, 8, s, behind);
 }
 
 }  // namespace svl
