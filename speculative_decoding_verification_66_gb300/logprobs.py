@@ -187,7 +187,21 @@ def _logprobs(described, logits, tokens, top_k, row_status, workspace, row_stats
         rows, token_ptr, top_k, ptr(logprobs), entropy.data_ptr(), lse.data_ptr(), ptr(rank),
         ptr(top_tokens), ptr(top_logprobs), stats_ptr, status_ptr,
         *_workspace(workspace, logits, shape.numel(), top_k, stream), stream), "sv_token_logprobs")
+    _wrote(row_stats)
     return TokenLogprobs(logprobs, rank, entropy, lse, top_tokens, top_logprobs)
+
+
+def _version(x):
+    """How often a tensor was changed in place (inference tensors do not tell)."""
+    return None if x.is_inference() else x._version
+
+
+def _wrote(*tensors):
+    """Tells autograd of a caller's tensors that a call has written, as torch's own calls do: a graph
+    that has saved one of them refuses its backward pass."""
+    for x in tensors:
+        if x is not None:
+            torch.autograd.graph.increment_version(x)
 
 
 class _Call:
@@ -198,12 +212,16 @@ class _Call:
 
     def __init__(self, described, inputs, row_stats, args):
         self.described, self.inputs = described, inputs
-        self.versions = [x._version for x in inputs]
         self.row_stats, self.args, self.results = row_stats, args, None
 
+    def begun(self):
+        """To be called when the forward call has written its results."""
+        self.versions = [_version(x) for x in (*self.inputs, self.row_stats)]
+
     def check(self):
-        if [x._version for x in self.inputs] != self.versions:
-            raise RuntimeError("an input of the forward call has been changed in place since")
+        if [_version(x) for x in (*self.inputs, self.row_stats)] != self.versions:
+            raise RuntimeError("an input or the row_stats of the forward call has been changed in "
+                               "place since")
 
 
 class _TokenLogprobs(torch.autograd.Function):
@@ -214,6 +232,7 @@ class _TokenLogprobs(torch.autograd.Function):
             call.row_stats = torch.empty((*call.described[2], SV_ROW_STATS), dtype=torch.float32,
                                          device=logits.device)
         call.results = out = _logprobs(call.described, logits, *call.args, call.row_stats)
+        call.begun()
         ctx.save_for_backward(logits)
         ctx.call = call
         ctx.set_materialize_grads(False)
@@ -293,6 +312,7 @@ def sv_token_logprobs_backward(logits, row_stats, *, tokens=None, grad_logprobs=
         g = _grad_like(logits) if grad is None else grad
         _check(_lib.load_logprobs().sv_token_logprobs_backward(
             rows, *ptrs, g.data_ptr(), *_strides(g)[2:], s), "sv_token_logprobs_backward")
+        _wrote(grad)
         return g
 
     return _on(dev, stream, call, (logits, row_stats, tokens, grad_logprobs, grad_entropy, grad_lse,
@@ -342,8 +362,10 @@ class _DistillLoss(torch.autograd.Function):
                                      device=logits.device)
         ctx.save_for_backward(logits)
         ctx.call = call
-        return _distill(call.described, logits, *call.inputs, None, tail, None, None, call.row_stats,
+        loss = _distill(call.described, logits, *call.inputs, None, tail, None, None, call.row_stats,
                         row_status, workspace)
+        call.begun()
+        return loss
 
     @staticmethod
     def backward(ctx, grad_loss):
@@ -394,18 +416,20 @@ def sv_distill(logits, teacher_tokens, teacher_logprobs, *, weights=None, temper
                tail: str = "renormalise", loss=None, grad=None, row_stats=None, row_status=None,
                workspace=None, stream=None):
     """``sv_distill_loss`` and its gradient at once: (loss, grad), grad being the logits' gradient of
-    the sum of ``weights`` (float32, one for each row; default 1) times the losses. Continue with ``logits.backward(grad)``, or with the head's products. ``grad`` may be the
-    logits themselves, whose values are then gone. Arguments otherwise as in
-    ``sv_distill_loss``; ``row_stats`` (float32 [..., SV_ROW_STATS]) receives what ``sv_distill_backward``
-    needs."""
+    the sum of ``weights`` (float32, one for each row; default 1) times the losses. Continue with
+    ``logits.backward(grad)``, or with the head's products. ``grad`` may be the logits themselves,
+    whose values are then gone. Arguments otherwise as in ``sv_distill_loss``; ``row_stats``
+    (float32 [..., SV_ROW_STATS]) receives what ``sv_distill_backward`` needs."""
     described = _describe(logits, temperature)
     if grad is not None:
         _check_grad(grad, logits)
 
     def call(_):
         g = _grad_like(logits) if grad is None else grad
-        return _distill(described, logits, teacher_tokens, teacher_logprobs, weights, tail, loss, g,
-                        row_stats, row_status, workspace), g
+        result = _distill(described, logits, teacher_tokens, teacher_logprobs, weights, tail, loss, g,
+                          row_stats, row_status, workspace)
+        _wrote(loss, grad, row_stats)
+        return result, g
 
     return _on(logits.device, stream, call, (logits, teacher_tokens, teacher_logprobs, weights, loss,
                                              grad, row_stats, row_status, workspace))
@@ -427,6 +451,7 @@ def sv_distill_backward(logits, teacher_tokens, teacher_logprobs, row_stats, gra
         g = _grad_like(logits) if grad is None else grad
         _check(_lib.load_logprobs().sv_distill_backward(
             rows, *teacher, *ptrs, g.data_ptr(), *_strides(g)[2:], s), "sv_distill_backward")
+        _wrote(grad)
         return g
 
     return _on(dev, stream, call, (logits, teacher_tokens, teacher_logprobs, row_stats, grad_loss,

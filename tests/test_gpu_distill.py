@@ -403,3 +403,25 @@ def test_inputs_changed_before_the_backward_pass_are_noticed():
     lp.mul_(1.0)
     with pytest.raises(RuntimeError):
         loss.sum().backward()
+
+
+def test_what_a_call_overwrites_is_noticed():
+    x, ids, lp = teacher((4,), 500, 5, 1)
+    y = x.requires_grad_() * 1.0
+    loss = sv.sv_distill_loss(y, ids, lp)
+    sv.sv_distill(y, ids, lp, grad=y)
+    with pytest.raises(RuntimeError):
+        loss.sum().backward()
+
+
+def test_a_teacher_made_in_inference_mode():
+    x, ids, lp = teacher((4,), 500, 5, 1)
+    x.requires_grad_()
+    with torch.inference_mode():
+        there = ids.clone(), lp.clone()
+    grads = []
+    for t in (there, (ids, lp)):
+        x.grad = None
+        sv.sv_distill_loss(x, *t).sum().backward()
+        grads.append(x.grad)
+    assert torch.equal(*grads)

@@ -471,3 +471,32 @@ def test_inputs_changed_before_the_backward_pass_are_noticed():
     tokens.add_(0)
     with pytest.raises(RuntimeError):
         r.logprobs.sum().backward()
+
+
+def test_what_a_call_overwrites_is_noticed():
+    x = draw((3, 500), "f32").requires_grad_()
+    tokens = draw_tokens((3,), 500)
+    stats = torch.empty(3, sv.SV_ROW_STATS, device="cuda")
+    r = sv.sv_token_logprobs(x, tokens, row_stats=stats)
+    sv.sv_token_logprobs(x.detach() * 2.0, tokens, row_stats=stats)
+    with pytest.raises(RuntimeError):
+        r.logprobs.sum().backward()
+    y = x * 1.0
+    r = sv.sv_token_logprobs(y, tokens, row_stats=stats)
+    sv.sv_token_logprobs_backward(y, stats, tokens=tokens, grad_lse=torch.ones(3, device="cuda"), grad=y)
+    with pytest.raises(RuntimeError):
+        r.logprobs.sum().backward()
+
+
+def test_tokens_made_in_inference_mode():
+    x = draw((3, 500), "f32").requires_grad_()
+    with torch.inference_mode():
+        tokens = draw_tokens((3,), 500, skip=0.0)
+        stats = torch.empty(3, sv.SV_ROW_STATS, device="cuda")
+        sv.sv_token_logprobs(x, tokens, row_stats=stats)
+    grads = []
+    for t, s in ((tokens, stats), (tokens.clone(), None)):
+        x.grad = None
+        sv.sv_token_logprobs(x, t, row_stats=s).logprobs.sum().backward()
+        grads.append(x.grad)
+    assert torch.equal(*grads)
