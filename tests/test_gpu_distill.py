@@ -425,3 +425,26 @@ def test_a_teacher_made_in_inference_mode():
         sv.sv_distill_loss(x, *t).sum().backward()
         grads.append(x.grad)
     assert torch.equal(*grads)
+
+
+@pytest.mark.parametrize("tail", TAILS)
+def test_long_rows_captured_and_replayed_without_a_pause(tail):
+    # (their gradient is a launch of its own, which begins before the sums' ends)
+    shape, V, k = (9,), 70001, 12
+    x, ids, lp = teacher(shape, V, k, 1)
+    graph = torch.cuda.CUDAGraph()
+    sv.sv_distill(x, ids, lp, tail=tail)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        loss, grad = sv.sv_distill(x, ids, lp, tail=tail)
+        l2, g2 = sv.sv_distill(grad, ids, lp, tail=tail)
+    inputs = [teacher(shape, V, k, seed) for seed in (5, 6, 7)]
+    torch.cuda.synchronize()
+    results = []
+    for y, i, p in inputs:
+        x.copy_(y), ids.copy_(i), lp.copy_(p)
+        graph.replay()
+        results.append([t.clone() for t in (loss, grad, l2, g2)])
+    for (y, i, p), (loss, grad, l2, g2) in zip(inputs, results):
+        check(y, i, p, 1.0, tail, loss, grad)
+        check(grad, i, p, 1.0, tail, l2, g2)
