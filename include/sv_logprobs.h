@@ -158,7 +158,7 @@ int sv_token_logprobs_backward(const sv_logit_rows* rows, const int32_t* tokens,
  *   loss        device float [rows], or NULL.
  *   grad        as in sv_token_logprobs_backward, or NULL.
  *   row_stats   device float [rows][SV_ROW_STATS], 16-byte aligned, or NULL.
- * One launch; one more for the gradient of rows over 64 KB (about), which are read again.
+ * One launch; one more for the gradient of long rows, which are read again.
  */
 int sv_distill(const sv_logit_rows* rows, const int32_t* teacher_tokens,
                const float* teacher_logprobs, int64_t k, int tail, const float* weights,

@@ -17,7 +17,6 @@
 namespace svl {
 namespace {
 
-constexpr int kMaxWarps = 4;
 // Turns that a block's bitmap of entries is for.
 constexpr int32_t kSpan = kMostTurns;
 
@@ -245,12 +244,12 @@ __device__ __forceinline__ uint32_t marks_of(const uint32_t* map, int32_t i)
 
 // A piece of a row to a block. SPLIT: of several. GRAD: a whole row, and its gradient after it.
 template <int DT, bool SPLIT, bool GRAD>
-__global__ void __launch_bounds__(kMaxWarps * 32, 8)
+__global__ void __launch_bounds__((GRAD ? kMostWarps : kLeastWarps) * 32, GRAD ? 2 : 8)
     distill_kernel(const __grid_constant__ DistillArgs a, const __grid_constant__ DistillPlan plan)
 {
     constexpr int32_t kBits = kSpan * kTile * kPerVec<DT>;
     __shared__ uint32_t map[kBits / 32];
-    __shared__ RowSum part[kMaxWarps];
+    __shared__ RowSum part[GRAD ? kMostWarps : kLeastWarps];
     __shared__ Entries entries;
     __shared__ uint32_t flag;
     // (GRAD: in shared memory, so that the loops' registers are not laid out for it)
@@ -355,11 +354,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 8)
                           w * (done.listed * ex2((t.x[q] - done.listed_M) * c) - t.p[q] * done.inv));
 }
 
-// Loss and gradient by one block a row, in one launch: rows of up to 64 KB, some of which are
-// still in L2 when the block comes to them again. 512, 2000 and 8192 rows of 32000 (bfloat16):
-// 31, 78 and 272 us; in two launches 37, 86 and 281. Rows of 50257: 45, 117 and (5000 rows) 272;
-// 49, 119 and 268. Of 128256, 512 and 2048 rows: 88 and 262; 82 and 264.
-inline bool one_block(int32_t tiles, bool grad) { return grad && tiles <= 33; }
+// Loss and gradient by one block a row, in one launch, where rows are short or make one wave of
+// blocks: what of them is still in L2 when the block comes to them again saves reads, and a
+// launch is saved. In two launches the few rows of a call are cut finer. us, one and two, bfloat16:
+//   rows              32        152       304       512       912        2000       8192
+//   32000 (64 KB)     14 / 21   16 / 23   20 / 29   27 / 33   41 / 43    78 / 82    272 / 281
+//   50257 (100 KB)    21 / 23   23 / 27   29 / 33   39 / 45   57 / 59    117 / 115
+//   128256            29 / 23   35 / 35   49 / 53   76 / 80   123 / 123  262 / 256
+// and float32 rows of 128256: 304 of them 84 / 87, 512 135 / 133. With 4, 8 and 16 warps a block,
+// of 32000: 32 rows 23, 18 and 14; 456 rows 31, 27 and 31; 912 rows 41, 45 and 47.
+inline bool one_block(int64_t rows, int32_t tiles, bool grad)
+{
+    if (!grad) return false;
+    return tiles <= 33 || (tiles <= 50 && rows * 4 <= kEnoughWarps) ||
+           (tiles <= 130 && rows * 32 >= kEnoughWarps && rows * 8 <= kEnoughWarps);
+}
 
 template <int DT>
 DistillPlan plan_of(const Rows& r, bool grad, int* warps)
@@ -368,9 +377,11 @@ DistillPlan plan_of(const Rows& r, bool grad, int* warps)
     const int32_t tiles = tiles_of((static_cast<int64_t>(r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
     p.pieces = 1;
     p.piece = tiles;
-    if (!one_block(tiles, grad)) p.pieces = pieces_of(r.rows, tiles, kMaxWarps, &p.piece);
+    const bool one = one_block(r.rows, tiles, grad);
+    if (!one) p.pieces = pieces_of(r.rows, tiles, kLeastWarps, &p.piece);
+    const int most = one ? warps_of(r.rows) : kLeastWarps;
     *warps = 1;
-    while (*warps < kMaxWarps && *warps < p.piece) *warps *= 2;
+    while (*warps < most && *warps < p.piece) *warps *= 2;
     return p;
 }
 
@@ -382,7 +393,7 @@ cudaError_t launch(const DistillArgs& a, void* workspace, bool* all_done, cudaSt
     DistillPlan p = plan_of<DT>(a.r, grad, &warps);
     if (p.pieces > 1) p.split = split_of(workspace, a.r.rows, p.pieces);
     const int32_t tiles = tiles_of((static_cast<int64_t>(a.r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
-    const bool one = one_block(tiles, grad);
+    const bool one = one_block(a.r.rows, tiles, grad);
     const auto k = one             ? distill_kernel<DT, false, true>
                    : p.pieces > 1 ? distill_kernel<DT, true, false>
                                   : distill_kernel<DT, false, false>;

@@ -28,8 +28,6 @@
 namespace svl {
 namespace {
 
-constexpr int kMaxWarps = 4;
-
 struct LogprobPlan {
     int32_t pieces;      // of a row, a block each
     int32_t piece;       // warps' turns in a piece
@@ -106,7 +104,7 @@ constexpr int kIdleBits = DT == SV_F32 ? 0 : DT == SV_BF16 ? 16 : 13;
 struct Choice {
     uint32_t bins[256];
     uint32_t digit, need;
-    int32_t over[kMaxWarps], ties[kMaxWarps];
+    int32_t over[kMostWarps], ties[kMostWarps];
 };
 
 // The k that come first of n ordered keys (larger first, then lower index; n > 0, no key is 0):
@@ -482,12 +480,12 @@ __device__ __forceinline__ void do_tile(Running& st, int32_t& ahead, const uint4
 
 // A piece of a row to a block. SPLIT: of several.
 template <int DT, bool TOP, bool SPLIT>
-__global__ void __launch_bounds__(kMaxWarps * 32, 8)
+__global__ void __launch_bounds__((TOP ? kMostWarps : kLeastWarps) * 32, TOP ? 2 : 8)
     logprobs_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__ LogprobPlan plan)
 {
     // Keys, then candidates.
     extern __shared__ __align__(16) uint32_t dynamic[];
-    __shared__ RowSum part[kMaxWarps];
+    __shared__ RowSum part[TOP ? kMostWarps : kLeastWarps];
     __shared__ Top top;
     const int32_t row = SPLIT ? blockIdx.x / plan.pieces : blockIdx.x;
     const int32_t piece = SPLIT ? blockIdx.x - row * plan.pieces : 0, V = a.r.V;
@@ -539,9 +537,13 @@ LogprobPlan plan_of(const Rows& r, int32_t k, int* warps)
 {
     LogprobPlan p{};
     const int32_t tiles = tiles_of((static_cast<int64_t>(r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
-    p.pieces = pieces_of(r.rows, tiles, kMaxWarps, &p.piece);
+    // (alternatives, 128 of 128256 bfloat16: with 4, 8 and 16 warps 40 rows 29, 23 and 21 us, 304 rows
+    // 49, 39 and 33, 608 rows 66, 49 and 74, 912 rows 72, 88 and 100; 20 of them 20, 18, 18, 31, 31,
+    // 29, 45, 41, 66, 57, 72, 89; none 12, 12, 14, 23, 24, 23, 37, 35, 47, 49, 55, 64)
+    const int most = k > 0 ? warps_of(r.rows) : kLeastWarps;
+    p.pieces = pieces_of(r.rows, tiles, most, &p.piece);
     *warps = 1;
-    while (*warps < kMaxWarps && *warps < p.piece) *warps *= 2;
+    while (*warps < most && *warps < p.piece) *warps *= 2;
     p.groups = tiles * kInFlight;
     const int32_t vectors = 32 * (k < p.groups ? k : p.groups);
     p.keys = p.groups > vectors ? p.groups : vectors;

@@ -111,9 +111,13 @@ SV_EXPORT int sv_logprobs_workspace_bytes(const sv_logit_rows* rows, int64_t top
     if (rc != SV_OK) return rc;
     if (bytes == nullptr || top_k < 0 || top_k > r.V) return SV_ERR_ARG;
     if (top_k > SV_MAX_TOP || (top_k > 0 && r.V > SV_MAX_TOP_VOCAB)) return SV_ERR_SIZE;
-    const size_t a = svl::logprobs_workspace(r, rows->dtype, static_cast<int32_t>(top_k));
-    const size_t b = distill_bytes(r, rows->dtype, true);
-    *bytes = a > b ? a : b;
+    // (calls with fewer alternatives, or none, may cut rows into more pieces)
+    size_t most = distill_bytes(r, rows->dtype, true);
+    for (const int64_t k : {top_k, int64_t(0)}) {
+        const size_t n = svl::logprobs_workspace(r, rows->dtype, static_cast<int32_t>(k));
+        most = n > most ? n : most;
+    }
+    *bytes = most;
     return SV_OK;
 }
 

@@ -327,13 +327,23 @@ __host__ __device__ __forceinline__ int32_t tiles_of(int64_t vectors)
 // counters are 0 between calls; then the pieces' sums; then the groups' maxima.
 constexpr int64_t kMaxSplitRows = 65536;   // more rows are enough blocks as they are
 constexpr int32_t kMostTurns = 32;         // of a bitmap of entries
-constexpr int64_t kEnoughBlocks = 1216;    // eight an SM
+constexpr int64_t kEnoughWarps = 4864;     // 32 an SM
 
 struct Split {
     uint32_t* counters;
     RowSum* sums;
     float* maxima;
 };
+
+// Warps of a block that has much to do after its sums: 4, or up to 16 where that makes no more of
+// them than run at a time, 32 an SM.
+constexpr int kLeastWarps = 4, kMostWarps = 16;
+inline int warps_of(int64_t rows)
+{
+    int warps = kMostWarps;
+    while (warps > kLeastWarps && warps * rows > kEnoughWarps) warps /= 2;
+    return warps;
+}
 
 // Pieces of a row of so many turns, and their turns. As many as make one wave of blocks, with two
 // turns a warp at least: more blocks than run at a time end in a wave that is not full, and a
@@ -346,9 +356,10 @@ inline int32_t pieces_of(int64_t rows, int32_t tiles, int32_t warps, int32_t* pi
 {
     *piece = tiles;
     if (rows > kMaxSplitRows || rows == 0) return 1;
-    int64_t n = rows <= kEnoughBlocks                        ? kEnoughBlocks / rows
-                : rows < 4 * kEnoughBlocks && tiles >= 64 ? 2
-                                                          : 1;
+    const int64_t blocks = kEnoughWarps / warps;
+    int64_t n = rows <= blocks                        ? blocks / rows
+                : rows < 4 * blocks && tiles >= 64 ? 2
+                                                   : 1;
     if (n > tiles / (2 * warps)) n = tiles / (2 * warps);
     if (n <= 1) return 1;
     *piece = static_cast<int32_t>((tiles + n - 1) / n);  // evenly, in whole turns of all warps
