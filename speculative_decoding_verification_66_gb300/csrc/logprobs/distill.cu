@@ -11,6 +11,9 @@
 // the teacher into its lanes' registers and finds the row's few logarithms; a duplicate token
 // shows by its mark being there already, and only then the entries are compared with one
 // another.
+//
+// Bound by memory: the loss of 1024 rows of 128256 bfloat16 takes 54 us (4.9 TB/s), of 4096
+// rows 191 (5.5 TB/s).
 #include "lp_finish.cuh"
 #include "lp_stream.cuh"
 

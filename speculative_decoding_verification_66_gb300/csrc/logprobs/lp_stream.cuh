@@ -350,8 +350,9 @@ inline int warps_of(int64_t rows)
 // block's beginning and end cost as much as three turns a warp. For 1024 rows of 128256
 // (bfloat16, without alternatives): one piece 52 us, two 62, four 56, eight 58; 544 rows: 41, 35,
 // 38, 38; 40 rows: 35, 23, 17, 15. Two where there are somewhat more long rows than blocks run
-// at a time, some of which may have nothing to do: 1280 rows with 20 alternatives, one piece 99,
-// two 87; 2304 rows 124 and 134; but 2000 rows of 64 KB 31 and 33.
+// at a time, some of which may have nothing to do: 2304 rows with 20 alternatives, half of the rows
+// empty, one piece 96, two 86 (blocks of two warps 106); 1280 full rows 99 and 87; but 2304 full
+// ones 125 and 135, and 2000 rows of 64 KB 31 and 33.
 inline int32_t pieces_of(int64_t rows, int32_t tiles, int32_t warps, int32_t* piece)
 {
     *piece = tiles;
