@@ -448,3 +448,28 @@ def test_long_rows_captured_and_replayed_without_a_pause(tail):
     for (y, i, p), (loss, grad, l2, g2) in zip(inputs, results):
         check(y, i, p, 1.0, tail, loss, grad)
         check(grad, i, p, 1.0, tail, l2, g2)
+
+
+@pytest.mark.parametrize("tail", TAILS)
+@pytest.mark.parametrize("dtype,rows,V", [("bf16", 40, 50257), ("bf16", 153, 33000), ("bf16", 300, 100003),
+                                          ("fp16", 305, 131001), ("f32", 608, 66001), ("f32", 609, 60001)])
+def test_a_row_to_a_block_of_any_size(dtype, rows, V, tail):
+    """Loss and gradient by blocks of 4 to 16 warps, whose bitmaps are filled several times; rows at
+    odd alignments, tokens twice."""
+    room = torch.zeros((rows, V + 5), dtype=u.DTYPES[dtype], device="cuda")
+    x, out = room[:, 1:V + 1], torch.full_like(room, 7.0)
+    ids = torch.empty((rows, 40), dtype=torch.int32, device="cuda")
+    lp = torch.empty((rows, 40), device="cuda")
+    step = max(1, 20_000_000 // V)
+    for n, i in enumerate(range(0, rows, step)):
+        s = slice(i, min(i + step, rows))
+        x[s], ids[s], lp[s] = teacher((s.stop - s.start,), V, 40, n)
+    ids[::5, 20:] = ids[::5, :20]
+    ids[3::50, 0] = V
+    status = torch.full((rows,), 55, dtype=torch.int32, device="cuda")
+    w = torch.rand(rows, device="cuda")
+    loss, grad = sv.sv_distill(x, ids, lp, weights=w, tail=tail, row_status=status, grad=out[:, 1:V + 1])
+    for i in range(0, rows, step):
+        s = slice(i, min(i + step, rows))
+        check(x[s], ids[s], lp[s], 1.0, tail, loss[s], grad[s], w[s], status[s])
+    assert (out[:, 0] == 7.0).all() and (out[:, V + 1:] == 7.0).all()

@@ -500,3 +500,16 @@ def test_tokens_made_in_inference_mode():
         sv.sv_token_logprobs(x, t, row_stats=s).logprobs.sum().backward()
         grads.append(x.grad)
     assert torch.equal(*grads)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [21, 304, 305, 608, 609])
+def test_alternatives_by_blocks_of_any_size(dtype, rows):
+    """Many and few alternatives by blocks of 4 to 16 warps; rows of ties among the others."""
+    V = 50001
+    x = draw((rows, V), dtype, rows)
+    x[::7] = (x[::7] * 2).round()
+    x[5::50, 100:] = -math.inf
+    tokens = draw_tokens((rows,), V)
+    for k in (3, 128):
+        call(x, tokens, 0.9, k)
