@@ -13,7 +13,7 @@
 // another.
 //
 // Bound by memory: the loss of 1024 rows of 128256 bfloat16 takes 54 us (4.9 TB/s), of 4096
-// rows 191 (5.5 TB/s).
+// rows 179 (5.9 TB/s).
 #include "lp_finish.cuh"
 #include "lp_stream.cuh"
 
@@ -24,9 +24,8 @@ namespace {
 constexpr int32_t kSpan = kMostTurns;
 
 struct DistillPlan {
-    int32_t pieces;      // of a row, a block each
-    int32_t piece;       // warps' turns in a piece
-    Split split;         // with more than one piece
+    Cut cut;
+    Split split;         // where rows are cut
 };
 
 // The teacher in its warp: entry lane + 32 q is the lane's q-th.
@@ -258,8 +257,7 @@ __global__ void __launch_bounds__((GRAD ? kMostWarps : kLeastWarps) * 32, GRAD ?
     // (GRAD: in shared memory, so that the loops' registers are not laid out for it)
     __shared__ Teacher teacher[GRAD ? 32 : 1];
     __shared__ RowStats done;
-    const int32_t row = SPLIT ? blockIdx.x / plan.pieces : blockIdx.x;
-    const int32_t piece = SPLIT ? blockIdx.x - row * plan.pieces : 0, V = a.r.V;
+    const int32_t row = SPLIT ? row_of(plan.cut, blockIdx.x) : blockIdx.x, V = a.r.V;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const float c = a.r.c;
     if (!GRAD) sv::pdl_trigger();   // (the gradient's blocks, if there are to be any, may be launched)
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__((GRAD ? kMostWarps : kLeastWarps) * 32, GRAD ?
         any |= a.ids[at] != -1 || lp != lp || lp == inf();
     }
     if (!__syncthreads_or(any)) {
-        if (piece == 0 && tid == 0) {
+        if (tid == 0 && (!SPLIT || part_of(plan.cut, blockIdx.x, row, 0).piece == 0)) {
             if (a.loss != nullptr) a.loss[row] = 0.f;
             if (a.stats != nullptr) a.stats[row].kind = kRowSkipped;
             if (a.status != nullptr) a.status[row] = 0;
@@ -285,8 +283,8 @@ __global__ void __launch_bounds__((GRAD ? kMostWarps : kLeastWarps) * 32, GRAD ?
     const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
     const float step = 16.f / c, low = lowest_of<DT>(c);
     const int32_t tiles = tiles_of(in.n);
-    const int32_t first = SPLIT ? piece * plan.piece : 0;
-    const int32_t end = SPLIT ? min(first + plan.piece, tiles) : tiles;
+    const Part mine = SPLIT ? part_of(plan.cut, blockIdx.x, row, tiles) : Part{row, 0, 1, 0, tiles};
+    const int32_t first = mine.first, end = mine.end;
     Running st;
     start(st);
     int32_t twice = 0;
@@ -323,10 +321,11 @@ __global__ void __launch_bounds__((GRAD ? kMostWarps : kLeastWarps) * 32, GRAD ?
         }
     }
     RowSum all = block_join(part, warp_join(st, twice, c), c);
-    if (SPLIT && !last_piece(plan.split, row, piece, plan.pieces, all, &flag)) return;
+    const bool cut = SPLIT && mine.pieces > 1;
+    if (cut && !last_piece(plan.split, row - plan.cut.whole, mine, all, &flag)) return;
     if (!GRAD) {
         if (warp != 0) return;
-        if (SPLIT) all = join_pieces(plan.split, row, plan.pieces, c, lane);
+        if (cut) all = join_pieces(plan.split, row - plan.cut.whole, mine.pieces, c, lane);
         Teacher t;
         read_teacher<DT>(t, a, row, in.a0 + in.head * kElem<DT>, lane);
         make_teacher(t, entries, a, lane, all.ahead != 0);
@@ -363,7 +362,7 @@ __global__ void __launch_bounds__((GRAD ? kMostWarps : kLeastWarps) * 32, GRAD ?
 //   rows              32        152       304       512       912        2000       8192
 //   32000 (64 KB)     14 / 21   16 / 23   20 / 29   27 / 33   41 / 43    78 / 82    272 / 281
 //   50257 (100 KB)    21 / 23   23 / 27   29 / 33   39 / 45   57 / 59    117 / 115
-//   128256            29 / 23   35 / 35   49 / 53   76 / 80   123 / 123  262 / 256
+//   128256            29 / 23   35 / 35   49 / 53   76 / 80   123 / 123  262 / 248
 // and float32 rows of 128256: 304 of them 84 / 87, 512 135 / 133. With 4, 8 and 16 warps a block,
 // of 32000: 32 rows 23, 18 and 14; 456 rows 31, 27 and 31; 912 rows 41, 45 and 47.
 inline bool one_block(int64_t rows, int32_t tiles, bool grad)
@@ -378,13 +377,11 @@ DistillPlan plan_of(const Rows& r, bool grad, int* warps)
 {
     DistillPlan p{};
     const int32_t tiles = tiles_of((static_cast<int64_t>(r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
-    p.pieces = 1;
-    p.piece = tiles;
     const bool one = one_block(r.rows, tiles, grad);
-    if (!one) p.pieces = pieces_of(r.rows, tiles, kLeastWarps, &p.piece);
+    p.cut = one ? Cut{r.rows, 1, tiles} : cut_of(r.rows, tiles, kLeastWarps, false);
     const int most = one ? warps_of(r.rows) : kLeastWarps;
     *warps = 1;
-    while (*warps < most && *warps < p.piece) *warps *= 2;
+    while (*warps < most && *warps < p.cut.piece) *warps *= 2;
     return p;
 }
 
@@ -394,13 +391,14 @@ cudaError_t launch(const DistillArgs& a, void* workspace, bool* all_done, cudaSt
     int warps = 1;
     const bool grad = a.grad.base != nullptr;
     DistillPlan p = plan_of<DT>(a.r, grad, &warps);
-    if (p.pieces > 1) p.split = split_of(workspace, a.r.rows, p.pieces);
+    const bool cut = p.cut.pieces > 1;
+    if (cut) p.split = split_of(workspace, a.r.rows - p.cut.whole, p.cut.pieces);
     const int32_t tiles = tiles_of((static_cast<int64_t>(a.r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
     const bool one = one_block(a.r.rows, tiles, grad);
     const auto k = one             ? distill_kernel<DT, false, true>
-                   : p.pieces > 1 ? distill_kernel<DT, true, false>
+                   : cut ? distill_kernel<DT, true, false>
                                   : distill_kernel<DT, false, false>;
-    k<<<static_cast<unsigned>(static_cast<int64_t>(p.pieces) * a.r.rows), warps * 32, 0, s>>>(a, p);
+    k<<<static_cast<unsigned>(blocks_of(p.cut, a.r.rows)), warps * 32, 0, s>>>(a, p);
     *all_done = one || !grad;
     return cudaGetLastError();
 }
@@ -412,7 +410,7 @@ size_t distill_workspace(const Rows& r, int dtype)
     int warps;
     const DistillPlan p = dtype == SV_F32 ? plan_of<SV_F32>(r, false, &warps)
                                           : plan_of<SV_BF16>(r, false, &warps);
-    return p.pieces > 1 ? split_bytes(r.rows, p.pieces, 0) : 0;
+    return p.cut.pieces > 1 ? split_bytes(r.rows - p.cut.whole, p.cut.pieces, 0) : 0;
 }
 
 cudaError_t launch_distill(const DistillArgs& a, int dtype, void* workspace, bool* all_done,

@@ -16,7 +16,7 @@
 // Should they be many (ties, or a sorted row), the same argument is applied once more, to
 // the vectors of 16 bytes in those groups, and leaves 8 k elements at most.
 //
-// Few rows are cut into pieces, a block each (pieces_of; one row of 128256 bfloat16 is read by
+// Few rows are cut into pieces, a block each (cut_of; one row of 128256 bfloat16 is read by
 // fifteen SMs). A piece leaves its sums and its groups' maxima in the workspace; the block that is
 // the last of its row to do so (a counter a row, which starts at 0 and is 0 again afterwards)
 // finishes the row while others read on. Pieces are joined in order, so that who is last makes no
@@ -25,7 +25,7 @@
 // Bound by memory for many rows: half of the issue slots are taken (some six to seven instructions
 // an element). 1024 rows of 128256 bfloat16, 263 MB: 54 us without alternatives, 62 with 20, 80
 // with 128 (a block's choice and order of 128 is not hidden where all rows make one wave); 4096
-// rows 187, 224 and 294: 5.6, 4.7 and 3.6 TB/s. A plain sum over the 263 MB takes 49.
+// rows 174, 221 and 294: 6.0, 4.8 and 3.6 TB/s. A plain sum over the 263 MB takes 49.
 #include "lp_finish.cuh"
 #include "lp_stream.cuh"
 
@@ -33,13 +33,12 @@ namespace svl {
 namespace {
 
 struct LogprobPlan {
-    int32_t pieces;      // of a row, a block each
-    int32_t piece;       // warps' turns in a piece
+    Cut cut;
     int32_t groups;      // maxima of a row (a multiple of 4)
     int32_t keys;        // room for them, and for those of the chosen groups' vectors
     int32_t candidates;  // elements kept for the last choice: a vector of each of the first k,
                          // at least
-    Split split;         // with more than one piece
+    Split split;         // where rows are cut
 };
 
 // Numbers of the logits' type as words that hold one or two of them, and the next one up
@@ -491,18 +490,18 @@ __global__ void __launch_bounds__((TOP ? kMostWarps : kLeastWarps) * 32, TOP ? 2
     extern __shared__ __align__(16) uint32_t dynamic[];
     __shared__ RowSum part[TOP ? kMostWarps : kLeastWarps];
     __shared__ Top top;
-    const int32_t row = SPLIT ? blockIdx.x / plan.pieces : blockIdx.x;
-    const int32_t piece = SPLIT ? blockIdx.x - row * plan.pieces : 0, V = a.r.V;
+    const int32_t row = SPLIT ? row_of(plan.cut, blockIdx.x) : blockIdx.x, V = a.r.V;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int32_t token = a.tokens == nullptr ? 0 : a.tokens[row];
     if (token < 0 || token >= V) {
-        if (piece == 0) finish_other<DT>(a, row, token, &top.flags);
+        if (!SPLIT || part_of(plan.cut, blockIdx.x, row, 0).piece == 0)
+            finish_other<DT>(a, row, token, &top.flags);
         return;
     }
     const float c = a.r.c;
     const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
     float* maxima = !TOP    ? nullptr
-                    : SPLIT ? plan.split.maxima + static_cast<int64_t>(row) * plan.groups
+                    : SPLIT ? plan.split.maxima + static_cast<int64_t>(row - plan.cut.whole) * plan.groups
                             : reinterpret_cast<float*>(dynamic);
     const Asked q = asked_of<DT>(a, in, token);
     const float step = 16.f / c, low = lowest_of<DT>(c);
@@ -510,17 +509,16 @@ __global__ void __launch_bounds__((TOP ? kMostWarps : kLeastWarps) * 32, TOP ? 2
     start(st);
     int32_t ahead = 0;
     const int32_t tiles = tiles_of(in.n);
-    const int32_t first = SPLIT ? piece * plan.piece : 0;
-    const int32_t end = SPLIT ? min(first + plan.piece, tiles) : tiles;
-    for (int32_t tile = first + warp; tile < end; tile += warps) {
+    const Part mine = SPLIT ? part_of(plan.cut, blockIdx.x, row, tiles) : Part{row, 0, 1, 0, tiles};
+    for (int32_t tile = mine.first + warp; tile < mine.end; tile += warps) {
         uint4 v[kInFlight];
         ld_tile<DT>(v, in, tile * kTile, lane, V);
         do_tile<DT, TOP>(st, ahead, v, tile, in.head, q, maxima, c, step, low, lane);
     }
     RowSum all = block_join(part, warp_join(st, ahead, c), c);
-    if (SPLIT) {
-        if (!last_piece(plan.split, row, piece, plan.pieces, all, &top.flags)) return;
-        all = join_pieces(plan.split, row, plan.pieces, c, lane);
+    if (SPLIT && mine.pieces > 1) {
+        if (!last_piece(plan.split, row - plan.cut.whole, mine, all, &top.flags)) return;
+        all = join_pieces(plan.split, row - plan.cut.whole, mine.pieces, c, lane);
     } else {
         if (tid == 0) part[0] = all;
         __syncthreads();
@@ -545,9 +543,9 @@ LogprobPlan plan_of(const Rows& r, int32_t k, int* warps)
     // 49, 39 and 33, 608 rows 66, 49 and 74, 912 rows 72, 88 and 100; 20 of them 20, 18, 18, 31, 31,
     // 29, 45, 41, 66, 57, 72, 89; none 12, 12, 14, 23, 24, 23, 37, 35, 47, 49, 55, 64)
     const int most = k > 0 ? warps_of(r.rows) : kLeastWarps;
-    p.pieces = pieces_of(r.rows, tiles, most, &p.piece);
+    p.cut = cut_of(r.rows, tiles, most, k > 0);
     *warps = 1;
-    while (*warps < most && *warps < p.piece) *warps *= 2;
+    while (*warps < most && *warps < p.cut.piece) *warps *= 2;
     p.groups = tiles * kInFlight;
     const int32_t vectors = 32 * (k < p.groups ? k : p.groups);
     p.keys = p.groups > vectors ? p.groups : vectors;
@@ -560,10 +558,11 @@ cudaError_t launch(const LogprobArgs& a, void* workspace, cudaStream_t s)
 {
     int warps = 1;
     LogprobPlan p = plan_of<DT>(a.r, a.k, &warps);
-    if (p.pieces > 1) p.split = split_of(workspace, a.r.rows, p.pieces);
+    const bool cut = p.cut.pieces > 1;
+    if (cut) p.split = split_of(workspace, a.r.rows - p.cut.whole, p.cut.pieces);
     const size_t bytes = TOP ? p.keys * 4 + p.candidates * 8 : 0;
-    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.pieces) * a.r.rows);
-    const auto k = p.pieces > 1 ? logprobs_kernel<DT, TOP, true> : logprobs_kernel<DT, TOP, false>;
+    const unsigned grid = static_cast<unsigned>(blocks_of(p.cut, a.r.rows));
+    const auto k = cut ? logprobs_kernel<DT, TOP, true> : logprobs_kernel<DT, TOP, false>;
     if (bytes > 45000) {  // (beside the static part, more than is allowed unasked)
         const cudaError_t e =
             cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
@@ -580,7 +579,7 @@ size_t logprobs_workspace(const Rows& r, int dtype, int32_t k)
     int warps;
     const LogprobPlan p = dtype == SV_F32 ? plan_of<SV_F32>(r, k, &warps)
                                           : plan_of<SV_BF16>(r, k, &warps);
-    return p.pieces > 1 ? split_bytes(r.rows, p.pieces, k > 0 ? p.groups : 0) : 0;
+    return p.cut.pieces > 1 ? split_bytes(r.rows - p.cut.whole, p.cut.pieces, k > 0 ? p.groups : 0) : 0;
 }
 
 cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, void* workspace, cudaStream_t s)

@@ -325,7 +325,7 @@ __host__ __device__ __forceinline__ int32_t tiles_of(int64_t vectors)
 // Rows in pieces, a block each. What the pieces leave for one another lies in the workspace: a
 // counter a row, in a place of their own that other calls' workspaces have too, since the
 // counters are 0 between calls; then the pieces' sums; then the groups' maxima.
-constexpr int64_t kMaxSplitRows = 65536;   // more rows are enough blocks as they are
+constexpr int64_t kMaxSplitRows = 65536;   // (no more than 4864 are cut)
 constexpr int32_t kMostTurns = 32;         // of a bitmap of entries
 constexpr int64_t kEnoughWarps = 4864;     // 32 an SM
 
@@ -345,29 +345,64 @@ inline int warps_of(int64_t rows)
     return warps;
 }
 
-// Pieces of a row of so many turns, and their turns. As many as make one wave of blocks, with two
-// turns a warp at least: more blocks than run at a time end in a wave that is not full, and a
-// block's beginning and end cost as much as three turns a warp. For 1024 rows of 128256
-// (bfloat16, without alternatives): one piece 52 us, two 62, four 56, eight 58; 544 rows: 41, 35,
-// 38, 38; 40 rows: 35, 23, 17, 15. Two where there are somewhat more long rows than blocks run
-// at a time, some of which may have nothing to do: 2304 rows with 20 alternatives, half of the rows
-// empty, one piece 96, two 86 (blocks of two warps 106); 1280 full rows 99 and 87; but 2304 full
-// ones 125 and 135, and 2000 rows of 64 KB 31 and 33.
-inline int32_t pieces_of(int64_t rows, int32_t tiles, int32_t warps, int32_t* piece)
+// Rows [0, whole) are a block each; the others are cut into `pieces` of `piece` turns.
+struct Cut {
+    int32_t whole, pieces, piece;
+};
+
+// How rows of so many turns are cut. All of them, if they are few: into as many pieces as make
+// one wave of blocks, with two turns a warp at least: more blocks than run at a time end in a wave that
+// is not full, and a block's beginning and end cost as much as three turns a warp. For 1024 rows of
+// 128256 (bfloat16, without alternatives): one piece 52 us, two 62, four 56, eight 58; 544 rows:
+// 41, 35, 38, 38; 40 rows: 35, 23, 17, 15. If there are more long rows than run at a time, those of
+// a last wave that is at most half full: losses of 1400, 2048 and 4096 rows, all whole 88, 99 and
+// 182, all in two 78, 107 and 191, so 72, 99 and 179; but of 4096 rows of 64 KB 68, and so 70.
+// `ragged` (with alternatives): somewhat more long rows than run at a time are all cut in two, since
+// some may have nothing to do: 2304 rows with 20 alternatives, half of the rows empty, one piece
+// 96, two 86 (blocks of two warps 106); 1280 full rows 99 and 87; but 2304 full ones 125 and 135.
+inline Cut cut_of(int64_t rows, int32_t tiles, int32_t warps, bool ragged)
 {
-    *piece = tiles;
-    if (rows > kMaxSplitRows || rows == 0) return 1;
+    const Cut none{static_cast<int32_t>(rows), 1, tiles};
+    if (rows == 0) return none;
     const int64_t blocks = kEnoughWarps / warps;
-    int64_t n = rows <= blocks                        ? blocks / rows
-                : rows < 4 * blocks && tiles >= 64 ? 2
-                                                   : 1;
+    int64_t whole = 0, n = 1;
+    if (rows <= blocks) {
+        n = blocks / rows;
+    } else if (tiles < 64) {
+        return none;
+    } else if (ragged) {
+        if (rows < 4 * blocks) n = 2;
+    } else {
+        whole = rows / blocks * blocks;
+        n = rows > whole ? blocks / (rows - whole) : 1;
+    }
     if (n > tiles / (2 * warps)) n = tiles / (2 * warps);
-    if (n <= 1) return 1;
-    *piece = static_cast<int32_t>((tiles + n - 1) / n);  // evenly, in whole turns of all warps
-    *piece = (*piece + warps - 1) / warps * warps;
-    return (tiles + *piece - 1) / *piece;
+    if (n <= 1) return none;
+    // (evenly, in whole turns of all warps)
+    const int64_t piece = ((tiles + n - 1) / n + warps - 1) / warps * warps;
+    return {static_cast<int32_t>(whole), static_cast<int32_t>((tiles + piece - 1) / piece),
+            static_cast<int32_t>(piece)};
 }
 
+inline int64_t blocks_of(const Cut& c, int64_t rows) { return c.whole + (rows - c.whole) * c.pieces; }
+
+// A block's part of a row.
+struct Part {
+    int32_t row, piece, pieces;
+    int32_t first, end;     // turns
+};
+__device__ __forceinline__ int32_t row_of(const Cut& c, int32_t block)
+{
+    return block < c.whole ? block : c.whole + (block - c.whole) / c.pieces;
+}
+__device__ __forceinline__ Part part_of(const Cut& c, int32_t block, int32_t row, int32_t tiles)
+{
+    if (block < c.whole) return {row, 0, 1, 0, tiles};
+    const int32_t piece = block - c.whole - (row - c.whole) * c.pieces, first = piece * c.piece;
+    return {row, piece, c.pieces, first, min(first + c.piece, tiles)};
+}
+
+// (rows that are cut, here and further down: counted from the first one)
 inline size_t split_bytes(int64_t rows, int64_t pieces, int64_t groups)
 {
     return kMaxSplitRows * 4 + static_cast<size_t>(rows) * pieces * sizeof(RowSum) +
@@ -401,20 +436,20 @@ __device__ __forceinline__ RowSum block_join(RowSum* part, const RowSum& mine, f
 // Leaves a piece's sums (those of thread 0) and says whether all of the row's are there now;
 // everything that the block's threads wrote before is then visible to the block that is told so,
 // past the first-level cache.
-__device__ __forceinline__ bool last_piece(const Split& s, int32_t row, int32_t piece, int32_t pieces,
+__device__ __forceinline__ bool last_piece(const Split& s, int32_t row, const Part& p,
                                            const RowSum& mine, uint32_t* shared)
 {
     __syncthreads();
     if (threadIdx.x == 0) {
-        __stcg(reinterpret_cast<float4*>(s.sums + static_cast<int64_t>(row) * pieces + piece),
+        __stcg(reinterpret_cast<float4*>(s.sums + static_cast<int64_t>(row) * p.pieces + p.piece),
                make_float4(mine.m, mine.s, mine.e, __int_as_float(mine.ahead)));
         // (releases what the barrier has shown this thread of the others' writes too)
         uint32_t before;
         asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
                      : "=r"(before)
-                     : "l"(s.counters + row), "r"(static_cast<uint32_t>(pieces - 1))
+                     : "l"(s.counters + row), "r"(static_cast<uint32_t>(p.pieces - 1))
                      : "memory");
-        *shared = before == static_cast<uint32_t>(pieces - 1);
+        *shared = before == static_cast<uint32_t>(p.pieces - 1);
     }
     __syncthreads();
     return *shared != 0;
