@@ -207,11 +207,13 @@ def _wrote(*tensors):
 class _Call:
     """What a differentiable call's backward pass needs beside the logits. (One object in place of
     arguments and saved tensors: autograd takes its time for each of those. Inputs that were
-    changed in between are noticed here, as autograd notices it of the logits.)"""
-    __slots__ = ("described", "inputs", "versions", "row_stats", "results", "args")
+    changed in between are noticed here, as autograd notices it of the logits.) ``described`` is
+    for the forward call alone: the logits that autograd hands back may be others in another place
+    (recomputed under a checkpoint, or copied by a hook for saved tensors)."""
+    __slots__ = ("described", "temperature", "inputs", "versions", "row_stats", "results", "args")
 
-    def __init__(self, described, inputs, row_stats, args):
-        self.described, self.inputs = described, inputs
+    def __init__(self, described, temperature, inputs, row_stats, args):
+        self.described, self.temperature, self.inputs = described, temperature, inputs
         self.row_stats, self.args, self.results = row_stats, args, None
 
     def begun(self):
@@ -224,6 +226,15 @@ class _Call:
                                "place since")
 
 
+def _saved(ctx):
+    """(logits, packed struct sv_logit_rows of where they are now, call) of a backward pass."""
+    (logits,), call = ctx.saved_tensors, ctx.call
+    call.check()
+    if logits.stride(-1) != 1:
+        logits = logits.contiguous()
+    return logits, _describe(logits, call.temperature)[0], call
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, call):
@@ -233,6 +244,7 @@ class _TokenLogprobs(torch.autograd.Function):
                                          device=logits.device)
         call.results = out = _logprobs(call.described, logits, *call.args, call.row_stats)
         call.begun()
+        call.described = None
         ctx.save_for_backward(logits)
         ctx.call = call
         ctx.set_materialize_grads(False)
@@ -245,15 +257,13 @@ class _TokenLogprobs(torch.autograd.Function):
 
 
 def _logprobs_backward(ctx, grad_logprobs, grad_entropy, grad_lse):
-    (logits,), call = ctx.saved_tensors, ctx.call
-    call.check()
-    rows, dev, _ = call.described
+    logits, rows, call = _saved(ctx)
     grads = [None if g is None else g.contiguous() for g in (grad_logprobs, grad_entropy, grad_lse)]
     out = _grad_like(logits)
     _check(_lib.load_logprobs().sv_token_logprobs_backward(
         rows, call.inputs[0].data_ptr() if call.inputs else None, call.row_stats.data_ptr(),
         *[None if g is None else g.data_ptr() for g in grads], out.data_ptr(), *_strides(out)[2:],
-        torch._C._cuda_getCurrentRawStream(dev.index)), "sv_token_logprobs_backward")
+        torch._C._cuda_getCurrentRawStream(logits.device.index)), "sv_token_logprobs_backward")
     return out, None
 
 
@@ -281,7 +291,7 @@ def sv_token_logprobs(logits, tokens=None, *, temperature: float = 1.0, top_k: i
 
     def call(_):
         if logits.requires_grad and torch.is_grad_enabled():
-            c = _Call(described, () if tokens is None else (tokens,), row_stats,
+            c = _Call(described, temperature, () if tokens is None else (tokens,), row_stats,
                       (tokens, top_k, row_status, workspace))
             logprobs, entropy, lse = _TokenLogprobs.apply(logits, c)
             _, rank, _, _, top_tokens, top_logprobs = c.results
@@ -365,6 +375,7 @@ class _DistillLoss(torch.autograd.Function):
         loss = _distill(call.described, logits, *call.inputs, None, tail, None, None, call.row_stats,
                         row_status, workspace)
         call.begun()
+        call.described = None
         return loss
 
     @staticmethod
@@ -374,15 +385,13 @@ class _DistillLoss(torch.autograd.Function):
 
 
 def _distill_backward(ctx, grad_loss):
-    (logits,), call = ctx.saved_tensors, ctx.call
-    call.check()
-    rows, dev, _ = call.described
+    logits, rows, call = _saved(ctx)
     tokens, logprobs = call.inputs
     grad_loss, out = grad_loss.contiguous(), _grad_like(logits)
     _check(_lib.load_logprobs().sv_distill_backward(
         rows, tokens.data_ptr(), logprobs.data_ptr(), tokens.shape[-1], _TAILS[call.args[0]],
         call.row_stats.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), *_strides(out)[2:],
-        torch._C._cuda_getCurrentRawStream(dev.index)), "sv_distill_backward")
+        torch._C._cuda_getCurrentRawStream(logits.device.index)), "sv_distill_backward")
     return out, None
 
 
@@ -404,7 +413,8 @@ def sv_distill_loss(logits, teacher_tokens, teacher_logprobs, *, temperature: fl
     def call(_):
         if logits.requires_grad and torch.is_grad_enabled():
             return _DistillLoss.apply(logits, _Call(
-                described, (teacher_tokens, teacher_logprobs), None, (tail, row_status, workspace)))
+                described, temperature, (teacher_tokens, teacher_logprobs), None,
+                (tail, row_status, workspace)))
         return _distill(described, logits, teacher_tokens, teacher_logprobs, None, tail, None, None,
                         None, row_status, workspace)
 
