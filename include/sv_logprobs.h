@@ -126,8 +126,9 @@ int sv_token_logprobs(const sv_logit_rows* rows, const int32_t* tokens, int64_t 
  * The logits' gradient, from gradients a, b and c of log probability, entropy and
  * lse (device float [rows] each, NULL for zeros; grad_logprobs needs tokens):
  *   grad_v = (a ([v = token] - p_v) - b p_v (log p_v + entropy) + c p_v) / T.
- * Rows of token -1 get zeros.
- *   row_stats   what sv_token_logprobs wrote for these rows and tokens.
+ * The tokens may be others than the forward call's. Rows whose token is out of
+ * range, here or there, get NaN; other rows of token -1, here or there, zeros.
+ *   row_stats   what sv_token_logprobs wrote for these rows.
  *   grad        device, the logits' type, vocab elements a row; row o * inner + i
  *               begins at grad + o * grad_outer_stride + i * grad_inner_stride.
  *               Rows must not overlap. It may be the logits themselves.

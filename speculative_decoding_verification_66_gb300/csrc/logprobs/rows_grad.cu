@@ -64,8 +64,12 @@ __global__ void __launch_bounds__(kMaxThreads)
     const Vecs out = vectors_of<DT>(row_begin(a.grad, a.r.inner, row), V);
     const Piece pc = my_piece(plan, out.n);
     const RowStats st = a.stats[row];
-    if (st.kind != kRowGood) {
-        fill_tiles<DT>(out, pc.mine, pc.step, pc.end, V, st.kind == kRowBad ? nan() : 0.f);
+    // The kind is of the forward call's tokens, and these may be others.
+    const int32_t token = a.tokens == nullptr ? 0 : a.tokens[row];
+    const bool out_of_range = token < -1 || token >= V;
+    if (st.kind != kRowGood || token == -1 || out_of_range) {
+        const bool bad = st.kind == kRowBad || out_of_range;
+        fill_tiles<DT>(out, pc.mine, pc.step, pc.end, V, bad ? nan() : 0.f);
         return;
     }
     const float da = a.a == nullptr ? 0.f : a.a[row];
@@ -75,9 +79,8 @@ __global__ void __launch_bounds__(kMaxThreads)
     const float A = (dc - da - db * st.mean) * s, B = -db * kLn2 * s;
     // The token's own gradient, where it is in this piece: its logit is read before anything
     // is written, over the logits perhaps.
-    const int32_t token = a.tokens == nullptr ? -1 : a.tokens[row];
     const int64_t at =
-        token < 0 ? -1 : (static_cast<int64_t>(token) + out.head) / (kPerVec<DT> * kTile);
+        a.tokens == nullptr ? -1 : (static_cast<int64_t>(token) + out.head) / (kPerVec<DT> * kTile);
     const bool mine = at >= pc.first && at < pc.end;
     float own = 0.f;
     if (mine) {

@@ -307,7 +307,9 @@ def sv_token_logprobs_backward(logits, row_stats, *, tokens=None, grad_logprobs=
                                grad=None, stream=None):
     """The logits' gradient from those of ``sv_token_logprobs``' log probabilities, entropies and
     log-sum-exps (float32, one for each row; None: zeros), with the ``row_stats`` that it filled.
-    ``grad`` may be the logits themselves, whose values are then gone."""
+    ``tokens`` may be others than the forward call's, or given here alone; rows whose token is out of
+    range get NaN, rows of token -1 zeros. ``grad`` may be the logits themselves, whose values are
+    then gone."""
     rows, dev, shape = _describe(logits, temperature)
     f32 = torch.float32
     ptrs = [_per_row(tokens, "tokens", shape, torch.int32, dev),
