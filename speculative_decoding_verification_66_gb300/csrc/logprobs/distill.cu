@@ -376,7 +376,7 @@ template <int DT>
 DistillPlan plan_of(const Rows& r, bool grad, int* warps)
 {
     DistillPlan p{};
-    const int32_t tiles = tiles_of((static_cast<int64_t>(r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
+    const int32_t tiles = most_tiles(r.V, kPerVec<DT>);
     const bool one = one_block(r.rows, tiles, grad);
     p.cut = one ? Cut{r.rows, 1, tiles} : cut_of(r.rows, tiles, kLeastWarps, false);
     const int most = one ? warps_of(r.rows) : kLeastWarps;
@@ -393,7 +393,7 @@ cudaError_t launch(const DistillArgs& a, void* workspace, bool* all_done, cudaSt
     DistillPlan p = plan_of<DT>(a.r, grad, &warps);
     const bool cut = p.cut.pieces > 1;
     if (cut) p.split = split_of(workspace, a.r.rows - p.cut.whole, p.cut.pieces);
-    const int32_t tiles = tiles_of((static_cast<int64_t>(a.r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
+    const int32_t tiles = most_tiles(a.r.V, kPerVec<DT>);
     const bool one = one_block(a.r.rows, tiles, grad);
     const auto k = one             ? distill_kernel<DT, false, true>
                    : cut ? distill_kernel<DT, true, false>

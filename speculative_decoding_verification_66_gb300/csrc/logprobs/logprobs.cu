@@ -538,7 +538,7 @@ template <int DT>
 LogprobPlan plan_of(const Rows& r, int32_t k, int* warps)
 {
     LogprobPlan p{};
-    const int32_t tiles = tiles_of((static_cast<int64_t>(r.V) + kPerVec<DT> - 1) / kPerVec<DT> + 1);
+    const int32_t tiles = most_tiles(r.V, kPerVec<DT>);
     // (alternatives, 128 of 128256 bfloat16: with 4, 8 and 16 warps 40 rows 29, 23 and 21 us, 304 rows
     // 49, 39 and 33, 608 rows 66, 49 and 74, 912 rows 72, 88 and 100; 20 of them 20, 18, 18, 31, 31,
     // 29, 45, 41, 66, 57, 72, 89; none 12, 12, 14, 23, 24, 23, 37, 35, 47, 49, 55, 64)

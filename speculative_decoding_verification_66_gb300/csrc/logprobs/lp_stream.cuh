@@ -322,6 +322,13 @@ __host__ __device__ __forceinline__ int32_t tiles_of(int64_t vectors)
     return static_cast<int32_t>((vectors + kTile - 1) / kTile);
 }
 
+// Most turns of a row of V elements, which may begin anywhere. (V up to 2^31 - 1, and elements in
+// front of the row: sums of them need 64 bits.)
+__host__ __device__ __forceinline__ int32_t most_tiles(int32_t V, int per_vec)
+{
+    return tiles_of((static_cast<int64_t>(V) + per_vec - 1) / per_vec + 1);
+}
+
 // Rows in pieces, a block each. What the pieces leave for one another lies in the workspace: a
 // counter a row, in a place of their own that other calls' workspaces have too, since the
 // counters are 0 between calls; then the pieces' sums; then the groups' maxima.
@@ -385,6 +392,25 @@ inline Cut cut_of(int64_t rows, int32_t tiles, int32_t warps, bool ragged)
 }
 
 inline int64_t blocks_of(const Cut& c, int64_t rows) { return c.whole + (rows - c.whole) * c.pieces; }
+
+// A gradient's rows: a warp has up to four turns, in blocks of one to eight warps: short rows leave
+// few threads idle, long ones are cut where a block's start no longer shows.
+constexpr int kGradWarps = 8;
+struct GradPlan {
+    int32_t pieces;          // of a row
+    int32_t piece;           // warps' turns in a piece
+};
+inline GradPlan grad_plan_of(int32_t rows, int32_t tiles, int* warps)
+{
+    *warps = 1;
+    while (*warps < kGradWarps && *warps < tiles) *warps *= 2;
+    int64_t piece = *warps * 4, pieces = (tiles + piece - 1) / piece;
+    while (pieces * rows >= (int64_t(1) << 31)) {
+        piece *= 2;
+        pieces = (tiles + piece - 1) / piece;
+    }
+    return {static_cast<int32_t>(pieces), static_cast<int32_t>(piece)};
+}
 
 // A block's part of a row.
 struct Part {

@@ -16,12 +16,7 @@
 namespace svl {
 namespace {
 
-constexpr int kMaxThreads = 256;
-
-struct GradPlan {
-    int32_t pieces;          // of a row
-    int32_t piece;           // warps' turns in a piece
-};
+constexpr int kMaxThreads = kGradWarps * 32;
 
 // This block's turns in its row.
 struct Piece {
@@ -150,24 +145,13 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
 }
 
-// A warp has up to four turns, in blocks of one to eight warps: short rows leave few threads
-// idle, long ones are cut where a block's start no longer shows.
 template <typename Kernel, typename Args>
 cudaError_t launch(Kernel k, const Args& a, int per_vec, cudaStream_t s, bool early = false)
 {
-    const int64_t tiles = tiles_of((a.r.V + per_vec - 1) / per_vec + 1);
-    int warps = 1;
-    while (warps * 32 < kMaxThreads && warps < tiles) warps *= 2;
-    GradPlan g;
-    g.piece = warps * 4;
-    int64_t pieces = (tiles + g.piece - 1) / g.piece;
-    while (pieces * a.r.rows >= (int64_t(1) << 31)) {
-        g.piece *= 2;
-        pieces = (tiles + g.piece - 1) / g.piece;
-    }
-    g.pieces = static_cast<int32_t>(pieces);
+    int warps;
+    const GradPlan g = grad_plan_of(a.r.rows, most_tiles(a.r.V, per_vec), &warps);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(pieces * a.r.rows));
+    cfg.gridDim = dim3(static_cast<unsigned>(g.pieces) * static_cast<unsigned>(a.r.rows));
     cfg.blockDim = dim3(warps * 32);
     cfg.stream = s;
     cudaLaunchAttribute at[1];

@@ -60,3 +60,39 @@ def test_tokens_of_inference_mode_changed_before_the_backward_pass():
     r.logprobs.sum().backward()
     assert x.grad[[0, 2]].isnan().all()
     check_gradient(x.grad[1:2], x[1:2], tokens[1:2], torch.ones(1, device="cuda"), None, None, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_largest_vocabulary_and_its_gradients(dtype):
+    """2^31 - 1 tokens, nearly all of them masked, the gradient over the logits themselves."""
+    V = 2 ** 31 - 1
+    at = torch.tensor([0, 5, 1023, 1024, 2 ** 30 + 7, V - 9, V - 2, V - 1], device="cuda")
+    some = draw((1, len(at)), dtype, 1)
+    x = torch.empty(V, dtype=some.dtype, device="cuda")
+
+    def others_are_zero(want):
+        assert sum(int((part != 0).sum()) for part in x.split(1 << 28)) == int((want != 0).sum())
+
+    for t in (3, 7):
+        x.fill_(-math.inf)
+        x[at] = some[0]
+        token = at[t].to(torch.int32)
+        stats = torch.empty(sv.SV_ROW_STATS, device="cuda")
+        r = sv.sv_token_logprobs(x, token, row_stats=stats)
+        w = u.logprobs(some, torch.tensor([t], device="cuda"))
+        for name in ("logprobs", "entropy", "lse"):
+            u.close(getattr(r, name), w[name][0], 1e-5, name)
+        assert int(r.rank) == int(w["rank"])
+        one = torch.ones((), device="cuda")
+        grad = sv.sv_token_logprobs_backward(x, stats, tokens=token, grad_logprobs=one, grad=x)
+        want = u.logprobs_grad(some, torch.tensor([t], device="cuda"), one[None], None, None)
+        u.check_grad(grad[at], want[0], 1.0, len(at), 8.0)
+        others_are_zero(want)
+    x.fill_(-math.inf)
+    x[at] = some[0]
+    ids, lp = torch.tensor([5, 1, 2], device="cuda"), torch.tensor([-1.0, -2.0, -3.0], device="cuda")
+    want, g, _ = u.distill(some, ids[None], lp[None])
+    loss, grad = sv.sv_distill(x, at[ids].to(torch.int32), lp, grad=x)
+    u.close(loss, want[0], 1e-5, "loss")
+    u.check_grad(grad[at], g[0], 1.0, len(at), 8.0)
+    others_are_zero(g)
