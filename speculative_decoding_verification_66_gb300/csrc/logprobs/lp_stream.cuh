@@ -356,6 +356,7 @@ inline int warps_of(int64_t rows)
 struct Cut {
     int32_t whole, pieces, piece;
 };
+inline int64_t blocks_of(const Cut& c, int64_t rows) { return c.whole + (rows - c.whole) * c.pieces; }
 
 // How rows of so many turns are cut. All of them, if they are few: into as many pieces as make
 // one wave of blocks, with two turns a warp at least: more blocks than run at a time end in a wave that
@@ -387,11 +388,11 @@ inline Cut cut_of(int64_t rows, int32_t tiles, int32_t warps, bool ragged)
     if (n <= 1) return none;
     // (evenly, in whole turns of all warps)
     const int64_t piece = ((tiles + n - 1) / n + warps - 1) / warps * warps;
-    return {static_cast<int32_t>(whole), static_cast<int32_t>((tiles + piece - 1) / piece),
-            static_cast<int32_t>(piece)};
+    const Cut cut{static_cast<int32_t>(whole), static_cast<int32_t>((tiles + piece - 1) / piece),
+                  static_cast<int32_t>(piece)};
+    // (a grid ends at 2^31 - 1 blocks, and rows may be as many)
+    return blocks_of(cut, rows) < (int64_t(1) << 31) ? cut : none;
 }
-
-inline int64_t blocks_of(const Cut& c, int64_t rows) { return c.whole + (rows - c.whole) * c.pieces; }
 
 // A gradient's rows: a warp has up to four turns, in blocks of one to eight warps: short rows leave
 // few threads idle, long ones are cut where a block's start no longer shows.

@@ -19,7 +19,13 @@ int main()
         const int tiles = svl::most_tiles(static_cast<int>(V), per_vec);
         int warps;
         const svl::GradPlan g = svl::grad_plan_of(static_cast<int>(rows), tiles, &warps);
-        std::printf("%d %d %d %d\n", tiles, g.pieces, g.piece, warps);
+        std::printf("%d %d %d %d", tiles, g.pieces, g.piece, warps);
+        for (int w : {4, 8, 16})
+            for (int ragged = 0; ragged < 2; ++ragged) {
+                const svl::Cut c = svl::cut_of(rows, tiles, w, ragged != 0);
+                std::printf(" %d %d %d", c.whole, c.pieces, c.piece);
+            }
+        std::printf("\n");
     }
 }
 """
@@ -49,8 +55,13 @@ def test_all_turns_are_somebodys(plans):
                     top - 2, top - 1, top]
     counts = [1, 2, 3, 40, 304, 1216, 1217, 2304, 4863, 4864, 5000, 65536, top - 1, top]
     sizes = [(rows, V, p) for rows in counts for V in vocabularies for p in (4, 8)]
-    for (rows, V, p), (tiles, pieces, piece, warps) in zip(sizes, plans(sizes), strict=True):
+    for (rows, V, p), (tiles, pieces, piece, warps, *cuts) in zip(sizes, plans(sizes), strict=True):
         # p - 1 elements may lie in front of a row
         assert tiles == -(-(-(-V // p) + 1) // 128) >= -(-(V + p - 1) // (128 * p))
         assert 1 <= warps <= 8 and 1 <= piece < 2 ** 31 and pieces >= 1
         assert pieces * piece >= tiles and pieces * rows < 2 ** 31
+        for whole, n, each in zip(cuts[::3], cuts[1::3], cuts[2::3], strict=True):
+            assert 0 <= whole <= rows and n >= 1 and n * each >= tiles
+            assert whole + (rows - whole) * n < 2 ** 31
+            # (the pieces' counters)
+            assert n == 1 or rows - whole <= 4864
