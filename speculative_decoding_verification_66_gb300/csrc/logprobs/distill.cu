@@ -281,7 +281,7 @@ __global__ void __launch_bounds__((GRAD ? kMostWarps : kLeastWarps) * 32, GRAD ?
         return;
     }
     const Vecs in = vectors_of<DT>(row_begin(a.r.x, a.r.inner, row), V);
-    const float step = 16.f / c, low = lowest_of<DT>(c);
+    const float step = kBehindSum / c, low = lowest_of<DT>(c);
     const int32_t tiles = tiles_of(in.n);
     const Part mine = SPLIT ? part_of(plan.cut, blockIdx.x, row, tiles) : Part{row, 0, 1, 0, tiles};
     const int32_t first = mine.first, end = mine.end;

@@ -504,7 +504,7 @@ __global__ void __launch_bounds__((TOP ? kMostWarps : kLeastWarps) * 32, TOP ? 2
                     : SPLIT ? plan.split.maxima + static_cast<int64_t>(row - plan.cut.whole) * plan.groups
                             : reinterpret_cast<float*>(dynamic);
     const Asked q = asked_of<DT>(a, in, token);
-    const float step = 16.f / c, low = lowest_of<DT>(c);
+    const float step = kBehindEntropy / c, low = lowest_of<DT>(c);
     Running st;
     start(st);
     int32_t ahead = 0;

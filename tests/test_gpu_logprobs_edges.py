@@ -96,3 +96,24 @@ def test_the_largest_vocabulary_and_its_gradients(dtype):
     u.close(loss, want[0], 1e-5, "loss")
     u.check_grad(grad[at], g[0], 1.0, len(at), 8.0)
     others_are_zero(g)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "f32"])
+def test_entropies_are_as_exact_wherever_the_largest_logit_is(dtype):
+    """Rows of normal logits and one that has about half of the probability: in the first turn of its
+    warp, whose sums are then relative to it throughout, or later, some 15 bits above what its lane has
+    seen. What a lane adds after the largest logit is rounded relative to the sums at that time: no
+    more than half a step of its logit's own share each, in both cases, and there are fewer of those
+    additions in the second. So that one's root mean square error is at most the first one's, but for
+    the sampling: 400 rows give either within 1 / sqrt(800), their ratio within 5 % (one standard
+    deviation), 50 % are ten of those."""
+    N, V = 400, 128256
+    x = torch.randn((N, V), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    at = torch.randint(4200, 40000, (N, 1), generator=torch.Generator().manual_seed(5)).cuda()
+    off = []
+    for where in (torch.zeros_like(at), at):
+        y = x.scatter(1, where, 12.5).to(u.DTYPES[dtype])
+        r = sv.sv_token_logprobs(y)
+        w = torch.cat([u.logprobs(rows)["entropy"] for rows in y.split(50)])
+        off.append((r.entropy.double() - w).square().mean().sqrt().item())
+    assert off[1] <= 1.5 * off[0], off
