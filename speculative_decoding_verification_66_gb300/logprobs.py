@@ -6,9 +6,11 @@ Argument marshalling only, as in api.py. Logits are [V], [rows, V] or
 slice of positions or of a padded vocabulary is read where it lies). What is
 given or returned for each row has the logits' shape without V.
 
-``sv_token_logprobs`` and ``sv_distill_loss`` are differentiable in the logits.
-``sv_distill`` gives loss and gradient at once, for training that calls ``logits.backward(grad)`` itself; the ``_backward`` calls are
-the gradients alone. All of these can be captured into a CUDA graph. Of a backward
+``sv_token_logprobs`` and ``sv_distill_loss`` are differentiable in the logits, once
+and in reverse mode; tokens, teachers and weights are constants to them.
+``sv_distill`` gives loss and gradient at once, for training that calls
+``logits.backward(grad)`` itself; the ``_backward`` calls are the gradients alone.
+All of these can be captured into a CUDA graph. Of a backward
 pass through autograd torch asks that no eager graph of the same leaf is alive when
 it is captured: that graph has bound the leaf to its own stream, and the capture ends
 in an error (``torch.autograd.grad`` included). ``sv_distill`` and the ``_backward``
@@ -23,6 +25,7 @@ from functools import lru_cache
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from .api import SV_BF16, SV_F32, _check
@@ -226,6 +229,12 @@ class _Call:
                                "place since")
 
 
+def _refuse_tangents(logits):
+    # (nobody's outside of a dual level, which is known at once)
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(logits).tangent is not None:
+        raise NotImplementedError("log probabilities and divergences have no forward-mode derivatives")
+
+
 def _saved(ctx):
     """(logits, packed struct sv_logit_rows of where they are now, call) of a backward pass."""
     (logits,), call = ctx.saved_tensors, ctx.call
@@ -288,6 +297,7 @@ def sv_token_logprobs(logits, tokens=None, *, temperature: float = 1.0, top_k: i
     (``sv_logprobs_workspace_bytes``, its first SV_LOGPROBS_COUNTER_BYTES zeros when it is new).
     Asynchronous on ``stream`` (default: the current stream of the logits' device)."""
     described = _describe(logits, temperature)
+    _refuse_tangents(logits)
 
     def call(_):
         if logits.requires_grad and torch.is_grad_enabled():
@@ -411,6 +421,7 @@ def sv_distill_loss(logits, teacher_tokens, teacher_logprobs, *, temperature: fl
     teacher have loss 0 and are not read. ``row_status`` and ``workspace`` as in
     ``sv_token_logprobs``."""
     described = _describe(logits, temperature)
+    _refuse_tangents(logits)
 
     def call(_):
         if logits.requires_grad and torch.is_grad_enabled():

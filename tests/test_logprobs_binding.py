@@ -4,6 +4,7 @@ import struct
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.graph import saved_tensors_hooks
 from torch.utils.checkpoint import checkpoint
 
@@ -76,3 +77,15 @@ def test_the_backward_pass_reads_what_a_hook_has_kept(library, loss):
     name, rows, _ = library.calls[-1]
     assert name.endswith("_backward") and rows[0] == room[:, 5:].data_ptr()
     assert rows[1:6] == (1, 4, 0, 70, 50) and rows[7] == 0.5
+
+
+@pytest.mark.parametrize("loss", LOSSES)
+@pytest.mark.parametrize("reverse_too", [False, True])
+def test_forward_mode_is_refused(library, loss, reverse_too):
+    x = torch.randn(4, 50, requires_grad=reverse_too)
+    with forward_ad.dual_level():
+        with pytest.raises(NotImplementedError):
+            loss(forward_ad.make_dual(x, torch.ones(4, 50)))
+        assert not library.calls
+        loss(x)  # (no tangent of its own)
+    assert library.calls
