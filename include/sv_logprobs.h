@@ -131,7 +131,8 @@ int sv_token_logprobs(const sv_logit_rows* rows, const int32_t* tokens, int64_t 
  *   row_stats   what sv_token_logprobs wrote for these rows.
  *   grad        device, the logits' type, vocab elements a row; row o * inner + i
  *               begins at grad + o * grad_outer_stride + i * grad_inner_stride.
- *               Rows must not overlap. It may be the logits themselves.
+ *               Rows must not overlap. It may be the logits themselves, or must have no
+ *               element in common with them (its rows may lie between theirs).
  * One launch.
  */
 int sv_token_logprobs_backward(const sv_logit_rows* rows, const int32_t* tokens,

@@ -61,6 +61,12 @@ def _strides(x):
     return 1, 1, 0, 0
 
 
+def _steps(x):
+    """The same, with stride 0 where there is one of a kind: equal wherever the rows are."""
+    outer, inner, s, t = _strides(x)
+    return outer, inner, s if outer > 1 else 0, t if inner > 1 else 0
+
+
 def _describe(logits, temperature):
     """(packed struct sv_logit_rows, device, shape of the rows)."""
     shape = logits.shape
@@ -152,6 +158,29 @@ def _span(x):
     return x.data_ptr(), x.data_ptr() + (last + 1) * x.element_size()
 
 
+def _apart(grad, logits):
+    """Whether the rows of grad, which have no element in common with one another, have none in common
+    with those of logits, whose spans they share. Known of equal strides alone: then a row of the one
+    lies d + i s + j t elements from a row of the other, with s and t the strides and i and j the
+    distances along the dimensions, the rows' own lengths apart along the larger stride."""
+    outer, inner, s, t = _steps(grad)
+    if (outer, inner, s, t) != _steps(logits):
+        return False
+    d, V = (grad.data_ptr() - logits.data_ptr()) // grad.element_size(), grad.shape[-1]
+    if s < t:
+        outer, inner, s, t = inner, outer, t, s
+    if s < (inner - 1) * t + V and outer > 1 and inner > 1:
+        return False
+    s, t = max(s, 1), max(t, 1)
+    near = range(max(1 - outer, (-d - inner * t - V) // s), min(outer - 1, (-d + inner * t + V) // s + 1) + 1)
+    for i in near:
+        left = d + i * s
+        for j in (-left // t, -left // t + 1):
+            if abs(left + min(max(j, 1 - inner), inner - 1) * t) < V:
+                return False
+    return True
+
+
 def _check_grad(grad, logits):
     if grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != logits.device \
             or (grad.shape[-1] > 1 and grad.stride(-1) != 1):
@@ -160,8 +189,10 @@ def _check_grad(grad, logits):
     if grad.numel() == 0:
         return
     a, b = _span(grad), _span(logits)
-    if a[0] < b[1] and b[0] < a[1] and (a[0] != b[0] or _strides(grad) != _strides(logits)):
-        raise ValueError("grad must be the logits themselves or lie apart from them")
+    if a[0] < b[1] and b[0] < a[1] and (a[0] != b[0] or _steps(grad) != _steps(logits)) \
+            and not _apart(grad, logits):
+        raise ValueError("grad must be the logits themselves or lie apart from them (between their rows: "
+                         "with their strides)")
 
 
 def _logprobs(described, logits, tokens, top_k, row_status, workspace, row_stats):

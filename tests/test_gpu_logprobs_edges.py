@@ -6,6 +6,7 @@ import torch
 
 import logprobs_util as u
 import speculative_decoding_verification_66_gb300 as sv
+from test_gpu_distill import check as check_distillation
 from test_gpu_logprobs import check_gradient, draw, draw_tokens
 
 pytestmark = pytest.mark.gpu
@@ -117,3 +118,27 @@ def test_entropies_are_as_exact_wherever_the_largest_logit_is(dtype):
         w = torch.cat([u.logprobs(rows)["entropy"] for rows in y.split(50)])
         off.append((r.entropy.double() - w).square().mean().sqrt().item())
     assert off[1] <= 1.5 * off[0], off
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [33, 2048, 70001])
+def test_gradients_between_the_logits_rows(dtype, V):
+    room = draw((5, 2, 3, V), dtype, V)
+    x, out = room[:, 0], room[:, 1]
+    tokens, a = draw_tokens((5, 3), V), torch.randn(5, 3, device="cuda")
+    before = x.clone()
+    grad = sv.sv_token_logprobs_backward(x, stats_of(x, tokens), tokens=tokens, grad_logprobs=a, grad=out)
+    assert torch.equal(x, before)
+    check_gradient(grad, x, tokens, a, None, None, 1.0)
+    r = sv.sv_token_logprobs(0.9 * before, top_k=5)
+    loss, grad = sv.sv_distill(x, r.top_tokens, r.top_logprobs, grad=out)
+    check_distillation(before, r.top_tokens, r.top_logprobs, 1.0, "renormalise", loss, grad)
+    assert torch.equal(x, before)
+
+
+def test_a_gradient_in_place_by_another_view():
+    x, tokens, a = draw((1, 6, 1000), "bf16"), draw_tokens((1, 6), 1000), torch.randn(1, 6, device="cuda")
+    stats = stats_of(x, tokens)
+    want = sv.sv_token_logprobs_backward(x, stats, tokens=tokens, grad_logprobs=a)
+    view = x.as_strided((1, 6, 1000), (24, 1000, 1))
+    assert torch.equal(sv.sv_token_logprobs_backward(x, stats, tokens=tokens, grad_logprobs=a, grad=view), want)

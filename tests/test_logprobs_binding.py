@@ -1,5 +1,6 @@
 """The binding of the log probabilities and of distillation without a GPU: a library that notes what it
 is given, and host tensors that pass for the GPU's."""
+import random
 import struct
 
 import pytest
@@ -89,3 +90,41 @@ def test_forward_mode_is_refused(library, loss, reverse_too):
         assert not library.calls
         loss(x)  # (no tangent of its own)
     assert library.calls
+
+
+def test_gradients_that_share_elements_with_the_logits_are_refused_and_no_others():
+    """Against the sets of elements, for strides and offsets of all kinds. (Gradients whose rows overlap
+    one another, or that have other strides between the logits' rows, are refused as well.)"""
+    rng = random.Random(1)
+    room, taken = torch.zeros(1000), 0
+    for _ in range(20000):
+        outer, inner, V = rng.randint(1, 4), rng.randint(1, 4), rng.randint(1, 9)
+        s, t, a, b = rng.randint(0, 60), rng.randint(0, 60), rng.randint(0, 120), rng.randint(0, 120)
+        logits, grad = (room.as_strided((outer, inner, V), (s, t, 1), at) for at in (a, b))
+        step = [i * s + j * t for i in range(outer) for j in range(inner)]
+        if any(abs(p - q) < V for n, p in enumerate(step) for q in step[:n]):
+            continue
+        if outer > 1 and inner > 1 and s < (inner - 1) * t + V and t < (outer - 1) * s + V:
+            continue
+        shared = any(abs(a + p - b - q) < V for p in step for q in step)
+        try:
+            lp._check_grad(grad, logits)
+            assert a == b or not shared, (outer, inner, V, s, t, a, b)
+            taken += 1
+        except ValueError:
+            assert a != b and shared, (outer, inner, V, s, t, a, b)
+    assert taken > 5000
+
+
+def test_gradients_of_other_strides():
+    room = torch.zeros(600)
+    logits = room[:400].view(4, 100)[:, :40]
+    lp._check_grad(room[400:560].view(4, 40), logits)
+    with pytest.raises(ValueError):
+        lp._check_grad(room[40:].as_strided((4, 40), (50, 1)), logits)
+    # Where there is one row of a kind, its stride is nobody's.
+    x = torch.zeros(1, 6, 50)
+    lp._check_grad(x.as_strided((1, 6, 50), (7, 50, 1)), x)
+    lp._check_grad(x[:, 2:3].as_strided((1, 1, 50), (1, 9, 1)), x[:, 2:3])
+    with pytest.raises(ValueError):
+        lp._check_grad(x[:, 1:5].as_strided((1, 4, 50), (7, 50, 1)), x[:, :4])
