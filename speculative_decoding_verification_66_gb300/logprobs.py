@@ -221,7 +221,7 @@ def _logprobs(described, logits, tokens, top_k, row_status, workspace, row_stats
         rows, token_ptr, top_k, ptr(logprobs), entropy.data_ptr(), lse.data_ptr(), ptr(rank),
         ptr(top_tokens), ptr(top_logprobs), stats_ptr, status_ptr,
         *_workspace(workspace, logits, shape.numel(), top_k, stream), stream), "sv_token_logprobs")
-    _wrote(row_stats)
+    _wrote(row_stats, row_status)
     return TokenLogprobs(logprobs, rank, entropy, lse, top_tokens, top_logprobs)
 
 
@@ -404,6 +404,7 @@ def _distill(described, logits, teacher_tokens, teacher_logprobs, weights, tail,
         _per_row(row_stats, "row_stats", shape, f32, dev, (SV_ROW_STATS,)),
         _per_row(row_status, "row_status", shape, torch.int32, dev),
         *_workspace(workspace, logits, shape.numel(), 0, stream), stream), "sv_distill")
+    _wrote(row_status)
     return loss
 
 

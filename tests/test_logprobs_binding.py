@@ -128,3 +128,25 @@ def test_gradients_of_other_strides():
     lp._check_grad(x[:, 2:3].as_strided((1, 1, 50), (1, 9, 1)), x[:, 2:3])
     with pytest.raises(ValueError):
         lp._check_grad(x[:, 1:5].as_strided((1, 4, 50), (7, 50, 1)), x[:, :4])
+
+
+def test_all_that_a_call_writes_is_told_to_autograd(library):
+    x, f32, i32 = torch.randn(4, 50), torch.float32, torch.int32
+
+    def given(*names):
+        shapes = dict(row_status=((4,), i32), row_stats=((4, lp.SV_ROW_STATS), f32), loss=((4,), f32),
+                      grad=((4, 50), f32))
+        return {n: torch.zeros(shapes[n][0], dtype=shapes[n][1]) for n in names}
+
+    for leaf in (False, True):
+        y = x.clone().requires_grad_(leaf)
+        for call, names in ((lambda **kw: lp.sv_token_logprobs(y, **kw), ("row_status", "row_stats")),
+                            (lambda **kw: lp.sv_distill_loss(y, IDS, LOGP, **kw), ("row_status",)),
+                            (lambda **kw: lp.sv_distill(y, IDS, LOGP, **kw),
+                             ("row_status", "row_stats", "loss", "grad")),
+                            (lambda **kw: lp.sv_token_logprobs_backward(y, torch.zeros(4, 8), **kw), ("grad",)),
+                            (lambda **kw: lp.sv_distill_backward(y, IDS, LOGP, torch.zeros(4, 8), LOGP[:, 0].contiguous(),
+                                                                 **kw), ("grad",))):
+            out = given(*names)
+            call(**out)
+            assert all(t._version == 1 for t in out.values()), names
