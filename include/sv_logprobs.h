@@ -20,7 +20,9 @@
  *                     the vocabulary.
  *   SV_SEQ_NONFINITE  the row has a NaN or +inf, or nothing but -inf; or the
  *                     teacher's log probabilities have a NaN or +inf, or no
- *                     finite one where they are to be renormalised.
+ *                     finite one where they are to be renormalised, or
+ *                     probabilities that float32 cannot add up where they are
+ *                     not (logarithms from some 88 up).
  * The row's floating outputs, gradients included, are then NaN, its whole
  * outputs -1. No input makes a kernel read or write outside the arrays.
  *

@@ -128,7 +128,9 @@ __device__ __forceinline__ void make_teacher(Teacher& t, Entries& s, const Disti
     }
     t.mass = warp_sum(mass);
     t.distinct = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (!a.bucket && t.distinct > 0 && !(t.mass > 0.0)) t.status |= SV_SEQ_NONFINITE;
+    // (Nothing to be renormalised; or more than float32 holds, as of logits given for probabilities.)
+    if (a.bucket ? !(t.mass <= 3.40282347e38) : t.distinct > 0 && !(t.mass > 0.0))
+        t.status |= SV_SEQ_NONFINITE;
 }
 
 // 1 / x to some 2^-40, for x in the range of floats.

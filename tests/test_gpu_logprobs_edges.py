@@ -7,6 +7,7 @@ import torch
 import logprobs_util as u
 import speculative_decoding_verification_66_gb300 as sv
 from test_gpu_distill import check as check_distillation
+from test_gpu_distill import teacher
 from test_gpu_logprobs import check_gradient, draw, draw_tokens
 
 pytestmark = pytest.mark.gpu
@@ -142,3 +143,28 @@ def test_a_gradient_in_place_by_another_view():
     want = sv.sv_token_logprobs_backward(x, stats, tokens=tokens, grad_logprobs=a)
     view = x.as_strided((1, 6, 1000), (24, 1000, 1))
     assert torch.equal(sv.sv_token_logprobs_backward(x, stats, tokens=tokens, grad_logprobs=a, grad=view), want)
+
+
+@pytest.mark.parametrize("V", [3001, 70001])
+def test_probabilities_past_float32(V):
+    """Logits of a hundred given for log probabilities: renormalised they are what they are; as they
+    stand they have no sum."""
+    x, ids, lp = teacher((6,), V, 5, 8, missing=0.0, none=0.0)
+    lp[0, 2] = 100.0
+    lp[1] = 88.0                             # each is in range, their sum is not
+    lp[2, 0], lp[2, 1], ids[2, 1] = 88.5, 88.5, ids[2, 0].clone()
+    lp[3] = torch.tensor([80.0, -3.0, -4.0, 60.0, 1.0])
+    status = torch.empty(6, dtype=torch.int32, device="cuda")
+    loss, grad = sv.sv_distill(x, ids, lp, tail="bucket", row_status=status)
+    assert status.tolist() == [u.NONFINITE] * 3 + [0] * 3
+    assert loss[:3].isnan().all() and grad[:3].isnan().all() and grad[3:].isfinite().all()
+    want, g, _ = u.distill(x[3:], ids[3:], lp[3:], 1.0, "bucket")
+    assert ((loss[3:] - want) / want).abs().max() < 1e-5   # (80 roundings of 2^-24 in a logarithm of 80)
+    y = x.detach().requires_grad_()
+    l2 = sv.sv_distill_loss(y, ids, lp, tail="bucket", row_status=status)
+    l2.sum().backward()
+    assert l2[:3].isnan().all() and y.grad[:3].isnan().all() and y.grad[3:].isfinite().all()
+    assert status.tolist() == [u.NONFINITE] * 3 + [0] * 3
+    loss, grad = sv.sv_distill(x, ids, lp, row_status=status)
+    assert not status.any()
+    check_distillation(x, ids, lp, 1.0, "renormalise", loss, grad)
