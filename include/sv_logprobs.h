@@ -85,7 +85,7 @@ enum sv_tail { SV_TAIL_RENORMALISE = 0, SV_TAIL_BUCKET = 1 };
  *            not looked at where there is one of a kind.
  *   vocab    1 .. 2^31 - 1.
  *   dtype    SV_F32, SV_BF16 or SV_F16.
- *   temperature  finite, > 0, with log2(e) / T and 1 / T finite in float32.
+ *   temperature  > 0 and up to 2^117, with log2(e) / T and 1 / T finite in float32.
  */
 typedef struct sv_logit_rows {
     const void* logits;

@@ -29,7 +29,9 @@ int check_rows(const sv_logit_rows* d, svl::Rows* r, bool pointers = true)
         return SV_ERR_SIZE;
     const float T = d->temperature;
     const double c = 1.44269504088896340736 / T;
-    if (!(T > 0.f) || !std::isfinite(T) || !std::isfinite(static_cast<float>(c)) ||
+    // (up to 2^117 two logits that float32 cannot subtract are 2^128 c > 2900 bits apart at least, and
+    // the lower one's weight is 0 whether their difference is infinite or not)
+    if (!(T > 0.f) || !(T <= 0x1p117f) || !std::isfinite(static_cast<float>(c)) ||
         !std::isfinite(1.0f / T))
         return SV_ERR_ARG;
     const int64_t rows = d->outer * d->inner;

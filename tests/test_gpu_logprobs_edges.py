@@ -168,3 +168,35 @@ def test_probabilities_past_float32(V):
     loss, grad = sv.sv_distill(x, ids, lp, row_status=status)
     assert not status.any()
     check_distillation(x, ids, lp, 1.0, "renormalise", loss, grad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2.0 ** 117, 1e30, 1e-3, 1e-38])
+def test_temperatures_at_their_ends(dtype, T):
+    """Logits from end to end of the type, which differ by more than float32 holds; at the highest
+    temperature they are some 2000 apart."""
+    V = 5003
+    big = float(torch.finfo(u.DTYPES[dtype]).max)
+    x = draw((5, V), dtype, 7)
+    x[0, ::3], x[0, 1] = -big, big
+    x[1, ::2], x[1, 5] = -math.inf, 3.0
+    x[2] = x[2] * (big / 32)
+    x[3] = (x[3].float() * min(T, 1e36)).to(x.dtype)
+    tokens = torch.tensor([1, 5, 77, 4000, V - 1], dtype=torch.int32, device="cuda")
+    tokens[2], tokens[3] = x[2].argmax().int(), x[3].argmax().int()
+    status = torch.full((5,), 77, dtype=torch.int32, device="cuda")
+    y = x.detach().requires_grad_()
+    r = sv.sv_token_logprobs(y, tokens, temperature=T, top_k=4, row_status=status)
+    # (log-sum-exps past float32 are infinite)
+    u.check_logprobs(x, tokens, T, 4, r, status)
+    if T > 1e-30:
+        a = torch.randn(5, device="cuda")
+        g, = torch.autograd.grad(r.logprobs, y, a)
+        # Beside what check_gradient allows, the token's own gradient a (1 - p) / T has three roundings of
+        # 2^-24 in float32: the temperature's to float32, its inverse's, and the product's.
+        want = u.logprobs_grad(x, tokens, a, None, None, T)
+        w = u.logprobs(x, tokens, T)
+        far = torch.where(w["p"] > 0, w["logp"].abs(), 0.0) + w["entropy"][:, None] + 1
+        tol = (u.half_step(x.dtype) * (1 + 2 ** -6) + 3 * u.U) * want.abs() + 1e-38 \
+            + 4 * u.sum_tol(V, 8.0) * w["p"] * a.double().abs()[:, None] * far / T
+        u.close(g, want, tol, "grad")
