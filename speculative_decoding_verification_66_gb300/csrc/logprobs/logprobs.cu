@@ -17,10 +17,10 @@
 // the vectors of 16 bytes in those groups, and leaves 8 k elements at most.
 //
 // Few rows are cut into pieces, a block each (cut_of; one row of 128256 bfloat16 is read by
-// fifteen SMs). A piece leaves its sums and its groups' maxima in the workspace; the block that is
-// the last of its row to do so (a counter a row, which starts at 0 and is 0 again afterwards)
-// finishes the row while others read on. Pieces are joined in order, so that who is last makes no
-// difference.
+// eleven SMs, or by three with alternatives). A piece leaves its sums and its groups' maxima in the
+// workspace; the block that is the last of its row to do so (a counter a row, which starts at 0 and
+// is 0 again afterwards) finishes the row while others read on. Pieces are joined in order, so that
+// who is last makes no difference.
 //
 // Bound by memory for many rows: half of the issue slots are taken (some six to seven instructions
 // an element). 1024 rows of 128256 bfloat16, 263 MB: 54 us without alternatives, 62 with 20, 80
@@ -534,6 +534,13 @@ __global__ void __launch_bounds__((TOP ? kMostWarps : kLeastWarps) * 32, TOP ? 2
     finish_all<DT, TOP, SPLIT>(a, row, in, all, q.x_t, top, maxima, dynamic);
 }
 
+// Keys and candidates of the longest row and of most alternatives have room beside the static part
+// in what a block gets unasked.
+constexpr int32_t kMostGroups = ((SV_MAX_TOP_VOCAB + 3) / 4 + 1 + kTile - 1) / kTile * kInFlight;
+static_assert(32 * SV_MAX_TOP <= kMostGroups, "the groups' maxima are the most keys");
+static_assert(kMostGroups * 4 + 8 * SV_MAX_TOP * 8 + sizeof(Top) + kMostWarps * sizeof(RowSum) <= 49152,
+              "else the kernel has to be allowed more");
+
 template <int DT>
 LogprobPlan plan_of(const Rows& r, int32_t k, int* warps)
 {
@@ -563,11 +570,6 @@ cudaError_t launch(const LogprobArgs& a, void* workspace, cudaStream_t s)
     const size_t bytes = TOP ? p.keys * 4 + p.candidates * 8 : 0;
     const unsigned grid = static_cast<unsigned>(blocks_of(p.cut, a.r.rows));
     const auto k = cut ? logprobs_kernel<DT, TOP, true> : logprobs_kernel<DT, TOP, false>;
-    if (bytes > 45000) {  // (beside the static part, more than is allowed unasked)
-        const cudaError_t e =
-            cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
-        if (e != cudaSuccess) return e;
-    }
     k<<<grid, warps * 32, bytes, s>>>(a, p);
     return cudaGetLastError();
 }
