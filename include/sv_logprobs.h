@@ -33,11 +33,11 @@
  * captured into a CUDA graph.
  *
  * Workspace. Rows are cut into pieces whose blocks leave one another their sums.
- *   workspace  device, 256-byte aligned, at least sv_logprobs_workspace_bytes (which
- *              may be 0: then it may be NULL). Its first SV_LOGPROBS_COUNTER_BYTES
- *              must be 0 before it is used for the first time, with rows of whatever
- *              sizes; every call leaves them 0. Calls that share a workspace must be
- *              ordered (one stream, or events); a captured call's replays too.
+ *   workspace  device, 256-byte aligned, at least sv_logprobs_workspace_bytes. Its
+ *              first SV_LOGPROBS_COUNTER_BYTES must be 0 before it is used for the
+ *              first time, with rows of whatever sizes; every call leaves them 0.
+ *              Calls that share a workspace must be ordered (one stream, or events);
+ *              a captured call's replays too.
  */
 #ifndef SV_LOGPROBS_H
 #define SV_LOGPROBS_H

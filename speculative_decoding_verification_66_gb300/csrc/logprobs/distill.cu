@@ -12,8 +12,8 @@
 // shows by its mark being there already, and only then the entries are compared with one
 // another.
 //
-// Bound by memory: the loss of 1024 rows of 128256 bfloat16 takes 54 us (4.9 TB/s), of 4096
-// rows 179 (5.9 TB/s).
+// Bound by memory: the loss of 1024 rows of 128256 bfloat16 takes 53 us (4.9 TB/s), of 4096
+// rows 180 (5.8 TB/s).
 #include "lp_finish.cuh"
 #include "lp_stream.cuh"
 
@@ -366,7 +366,9 @@ __global__ void __launch_bounds__((GRAD ? kMostWarps : kLeastWarps) * 32, GRAD ?
 //   50257 (100 KB)    21 / 23   23 / 27   29 / 33   39 / 45   57 / 59    117 / 115
 //   128256            29 / 23   35 / 35   49 / 53   76 / 80   123 / 123  262 / 248
 // and float32 rows of 128256: 304 of them 84 / 87, 512 135 / 133. With 4, 8 and 16 warps a block,
-// of 32000: 32 rows 23, 18 and 14; 456 rows 31, 27 and 31; 912 rows 41, 45 and 47.
+// of 32000: 32 rows 23, 18 and 14; 456 rows 31, 27 and 31; 912 rows 41, 45 and 47. (The limits of 33, 50
+// and 130 turns are those of the three vocabularies that were measured: 32, 50 and 126 turns. Where
+// one way overtakes the other between them is not known.)
 inline bool one_block(int64_t rows, int32_t tiles, bool grad)
 {
     if (!grad) return false;

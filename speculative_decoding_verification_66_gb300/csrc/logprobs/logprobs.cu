@@ -23,9 +23,9 @@
 // who is last makes no difference.
 //
 // Bound by memory for many rows: half of the issue slots are taken (some six to seven instructions
-// an element). 1024 rows of 128256 bfloat16, 263 MB: 54 us without alternatives, 62 with 20, 80
+// an element). 1024 rows of 128256 bfloat16, 263 MB: 51 us without alternatives, 61 with 20, 80
 // with 128 (a block's choice and order of 128 is not hidden where all rows make one wave); 4096
-// rows 174, 221 and 294: 6.0, 4.8 and 3.6 TB/s. A plain sum over the 263 MB takes 49.
+// rows 172, 217 and 291: 6.1, 4.8 and 3.6 TB/s. A plain sum over the 263 MB takes 49.
 #include "lp_finish.cuh"
 #include "lp_stream.cuh"
 

@@ -24,8 +24,9 @@ constexpr float kNear = 1048576.f;
 // by so many bits at most: it moves hardly ever. A sum of 2^t alone takes no harm from that. In one
 // of 2^t t a largest element whose t is d weighs d times what it does with o at the element itself,
 // and so does every rounding after it, though nearly all of that is taken off again at the end. Log
-// probabilities of 256 x 9 rows: 16 bits leave their entropies 3.5e-7 off in norm and 8.6e-6 at most,
-// 8 leave 0.85e-7 and 1.3e-6, 4 and fewer 0.71e-7 and 1.2e-6; 4096 rows take 166, 167 and 171 us.
+// probabilities of rows of 128256 at temperature 0.7: 16 bits leave the entropies 3.5e-7 off in norm and
+// 8.6e-6 at most, 8 leave 0.85e-7 and 1.3e-6, 4 and fewer 0.71e-7 and 1.2e-6; 4096 rows take 167, 168
+// and 171 us, 256 x 9 ragged ones with 20 alternatives 80, 81 and 83.
 constexpr float kBehindSum = 16.f, kBehindEntropy = 8.f;
 struct Running {
     float m;            // largest logit (NaN if there is one)
@@ -372,7 +373,8 @@ inline int64_t blocks_of(const Cut& c, int64_t rows) { return c.whole + (rows - 
 // 182, all in two 78, 107 and 191, so 72, 99 and 179; but of 4096 rows of 64 KB 68, and so 70.
 // `ragged` (with alternatives): somewhat more long rows than run at a time are all cut in two, since
 // some may have nothing to do: 2304 rows with 20 alternatives, half of the rows empty, one piece
-// 96, two 86 (blocks of two warps 106); 1280 full rows 99 and 87; but 2304 full ones 125 and 135.
+// 96, two 86 (blocks of two warps 106); 1280 full rows 99 and 87; but 2304 full ones 125 and 135. (Rows
+// of calls without tokens are never empty, and are cut all the same.)
 inline Cut cut_of(int64_t rows, int32_t tiles, int32_t warps, bool ragged)
 {
     const Cut none{static_cast<int32_t>(rows), 1, tiles};

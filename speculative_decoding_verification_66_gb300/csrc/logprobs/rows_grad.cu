@@ -8,8 +8,8 @@
 // that has the token in its piece, a barrier later.
 //
 // One read and one write of 16-byte vectors and some seven instructions an element:
-// bound by memory. A block takes a piece of a row. 4096 rows of 128256 bfloat16, 2.1 GB: 320 us
-// (6.6 TB/s); 1024 rows 87, or 91 with a teacher's 32 entries a row.
+// bound by memory. A block takes a piece of a row. 4096 rows of 128256 bfloat16, 2.1 GB: 313 us
+// (6.7 TB/s), or 322 with a teacher's 32 entries a row; 1024 rows 86 and 92.
 #include "lp_finish.cuh"
 #include "lp_stream.cuh"
 

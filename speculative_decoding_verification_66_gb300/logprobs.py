@@ -92,7 +92,7 @@ def _workspace_bytes(rows, V, code, top_k):
 
 def sv_logprobs_workspace_bytes(rows: int, V: int, dtype, top_k: int = 0) -> int:
     """Workspace that ``sv_token_logprobs``, ``sv_distill`` and ``sv_distill_loss`` need for so many
-    rows, with up to ``top_k`` alternatives; 0 where none is used."""
+    rows, with up to ``top_k`` alternatives."""
     if dtype not in _CODES:
         raise TypeError(f"logits must be float32, bfloat16 or float16, got {dtype}")
     return _workspace_bytes(rows, V, _CODES[dtype], top_k)
