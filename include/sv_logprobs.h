@@ -151,7 +151,9 @@ int sv_token_logprobs_backward(const sv_logit_rows* rows, const int32_t* tokens,
  * SV_TAIL_BUCKET P_o what the entries leave and q_o the sum of q over the tokens
  * that have none (both left out where all tokens have one):
  *   loss = sum_v P_v (log P_v - log q_v)  [ + P_o (log P_o - log q_o) ]
- * over the tokens with entries (0 log 0 = 0), and with M the sum of all P, P_o too,
+ * over the tokens with entries (0 log 0 = 0; a P_o of up to 2^-20, the rounding of a
+ * whole teacher's float32 logarithms, is 0 where q_o is below float32's range, as of
+ * masked tokens), and with M the sum of all P, P_o too,
  *   dloss/dx_v = (M q_v - P_v) / T                  for tokens with entries
  *              = (M q_v - P_o q_v / q_o) / T        for the others.
  * Rows without entries are not read; they have loss 0 and gradient 0.

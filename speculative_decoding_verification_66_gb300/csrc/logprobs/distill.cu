@@ -40,6 +40,10 @@ struct Teacher {
     int32_t status;
 };
 
+// The sum of a teacher's probabilities that are all there is: entropies of up to log 128 make its
+// float32 logarithms' roundings 4.9 x 2^-24 of it, the exponentials' add 2 and the numbers' own 1.
+constexpr double kRounding = 0x1p-20;
+
 // Room for looking for entries of one token.
 struct Entries {
     int32_t id[SV_MAX_TOP];
@@ -190,7 +194,11 @@ __device__ __forceinline__ RowStats finish(const Teacher& t, const DistillArgs& 
     float scale = listed * fall;
     if (a.bucket) {
         const double q_e = S_e * over_S;
-        const double P_o = t.distinct < a.r.V ? fmax(0.0, 1.0 - t.mass) : 0.0;
+        double P_o = t.distinct < a.r.V ? fmax(0.0, 1.0 - t.mass) : 0.0;
+        // Tokens that a mask takes from student and teacher alike: what the entries leave them is the
+        // rounding of their sum, and would be multiplied by the logarithm of a probability of 0.
+        const bool none = !(S_o > 0.f) || fall == 0.f;
+        if (none && P_o <= kRounding) P_o = 0.0;
         if (P_o > 0.0) {
             const float m = static_cast<float>(t.mass);
             const double log_P = m < 0.5f ? log1pf(-m) : logf(static_cast<float>(P_o));
@@ -200,9 +208,9 @@ __device__ __forceinline__ RowStats finish(const Teacher& t, const DistillArgs& 
         }
         listed = static_cast<float>((t.mass + P_o) * over_S);
         // (no other token, or all of probability 0: their gradient is 0)
-        scale = !(S_o > 0.f)    ? 0.f
-                : t.mass <= 1.0 ? static_cast<float>(t.mass - q_e) / S_o
-                                : listed * fall;
+        scale = !(S_o > 0.f)               ? 0.f
+                : P_o > 0.0 && t.mass <= 1.0 ? static_cast<float>(t.mass - q_e) / S_o
+                                             : listed * fall;
     }
     // (M_o where nothing is finite: any finite number)
     st = {S_o > 0.f ? M_o : 0.f,

@@ -200,3 +200,53 @@ def test_temperatures_at_their_ends(dtype, T):
         tol = (u.half_step(x.dtype) * (1 + 2 ** -6) + 3 * u.U) * want.abs() + 1e-38 \
             + 4 * u.sum_tol(V, 8.0) * w["p"] * a.double().abs()[:, None] * far / T
         u.close(g, want, tol, "grad")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "f32"])
+@pytest.mark.parametrize("mask", ["-inf", "lowest"])
+@pytest.mark.parametrize("V", [300, 70001])
+def test_a_teacher_and_a_student_that_are_allowed_the_same_few_tokens(dtype, mask, V):
+    """Where a mask leaves at most ten tokens, twenty entries have all of the teacher's probability, but
+    for the rounding of their sum: nothing is left for the tokens that nobody may take."""
+    N, dt = 300, u.DTYPES[dtype]
+    g = torch.Generator(device="cuda").manual_seed(V)
+    low = -math.inf if mask == "-inf" else -float(torch.finfo(dt).max)
+    allowed = torch.randint(0, V, (N, 10), generator=g, device="cuda")
+    there = torch.zeros(N, V, dtype=torch.bool, device="cuda").scatter_(1, allowed, True)
+    target, x = (torch.randn((N, V), generator=g, device="cuda").mul_(2.5).to(dt).masked_fill_(~there, low)
+                 for _ in range(2))
+    r = sv.sv_token_logprobs(target, top_k=20)
+    status = torch.empty(N, dtype=torch.int32, device="cuda")
+    loss, grad = sv.sv_distill(x, r.top_tokens, r.top_logprobs, tail="bucket", row_status=status)
+    assert not status.any()
+    P = torch.zeros(N, V, dtype=torch.float64, device="cuda")
+    P.scatter_add_(1, r.top_tokens.long(), r.top_logprobs.double().exp())
+    logq = torch.log_softmax(x.double(), -1)
+    want = (torch.special.xlogy(P, P) - torch.where(P > 0, P * logq, 0.0)).sum(-1)
+    # (as in the other tests: the entries' probabilities by 2 roundings and their logarithms by one, log q
+    # by its distance from the mean of some 20, and the sums)
+    u.close(loss, want, u.sum_tol(V, 8.0) + 4 * u.U * (20 + 20 + want), "loss")
+    q = logq.exp()
+    # (the sum of P is 1 but for kRounding's 8 roundings, and stands before q)
+    u.check_grad(grad, P.sum(-1, keepdim=True) * q - P, q * 20 + P, V, 8.0)
+    y = x.detach().requires_grad_()
+    l2 = sv.sv_distill_loss(y, r.top_tokens, r.top_logprobs, tail="bucket")
+    l2.sum().backward()
+    u.close(l2.detach(), want, u.sum_tol(V, 8.0) + 4 * u.U * (20 + 20 + want), "loss")
+    u.check_grad(y.grad, P.sum(-1, keepdim=True) * q - P, q * 20 + P, V, 8.0)
+
+
+@pytest.mark.parametrize("V", [300, 70001])
+def test_what_a_teacher_leaves_to_masked_tokens_is_missed(V):
+    """A rest above what roundings leave is the teacher's, and costs what it costs."""
+    x = torch.full((2, V), -math.inf, device="cuda")
+    x[:, :4] = 0.0
+    x[1, 4:] = -500.0
+    ids = torch.tensor([[0, 1, 2, 3]] * 2, dtype=torch.int32, device="cuda")
+    for rest in (1e-3, 1e-5):
+        lp = torch.full((2, 4), math.log((1 - rest) / 4), device="cuda")
+        loss, grad = sv.sv_distill(x, ids, lp, tail="bucket")
+        want, g, _ = u.distill(x, ids, lp, 1.0, "bucket")
+        assert loss[0] == math.inf and grad.isfinite().all()
+        # (four roundings of probabilities of 1/4, times the distance of 500)
+        u.close(loss[1], want[1], 4 * u.U * 520 + u.sum_tol(V, 8.0), "loss")
