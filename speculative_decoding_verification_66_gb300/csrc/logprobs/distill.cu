@@ -41,7 +41,8 @@ struct Teacher {
 };
 
 // The sum of a teacher's probabilities that are all there is: entropies of up to log 128 make its
-// float32 logarithms' roundings 4.9 x 2^-24 of it, the exponentials' add 2 and the numbers' own 1.
+// float32 logarithms' roundings 4.9 x 2^-24 of it, the exponentials' add 2 and the numbers' own 1; this
+// is twice that.
 constexpr double kRounding = 0x1p-20;
 
 // Room for looking for entries of one token.

@@ -247,7 +247,8 @@ class _Call:
     __slots__ = ("described", "temperature", "inputs", "versions", "row_stats", "results", "args")
 
     def __init__(self, described, temperature, inputs, row_stats, args):
-        self.described, self.temperature, self.inputs = described, temperature, inputs
+        # (a number: a tensor given for it may change before the backward pass)
+        self.described, self.temperature, self.inputs = described, float(temperature), inputs
         self.row_stats, self.args, self.results = row_stats, args, None
 
     def begun(self):

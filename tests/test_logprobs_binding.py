@@ -150,3 +150,13 @@ def test_all_that_a_call_writes_is_told_to_autograd(library):
             out = given(*names)
             call(**out)
             assert all(t._version == 1 for t in out.values()), names
+
+
+@pytest.mark.parametrize("call", [lambda x, T: lp.sv_token_logprobs(x, temperature=T).lse,
+                                  lambda x, T: lp.sv_distill_loss(x, IDS, LOGP, temperature=T)])
+def test_the_backward_pass_has_the_forward_calls_temperature(library, call):
+    T = torch.tensor(0.5)
+    y = call(torch.randn(4, 50, requires_grad=True), T)
+    T.fill_(2.0)
+    y.sum().backward()
+    assert [rows[7] for _, rows, _ in library.calls] == [0.5, 0.5]
